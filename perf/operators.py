@@ -208,8 +208,8 @@ def prepare(case, seed):
                   lse=torch.empty(total, Hq, dtype=torch.float32, device="cuda"))
         if op == "accum":
             # weights counted by earlier steps: most tokens next to nothing, a few a lot
-            st["acc"] = torch.rand(nb, Hkv, BLOCK, generator=gen, device="cuda").pow(8).mul_(20)
-            st["acc_out"] = torch.zeros(nb, Hkv, BLOCK, device="cuda")
+            st["acc"] = torch.rand(case["S"], Hkv, mbps * BLOCK, generator=gen, device="cuda").pow(8).mul_(20)
+            st["acc_out"] = torch.zeros_like(st["acc"])
         if own:
             from paged_kv_cache_tiled_gb300 import fattn as F
             size = F.fa_paged_attn_accum_workspace_size if op == "accum" else F.fa_paged_attn_mod_workspace_size
@@ -240,11 +240,12 @@ def prepare(case, seed):
     mbps, dmbps = -(-max(ctx) // BLOCK), -(-max(new) // BLOCK)
     table, perm, at = _tables(gen, ctx, mbps, nb)
     dst, _, _ = _tables(gen, new, dmbps, nb, perm, at)
-    acc = torch.rand(nb, Hkv, BLOCK, generator=gen, device="cuda").pow(8).mul_(20)
+    acc = torch.rand(case["S"], Hkv, mbps * BLOCK, generator=gen, device="cuda").pow(8).mul_(20)
     acc[acc < 1e-3] = 0.0  # tokens that no query looked at: many equal values
     st.update(kc=_normal(gen, nb, Hkv, BLOCK, d), vc=_normal(gen, nb, Hkv, BLOCK, d), acc=acc, table=table, dst=dst,
               ctx=_i32(ctx), new_lens=torch.empty(case["S"], dtype=torch.int32, device="cuda"),
-              kept=torch.empty(case["S"], Hkv, case["keep"], dtype=torch.int32, device="cuda"))
+              kept=torch.empty(case["S"], Hkv, case["keep"], dtype=torch.int32, device="cuda"),
+              acc_out=torch.zeros(case["S"], Hkv, case["keep"], device="cuda"))
     if own:
         from paged_kv_cache_tiled_gb300 import fattn as F
         st["ws"] = torch.empty(F.fa_cache_evict_workspace_size(case["S"], mbps, Hkv, case["keep"]), dtype=torch.uint8,
@@ -343,16 +344,12 @@ def _plain_paged(st):
 
 def _plain_accum(st):
     p, got = _plain_paged(st)
-    Hkv = st["case"]["Hkv"]
-    w = p.sum((2, 3)).transpose(1, 2)  # [S, keys, Hkv]
-    table, ctx = st["table"].long(), st["ctx"].long()
-    keys = torch.arange(w.shape[1], device="cuda")
-    old = _gathered(st["acc"], st["table"])
-    before = keys < (ctx - st["ql"].long())[:, None]
-    new = torch.where(before[..., None], old * st["case"]["decay"], torch.zeros_like(old)) + w
-    place = ((table[:, keys // BLOCK] * Hkv)[..., None] + torch.arange(Hkv, device="cuda")) * BLOCK + (keys % BLOCK)[:, None]
-    real = keys < ctx[:, None]
-    st["acc_out"].view(-1)[place[real]] = new[real]
+    w = p.sum((2, 3))  # [S, Hkv, keys]
+    ctx, old = st["ctx"].long(), st["acc"]
+    keys = torch.arange(w.shape[2], device="cuda")
+    before = keys < (ctx - st["ql"].long())[:, None, None]
+    new = torch.where(before, old * st["case"]["decay"], torch.zeros_like(old)) + w
+    st["acc_out"].copy_(torch.where(keys < ctx[:, None, None], new, st["acc_out"]))
     return dict(got, acc=st["acc_out"])
 
 
@@ -380,7 +377,7 @@ def _plain_evict(st):
     case = st["case"]
     keep = case["keep"]
     ctx = st["ctx"].long()
-    a = _gathered(st["acc"], st["table"]).transpose(1, 2)  # [S, Hkv, tokens]
+    a = st["acc"]
     t = torch.arange(a.shape[2], device="cuda")
     end = ctx[:, None, None]
     a = a.masked_fill((t < case["sink"]) | (t >= end - case["recent"]), math.inf).masked_fill(t >= end, -math.inf)
@@ -396,9 +393,10 @@ def _plain_evict(st):
     s = torch.arange(case["S"], device="cuda")[:, None, None].expand_as(first)[real]
     src, to = first[real], r.expand_as(first)[real]
     sb, db = st["table"][s, src // BLOCK].long(), st["dst"][s, to // BLOCK].long()
-    for x in (st["kc"], st["vc"], st["acc"]):
+    for x in (st["kc"], st["vc"]):
         x[db, h, to % BLOCK] = x[sb, h, src % BLOCK]
-    return dict(kc=st["kc"], vc=st["vc"], acc=st["acc"], kept=st["kept"], new_lens=st["new_lens"])
+    st["acc_out"][s, h, to] = st["acc"][s, h, src]
+    return dict(kc=st["kc"], vc=st["vc"], acc=st["acc_out"], kept=st["kept"], new_lens=st["new_lens"])
 
 
 # --------------------------------------------------------------------- run --
@@ -442,8 +440,9 @@ def _own(st):
                                 st["vc"], st["slots"], q_out=st["q_out"])
         return dict(q=st["q_out"], kc=st["kc"], vc=st["vc"])
     F.fa_cache_evict(st["kc"], st["vc"], st["acc"], st["table"], st["ctx"], st["dst"], case["keep"],
-                     recent=case["recent"], sink=case["sink"], new_lens=st["new_lens"], kept=st["kept"], ws=st["ws"])
-    return dict(kc=st["kc"], vc=st["vc"], acc=st["acc"], kept=st["kept"], new_lens=st["new_lens"])
+                     recent=case["recent"], sink=case["sink"], acc_out=st["acc_out"], new_lens=st["new_lens"],
+                     kept=st["kept"], ws=st["ws"])
+    return dict(kc=st["kc"], vc=st["vc"], acc=st["acc_out"], kept=st["kept"], new_lens=st["new_lens"])
 
 
 # -------------------------------------------------------------------- work --
@@ -548,17 +547,18 @@ def exact(case, seed):
         return dict(q=turned[0], kc=kc, vc=vc)
     if op == "evict":
         keep, S = case["keep"], case["S"]
-        kc, vc, acc = st["kc"].double(), st["vc"].double(), st["acc"].double()
+        kc, vc, acc = st["kc"].double(), st["vc"].double(), st["acc_out"].double()
         for s, c in enumerate(st["ctx"].tolist()):
             src, dst = st["table"][s].long(), st["dst"][s].long()
             for h in range(Hkv):
-                a = st["acc"][src[:-(-c // BLOCK)], h].reshape(-1)[:c].tolist()
+                a = st["acc"][s, h, :c].tolist()
                 must = set(range(min(c, case["sink"]))) | set(range(max(0, c - case["recent"]), c))
                 best = sorted((t for t in range(c) if t not in must), key=lambda t: (-a[t], t))
                 got = sorted((sorted(must) + best)[:keep])
                 f, t = torch.tensor(got, device="cuda"), torch.arange(len(got), device="cuda")
-                for x, y in ((kc, st["kc"]), (vc, st["vc"]), (acc, st["acc"])):
+                for x, y in ((kc, st["kc"]), (vc, st["vc"])):
                     x[dst[t // BLOCK], h, t % BLOCK] = y[src[f // BLOCK], h, f % BLOCK].double()
+                acc[s, h, :len(got)] = st["acc"][s, h, f].double()
         return dict(kc=kc, vc=vc, acc=acc, kept=None, new_lens=None)
     Hq, scale = case["Hq"], 1.0 / math.sqrt(d)
     g = Hq // Hkv
@@ -592,7 +592,6 @@ def exact(case, seed):
         blocks = st["table"][s, :-(-c // BLOCK)].long()
         pos = torch.arange(c - n, c, device="cuda")
         vis = _visible(pos, c, True, case["window"], p if case["prefix"] else 0)
-        t = torch.arange(c, device="cuda")
         for h in range(Hkv):
             k = st["kc"][blocks, h].reshape(-1, d)[:c]
             v = st["vc"][blocks, h].reshape(-1, d)[:c]
@@ -602,9 +601,9 @@ def exact(case, seed):
                     st["q"][at:at + n, i], k, v, scale, case["cap"], st["slopes"][i] if case["bias"] else None, pos, vis)
                 counted += w.sum(0)
             if acc is not None:
-                old = st["acc"][blocks, h].reshape(-1)[:c].double() * case["decay"]
+                old = st["acc"][s, h, :c].double() * case["decay"]
                 old[c - n:] = 0.0
-                acc[blocks[t // BLOCK], h, t % BLOCK] = old + counted
+                acc[s, h, :c] = old + counted
         at += n
     got = dict(out=out, lse=lse)
     return got if acc is None else dict(got, acc=acc)
