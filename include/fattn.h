@@ -151,6 +151,44 @@ fa_status fa_prefill_masked(const void* q, const void* k, const void* v, const f
                             fa_stream_t stream);
 
 /*
+ * fa_prefill_mod -- fa_prefill with modified scores: a cap, a bias that falls
+ * with distance, and masks given by a few numbers instead of a T x T matrix.
+ * Passage: "FlashAttention-Style Kernels", attention equation (the scores and
+ * M are functions of the positions, so no tile of M is ever read).
+ * Logit of query i and key j of head h, positions counted from the start of
+ * the sequence:
+ *     x_ij = f(scale q_i . k_j) - slope_h |i - j|,
+ *     f(z) = softcap tanh(z / softcap) when softcap > 0, else z.
+ * Key j is visible to query i when every mask given allows it:
+ *     causal != 0:  j <= i, or j < prefix_lens[b]
+ *     window > 0:   j > i - window, and, without causal, j < i + window
+ *     doc_ids:      every position from i to j holds the same id >= 0
+ *   softcap       >= 0, finite; 0: no cap
+ *   alibi_slopes  fp32 [Hq] or NULL (no bias); any finite values
+ *   window        >= 0; 0: none
+ *   prefix_lens   int32 [B] or NULL; ignored without causal (everything is
+ *                 visible then); values below 1 change nothing, values past T
+ *                 count as T
+ *   doc_ids       int32 [B, T] or NULL; a document is a run of equal ids, and a
+ *                 negative id marks padding: such a query sees nothing, and
+ *                 no other query sees such a key
+ *   lse           fp32 [B, Hq, T] log-sum-exp of the visible logits, or NULL
+ *   ws            needed with doc_ids only: at least
+ *                 fa_prefill_mod_workspace_size(B, T) bytes, 256-byte aligned
+ *                 (row ranges and tile order); contents need not be initialised
+ * A query that sees no key gets output 0 and LSE -inf.  Tiles of 128 keys that
+ * none of a tile's queries see are skipped; keys and values in the tiles that
+ * are visited must be finite (a weight of 0 times infinity is not a number).
+ * q, k, v, out, scale and errors as for fa_prefill; FA_ERR_UNSUPPORTED when
+ * B * T does not fit 31 bits.
+ */
+size_t fa_prefill_mod_workspace_size(int B, int T);
+fa_status fa_prefill_mod(const void* q, const void* k, const void* v, void* out, float* lse, int B,
+                         int T, int Hq, int Hkv, int d, int causal, float scale, float softcap,
+                         const float* alibi_slopes, int window, const int32_t* prefix_lens,
+                         const int32_t* doc_ids, void* ws, size_t ws_bytes, fa_stream_t stream);
+
+/*
  * fa_mask_tile_classes -- classes of the 128 x 128 tiles of an additive mask
  * (the first pass of fa_prefill_masked, callable alone).
  * Passage: "FlashAttention-Style Kernels", attention equation with additive M
@@ -223,6 +261,26 @@ fa_status fa_cache_append_rope(const void* q, const void* k, const void* v, cons
                                const float* cos_sin, int max_pos, void* q_out, void* k_cache,
                                void* v_cache, const int32_t* slot_mapping, int N, int Hq, int Hkv,
                                int d, int num_blocks, fa_dtype in_dtype, fa_stream_t stream);
+
+/*
+ * fa_cache_append_mrope -- fa_cache_append_rope with a position on each of
+ * several axes (time, height and width of image and video tokens).
+ * Passage: as fa_cache_append_rope.  Channel pair j (channels j and j + d/2)
+ * belongs to axis pair_axes[j] and turns by table row
+ * positions[pair_axes[j]][i], columns j and d/2 + j.  One axis is
+ * fa_cache_append_rope.
+ *   positions    int32 [n_axes, N]; a token with any position outside
+ *                [0, max_pos) records FA_ERR_BOUNDS and is skipped entirely
+ *   n_axes       1 to 4 (FA_ERR_UNSUPPORTED above)
+ *   pair_axes    HOST uint8 [d/2], read during the call; values below n_axes.
+ *                Sections and interleaved axes are both such a list
+ * Everything else as for fa_cache_append_rope.
+ */
+fa_status fa_cache_append_mrope(const void* q, const void* k, const void* v,
+                                const int32_t* positions, int n_axes, const uint8_t* pair_axes,
+                                const float* cos_sin, int max_pos, void* q_out, void* k_cache,
+                                void* v_cache, const int32_t* slot_mapping, int N, int Hq, int Hkv,
+                                int d, int num_blocks, fa_dtype in_dtype, fa_stream_t stream);
 
 /*
  * fa_cache_append_fp8 / fa_paged_attn_fp8 -- the 8-bit (E4M3) KV cache.
@@ -298,6 +356,109 @@ fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache,
                         int num_blocks, int Hq, int Hkv, int d, int block_size, int causal,
                         float scale, int total_q, int max_q_len, void* ws, size_t ws_bytes,
                         fa_stream_t stream);
+
+/*
+ * fa_paged_attn_mod -- fa_paged_attn with modified scores (as fa_prefill_mod).
+ * Passage: "Paged Attention Kernels"; "FlashAttention-Style Kernels",
+ * attention equation.
+ * Positions are cache positions: query r of sequence s sits at
+ * ctx_lens[s] - q_lens[s] + r.  Logits and masks as for fa_prefill_mod, with
+ * prefix_lens int32 [num_seqs] (in cache positions) and no documents.
+ *   lse   fp32 [total_q, Hq] natural-log log-sum-exp of the visible logits, or
+ *         NULL
+ * With a window, blocks that no query of a chunk sees are not read, nor are
+ * their block-table entries (they may have been freed); a block that is partly
+ * visible must hold finite values.  Everything else as for fa_paged_attn.
+ */
+size_t fa_paged_attn_mod_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv,
+                                        int d, int total_q, int max_q_len);
+fa_status fa_paged_attn_mod(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* ctx_lens,
+                            const int32_t* q_lens, void* out, float* lse, int num_seqs,
+                            int max_blocks_per_seq, int num_blocks, int Hq, int Hkv, int d,
+                            int block_size, int causal, float scale, float softcap,
+                            const float* alibi_slopes, int window, const int32_t* prefix_lens,
+                            int total_q, int max_q_len, void* ws, size_t ws_bytes,
+                            fa_stream_t stream);
+
+/*
+ * fa_paged_attn_accum -- fa_paged_attn_mod that also adds up how much weight
+ * every cached token received (what fa_cache_evict decides by).
+ * Passage: "FlashAttention-Style Kernels" (the softmax weights, which the
+ * tiled method never stores); "Paged Attention Kernels".
+ * For every sequence s, kv head h and token t < ctx_lens[s]:
+ *     acc_out[s][h][t] = decay * old + sum of exp(x_rt - lse_r)
+ * over the chunk's queries and the Hq/Hkv heads of the group, where
+ * old = acc_in[s][h][t] for the tokens before the chunk and 0 for the chunk's
+ * own tokens (and everywhere when acc_in is NULL).  Masked tokens add 0.
+ * A sequence with q_lens[s] = 0 gets decay * acc_in.
+ *   acc_in, acc_out fp32 [num_seqs, Hkv, acc_len]; may be the same array;
+ *         elements at t >= ctx_lens[s] are left as they were.  A context longer
+ *         than acc_len records FA_ERR_BOUNDS and its sums are not written
+ *   decay finite, >= 0
+ *   lse   fp32 [total_q, Hq], required (written)
+ *   ws    at least fa_paged_attn_accum_workspace_size(...) bytes, with the
+ *         same max_q_len: beside fa_paged_attn's, the logits of the decode rows
+ *         (64 bytes per row, page and kv head that the tables can hold)
+ * The sums run in a fixed order: equal inputs give equal bits.  A call without
+ * queries (total_q = 0) does nothing.  Everything else as for
+ * fa_paged_attn_mod.
+ */
+size_t fa_paged_attn_accum_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv,
+                                          int d, int total_q, int max_q_len);
+fa_status fa_paged_attn_accum(const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_table, const int32_t* ctx_lens,
+                              const int32_t* q_lens, void* out, float* lse, const float* acc_in,
+                              float* acc_out, int acc_len, float decay, int num_seqs,
+                              int max_blocks_per_seq, int num_blocks, int Hq, int Hkv, int d,
+                              int block_size, int causal, float scale, float softcap,
+                              const float* alibi_slopes, int window, const int32_t* prefix_lens,
+                              int total_q, int max_q_len, void* ws, size_t ws_bytes,
+                              fa_stream_t stream);
+
+/*
+ * fa_cache_evict -- thins out the cache by accumulated attention weight.
+ * Passage: "Paged Attention Kernels" (a logical sequence is a block table, so a
+ * shorter sequence is another table); which tokens stay is the caller's acc.
+ * Per sequence s and kv head h with ctx_lens[s] > keep: the first `sink` tokens,
+ * the last `recent` ones and, of the others, those with the largest
+ * acc[s][h][t] (equal weights: the earlier token; NaN counts as the smallest)
+ * stay, `keep` in all; a sequence of at most `keep` tokens stays whole.  The
+ * heads may keep different tokens.  The i-th token kept, in order of position,
+ * becomes token i of the blocks in dst_table: K and V rows are copied bit for
+ * bit, acc_out[s][h][i] gets its weight.
+ *   acc          fp32 [num_seqs, Hkv, acc_len]
+ *   block_table  int32 [num_seqs, max_blocks_per_seq], ctx_lens as for
+ *                fa_paged_attn
+ *   dst_table    int32 [num_seqs, dst_blocks_per_seq]: blocks for
+ *                min(ctx_lens[s], keep) tokens, none of them a block that
+ *                block_table lists for any sequence of the call (new blocks of
+ *                the pool: the old ones may be shared with other sequences and
+ *                are released afterwards); FA_ERR_INVALID_ARG when it is
+ *                block_table itself
+ *   acc_out      fp32 [num_seqs, Hkv, acc_out_len] or NULL; acc_out_len >=
+ *                keep; may be acc itself (with the same row length); elements
+ *                past the kept tokens are left as they were
+ *   new_lens     int32 [num_seqs] (written): min(ctx_lens[s], keep)
+ *   kept         int32 [num_seqs, Hkv, keep] (written) or NULL: the kept tokens'
+ *                old positions, ascending, -1 behind the last
+ *   keep > 0, recent >= 0, sink >= 0, sink + recent <= keep
+ *   ws           needed when kept is NULL: at least
+ *                fa_cache_evict_workspace_size(...) bytes, 256-byte aligned
+ * A sequence whose lengths do not fit its tables or acc_len records
+ * FA_ERR_BOUNDS and keeps nothing (new_lens 0); so does a block id outside the
+ * pool, whose rows are skipped.  Keys keep the rotation they were written with;
+ * cache positions (window, prefix and distance bias of later calls) count the
+ * kept tokens only.  bf16 caches, d = 64 or 128, block_size 16.
+ */
+size_t fa_cache_evict_workspace_size(int num_seqs, int max_blocks_per_seq, int Hkv, int keep);
+fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc_len,
+                         const int32_t* block_table, const int32_t* ctx_lens,
+                         const int32_t* dst_table, float* acc_out, int acc_out_len,
+                         int32_t* new_lens, int32_t* kept, int num_seqs, int max_blocks_per_seq,
+                         int dst_blocks_per_seq, int num_blocks, int Hkv, int d, int block_size,
+                         int keep, int recent, int sink, void* ws, size_t ws_bytes,
+                         fa_stream_t stream);
 
 /*
  * fa_paged_attn_noalloc -- fa_paged_attn for callers that cannot allocate

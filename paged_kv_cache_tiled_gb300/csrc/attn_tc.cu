@@ -49,6 +49,11 @@
 namespace fa {
 
 enum { MODE_DENSE = 0, MODE_MASKED = 1, MODE_PAGED = 2 };
+// Score modifiers of a kernel variant (DENSE and PAGED modes): MOD_RANGE gives
+// every row a run [lo, hi) of visible keys (window, prefix, documents) and is
+// set in every modified variant; MOD_CAP caps the scores; MOD_BIAS subtracts
+// slope |i - j| (and caps them when asked: a rare pair that needs no variant).
+enum { MOD_RANGE = 1, MOD_CAP = 2, MOD_BIAS = 4 };
 constexpr int kRangeHoles = 1 << 30;  // flag bit of a query tile's visible KV range
 constexpr int kTcThreads = 320;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
@@ -109,6 +114,10 @@ struct TcParams {
     const int32_t* work_list;
     const int32_t* work_count;
     int mbps, num_blocks;
+    // modified variants
+    ScoreMod mod;
+    const int2* doc_rows;      // dense: per row of [B, T] its document's [first, end), empty for padding; or null
+    const int32_t* doc_order;  // dense with documents: (sequence, query tile) entries, longest first
     DevCtx ctx;
 };
 
@@ -123,6 +132,7 @@ struct Unit {
     int pos_off;    // key position of query row i is i + pos_off
     int kt0;        // first KV tile to scan
     int n_kt;       // KV tiles to scan: [kt0, n_kt)
+    int kv_lo;      // modified variants: first key any row of the unit sees
     int holes;      // masked: some tile in [kt0, n_kt) is all -inf for both slots (must be skipped)
 };
 
@@ -167,10 +177,34 @@ __device__ __forceinline__ int paged_units_per_entry(const TcParams& p) {
     return p.pack ? p.Hkv : (p.pair_heads ? p.Hkv * (p.g / 2) : p.Hq);
 }
 
+// Run [lo, hi) of keys that query row `row` of a unit sees in a modified
+// variant; `pos` is the row's position, kv_len the sequence's keys.  Both ends
+// never decrease along the rows, so a unit's first and last row bound its range.
 template <int MODE>
+__device__ __forceinline__ int2 row_range(const TcParams& p, int b, int row, int pos, int kv_len) {
+    int lo = 0, hi = kv_len;
+    if (p.causal) {
+        hi = pos + 1;
+        if (p.mod.prefix) hi = max(hi, __ldg(p.mod.prefix + b));
+    } else if (p.mod.window > 0) {
+        hi = min(hi, pos + p.mod.window);
+    }
+    if (p.mod.window > 0) lo = max(0, pos - p.mod.window + 1);
+    if constexpr (MODE == MODE_DENSE) {
+        if (p.doc_rows) {
+            const int2 doc = __ldg(p.doc_rows + (long)b * p.T + row);
+            lo = max(lo, doc.x);
+            hi = min(hi, doc.y);
+        }
+    }
+    return make_int2(lo, min(hi, kv_len));
+}
+
+template <int MODE, int MOD>
 __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
     Unit U;
     U.holes = 0;
+    U.kv_lo = 0;
     if constexpr (MODE == MODE_PAGED) {
         const int per_entry = paged_units_per_entry(p);
         const int e = u / per_entry, rest = u % per_entry;
@@ -205,22 +239,36 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
         }
         U.kv_len = cl;
         U.pos_off = cl - ql;
-        const int kv_end = p.causal ? min(cl, cl - ql + last) : cl;
-        U.kt0 = 0;
-        U.n_kt = (kv_end + kTcRows - 1) / kTcRows;
+        if constexpr (MOD != 0) {
+            U.kv_lo = row_range<MODE>(p, seq, U.row0[0], U.pos_off + U.row0[0], cl).x;
+            U.kt0 = U.kv_lo / kTcRows;
+            U.n_kt = (row_range<MODE>(p, seq, last - 1, U.pos_off + last - 1, cl).y + kTcRows - 1) / kTcRows;
+        } else {
+            const int kv_end = p.causal ? min(cl, cl - ql + last) : cl;
+            U.kt0 = 0;
+            U.n_kt = (kv_end + kTcRows - 1) / kTcRows;
+        }
     } else {
         const int nqt = (p.Tq + kTcRows - 1) / kTcRows;  // query tiles of this launch
         const int qt0 = p.q0 / kTcRows;                  // its first tile within the sequence
         if (p.pair_heads) {
             const int half = p.g / 2;
-            const int upt = p.B * p.Hkv * half;
+            bool listed = false;  // documents: entries (sequence, query tile), longest first
+            if constexpr (MOD != 0) listed = p.doc_order != nullptr;
+            const int upt = (listed ? 1 : p.B) * p.Hkv * half;
             const int rank = u / upt, rest = u % upt;
             int qt;
+            U.b = rest / (p.Hkv * half);
             if constexpr (MODE == MODE_MASKED)
                 qt = __ldg(p.qt_order + rank);
             else
                 qt = p.causal ? nqt - 1 - rank : rank;
-            U.b = rest / (p.Hkv * half);
+            if constexpr (MOD != 0)
+                if (listed) {
+                    const int e = __ldg(p.doc_order + rank);
+                    U.b = e / nqt;
+                    qt = e % nqt;
+                }
             U.hk = (rest / half) % p.Hkv;
             const int pp = rest % half;
             U.head[0] = U.hk * p.g + 2 * pp;
@@ -228,10 +276,18 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
             U.row0[0] = U.row0[1] = (qt0 + qt) * kTcRows;
         } else {
             const int ntp = (nqt + 1) / 2;
-            const int upt = p.B * p.Hq;
+            bool listed = false;
+            if constexpr (MOD != 0) listed = p.doc_order != nullptr;
+            const int upt = (listed ? 1 : p.B) * p.Hq;
             const int rank = u / upt, rest = u % upt;
-            const int pt = (p.causal && MODE == MODE_DENSE) ? ntp - 1 - rank : rank;
+            int pt = (p.causal && MODE == MODE_DENSE) ? ntp - 1 - rank : rank;
             U.b = rest / p.Hq;
+            if constexpr (MOD != 0)
+                if (listed) {
+                    const int e = __ldg(p.doc_order + rank);
+                    U.b = e / ntp;
+                    pt = e % ntp;
+                }
             U.head[0] = U.head[1] = rest % p.Hq;
             U.hk = U.head[0] / p.g;
             U.row0[0] = (qt0 + 2 * pt) * kTcRows;
@@ -246,9 +302,15 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
         }
         U.kv_len = p.Tk;
         U.pos_off = 0;  // rows and keys are both absolute positions in the sequence
-        const int kv_end = p.causal ? min(p.Tk, last) : p.Tk;
-        U.kt0 = 0;
-        U.n_kt = (kv_end + kTcRows - 1) / kTcRows;
+        if constexpr (MOD != 0) {
+            U.kv_lo = row_range<MODE>(p, U.b, U.row0[0], U.row0[0], p.Tk).x;
+            U.kt0 = U.kv_lo / kTcRows;
+            U.n_kt = (row_range<MODE>(p, U.b, last - 1, last - 1, p.Tk).y + kTcRows - 1) / kTcRows;
+        } else {
+            const int kv_end = p.causal ? min(p.Tk, last) : p.Tk;
+            U.kt0 = 0;
+            U.n_kt = (kv_end + kTcRows - 1) / kTcRows;
+        }
         if constexpr (MODE == MODE_MASKED) {
             // restrict the scan to the KV tiles the mask leaves visible; the
             // tiles inside that range need a per-tile class check only when
@@ -402,6 +464,37 @@ __device__ __noinline__ float masked_logits_row(uint32_t taddr, const float* mro
     return fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])), fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
 }
 
+// The same for a modified tile that one multiply-add per score cannot do: a
+// distance bias on a tile with keys on both sides of the row's position, or a
+// cap together with a bias.  Columns outside [vlo, vlim) get -inf; d0 is the
+// first column's key minus the row's position.
+__device__ __noinline__ float modified_logits_row(uint32_t taddr, int vlo, int vlim, float scale_log2, float cap_in,
+                                                  float cap_out, float slope, int d0) {
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+        uint32_t raw[32];
+        __syncwarp();  // warp-collective TMEM accesses
+        tmem_ld32(taddr + h * 32, raw);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int c = h * 32 + j;
+            const float z = __uint_as_float(raw[j]);
+            float x = cap_out > 0.f ? cap_out * tanh_f32(z * cap_in) : z * scale_log2;
+            x = fmaf(-slope, fabsf((float)(d0 + c)), x);
+            if (c < vlo || c >= vlim) x = -INFINITY;
+            raw[j] = __float_as_uint(x);
+            if (j & 1) mx1 = fmaxf(mx1, x);
+            else mx0 = fmaxf(mx0, x);
+        }
+        __syncwarp();
+        tmem_st32(taddr + h * 32, raw);
+    }
+    tmem_wait_st();
+    return fmaxf(mx0, mx1);
+}
+
 // The i-th unit of this CTA as the MMA and softmax warps see it: in paged mode
 // the one the producer published in mailbox i % kUnitSlots (false if the wait
 // gave up), otherwise the static order.
@@ -441,7 +534,7 @@ __device__ __forceinline__ bool mbar_wait_warp_sleepy(uint64_t* bar, uint32_t pa
 }
 
 // ------------------------------------------------------------------ kernel --
-template <int D, int MODE>
+template <int D, int MODE, int MOD>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const TcParams p,
@@ -511,7 +604,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_arrive(&ufull[0]);
         }
         if (u0 >= 0) {
-            const Unit U0 = decode_unit<MODE>(p, u0);
+            const Unit U0 = decode_unit<MODE, MOD>(p, u0);
             if (unit_active<MODE>(p, U0))
                 for (int s = 0; s < 2; ++s) {
                     mbar_arrive_expect_tx(&qfull[s], C::kTileBytes);
@@ -587,7 +680,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 u = cta_unit(sched, i, G, num_units);
             }
             if (u < 0) break;
-            const Unit U = decode_unit<MODE>(p, u);
+            const Unit U = decode_unit<MODE, MOD>(p, u);
             if (!unit_active<MODE>(p, U)) continue;
             for (int s = 0; s < 2 && ok && i > 0; ++s) {  // unit 0's Q tiles were requested at the start
                 if (!mbar_wait_warp_sleepy(&qempty[s], (qcnt & 1) ^ 1, lim_ns, abort_flag)) {
@@ -614,7 +707,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // tile are read a tile ahead, so their load latency is off the copy path
             auto load_blk = [&](int kt) -> int {
                 const int lb = kt * 8 + lane;
-                return (lane < 8 && lb * 16 < U.kv_len) ? __ldg(p.bt + (long)U.b * p.mbps + lb) : 0;
+                return (lane < 8 && lb * 16 < U.kv_len && lb * 16 + 16 > U.kv_lo)
+                           ? __ldg(p.bt + (long)U.b * p.mbps + lb)
+                           : 0;
             };
             int blk_next = 0;
             if constexpr (MODE == MODE_PAGED) blk_next = load_blk(U.kt0);
@@ -624,7 +719,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if constexpr (MODE == MODE_PAGED) {
                     const int cur = blk_next;
                     if (kt + 1 < U.n_kt) blk_next = load_blk(kt + 1);
-                    if (lane < 8 && (kt * 8 + lane) * 16 < U.kv_len) {
+                    // (blocks wholly before the first key any row sees are not read: zeros)
+                    const int tok = (kt * 8 + lane) * 16;
+                    if (lane < 8 && tok < U.kv_len && tok + 16 > U.kv_lo) {
                         if (cur < 0 || cur >= p.num_blocks)
                             raise_error(p.ctx, ERR_BOUNDS_BIT);
                         else
@@ -677,7 +774,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             bool q0 = false;
             if (qcnt == 0) {
                 const int u0 = cta_unit(sched, 0, G, num_units);
-                q0 = u0 >= 0 && unit_active<MODE>(p, decode_unit<MODE>(p, u0));
+                q0 = u0 >= 0 && unit_active<MODE>(p, decode_unit<MODE, MOD>(p, u0));
             }
             if (qcnt > 0 || q0)
                 for (int s = 0; s < 2; ++s)
@@ -755,7 +852,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 break;
             }
             if (u < 0) break;
-            const Unit U = decode_unit<MODE>(p, u);
+            const Unit U = decode_unit<MODE, MOD>(p, u);
             if (!unit_active<MODE>(p, U)) continue;
             // the next unit's Q tiles take ~1 us to land: a sleeping wait leaves the
             // sub-partition's issue slots to the softmax warps' epilogue
@@ -861,7 +958,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 break;
             }
             if (u < 0) break;
-            const Unit U = decode_unit<MODE>(p, u);
+            const Unit U = decode_unit<MODE, MOD>(p, u);
             // query token of this thread's row, and its head within a packed slot
             const int tok = (MODE == MODE_PAGED && p.pack) ? r >> p.pack_shift : r;
             const int hl = (MODE == MODE_PAGED && p.pack) ? r & (p.g - 1) : 0;
@@ -870,14 +967,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!unit_active<MODE>(p, U)) {
                 if (valid) {
                     float* lse = nullptr;
-                    if constexpr (MODE != MODE_PAGED)
-                        if (p.lse) lse = p.lse + ((long)U.b * p.Hq + sel(U.head, s)) * p.T + row;
+                    if constexpr (MODE == MODE_PAGED) {
+                        if (MOD != 0 && p.lse) lse = p.lse + ((long)sel(U.qtok, s) + tok) * p.Hq + sel(U.head, s) + hl;
+                    } else if (p.lse)
+                        lse = p.lse + ((long)U.b * p.Hq + sel(U.head, s)) * p.T + row;
                     store_zero_row<D>(out_row<D, MODE>(p, U, s, tok, hl), lse);
                 }
                 continue;
             }
             // key j is visible when j <= row + pos_off (causal) and j < kv_len
-            const int vis_end = p.causal ? min(U.kv_len, row + U.pos_off + 1) : U.kv_len;
+            int vis_end = p.causal ? min(U.kv_len, row + U.pos_off + 1) : U.kv_len;
+            int vis_lo = 0;
+            float slope = 0.f;  // distance slope of this row's head, log2 units
+            const int qpos = row + U.pos_off;
+            if constexpr (MOD != 0) {
+                // rows past the slot's last take that row's run (their results are dropped)
+                const int over = max(0, tok - max(0, sel(U.nrows, s) - 1));
+                const int rowc = sel(U.nrows, s) > 0 ? row - over : U.row0[0];
+                const int2 run = row_range<MODE>(p, U.b, rowc, rowc + U.pos_off, U.kv_len);
+                vis_lo = run.x;
+                vis_end = run.y;
+                if constexpr ((MOD & MOD_BIAS) != 0) slope = __ldg(p.mod.slopes + sel(U.head, s) + hl) * kLog2e;
+            }
             float m = -INFINITY, l = 0.f;
             int it = 0;
             // masked mode: this slot's class of the next tile and, for a class-3
@@ -921,6 +1032,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after();
                 const int kv0 = kt * kTcRows;
                 const int lim = vis_end - kv0;  // visible columns of this tile: [0, lim)
+                // causal without a prefix: no key past the row's own is visible
+                [[maybe_unused]] const bool vlim_causal = MOD != 0 && p.causal && !p.mod.prefix;
                 const float* mrow = (cls == 2 && valid) ? p.mask + (long)row * p.T + kv0 : nullptr;
                 // cls is the same for the whole warp (it depends on the slot and the
                 // tile only).  Without mask values (cls 0 or 1) the scores need only
@@ -928,19 +1041,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // mask values (cls 2, "general") the masked, scaled logits are
                 // written back over S in pass 1 so that pass 2 reads them instead of
                 // re-reading the mask.
-                const bool general = cls == 2;
+                bool general = cls == 2;
+                if constexpr ((MOD & MOD_BIAS) != 0)
+                    general = p.mod.cap_out > 0.f ||
+                              !(__all_sync(0xffffffffu, kv0 + kTcRows - 1 <= qpos || vlim_causal) ||
+                                __all_sync(0xffffffffu, kv0 >= qpos));
                 // visible columns of this row: [vlo, vlim); a class-3 tile keeps
                 // the row's run of keys, applied like the causal limit (the
                 // limit path takes the general path's operations, so both give
                 // the same bits)
                 int vlo = 0, vlim = cls == 0 ? 0 : lim;
+                if constexpr (MOD != 0) vlo = vis_lo - kv0;
                 if constexpr (MODE == MODE_MASKED)
                     if (cls == 3) {
                         vlo = run.x;
                         vlim = min(lim, (int)run.y);
                     }
                 // every column of every row of the warp visible and no mask values
-                const bool plain = !general && __all_sync(0xffffffffu, vlo == 0 && vlim >= kTcRows);
+                const bool plain = !general && __all_sync(0xffffffffu, vlo <= 0 && vlim >= kTcRows);
+                float bias_k = 0.f, bias0 = 0.f;  // logit bias of column c: bias_k c + bias0
+                if constexpr ((MOD & MOD_BIAS) != 0) {
+                    const int d0 = kv0 - qpos;
+                    bias_k = (d0 >= 0 && !vlim_causal) ? -slope : slope;
+                    bias0 = bias_k * (float)d0;
+                }
                 // pass 1: row max.  Without mask values the whole 128-column score row
                 // is loaded with one TMEM wait; the general case takes 64 columns per
                 // wait.  8 independent partial maxima / sums keep the reductions off a
@@ -954,7 +1078,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int c = 0; c < kTcRows / 32; ++c)
                         tmem_ld32(trow + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(raw + 32 * c));
                     tmem_wait_ld();
-                    if (plain) {
+                    if constexpr ((MOD & MOD_BIAS) != 0) {
+                        // logit pairs: s scale + (slope (d0 + c)), the distance d0 an integer below 2^24 in size
+#pragma unroll
+                        for (int j = 0; j < kTcRows; j += 2) {
+                            const float2 x = __ffma2_rn(
+                                make_float2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])),
+                                make_float2(p.scale_log2, p.scale_log2),
+                                __ffma2_rn(make_float2((float)j, (float)(j + 1)), make_float2(bias_k, bias_k),
+                                           make_float2(bias0, bias0)));
+                            mxp[(j >> 1) & 7] =
+                                plain ? fmax3f(mxp[(j >> 1) & 7], x.x, x.y)
+                                      : fmax3f(mxp[(j >> 1) & 7], j >= vlo && j < vlim ? x.x : -INFINITY,
+                                               j + 1 >= vlo && j + 1 < vlim ? x.y : -INFINITY);
+                        }
+                    } else if (plain) {
 #pragma unroll
                         for (int j = 0; j < kTcRows; j += 2)
                             mxp[(j >> 1) & 7] =
@@ -966,12 +1104,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 fmax3f(mxp[(j >> 1) & 7], j >= vlo && j < vlim ? __uint_as_float(raw[j]) : -INFINITY,
                                        j + 1 >= vlo && j + 1 < vlim ? __uint_as_float(raw[j + 1]) : -INFINITY);
                     }
+                } else if constexpr ((MOD & MOD_BIAS) != 0) {
+                    mxp[0] = modified_logits_row(trow + s_col, vlo, vlim, p.scale_log2, p.mod.cap_in, p.mod.cap_out,
+                                                 slope, kv0 - qpos);
                 } else {
                     mxp[0] = masked_logits_row(trow + s_col, mrow, lim, p.scale_log2, mrow && ((p.T & 3) == 0));
                 }
                 float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
                                  fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
-                if (!general) mx *= p.scale_log2;
+                if constexpr ((MOD & MOD_CAP) != 0) {  // increasing: the max of the raw scores gives the max logit
+                    mx = mx == -INFINITY ? mx : p.mod.cap_out * tanh_f32(mx * p.mod.cap_in);
+                } else if constexpr ((MOD & MOD_BIAS) == 0) {
+                    if (!general) mx *= p.scale_log2;
+                }
                 const float m_new = fmaxf(m, mx);
                 const bool need = m_new > m + kRescaleThreshold;
                 float alpha = 1.f;
@@ -1004,7 +1149,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tmem_ld32(trow + s_col + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(raw + 32));
                     tmem_wait_ld();
                     uint32_t pk[32];
-                    if (plain || general) {  // every column visible, or masked logits already -inf
+                    if constexpr ((MOD & MOD_CAP) != 0) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int cj = h * 64 + 2 * j;
+                            const float x0 = p.mod.cap_out * tanh_f32(__uint_as_float(raw[2 * j]) * p.mod.cap_in);
+                            const float x1 = p.mod.cap_out * tanh_f32(__uint_as_float(raw[2 * j + 1]) * p.mod.cap_in);
+                            float2 pp = make_float2(fast_exp2(x0 - m_use), fast_exp2(x1 - m_use));
+                            if (!plain) {
+                                pp.x = cj >= vlo && cj < vlim ? pp.x : 0.f;
+                                pp.y = cj + 1 >= vlo && cj + 1 < vlim ? pp.y : 0.f;
+                            }
+                            rsp[j & 3] = __fadd2_rn(rsp[j & 3], pp);
+                            pk[j] = pack_bf16x2(pp.x, pp.y);
+                        }
+                    } else if ((MOD & MOD_BIAS) != 0 && !general) {
+                        const float b0 = fmaf(bias_k, (float)(h * 64), bias0);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int cj = h * 64 + 2 * j;
+                            float2 x = __ffma2_rn(
+                                make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), sc2,
+                                __ffma2_rn(make_float2((float)(2 * j), (float)(2 * j + 1)),
+                                           make_float2(bias_k, bias_k), make_float2(b0, b0)));
+                            x = __fadd2_rn(x, neg_m);
+                            float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            if (!plain) {
+                                pp.x = cj >= vlo && cj < vlim ? pp.x : 0.f;
+                                pp.y = cj + 1 >= vlo && cj + 1 < vlim ? pp.y : 0.f;
+                            }
+                            rsp[j & 3] = __fadd2_rn(rsp[j & 3], pp);
+                            pk[j] = pack_bf16x2(pp.x, pp.y);
+                        }
+                    } else if (plain || general) {  // every column visible, or masked logits already -inf
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const float2 x = __ffma2_rn(
@@ -1055,7 +1232,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             ++oc;
             tc_fence_after();
-            const Unit E = decode_unit<MODE>(p, u);  // re-derived here so its fields are not live across the tile loop
+            const Unit E = decode_unit<MODE, MOD>(p, u);  // re-derived here so its fields are not live across the tile loop
             uint16_t* orow = out_row<D, MODE>(p, E, s, tok, hl);
             const float inv_l = l > 0.f ? 1.f / l : 0.f;
             // 64 columns per TMEM wait; 32-byte stores of the bf16 row
@@ -1069,6 +1246,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     pk[j] = pack_bf16x2(__uint_as_float(raw[2 * j]) * inv_l, __uint_as_float(raw[2 * j + 1]) * inv_l);
+                if constexpr (MOD != 0)
+                    if (!(l > 0.f))  // a row that saw no key: zeros, whatever the values of the tiles it passed
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) pk[j] = 0u;
                 if (valid) {
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4)
@@ -1076,9 +1257,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                      pk[8 * q4 + 3], pk[8 * q4 + 4], pk[8 * q4 + 5], pk[8 * q4 + 6], pk[8 * q4 + 7]);
                 }
             }
-            if constexpr (MODE != MODE_PAGED)
+            if constexpr (MODE != MODE_PAGED) {
                 if (p.lse && valid)
                     p.lse[((long)E.b * p.Hq + sel(E.head, s)) * p.T + row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+            } else if constexpr (MOD != 0) {
+                if (p.lse && valid)
+                    p.lse[((long)sel(E.qtok, s) + tok) * p.Hq + sel(E.head, s) + hl] =
+                        l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+            }
         }
         if (!ok && lane == 0) fail();
     }
@@ -1127,22 +1313,118 @@ __global__ void __launch_bounds__(256) mask_order_kernel(const uint8_t* __restri
 
 fa_status launch_mask_classify(const float* M, int Tq, int Tk, uint8_t* cls, uint8_t* iv, cudaStream_t s);
 
+// ------------------------------------------------------------ documents ---
+// One CTA over the ids [B, T]: a document is a run of equal ids >= 0 within a
+// sequence.  Writes every row's run [first, end) of positions (empty, at the
+// run's first position, for ids < 0), then orders the query entries
+// (entry_tiles tiles of 128 rows) by decreasing number of KV tiles with a
+// counting sort.  `starts` is scratch for the runs' first rows.
+constexpr int kDocRows = 8;  // consecutive ids per thread and pass
+__global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restrict__ ids, int B, int T, int entry_tiles,
+                                                         int2* rows, int* starts, int32_t* __restrict__ order,
+                                                         TcParams p) {
+    extern __shared__ int hist[];  // [nbins + 1]
+    __shared__ int warp_sums[32];
+    const int n = B * T, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int nbins = (T + kTcRows - 1) / kTcRows + 1;
+    for (int i = threadIdx.x; i <= nbins; i += blockDim.x) hist[i] = 0;
+    int carry = 0;
+    for (int base = 0; base < n; base += blockDim.x * kDocRows) {
+        const int i0 = base + threadIdx.x * kDocRows;
+        int id[kDocRows + 1];
+        id[0] = i0 > 0 && i0 <= n ? __ldg(ids + i0 - 1) : 0;
+#pragma unroll
+        for (int k = 0; k < kDocRows; ++k) id[k + 1] = i0 + k < n ? __ldg(ids + i0 + k) : 0;
+        unsigned first = 0;
+#pragma unroll
+        for (int k = 0; k < kDocRows; ++k)
+            if (i0 + k < n && ((i0 + k) % T == 0 || id[k + 1] != id[k])) first |= 1u << k;
+        const int c = __popc(first);
+        int x = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_sums[w] = x;
+        __syncthreads();
+        int before = 0, total = 0;
+        for (int k = 0; k < 32; ++k) {
+            const int t = warp_sums[k];
+            before += k < w ? t : 0;
+            total += t;
+        }
+        int run = carry + before + x - c - 1;
+#pragma unroll
+        for (int k = 0; k < kDocRows; ++k)
+            if (i0 + k < n) {
+                if (first & (1u << k)) starts[++run] = i0 + k;
+                rows[i0 + k] = make_int2(run, id[k + 1]);
+            }
+        carry += total;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) starts[carry] = n;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int2 r = rows[i];
+        const int s0 = i / T * T, lo = starts[r.x] - s0;
+        rows[i] = make_int2(lo, r.y < 0 ? lo : starts[r.x + 1] - s0);
+    }
+    __syncthreads();
+    const int er = entry_tiles * kTcRows, per = (T + er - 1) / er, entries = B * per;
+    auto cost = [&](int e) {
+        const int b = e / per, r0 = e % per * er, r1 = min(T, r0 + er) - 1;
+        auto range = [&](int row) {
+            int lo = 0, hi = T;
+            if (p.causal) hi = p.mod.prefix ? max(row + 1, p.mod.prefix[b]) : row + 1;
+            else if (p.mod.window > 0) hi = min(hi, row + p.mod.window);
+            if (p.mod.window > 0) lo = max(0, row - p.mod.window + 1);
+            const int2 doc = rows[(long)b * T + row];
+            return make_int2(max(lo, doc.x), min(min(hi, doc.y), T));
+        };
+        return max(0, (range(r1).y + kTcRows - 1) / kTcRows - range(r0).x / kTcRows);
+    };
+    for (int e = threadIdx.x; e < entries; e += blockDim.x) atomicAdd(&hist[cost(e)], 1);
+    __syncthreads();
+    if (threadIdx.x == 0) {  // bucket starts, highest cost first
+        int run = 0;
+        for (int b = nbins; b >= 0; --b) {
+            const int c = hist[b];
+            hist[b] = run;
+            run += c;
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < entries; e += blockDim.x) order[atomicAdd(&hist[cost(e)], 1)] = e;
+}
+
 // ------------------------------------------------------------ launchers ---
-template <int D, int MODE>
+template <int D, int MODE, int MOD>
 static fa_status launch_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TcParams& p,
                            int grid, cudaStream_t s, const TcSched& sched) {
-    const fa_status st = raise_dynamic_smem(reinterpret_cast<const void*>(attn_tc_kernel<D, MODE>), TcCfg<D>::kSmem);
+    const fa_status st = raise_dynamic_smem(reinterpret_cast<const void*>(attn_tc_kernel<D, MODE, MOD>), TcCfg<D>::kSmem);
     if (st != FA_OK) return st;
-    attn_tc_kernel<D, MODE><<<grid, kTcThreads, TcCfg<D>::kSmem, s>>>(tq, tk, tv, p, sched);
+    attn_tc_kernel<D, MODE, MOD><<<grid, kTcThreads, TcCfg<D>::kSmem, s>>>(tq, tk, tv, p, sched);
     return cuda_status(cudaGetLastError());
 }
 
-template <int MODE>
+template <int MODE, int MOD = 0>
 static fa_status launch_tc_d(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const TcParams& p, int grid, cudaStream_t s, const TcSched* sched = nullptr) {
     static const TcSched kNone = {};  // n == 0: the unit_of order
     const TcSched& sc = sched ? *sched : kNone;
-    return d == 128 ? launch_tc<128, MODE>(tq, tk, tv, p, grid, s, sc) : launch_tc<64, MODE>(tq, tk, tv, p, grid, s, sc);
+    return d == 128 ? launch_tc<128, MODE, MOD>(tq, tk, tv, p, grid, s, sc)
+                    : launch_tc<64, MODE, MOD>(tq, tk, tv, p, grid, s, sc);
+}
+
+// The variant that a call's score modifiers ask for (p.mod is set).
+template <int MODE>
+static fa_status launch_tc_mod(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const TcParams& p, int grid, cudaStream_t s, const TcSched* sched = nullptr) {
+    if (p.mod.slopes) return launch_tc_d<MODE, MOD_RANGE | MOD_BIAS>(d, tq, tk, tv, p, grid, s, sched);
+    if (p.mod.cap_out > 0.f) return launch_tc_d<MODE, MOD_RANGE | MOD_CAP>(d, tq, tk, tv, p, grid, s, sched);
+    return launch_tc_d<MODE, MOD_RANGE>(d, tq, tk, tv, p, grid, s, sched);
 }
 
 // Balanced unit-to-CTA assignment for dense causal prefill.  A unit's cost is
@@ -1283,39 +1565,48 @@ static int dense_units(const TcParams& p) {
     return p.pair_heads ? p.B * p.Hkv * (p.g / 2) * nqt : p.B * p.Hq * ((nqt + 1) / 2);
 }
 
+// Map of the packed queries [total_q, Hq, d]: one box is a query tile (packed:
+// 128/g tokens x the g heads of a group, row = token * g + head; else 128 tokens
+// of one head).
+fa_status paged_query_map(CUtensorMap* tq, const void* q, int Hq, int Hkv, int d, int total_q) {
+    const int g = Hq / Hkv;
+    const uint32_t qbox[4] = {64, paged_tc_pack(g) ? (uint32_t)g : 1u, (uint32_t)paged_tc_slot_tokens(g), 1};
+    const uint64_t dq[4] = {(uint64_t)d, (uint64_t)Hq, (uint64_t)total_q, 1};
+    const uint64_t sq[3] = {(uint64_t)d * 2, (uint64_t)Hq * d * 2, (uint64_t)total_q * Hq * d * 2};
+    return encode_tmap_bf16_4d(tq, q, dq, sq, qbox);
+}
+
+// Map of a paged cache [num_blocks, Hkv, 16, d]: one box is a (block, kv head).
+// d = 128: 64 channels x 8 rows x 2 halves x 2 row groups, landing as
+// [group][half][8 rows][128 B], the last dimension block * Hkv + head.
+fa_status paged_cache_map(CUtensorMap* tk, const void* cache, int num_blocks, int Hkv, int d) {
+    if (d == 128) {
+        const uint32_t cbox[5] = {64, 8, 2, 2, 1};
+        const uint64_t dc[5] = {64, 8, 2, 2, (uint64_t)num_blocks * Hkv};
+        const uint64_t scs[4] = {256, 128, 2048, 4096};
+        return encode_tmap_bf16_5d(tk, cache, dc, scs, cbox);
+    }
+    const uint32_t cbox[4] = {64, 16, 1, 1};
+    const uint64_t dc[4] = {(uint64_t)d, 16, (uint64_t)Hkv, (uint64_t)num_blocks};
+    const uint64_t scs[3] = {(uint64_t)d * 2, (uint64_t)16 * d * 2, (uint64_t)Hkv * 16 * d * 2};
+    return encode_tmap_bf16_4d(tk, cache, dc, scs, cbox);
+}
+
 fa_status launch_paged_prefill(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                                const int32_t* ctx_lens, const int32_t* q_lens, const int32_t* q_start,
                                const int32_t* work_list, const int32_t* work_count, void* out, int num_seqs,
                                int mbps, int num_blocks, int Hq, int Hkv, int d, int causal, float scale,
-                               int total_q, cudaStream_t s, const DevCtx& ctx) {
+                               int total_q, cudaStream_t s, const DevCtx& ctx, const ScoreMod* mod) {
     (void)num_seqs;
     CUtensorMap tq, tk, tv;
-    const int g = Hq / Hkv;
-    const bool pack = paged_tc_pack(g);
-    // packed: one box is 128/g tokens x the g heads of a group (row = token * g + head)
-    const uint32_t qbox[4] = {64, pack ? (uint32_t)g : 1u, (uint32_t)paged_tc_slot_tokens(g), 1};
-    const uint64_t dq[4] = {(uint64_t)d, (uint64_t)Hq, (uint64_t)total_q, 1};
-    const uint64_t sq[3] = {(uint64_t)d * 2, (uint64_t)Hq * d * 2, (uint64_t)total_q * Hq * d * 2};
-    fa_status st = encode_tmap_bf16_4d(&tq, q, dq, sq, qbox);
-    if (d == 128) {
-        // one box per (block, kv head): 64 channels x 8 rows x 2 halves x 2 row groups,
-        // landing as [group][half][8 rows][128 B]; the last dimension is block * Hkv + head
-        const uint32_t cbox[5] = {64, 8, 2, 2, 1};
-        const uint64_t dc[5] = {64, 8, 2, 2, (uint64_t)num_blocks * Hkv};
-        const uint64_t scs[4] = {256, 128, 2048, 4096};
-        if (st == FA_OK) st = encode_tmap_bf16_5d(&tk, k_cache, dc, scs, cbox);
-        if (st == FA_OK) st = encode_tmap_bf16_5d(&tv, v_cache, dc, scs, cbox);
-    } else {
-        const uint32_t cbox[4] = {64, 16, 1, 1};
-        const uint64_t dc[4] = {(uint64_t)d, 16, (uint64_t)Hkv, (uint64_t)num_blocks};
-        const uint64_t scs[3] = {(uint64_t)d * 2, (uint64_t)16 * d * 2, (uint64_t)Hkv * 16 * d * 2};
-        if (st == FA_OK) st = encode_tmap_bf16_4d(&tk, k_cache, dc, scs, cbox);
-        if (st == FA_OK) st = encode_tmap_bf16_4d(&tv, v_cache, dc, scs, cbox);
-    }
+    const bool pack = paged_tc_pack(Hq / Hkv);
+    fa_status st = paged_query_map(&tq, q, Hq, Hkv, d, total_q);
+    if (st == FA_OK) st = paged_cache_map(&tk, k_cache, num_blocks, Hkv, d);
+    if (st == FA_OK) st = paged_cache_map(&tv, v_cache, num_blocks, Hkv, d);
     if (st != FA_OK) return st;
     TcParams p = base_params(0, 0, Hq, Hkv, causal, scale, out, nullptr, ctx);
     p.pack = pack ? 1 : 0;
-    p.pack_shift = pack ? __builtin_ctz((unsigned)g) : 0;
+    p.pack_shift = pack ? __builtin_ctz((unsigned)(Hq / Hkv)) : 0;
     p.bt = block_table;
     p.ctx_lens = ctx_lens;
     p.q_lens = q_lens;
@@ -1324,6 +1615,11 @@ fa_status launch_paged_prefill(const void* q, const void* k_cache, const void* v
     p.work_count = work_count;
     p.mbps = mbps;
     p.num_blocks = num_blocks;
+    if (mod) {
+        p.mod = *mod;
+        p.lse = mod->lse;
+        return launch_tc_mod<MODE_PAGED>(d, tq, tk, tv, p, sm_count(), s);
+    }
     return launch_tc_d<MODE_PAGED>(d, tq, tk, tv, p, sm_count(), s);
 }
 
@@ -1433,6 +1729,63 @@ fa_status fa_prefill_masked(const void* q, const void* k, const void* v, const f
     const int grid = std::min(p.num_units, sm_count());
     st = launch_tc_d<MODE_MASKED>(d, tq, tk, tv, p, grid, s);
     if (st == FA_OK) set_launch_count(3);
+    return st;
+}
+
+size_t fa_prefill_mod_workspace_size(int B, int T) {
+    if (B <= 0 || T <= 0) return 0;
+    const size_t n = (size_t)B * T, nt = (size_t)(T + kTcRows - 1) / kTcRows;
+    return align256(n * sizeof(int2)) + align256((n + 1) * sizeof(int32_t)) + align256(B * nt * sizeof(int32_t));
+}
+
+fa_status fa_prefill_mod(const void* q, const void* k, const void* v, void* out, float* lse, int B, int T, int Hq,
+                         int Hkv, int d, int causal, float scale, float softcap, const float* alibi_slopes, int window,
+                         const int32_t* prefix_lens, const int32_t* doc_ids, void* ws, size_t ws_bytes,
+                         fa_stream_t stream) {
+    set_launch_count(0);
+    fa_status st = check_prefill_args(q, k, v, out, B, T, Hq, Hkv, d, scale);
+    if (st != FA_OK) return st;
+    ScoreMod mod;
+    if ((st = make_score_mod(&mod, scale, softcap, alibi_slopes, window, causal ? prefix_lens : nullptr, lse)) != FA_OK)
+        return st;
+    if (B == 0 || T == 0) return FA_OK;
+    if ((long)B * T >= (1L << 31) - 8192) return FA_ERR_UNSUPPORTED;
+    const int nt = (T + kTcRows - 1) / kTcRows;
+    const size_t hist_bytes = (size_t)(nt + 2) * sizeof(int);
+    if (doc_ids) {
+        if (!ws || ws_bytes < fa_prefill_mod_workspace_size(B, T) || (reinterpret_cast<uintptr_t>(ws) & 255))
+            return FA_ERR_WORKSPACE;
+        if (hist_bytes > 200 * 1024) return FA_ERR_UNSUPPORTED;
+    }
+    if ((st = check_device()) != FA_OK) return st;
+    DevCtx ctx;
+    if ((st = make_ctx(&ctx)) != FA_OK) return st;
+    CUtensorMap tq, tk, tv;
+    if ((st = dense_maps(q, k, v, B, T, Hq, Hkv, d, &tq, &tk, &tv)) != FA_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    TcParams p = base_params(B, T, Hq, Hkv, causal, scale, out, lse, ctx);
+    p.mod = mod;
+    p.num_units = dense_units(p);
+    int launches = 0;
+    if (doc_ids) {
+        uint8_t* wsb = static_cast<uint8_t*>(ws);
+        int2* rows = reinterpret_cast<int2*>(wsb);
+        int* starts = reinterpret_cast<int*>(wsb + align256((size_t)B * T * sizeof(int2)));
+        int32_t* order = starts + align256(((size_t)B * T + 1) * sizeof(int32_t)) / sizeof(int32_t);
+        if (hist_bytes > 48 * 1024 &&
+            (st = raise_dynamic_smem(reinterpret_cast<const void*>(doc_order_kernel), (int)hist_bytes)) != FA_OK)
+            return st;
+        doc_order_kernel<<<1, 1024, hist_bytes, s>>>(doc_ids, B, T, p.pair_heads ? 1 : 2, rows, starts, order, p);
+        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+        ++launches;
+        p.doc_rows = rows;
+        p.doc_order = order;
+    }
+    const int grid = std::min(p.num_units, sm_count());
+    // unit costs are those of the plain causal problem when only the scores are modified
+    const bool plain_ranges = !mod.prefix && mod.window == 0 && !doc_ids;
+    st = launch_tc_mod<MODE_DENSE>(d, tq, tk, tv, p, grid, s, plain_ranges ? dense_schedule(p, grid) : nullptr);
+    if (st == FA_OK) set_launch_count(launches + 1);
     return st;
 }
 

@@ -150,6 +150,88 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const void* __restrict
     }
 }
 
+// ----------------------------------------- rotary append, several axes ----
+// As rope_append_kernel, but every channel pair j has an axis (time, height,
+// width, ...) and turns by the table row of the token's position on that axis:
+// c, s = columns j, d/2 + j of row positions[axis[j]][token].  A thread takes 8
+// pairs of kMropeRows rows of a token, so that it looks the 16 factors up
+// once for all of them.
+constexpr int kMaxAxes = 4;
+constexpr int kMropeRows = 4;
+struct PairAxes {
+    uint8_t axis[64];
+};
+template <bool kF32>
+__global__ void __launch_bounds__(256) mrope_append_kernel(const void* __restrict__ q, const void* __restrict__ k,
+                                                           const void* __restrict__ v,
+                                                           const int32_t* __restrict__ positions, int n_axes,
+                                                           const PairAxes axes, const float* __restrict__ cos_sin,
+                                                           int max_pos, uint16_t* __restrict__ q_out,
+                                                           uint16_t* __restrict__ kc, uint16_t* __restrict__ vc,
+                                                           const int32_t* __restrict__ slots, int N, int Hq, int Hkv,
+                                                           int d, int num_blocks, DevCtx ctx) {
+    const int half = d >> 1, cph = half >> 3;  // 8-pair chunks per row
+    const int rpt = Hq + Hkv, groups = (rpt + kMropeRows - 1) / kMropeRows;
+    const long total = (long)N * groups * cph;
+    for (long idx = (long)blockIdx.x * blockDim.x + threadIdx.x; idx < total; idx += (long)gridDim.x * blockDim.x) {
+        const int c = (int)(idx % cph);
+        const long gi = idx / cph;
+        const int r0 = (int)(gi % groups) * kMropeRows;
+        const long tok = gi / groups;
+        int pos[kMaxAxes];
+        bool bad = false;
+#pragma unroll
+        for (int a = 0; a < kMaxAxes; ++a) {
+            pos[a] = a < n_axes ? __ldg(positions + (long)a * N + tok) : 0;
+            bad |= pos[a] < 0 || pos[a] >= max_pos;
+        }
+        const int slot = __ldg(slots + tok);
+        if (bad) {  // the token is left out whole
+            raise_error(ctx, ERR_BOUNDS_BIT);
+            continue;
+        }
+        const bool slot_bad = slot >= num_blocks * kBlock;
+        if (slot_bad) raise_error(ctx, ERR_BOUNDS_BIT);
+        float co[8], si[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int a = axes.axis[c * 8 + i];
+            const int p = a == 0 ? pos[0] : (a == 1 ? pos[1] : (a == 2 ? pos[2] : pos[3]));
+            co[i] = __ldg(cos_sin + (long)p * d + c * 8 + i);
+            si[i] = __ldg(cos_sin + (long)p * d + half + c * 8 + i);
+        }
+#pragma unroll
+        for (int rr = 0; rr < kMropeRows; ++rr) {
+            const int r = r0 + rr;
+            const bool is_q = r < Hq;
+            if (r >= rpt || (!is_q && (slot < 0 || slot_bad))) continue;
+            const int h = is_q ? r : r - Hq;
+            const long src = is_q ? (tok * Hq + h) * d : (tok * Hkv + h) * d;
+            float x1[8], x2[8], y1[8], y2[8];
+            load8<kF32>(is_q ? q : k, src + c * 8, x1);
+            load8<kF32>(is_q ? q : k, src + half + c * 8, x2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y1[i] = fmaf(x1[i], co[i], -(x2[i] * si[i]));
+                y2[i] = fmaf(x2[i], co[i], x1[i] * si[i]);
+            }
+            if (is_q) {
+                *reinterpret_cast<uint4*>(q_out + src + c * 8) = pack8(y1);
+                *reinterpret_cast<uint4*>(q_out + src + half + c * 8) = pack8(y2);
+            } else {
+                const long dst = (((long)(slot / kBlock) * Hkv + h) * kBlock + (slot % kBlock)) * d;
+                float v1[8], v2[8];
+                load8<kF32>(v, src + c * 8, v1);
+                load8<kF32>(v, src + half + c * 8, v2);
+                *reinterpret_cast<uint4*>(kc + dst + c * 8) = pack8(y1);
+                *reinterpret_cast<uint4*>(kc + dst + half + c * 8) = pack8(y2);
+                *reinterpret_cast<uint4*>(vc + dst + c * 8) = pack8(v1);
+                *reinterpret_cast<uint4*>(vc + dst + half + c * 8) = pack8(v2);
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------- 8-bit append -----
 // One thread quantises 16 channels of one (token, head) row of K and of V:
 // code = E4M3(x / scale) (binary32 division, round to nearest even,
@@ -472,6 +554,42 @@ fa_status fa_cache_append_rope(const void* q, const void* k, const void* v, cons
         rope_append_kernel<false><<<grid_for(work, 256), 256, 0, s>>>(
             q, k, v, positions, cos_sin, max_pos, static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_cache),
             static_cast<uint16_t*>(v_cache), slot_mapping, N, Hq, Hkv, d, num_blocks, ctx);
+    st = cuda_status(cudaGetLastError());
+    if (st == FA_OK) set_launch_count(1);
+    return st;
+}
+
+fa_status fa_cache_append_mrope(const void* q, const void* k, const void* v, const int32_t* positions, int n_axes,
+                                const uint8_t* pair_axes, const float* cos_sin, int max_pos, void* q_out,
+                                void* k_cache, void* v_cache, const int32_t* slot_mapping, int N, int Hq, int Hkv,
+                                int d, int num_blocks, fa_dtype in_dtype, fa_stream_t stream) {
+    set_launch_count(0);
+    if (N < 0 || Hq <= 0 || Hkv <= 0 || num_blocks < 0 || max_pos <= 0 || n_axes <= 0) return FA_ERR_INVALID_ARG;
+    if (in_dtype != FA_BF16 && in_dtype != FA_F32) return FA_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || n_axes > kMaxAxes) return FA_ERR_UNSUPPORTED;
+    if (!pair_axes) return FA_ERR_INVALID_ARG;
+    PairAxes axes{};
+    for (int j = 0; j < d / 2; ++j) {
+        if (pair_axes[j] >= n_axes) return FA_ERR_INVALID_ARG;
+        axes.axis[j] = pair_axes[j];
+    }
+    if (N == 0) return FA_OK;
+    if (!q || !k || !v || !positions || !cos_sin || !q_out || !k_cache || !v_cache || !slot_mapping)
+        return FA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cos_sin) || !aligned16(q_out) ||
+        !aligned16(k_cache) || !aligned16(v_cache))
+        return FA_ERR_INVALID_ARG;
+    fa_status st = check_device();
+    if (st != FA_OK) return st;
+    DevCtx ctx;
+    if ((st = make_ctx(&ctx)) != FA_OK) return st;
+    const long work = (long)N * ((Hq + Hkv + kMropeRows - 1) / kMropeRows) * (d / 16);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto kernel = in_dtype == FA_F32 ? mrope_append_kernel<true> : mrope_append_kernel<false>;
+    kernel<<<grid_for(work, 256), 256, 0, s>>>(q, k, v, positions, n_axes, axes, cos_sin, max_pos,
+                                               static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_cache),
+                                               static_cast<uint16_t*>(v_cache), slot_mapping, N, Hq, Hkv, d, num_blocks,
+                                               ctx);
     st = cuda_status(cudaGetLastError());
     if (st == FA_OK) set_launch_count(1);
     return st;

@@ -293,6 +293,43 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// tanh in fp32.  |u| <= 1: u times a degree-6 polynomial in u^2, a minimax fit of
+// tanh(u) / u made for this file (relative error 5e-8, 1.6e-7 as evaluated);
+// beyond, 1 - 2 / (1 + e^(2|u|)), whose cancellation is harmless there (absolute
+// error below 3e-7).  The hardware's tanh.approx is off by up to 2^-11, which a
+// cap of 50 would turn into 0.02 on a logit.
+constexpr float kTanhC0 = 0.99999994f, kTanhC1 = -0.3333284f, kTanhC2 = 0.13325204f, kTanhC3 = -0.053457025f,
+                kTanhC4 = 0.020289972f, kTanhC5 = -0.006203373f, kTanhC6 = 0.0010410206f;
+__device__ __forceinline__ float tanh_f32(float u) {
+    const float a = fabsf(u), w = u * u;
+    float t = fmaf(kTanhC6, w, kTanhC5);
+    t = fmaf(t, w, kTanhC4);
+    t = fmaf(t, w, kTanhC3);
+    t = fmaf(t, w, kTanhC2);
+    t = fmaf(t, w, kTanhC1);
+    t = fmaf(t, w, kTanhC0);
+    const float e = fast_exp2(a * 2.885390081777927f);  // e^(2a); +inf gives 1
+    const float big = copysignf(1.f - __fdividef(2.f, 1.f + e), u);
+    return a <= 1.f ? u * t : big;
+}
+
+// ------------------------------------------------------- score modifiers ---
+// Logit of query position i and key position j for dot product s, in log2
+// units:  f(s) - slope_h log2(e) |i - j|,  f(s) = s scale log2(e), or with a cap
+// c log2(e) tanh(s scale / c).  Key j is visible when every mask given allows
+// it: causal or prefix (j <= i, or j < prefix), window (j > i - window; without
+// the causal flag also j < i + window), and the documents (dense only).
+struct ScoreMod {
+    float cap_in;           // scale / cap
+    float cap_out;          // cap * log2(e); 0: no cap
+    const float* slopes;    // fp32 [Hq], or null
+    const int32_t* prefix;  // int32 per sequence, or null
+    int window;             // 0: none
+    float* lse;             // fp32 log-sum-exp per row ([rows, Hq] paged), or null
+    float* logits;          // decode rows: logits kept for the weight sums (log2 units), or null
+    int logit_rows;         // rows a page's logits take in that buffer
+};
+
 // Four E4M3 bytes (byte i = element i) to two f16x2 words: lo = elements
 // 0, 1 and hi = elements 2, 3 (exact: every E4M3 value is an f16 value).
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t& lo, uint32_t& hi) {

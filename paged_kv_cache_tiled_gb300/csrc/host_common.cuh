@@ -39,10 +39,31 @@ fa_status encode_tmap_bf16_5d(CUtensorMap* map, const void* base, const uint64_t
 fa_status encode_tmap_4d(CUtensorMap* map, const void* base, const uint64_t dims[4], const uint64_t strides_bytes[3],
                          const uint32_t box[4], CUtensorMapDataType dtype, CUtensorMapSwizzle swizzle);
 
+// Tensor maps of the paged tensor-core kernels (defined in attn_tc.cu).
+fa_status paged_query_map(CUtensorMap* tq, const void* q, int Hq, int Hkv, int d, int total_q);
+fa_status paged_cache_map(CUtensorMap* tk, const void* cache, int num_blocks, int Hkv, int d);
+
 // Prefill of query rows [q0, q0 + Tq) of every sequence against keys [0, Tk)
 // (defined in attn_tc.cu; used by the host-buffer pipeline).
 fa_status launch_prefill_rows(const void* q, const void* k, const void* v, void* out, int B, int T, int Hq, int Hkv,
                               int d, int causal, float scale, int q0, int Tq, int Tk, cudaStream_t s);
+
+// Checks and packs the score modifiers of a call (lse may be null).  A window
+// beyond any length the library can hold is the same as a very long one.
+inline fa_status make_score_mod(ScoreMod* m, float scale, float softcap, const float* slopes, int window,
+                                const int32_t* prefix, float* lse) {
+    if (!(softcap >= 0.f) || !(softcap < INFINITY) || window < 0) return FA_ERR_INVALID_ARG;
+    *m = ScoreMod{};
+    if (softcap > 0.f) {
+        m->cap_in = scale / softcap;
+        m->cap_out = softcap * 1.4426950408889634f;
+    }
+    m->slopes = slopes;
+    m->prefix = prefix;
+    m->window = window < (1 << 29) ? window : (1 << 29);
+    m->lse = lse;
+    return FA_OK;
+}
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

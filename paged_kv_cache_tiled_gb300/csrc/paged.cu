@@ -44,7 +44,13 @@ fa_status launch_paged_prefill(const void* q, const void* k_cache, const void* v
                                const int32_t* ctx_lens, const int32_t* q_lens, const int32_t* q_start,
                                const int32_t* work_list, const int32_t* work_count, void* out, int num_seqs,
                                int mbps, int num_blocks, int Hq, int Hkv, int d, int causal, float scale,
-                               int total_q, cudaStream_t s, const DevCtx& ctx);
+                               int total_q, cudaStream_t s, const DevCtx& ctx, const ScoreMod* mod);
+// Weight sums of the sequences that take the tensor-core path (attn_colsum.cu).
+fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* block_table, const int32_t* ctx_lens,
+                             const int32_t* q_lens, const int32_t* q_start, const float* lse, const float* acc_in,
+                             float* acc_out, int acc_len, float decay, int num_seqs, int mbps, int num_blocks, int Hq,
+                             int Hkv, int d, int causal, float scale, int total_q, const ScoreMod& mod, cudaStream_t s,
+                             const DevCtx& ctx);
 
 __host__ __device__ inline bool is_decode_row(int q_len, int g) { return q_len >= 1 && g * q_len <= kDecodeRows; }
 
@@ -92,13 +98,19 @@ inline PagedWs paged_ws_layout(int num_seqs, int mbps, int Hq, int Hkv, int d, i
 // or 2c+1 (its last) for the merge kernel.  Every page is read once; every warp
 // streams the same number of bytes, so no SM waits on a long sequence.
 
+// First block of a context that a query of its chunk can see through a sliding
+// window (0: no window): the chunk's first query sits at cl - ql.
+__device__ __forceinline__ int first_block(int cl, int ql, int window) {
+    return window > 0 ? max(0, cl - ql - window + 1) / kBS : 0;
+}
+
 // Pages one kv head of sequence s contributes to the decode stream (0 when the
 // sequence takes the tensor-core path or its lengths are inconsistent).
 __device__ __forceinline__ int decode_blocks(const int32_t* __restrict__ q_lens, const int32_t* __restrict__ ctx_lens,
-                                             int s, int g, int mbps) {
+                                             int s, int g, int mbps, int window) {
     const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s);
     if (!is_decode_row(ql, g) || ql > cl || cl > mbps * kBS) return 0;
-    return (cl + kBS - 1) / kBS;
+    return (cl + kBS - 1) / kBS - first_block(cl, ql, window);
 }
 
 // The stream partition: warp w of W starts at page floor(w * P / W).  With
@@ -147,6 +159,7 @@ struct StreamSmem {
 // Position of a stream cursor: sequence, kv head, block within the sequence.
 struct Cursor {
     int s, hk, blk, nblk;  // nblk: pages per kv head of sequence s
+    int blk0;              // block of the sequence that page 0 is (0 without a window)
     int q0;                // first packed query row of sequence s
 };
 
@@ -160,15 +173,23 @@ struct Cursor {
 // = elements (4t .. 4t+3); queries are loaded in the same order for Q K^T,
 // and for P V the S tile's columns (tokens) are produced in that order by
 // loading K rows 4t+2nt+e into n-tile nt, column 2t+e.
+// MOD 1 applies the score modifiers `mod` (cap, distance slopes, window, prefix)
+// and writes the rows' log-sum-exp; a window drops whole blocks from the
+// stream.  MOD 2 also keeps every logit (log2 units, -inf where masked) at
+// [page of the stream][row][token] for the weight sums that need the final
+// log-sum-exp: logit_rows * 64 bytes beside the page's 64 d.
 constexpr int kLensPerLane = 8;  // sequences per lane whose lengths are loaded in one batch
-template <int D, bool KV8, int ROWS>
+constexpr float kLn2f = 0.6931471805599453f, kLog2ef = 1.4426950408889634f;
+template <int D, bool KV8, int ROWS, int MOD>
 __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const uint16_t* __restrict__ q, const int32_t* __restrict__ bt,
                         const int32_t* __restrict__ ctx_lens, const int32_t* __restrict__ q_lens,
                         uint16_t* __restrict__ out, float* __restrict__ part_o, float2* __restrict__ part_ml,
                         int num_seqs, int mbps, int num_blocks, int Hq, int Hkv, int q_prefetch_rows, int causal,
-                        float scale_log2, float v_scale, DevCtx ctx) {
+                        float scale_log2, float v_scale, DevCtx ctx, ScoreMod mod) {
+    static_assert(MOD == 0 || !KV8, "score modifiers are built for the bf16 cache");
+    const int window = MOD ? mod.window : 0;
     // the merge kernel that follows may be scheduled now; it waits for this
     // grid's completion before reading anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -225,7 +246,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
             bad = true;
             return;
         }
-        my_p += (long long)Hkv * ((cl + kBS - 1) / kBS);
+        my_p += (long long)Hkv * ((cl + kBS - 1) / kBS - first_block(cl, ql, window));
     };
     if (per <= kLensPerLane) {
         int qv[kLensPerLane], cv[kLensPerLane];
@@ -271,8 +292,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
             for (int s = s_lo; s < s_hi; ++s) {
                 const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s);
                 const long long n =
-                    (is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS) ? (long long)Hkv * ((cl + kBS - 1) / kBS)
-                                                                            : 0;
+                    (is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS)
+                        ? (long long)Hkv * ((cl + kBS - 1) / kBS - first_block(cl, ql, window))
+                        : 0;
                 if (off < n) {
                     a_s = s;
                     a_off = (int)off;
@@ -286,7 +308,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         start.s = __shfl_sync(0xffffffffu, a_s, src);
         a_off = __shfl_sync(0xffffffffu, a_off, src);
         start.q0 = __shfl_sync(0xffffffffu, a_q0, src);
-        start.nblk = decode_blocks(q_lens, ctx_lens, start.s, g, mbps);
+        start.nblk = decode_blocks(q_lens, ctx_lens, start.s, g, mbps, window);
+        start.blk0 = MOD ? first_block(__ldg(ctx_lens + start.s), __ldg(q_lens + start.s), window) : 0;
         start.hk = a_off / start.nblk;
         start.blk = a_off % start.nblk;
     }
@@ -308,14 +331,16 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         do {
             c.q0 += __ldg(q_lens + c.s);
             ++c.s;
-            c.nblk = c.s < num_seqs ? decode_blocks(q_lens, ctx_lens, c.s, g, mbps) : 0;
+            c.nblk = c.s < num_seqs ? decode_blocks(q_lens, ctx_lens, c.s, g, mbps, window) : 0;
         } while (c.s < num_seqs && c.nblk == 0);
+        if constexpr (MOD != 0)
+            if (c.s < num_seqs) c.blk0 = first_block(__ldg(ctx_lens + c.s), __ldg(q_lens + c.s), window);
     };
 
     Cursor ci = start;  // issue cursor (lane 0 only)
     // lane 0 reads the block-table entry of the next page one issue ahead, so
     // that load's latency is not on the copy's path
-    int next_phys = lane == 0 ? __ldg(bt + (long)ci.s * mbps + ci.blk) : 0;
+    int next_phys = lane == 0 ? __ldg(bt + (long)ci.s * mbps + ci.blk0 + ci.blk) : 0;
     auto issue = [&](int i) {
         const int stage = i % kStreamStages;
         int phys = next_phys;
@@ -337,7 +362,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
             }
         }
         advance(ci);
-        if (i + 1 < n_pages) next_phys = __ldg(bt + (long)ci.s * mbps + ci.blk);
+        if (i + 1 < n_pages) next_phys = __ldg(bt + (long)ci.s * mbps + ci.blk0 + ci.blk);
     };
     bool ok = !ctx.force_timeout || mbar_wait_warp(never, 0, ctx.wait_ns, abort_flag);
     if (!ok && lane == 0) {
@@ -355,6 +380,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     long long seg_last_first = seg_first;
     int seg_last_rows = 0, first_rows = -1;  // and the first segment's query rows
     int ctx_len = 0, q_len = 0, nrows = 0, pos_r0 = 0, pos_r1 = 0;
+    int qpos[2] = {0, 0}, lo_r[2] = {0, 0};  // MOD: position and first visible key of rows gid, gid + 8
+    float slope[2] = {0.f, 0.f};             // MOD: their distance slopes (log2 units)
     uint32_t qa[D / 16][4];
     float o[D / 8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
@@ -399,6 +426,21 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         // keys <= pos(row) are visible
         pos_r0 = causal ? ctx_len - q_len + gid / g : ctx_len - 1;
         pos_r1 = causal ? ctx_len - q_len + (gid + 8) / g : ctx_len - 1;
+        if constexpr (MOD != 0) {
+            const int prefix = causal && mod.prefix ? __ldg(mod.prefix + cc.s) : 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                qpos[i] = ctx_len - q_len + rr[i] / g;
+                lo_r[i] = window > 0 ? qpos[i] - window + 1 : 0;
+                slope[i] = mod.slopes && rr[i] < nrows ? __ldg(mod.slopes + cc.hk * g + rr[i] % g) * kLog2ef : 0.f;
+            }
+            pos_r0 = max(pos_r0, prefix - 1);
+            pos_r1 = max(pos_r1, prefix - 1);
+            if (!causal && window > 0) {
+                pos_r0 = min(pos_r0, qpos[0] + window - 1);
+                pos_r1 = min(pos_r1, qpos[1] + window - 1);
+            }
+        }
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
         m0 = m1 = -INFINITY;
@@ -421,6 +463,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
                 if (r >= nrows) continue;
                 const float inv = ls[i] > 0.f ? v_scale / ls[i] : 0.f;
                 uint16_t* dst = out + ((long)(cc.q0 + r / g) * Hq + cc.hk * g + r % g) * D;
+                if constexpr (MOD != 0)
+                    if (mod.lse && tig == 0)
+                        mod.lse[(long)(cc.q0 + r / g) * Hq + cc.hk * g + r % g] =
+                            ls[i] > 0.f ? (ml[i] + __log2f(ls[i])) * kLn2f : -INFINITY;
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
                     *reinterpret_cast<uint32_t*>(dst + n * 8 + tig * 2) =
@@ -461,7 +507,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         }
         const uint32_t kbase = smem_u32(ring + stage * L::kStage);
         const uint32_t vbase = kbase + L::kPage;
-        const int tok0 = cc.blk * kBS;
+        const int tok0 = (cc.blk0 + cc.blk) * kBS;
 
         // S = Q K^T : 16 rows x 16 tokens
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -500,8 +546,24 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
             for (int e = 0; e < 4; ++e) {
                 const int t = KV8 ? tok0 + tig * 4 + nt * 2 + (e & 1) : tok0 + nt * 8 + tig * 2 + (e & 1);
                 const int lim = (e < 2) ? pos_r0 : pos_r1;
-                x[nt][e] = (t <= lim && t < ctx_len) ? sc[nt][e] * scale_log2 : -INFINITY;
+                if constexpr (MOD != 0) {
+                    float z = mod.cap_out > 0.f ? mod.cap_out * tanh_f32(sc[nt][e] * mod.cap_in) : sc[nt][e] * scale_log2;
+                    z = fmaf(-slope[e >> 1], fabsf((float)(t - qpos[e >> 1])), z);
+                    x[nt][e] = (t <= lim && t < ctx_len && t >= lo_r[e >> 1]) ? z : -INFINITY;
+                } else {
+                    x[nt][e] = (t <= lim && t < ctx_len) ? sc[nt][e] * scale_log2 : -INFINITY;
+                }
             }
+        if constexpr (MOD == 2) {
+            float* lg = mod.logits + (long)(b0 + i) * mod.logit_rows * kBS + tig * 2;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int rr = 0; rr < 2; ++rr)
+                    if (gid + 8 * rr < min(nrows, mod.logit_rows))
+                        *reinterpret_cast<float2*>(lg + (gid + 8 * rr) * kBS + nt * 8) =
+                            make_float2(x[nt][2 * rr], x[nt][2 * rr + 1]);
+        }
         float mx0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
         float mx1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
@@ -695,6 +757,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         if (t.x < 0) {
             const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
             uint16_t* dst = out + ((long)(h.x + r / g) * Hq + h.y * g + r % g) * D + lane * kPer;
+            if constexpr (MOD != 0)
+                if (mod.lse && lane == 0)
+                    mod.lse[(long)(h.x + r / g) * Hq + h.y * g + r % g] =
+                        lsum > 0.f ? (M + __log2f(lsum)) * kLn2f : -INFINITY;
             if constexpr (kPer == 4)
                 *reinterpret_cast<uint2*>(dst) =
                     make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
@@ -722,12 +788,13 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
 // trip.  The programmatic launch lets the CTAs compute their offsets as decode
 // CTAs exit; they read partials only after griddepcontrol.wait.
 constexpr int kMergeMaxThreads = 32 * kDecodeRows;
-template <int D>
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const int32_t* __restrict__ ctx_lens,
                                                                     const int32_t* __restrict__ q_lens,
                                                                     const float* part_o, const float2* part_ml,
                                                                     uint16_t* __restrict__ out, int num_seqs,
-                                                                    int Hq, int Hkv, int mbps, int W) {
+                                                                    int Hq, int Hkv, int mbps, int W, ScoreMod mod) {
+    const int window = MOD ? mod.window : 0;
     // one warp per output row: warp w of CTA (s, hk) merges row w
     const int s = blockIdx.x, hk = blockIdx.y, r = threadIdx.x >> 5, g = Hq / Hkv;
     const int lane = threadIdx.x & 31;
@@ -738,12 +805,14 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
-    const int nblk = (cl_s + kBS - 1) / kBS;
+    const int nblk = (cl_s + kBS - 1) / kBS - first_block(cl_s, ql_s, window);
     // inputs only so far: total pages, this sequence's first page and query row
     long long tot = 0, pre = 0, q0 = 0;
     for (int i = lane; i < num_seqs; i += 32) {
         const int ql = __ldg(q_lens + i), cl = __ldg(ctx_lens + i);
-        const long long n = (is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS) ? (cl + kBS - 1) / kBS : 0;
+        const long long n = (is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS)
+                                ? (cl + kBS - 1) / kBS - first_block(cl, ql, window)
+                                : 0;
         tot += n;
         if (i < s) {
             pre += n;
@@ -880,12 +949,81 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+    if constexpr (MOD != 0)
+        if (mod.lse && lane == 0)
+            mod.lse[(long)(q0 + r / g) * Hq + hk * g + r % g] = lsum > 0.f ? (M + __log2f(lsum)) * kLn2f : -INFINITY;
     uint16_t* dst = out + ((long)(q0 + r / g) * Hq + hk * g + r % g) * D + lane * kPer;
     if constexpr (kPer == 4)
         *reinterpret_cast<uint2*>(dst) =
             make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
     else
         *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+}
+
+// --------------------------------------------------------- weight sums -----
+// acc_out[s][hk][t] = decay acc_in[s][hk][t] (0 for the chunk's own tokens, and
+// without acc_in) + sum over the sequence's query rows r of the group of
+// 2^(x_rt - lse_r), from the logits x that the decode kernel kept and the
+// final log-sum-exp: sequences that took the decode kernel, and those without
+// queries.  Memory bound: rows * 4 bytes a key read, 8 bytes of sums.  The sum
+// over rows runs in a fixed order.  CTA (s, hk, split): pages
+// [kAccumPages split, + kAccumPages) of the context, a half-warp per page.
+constexpr int kAccumPages = 64;  // pages per CTA
+__global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __restrict__ ctx_lens,
+                                                           const int32_t* __restrict__ q_lens,
+                                                           const float* __restrict__ lse,
+                                                           const float* __restrict__ logits, int logit_rows,
+                                                           const float* acc_in, float* acc_out, int acc_len,
+                                                           float decay, int num_seqs, int mbps, int Hq, int Hkv,
+                                                           int window, DevCtx ctx) {
+    const int s = blockIdx.x, hk = blockIdx.y, g = Hq / Hkv, lane = threadIdx.x & 31;
+    const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s);
+    if (ql > cl || ql < 0 || cl > mbps * kBS || (ql > 0 && !is_decode_row(ql, g))) return;
+    const int p0 = blockIdx.z * kAccumPages;
+    const int npages = (cl + kBS - 1) / kBS;
+    if (p0 >= npages) return;
+    if (cl > acc_len) {
+        if (threadIdx.x == 0) raise_error(ctx, ERR_BOUNDS_BIT);
+        return;
+    }
+    __shared__ float neg_lse2[kDecodeRows];
+    long long pre = 0, q0 = 0;  // pages and query rows of the sequences before s (every warp)
+    if (ql > 0) {
+        for (int i = lane; i < s; i += 32) {
+            const int qi = __ldg(q_lens + i), ci = __ldg(ctx_lens + i);
+            if (is_decode_row(qi, g) && qi <= ci && ci <= mbps * kBS)
+                pre += (ci + kBS - 1) / kBS - first_block(ci, qi, window);
+            q0 += qi;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            pre += __shfl_xor_sync(0xffffffffu, pre, o);
+            q0 += __shfl_xor_sync(0xffffffffu, q0, o);
+        }
+    }
+    const int nrows = ql > 0 ? min(g * ql, logit_rows) : 0;
+    if (threadIdx.x < nrows) {
+        const int r = threadIdx.x;
+        const float L = lse[(q0 + r / g) * Hq + hk * g + r % g];
+        neg_lse2[r] = L == -INFINITY ? 0.f : -L * kLog2ef;
+    }
+    __syncthreads();
+    const int blk0 = ql > 0 ? first_block(cl, ql, window) : 0;
+    const long long seg = pre * Hkv + (long long)hk * (npages - blk0);  // the segment's first page of the stream
+    const long row = ((long)s * Hkv + hk) * acc_len;
+    const int i = threadIdx.x & 15;
+    for (int p = p0 + (threadIdx.x >> 4); p < min(npages, p0 + kAccumPages); p += 16) {
+        const int t = p * kBS + i;
+        if (t >= cl) continue;
+        float a = acc_in && t < cl - ql ? decay * acc_in[row + t] : 0.f;
+        if (p >= blk0) {
+            const float* x = logits + (seg + p - blk0) * logit_rows * kBS + i;
+            float w = 0.f;
+            for (int r = 0; r < nrows; ++r) w += fast_exp2(__ldg(x + r * kBS) + neg_lse2[r]);
+            a += w;
+        }
+        acc_out[row + t] = a;
+    }
 }
 
 // ------------------------------------------------------------ metadata -----
@@ -899,6 +1037,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
                                                           int g, int causal, int entry_tokens,
                                                           int32_t* __restrict__ q_start, int32_t* __restrict__ count,
                                                           int32_t* __restrict__ list, int max_entries,
+                                                          int window, const int32_t* __restrict__ prefix,
                                                           DevCtx ctx) {
     extern __shared__ int hist[];  // [nbins + 1]
     __shared__ int warp_sums[32];
@@ -938,10 +1077,12 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     }
     if (threadIdx.x == 0) q_start[num_seqs] = carry;
     // histogram of entry costs
-    auto entry_cost = [&](int ql, int cl, int t0) {
+    auto entry_cost = [&](int s, int ql, int cl, int t0) {
         const int last_row = min(ql, t0 + entry_tokens) - 1;  // last query row of the entry
-        const int kv_end = causal ? cl - ql + last_row + 1 : cl;
-        return (kv_end + 127) / 128;
+        int kv_end = causal ? cl - ql + last_row + 1 : cl;
+        if (causal && prefix) kv_end = max(kv_end, min(cl, prefix[s]));
+        const int kt0 = window > 0 ? max(0, cl - ql + t0 - window + 1) / 128 : 0;
+        return (kv_end + 127) / 128 - kt0;
     };
     for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
         const int ql = q_lens[s], cl = ctx_lens[s];
@@ -950,7 +1091,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
             raise_error(ctx, ERR_BOUNDS_BIT);
             continue;
         }
-        for (int t0 = 0; t0 < ql; t0 += entry_tokens) atomicAdd(&hist[entry_cost(ql, cl, t0)], 1);
+        for (int t0 = 0; t0 < ql; t0 += entry_tokens) atomicAdd(&hist[entry_cost(s, ql, cl, t0)], 1);
     }
     __syncthreads();
     if (threadIdx.x == 0) {  // bucket starts, highest cost first
@@ -969,7 +1110,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         const int ql = q_lens[s], cl = ctx_lens[s];
         if (ql <= 0 || is_decode_row(ql, g) || ql > cl || cl > mbps * kBS) continue;
         for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
-            const int pos = atomicAdd(&hist[entry_cost(ql, cl, t0)], 1);
+            const int pos = atomicAdd(&hist[entry_cost(s, ql, cl, t0)], 1);
             if (pos < max_entries) {
                 list[2 * pos] = s;
                 list[2 * pos + 1] = t0;
@@ -1001,13 +1142,13 @@ static fa_status side_stream(SideStream** out) {
     return FA_OK;
 }
 
-template <int D, bool KV8 = false>
+template <int D, bool KV8 = false, int MOD = 0>
 static fa_status launch_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* bt,
                                const int32_t* ctx_lens, const int32_t* q_lens, void* out, const PagedWs& w,
                                uint8_t* ws, int num_seqs, int mbps, int num_blocks, int Hq, int Hkv,
                                int q_prefetch_rows, int causal, float scale, int merge_rows, cudaStream_t s,
                                const DevCtx& ctx, int* launches,
-                               float k_scale = 1.f, float v_scale = 1.f) {
+                               float k_scale = 1.f, float v_scale = 1.f, const ScoreMod& mod = ScoreMod{}) {
     CUtensorMap tk, tv;
     fa_status st;
     if constexpr (KV8) {
@@ -1040,11 +1181,12 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
     auto launch = [&](auto rows) -> fa_status {
         constexpr int R = decltype(rows)::value;
         using L = StreamSmem<D, KV8, R>;
-        const fa_status st2 = raise_dynamic_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, KV8, R>), L::kBytes);
+        const fa_status st2 = raise_dynamic_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, KV8, R, MOD>), L::kBytes);
         if (st2 != FA_OK) return st2;
-        paged_decode_kernel<D, KV8, R><<<grid, kStreamWarps * 32, L::kBytes, s>>>(
+        paged_decode_kernel<D, KV8, R, MOD><<<grid, kStreamWarps * 32, L::kBytes, s>>>(
             tk, tv, static_cast<const uint16_t*>(q), bt, ctx_lens, q_lens, static_cast<uint16_t*>(out), part_o, part_ml,
-            num_seqs, mbps, num_blocks, Hq, Hkv, q_prefetch_rows, causal, scale_log2, v_scale, ctx);
+            num_seqs, mbps, num_blocks, Hq, Hkv, q_prefetch_rows, causal, scale_log2, v_scale, ctx,
+            mod);
         return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     };
     st = merge_rows <= 6 ? launch(std::integral_constant<int, 6>{}) : launch(std::integral_constant<int, kDecodeRows>{});
@@ -1059,29 +1201,40 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, ctx_lens, q_lens, static_cast<const float*>(part_o),
+    if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, MOD != 0>, ctx_lens, q_lens, static_cast<const float*>(part_o),
                            static_cast<const float2*>(part_ml), static_cast<uint16_t*>(out), num_seqs, Hq, Hkv,
-                           mbps, grid * kStreamWarps) != cudaSuccess)
+                           mbps, grid * kStreamWarps, mod) != cudaSuccess)
         return FA_ERR_CUDA;
     ++*launches;
     return FA_OK;
 }
 
-}  // namespace fa
-
-using namespace fa;
-
-extern "C" {
-
-size_t fa_paged_attn_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv, int d, int total_q) {
-    if (num_seqs < 0 || max_blocks_per_seq < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || total_q < 0) return 0;
-    return paged_ws_layout(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q).total;
+// Weight sums wanted by a call (fa_paged_attn_accum), and where its workspace
+// keeps the decode rows' logits: behind the attention's own, min(16, g *
+// max_q_len) rows of 16 logits for every page that the tables can hold.
+struct AccumArgs {
+    const float* in;
+    float* out;
+    int len;
+    float decay;
+};
+struct AccumWs {
+    size_t logits, total;
+};
+static AccumWs accum_ws_layout(size_t base, int num_seqs, int mbps, int Hq, int Hkv, int max_q_len) {
+    const int g = Hq / Hkv;
+    const long rows = g <= kDecodeRows ? std::min<long>(kDecodeRows, (long)g * max_q_len) : 0;
+    AccumWs a{};
+    a.logits = align256(base);
+    a.total = align256(a.logits + (size_t)num_seqs * mbps * Hkv * rows * kBS * sizeof(float));
+    return a;
 }
 
-fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+static fa_status paged_attn_run(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                         const int32_t* ctx_lens, const int32_t* q_lens, void* out, int num_seqs,
                         int max_blocks_per_seq, int num_blocks, int Hq, int Hkv, int d, int block_size, int causal,
-                        float scale, int total_q, int max_q_len, void* ws, size_t ws_bytes, fa_stream_t stream) {
+                        float scale, int total_q, int max_q_len, void* ws, size_t ws_bytes, fa_stream_t stream,
+                                ScoreMod* mod, const AccumArgs* acc) {
     set_launch_count(0);
     if (num_seqs < 0 || max_blocks_per_seq < 0 || num_blocks < 0 || Hq <= 0 || Hkv <= 0 || total_q < 0 ||
         max_q_len < 0 || !(scale > 0.f) || !(scale < INFINITY))
@@ -1092,7 +1245,8 @@ fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache,
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned32(out)) return FA_ERR_INVALID_ARG;
     if (num_blocks == 0 || max_blocks_per_seq == 0) return FA_ERR_INVALID_ARG;
     const PagedWs w = paged_ws_layout(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q);
-    if (!ws || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(ws) & 255)) return FA_ERR_WORKSPACE;
+    const AccumWs aw = acc ? accum_ws_layout(w.total, num_seqs, max_blocks_per_seq, Hq, Hkv, max_q_len) : AccumWs{};
+    if (!ws || ws_bytes < (acc ? aw.total : w.total) || (reinterpret_cast<uintptr_t>(ws) & 255)) return FA_ERR_WORKSPACE;
     fa_status st = check_device();
     if (st != FA_OK) return st;
     DevCtx ctx;
@@ -1127,7 +1281,8 @@ fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache,
             ms = ss->s;
         }
         paged_meta_kernel<<<1, 1024, hist_bytes, ms>>>(ctx_lens, q_lens, num_seqs, max_blocks_per_seq, g, causal,
-                                                       entry_tokens, q_start, count, list, w.max_entries, ctx);
+                                                       entry_tokens, q_start, count, list, w.max_entries,
+                                                       mod ? mod->window : 0, mod ? mod->prefix : nullptr, ctx);
         const bool launched = cudaGetLastError() == cudaSuccess;
         if (ss && (cudaEventRecord(ss->join, ss->s) != cudaSuccess || !launched)) {
             (void)cudaStreamWaitEvent(s, ss->join, 0);  // leave the side stream joined
@@ -1139,12 +1294,23 @@ fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache,
     if (decode_path) {
         const int merge_rows = (int)std::min<long>(kDecodeRows, (long)g * max_q_len);
         const int qpf = is_decode_row(max_q_len, g) ? total_q : 0;  // every query row is a decode row
-        st = d == 128 ? launch_decode<128>(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w, wsb, num_seqs,
-                                           max_blocks_per_seq, num_blocks, Hq, Hkv, qpf, causal, scale, merge_rows, s,
-                                           ctx, &launches)
-                      : launch_decode<64>(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w, wsb, num_seqs,
-                                          max_blocks_per_seq, num_blocks, Hq, Hkv, qpf, causal, scale, merge_rows, s,
-                                          ctx, &launches);
+        if (acc) {
+            mod->logits = reinterpret_cast<float*>(wsb + aw.logits);
+            mod->logit_rows = merge_rows;
+        }
+        auto go = [&](auto dim, auto variant) {
+            return launch_decode<decltype(dim)::value, false, decltype(variant)::value>(
+                q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w, wsb, num_seqs, max_blocks_per_seq,
+                num_blocks, Hq, Hkv, qpf, causal, scale, merge_rows, s, ctx, &launches, 1.f, 1.f,
+                mod ? *mod : ScoreMod{});
+        };
+        auto go_d = [&](auto variant) {
+            return d == 128 ? go(std::integral_constant<int, 128>{}, variant)
+                            : go(std::integral_constant<int, 64>{}, variant);
+        };
+        st = acc   ? go_d(std::integral_constant<int, 2>{})
+             : mod ? go_d(std::integral_constant<int, 1>{})
+                   : go_d(std::integral_constant<int, 0>{});
         if (st != FA_OK) {
             if (ss) (void)cudaStreamWaitEvent(s, ss->join, 0);  // keep the side stream joined
             return st;
@@ -1157,12 +1323,96 @@ fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache,
         int32_t* list = reinterpret_cast<int32_t*>(wsb + w.work_list);
         st = launch_paged_prefill(q, k_cache, v_cache, block_table, ctx_lens, q_lens, q_start, list, count, out,
                                   num_seqs, max_blocks_per_seq, num_blocks, Hq, Hkv, d, causal, scale, total_q, s,
-                                  ctx);
+                                  ctx, mod);
         if (st != FA_OK) return st;
         ++launches;
     }
+    if (acc) {
+        // rows whose queries took the decode kernel (and sequences without
+        // queries), then the chunks: each sequence is one or the other
+        const dim3 grid(num_seqs, Hkv, (max_blocks_per_seq + kAccumPages - 1) / kAccumPages);
+        accum_decode_kernel<<<grid, 256, 0, s>>>(ctx_lens, q_lens, mod->lse, mod->logits, mod->logit_rows, acc->in,
+                                                 acc->out, acc->len, acc->decay, num_seqs, max_blocks_per_seq, Hq, Hkv,
+                                                 mod->window, ctx);
+        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+        ++launches;
+        if (tc_path) {
+            st = launch_accum_chunk(q, k_cache, block_table, ctx_lens, q_lens,
+                                    reinterpret_cast<int32_t*>(wsb + w.q_start), mod->lse, acc->in, acc->out, acc->len,
+                                    acc->decay, num_seqs, max_blocks_per_seq, num_blocks, Hq, Hkv, d, causal, scale,
+                                    total_q, *mod, s, ctx);
+            if (st != FA_OK) return st;
+            ++launches;
+        }
+    }
     set_launch_count(launches);
     return FA_OK;
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_paged_attn_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv, int d, int total_q) {
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || total_q < 0) return 0;
+    return paged_ws_layout(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q).total;
+}
+
+fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                        const int32_t* ctx_lens, const int32_t* q_lens, void* out, int num_seqs,
+                        int max_blocks_per_seq, int num_blocks, int Hq, int Hkv, int d, int block_size, int causal,
+                        float scale, int total_q, int max_q_len, void* ws, size_t ws_bytes, fa_stream_t stream) {
+    return paged_attn_run(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, num_seqs, max_blocks_per_seq,
+                          num_blocks, Hq, Hkv, d, block_size, causal, scale, total_q, max_q_len, ws, ws_bytes, stream,
+                          nullptr, nullptr);
+}
+
+size_t fa_paged_attn_mod_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv, int d, int total_q,
+                                        int max_q_len) {
+    if (max_q_len < 0) return 0;
+    return fa_paged_attn_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q);
+}
+
+fa_status fa_paged_attn_mod(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                            const int32_t* ctx_lens, const int32_t* q_lens, void* out, float* lse, int num_seqs,
+                            int max_blocks_per_seq, int num_blocks, int Hq, int Hkv, int d, int block_size, int causal,
+                            float scale, float softcap, const float* alibi_slopes, int window,
+                            const int32_t* prefix_lens, int total_q, int max_q_len, void* ws, size_t ws_bytes,
+                            fa_stream_t stream) {
+    set_launch_count(0);
+    ScoreMod mod;
+    const fa_status st = make_score_mod(&mod, scale, softcap, alibi_slopes, window, prefix_lens, lse);
+    if (st != FA_OK) return st;
+    return paged_attn_run(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, num_seqs, max_blocks_per_seq,
+                          num_blocks, Hq, Hkv, d, block_size, causal, scale, total_q, max_q_len, ws, ws_bytes, stream,
+                          &mod, nullptr);
+}
+
+size_t fa_paged_attn_accum_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv, int d, int total_q,
+                                          int max_q_len) {
+    const size_t base = fa_paged_attn_mod_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len);
+    return base == 0 ? 0 : accum_ws_layout(base, num_seqs, max_blocks_per_seq, Hq, Hkv, max_q_len).total;
+}
+
+fa_status fa_paged_attn_accum(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                              const int32_t* ctx_lens, const int32_t* q_lens, void* out, float* lse,
+                              const float* acc_in, float* acc_out, int acc_len, float decay, int num_seqs,
+                              int max_blocks_per_seq, int num_blocks, int Hq, int Hkv, int d, int block_size,
+                              int causal, float scale, float softcap, const float* alibi_slopes, int window,
+                              const int32_t* prefix_lens, int total_q, int max_q_len, void* ws, size_t ws_bytes,
+                              fa_stream_t stream) {
+    set_launch_count(0);
+    if (acc_len < 0 || !(decay >= 0.f) || !(decay < INFINITY)) return FA_ERR_INVALID_ARG;
+    ScoreMod mod;
+    const fa_status st = make_score_mod(&mod, scale, softcap, alibi_slopes, window, prefix_lens, lse);
+    if (st != FA_OK) return st;
+    if (num_seqs > 0 && total_q > 0 && max_q_len > 0 && (!lse || !acc_out)) return FA_ERR_INVALID_ARG;
+    const AccumArgs acc{acc_in, acc_out, acc_len, decay};
+    return paged_attn_run(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, num_seqs, max_blocks_per_seq,
+                          num_blocks, Hq, Hkv, d, block_size, causal, scale, total_q, max_q_len, ws, ws_bytes, stream,
+                          &mod, &acc);
 }
 
 fa_status fa_paged_attn_fp8(const void* q, const void* k_cache, const void* v_cache, float k_scale, float v_scale,

@@ -31,7 +31,9 @@ EXPORTS = [
     "fa_decode_graph_destroy", "fa_pool_create", "fa_pool_destroy", "fa_pool_add_seq", "fa_pool_fork",
     "fa_pool_append", "fa_pool_release", "fa_pool_tables", "fa_pool_num_free", "fa_pool_refcount", "fa_pool_seq_len",
     "fa_copy_blocks", "fa_cache_append_fp8", "fa_paged_attn_fp8", "fa_prefill_host", "fa_mask_tile_classes",
-    "fa_prefill_rows",
+    "fa_prefill_rows", "fa_prefill_mod_workspace_size", "fa_prefill_mod", "fa_cache_append_mrope",
+    "fa_paged_attn_mod_workspace_size", "fa_paged_attn_mod", "fa_paged_attn_accum_workspace_size",
+    "fa_paged_attn_accum", "fa_cache_evict_workspace_size", "fa_cache_evict",
 ]
 NOALLOC_SCRATCH_BYTES = 32 << 20  # FA_NOALLOC_SCRATCH_BYTES
 
@@ -86,6 +88,16 @@ def _load() -> ctypes.CDLL:
         "fa_debug_force_timeout": (None, [I]),
         "fa_paged_attn_noalloc": (I, [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, I, P]),
         "fa_last_launch_count": (I, []),
+        "fa_prefill_mod_workspace_size": (Z, [I, I]),
+        "fa_prefill_mod": (I, [P, P, P, P, P, I, I, I, I, I, I, F, F, P, I, P, P, P, Z, P]),
+        "fa_cache_append_mrope": (I, [P, P, P, P, I, P, P, I, P, P, P, P, I, I, I, I, I, I, P]),
+        "fa_paged_attn_mod_workspace_size": (Z, [I, I, I, I, I, I, I]),
+        "fa_paged_attn_mod": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, F, P, I, P, I, I, P, Z, P]),
+        "fa_paged_attn_accum_workspace_size": (Z, [I, I, I, I, I, I, I]),
+        "fa_paged_attn_accum": (I, [P, P, P, P, P, P, P, P, P, P, I, F, I, I, I, I, I, I, I, I, F, F, P, I, P, I, I, P,
+                                    Z, P]),
+        "fa_cache_evict_workspace_size": (Z, [I, I, I, I]),
+        "fa_cache_evict": (I, [P, P, P, I, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, I, P, Z, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -132,6 +144,27 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: int | None = None):
         raise ValueError(f"{name} must be contiguous")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims")
+
+
+def _shape(t, name: str, *shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _one_device(**tensors):
+    """Every tensor given must live on the current device, whose stream the call runs on."""
+    cur = torch.cuda.current_device()
+    for n, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{n} is on {t.device}, but the current device is cuda:{cur}")
+
+
+def _workspace(ws, nbytes: int, device):
+    if ws is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor")
+    return ws
 
 
 # ------------------------------------------------------------------ prefill
@@ -219,6 +252,45 @@ def fa_prefill_masked(q, k, v, mask, causal: bool = False, scale: float | None =
     return out
 
 
+def fa_prefill_mod_workspace_size(B: int, T: int) -> int:
+    return int(_lib.fa_prefill_mod_workspace_size(int(B), int(T)))
+
+
+def fa_prefill_mod(q, k, v, causal: bool = True, scale: float | None = None, softcap: float = 0.0,
+                   alibi_slopes=None, window: int = 0, prefix_lens=None, doc_ids=None, out=None, lse=None, ws=None,
+                   stream=None):
+    """fa_prefill with modified scores: logits f(scale q.k) - alibi_slopes[h] |i - j|, f(z) = softcap
+    tanh(z / softcap) (softcap > 0); a key is visible when every mask given allows it: causal (or below
+    prefix_lens[b]), window, doc_ids [B, T] (runs of equal ids; negative: padding)."""
+    for n, t in (("q", q), ("k", k), ("v", v)):
+        _need(t, n, torch.bfloat16, 4)
+    B, T, Hq, d = q.shape
+    Hkv = k.shape[2]
+    _shape(k, "k", B, T, Hkv, d)
+    _shape(v, "v", B, T, Hkv, d)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, 4)
+    _shape(out, "out", B, T, Hq, d)
+    for n, t, dt, shape in (("alibi_slopes", alibi_slopes, torch.float32, (Hq,)),
+                            ("prefix_lens", prefix_lens, torch.int32, (B,)),
+                            ("doc_ids", doc_ids, torch.int32, (B, T)), ("lse", lse, torch.float32, (B, Hq, T))):
+        if t is not None:
+            _need(t, n, dt)
+            _shape(t, n, *shape)
+    if doc_ids is not None:
+        ws = _workspace(ws, fa_prefill_mod_workspace_size(B, T), q.device)
+    _one_device(q=q, k=k, v=v, out=out, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, doc_ids=doc_ids, lse=lse,
+                ws=ws)
+    _check(_lib.fa_prefill_mod(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, T, Hq, Hkv, d, int(causal),
+                               float(scale), float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens),
+                               _ptr(doc_ids), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                               _stream(stream)), "fa_prefill_mod")
+    return out
+
+
 def fa_mask_tile_classes(mask, out=None, intervals=None, stream=None):
     """uint8 [ceil(Tq/128), ceil(Tk/128)] classes of an fp32 mask [Tq, Tk]: 0 all -inf, 1 all zero,
     3 zeros forming one run per row among -inf, 2 otherwise.  `intervals` (optional, uint8
@@ -289,6 +361,46 @@ def fa_cache_append_rope(q, k, v, positions, cos_sin, k_cache, v_cache, slot_map
     _check(_lib.fa_cache_append_rope(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
                                      _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), N, Hq, Hkv, d,
                                      k_cache.shape[0], dt, _stream(stream)), "fa_cache_append_rope")
+    return q_out
+
+
+def fa_cache_append_mrope(q, k, v, positions, pair_axes, cos_sin, k_cache, v_cache, slot_mapping, q_out=None,
+                          stream=None):
+    """fa_cache_append_rope with positions [n_axes, N]: channel pair j turns by the table row of
+    positions[pair_axes[j]] (pair_axes: d/2 small integers on the host)."""
+    if q.dtype not in (torch.bfloat16, torch.float32) or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k, v must all be bf16 or all fp32")
+    _need(q, "q", q.dtype, 3)
+    _need(k, "k", q.dtype, 3)
+    _need(v, "v", q.dtype, 3)
+    _need(positions, "positions", torch.int32, 2)
+    _need(cos_sin, "cos_sin", torch.float32, 2)
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(slot_mapping, "slot_mapping", torch.int32, 1)
+    N, Hq, d = q.shape
+    Hkv, nb = k.shape[1], k_cache.shape[0]
+    n_axes = positions.shape[0]
+    _shape(k, "k", N, Hkv, d)
+    _shape(v, "v", N, Hkv, d)
+    _shape(positions, "positions", n_axes, N)
+    _shape(cos_sin, "cos_sin", cos_sin.shape[0], d)
+    _shape(k_cache, "k_cache", nb, Hkv, 16, d)
+    _shape(v_cache, "v_cache", nb, Hkv, 16, d)
+    _shape(slot_mapping, "slot_mapping", N)
+    axes = [int(a) for a in pair_axes]
+    if len(axes) != d // 2 or any(a < 0 or a >= n_axes for a in axes):
+        raise ValueError(f"pair_axes must be {d // 2} integers in [0, {n_axes})")
+    if q_out is None:
+        q_out = torch.empty(N, Hq, d, dtype=torch.bfloat16, device=q.device)
+    _need(q_out, "q_out", torch.bfloat16, 3)
+    _shape(q_out, "q_out", N, Hq, d)
+    _one_device(q=q, k=k, v=v, positions=positions, cos_sin=cos_sin, k_cache=k_cache, v_cache=v_cache,
+                slot_mapping=slot_mapping, q_out=q_out)
+    dt = FA_F32 if q.dtype == torch.float32 else FA_BF16
+    _check(_lib.fa_cache_append_mrope(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), n_axes, bytes(axes), _ptr(cos_sin),
+                                      cos_sin.shape[0], _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+                                      N, Hq, Hkv, d, nb, dt, _stream(stream)), "fa_cache_append_mrope")
     return q_out
 
 
@@ -478,6 +590,137 @@ def fa_paged_attn(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal: bo
                               float(scale), total_q, int(max_q_len), _ptr(ws), ws.numel() * ws.element_size(),
                               _stream(stream)), "fa_paged_attn")
     return out
+
+
+def fa_paged_attn_mod_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len) -> int:
+    return int(_lib.fa_paged_attn_mod_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len))
+
+
+def fa_paged_attn_accum_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len) -> int:
+    return int(_lib.fa_paged_attn_accum_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len))
+
+
+def _paged_mod_args(q, k_cache, v_cache, block_table, ctx_lens, q_lens, alibi_slopes, prefix_lens, out, lse,
+                    max_q_len):
+    """Checks shared by the paged calls with modified scores; returns (out, max_q_len, sizes)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(ctx_lens, "ctx_lens", torch.int32, 1)
+    _need(q_lens, "q_lens", torch.int32, 1)
+    total_q, Hq, d = q.shape
+    num_blocks, Hkv, bs, _ = k_cache.shape
+    num_seqs, mbps = block_table.shape
+    _shape(k_cache, "k_cache", num_blocks, Hkv, bs, d)
+    _shape(v_cache, "v_cache", num_blocks, Hkv, bs, d)
+    _shape(ctx_lens, "ctx_lens", num_seqs)
+    _shape(q_lens, "q_lens", num_seqs)
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, 3)
+    _shape(out, "out", total_q, Hq, d)
+    for n, t, dt, shape in (("alibi_slopes", alibi_slopes, torch.float32, (Hq,)),
+                            ("prefix_lens", prefix_lens, torch.int32, (num_seqs,)),
+                            ("lse", lse, torch.float32, (total_q, Hq))):
+        if t is not None:
+            _need(t, n, dt)
+            _shape(t, n, *shape)
+    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, ctx_lens=ctx_lens, q_lens=q_lens,
+                alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, out=out, lse=lse)
+    return out, total_q if max_q_len is None else int(max_q_len), (num_seqs, mbps, num_blocks, Hq, Hkv, d, bs, total_q)
+
+
+def fa_paged_attn_mod(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal: bool = True,
+                      scale: float | None = None, softcap: float = 0.0, alibi_slopes=None, window: int = 0,
+                      prefix_lens=None, out=None, lse=None, max_q_len: int | None = None, ws=None, stream=None):
+    """fa_paged_attn with modified scores (as fa_prefill_mod, in cache positions); lse (optional, fp32
+    [total_q, Hq]) receives the log-sum-exp of every row."""
+    out, max_q_len, (S, mbps, nb, Hq, Hkv, d, bs, total_q) = _paged_mod_args(
+        q, k_cache, v_cache, block_table, ctx_lens, q_lens, alibi_slopes, prefix_lens, out, lse, max_q_len)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    ws = _workspace(ws, fa_paged_attn_mod_workspace_size(S, mbps, Hq, Hkv, d, total_q, max_q_len), q.device)
+    _one_device(ws=ws)
+    _check(_lib.fa_paged_attn_mod(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(ctx_lens),
+                                  _ptr(q_lens), _ptr(out), _ptr(lse), S, mbps, nb, Hq, Hkv, d, bs, int(causal),
+                                  float(scale), float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens),
+                                  total_q, max_q_len, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "fa_paged_attn_mod")
+    return out
+
+
+def fa_paged_attn_accum(q, k_cache, v_cache, block_table, ctx_lens, q_lens, acc_in, acc_out, decay: float = 1.0,
+                        causal: bool = True, scale: float | None = None, softcap: float = 0.0, alibi_slopes=None,
+                        window: int = 0, prefix_lens=None, out=None, lse=None, max_q_len: int | None = None, ws=None,
+                        stream=None):
+    """fa_paged_attn_mod that also writes acc_out [num_seqs, Hkv, acc_len] = decay * acc_in (0 for the chunk's own
+    tokens, and where acc_in is None) + the softmax weights every cached token received from the chunk's queries and
+    the group's heads.  acc_in and acc_out may be the same tensor."""
+    if lse is None:
+        lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
+    out, max_q_len, (S, mbps, nb, Hq, Hkv, d, bs, total_q) = _paged_mod_args(
+        q, k_cache, v_cache, block_table, ctx_lens, q_lens, alibi_slopes, prefix_lens, out, lse, max_q_len)
+    _need(acc_out, "acc_out", torch.float32, 3)
+    acc_len = acc_out.shape[2]
+    _shape(acc_out, "acc_out", S, Hkv, acc_len)
+    if acc_in is not None:
+        _need(acc_in, "acc_in", torch.float32, 3)
+        _shape(acc_in, "acc_in", S, Hkv, acc_len)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    ws = _workspace(ws, fa_paged_attn_accum_workspace_size(S, mbps, Hq, Hkv, d, total_q, max_q_len), q.device)
+    _one_device(ws=ws, acc_in=acc_in, acc_out=acc_out)
+    _check(_lib.fa_paged_attn_accum(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(ctx_lens),
+                                    _ptr(q_lens), _ptr(out), _ptr(lse), _ptr(acc_in), _ptr(acc_out), acc_len,
+                                    float(decay), S, mbps, nb, Hq, Hkv, d, bs, int(causal), float(scale),
+                                    float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens), total_q,
+                                    max_q_len, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "fa_paged_attn_accum")
+    return out
+
+
+def fa_cache_evict_workspace_size(num_seqs, max_blocks_per_seq, Hkv, keep) -> int:
+    return int(_lib.fa_cache_evict_workspace_size(num_seqs, max_blocks_per_seq, Hkv, keep))
+
+
+def fa_cache_evict(k_cache, v_cache, acc, block_table, ctx_lens, dst_table, keep: int, recent: int = 0, sink: int = 0,
+                   acc_out=None, new_lens=None, kept=None, ws=None, stream=None):
+    """Copies, per sequence and kv head, the first `sink`, the last `recent` and the tokens of largest acc
+    [num_seqs, Hkv, acc_len] (`keep` in all) from the blocks of block_table to those of dst_table, in order of
+    position; returns the new lengths int32 [num_seqs].  acc_out and kept (int32 [num_seqs, Hkv, keep], old
+    positions) are optional outputs."""
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(acc, "acc", torch.float32, 3)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(dst_table, "dst_table", torch.int32, 2)
+    _need(ctx_lens, "ctx_lens", torch.int32, 1)
+    nb, Hkv, bs, d = k_cache.shape
+    S, mbps = block_table.shape
+    _shape(v_cache, "v_cache", nb, Hkv, bs, d)
+    _shape(acc, "acc", S, Hkv, acc.shape[2])
+    _shape(dst_table, "dst_table", S, dst_table.shape[1])
+    _shape(ctx_lens, "ctx_lens", S)
+    if acc_out is not None:
+        _need(acc_out, "acc_out", torch.float32, 3)
+        _shape(acc_out, "acc_out", S, Hkv, acc_out.shape[2])
+    if new_lens is None:
+        new_lens = torch.empty(S, dtype=torch.int32, device=k_cache.device)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    _shape(new_lens, "new_lens", S)
+    if kept is not None:
+        _need(kept, "kept", torch.int32, 3)
+        _shape(kept, "kept", S, Hkv, int(keep))
+    else:
+        ws = _workspace(ws, fa_cache_evict_workspace_size(S, mbps, Hkv, int(keep)), k_cache.device)
+    _one_device(k_cache=k_cache, v_cache=v_cache, acc=acc, block_table=block_table, dst_table=dst_table,
+                ctx_lens=ctx_lens, acc_out=acc_out, new_lens=new_lens, kept=kept, ws=ws)
+    _check(_lib.fa_cache_evict(_ptr(k_cache), _ptr(v_cache), _ptr(acc), acc.shape[2], _ptr(block_table),
+                               _ptr(ctx_lens), _ptr(dst_table), _ptr(acc_out),
+                               0 if acc_out is None else acc_out.shape[2], _ptr(new_lens), _ptr(kept), S, mbps,
+                               dst_table.shape[1], nb, Hkv, d, bs, int(keep), int(recent), int(sink), _ptr(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+           "fa_cache_evict")
+    return new_lens
 
 
 def fa_paged_attn_noalloc(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal: bool = True,
