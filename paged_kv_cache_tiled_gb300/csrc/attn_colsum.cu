@@ -15,6 +15,7 @@
 // other's work.  Per logit the sum costs one multiply-add, one exponential and
 // one add, against two passes over the scores in the attention itself.
 #include <cmath>
+#include <type_traits>
 
 #include "host_common.cuh"
 
@@ -268,44 +269,50 @@ __global__ void __launch_bounds__(kCsThreads, 2)
                 break;
             }
             tc_fence_after();
+            // four columns at a time; `masked`: some row of the tile is not real or does not see some key
+            auto columns = [&](auto masked) {
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t raw[32];
-                tmem_ld32(trow + b * 32, raw);
-                tmem_wait_ld();
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t raw[32];
+                    tmem_ld32(trow + b * 32, raw);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 nl = *reinterpret_cast<const float4*>(nlse + b * 32 + j);
-                    const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 nl = *reinterpret_cast<const float4*>(nlse + b * 32 + j);
+                        const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
 #pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        float2 x = make_float2(__uint_as_float(raw[j + e]), __uint_as_float(raw[j + e + 1]));
-                        const float2 l2 = make_float2(nls[e], nls[e + 1]);
-                        if (MOD == CS_CAP || (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
-                            x.x = fmaf(p.mod.cap_out, tanh_f32(x.x * p.mod.cap_in), l2.x);
-                            x.y = fmaf(p.mod.cap_out, tanh_f32(x.y * p.mod.cap_in), l2.y);
-                        } else {
-                            x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), l2);
+                        for (int e = 0; e < 4; e += 2) {
+                            float2 x = make_float2(__uint_as_float(raw[j + e]), __uint_as_float(raw[j + e + 1]));
+                            const float2 l2 = make_float2(nls[e], nls[e + 1]);
+                            if (MOD == CS_CAP || (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
+                                x.x = fmaf(p.mod.cap_out, tanh_f32(x.x * p.mod.cap_in), l2.x);
+                                x.y = fmaf(p.mod.cap_out, tanh_f32(x.y * p.mod.cap_in), l2.y);
+                            } else {
+                                x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), l2);
+                            }
+                            if constexpr (MOD == CS_BIAS) {
+                                const float2 sl = *reinterpret_cast<const float2*>(slope + b * 32 + j + e);
+                                const int2 cp = *reinterpret_cast<const int2*>(cpos + b * 32 + j + e);
+                                x.x = fmaf(sl.x, fabsf((float)(k_lo + lane - cp.x)), x.x);
+                                x.y = fmaf(sl.y, fabsf((float)(k_lo + lane - cp.y)), x.y);
+                            }
+                            float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            if constexpr (decltype(masked)::value) {
+                                const int c = b * 32 + j + e, key = k_lo + lane;
+                                const int t0 = tok0 + (p.pack ? c >> p.pack_shift : c);
+                                const int t1 = tok0 + (p.pack ? (c + 1) >> p.pack_shift : c + 1);
+                                const int2 r0 = cs_range(p, pos0 + t0, prefix, cl);
+                                const int2 r1 = cs_range(p, pos0 + t1, prefix, cl);
+                                pr.x = t0 < ql && key >= r0.x && key < r0.y ? pr.x : 0.f;
+                                pr.y = t1 < ql && key >= r1.x && key < r1.y ? pr.y : 0.f;
+                            }
+                            sum[(j + e) >> 1 & 3] = __fadd2_rn(sum[(j + e) >> 1 & 3], pr);
                         }
-                        if constexpr (MOD == CS_BIAS) {
-                            const float2 sl = *reinterpret_cast<const float2*>(slope + b * 32 + j + e);
-                            const int2 cp = *reinterpret_cast<const int2*>(cpos + b * 32 + j + e);
-                            x.x = fmaf(sl.x, fabsf((float)(k_lo + lane - cp.x)), x.x);
-                            x.y = fmaf(sl.y, fabsf((float)(k_lo + lane - cp.y)), x.y);
-                        }
-                        float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        if (!plain) {
-                            const int c = b * 32 + j + e, key = k_lo + lane;
-                            const int t0 = tok0 + (p.pack ? c >> p.pack_shift : c);
-                            const int t1 = tok0 + (p.pack ? (c + 1) >> p.pack_shift : c + 1);
-                            const int2 r0 = cs_range(p, pos0 + t0, prefix, cl), r1 = cs_range(p, pos0 + t1, prefix, cl);
-                            pr.x = t0 < ql && key >= r0.x && key < r0.y ? pr.x : 0.f;
-                            pr.y = t1 < ql && key >= r1.x && key < r1.y ? pr.y : 0.f;
-                        }
-                        sum[(j + e) >> 1 & 3] = __fadd2_rn(sum[(j + e) >> 1 & 3], pr);
                     }
                 }
-            }
+            };
+            if (plain) columns(std::false_type{});
+            else columns(std::true_type{});
             tc_fence_before();
             mbar_arrive(&sempty[w]);
         }

@@ -42,6 +42,7 @@
 
 #include <memory>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "host_common.cuh"
@@ -54,6 +55,7 @@ enum { MODE_DENSE = 0, MODE_MASKED = 1, MODE_PAGED = 2 };
 // set in every modified variant; MOD_CAP caps the scores; MOD_BIAS subtracts
 // slope |i - j| (and caps them when asked: a rare pair that needs no variant).
 enum { MOD_RANGE = 1, MOD_CAP = 2, MOD_BIAS = 4 };
+constexpr float kBiasSlack = 32.f;  // log2 units that the running max of a biased row may lie above its largest logit
 constexpr int kRangeHoles = 1 << 30;  // flag bit of a query tile's visible KV range
 constexpr int kTcThreads = 320;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
@@ -1043,7 +1045,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // re-reading the mask.
                 bool general = cls == 2;
                 if constexpr ((MOD & MOD_BIAS) != 0)
-                    general = p.mod.cap_out > 0.f ||
+                    general = p.mod.cap_out > 0.f || __any_sync(0xffffffffu, fabsf(slope) * 15.f > kBiasSlack) ||
                               !(__all_sync(0xffffffffu, kv0 + kTcRows - 1 <= qpos || vlim_causal) ||
                                 __all_sync(0xffffffffu, kv0 >= qpos));
                 // visible columns of this row: [vlo, vlim); a class-3 tile keeps
@@ -1059,6 +1061,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 // every column of every row of the warp visible and no mask values
                 const bool plain = !general && __all_sync(0xffffffffu, vlo <= 0 && vlim >= kTcRows);
+                [[maybe_unused]] int cap_tier = 0;
                 float bias_k = 0.f, bias0 = 0.f;  // logit bias of column c: bias_k c + bias0
                 if constexpr ((MOD & MOD_BIAS) != 0) {
                     const int d0 = kv0 - qpos;
@@ -1078,19 +1081,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int c = 0; c < kTcRows / 32; ++c)
                         tmem_ld32(trow + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(raw + 32 * c));
                     tmem_wait_ld();
-                    if constexpr ((MOD & MOD_BIAS) != 0) {
-                        // logit pairs: s scale + (slope (d0 + c)), the distance d0 an integer below 2^24 in size
+                    if constexpr (MOD != 0) {
+                        // with a bias group g is the raw maximum of columns [16 g, 16 g + 16)
+                        if (plain) {
 #pragma unroll
-                        for (int j = 0; j < kTcRows; j += 2) {
-                            const float2 x = __ffma2_rn(
-                                make_float2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])),
-                                make_float2(p.scale_log2, p.scale_log2),
-                                __ffma2_rn(make_float2((float)j, (float)(j + 1)), make_float2(bias_k, bias_k),
-                                           make_float2(bias0, bias0)));
-                            mxp[(j >> 1) & 7] =
-                                plain ? fmax3f(mxp[(j >> 1) & 7], x.x, x.y)
-                                      : fmax3f(mxp[(j >> 1) & 7], j >= vlo && j < vlim ? x.x : -INFINITY,
-                                               j + 1 >= vlo && j + 1 < vlim ? x.y : -INFINITY);
+                            for (int j = 0; j < kTcRows; j += 2) {
+                                float& mj = mxp[(MOD & MOD_BIAS) != 0 ? j >> 4 : (j >> 1) & 7];
+                                mj = fmax3f(mj, __uint_as_float(raw[j]), __uint_as_float(raw[j + 1]));
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < kTcRows; j += 2) {
+                                float& mj = mxp[(MOD & MOD_BIAS) != 0 ? j >> 4 : (j >> 1) & 7];
+                                mj = fmax3f(mj, j >= vlo && j < vlim ? __uint_as_float(raw[j]) : -INFINITY,
+                                            j + 1 >= vlo && j + 1 < vlim ? __uint_as_float(raw[j + 1]) : -INFINITY);
+                            }
+                        }
+                        if constexpr ((MOD & MOD_BIAS) != 0) {
+                            // The running max only has to be near the row's: a group's raw maximum with
+                            // the bias of its best column is at most 15 slopes above it (kBiasSlack).
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                mxp[i] = fmaf(mxp[i], p.scale_log2,
+                                              bias0 + fmaxf(bias_k * (float)(16 * i), bias_k * (float)(16 * i + 15)));
+                        }
+                        if constexpr ((MOD & MOD_CAP) != 0) {
+                            // which tanh serves every column of the warp's rows (masked columns are dropped
+                            // whatever it makes of them, but keep the decision on the safe side)
+                            float mn[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int j = 0; j < kTcRows; j += 2)
+                                mn[(j >> 1) & 3] =
+                                    fmin3f(mn[(j >> 1) & 3], __uint_as_float(raw[j]), __uint_as_float(raw[j + 1]));
+                            const float hi = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
+                                                   fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
+                            const float size = fmaxf(hi, -fminf(fminf(mn[0], mn[1]), fminf(mn[2], mn[3]))) * p.mod.cap_in;
+                            cap_tier = __all_sync(0xffffffffu, size <= kTanhNear) ? 0
+                                                                                 : (__all_sync(0xffffffffu, size <= 1.f) ? 1 : 2);
                         }
                     } else if (plain) {
 #pragma unroll
@@ -1149,38 +1176,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tmem_ld32(trow + s_col + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(raw + 32));
                     tmem_wait_ld();
                     uint32_t pk[32];
-                    if constexpr ((MOD & MOD_CAP) != 0) {
+                    // modified scores: `logit` gives a pair's logits minus the row's max
+                    auto exp_pairs = [&](auto logit, auto masked) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            const int cj = h * 64 + 2 * j;
-                            const float x0 = p.mod.cap_out * tanh_f32(__uint_as_float(raw[2 * j]) * p.mod.cap_in);
-                            const float x1 = p.mod.cap_out * tanh_f32(__uint_as_float(raw[2 * j + 1]) * p.mod.cap_in);
-                            float2 pp = make_float2(fast_exp2(x0 - m_use), fast_exp2(x1 - m_use));
-                            if (!plain) {
+                            const float2 x =
+                                logit(make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), 2 * j);
+                            float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            if constexpr (decltype(masked)::value) {
+                                const int cj = h * 64 + 2 * j;
                                 pp.x = cj >= vlo && cj < vlim ? pp.x : 0.f;
                                 pp.y = cj + 1 >= vlo && cj + 1 < vlim ? pp.y : 0.f;
                             }
                             rsp[j & 3] = __fadd2_rn(rsp[j & 3], pp);
                             pk[j] = pack_bf16x2(pp.x, pp.y);
+                        }
+                    };
+                    auto exp_all = [&](auto logit) {
+                        if (plain) exp_pairs(logit, std::false_type{});
+                        else exp_pairs(logit, std::true_type{});
+                    };
+                    if constexpr ((MOD & MOD_CAP) != 0) {
+                        const float2 ci = both(p.mod.cap_in), cp2 = both(p.mod.cap_out);
+                        if (cap_tier == 0) {
+                            exp_all([&](float2 z, int) {
+                                const float2 u = __fmul2_rn(z, ci);
+                                return __ffma2_rn(__fmul2_rn(u, cp2), tanh_ratio_near(__fmul2_rn(u, u)), neg_m);
+                            });
+                        } else if (cap_tier == 1) {
+                            exp_all([&](float2 z, int) {
+                                const float2 u = __fmul2_rn(z, ci);
+                                return __ffma2_rn(__fmul2_rn(u, cp2), tanh_ratio_unit(__fmul2_rn(u, u)), neg_m);
+                            });
+                        } else {
+                            exp_pairs([&](float2 z, int) {
+                                return __ffma2_rn(make_float2(tanh_f32(z.x * p.mod.cap_in), tanh_f32(z.y * p.mod.cap_in)),
+                                                  cp2, neg_m);
+                            }, std::true_type{});
                         }
                     } else if ((MOD & MOD_BIAS) != 0 && !general) {
-                        const float b0 = fmaf(bias_k, (float)(h * 64), bias0);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int cj = h * 64 + 2 * j;
-                            float2 x = __ffma2_rn(
-                                make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), sc2,
-                                __ffma2_rn(make_float2((float)(2 * j), (float)(2 * j + 1)),
-                                           make_float2(bias_k, bias_k), make_float2(b0, b0)));
-                            x = __fadd2_rn(x, neg_m);
-                            float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                            if (!plain) {
-                                pp.x = cj >= vlo && cj < vlim ? pp.x : 0.f;
-                                pp.y = cj + 1 >= vlo && cj + 1 < vlim ? pp.y : 0.f;
-                            }
-                            rsp[j & 3] = __fadd2_rn(rsp[j & 3], pp);
-                            pk[j] = pack_bf16x2(pp.x, pp.y);
-                        }
+                        const float2 k2 = both(bias_k), b2 = both(fmaf(bias_k, (float)(h * 64), bias0) - m_use);
+                        exp_all([&](float2 z, int c) {
+                            return __ffma2_rn(z, sc2, __ffma2_rn(make_float2((float)c, (float)(c + 1)), k2, b2));
+                        });
                     } else if (plain || general) {  // every column visible, or masked logits already -inf
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {

@@ -10,6 +10,8 @@
 //     ("FlashAttention-Style Kernels", attention equation with additive M).
 // All of them move data with 16-byte vector accesses and are sized by
 // grid-stride loops over a multiple of the SM count.
+#include <algorithm>
+
 #include "host_common.cuh"
 
 namespace fa {
@@ -153,15 +155,17 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const void* __restrict
 // ----------------------------------------- rotary append, several axes ----
 // As rope_append_kernel, but every channel pair j has an axis (time, height,
 // width, ...) and turns by the table row of the token's position on that axis:
-// c, s = columns j, d/2 + j of row positions[axis[j]][token].  A thread takes 8
-// pairs of kMropeRows rows of a token, so that it looks the 16 factors up
-// once for all of them.
+// c, s = columns j, d/2 + j of row positions[axis[j]][token].  A CTA takes a
+// few tokens: their d factors are looked up once, element by element since
+// neighbouring pairs may use different rows, into shared memory, while every
+// thread already has its first rows' values on the way; then the rows of all
+// heads of those tokens are turned 16 bytes at a time.
 constexpr int kMaxAxes = 4;
-constexpr int kMropeRows = 4;
+constexpr int kMropeTokens = 4;  // tokens per CTA, at most
 struct PairAxes {
     uint8_t axis[64];
 };
-template <bool kF32>
+template <bool kF32, int D>
 __global__ void __launch_bounds__(256) mrope_append_kernel(const void* __restrict__ q, const void* __restrict__ k,
                                                            const void* __restrict__ v,
                                                            const int32_t* __restrict__ positions, int n_axes,
@@ -169,65 +173,84 @@ __global__ void __launch_bounds__(256) mrope_append_kernel(const void* __restric
                                                            int max_pos, uint16_t* __restrict__ q_out,
                                                            uint16_t* __restrict__ kc, uint16_t* __restrict__ vc,
                                                            const int32_t* __restrict__ slots, int N, int Hq, int Hkv,
-                                                           int d, int num_blocks, DevCtx ctx) {
-    const int half = d >> 1, cph = half >> 3;  // 8-pair chunks per row
-    const int rpt = Hq + Hkv, groups = (rpt + kMropeRows - 1) / kMropeRows;
-    const long total = (long)N * groups * cph;
-    for (long idx = (long)blockIdx.x * blockDim.x + threadIdx.x; idx < total; idx += (long)gridDim.x * blockDim.x) {
-        const int c = (int)(idx % cph);
-        const long gi = idx / cph;
-        const int r0 = (int)(gi % groups) * kMropeRows;
-        const long tok = gi / groups;
-        int pos[kMaxAxes];
-        bool bad = false;
-#pragma unroll
-        for (int a = 0; a < kMaxAxes; ++a) {
-            pos[a] = a < n_axes ? __ldg(positions + (long)a * N + tok) : 0;
-            bad |= pos[a] < 0 || pos[a] >= max_pos;
+                                                           int tokens, int num_blocks, DevCtx ctx) {
+    constexpr int half = D / 2, cph = half / 8;  // 8-pair chunks per row
+    __shared__ __align__(16) float factors[kMropeTokens][D];
+    __shared__ int slot_of[kMropeTokens];  // cache slot, -1: not cached
+    __shared__ int bad[kMropeTokens];      // a position outside the table: the token is left out whole
+    const long tok0 = (long)blockIdx.x * tokens;
+    const int n = (int)min((long)tokens, N - tok0);
+    const int rpt = Hq + Hkv, rows = n * rpt;
+    if (threadIdx.x < n) {
+        const long tok = tok0 + threadIdx.x;
+        bool b = false;
+        for (int a = 0; a < n_axes; ++a) {
+            const int p = __ldg(positions + (long)a * N + tok);
+            b |= p < 0 || p >= max_pos;
         }
-        const int slot = __ldg(slots + tok);
-        if (bad) {  // the token is left out whole
-            raise_error(ctx, ERR_BOUNDS_BIT);
-            continue;
+        int slot = __ldg(slots + tok);
+        if (b || slot >= num_blocks * kBlock) raise_error(ctx, ERR_BOUNDS_BIT);
+        slot_of[threadIdx.x] = slot >= num_blocks * kBlock ? -1 : slot;
+        bad[threadIdx.x] = b;
+    }
+    // item = (row, chunk), chunks fastest; a row is (token, head of q, then of k)
+    const int c = threadIdx.x % cph;
+    constexpr int kStep = 256 / cph;  // rows side by side
+    int row = threadIdx.x / cph;
+    float x1[8], x2[8];
+    auto load = [&](int r) {
+        const long tok = tok0 + r / rpt;
+        const int h = r % rpt;
+        const void* base = h < Hq ? q : k;
+        const long src = h < Hq ? (tok * Hq + h) * D : (tok * Hkv + (h - Hq)) * D;
+        load8<kF32>(base, src + c * 8, x1);
+        load8<kF32>(base, src + half + c * 8, x2);
+    };
+    if (row < rows) load(row);
+    for (int e = threadIdx.x; e < n * half; e += 256) {
+        const int t = e / half, j = e % half;
+        const int p = __ldg(positions + (long)axes.axis[j] * N + tok0 + t);
+        if (p >= 0 && p < max_pos) {
+            factors[t][j] = __ldg(cos_sin + (long)p * D + j);
+            factors[t][half + j] = __ldg(cos_sin + (long)p * D + half + j);
         }
-        const bool slot_bad = slot >= num_blocks * kBlock;
-        if (slot_bad) raise_error(ctx, ERR_BOUNDS_BIT);
-        float co[8], si[8];
+    }
+    __syncthreads();
+    for (; row < rows; row += kStep) {
+        const int t = row / rpt, r = row % rpt;
+        const long tok = tok0 + t;
+        const bool is_q = r < Hq;
+        const int slot = slot_of[t];
+        const bool skip = bad[t] || (!is_q && slot < 0);
+        float y1[8], y2[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int a = axes.axis[c * 8 + i];
-            const int p = a == 0 ? pos[0] : (a == 1 ? pos[1] : (a == 2 ? pos[2] : pos[3]));
-            co[i] = __ldg(cos_sin + (long)p * d + c * 8 + i);
-            si[i] = __ldg(cos_sin + (long)p * d + half + c * 8 + i);
-        }
+        for (int i = 0; i < 8; i += 4) {
+            const float4 co = *reinterpret_cast<const float4*>(&factors[t][c * 8 + i]);
+            const float4 si = *reinterpret_cast<const float4*>(&factors[t][half + c * 8 + i]);
+            const float cs[4] = {co.x, co.y, co.z, co.w}, sn[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-        for (int rr = 0; rr < kMropeRows; ++rr) {
-            const int r = r0 + rr;
-            const bool is_q = r < Hq;
-            if (r >= rpt || (!is_q && (slot < 0 || slot_bad))) continue;
-            const int h = is_q ? r : r - Hq;
-            const long src = is_q ? (tok * Hq + h) * d : (tok * Hkv + h) * d;
-            float x1[8], x2[8], y1[8], y2[8];
-            load8<kF32>(is_q ? q : k, src + c * 8, x1);
-            load8<kF32>(is_q ? q : k, src + half + c * 8, x2);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y1[i] = fmaf(x1[i], co[i], -(x2[i] * si[i]));
-                y2[i] = fmaf(x2[i], co[i], x1[i] * si[i]);
+            for (int e = 0; e < 4; ++e) {
+                y1[i + e] = fmaf(x1[i + e], cs[e], -(x2[i + e] * sn[e]));
+                y2[i + e] = fmaf(x2[i + e], cs[e], x1[i + e] * sn[e]);
             }
-            if (is_q) {
-                *reinterpret_cast<uint4*>(q_out + src + c * 8) = pack8(y1);
-                *reinterpret_cast<uint4*>(q_out + src + half + c * 8) = pack8(y2);
-            } else {
-                const long dst = (((long)(slot / kBlock) * Hkv + h) * kBlock + (slot % kBlock)) * d;
-                float v1[8], v2[8];
-                load8<kF32>(v, src + c * 8, v1);
-                load8<kF32>(v, src + half + c * 8, v2);
-                *reinterpret_cast<uint4*>(kc + dst + c * 8) = pack8(y1);
-                *reinterpret_cast<uint4*>(kc + dst + half + c * 8) = pack8(y2);
-                *reinterpret_cast<uint4*>(vc + dst + c * 8) = pack8(v1);
-                *reinterpret_cast<uint4*>(vc + dst + half + c * 8) = pack8(v2);
-            }
+        }
+        if (row + kStep < rows) load(row + kStep);
+        if (skip) continue;
+        if (is_q) {
+            const long dst = (tok * Hq + r) * D;
+            *reinterpret_cast<uint4*>(q_out + dst + c * 8) = pack8(y1);
+            *reinterpret_cast<uint4*>(q_out + dst + half + c * 8) = pack8(y2);
+        } else {
+            const int h = r - Hq;
+            const long src = (tok * Hkv + h) * D;
+            const long dst = (((long)(slot / kBlock) * Hkv + h) * kBlock + (slot % kBlock)) * D;
+            float v1[8], v2[8];
+            load8<kF32>(v, src + c * 8, v1);
+            load8<kF32>(v, src + half + c * 8, v2);
+            *reinterpret_cast<uint4*>(kc + dst + c * 8) = pack8(y1);
+            *reinterpret_cast<uint4*>(kc + dst + half + c * 8) = pack8(y2);
+            *reinterpret_cast<uint4*>(vc + dst + c * 8) = pack8(v1);
+            *reinterpret_cast<uint4*>(vc + dst + half + c * 8) = pack8(v2);
         }
     }
 }
@@ -583,13 +606,15 @@ fa_status fa_cache_append_mrope(const void* q, const void* k, const void* v, con
     if (st != FA_OK) return st;
     DevCtx ctx;
     if ((st = make_ctx(&ctx)) != FA_OK) return st;
-    const long work = (long)N * ((Hq + Hkv + kMropeRows - 1) / kMropeRows) * (d / 16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    auto kernel = in_dtype == FA_F32 ? mrope_append_kernel<true> : mrope_append_kernel<false>;
-    kernel<<<grid_for(work, 256), 256, 0, s>>>(q, k, v, positions, n_axes, axes, cos_sin, max_pos,
-                                               static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_cache),
-                                               static_cast<uint16_t*>(v_cache), slot_mapping, N, Hq, Hkv, d, num_blocks,
-                                               ctx);
+    // one token per CTA while that leaves SMs idle, more beyond
+    const int tokens = (int)std::min<long>(kMropeTokens, std::max<long>(1, N / ((long)sm_count() * 4)));
+    auto kernel = in_dtype == FA_F32 ? (d == 128 ? mrope_append_kernel<true, 128> : mrope_append_kernel<true, 64>)
+                                     : (d == 128 ? mrope_append_kernel<false, 128> : mrope_append_kernel<false, 64>);
+    kernel<<<(N + tokens - 1) / tokens, 256, 0, s>>>(q, k, v, positions, n_axes, axes, cos_sin, max_pos,
+                                                     static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_cache),
+                                                     static_cast<uint16_t*>(v_cache), slot_mapping, N, Hq, Hkv, tokens,
+                                                     num_blocks, ctx);
     st = cuda_status(cudaGetLastError());
     if (st == FA_OK) set_launch_count(1);
     return st;

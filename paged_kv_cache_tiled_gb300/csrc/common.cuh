@@ -285,6 +285,11 @@ __device__ __forceinline__ float fmax3f(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+__device__ __forceinline__ float fmin3f(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 // m16n8k16 warp MMA, f16 inputs, fp32 accumulation (D += A B).
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -311,6 +316,28 @@ __device__ __forceinline__ float tanh_f32(float u) {
     const float e = fast_exp2(a * 2.885390081777927f);  // e^(2a); +inf gives 1
     const float big = copysignf(1.f - __fdividef(2.f, 1.f + e), u);
     return a <= 1.f ? u * t : big;
+}
+
+// tanh(u) / u for a pair with |u| <= kTanhNear (w = u^2): a degree-4 minimax
+// polynomial of the same kind (relative error 1.8e-7 as evaluated), in packed operations.
+constexpr float kTanhNear = 0.6f;
+constexpr float kTanhD0 = 0.99999994f, kTanhD1 = -0.3333231f, kTanhD2 = 0.13310173f, kTanhD3 = -0.05210147f,
+                kTanhD4 = 0.015475417f;
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 tanh_ratio_near(float2 w) {
+    float2 t = __ffma2_rn(both(kTanhD4), w, both(kTanhD3));
+    t = __ffma2_rn(t, w, both(kTanhD2));
+    t = __ffma2_rn(t, w, both(kTanhD1));
+    return __ffma2_rn(t, w, both(kTanhD0));
+}
+// The same for |u| <= 1.
+__device__ __forceinline__ float2 tanh_ratio_unit(float2 w) {
+    float2 t = __ffma2_rn(both(kTanhC6), w, both(kTanhC5));
+    t = __ffma2_rn(t, w, both(kTanhC4));
+    t = __ffma2_rn(t, w, both(kTanhC3));
+    t = __ffma2_rn(t, w, both(kTanhC2));
+    t = __ffma2_rn(t, w, both(kTanhC1));
+    return __ffma2_rn(t, w, both(kTanhC0));
 }
 
 // ------------------------------------------------------- score modifiers ---

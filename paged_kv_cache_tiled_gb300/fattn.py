@@ -127,12 +127,12 @@ def _check(st: int, where: str):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream))
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t: torch.Tensor, name: str, dtype, ndim: int | None = None):
@@ -146,25 +146,69 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: int | None = None):
         raise ValueError(f"{name} must have {ndim} dims")
 
 
-def _shape(t, name: str, *shape):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-
-
-def _one_device(**tensors):
-    """Every tensor given must live on the current device, whose stream the call runs on."""
+def _device_of(q, name: str) -> int:
+    """The current device, on which q must live: a call runs on a stream of the current device."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     cur = torch.cuda.current_device()
-    for n, t in tensors.items():
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"{n} is on {t.device}, but the current device is cuda:{cur}")
+    if q.get_device() != cur:
+        raise ValueError(f"{name} is on {q.device}, but the current device is cuda:{cur}")
+    return cur
 
 
-def _workspace(ws, nbytes: int, device):
+def _arg(t, name: str, dtype, shape, dev: int):
+    """Checks a tensor's type, shape, layout and device in as few attribute reads as a small call can
+    afford; returns its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _opt(t, name: str, dtype, shape, dev: int):
+    return None if t is None else _arg(t, name, dtype, shape, dev)
+
+
+def _dims(t, name: str, n: int):
+    """The shape of a tensor of n dims."""
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a tensor of {n} dims")
+    return t.shape
+
+
+def _kept_for(stream, *tensors):
+    """Tensors that a call made itself come from the current stream's memory: when the call runs on another stream,
+    that memory must not be handed out again before it is done there."""
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        for t in tensors:
+            t.record_stream(s)
+
+
+def _workspace(ws, nbytes: int, dev: int, stream):
+    """(address, bytes) of the workspace given, or of a new one; the tensor comes last to be kept alive."""
+    if nbytes == 0 and ws is None:
+        return None, 0, None
     if ws is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("ws must be a contiguous CUDA tensor")
-    return ws
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+        _kept_for(stream, ws)
+    elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on cuda:{dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _current_stream(stream, dev: int):
+    return _stream(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 # ------------------------------------------------------------------ prefill
@@ -262,32 +306,19 @@ def fa_prefill_mod(q, k, v, causal: bool = True, scale: float | None = None, sof
     """fa_prefill with modified scores: logits f(scale q.k) - alibi_slopes[h] |i - j|, f(z) = softcap
     tanh(z / softcap) (softcap > 0); a key is visible when every mask given allows it: causal (or below
     prefix_lens[b]), window, doc_ids [B, T] (runs of equal ids; negative: padding)."""
-    for n, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, n, torch.bfloat16, 4)
-    B, T, Hq, d = q.shape
-    Hkv = k.shape[2]
-    _shape(k, "k", B, T, Hkv, d)
-    _shape(v, "v", B, T, Hkv, d)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    B, T, Hq, d = _dims(q, "q", 4)
+    Hkv = _dims(k, "k", 4)[2]
+    dev, bf16, f32, i32 = _device_of(q, "q"), torch.bfloat16, torch.float32, torch.int32
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", torch.bfloat16, 4)
-    _shape(out, "out", B, T, Hq, d)
-    for n, t, dt, shape in (("alibi_slopes", alibi_slopes, torch.float32, (Hq,)),
-                            ("prefix_lens", prefix_lens, torch.int32, (B,)),
-                            ("doc_ids", doc_ids, torch.int32, (B, T)), ("lse", lse, torch.float32, (B, Hq, T))):
-        if t is not None:
-            _need(t, n, dt)
-            _shape(t, n, *shape)
-    if doc_ids is not None:
-        ws = _workspace(ws, fa_prefill_mod_workspace_size(B, T), q.device)
-    _one_device(q=q, k=k, v=v, out=out, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, doc_ids=doc_ids, lse=lse,
-                ws=ws)
-    _check(_lib.fa_prefill_mod(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, T, Hq, Hkv, d, int(causal),
-                               float(scale), float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens),
-                               _ptr(doc_ids), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                               _stream(stream)), "fa_prefill_mod")
+    wp, wn, ws = _workspace(ws, fa_prefill_mod_workspace_size(B, T), dev, stream) if doc_ids is not None else (None, 0, None)
+    _check(_lib.fa_prefill_mod(
+        _arg(q, "q", bf16, (B, T, Hq, d), dev), _arg(k, "k", bf16, (B, T, Hkv, d), dev),
+        _arg(v, "v", bf16, (B, T, Hkv, d), dev), _arg(out, "out", bf16, (B, T, Hq, d), dev),
+        _opt(lse, "lse", f32, (B, Hq, T), dev), B, T, Hq, Hkv, d, 1 if causal else 0,
+        d ** -0.5 if scale is None else scale, softcap, _opt(alibi_slopes, "alibi_slopes", f32, (Hq,), dev), window,
+        _opt(prefix_lens, "prefix_lens", i32, (B,), dev), _opt(doc_ids, "doc_ids", i32, (B, T), dev), wp, wn,
+        _current_stream(stream, dev)), "fa_prefill_mod")
     return out
 
 
@@ -368,39 +399,27 @@ def fa_cache_append_mrope(q, k, v, positions, pair_axes, cos_sin, k_cache, v_cac
                           stream=None):
     """fa_cache_append_rope with positions [n_axes, N]: channel pair j turns by the table row of
     positions[pair_axes[j]] (pair_axes: d/2 small integers on the host)."""
-    if q.dtype not in (torch.bfloat16, torch.float32) or k.dtype != q.dtype or v.dtype != q.dtype:
+    N, Hq, d = _dims(q, "q", 3)
+    Hkv = _dims(k, "k", 3)[1]
+    n_axes = _dims(positions, "positions", 2)[0]
+    nb, max_pos = _dims(k_cache, "k_cache", 4)[0], _dims(cos_sin, "cos_sin", 2)[0]
+    dev, dt, bf16 = _device_of(q, "q"), q.dtype, torch.bfloat16
+    if dt is not torch.bfloat16 and dt is not torch.float32:
         raise ValueError("q, k, v must all be bf16 or all fp32")
-    _need(q, "q", q.dtype, 3)
-    _need(k, "k", q.dtype, 3)
-    _need(v, "v", q.dtype, 3)
-    _need(positions, "positions", torch.int32, 2)
-    _need(cos_sin, "cos_sin", torch.float32, 2)
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, 4)
-    _need(slot_mapping, "slot_mapping", torch.int32, 1)
-    N, Hq, d = q.shape
-    Hkv, nb = k.shape[1], k_cache.shape[0]
-    n_axes = positions.shape[0]
-    _shape(k, "k", N, Hkv, d)
-    _shape(v, "v", N, Hkv, d)
-    _shape(positions, "positions", n_axes, N)
-    _shape(cos_sin, "cos_sin", cos_sin.shape[0], d)
-    _shape(k_cache, "k_cache", nb, Hkv, 16, d)
-    _shape(v_cache, "v_cache", nb, Hkv, 16, d)
-    _shape(slot_mapping, "slot_mapping", N)
-    axes = [int(a) for a in pair_axes]
-    if len(axes) != d // 2 or any(a < 0 or a >= n_axes for a in axes):
+    if not isinstance(pair_axes, bytes):
+        pair_axes = bytes(pair_axes)  # ValueError outside 0 .. 255
+    if len(pair_axes) != d // 2 or max(pair_axes) >= n_axes:
         raise ValueError(f"pair_axes must be {d // 2} integers in [0, {n_axes})")
     if q_out is None:
-        q_out = torch.empty(N, Hq, d, dtype=torch.bfloat16, device=q.device)
-    _need(q_out, "q_out", torch.bfloat16, 3)
-    _shape(q_out, "q_out", N, Hq, d)
-    _one_device(q=q, k=k, v=v, positions=positions, cos_sin=cos_sin, k_cache=k_cache, v_cache=v_cache,
-                slot_mapping=slot_mapping, q_out=q_out)
-    dt = FA_F32 if q.dtype == torch.float32 else FA_BF16
-    _check(_lib.fa_cache_append_mrope(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), n_axes, bytes(axes), _ptr(cos_sin),
-                                      cos_sin.shape[0], _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
-                                      N, Hq, Hkv, d, nb, dt, _stream(stream)), "fa_cache_append_mrope")
+        q_out = torch.empty(N, Hq, d, dtype=bf16, device=q.device)
+    _check(_lib.fa_cache_append_mrope(
+        _arg(q, "q", dt, (N, Hq, d), dev), _arg(k, "k", dt, (N, Hkv, d), dev), _arg(v, "v", dt, (N, Hkv, d), dev),
+        _arg(positions, "positions", torch.int32, (n_axes, N), dev), n_axes, pair_axes,
+        _arg(cos_sin, "cos_sin", torch.float32, (max_pos, d), dev), max_pos,
+        _arg(q_out, "q_out", bf16, (N, Hq, d), dev), _arg(k_cache, "k_cache", bf16, (nb, Hkv, 16, d), dev),
+        _arg(v_cache, "v_cache", bf16, (nb, Hkv, 16, d), dev), _arg(slot_mapping, "slot_mapping", torch.int32, (N,), dev),
+        N, Hq, Hkv, d, nb, FA_F32 if dt is torch.float32 else FA_BF16, _current_stream(stream, dev)),
+        "fa_cache_append_mrope")
     return q_out
 
 
@@ -600,35 +619,23 @@ def fa_paged_attn_accum_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d,
     return int(_lib.fa_paged_attn_accum_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len))
 
 
-def _paged_mod_args(q, k_cache, v_cache, block_table, ctx_lens, q_lens, alibi_slopes, prefix_lens, out, lse,
-                    max_q_len):
-    """Checks shared by the paged calls with modified scores; returns (out, max_q_len, sizes)."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, 4)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(ctx_lens, "ctx_lens", torch.int32, 1)
-    _need(q_lens, "q_lens", torch.int32, 1)
-    total_q, Hq, d = q.shape
-    num_blocks, Hkv, bs, _ = k_cache.shape
-    num_seqs, mbps = block_table.shape
-    _shape(k_cache, "k_cache", num_blocks, Hkv, bs, d)
-    _shape(v_cache, "v_cache", num_blocks, Hkv, bs, d)
-    _shape(ctx_lens, "ctx_lens", num_seqs)
-    _shape(q_lens, "q_lens", num_seqs)
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, "out", torch.bfloat16, 3)
-    _shape(out, "out", total_q, Hq, d)
-    for n, t, dt, shape in (("alibi_slopes", alibi_slopes, torch.float32, (Hq,)),
-                            ("prefix_lens", prefix_lens, torch.int32, (num_seqs,)),
-                            ("lse", lse, torch.float32, (total_q, Hq))):
-        if t is not None:
-            _need(t, n, dt)
-            _shape(t, n, *shape)
-    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, ctx_lens=ctx_lens, q_lens=q_lens,
-                alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, out=out, lse=lse)
-    return out, total_q if max_q_len is None else int(max_q_len), (num_seqs, mbps, num_blocks, Hq, Hkv, d, bs, total_q)
+def _paged_mod_args(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal, scale, softcap, alibi_slopes, window,
+                    prefix_lens, out, lse, max_q_len):
+    """Checks shared by the paged calls with modified scores: (device, the arguments up to lse, those from num_seqs to
+    max_q_len, the workspace queries' sizes)."""
+    total_q, Hq, d = _dims(q, "q", 3)
+    nb, Hkv, bs, _ = _dims(k_cache, "k_cache", 4)
+    S, mbps = _dims(block_table, "block_table", 2)
+    dev, bf16, i32 = _device_of(q, "q"), torch.bfloat16, torch.int32
+    max_q_len = total_q if max_q_len is None else max_q_len
+    head = (_arg(q, "q", bf16, (total_q, Hq, d), dev), _arg(k_cache, "k_cache", bf16, (nb, Hkv, bs, d), dev),
+            _arg(v_cache, "v_cache", bf16, (nb, Hkv, bs, d), dev), _arg(block_table, "block_table", i32, (S, mbps), dev),
+            _arg(ctx_lens, "ctx_lens", i32, (S,), dev), _arg(q_lens, "q_lens", i32, (S,), dev),
+            _arg(out, "out", bf16, (total_q, Hq, d), dev), _opt(lse, "lse", torch.float32, (total_q, Hq), dev))
+    tail = (S, mbps, nb, Hq, Hkv, d, bs, 1 if causal else 0, d ** -0.5 if scale is None else scale, softcap,
+            _opt(alibi_slopes, "alibi_slopes", torch.float32, (Hq,), dev), window,
+            _opt(prefix_lens, "prefix_lens", i32, (S,), dev), total_q, max_q_len)
+    return dev, head, tail, (S, mbps, Hq, Hkv, d, total_q, max_q_len)
 
 
 def fa_paged_attn_mod(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal: bool = True,
@@ -636,16 +643,12 @@ def fa_paged_attn_mod(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal
                       prefix_lens=None, out=None, lse=None, max_q_len: int | None = None, ws=None, stream=None):
     """fa_paged_attn with modified scores (as fa_prefill_mod, in cache positions); lse (optional, fp32
     [total_q, Hq]) receives the log-sum-exp of every row."""
-    out, max_q_len, (S, mbps, nb, Hq, Hkv, d, bs, total_q) = _paged_mod_args(
-        q, k_cache, v_cache, block_table, ctx_lens, q_lens, alibi_slopes, prefix_lens, out, lse, max_q_len)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    ws = _workspace(ws, fa_paged_attn_mod_workspace_size(S, mbps, Hq, Hkv, d, total_q, max_q_len), q.device)
-    _one_device(ws=ws)
-    _check(_lib.fa_paged_attn_mod(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(ctx_lens),
-                                  _ptr(q_lens), _ptr(out), _ptr(lse), S, mbps, nb, Hq, Hkv, d, bs, int(causal),
-                                  float(scale), float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens),
-                                  total_q, max_q_len, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "fa_paged_attn_mod")
+    if out is None:
+        out = torch.empty_like(q)
+    dev, head, tail, sizes = _paged_mod_args(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal, scale, softcap,
+                                             alibi_slopes, window, prefix_lens, out, lse, max_q_len)
+    wp, wn, ws = _workspace(ws, 0 if ws is not None else fa_paged_attn_mod_workspace_size(*sizes), dev, stream)
+    _check(_lib.fa_paged_attn_mod(*head, *tail, wp, wn, _current_stream(stream, dev)), "fa_paged_attn_mod")
     return out
 
 
@@ -656,25 +659,18 @@ def fa_paged_attn_accum(q, k_cache, v_cache, block_table, ctx_lens, q_lens, acc_
     """fa_paged_attn_mod that also writes acc_out [num_seqs, Hkv, acc_len] = decay * acc_in (0 for the chunk's own
     tokens, and where acc_in is None) + the softmax weights every cached token received from the chunk's queries and
     the group's heads.  acc_in and acc_out may be the same tensor."""
+    if out is None:
+        out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
-    out, max_q_len, (S, mbps, nb, Hq, Hkv, d, bs, total_q) = _paged_mod_args(
-        q, k_cache, v_cache, block_table, ctx_lens, q_lens, alibi_slopes, prefix_lens, out, lse, max_q_len)
-    _need(acc_out, "acc_out", torch.float32, 3)
-    acc_len = acc_out.shape[2]
-    _shape(acc_out, "acc_out", S, Hkv, acc_len)
-    if acc_in is not None:
-        _need(acc_in, "acc_in", torch.float32, 3)
-        _shape(acc_in, "acc_in", S, Hkv, acc_len)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    ws = _workspace(ws, fa_paged_attn_accum_workspace_size(S, mbps, Hq, Hkv, d, total_q, max_q_len), q.device)
-    _one_device(ws=ws, acc_in=acc_in, acc_out=acc_out)
-    _check(_lib.fa_paged_attn_accum(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(ctx_lens),
-                                    _ptr(q_lens), _ptr(out), _ptr(lse), _ptr(acc_in), _ptr(acc_out), acc_len,
-                                    float(decay), S, mbps, nb, Hq, Hkv, d, bs, int(causal), float(scale),
-                                    float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens), total_q,
-                                    max_q_len, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "fa_paged_attn_accum")
+        _kept_for(stream, lse)
+    dev, head, tail, sizes = _paged_mod_args(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal, scale, softcap,
+                                             alibi_slopes, window, prefix_lens, out, lse, max_q_len)
+    rows = (sizes[0], sizes[3], _dims(acc_out, "acc_out", 3)[2])
+    wp, wn, ws = _workspace(ws, 0 if ws is not None else fa_paged_attn_accum_workspace_size(*sizes), dev, stream)
+    _check(_lib.fa_paged_attn_accum(*head, _opt(acc_in, "acc_in", torch.float32, rows, dev),
+                                    _arg(acc_out, "acc_out", torch.float32, rows, dev), rows[2], decay, *tail, wp, wn,
+                                    _current_stream(stream, dev)), "fa_paged_attn_accum")
     return out
 
 
@@ -688,38 +684,22 @@ def fa_cache_evict(k_cache, v_cache, acc, block_table, ctx_lens, dst_table, keep
     [num_seqs, Hkv, acc_len] (`keep` in all) from the blocks of block_table to those of dst_table, in order of
     position; returns the new lengths int32 [num_seqs].  acc_out and kept (int32 [num_seqs, Hkv, keep], old
     positions) are optional outputs."""
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, 4)
-    _need(acc, "acc", torch.float32, 3)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(dst_table, "dst_table", torch.int32, 2)
-    _need(ctx_lens, "ctx_lens", torch.int32, 1)
-    nb, Hkv, bs, d = k_cache.shape
-    S, mbps = block_table.shape
-    _shape(v_cache, "v_cache", nb, Hkv, bs, d)
-    _shape(acc, "acc", S, Hkv, acc.shape[2])
-    _shape(dst_table, "dst_table", S, dst_table.shape[1])
-    _shape(ctx_lens, "ctx_lens", S)
-    if acc_out is not None:
-        _need(acc_out, "acc_out", torch.float32, 3)
-        _shape(acc_out, "acc_out", S, Hkv, acc_out.shape[2])
+    nb, Hkv, bs, d = _dims(k_cache, "k_cache", 4)
+    S, mbps = _dims(block_table, "block_table", 2)
+    acc_len, dmbps = _dims(acc, "acc", 3)[2], _dims(dst_table, "dst_table", 2)[1]
+    dev, bf16, f32, i32 = _device_of(k_cache, "k_cache"), torch.bfloat16, torch.float32, torch.int32
     if new_lens is None:
-        new_lens = torch.empty(S, dtype=torch.int32, device=k_cache.device)
-    _need(new_lens, "new_lens", torch.int32, 1)
-    _shape(new_lens, "new_lens", S)
-    if kept is not None:
-        _need(kept, "kept", torch.int32, 3)
-        _shape(kept, "kept", S, Hkv, int(keep))
-    else:
-        ws = _workspace(ws, fa_cache_evict_workspace_size(S, mbps, Hkv, int(keep)), k_cache.device)
-    _one_device(k_cache=k_cache, v_cache=v_cache, acc=acc, block_table=block_table, dst_table=dst_table,
-                ctx_lens=ctx_lens, acc_out=acc_out, new_lens=new_lens, kept=kept, ws=ws)
-    _check(_lib.fa_cache_evict(_ptr(k_cache), _ptr(v_cache), _ptr(acc), acc.shape[2], _ptr(block_table),
-                               _ptr(ctx_lens), _ptr(dst_table), _ptr(acc_out),
-                               0 if acc_out is None else acc_out.shape[2], _ptr(new_lens), _ptr(kept), S, mbps,
-                               dst_table.shape[1], nb, Hkv, d, bs, int(keep), int(recent), int(sink), _ptr(ws),
-                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
-           "fa_cache_evict")
+        new_lens = torch.empty(S, dtype=i32, device=k_cache.device)
+    out_len = 0 if acc_out is None else _dims(acc_out, "acc_out", 3)[2]
+    need = fa_cache_evict_workspace_size(S, mbps, Hkv, keep) if kept is None and ws is None else 0
+    wp, wn, ws = _workspace(ws, need, dev, stream)
+    _check(_lib.fa_cache_evict(
+        _arg(k_cache, "k_cache", bf16, (nb, Hkv, bs, d), dev), _arg(v_cache, "v_cache", bf16, (nb, Hkv, bs, d), dev),
+        _arg(acc, "acc", f32, (S, Hkv, acc_len), dev), acc_len, _arg(block_table, "block_table", i32, (S, mbps), dev),
+        _arg(ctx_lens, "ctx_lens", i32, (S,), dev), _arg(dst_table, "dst_table", i32, (S, dmbps), dev),
+        _opt(acc_out, "acc_out", f32, (S, Hkv, out_len), dev), out_len, _arg(new_lens, "new_lens", i32, (S,), dev),
+        _opt(kept, "kept", i32, (S, Hkv, keep), dev), S, mbps, dmbps, nb, Hkv, d, bs, keep, recent, sink, wp, wn,
+        _current_stream(stream, dev)), "fa_cache_evict")
     return new_lens
 
 
