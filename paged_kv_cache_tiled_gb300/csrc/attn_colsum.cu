@@ -51,8 +51,8 @@ struct CsCfg {
     static constexpr int kTileBytes = kAtoms * kAtomBytes;
     static constexpr uint32_t kGroup = kAtoms * 1024;  // 8-row groups of the K tile (halves side by side)
     static constexpr int kBars = 1 + 2 * kCsStages + 4 + 2;
-    // per summing warp and column: -lse, distance slope, position (each warp keeps
-    // its own, so no barrier across warps is needed in the loop)
+    // per summing warp and column: -lse, distance slope, run of keys seen (each warp keeps its own, so no barrier across
+    // warps is needed in the loop)
     static constexpr int kColBytes = 8 * 3 * kCsRows * 4;
     static constexpr int kSmem = 1024 + (1 + kCsStages) * kTileBytes + kColBytes + kCsRows * 4 + kBars * 8 + 16;
 };
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kCsThreads, 2)
         const uint32_t trow = tbase + ((uint32_t)(quarter * 32) << 16) + w * 128;
         float* nlse = cols + warp * 3 * kCsRows;
         float* slope = nlse + kCsRows;
-        int* cpos = reinterpret_cast<int*>(slope + kCsRows);
+        short2* run = reinterpret_cast<short2*>(slope + kCsRows);  // from this warp's first key
         float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const int k_lo = kv0 + quarter * 32, k_hi = min(cl, k_lo + 32);  // this warp's keys
         for (int i = w; ok && i < n; i += 2) {
@@ -254,10 +254,9 @@ __global__ void __launch_bounds__(kCsThreads, 2)
                     L = L == -INFINITY ? 0.f : -L * kCsLog2e;
                 }
                 nlse[c] = L;
-                if constexpr (MOD == CS_BIAS) {
-                    slope[c] = -__ldg(p.mod.slopes + head) * kCsLog2e;
-                    cpos[c] = pos0 + tok;
-                }
+                const int2 seen = tok < ql ? cs_range(p, pos0 + tok, prefix, cl) : make_int2(0, 0);
+                run[c] = make_short2((short)min(32, max(0, seen.x - k_lo)), (short)min(32, max(0, seen.y - k_lo)));
+                if constexpr (MOD == CS_BIAS) slope[c] = -__ldg(p.mod.slopes + head) * kCsLog2e;
             }
             __syncwarp();
             // every row of the tile is real and sees every key of this warp (warp-uniform)
@@ -292,19 +291,15 @@ __global__ void __launch_bounds__(kCsThreads, 2)
                             }
                             if constexpr (MOD == CS_BIAS) {
                                 const float2 sl = *reinterpret_cast<const float2*>(slope + b * 32 + j + e);
-                                const int2 cp = *reinterpret_cast<const int2*>(cpos + b * 32 + j + e);
-                                x.x = fmaf(sl.x, fabsf((float)(k_lo + lane - cp.x)), x.x);
-                                x.y = fmaf(sl.y, fabsf((float)(k_lo + lane - cp.y)), x.y);
+                                const int c = b * 32 + j + e, d0 = k_lo + lane - pos0 - tok0;
+                                x.x = fmaf(sl.x, fabsf((float)(d0 - (p.pack ? c >> p.pack_shift : c))), x.x);
+                                x.y = fmaf(sl.y, fabsf((float)(d0 - (p.pack ? (c + 1) >> p.pack_shift : c + 1))), x.y);
                             }
                             float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                             if constexpr (decltype(masked)::value) {
-                                const int c = b * 32 + j + e, key = k_lo + lane;
-                                const int t0 = tok0 + (p.pack ? c >> p.pack_shift : c);
-                                const int t1 = tok0 + (p.pack ? (c + 1) >> p.pack_shift : c + 1);
-                                const int2 r0 = cs_range(p, pos0 + t0, prefix, cl);
-                                const int2 r1 = cs_range(p, pos0 + t1, prefix, cl);
-                                pr.x = t0 < ql && key >= r0.x && key < r0.y ? pr.x : 0.f;
-                                pr.y = t1 < ql && key >= r1.x && key < r1.y ? pr.y : 0.f;
+                                const short2 ra = run[b * 32 + j + e], rb = run[b * 32 + j + e + 1];
+                                pr.x = lane >= ra.x && lane < ra.y ? pr.x : 0.f;
+                                pr.y = lane >= rb.x && lane < rb.y ? pr.y : 0.f;
                             }
                             sum[(j + e) >> 1 & 3] = __fadd2_rn(sum[(j + e) >> 1 & 3], pr);
                         }

@@ -88,6 +88,12 @@ struct TcCfg {
     static constexpr uint32_t kPagedGroup = kAtoms * 1024;
 };
 
+// Column numbers of a half tile in pairs, operands of the distance bias.
+#define FA_COL8(c) {c, c + 1}, {c + 2, c + 3}, {c + 4, c + 5}, {c + 6, c + 7}
+__constant__ float2 kColumns[32] = {FA_COL8(0.f),  FA_COL8(8.f),  FA_COL8(16.f), FA_COL8(24.f),
+                                    FA_COL8(32.f), FA_COL8(40.f), FA_COL8(48.f), FA_COL8(56.f)};
+#undef FA_COL8
+
 struct TcParams {
     int B, T;        // dense / masked: sequence length (row stride of q/k/v/out)
     int q0, Tq, Tk;  // dense: query rows [q0, q0 + Tq) of each sequence against keys [0, Tk)
@@ -118,6 +124,7 @@ struct TcParams {
     int mbps, num_blocks;
     // modified variants
     ScoreMod mod;
+    CapPoly cap;
     const int2* doc_rows;      // dense: per row of [B, T] its document's [first, end), empty for padding; or null
     const int32_t* doc_order;  // dense with documents: (sequence, query tile) entries, longest first
     DevCtx ctx;
@@ -1061,7 +1068,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 // every column of every row of the warp visible and no mask values
                 const bool plain = !general && __all_sync(0xffffffffu, vlo <= 0 && vlim >= kTcRows);
-                [[maybe_unused]] int cap_tier = 0;
                 float bias_k = 0.f, bias0 = 0.f;  // logit bias of column c: bias_k c + bias0
                 if constexpr ((MOD & MOD_BIAS) != 0) {
                     const int d0 = kv0 - qpos;
@@ -1105,20 +1111,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 mxp[i] = fmaf(mxp[i], p.scale_log2,
                                               bias0 + fmaxf(bias_k * (float)(16 * i), bias_k * (float)(16 * i + 15)));
                         }
-                        if constexpr ((MOD & MOD_CAP) != 0) {
-                            // which tanh serves every column of the warp's rows (masked columns are dropped
-                            // whatever it makes of them, but keep the decision on the safe side)
-                            float mn[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int j = 0; j < kTcRows; j += 2)
-                                mn[(j >> 1) & 3] =
-                                    fmin3f(mn[(j >> 1) & 3], __uint_as_float(raw[j]), __uint_as_float(raw[j + 1]));
-                            const float hi = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
-                                                   fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
-                            const float size = fmaxf(hi, -fminf(fminf(mn[0], mn[1]), fminf(mn[2], mn[3]))) * p.mod.cap_in;
-                            cap_tier = __all_sync(0xffffffffu, size <= kTanhNear) ? 0
-                                                                                 : (__all_sync(0xffffffffu, size <= 1.f) ? 1 : 2);
-                        }
                     } else if (plain) {
 #pragma unroll
                         for (int j = 0; j < kTcRows; j += 2)
@@ -1139,6 +1131,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
                                  fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
+                [[maybe_unused]] const float raw_max = mx;
                 if constexpr ((MOD & MOD_CAP) != 0) {  // increasing: the max of the raw scores gives the max logit
                     mx = mx == -INFINITY ? mx : p.mod.cap_out * tanh_f32(mx * p.mod.cap_in);
                 } else if constexpr ((MOD & MOD_BIAS) == 0) {
@@ -1154,6 +1147,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     m = m_new;
                 }
                 const float m_use = (m == -INFINITY) ? 0.f : m;
+                // which form of the cap serves every row of the warp (CapPoly; a row that sees nothing takes any)
+                [[maybe_unused]] int cap_tier = 2;
+                if constexpr ((MOD & MOD_CAP) != 0) {
+                    const bool none = m == -INFINITY;
+                    if (__all_sync(0xffffffffu, none || (raw_max <= p.cap.near_max && m + p.cap.near_slack >= 30.f)))
+                        cap_tier = 0;
+                    else if (__all_sync(0xffffffffu, none || (raw_max <= p.cap.unit_max && m + p.cap.unit_slack >= 30.f)))
+                        cap_tier = 1;
+                }
                 // O must be rescaled before the first P*V of this tile: in that
                 // (rare) case both halves are signalled after the rescale
                 const bool rescale_o = warp_rescale && it > 0;
@@ -1197,28 +1199,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         else exp_pairs(logit, std::true_type{});
                     };
                     if constexpr ((MOD & MOD_CAP) != 0) {
-                        const float2 ci = both(p.mod.cap_in), cp2 = both(p.mod.cap_out);
                         if (cap_tier == 0) {
                             exp_all([&](float2 z, int) {
-                                const float2 u = __fmul2_rn(z, ci);
-                                return __ffma2_rn(__fmul2_rn(u, cp2), tanh_ratio_near(__fmul2_rn(u, u)), neg_m);
+                                const float2 w = __fmul2_rn(z, z);
+                                float2 t = __ffma2_rn(p.cap.near[4], w, p.cap.near[3]);
+                                t = __ffma2_rn(t, w, p.cap.near[2]);
+                                t = __ffma2_rn(t, w, p.cap.near[1]);
+                                t = __ffma2_rn(t, w, p.cap.near[0]);
+                                return __ffma2_rn(z, t, neg_m);
                             });
                         } else if (cap_tier == 1) {
                             exp_all([&](float2 z, int) {
-                                const float2 u = __fmul2_rn(z, ci);
-                                return __ffma2_rn(__fmul2_rn(u, cp2), tanh_ratio_unit(__fmul2_rn(u, u)), neg_m);
+                                const float2 w = __fmul2_rn(z, z);
+                                float2 t = __ffma2_rn(p.cap.unit[6], w, p.cap.unit[5]);
+                                t = __ffma2_rn(t, w, p.cap.unit[4]);
+                                t = __ffma2_rn(t, w, p.cap.unit[3]);
+                                t = __ffma2_rn(t, w, p.cap.unit[2]);
+                                t = __ffma2_rn(t, w, p.cap.unit[1]);
+                                t = __ffma2_rn(t, w, p.cap.unit[0]);
+                                return __ffma2_rn(z, t, neg_m);
                             });
                         } else {
                             exp_pairs([&](float2 z, int) {
                                 return __ffma2_rn(make_float2(tanh_f32(z.x * p.mod.cap_in), tanh_f32(z.y * p.mod.cap_in)),
-                                                  cp2, neg_m);
+                                                  both(p.mod.cap_out), neg_m);
                             }, std::true_type{});
                         }
                     } else if ((MOD & MOD_BIAS) != 0 && !general) {
                         const float2 k2 = both(bias_k), b2 = both(fmaf(bias_k, (float)(h * 64), bias0) - m_use);
-                        exp_all([&](float2 z, int c) {
-                            return __ffma2_rn(z, sc2, __ffma2_rn(make_float2((float)c, (float)(c + 1)), k2, b2));
-                        });
+                        exp_all([&](float2 z, int c) { return __ffma2_rn(z, sc2, __ffma2_rn(kColumns[c / 2], k2, b2)); });
                     } else if (plain || general) {  // every column visible, or masked logits already -inf
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
@@ -1371,8 +1380,13 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
         const int i0 = base + threadIdx.x * kDocRows;
         int id[kDocRows + 1];
         id[0] = i0 > 0 && i0 <= n ? __ldg(ids + i0 - 1) : 0;
+        if (i0 + kDocRows <= n && (reinterpret_cast<uintptr_t>(ids) & 15) == 0) {
+            const int4 a = __ldg(reinterpret_cast<const int4*>(ids + i0)), b = __ldg(reinterpret_cast<const int4*>(ids + i0) + 1);
+            id[1] = a.x; id[2] = a.y; id[3] = a.z; id[4] = a.w; id[5] = b.x; id[6] = b.y; id[7] = b.z; id[8] = b.w;
+        } else {
 #pragma unroll
-        for (int k = 0; k < kDocRows; ++k) id[k + 1] = i0 + k < n ? __ldg(ids + i0 + k) : 0;
+            for (int k = 0; k < kDocRows; ++k) id[k + 1] = i0 + k < n ? __ldg(ids + i0 + k) : 0;
+        }
         unsigned first = 0;
 #pragma unroll
         for (int k = 0; k < kDocRows; ++k)
@@ -1386,12 +1400,8 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
         }
         if (lane == 31) warp_sums[w] = x;
         __syncthreads();
-        int before = 0, total = 0;
-        for (int k = 0; k < 32; ++k) {
-            const int t = warp_sums[k];
-            before += k < w ? t : 0;
-            total += t;
-        }
+        const int mine = warp_sums[lane];
+        const int before = __reduce_add_sync(0xffffffffu, lane < w ? mine : 0), total = __reduce_add_sync(0xffffffffu, mine);
         int run = carry + before + x - c - 1;
 #pragma unroll
         for (int k = 0; k < kDocRows; ++k)
@@ -1425,12 +1435,18 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
     };
     for (int e = threadIdx.x; e < entries; e += blockDim.x) atomicAdd(&hist[cost(e)], 1);
     __syncthreads();
-    if (threadIdx.x == 0) {  // bucket starts, highest cost first
+    if (w == 0) {  // bucket starts, highest cost first
         int run = 0;
-        for (int b = nbins; b >= 0; --b) {
-            const int c = hist[b];
-            hist[b] = run;
-            run += c;
+        for (int b0 = nbins; b0 >= 0; b0 -= 32) {
+            const int b = b0 - lane, c = b >= 0 ? hist[b] : 0;
+            int x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b >= 0) hist[b] = run + x - c;
+            run += __shfl_sync(0xffffffffu, x, 31);
         }
     }
     __syncthreads();
@@ -1456,10 +1472,38 @@ static fa_status launch_tc_d(int d, const CUtensorMap& tq, const CUtensorMap& tk
                     : launch_tc<64, MODE, MOD>(tq, tk, tv, p, grid, s, sc);
 }
 
+static CapPoly cap_poly(const ScoreMod& m) {
+    CapPoly c{};
+    const double in = m.cap_in, out = m.cap_out;
+    const double near[5] = {kTanhD0, kTanhD1, kTanhD2, kTanhD3, kTanhD4};
+    const double unit[7] = {kTanhC0, kTanhC1, kTanhC2, kTanhC3, kTanhC4, kTanhC5, kTanhC6};
+    // the last coefficients may be subnormal: 1e-41 still carries 13 bits, more
+    // than the 1e-3 that they add to the result needs
+    auto fits = [](float x) { return std::fabs(x) > 1e-41f && std::fabs(x) < 1e30f; };
+    bool near_fits = true, unit_fits = true;
+    double f = out * in;
+    for (int k = 0; k < 7; ++k, f *= in * in) {
+        const float u = (float)(unit[k] * f);
+        c.unit[k] = make_float2(u, u);
+        unit_fits &= fits(u);
+        if (k < 5) {
+            const float n = (float)(near[k] * f);
+            c.near[k] = make_float2(n, n);
+            near_fits &= fits(n);
+        }
+    }
+    c.near_max = (float)(kTanhNear / in);
+    c.unit_max = (float)(1.0 / in);
+    c.near_slack = near_fits ? (float)(out * std::tanh(0.6)) : -INFINITY;
+    c.unit_slack = unit_fits ? (float)(out * std::tanh(1.0)) : -INFINITY;
+    return c;
+}
+
 // The variant that a call's score modifiers ask for (p.mod is set).
 template <int MODE>
-static fa_status launch_tc_mod(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const TcParams& p, int grid, cudaStream_t s, const TcSched* sched = nullptr) {
+static fa_status launch_tc_mod(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, TcParams& p,
+                               int grid, cudaStream_t s, const TcSched* sched = nullptr) {
+    if (p.mod.cap_out > 0.f) p.cap = cap_poly(p.mod);
     if (p.mod.slopes) return launch_tc_d<MODE, MOD_RANGE | MOD_BIAS>(d, tq, tk, tv, p, grid, s, sched);
     if (p.mod.cap_out > 0.f) return launch_tc_d<MODE, MOD_RANGE | MOD_CAP>(d, tq, tk, tv, p, grid, s, sched);
     return launch_tc_d<MODE, MOD_RANGE>(d, tq, tk, tv, p, grid, s, sched);

@@ -169,8 +169,8 @@ template <bool kF32, int D>
 __global__ void __launch_bounds__(256) mrope_append_kernel(const void* __restrict__ q, const void* __restrict__ k,
                                                            const void* __restrict__ v,
                                                            const int32_t* __restrict__ positions, int n_axes,
-                                                           const PairAxes axes, const float* __restrict__ cos_sin,
-                                                           int max_pos, uint16_t* __restrict__ q_out,
+                                                           const __grid_constant__ PairAxes axes,
+                                                           const float* __restrict__ cos_sin, int max_pos, uint16_t* __restrict__ q_out,
                                                            uint16_t* __restrict__ kc, uint16_t* __restrict__ vc,
                                                            const int32_t* __restrict__ slots, int N, int Hq, int Hkv,
                                                            int tokens, int num_blocks, DevCtx ctx) {

@@ -285,11 +285,6 @@ __device__ __forceinline__ float fmax3f(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float fmin3f(float a, float b, float c) {
-    float d;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
 // m16n8k16 warp MMA, f16 inputs, fp32 accumulation (D += A B).
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -318,27 +313,13 @@ __device__ __forceinline__ float tanh_f32(float u) {
     return a <= 1.f ? u * t : big;
 }
 
-// tanh(u) / u for a pair with |u| <= kTanhNear (w = u^2): a degree-4 minimax
-// polynomial of the same kind (relative error 1.8e-7 as evaluated), in packed operations.
+// tanh on |u| <= kTanhNear: u times a degree-4 polynomial in u^2 of the same kind
+// (relative error 1.8e-7 as evaluated).  Both polynomials go on rising past
+// the end of their range, so a score below it only gets a still lower logit.
 constexpr float kTanhNear = 0.6f;
 constexpr float kTanhD0 = 0.99999994f, kTanhD1 = -0.3333231f, kTanhD2 = 0.13310173f, kTanhD3 = -0.05210147f,
                 kTanhD4 = 0.015475417f;
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 tanh_ratio_near(float2 w) {
-    float2 t = __ffma2_rn(both(kTanhD4), w, both(kTanhD3));
-    t = __ffma2_rn(t, w, both(kTanhD2));
-    t = __ffma2_rn(t, w, both(kTanhD1));
-    return __ffma2_rn(t, w, both(kTanhD0));
-}
-// The same for |u| <= 1.
-__device__ __forceinline__ float2 tanh_ratio_unit(float2 w) {
-    float2 t = __ffma2_rn(both(kTanhC6), w, both(kTanhC5));
-    t = __ffma2_rn(t, w, both(kTanhC4));
-    t = __ffma2_rn(t, w, both(kTanhC3));
-    t = __ffma2_rn(t, w, both(kTanhC2));
-    t = __ffma2_rn(t, w, both(kTanhC1));
-    return __ffma2_rn(t, w, both(kTanhC0));
-}
 
 // ------------------------------------------------------- score modifiers ---
 // Logit of query position i and key position j for dot product s, in log2
@@ -355,6 +336,18 @@ struct ScoreMod {
     float* lse;             // fp32 log-sum-exp per row ([rows, Hq] paged), or null
     float* logits;          // decode rows: logits kept for the weight sums (log2 units), or null
     int logit_rows;         // rows a page's logits take in that buffer
+};
+
+// The capped logit as a polynomial of the raw dot product s, in pairs of equal
+// coefficients: c log2(e) tanh(s scale / c) = s (a_0 + a_1 s^2 + ...) while the
+// row's largest s scale / c is at most kTanhNear (near) or 1 (unit).  A score
+// below minus that bound gets a wrong logit, which is harmless when its weight
+// is below 2^-30 of the row's: `slack` plus the row's running max (log2 units)
+// has to reach 30.  slack is -inf when a coefficient leaves fp32's range.
+struct CapPoly {
+    float2 near[5], unit[7];
+    float near_max, unit_max;      // largest s
+    float near_slack, unit_slack;  // c log2(e) tanh(0.6), c log2(e) tanh(1)
 };
 
 // Four E4M3 bytes (byte i = element i) to two f16x2 words: lo = elements

@@ -4,11 +4,16 @@
 // are kept, `keep` in all, and copied in order of position from the blocks of
 // one table to those of another.
 //
-// evict_select_kernel (one CTA per sequence and kv head) finds the weight of
-// the last token kept with a radix select over order-preserving integer keys
-// (three passes of 11, 11 and 10 bits), then lists the kept tokens with one
-// scan; evict_move_kernel gathers their rows.  Memory bound: the weights are read
-// once from HBM (the passes after the first hit L2), each kept row once.
+// evict_select_kernel finds the weight of the last token kept with a radix
+// select over order-preserving integer keys (three passes of 11, 11 and 10
+// bits), then lists the kept tokens with one scan.  A sequence and kv head is one
+// CTA, or a cluster of up to eight when its row is long: each CTA histograms
+// its part (kept in registers when it has at most 8192 tokens), the parts are
+// added through distributed shared memory, and every CTA takes the same
+// decision.  evict_move_kernel gathers the kept rows.  Memory bound: the weights
+// are read once, each kept row once.
+#include <algorithm>
+
 #include "host_common.cuh"
 
 namespace fa {
@@ -25,62 +30,127 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The int at p (an address of this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ int cluster_load(const int* p, unsigned rank) {
+    uint32_t a;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+constexpr int kEvPass = kEvThreads * kEvItems;  // tokens of a scan pass
 __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* acc, int acc_len,
                                                                   const int32_t* __restrict__ ctx_lens, float* acc_out,
                                                                   int out_len, int32_t* __restrict__ list,
                                                                   int32_t* __restrict__ new_lens, int Hkv, int mbps,
                                                                   int dst_mbps, int keep, int recent, int sink,
                                                                   DevCtx ctx) {
-    __shared__ int hist[kEvBins];
+    __shared__ int hist[2][kEvBins];  // by turns, so that one cluster barrier per pass is enough
     __shared__ int2 warp_sums[32];
-    __shared__ int sel_digit, sel_above;
-    const int s = blockIdx.x / Hkv, h = blockIdx.x % Hkv, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    __shared__ int sel_digit, sel_above, totals[2];
+    // the rows' copy may be scheduled; it waits for this grid's end before it reads the list
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int CL = (int)cluster_size(), rank = (int)cluster_rank();
+    const int sh = blockIdx.x / CL, s = sh / Hkv, h = sh % Hkv;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int cl = __ldg(ctx_lens + s);
-    int32_t* out = list + (long)blockIdx.x * keep;
+    int32_t* out = list + (long)sh * keep;
     const int n = min(cl, keep);
-    if (cl < 0 || cl > mbps * kEvBlock || cl > acc_len || n > dst_mbps * kEvBlock) {
-        if (tid == 0) raise_error(ctx, ERR_BOUNDS_BIT);
-        for (int i = tid; i < keep; i += kEvThreads) out[i] = -1;
-        if (h == 0 && tid == 0) new_lens[s] = 0;
+    const bool first = h == 0 && rank == 0 && tid == 0;
+    const int gtid = rank * kEvThreads + tid, gthreads = CL * kEvThreads;
+    if (cl < 0 || cl > mbps * kEvBlock || cl > acc_len || n > dst_mbps * kEvBlock) {  // the same for the whole cluster
+        if (rank == 0 && tid == 0) raise_error(ctx, ERR_BOUNDS_BIT);
+        for (int i = gtid; i < keep; i += gthreads) out[i] = -1;
+        if (first) new_lens[s] = 0;
         return;
     }
-    if (h == 0 && tid == 0) new_lens[s] = n;
-    for (int i = n + tid; i < keep; i += kEvThreads) out[i] = -1;
-    const float* a = acc + (long)blockIdx.x * acc_len;
-    float* ao = acc_out ? acc_out + (long)blockIdx.x * out_len : nullptr;
+    if (first) new_lens[s] = n;
+    for (int i = n + gtid; i < keep; i += gthreads) out[i] = -1;
+    const float* a = acc + (long)sh * acc_len;
+    float* ao = acc_out ? acc_out + (long)sh * out_len : nullptr;
     if (cl <= keep) {
-        for (int i = tid; i < cl; i += kEvThreads) {
+        for (int i = gtid; i < cl; i += gthreads) {
             out[i] = i;
             if (ao) ao[i] = a[i];
         }
         return;
     }
+    // this CTA's tokens [p0, p1), a multiple of the scan's items except at the end
+    const int part = ((cl + CL - 1) / CL + kEvItems - 1) / kEvItems * kEvItems;
+    const int p0 = min(cl, rank * part), p1 = min(cl, p0 + part);
+    const bool vec = (acc_len & 3) == 0 && (reinterpret_cast<uintptr_t>(acc) & 15) == 0;
+    float v[kEvItems];
+    auto load = [&](int t0) {
+        if (vec && t0 + kEvItems <= p1) {
+            const float4 x = *reinterpret_cast<const float4*>(a + t0), y = *reinterpret_cast<const float4*>(a + t0 + 4);
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEvItems; ++k) v[k] = t0 + k < p1 ? a[t0 + k] : 0.f;
+        }
+    };
+    const bool once = p1 - p0 <= kEvPass;  // the part stays in registers
+    load(p0 + tid * kEvItems);
     // the `want` largest keys of the tokens [sink, mid_end)
     const int mid_end = cl - recent;
-    int want = keep - sink - recent;
+    const int want = keep - sink - recent;
     uint32_t prefix = 0;  // digits fixed so far
     int need = want;      // tokens still to take among those that match the prefix
+    for (int i = tid; i < kEvBins; i += kEvThreads) hist[0][i] = 0;
+    __syncthreads();
     for (int pass = 0; pass < 3 && want > 0; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-        for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
-        __syncthreads();
-        for (int t0 = sink + wid * 32; t0 < mid_end; t0 += kEvThreads) {
-            const int t = t0 + lane;
-            const uint32_t key = t < mid_end ? weight_key(a[t]) : 0u;
-            const bool in = t < mid_end && (pass == 0 || (key >> (shift + bits)) == (prefix >> (shift + bits)));
-            const uint32_t digit = in ? (key >> shift) & ((1u << bits) - 1) : 0xffffffffu;
-            int same;
-            __match_all_sync(0xffffffffu, digit, &same);
-            if (same) {  // many tokens may hold the same weight (0): one add for the warp
-                if (in && lane == 0) atomicAdd(&hist[digit], 32);
-            } else if (in) {
-                atomicAdd(&hist[digit], 1);
+        int* hs = hist[pass & 1];
+        for (int base = p0; base < p1; base += kEvPass) {
+            const int t0 = base + tid * kEvItems;
+            if (!once) load(t0);
+#pragma unroll
+            for (int k = 0; k < kEvItems; ++k) {
+                const int t = t0 + k;
+                const uint32_t key = weight_key(v[k]);
+                const bool in = t < p1 && t >= sink && t < mid_end &&
+                                (pass == 0 || (key >> (shift + bits)) == (prefix >> (shift + bits)));
+                const uint32_t digit = in ? (key >> shift) & ((1u << bits) - 1) : 0xffffffffu;
+                int same;
+                __match_all_sync(0xffffffffu, digit, &same);
+                if (same) {  // many tokens may hold the same weight (0): one add for the warp
+                    if (in && lane == 0) atomicAdd(&hs[digit], 32);
+                } else if (in) {
+                    atomicAdd(&hs[digit], 1);
+                }
             }
         }
-        __syncthreads();
+        if (CL > 1) cluster_sync_all();
+        else __syncthreads();
         // the digit where the count from the top reaches `need`: each thread owns two bins
         const int b1 = kEvBins - 1 - 2 * tid, b0 = b1 - 1;  // highest bins first
-        const int c1 = hist[b1], c0 = hist[b0];
+        int c1 = 0, c0 = 0;
+        if (CL > 1) {
+            for (int r = 0; r < CL; ++r) {
+                c1 += cluster_load(hs + b1, r);
+                c0 += cluster_load(hs + b0, r);
+            }
+        } else {
+            c1 = hs[b1];
+            c0 = hs[b0];
+        }
+        // the other buffer: every CTA read its counts of the pass before ahead of this pass's barrier
+        hist[(pass + 1) & 1][b1] = 0;
+        hist[(pass + 1) & 1][b0] = 0;
         int x = c0 + c1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -89,8 +159,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
         }
         if (lane == 31) warp_sums[wid].x = x;
         __syncthreads();
-        int before = 0;
-        for (int k = 0; k < wid; ++k) before += warp_sums[k].x;
+        const int before = __reduce_add_sync(0xffffffffu, lane < wid ? warp_sums[lane].x : 0);
         const int above = before + x - c0 - c1;  // keys in higher bins than b1
         if (above < need && above + c1 >= need) {
             sel_digit = b1;
@@ -102,25 +171,48 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
         __syncthreads();
         prefix |= (uint32_t)sel_digit << shift;
         need -= sel_above;
-        __syncthreads();
+        // (sel_* is written again only behind the next pass's barriers)
     }
     // tokens above the threshold key, the forced ones, and the first `need` equal to it
-    int kept_before = 0, eq_before = 0;
-    for (int base = 0; base < cl; base += kEvThreads * kEvItems) {
-        const int t0 = base + tid * kEvItems;
-        float v[kEvItems];
-        unsigned sure = 0, eq = 0;
+    auto classify = [&](int t0, unsigned& sure, unsigned& eq) {
+        sure = eq = 0;
 #pragma unroll
         for (int k = 0; k < kEvItems; ++k) {
             const int t = t0 + k;
-            v[k] = t < cl ? a[t] : 0.f;
-            if (t >= cl) continue;
+            if (t >= p1) continue;
             const uint32_t key = weight_key(v[k]);
             if (t < sink || t >= mid_end || (want > 0 && key > prefix))
                 sure |= 1u << k;
             else if (want > 0 && key == prefix)
                 eq |= 1u << k;
         }
+    };
+    int kept_before = 0, eq_before = 0;
+    if (CL > 1) {  // what the CTAs before this one hold
+        if (tid < 2) totals[tid] = 0;
+        __syncthreads();
+        for (int base = p0; base < p1; base += kEvPass) {
+            unsigned sure, eq;
+            if (!once) load(base + tid * kEvItems);
+            classify(base + tid * kEvItems, sure, eq);
+            const int ns = __reduce_add_sync(0xffffffffu, __popc(sure)), ne = __reduce_add_sync(0xffffffffu, __popc(eq));
+            if (lane == 0) {
+                atomicAdd(&totals[0], ns);
+                atomicAdd(&totals[1], ne);
+            }
+        }
+        cluster_sync_all();
+        for (int r = 0; r < rank; ++r) {
+            kept_before += cluster_load(&totals[0], r);
+            eq_before += cluster_load(&totals[1], r);
+        }
+        cluster_sync_all();  // no CTA leaves while another still reads its totals
+    }
+    for (int base = p0; base < p1; base += kEvPass) {
+        const int t0 = base + tid * kEvItems;
+        if (!once) load(t0);
+        unsigned sure, eq;
+        classify(t0, sure, eq);
         int2 x = make_int2(__popc(sure), __popc(eq));
         const int2 own = x;
 #pragma unroll
@@ -131,20 +223,15 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
                 x.y += y1;
             }
         }
+        __syncthreads();  // warp_sums of the pass before is read
         if (lane == 31) warp_sums[wid] = x;
         __syncthreads();
-        int2 pre = make_int2(0, 0), tot = make_int2(0, 0);
-        for (int k = 0; k < 32; ++k) {
-            const int2 t = warp_sums[k];
-            if (k < wid) {
-                pre.x += t.x;
-                pre.y += t.y;
-            }
-            tot.x += t.x;
-            tot.y += t.y;
-        }
-        int ns = kept_before + pre.x + x.x - own.x, ne = eq_before + pre.y + x.y - own.y;
-        // (every weight of this pass is read: acc_out may be acc itself, no write lands on a later token)
+        const int2 ws = warp_sums[lane];
+        int ns = kept_before + x.x - own.x + __reduce_add_sync(0xffffffffu, lane < wid ? ws.x : 0);
+        int ne = eq_before + x.y - own.y + __reduce_add_sync(0xffffffffu, lane < wid ? ws.y : 0);
+        kept_before += __reduce_add_sync(0xffffffffu, ws.x);
+        eq_before += __reduce_add_sync(0xffffffffu, ws.y);
+        // (every weight of this pass is in registers: acc_out may be acc itself, no write lands on a later token)
 #pragma unroll
         for (int k = 0; k < kEvItems; ++k) {
             const bool is_eq = (eq >> k) & 1u;
@@ -157,9 +244,6 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
             ns += (sure >> k) & 1u;
             ne += is_eq ? 1 : 0;
         }
-        kept_before += tot.x;
-        eq_before += tot.y;
-        __syncthreads();
     }
 }
 
@@ -171,6 +255,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(uint16_t* kc, uint16_t*
                                                          const int32_t* __restrict__ dst,
                                                          const int32_t* __restrict__ list, int num_seqs, int Hkv, int d,
                                                          int mbps, int dst_mbps, int keep, int num_blocks, DevCtx ctx) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is complete
     const int cpr = d >> 3;             // chunks per row
     const int lanes = 2 * cpr;          // threads per row pair (K and V)
     const int rows_cta = 256 / lanes;   // rows side by side
@@ -188,7 +273,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(uint16_t* kc, uint16_t*
         for (int k = 0; k < kEvRows; ++k) {
             const int i = i0 + k * rows_cta;
             to[k] = -1;
-            const int t = i < keep ? __ldg(list + sh * keep + i) : -1;
+            const int t = i < keep ? __ldcg(list + sh * keep + i) : -1;
             if (t < 0) continue;
             const int sb = __ldg(src + (long)s * mbps + t / kEvBlock);
             const int db = __ldg(dst + (long)s * dst_mbps + i / kEvBlock);
@@ -226,7 +311,7 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
         recent < 0 || sink < 0 || recent > keep || sink > keep - recent || acc_len < 0 || acc_out_len < 0)
         return FA_ERR_INVALID_ARG;
     if (block_size != kEvBlock || (d != 64 && d != 128)) return FA_ERR_UNSUPPORTED;
-    if ((long)num_seqs * Hkv >= 1L << 31) return FA_ERR_UNSUPPORTED;
+    if ((long)num_seqs * Hkv >= 1L << 27) return FA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return FA_OK;
     if (!k_cache || !v_cache || !acc || !block_table || !ctx_lens || !dst_table || !new_lens)
         return FA_ERR_INVALID_ARG;
@@ -246,17 +331,37 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
     DevCtx ctx;
     if ((st = make_ctx(&ctx)) != FA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    evict_select_kernel<<<num_seqs * Hkv, kEvThreads, 0, s>>>(acc, acc_len, ctx_lens, acc_out, acc_out_len, list,
-                                                              new_lens, Hkv, max_blocks_per_seq, dst_blocks_per_seq,
-                                                              keep, recent, sink, ctx);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    // CTAs per sequence and head: as many as leave each 2048 tokens, while they
+    // all fit the GPU at once; one when the weights move inside rows too long
+    // for the registers of a cluster (a CTA must not overwrite what another has
+    // yet to read)
+    const long rows = (long)num_seqs * Hkv, longest = std::min<long>((long)max_blocks_per_seq * kEvBlock, acc_len);
+    int cluster = 1;
+    while (cluster < 8 && longest > 2048L * cluster && rows * cluster * 2 <= 2L * sm_count()) cluster *= 2;
+    if (acc_out == acc && longest > (long)cluster * (kEvPass - kEvItems)) cluster = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * cluster));
+    cfg.blockDim = dim3(kEvThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, acc, acc_len, ctx_lens, acc_out, acc_out_len, list, new_lens, Hkv,
+                           max_blocks_per_seq, dst_blocks_per_seq, keep, recent, sink, ctx) != cudaSuccess)
+        return FA_ERR_CUDA;
     const int rows_item = 256 / (2 * (d / 8)) * kEvRows;
-    const long items = (long)num_seqs * Hkv * ((keep + rows_item - 1) / rows_item);
-    const long cap = (long)sm_count() * 8;
-    evict_move_kernel<<<(int)(items < cap ? items : cap), 256, 0, s>>>(
-        static_cast<uint16_t*>(k_cache), static_cast<uint16_t*>(v_cache), block_table, dst_table, list, num_seqs, Hkv, d,
-        max_blocks_per_seq, dst_blocks_per_seq, keep, num_blocks, ctx);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    const long items = rows * ((keep + rows_item - 1) / rows_item);
+    cfg.gridDim = dim3((unsigned)std::min<long>(items, 1L << 30));
+    cfg.blockDim = dim3(256);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (cudaLaunchKernelEx(&cfg, evict_move_kernel, static_cast<uint16_t*>(k_cache), static_cast<uint16_t*>(v_cache),
+                           block_table, dst_table, static_cast<const int32_t*>(list), num_seqs, Hkv, d,
+                           max_blocks_per_seq, dst_blocks_per_seq, keep, num_blocks, ctx) != cudaSuccess)
+        return FA_ERR_CUDA;
     set_launch_count(2);
     return FA_OK;
 }

@@ -794,6 +794,8 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
                                                                     const float* part_o, const float2* part_ml,
                                                                     uint16_t* __restrict__ out, int num_seqs,
                                                                     int Hq, int Hkv, int mbps, int W, ScoreMod mod) {
+    // (the weight sums that may follow wait for this grid's end before they read)
+    if constexpr (MOD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int window = MOD ? mod.window : 0;
     // one warp per output row: warp w of CTA (s, hk) merges row w
     const int s = blockIdx.x, hk = blockIdx.y, r = threadIdx.x >> 5, g = Hq / Hkv;
@@ -967,23 +969,25 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
 // final log-sum-exp: sequences that took the decode kernel, and those without
 // queries.  Memory bound: rows * 4 bytes a key read, 8 bytes of sums.  The sum
 // over rows runs in a fixed order.  CTA (s, hk, split): pages
-// [kAccumPages split, + kAccumPages) of the context, a half-warp per page.
-constexpr int kAccumPages = 64;  // pages per CTA
+// [kAccumPages split, + kAccumPages) of the context, a half-warp per page.  The
+// programmatic launch lets the CTAs find their places while the attention's
+// last kernel runs.
+constexpr int kAccumPages = 16;  // pages per CTA
 __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __restrict__ ctx_lens,
                                                            const int32_t* __restrict__ q_lens,
-                                                           const float* __restrict__ lse,
-                                                           const float* __restrict__ logits, int logit_rows,
+                                                           const float* lse, const float* logits, int logit_rows,
                                                            const float* acc_in, float* acc_out, int acc_len,
                                                            float decay, int num_seqs, int mbps, int Hq, int Hkv,
                                                            int window, DevCtx ctx) {
     const int s = blockIdx.x, hk = blockIdx.y, g = Hq / Hkv, lane = threadIdx.x & 31;
     const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s);
-    if (ql > cl || ql < 0 || cl > mbps * kBS || (ql > 0 && !is_decode_row(ql, g))) return;
     const int p0 = blockIdx.z * kAccumPages;
     const int npages = (cl + kBS - 1) / kBS;
-    if (p0 >= npages) return;
-    if (cl > acc_len) {
-        if (threadIdx.x == 0) raise_error(ctx, ERR_BOUNDS_BIT);
+    const bool mine = ql <= cl && ql >= 0 && cl <= mbps * kBS && (ql == 0 || is_decode_row(ql, g)) && p0 < npages;
+    if (!mine || cl > acc_len) {
+        if (mine && threadIdx.x == 0) raise_error(ctx, ERR_BOUNDS_BIT);
+        // every CTA waits for the grid before, so this one never completes ahead of it
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     __shared__ float neg_lse2[kDecodeRows];
@@ -1002,28 +1006,35 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
         }
     }
     const int nrows = ql > 0 ? min(g * ql, logit_rows) : 0;
-    if (threadIdx.x < nrows) {
-        const int r = threadIdx.x;
-        const float L = lse[(q0 + r / g) * Hq + hk * g + r % g];
-        neg_lse2[r] = L == -INFINITY ? 0.f : -L * kLog2ef;
-    }
-    __syncthreads();
     const int blk0 = ql > 0 ? first_block(cl, ql, window) : 0;
     const long long seg = pre * Hkv + (long long)hk * (npages - blk0);  // the segment's first page of the stream
     const long row = ((long)s * Hkv + hk) * acc_len;
-    const int i = threadIdx.x & 15;
-    for (int p = p0 + (threadIdx.x >> 4); p < min(npages, p0 + kAccumPages); p += 16) {
-        const int t = p * kBS + i;
-        if (t >= cl) continue;
-        float a = acc_in && t < cl - ql ? decay * acc_in[row + t] : 0.f;
-        if (p >= blk0) {
-            const float* x = logits + (seg + p - blk0) * logit_rows * kBS + i;
-            float w = 0.f;
-            for (int r = 0; r < nrows; ++r) w += fast_exp2(__ldg(x + r * kBS) + neg_lse2[r]);
-            a += w;
-        }
-        acc_out[row + t] = a;
+    const int i = threadIdx.x & 15, p = p0 + (threadIdx.x >> 4), t = p * kBS + i;
+    const bool live = p < npages && t < cl;
+    // inputs only so far; acc_in may be what the call before this one wrote
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float x[kDecodeRows];  // this token's logits: all loads in flight with the statistics'
+    if (live && p >= blk0) {
+        const float* src = logits + (seg + p - blk0) * logit_rows * kBS + i;
+#pragma unroll
+        for (int r = 0; r < kDecodeRows; ++r) x[r] = r < nrows ? __ldcg(src + r * kBS) : -INFINITY;
     }
+    float a = live && acc_in && t < cl - ql ? decay * acc_in[row + t] : 0.f;
+    if (threadIdx.x < nrows) {
+        const int r = threadIdx.x;
+        const float L = __ldcg(lse + (q0 + r / g) * Hq + hk * g + r % g);
+        neg_lse2[r] = L == -INFINITY ? 0.f : -L * kLog2ef;
+    }
+    __syncthreads();
+    if (!live) return;
+    if (p >= blk0) {
+        float w = 0.f;
+#pragma unroll
+        for (int r = 0; r < kDecodeRows; ++r)
+            if (r < nrows) w += fast_exp2(x[r] + neg_lse2[r]);
+        a += w;
+    }
+    acc_out[row + t] = a;
 }
 
 // ------------------------------------------------------------ metadata -----
@@ -1331,10 +1342,19 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         // rows whose queries took the decode kernel (and sequences without
         // queries), then the chunks: each sequence is one or the other
         const dim3 grid(num_seqs, Hkv, (max_blocks_per_seq + kAccumPages - 1) / kAccumPages);
-        accum_decode_kernel<<<grid, 256, 0, s>>>(ctx_lens, q_lens, mod->lse, mod->logits, mod->logit_rows, acc->in,
-                                                 acc->out, acc->len, acc->decay, num_seqs, max_blocks_per_seq, Hq, Hkv,
-                                                 mod->window, ctx);
-        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kAccumPages * kBS);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, accum_decode_kernel, ctx_lens, q_lens, static_cast<const float*>(mod->lse),
+                               static_cast<const float*>(mod->logits), mod->logit_rows, acc->in, acc->out, acc->len,
+                               acc->decay, num_seqs, max_blocks_per_seq, Hq, Hkv, mod->window, ctx) != cudaSuccess)
+            return FA_ERR_CUDA;
         ++launches;
         if (tc_path) {
             st = launch_accum_chunk(q, k_cache, block_table, ctx_lens, q_lens,

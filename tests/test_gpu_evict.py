@@ -183,6 +183,14 @@ def test_evict_long_row(F):
     run_evict(F, [20000], 1, 64, 9000, 10, 1, values="ties")
 
 
+@pytest.mark.parametrize("ctx, keep", [([20000], 9000), ([5000, 9000, 2100], 600), ([70000], 3000)], ids=str)
+@pytest.mark.parametrize("values", ["spread", "odd", "equal"])
+def test_evict_rows_shared_by_ctas(F, ctx, keep, values):
+    """Few long rows: several CTAs share a row, whose part fits their registers or not."""
+    run_evict(F, ctx, 1, 64, keep, 40, 3, values=values)
+    run_evict(F, ctx, 1, 64, keep, 0, 0, values=values, inplace=True)
+
+
 def test_evict_reports_bad_lengths_and_blocks(F):
     S, Hkv, d = 3, 1, 64
     kc, vc = (torch.randn(12, Hkv, 16, d).bfloat16().cuda() for _ in range(2))
