@@ -6,14 +6,21 @@
 //
 // The transposed product S^T = K Q^T puts a key in each TMEM lane and the query
 // rows in the columns, so the sum over queries is a sum along a thread's own
-// columns: no shuffles, no atomics, a fixed order.  A CTA owns 128 keys of one
-// (sequence, kv head): its K tile stays in shared memory while the group's
-// query tiles pass through a ring of two stages, each answered by one
-// 128x128xd product into one of two TMEM buffers; warpgroup w sums the tiles of
-// parity w while the tensor core fills the other buffer.  Two CTAs share an SM
-// (96 KB of tiles and half of the TMEM each), so one's set-up hides behind the
-// other's work.  Per logit the sum costs one multiply-add, one exponential and
-// one add, against two passes over the scores in the attention itself.
+// columns: no shuffles, no atomics, a fixed order.  Persistent CTAs (576 threads,
+// one per SM) take units of 256 keys of one (sequence, kv head) from a ticket
+// counter, chunks with many query tiles first.  A unit's two K tiles stay in
+// shared memory while the query tiles that see it pass through a ring of two
+// pairs; each pair (256 query rows), loaded once, meets both K tiles in two
+// 128x256xd products.  Warps:
+//   0-15  four summing warpgroups: warpgroup w = 2 kt + side owns TMEM columns
+//         [128 w, 128 w + 128) and sums the products of K tile kt with query
+//         tile `side` of every pair, while the tensor core works for the other K
+//         tile; side 1 hands its sums to side 0 at the end of a unit;
+//   16    TMA producer and ticket taker;  17  MMA issuer and TMEM owner.
+// Per logit the sum costs half a packed multiply-add, an exponential and half a
+// packed add, against two passes over the scores in the attention itself.  The
+// pace is the MMA warp's: 256 query rows per product, because eight MMAs of 128
+// columns took 950 cycles to issue and each commit and barrier check 100 to 200.
 #include <cmath>
 #include <type_traits>
 
@@ -21,10 +28,11 @@
 
 namespace fa {
 
-constexpr int kCsThreads = 320;  // two summing warpgroups, the TMA producer, the MMA issuer
-constexpr int kCsProducer = 8, kCsMma = 9;
-constexpr int kCsRows = 128;  // keys of a CTA, and query rows of a tile
-constexpr int kCsStages = 2;
+constexpr int kCsThreads = 576;
+constexpr int kCsProducer = 16, kCsMma = 17;
+constexpr int kCsReaders = 17;  // of a unit's mailbox: the summing warps and the MMA warp
+constexpr int kCsRows = 128;    // keys of a K tile, and query rows of a tile
+constexpr int kCsPairs = 2, kCsUnitSlots = 4;  // query pairs in flight, unit mailboxes
 constexpr float kCsLog2e = 1.4426950408889634f;
 enum { CS_PLAIN = 0, CS_CAP = 1, CS_BIAS = 2 };  // CS_BIAS also caps when asked
 
@@ -33,12 +41,15 @@ struct ColsumParams {
     const int32_t* ctx_lens;
     const int32_t* q_lens;
     const int32_t* q_start;
+    const int32_t* k_start;  // [rank] first unit row (256 keys each) of the sequence k_seq[rank], then their number
+    const int32_t* k_seq;    // sequences by decreasing number of query tiles
+    int32_t* tickets;
     const float* lse;
     const float* acc_in;
     float* acc_out;
     int acc_len;
     float decay;
-    int Hq, Hkv, g, pack, pack_shift, mbps, num_blocks, causal;
+    int num_seqs, Hq, Hkv, g, pack, pack_shift, mbps, num_blocks, causal;
     float scale_log2;
     ScoreMod mod;
     DevCtx ctx;
@@ -50,11 +61,13 @@ struct CsCfg {
     static constexpr int kAtomBytes = kCsRows * 128;
     static constexpr int kTileBytes = kAtoms * kAtomBytes;
     static constexpr uint32_t kGroup = kAtoms * 1024;  // 8-row groups of the K tile (halves side by side)
-    static constexpr int kBars = 1 + 2 * kCsStages + 4 + 2;
-    // per summing warp and column: -lse, distance slope, run of keys seen (each warp keeps its own, so no barrier across
-    // warps is needed in the loop)
-    static constexpr int kColBytes = 8 * 3 * kCsRows * 4;
-    static constexpr int kSmem = 1024 + (1 + kCsStages) * kTileBytes + kColBytes + kCsRows * 4 + kBars * 8 + 16;
+    static constexpr int kBars = 3 + 2 * kCsPairs + 4 + 4 + 2 * kCsUnitSlots + 2;
+    // per summing warp and column: -lse, distance slope, run of keys seen (each
+    // warp keeps its own, so no barrier across warps is needed in the loop)
+    static constexpr int kColBytes = 16 * 3 * kCsRows * 4;
+    static constexpr int kPartBytes = 2 * kCsRows * 4;
+    static constexpr int kSmem = 1024 + (2 + 2 * kCsPairs) * kTileBytes + kColBytes + kPartBytes + kBars * 8 +
+                                 kCsUnitSlots * 16 + 16;
 };
 
 // Keys [lo, hi) that a query at `pos` sees.
@@ -68,48 +81,82 @@ __device__ __forceinline__ int2 cs_range(const ColsumParams& p, int pos, int pre
     return make_int2(lo, min(hi, cl));
 }
 
+// A unit as every role sees it: 256 keys from kv0 of (seq, hk), and the query
+// tiles that see one of them.
+struct CsUnit {
+    int seq, hk, kv0, ql, cl, qs, pos0, prefix;
+    int t_lo, n;   // first query tile, number of query tiles (times the heads when not packed)
+    int nk;        // K tiles with keys: 1 or 2
+};
+
+__device__ __forceinline__ CsUnit cs_unit(const ColsumParams& p, int seq, int hk, int y, int tt, int heads) {
+    CsUnit U;
+    U.seq = seq;
+    U.hk = hk;
+    U.kv0 = y * 2 * kCsRows;
+    U.ql = __ldg(p.q_lens + seq);
+    U.cl = __ldg(p.ctx_lens + seq);
+    U.qs = __ldg(p.q_start + seq);
+    U.pos0 = U.cl - U.ql;
+    U.prefix = p.causal && p.mod.prefix ? __ldg(p.mod.prefix + seq) : 0;
+    U.nk = U.kv0 + kCsRows < U.cl ? 2 : 1;
+    // Both ends of a row's run never decrease along the rows, so the tiles that
+    // see a key of the unit are one run: from the first token whose run ends
+    // behind the first key to the last whose run begins before the last one.
+    const int kv_last = min(U.cl, U.kv0 + 2 * kCsRows) - 1, w = p.mod.window;
+    const int tok_lo = p.causal ? (U.prefix > U.kv0 ? 0 : max(0, U.kv0 - U.pos0))
+                                : (w > 0 ? max(0, U.kv0 - w + 1 - U.pos0) : 0);
+    const int tok_hi = w > 0 ? min(U.ql - 1, kv_last + w - 1 - U.pos0) : U.ql - 1;
+    const int ntok = (U.ql + tt - 1) / tt;
+    U.t_lo = min(ntok, tok_lo / tt);
+    U.n = (max(U.t_lo, tok_hi < 0 ? 0 : tok_hi / tt + 1) - U.t_lo) * heads;
+    return U;
+}
+
 template <int D, int MOD>
-__global__ void __launch_bounds__(kCsThreads, 2)
+__global__ void __launch_bounds__(kCsThreads, 1)
     attn_colsum_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const ColsumParams p) {
     using C = CsCfg<D>;
-    const int seq = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv, kv0 = blockIdx.y * kCsRows;
-    const int ql = __ldg(p.q_lens + seq), cl = __ldg(p.ctx_lens + seq);
-    // decode rows (at most 16 packed rows) are summed from their kept logits
-    if (ql <= 0 || p.g * ql <= 16 || ql > cl || cl > p.mbps * 16 || kv0 >= cl) return;
-    if (cl > p.acc_len) {
-        if (threadIdx.x == 0) raise_error(p.ctx, ERR_BOUNDS_BIT);
-        return;
-    }
-    const int qs = __ldg(p.q_start + seq), pos0 = cl - ql;
-    const int prefix = p.causal && p.mod.prefix ? __ldg(p.mod.prefix + seq) : 0;
-
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* kbuf = smem;
-    uint8_t* qring = smem + C::kTileBytes;
-    float* cols = reinterpret_cast<float*>(qring + kCsStages * C::kTileBytes);
-    float* part = cols + C::kColBytes / 4;
-    uint64_t* kfull = reinterpret_cast<uint64_t*>(part + kCsRows);
-    uint64_t* qfull = kfull + 1;
-    uint64_t* qempty = qfull + kCsStages;
-    uint64_t* sfull = qempty + kCsStages;  // [2] product of parity w complete
-    uint64_t* sempty = sfull + 2;          // [2] its columns read
-    uint64_t* drain = sempty + 2;
+    uint8_t* qring = smem + 2 * C::kTileBytes;
+    float* cols = reinterpret_cast<float*>(qring + 2 * kCsPairs * C::kTileBytes);
+    float* part = cols + C::kColBytes / 4;  // [K tile][key]: side 1's sums
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(part + 2 * kCsRows);  // [2] K tile kt in
+    uint64_t* kempty = kfull + 2;                                       // both read by the unit's last product
+    uint64_t* qfull = kempty + 1;
+    uint64_t* qempty = qfull + kCsPairs;
+    uint64_t* sfull = qempty + kCsPairs;  // [2] a pair's product with K tile kt is complete
+    uint64_t* sempty = sfull + 2;         // [2] its columns are in registers
+    uint64_t* pfull = sempty + 2;         // [2] K tile kt's sums of side 1 are in `part`
+    uint64_t* pempty = pfull + 2;         // [2] and read
+    uint64_t* ufull = pempty + 2;
+    uint64_t* uempty = ufull + kCsUnitSlots;
+    uint64_t* drain = uempty + kCsUnitSlots;
     uint64_t* never = drain + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
+    volatile int4* umbox = reinterpret_cast<volatile int4*>((reinterpret_cast<uintptr_t>(never + 1) + 15) & ~uintptr_t(15));
+    uint32_t* tmem_slot = const_cast<uint32_t*>(reinterpret_cast<volatile uint32_t*>(umbox + kCsUnitSlots));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        mbar_init(kfull, 1);
-        for (int i = 0; i < kCsStages; ++i) {
+        mbar_init(kempty, 1);
+        for (int i = 0; i < kCsPairs; ++i) {
             mbar_init(&qfull[i], 1);
             mbar_init(&qempty[i], 1);
         }
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(&sfull[w], 1);
-            mbar_init(&sempty[w], kCsRows);
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&kfull[k], 1);
+            mbar_init(&sfull[k], 1);
+            mbar_init(&sempty[k], 2 * kCsRows);
+            mbar_init(&pfull[k], kCsRows);
+            mbar_init(&pempty[k], kCsRows);
+        }
+        for (int k = 0; k < kCsUnitSlots; ++k) {
+            mbar_init(&ufull[k], 1);
+            mbar_init(&uempty[k], kCsReaders);
         }
         mbar_init(drain, 1);
         mbar_init(never, 1);
@@ -119,7 +166,7 @@ __global__ void __launch_bounds__(kCsThreads, 2)
         tma_prefetch_desc(&tm_k);
     }
     if (warp == kCsMma) {
-        tmem_alloc(tmem_slot, 256);
+        tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -127,104 +174,185 @@ __global__ void __launch_bounds__(kCsThreads, 2)
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
     const unsigned long long lim_ns = p.ctx.wait_ns;
-
     // query tiles: `tt` tokens of all heads of the group (packed) or of one head
     const int tt = p.pack ? kCsRows >> p.pack_shift : kCsRows;
     const int heads = p.pack ? 1 : p.g;
-    const int ntok = (ql + tt - 1) / tt;
-    const int kv_last = min(cl, kv0 + kCsRows) - 1;
-    // token tiles that see a key of this CTA: both ends of a row's run never
-    // decrease along the rows, so they are one run [t_lo, t_hi).  First token
-    // whose run ends behind the first key, last token whose run begins before
-    // the last one:
-    const int w_ = p.mod.window;
-    const int tok_lo = p.causal ? (prefix > kv0 ? 0 : max(0, kv0 - pos0)) : (w_ > 0 ? max(0, kv0 - w_ + 1 - pos0) : 0);
-    const int tok_hi = w_ > 0 ? min(ql - 1, kv_last + w_ - 1 - pos0) : ql - 1;
-    const int t_lo = min(ntok, tok_lo / tt), t_hi = max(t_lo, tok_hi < 0 ? 0 : tok_hi / tt + 1);
-    const int n = (t_hi - t_lo) * heads;
     auto fail = [&]() {
         raise_error(p.ctx, ERR_TIMEOUT_BIT);
         *abort_flag = 1;
     };
+    // the i-th unit of this CTA, as the producer published it; seq < 0: no more
+    auto next_unit = [&](int i, int4& u) -> bool {
+        const int k = i % kCsUnitSlots;
+        if (!mbar_wait_warp(&ufull[k], (i / kCsUnitSlots) & 1, lim_ns, abort_flag)) return false;
+        u.x = umbox[k].x;
+        u.y = umbox[k].y;
+        u.z = umbox[k].z;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&uempty[k]);
+        return true;
+    };
 
-    float mine = 0.f;  // summing warps: this thread's key over its warpgroup's tiles
     bool ok = !p.ctx.force_timeout || mbar_wait_warp(never, 0, lim_ns, abort_flag);
     if (warp == kCsProducer) {
-        int issued = 0;
-        bool k_out = false;
-        if (ok && n > 0) {
-            int blk = p.num_blocks;  // outside the map: zeros
-            if (lane < 8 && kv0 + lane * 16 < cl) {
-                const int b = __ldg(p.bt + (long)seq * p.mbps + kv0 / 16 + lane);
-                const int tok = kv0 + lane * 16;
-                // blocks that no query of the chunk sees are not read
-                const bool seen = p.mod.window == 0 || tok + 16 > pos0 - p.mod.window + 1;
-                if (seen) {
-                    if (b < 0 || b >= p.num_blocks)
-                        raise_error(p.ctx, ERR_BOUNDS_BIT);
-                    else
-                        blk = b;
+        int kf[2] = {0, 0}, ku = 0, qf = 0;  // K tiles, units with products and query pairs requested
+        const int rows = __ldg(p.k_start + p.num_seqs);
+        int ticket = 0;
+        if (lane == 0) ticket = atomicAdd(p.tickets, 1);
+        for (int i = 0; ok; ++i) {
+            // unit t: kv head t % Hkv of unit row t / Hkv (the heads of a row side by side);
+            // the ticket was asked for before the last unit's query tiles
+            const int t = __shfl_sync(0xffffffffu, ticket, 0);
+            int seq = -1, y = 0;
+            if ((long)t < (long)rows * p.Hkv) {
+                const int row = t / p.Hkv;
+                int lo = 0, hi = p.num_seqs - 1;  // last sequence whose first row is not behind `row`
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (__ldg(p.k_start + mid) <= row) lo = mid;
+                    else hi = mid - 1;
                 }
+                seq = __ldg(p.k_seq + lo);
+                y = row - __ldg(p.k_start + lo);
             }
-            if (lane == 0) mbar_arrive_expect_tx(kfull, C::kTileBytes);
-            __syncwarp();
-            if (lane < 8) {
-                if constexpr (D == 128)
-                    tma_load_5d(kbuf + lane * 4096, &tm_k, kfull, 0, 0, 0, 0, blk * p.Hkv + hk);
-                else
-                    tma_load_4d(kbuf + lane * 2048, &tm_k, kfull, 0, 0, hk, blk);
+            const int k = i % kCsUnitSlots;
+            if (i >= kCsUnitSlots && !mbar_wait_warp(&uempty[k], ((i / kCsUnitSlots) - 1) & 1, lim_ns, abort_flag)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                umbox[k].x = seq;
+                umbox[k].y = t % p.Hkv;
+                umbox[k].z = y;
+                mbar_arrive(&ufull[k]);
             }
             __syncwarp();
-            k_out = true;
-            for (; issued < n; ++issued) {
-                const int st = issued % kCsStages;
-                if (!mbar_wait_warp(&qempty[st], ((issued / kCsStages) & 1) ^ 1, lim_ns, abort_flag)) {
+            if (seq < 0) break;
+            if (lane == 0) ticket = atomicAdd(p.tickets, 1);
+            const CsUnit U = cs_unit(p, seq, t % p.Hkv, y, tt, heads);
+            if (U.n == 0) continue;
+            // lane j < 16: the unit's j-th block (blocks that no query of the chunk sees are not read)
+            int blk = p.num_blocks;  // outside the map: zeros
+            const int tok = U.kv0 + lane * 16;
+            if (lane < 16 && tok < U.cl && (p.mod.window == 0 || tok + 16 > U.pos0 - p.mod.window + 1)) {
+                const int b = __ldg(p.bt + (long)seq * p.mbps + tok / 16);
+                if (b < 0 || b >= p.num_blocks) raise_error(p.ctx, ERR_BOUNDS_BIT);
+                else blk = b;
+            }
+            // pair jj: tiles 2 jj and 2 jj + 1, laid out [64-channel half][256 rows][128 B]
+            auto request_pair = [&](int jj) {
+                const int st = qf % kCsPairs, tiles = min(2, U.n - 2 * jj);
+                if (!mbar_wait_warp(&qempty[st], ((qf / kCsPairs) & 1) ^ 1, lim_ns, abort_flag)) {
                     ok = false;
-                    break;
+                    return;
                 }
                 if (lane == 0) {
-                    const int tile = t_lo + issued / heads, h = hk * p.g + issued % heads;
-                    mbar_arrive_expect_tx(&qfull[st], C::kTileBytes);
+                    mbar_arrive_expect_tx(&qfull[st], tiles * C::kTileBytes);
+                    for (int e = 0; e < tiles; ++e) {
+                        const int j = 2 * jj + e;
 #pragma unroll
-                    for (int a = 0; a < C::kAtoms; ++a)
-                        tma_load_4d(qring + st * C::kTileBytes + a * C::kAtomBytes, &tm_q, &qfull[st], a * 64, h,
-                                    qs + tile * tt, 0);
+                        for (int a = 0; a < C::kAtoms; ++a)
+                            tma_load_4d(qring + st * 2 * C::kTileBytes + (2 * a + e) * C::kAtomBytes, &tm_q, &qfull[st],
+                                        a * 64, U.hk * p.g + j % heads, U.qs + (U.t_lo + j / heads) * tt, 0);
+                    }
                 }
                 __syncwarp();
+                ++qf;
+            };
+            request_pair(0);  // before the K tiles, whose places are free only when the unit before is done
+            if (!ok || !mbar_wait_warp(kempty, (ku & 1) ^ 1, lim_ns, abort_flag)) {
+                ok = false;
+                break;
             }
+            ++ku;
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                if (kt >= U.nk) continue;
+                if (lane == 0) mbar_arrive_expect_tx(&kfull[kt], C::kTileBytes);
+                __syncwarp();
+                if (lane >= 8 * kt && lane < 8 * kt + 8) {
+                    uint8_t* dst = kbuf + kt * C::kTileBytes;
+                    if constexpr (D == 128)
+                        tma_load_5d(dst + (lane & 7) * 4096, &tm_k, &kfull[kt], 0, 0, 0, 0, blk * p.Hkv + U.hk);
+                    else
+                        tma_load_4d(dst + (lane & 7) * 2048, &tm_k, &kfull[kt], 0, 0, U.hk, blk);
+                }
+                __syncwarp();
+                ++kf[kt];
+            }
+            for (int jj = 1; 2 * jj < U.n && ok; ++jj) request_pair(jj);
         }
         if (!ok) {
             if (lane == 0) fail();
             // the copies already issued land before the CTA exits
-            if (k_out) (void)mbar_wait_warp(kfull, 0, 1000000000ull, nullptr);
-            for (int f = max(0, issued - kCsStages); f < issued; ++f)
-                (void)mbar_wait_warp(&qfull[f % kCsStages], (f / kCsStages) & 1, 1000000000ull, nullptr);
+            for (int kt = 0; kt < 2; ++kt)
+                if (kf[kt] > 0) (void)mbar_wait_warp(&kfull[kt], (kf[kt] - 1) & 1, 1000000000ull, nullptr);
+            for (int f = max(0, qf - kCsPairs); f < qf; ++f)
+                (void)mbar_wait_warp(&qfull[f % kCsPairs], (f / kCsPairs) & 1, 1000000000ull, nullptr);
         }
     } else if (warp == kCsMma) {
-        constexpr uint32_t kIdesc = idesc_bf16_f32(128, 128, 0, 0);
+        constexpr uint32_t kIdesc1 = idesc_bf16_f32(128, 128, 0, 0), kIdesc2 = idesc_bf16_f32(128, 256, 0, 0);
         const uint32_t k_addr = smem_u32(kbuf), q_addr = smem_u32(qring);
-        if (ok && n > 0 && !mbar_wait_warp(kfull, 0, lim_ns, abort_flag)) ok = false;
-        for (int i = 0; ok && i < n; ++i) {
-            const int st = i % kCsStages, w = i & 1;
-            if (!mbar_wait_warp(&qfull[st], (i / kCsStages) & 1, lim_ns, abort_flag) ||
-                !mbar_wait_warp(&sempty[w], ((i >> 1) & 1) ^ 1, lim_ns, abort_flag)) {
+        int kc[2] = {0, 0}, qc = 0, sc[2] = {0, 0};  // K tiles and pairs consumed, products issued per K tile
+        for (int i = 0; ok; ++i) {
+            int4 u;
+            if (!next_unit(i, u)) {
                 ok = false;
                 break;
             }
-            tc_fence_after();
-            if (lane == 0) {
-                const uint64_t kd = smem_desc_sw128(k_addr, 16, C::kGroup);
-                const uint64_t qd = smem_desc_sw128(q_addr + st * C::kTileBytes, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t koff = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
-                    const uint32_t qoff = ((kk >> 2) * C::kAtomBytes + (kk & 3) * 32) >> 4;
-                    umma_ss(tbase + w * 128, kd + koff, qd + qoff, kIdesc, kk > 0);
+            if (u.x < 0) break;
+            const CsUnit U = cs_unit(p, u.x, u.y, u.z, tt, heads);
+            if (U.n == 0) continue;
+            for (int j = 0; j < U.n && ok; j += 2) {
+                const int st = qc % kCsPairs;
+                // the pair and both products' buffers are probed together: three checks in
+                // flight cost about one
+                uint32_t rdy[3];
+                mbar_test3(&qfull[st], (qc / kCsPairs) & 1, &sempty[0], (sc[0] & 1) ^ 1, &sempty[1], (sc[1] & 1) ^ 1, rdy);
+                if (!__all_sync(0xffffffffu, rdy[0]) &&
+                    !mbar_wait_warp(&qfull[st], (qc / kCsPairs) & 1, lim_ns, abort_flag)) {
+                    ok = false;
+                    break;
                 }
-                umma_commit(&qempty[st]);
-                umma_commit(&sfull[w]);
+                const uint64_t qd = smem_desc_sw128(q_addr + st * 2 * C::kTileBytes, 16, 1024);
+                const uint32_t idesc = j + 1 < U.n ? kIdesc2 : kIdesc1;
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) {
+                    if (kt >= U.nk || !ok) continue;
+                    if (j == 0 && !mbar_wait_warp(&kfull[kt], kc[kt] & 1, lim_ns, abort_flag)) {
+                        ok = false;
+                        continue;
+                    }
+                    const bool free_buf = __all_sync(0xffffffffu, rdy[1 + kt]);
+                    if (!free_buf && !mbar_wait_warp(&sempty[kt], (sc[kt] & 1) ^ 1, lim_ns, abort_flag)) {
+                        ok = false;
+                        continue;
+                    }
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t kd = smem_desc_sw128(k_addr + kt * C::kTileBytes, 16, C::kGroup);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t koff = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+                            const uint32_t qoff = ((kk >> 2) * 2 * C::kAtomBytes + (kk & 3) * 32) >> 4;
+                            umma_ss(tbase + kt * 256, kd + koff, qd + qoff, idesc, kk > 0);
+                        }
+                        umma_commit(&sfull[kt]);
+                    }
+                    __syncwarp();
+                    ++sc[kt];
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    umma_commit(&qempty[st]);
+                    if (j + 2 >= U.n) umma_commit(kempty);
+                }
+                __syncwarp();
+                ++qc;
             }
-            __syncwarp();
+            if (!ok) break;
+            ++kc[0];
+            if (U.nk > 1) ++kc[1];
         }
         if (!ok && lane == 0) fail();
         // every product issued above completes before TMEM is released
@@ -232,104 +360,180 @@ __global__ void __launch_bounds__(kCsThreads, 2)
         __syncwarp();
         (void)mbar_wait_bounded(drain, 0, 1000000000ull, nullptr);
     } else {
-        const int w = warp >> 2, quarter = warp & 3;
+        const int w = warp >> 2, kt = w >> 1, side = w & 1, quarter = warp & 3;
         const uint32_t trow = tbase + ((uint32_t)(quarter * 32) << 16) + w * 128;
         float* nlse = cols + warp * 3 * kCsRows;
         float* slope = nlse + kCsRows;
         short2* run = reinterpret_cast<short2*>(slope + kCsRows);  // from this warp's first key
-        float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const int k_lo = kv0 + quarter * 32, k_hi = min(cl, k_lo + 32);  // this warp's keys
-        for (int i = w; ok && i < n; i += 2) {
-            const int tile = t_lo + i / heads, h0 = hk * p.g + i % heads, tok0 = tile * tt;
-            // statistics of the tile's columns (query rows): four per lane
-            __syncwarp();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int c = b * 32 + lane;
-                const int tok = tok0 + (p.pack ? c >> p.pack_shift : c);
-                const int head = h0 + (p.pack ? c & (p.g - 1) : 0);
-                float L = 0.f;
-                if (tok < ql) {
-                    L = __ldg(p.lse + (long)(qs + tok) * p.Hq + head);
-                    L = L == -INFINITY ? 0.f : -L * kCsLog2e;
-                }
-                nlse[c] = L;
-                const int2 seen = tok < ql ? cs_range(p, pos0 + tok, prefix, cl) : make_int2(0, 0);
-                run[c] = make_short2((short)min(32, max(0, seen.x - k_lo)), (short)min(32, max(0, seen.y - k_lo)));
-                if constexpr (MOD == CS_BIAS) slope[c] = -__ldg(p.mod.slopes + head) * kCsLog2e;
-            }
-            __syncwarp();
-            // every row of the tile is real and sees every key of this warp (warp-uniform)
-            const int2 rf = cs_range(p, pos0 + tok0, prefix, cl);
-            const int2 rl = cs_range(p, pos0 + min(ql, tok0 + tt) - 1, prefix, cl);
-            const bool plain = tok0 + tt <= ql && k_lo >= rl.x && k_hi <= rf.y;
-            if (!mbar_wait_warp(&sfull[w], (i >> 1) & 1, lim_ns, abort_flag)) {
+        int sc = 0, handed = 0;  // pairs seen, sums handed over
+        for (int i = 0; ok; ++i) {
+            int4 u;
+            if (!next_unit(i, u)) {
                 ok = false;
                 break;
             }
-            tc_fence_after();
-            // four columns at a time; `masked`: some row of the tile is not real or does not see some key
-            auto columns = [&](auto masked) {
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t raw[32];
-                    tmem_ld32(trow + b * 32, raw);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 nl = *reinterpret_cast<const float4*>(nlse + b * 32 + j);
-                        const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            float2 x = make_float2(__uint_as_float(raw[j + e]), __uint_as_float(raw[j + e + 1]));
-                            const float2 l2 = make_float2(nls[e], nls[e + 1]);
-                            if (MOD == CS_CAP || (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
-                                x.x = fmaf(p.mod.cap_out, tanh_f32(x.x * p.mod.cap_in), l2.x);
-                                x.y = fmaf(p.mod.cap_out, tanh_f32(x.y * p.mod.cap_in), l2.y);
-                            } else {
-                                x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), l2);
-                            }
-                            if constexpr (MOD == CS_BIAS) {
-                                const float2 sl = *reinterpret_cast<const float2*>(slope + b * 32 + j + e);
-                                const int c = b * 32 + j + e, d0 = k_lo + lane - pos0 - tok0;
-                                x.x = fmaf(sl.x, fabsf((float)(d0 - (p.pack ? c >> p.pack_shift : c))), x.x);
-                                x.y = fmaf(sl.y, fabsf((float)(d0 - (p.pack ? (c + 1) >> p.pack_shift : c + 1))), x.y);
-                            }
-                            float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                            if constexpr (decltype(masked)::value) {
-                                const short2 ra = run[b * 32 + j + e], rb = run[b * 32 + j + e + 1];
-                                pr.x = lane >= ra.x && lane < ra.y ? pr.x : 0.f;
-                                pr.y = lane >= rb.x && lane < rb.y ? pr.y : 0.f;
-                            }
-                            sum[(j + e) >> 1 & 3] = __fadd2_rn(sum[(j + e) >> 1 & 3], pr);
-                        }
-                    }
+            if (u.x < 0) break;
+            const CsUnit U = cs_unit(p, u.x, u.y, u.z, tt, heads);
+            if (kt >= U.nk) continue;
+            const int k_lo = U.kv0 + kt * kCsRows + quarter * 32, k_hi = min(U.cl, k_lo + 32);  // this warp's keys
+            float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            // query tile j of the unit: tile `tile` of head `head` of the group, and of the
+            // next one of this side (no divisions in the loop)
+            int tile = U.t_lo + side / heads, head = side % heads, ntile = tile, nhead = head;
+            auto advance = [&](int& t, int& h) {
+                h += 2;
+                while (h >= heads) {
+                    h -= heads;
+                    ++t;
                 }
             };
-            if (plain) columns(std::false_type{});
-            else columns(std::true_type{});
-            tc_fence_before();
-            mbar_arrive(&sempty[w]);
+            // -lse (log2 units) of columns lane, lane + 32, ... of the next tile
+            const int ctok = p.pack ? lane >> p.pack_shift : lane, chead = p.pack ? lane & (p.g - 1) : 0;
+            const int cstep = p.pack ? 32 >> p.pack_shift : 32;  // tokens from column c to c + 32
+            const float* lse0 = p.lse + (long)(U.qs + ctok) * p.Hq + U.hk * p.g + chead;
+            float stat[4];
+            auto load_stats = [&](int t, int h) {
+                const int tok0 = t * tt;
+                const float* src = lse0 + (long)tok0 * p.Hq + h;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    stat[b] = tok0 + ctok + b * cstep < U.ql ? __ldg(src + (long)b * cstep * p.Hq) : 0.f;
+            };
+            if (side < U.n) load_stats(tile, head);
+            for (int j = side; j - side < U.n; j += 2) {
+                if (j >= U.n) {  // the last pair has one tile only: side 1 lets its turn pass
+                    if (!mbar_wait_warp(&sfull[kt], sc & 1, lim_ns, abort_flag)) ok = false;
+                    if (!ok) break;
+                    ++sc;
+                    mbar_arrive(&sempty[kt]);
+                    break;
+                }
+                const int tok0 = tile * tt;
+                // Warp-uniform: does every row of the tile exist and see every key of this warp
+                // (plain), or no row any of them (none)?
+                const int2 rf = cs_range(p, U.pos0 + tok0, U.prefix, U.cl);
+                const int2 rl = cs_range(p, U.pos0 + min(U.ql, tok0 + tt) - 1, U.prefix, U.cl);
+                const bool plain = tok0 + tt <= U.ql && k_lo >= rl.x && k_hi <= rf.y;
+                const bool none = k_lo >= rl.y || k_hi <= rf.x;
+                __syncwarp();
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int c = b * 32 + lane;
+                    nlse[c] = stat[b] == -INFINITY ? 0.f : -stat[b] * kCsLog2e;
+                    if constexpr (MOD == CS_BIAS)
+                        slope[c] = -__ldg(p.mod.slopes + U.hk * p.g + head + chead) * kCsLog2e;
+                    if (!plain) {
+                        const int tok = tok0 + ctok + b * cstep;
+                        const int2 seen = tok < U.ql ? cs_range(p, U.pos0 + tok, U.prefix, U.cl) : make_int2(0, 0);
+                        run[c] = make_short2((short)min(32, max(0, seen.x - k_lo)), (short)min(32, max(0, seen.y - k_lo)));
+                    }
+                }
+                __syncwarp();
+                advance(ntile, nhead);
+                if (j + 2 < U.n) load_stats(ntile, nhead);
+                if (!mbar_wait_warp(&sfull[kt], sc & 1, lim_ns, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                ++sc;
+                tc_fence_after();
+                // 32 columns at a time, the next ones on their way while these are summed;
+                // `masked`: some row of the tile is not real or does not see some key
+                auto columns = [&](auto masked) {
+                    constexpr int kAhead = MOD == CS_PLAIN ? 1 : 0;  // (registers: 96 a thread)
+                    uint32_t raw[1 + kAhead][32];
+                    if constexpr (kAhead) tmem_ld32(trow, raw[0]);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        if constexpr (!kAhead) tmem_ld32(trow + b * 32, raw[0]);
+                        tmem_wait_ld();
+                        if (b < 3) {
+                            if constexpr (kAhead) tmem_ld32(trow + (b + 1) * 32, raw[(b + 1) & kAhead]);
+                        } else {  // every column is in registers: the buffer is free
+                            tc_fence_before();
+                            mbar_arrive(&sempty[kt]);
+                        }
+#pragma unroll
+                        for (int jj = 0; jj < 32; jj += 4) {
+                            const float4 nl = *reinterpret_cast<const float4*>(nlse + b * 32 + jj);
+                            const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                const int c = b * 32 + jj + e;
+                                float2 x = make_float2(__uint_as_float(raw[b & kAhead][jj + e]),
+                                                       __uint_as_float(raw[b & kAhead][jj + e + 1]));
+                                const float2 l2 = make_float2(nls[e], nls[e + 1]);
+                                if (MOD == CS_CAP || (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
+                                    x.x = fmaf(p.mod.cap_out, tanh_f32(x.x * p.mod.cap_in), l2.x);
+                                    x.y = fmaf(p.mod.cap_out, tanh_f32(x.y * p.mod.cap_in), l2.y);
+                                } else {
+                                    x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), l2);
+                                }
+                                if constexpr (MOD == CS_BIAS) {
+                                    const float2 sl = *reinterpret_cast<const float2*>(slope + c);
+                                    const int d0 = k_lo + lane - U.pos0 - tok0;
+                                    x.x = fmaf(sl.x, fabsf((float)(d0 - (p.pack ? c >> p.pack_shift : c))), x.x);
+                                    x.y = fmaf(sl.y, fabsf((float)(d0 - (p.pack ? (c + 1) >> p.pack_shift : c + 1))), x.y);
+                                }
+                                float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                                if constexpr (decltype(masked)::value) {
+                                    const short2 ra = run[c], rb = run[c + 1];
+                                    pr.x = lane >= ra.x && lane < ra.y ? pr.x : 0.f;
+                                    pr.y = lane >= rb.x && lane < rb.y ? pr.y : 0.f;
+                                }
+                                sum[(c >> 1) & 3] = __fadd2_rn(sum[(c >> 1) & 3], pr);
+                            }
+                        }
+                    }
+                };
+                if (none) {
+                    mbar_arrive(&sempty[kt]);
+                } else if (plain) {
+                    columns(std::false_type{});
+                } else {
+                    columns(std::true_type{});
+                }
+                tile = ntile;
+                head = nhead;
+            }
+            if (!ok) break;
+            const float mine =
+                ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
+            float* at = part + kt * kCsRows + quarter * 32 + lane;
+            if (side == 1) {
+                if (!mbar_wait_warp(&pempty[kt], (handed & 1) ^ 1, lim_ns, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                *at = mine;
+                mbar_arrive(&pfull[kt]);
+            } else {
+                if (!mbar_wait_warp(&pfull[kt], handed & 1, lim_ns, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const float odd = *at;
+                mbar_arrive(&pempty[kt]);
+                const int key = k_lo + lane;
+                if (key < U.cl) {
+                    const long o = ((long)U.seq * p.Hkv + U.hk) * p.acc_len + key;
+                    const float old = p.acc_in && key < U.pos0 ? p.decay * p.acc_in[o] : 0.f;
+                    p.acc_out[o] = old + (mine + odd);
+                }
+            }
+            ++handed;
         }
         if (!ok && lane == 0) fail();
-        mine = ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
-        if (w == 1) part[quarter * 32 + lane] = mine;
     }
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kCsMma) tmem_dealloc(tbase, 256);
-    const int key = kv0 + threadIdx.x;
-    if (threadIdx.x < kCsRows && key < cl && !*abort_flag) {
-        const long at = ((long)seq * p.Hkv + hk) * p.acc_len + key;
-        const float old = p.acc_in && key < pos0 ? p.decay * p.acc_in[at] : 0.f;
-        p.acc_out[at] = old + (mine + part[threadIdx.x]);
-    }
+    if (warp == kCsMma) tmem_dealloc(tbase, 512);
 }
 
 template <int D, int MOD>
-static fa_status launch_colsum(const CUtensorMap& tq, const CUtensorMap& tk, const ColsumParams& p, dim3 grid,
+static fa_status launch_colsum(const CUtensorMap& tq, const CUtensorMap& tk, const ColsumParams& p, int grid,
                                cudaStream_t s) {
     const fa_status st =
         raise_dynamic_smem(reinterpret_cast<const void*>(attn_colsum_kernel<D, MOD>), CsCfg<D>::kSmem);
@@ -340,7 +544,8 @@ static fa_status launch_colsum(const CUtensorMap& tq, const CUtensorMap& tk, con
 
 // Weight sums of the sequences whose chunks took the tensor-core path.
 fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* block_table, const int32_t* ctx_lens,
-                             const int32_t* q_lens, const int32_t* q_start, const float* lse, const float* acc_in,
+                             const int32_t* q_lens, const int32_t* q_start, const int32_t* k_start,
+                             const int32_t* k_seq, int32_t* tickets, const float* lse, const float* acc_in,
                              float* acc_out, int acc_len, float decay, int num_seqs, int mbps, int num_blocks, int Hq,
                              int Hkv, int d, int causal, float scale, int total_q, const ScoreMod& mod, cudaStream_t s,
                              const DevCtx& ctx) {
@@ -353,6 +558,10 @@ fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* 
     p.ctx_lens = ctx_lens;
     p.q_lens = q_lens;
     p.q_start = q_start;
+    p.k_start = k_start;
+    p.k_seq = k_seq;
+    p.tickets = tickets;
+    p.num_seqs = num_seqs;
     p.lse = lse;
     p.acc_in = acc_in;
     p.acc_out = acc_out;
@@ -369,7 +578,7 @@ fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* 
     p.scale_log2 = scale * kCsLog2e;
     p.mod = mod;
     p.ctx = ctx;
-    const dim3 grid(num_seqs * Hkv, (mbps * 16 + kCsRows - 1) / kCsRows);
+    const int grid = sm_count();
     auto go = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
         if (mod.slopes) return launch_colsum<D, CS_BIAS>(tq, tk, p, grid, s);

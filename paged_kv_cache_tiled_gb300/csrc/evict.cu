@@ -8,7 +8,7 @@
 // select over order-preserving integer keys (three passes of 11, 11 and 10
 // bits), then lists the kept tokens with one scan.  A sequence and kv head is one
 // CTA, or a cluster of up to eight when its row is long: each CTA histograms
-// its part (kept in registers when it has at most 8192 tokens), the parts are
+// its part (kept in registers when it has at most 4096 tokens), the parts are
 // added through distributed shared memory, and every CTA takes the same
 // decision.  evict_move_kernel gathers the kept rows.  Memory bound: the weights
 // are read once, each kept row once.
@@ -19,7 +19,7 @@
 namespace fa {
 
 constexpr int kEvBlock = 16;
-constexpr int kEvThreads = 1024;
+constexpr int kEvThreads = 512;
 constexpr int kEvBins = 2048;
 constexpr int kEvItems = 8;  // consecutive tokens per thread and scan pass
 
@@ -43,7 +43,17 @@ __device__ __forceinline__ unsigned cluster_size() {
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The int at p (an address of this CTA's shared memory) in CTA `rank` of the cluster.
+// The ints at p (an address of this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ int4 cluster_load4(const int* p, unsigned rank) {
+    uint32_t a;
+    int4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ int cluster_load(const int* p, unsigned rank) {
     uint32_t a;
     int v;
@@ -59,7 +69,8 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
                                                                   int32_t* __restrict__ new_lens, int Hkv, int mbps,
                                                                   int dst_mbps, int keep, int recent, int sink,
                                                                   DevCtx ctx) {
-    __shared__ int hist[2][kEvBins];  // by turns, so that one cluster barrier per pass is enough
+    static_assert(kEvBins == 4 * kEvThreads, "a thread owns four bins");
+    __shared__ __align__(16) int hist[2][kEvBins];  // by turns, so that one cluster barrier per pass is enough
     __shared__ int2 warp_sums[32];
     __shared__ int sel_digit, sel_above, totals[2];
     // the rows' copy may be scheduled; it waits for this grid's end before it reads the list
@@ -93,7 +104,10 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
     const int part = ((cl + CL - 1) / CL + kEvItems - 1) / kEvItems * kEvItems;
     const int p0 = min(cl, rank * part), p1 = min(cl, p0 + part);
     const bool vec = (acc_len & 3) == 0 && (reinterpret_cast<uintptr_t>(acc) & 15) == 0;
+    const int mid_end = cl - recent;
     float v[kEvItems];
+    uint32_t key[kEvItems];
+    unsigned middle = 0;  // which of the thread's tokens the weights decide about
     auto load = [&](int t0) {
         if (vec && t0 + kEvItems <= p1) {
             const float4 x = *reinterpret_cast<const float4*>(a + t0), y = *reinterpret_cast<const float4*>(a + t0 + 4);
@@ -102,56 +116,60 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
 #pragma unroll
             for (int k = 0; k < kEvItems; ++k) v[k] = t0 + k < p1 ? a[t0 + k] : 0.f;
         }
+        middle = 0;
+#pragma unroll
+        for (int k = 0; k < kEvItems; ++k) {
+            key[k] = weight_key(v[k]);
+            if (t0 + k < p1 && t0 + k >= sink && t0 + k < mid_end) middle |= 1u << k;
+        }
     };
     const bool once = p1 - p0 <= kEvPass;  // the part stays in registers
     load(p0 + tid * kEvItems);
     // the `want` largest keys of the tokens [sink, mid_end)
-    const int mid_end = cl - recent;
     const int want = keep - sink - recent;
     uint32_t prefix = 0;  // digits fixed so far
     int need = want;      // tokens still to take among those that match the prefix
-    for (int i = tid; i < kEvBins; i += kEvThreads) hist[0][i] = 0;
+    const int top = kEvBins - 4 * (tid + 1);  // this thread's bins [top, top + 4): highest bins first
+    *reinterpret_cast<int4*>(&hist[0][top]) = make_int4(0, 0, 0, 0);
     __syncthreads();
     for (int pass = 0; pass < 3 && want > 0; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
         int* hs = hist[pass & 1];
         for (int base = p0; base < p1; base += kEvPass) {
-            const int t0 = base + tid * kEvItems;
-            if (!once) load(t0);
+            if (!once) load(base + tid * kEvItems);
+            if (!__any_sync(0xffffffffu, middle)) continue;
 #pragma unroll
             for (int k = 0; k < kEvItems; ++k) {
-                const int t = t0 + k;
-                const uint32_t key = weight_key(v[k]);
-                const bool in = t < p1 && t >= sink && t < mid_end &&
-                                (pass == 0 || (key >> (shift + bits)) == (prefix >> (shift + bits)));
-                const uint32_t digit = in ? (key >> shift) & ((1u << bits) - 1) : 0xffffffffu;
-                int same;
-                __match_all_sync(0xffffffffu, digit, &same);
-                if (same) {  // many tokens may hold the same weight (0): one add for the warp
-                    if (in && lane == 0) atomicAdd(&hs[digit], 32);
-                } else if (in) {
-                    atomicAdd(&hs[digit], 1);
-                }
+                const bool in = ((middle >> k) & 1u) && (pass == 0 || ((key[k] ^ prefix) >> (shift + bits)) == 0);
+                const uint32_t digit = in ? (key[k] >> shift) & ((1u << bits) - 1) : 0xffffffffu;
+                // many tokens may hold the same weight (0): one add for the warp then
+                const bool same = __all_sync(0xffffffffu, digit == __shfl_sync(0xffffffffu, digit, 0));
+                if (in && (!same || lane == 0)) atomicAdd(&hs[digit], same ? 32 : 1);
             }
         }
         if (CL > 1) cluster_sync_all();
         else __syncthreads();
-        // the digit where the count from the top reaches `need`: each thread owns two bins
-        const int b1 = kEvBins - 1 - 2 * tid, b0 = b1 - 1;  // highest bins first
-        int c1 = 0, c0 = 0;
+        // the digit where the count from the top reaches `need`
+        int4 c = make_int4(0, 0, 0, 0);
         if (CL > 1) {
-            for (int r = 0; r < CL; ++r) {
-                c1 += cluster_load(hs + b1, r);
-                c0 += cluster_load(hs + b0, r);
+            int4 part_c[8];  // all parts' loads in flight together
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                part_c[r] = r < CL ? cluster_load4(hs + top, r) : make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                c.x += part_c[r].x;
+                c.y += part_c[r].y;
+                c.z += part_c[r].z;
+                c.w += part_c[r].w;
             }
         } else {
-            c1 = hs[b1];
-            c0 = hs[b0];
+            c = *reinterpret_cast<const int4*>(hs + top);
         }
         // the other buffer: every CTA read its counts of the pass before ahead of this pass's barrier
-        hist[(pass + 1) & 1][b1] = 0;
-        hist[(pass + 1) & 1][b0] = 0;
-        int x = c0 + c1;
+        *reinterpret_cast<int4*>(&hist[(pass + 1) & 1][top]) = make_int4(0, 0, 0, 0);
+        const int own_c = c.x + c.y + c.z + c.w;
+        int x = own_c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -159,14 +177,17 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
         }
         if (lane == 31) warp_sums[wid].x = x;
         __syncthreads();
-        const int before = __reduce_add_sync(0xffffffffu, lane < wid ? warp_sums[lane].x : 0);
-        const int above = before + x - c0 - c1;  // keys in higher bins than b1
-        if (above < need && above + c1 >= need) {
-            sel_digit = b1;
-            sel_above = above;
-        } else if (above + c1 < need && above + c1 + c0 >= need) {
-            sel_digit = b0;
-            sel_above = above + c1;
+        int above = __reduce_add_sync(0xffffffffu, lane < wid ? warp_sums[lane].x : 0) + x - own_c;
+        if (above < need && above + own_c >= need) {  // in one of this thread's bins
+            const int cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int b = 3; b >= 0; --b) {
+                if (above < need && above + cs[b] >= need) {
+                    sel_digit = top + b;
+                    sel_above = above;
+                }
+                above += cs[b];
+            }
         }
         __syncthreads();
         prefix |= (uint32_t)sel_digit << shift;
@@ -180,10 +201,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
         for (int k = 0; k < kEvItems; ++k) {
             const int t = t0 + k;
             if (t >= p1) continue;
-            const uint32_t key = weight_key(v[k]);
-            if (t < sink || t >= mid_end || (want > 0 && key > prefix))
+            if (!((middle >> k) & 1u) || (want > 0 && key[k] > prefix))
                 sure |= 1u << k;
-            else if (want > 0 && key == prefix)
+            else if (want > 0 && key[k] == prefix)
                 eq |= 1u << k;
         }
     };
@@ -226,7 +246,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
         __syncthreads();  // warp_sums of the pass before is read
         if (lane == 31) warp_sums[wid] = x;
         __syncthreads();
-        const int2 ws = warp_sums[lane];
+        const int2 ws = lane < kEvThreads / 32 ? warp_sums[lane] : make_int2(0, 0);
         int ns = kept_before + x.x - own.x + __reduce_add_sync(0xffffffffu, lane < wid ? ws.x : 0);
         int ne = eq_before + x.y - own.y + __reduce_add_sync(0xffffffffu, lane < wid ? ws.y : 0);
         kept_before += __reduce_add_sync(0xffffffffu, ws.x);
@@ -248,46 +268,46 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
 }
 
 // Row i of (sequence, kv head): kept token list[i] from its block of `src` to
-// token i of `dst`, K and V, 16 bytes per thread; kEvRows rows per thread so
-// that their loads are in flight together.
-constexpr int kEvRows = 4;
-__global__ void __launch_bounds__(256) evict_move_kernel(uint16_t* kc, uint16_t* vc, const int32_t* __restrict__ src,
-                                                         const int32_t* __restrict__ dst,
-                                                         const int32_t* __restrict__ list, int num_seqs, int Hkv, int d,
-                                                         int mbps, int dst_mbps, int keep, int num_blocks, DevCtx ctx) {
+// token i of `dst`, K and V, 16 bytes per thread; kEvRows rows per thread whose
+// loads are in flight together, and full occupancy behind the three dependent
+// loads (token, blocks, values) of a row.
+constexpr int kEvRows = 2;
+__global__ void __launch_bounds__(256, 8) evict_move_kernel(uint16_t* kc, uint16_t* vc, const int32_t* __restrict__ src,
+                                                            const int32_t* __restrict__ dst, const int32_t* list,
+                                                            int Hkv, int d, int mbps, int dst_mbps, int keep,
+                                                            int num_blocks, int per, DevCtx ctx) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is complete
-    const int cpr = d >> 3;             // chunks per row
-    const int lanes = 2 * cpr;          // threads per row pair (K and V)
-    const int rows_cta = 256 / lanes;   // rows side by side
-    const long per = (keep + rows_cta * kEvRows - 1) / (rows_cta * kEvRows);  // CTA items per (sequence, head)
-    const long total = (long)num_seqs * Hkv * per;
+    const int cpr = d >> 3;            // chunks per row
+    const int lanes = 2 * cpr;         // threads per row pair (K and V)
+    const int rows_cta = 256 / lanes;  // rows side by side
     const int c = threadIdx.x % lanes, rr = threadIdx.x / lanes;
     uint16_t* cache = c < cpr ? kc : vc;
     const int off = (c < cpr ? c : c - cpr) * 8;
-    for (long item = blockIdx.x; item < total; item += gridDim.x) {
-        const long sh = item / per;
-        const int s = (int)(sh / Hkv), h = (int)(sh % Hkv), i0 = (int)(item % per) * rows_cta * kEvRows + rr;
-        long to[kEvRows];
-        uint4 v[kEvRows];
+    const int sh = blockIdx.x / per, s = sh / Hkv, h = sh % Hkv;
+    const int i0 = blockIdx.x % per * rows_cta * kEvRows + rr;
+    const int32_t* tokens = list + (long)sh * keep;
+    int t[kEvRows];
 #pragma unroll
-        for (int k = 0; k < kEvRows; ++k) {
-            const int i = i0 + k * rows_cta;
-            to[k] = -1;
-            const int t = i < keep ? __ldcg(list + sh * keep + i) : -1;
-            if (t < 0) continue;
-            const int sb = __ldg(src + (long)s * mbps + t / kEvBlock);
-            const int db = __ldg(dst + (long)s * dst_mbps + i / kEvBlock);
-            if (sb < 0 || sb >= num_blocks || db < 0 || db >= num_blocks) {
-                raise_error(ctx, ERR_BOUNDS_BIT);
-                continue;
-            }
-            v[k] = *reinterpret_cast<const uint4*>(cache + (((long)sb * Hkv + h) * kEvBlock + t % kEvBlock) * d + off);
-            to[k] = (((long)db * Hkv + h) * kEvBlock + i % kEvBlock) * d + off;
+    for (int k = 0; k < kEvRows; ++k) t[k] = i0 + k * rows_cta < keep ? __ldcg(tokens + i0 + k * rows_cta) : -1;
+    long to[kEvRows];
+    uint4 v[kEvRows];
+#pragma unroll
+    for (int k = 0; k < kEvRows; ++k) {
+        const int i = i0 + k * rows_cta;
+        to[k] = -1;
+        if (t[k] < 0) continue;
+        const int sb = __ldg(src + (long)s * mbps + t[k] / kEvBlock);
+        const int db = __ldg(dst + (long)s * dst_mbps + i / kEvBlock);
+        if (sb < 0 || sb >= num_blocks || db < 0 || db >= num_blocks) {
+            raise_error(ctx, ERR_BOUNDS_BIT);
+            continue;
         }
-#pragma unroll
-        for (int k = 0; k < kEvRows; ++k)
-            if (to[k] >= 0) *reinterpret_cast<uint4*>(cache + to[k]) = v[k];
+        v[k] = *reinterpret_cast<const uint4*>(cache + (((long)sb * Hkv + h) * kEvBlock + t[k] % kEvBlock) * d + off);
+        to[k] = (((long)db * Hkv + h) * kEvBlock + i % kEvBlock) * d + off;
     }
+#pragma unroll
+    for (int k = 0; k < kEvRows; ++k)
+        if (to[k] >= 0) *reinterpret_cast<uint4*>(cache + to[k]) = v[k];
 }
 
 }  // namespace fa
@@ -311,7 +331,8 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
         recent < 0 || sink < 0 || recent > keep || sink > keep - recent || acc_len < 0 || acc_out_len < 0)
         return FA_ERR_INVALID_ARG;
     if (block_size != kEvBlock || (d != 64 && d != 128)) return FA_ERR_UNSUPPORTED;
-    if ((long)num_seqs * Hkv >= 1L << 27) return FA_ERR_UNSUPPORTED;
+    if ((long)num_seqs * Hkv >= 1L << 27 || (long)num_seqs * Hkv * ((keep + 15) / 16) >= 1L << 31)
+        return FA_ERR_UNSUPPORTED;  // grid limits
     if (num_seqs == 0) return FA_OK;
     if (!k_cache || !v_cache || !acc || !block_table || !ctx_lens || !dst_table || !new_lens)
         return FA_ERR_INVALID_ARG;
@@ -353,14 +374,14 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
                            max_blocks_per_seq, dst_blocks_per_seq, keep, recent, sink, ctx) != cudaSuccess)
         return FA_ERR_CUDA;
     const int rows_item = 256 / (2 * (d / 8)) * kEvRows;
-    const long items = rows * ((keep + rows_item - 1) / rows_item);
-    cfg.gridDim = dim3((unsigned)std::min<long>(items, 1L << 30));
+    const int per = (keep + rows_item - 1) / rows_item;  // CTAs per sequence and head
+    cfg.gridDim = dim3((unsigned)(rows * per));
     cfg.blockDim = dim3(256);
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     if (cudaLaunchKernelEx(&cfg, evict_move_kernel, static_cast<uint16_t*>(k_cache), static_cast<uint16_t*>(v_cache),
-                           block_table, dst_table, static_cast<const int32_t*>(list), num_seqs, Hkv, d,
-                           max_blocks_per_seq, dst_blocks_per_seq, keep, num_blocks, ctx) != cudaSuccess)
+                           block_table, dst_table, static_cast<const int32_t*>(list), Hkv, d, max_blocks_per_seq,
+                           dst_blocks_per_seq, keep, num_blocks, per, ctx) != cudaSuccess)
         return FA_ERR_CUDA;
     set_launch_count(2);
     return FA_OK;

@@ -47,7 +47,8 @@ fa_status launch_paged_prefill(const void* q, const void* k_cache, const void* v
                                int total_q, cudaStream_t s, const DevCtx& ctx, const ScoreMod* mod);
 // Weight sums of the sequences that take the tensor-core path (attn_colsum.cu).
 fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* block_table, const int32_t* ctx_lens,
-                             const int32_t* q_lens, const int32_t* q_start, const float* lse, const float* acc_in,
+                             const int32_t* q_lens, const int32_t* q_start, const int32_t* k_start,
+                             const int32_t* k_seq, int32_t* tickets, const float* lse, const float* acc_in,
                              float* acc_out, int acc_len, float decay, int num_seqs, int mbps, int num_blocks, int Hq,
                              int Hkv, int d, int causal, float scale, int total_q, const ScoreMod& mod, cudaStream_t s,
                              const DevCtx& ctx);
@@ -968,8 +969,8 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
 // 2^(x_rt - lse_r), from the logits x that the decode kernel kept and the
 // final log-sum-exp: sequences that took the decode kernel, and those without
 // queries.  Memory bound: rows * 4 bytes a key read, 8 bytes of sums.  The sum
-// over rows runs in a fixed order.  CTA (s, hk, split): pages
-// [kAccumPages split, + kAccumPages) of the context, a half-warp per page.  The
+// over rows runs in a fixed order.  CTA (s, hk, split): every gridDim.z-th group
+// of kAccumPages pages of the context, a half-warp per page.  The
 // programmatic launch lets the CTAs find their places while the attention's
 // last kernel runs.
 constexpr int kAccumPages = 16;  // pages per CTA
@@ -981,7 +982,7 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
                                                            int window, DevCtx ctx) {
     const int s = blockIdx.x, hk = blockIdx.y, g = Hq / Hkv, lane = threadIdx.x & 31;
     const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s);
-    const int p0 = blockIdx.z * kAccumPages;
+    int p0 = blockIdx.z * kAccumPages;
     const int npages = (cl + kBS - 1) / kBS;
     const bool mine = ql <= cl && ql >= 0 && cl <= mbps * kBS && (ql == 0 || is_decode_row(ql, g)) && p0 < npages;
     if (!mine || cl > acc_len) {
@@ -1009,32 +1010,43 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
     const int blk0 = ql > 0 ? first_block(cl, ql, window) : 0;
     const long long seg = pre * Hkv + (long long)hk * (npages - blk0);  // the segment's first page of the stream
     const long row = ((long)s * Hkv + hk) * acc_len;
-    const int i = threadIdx.x & 15, p = p0 + (threadIdx.x >> 4), t = p * kBS + i;
-    const bool live = p < npages && t < cl;
+    const int i = threadIdx.x & 15;
+    float x[kDecodeRows];  // this token's logits: all loads in flight with the statistics'
+    float a = 0.f;
+    auto load = [&]() {
+        const int p = p0 + (threadIdx.x >> 4), t = p * kBS + i;
+        if (t >= cl) return;
+        if (p >= blk0) {
+            const float* src = logits + (seg + p - blk0) * logit_rows * kBS + i;
+#pragma unroll
+            for (int r = 0; r < kDecodeRows; ++r) x[r] = r < nrows ? __ldcg(src + r * kBS) : -INFINITY;
+        }
+        a = acc_in && t < cl - ql ? decay * acc_in[row + t] : 0.f;
+    };
     // inputs only so far; acc_in may be what the call before this one wrote
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float x[kDecodeRows];  // this token's logits: all loads in flight with the statistics'
-    if (live && p >= blk0) {
-        const float* src = logits + (seg + p - blk0) * logit_rows * kBS + i;
-#pragma unroll
-        for (int r = 0; r < kDecodeRows; ++r) x[r] = r < nrows ? __ldcg(src + r * kBS) : -INFINITY;
-    }
-    float a = live && acc_in && t < cl - ql ? decay * acc_in[row + t] : 0.f;
+    load();
     if (threadIdx.x < nrows) {
         const int r = threadIdx.x;
         const float L = __ldcg(lse + (q0 + r / g) * Hq + hk * g + r % g);
         neg_lse2[r] = L == -INFINITY ? 0.f : -L * kLog2ef;
     }
     __syncthreads();
-    if (!live) return;
-    if (p >= blk0) {
-        float w = 0.f;
+    while (true) {
+        const int p = p0 + (threadIdx.x >> 4), t = p * kBS + i;
+        if (t < cl) {
+            float w = 0.f;
+            if (p >= blk0) {
 #pragma unroll
-        for (int r = 0; r < kDecodeRows; ++r)
-            if (r < nrows) w += fast_exp2(x[r] + neg_lse2[r]);
-        a += w;
+                for (int r = 0; r < kDecodeRows; ++r)
+                    if (r < nrows) w += fast_exp2(x[r] + neg_lse2[r]);
+            }
+            acc_out[row + t] = a + w;
+        }
+        p0 += gridDim.z * kAccumPages;
+        if (p0 >= npages) return;
+        load();
     }
-    acc_out[row + t] = a;
 }
 
 // ------------------------------------------------------------ metadata -----
@@ -1049,7 +1061,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
                                                           int32_t* __restrict__ q_start, int32_t* __restrict__ count,
                                                           int32_t* __restrict__ list, int max_entries,
                                                           int window, const int32_t* __restrict__ prefix,
-                                                          DevCtx ctx) {
+                                                          int32_t* __restrict__ k_start, int acc_len, DevCtx ctx) {
     extern __shared__ int hist[];  // [nbins + 1]
     __shared__ int warp_sums[32];
     __shared__ int carry;
@@ -1087,6 +1099,55 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         __syncthreads();
     }
     if (threadIdx.x == 0) q_start[num_seqs] = carry;
+    // weight sums: sequences by decreasing chunk length (a counting sort over 64
+    // lengths; the order only decides who goes first), then their units of 256
+    // keys in that order (none for a sequence whose sums do not fit, which is
+    // reported, and for those without a chunk)
+    if (k_start) {
+        __shared__ int order[64];
+        int32_t* k_seq = k_start + num_seqs + 1;
+        auto rank_bin = [&](int s) { return 63 - min(63, max(0, q_lens[s]) / 32); };
+        __syncthreads();
+        if (threadIdx.x < 64) order[threadIdx.x] = 0;
+        if (threadIdx.x == 0) carry = 0;
+        __syncthreads();
+        for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) atomicAdd(&order[rank_bin(s)], 1);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int run = 0;
+            for (int b = 0; b < 64; ++b) {
+                const int c = order[b];
+                order[b] = run;
+                run += c;
+            }
+        }
+        __syncthreads();
+        for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) k_seq[atomicAdd(&order[rank_bin(s)], 1)] = s;
+        __syncthreads();
+        for (int base = 0; base < num_seqs; base += blockDim.x) {
+            const int r = base + threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+            const int s = r < num_seqs ? k_seq[r] : 0;
+            const int ql = r < num_seqs ? q_lens[s] : 0, cl = r < num_seqs ? ctx_lens[s] : 0;
+            const bool chunk = ql > 0 && !is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS;
+            if (chunk && cl > acc_len) raise_error(ctx, ERR_BOUNDS_BIT);
+            const int v = chunk && cl <= acc_len ? (cl + 255) / 256 : 0;
+            int x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) warp_sums[w] = x;
+            __syncthreads();
+            const int t = warp_sums[lane];
+            const int before = carry + __reduce_add_sync(0xffffffffu, lane < w ? t : 0) + x - v;
+            if (r < num_seqs) k_start[r] = before;
+            __syncthreads();
+            if (threadIdx.x == blockDim.x - 1) carry = before + v;
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) k_start[num_seqs] = carry;
+    }
     // histogram of entry costs
     auto entry_cost = [&](int s, int ql, int cl, int t0) {
         const int last_row = min(ql, t0 + entry_tokens) - 1;  // last query row of the entry
@@ -1115,6 +1176,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         hist[nbins] = run;
         *count = run < max_entries ? run : max_entries;
         count[1] = 0;  // the tensor-core kernel's unit tickets
+        count[2] = 0;  // and the weight sums'
     }
     __syncthreads();
     for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
@@ -1221,8 +1283,9 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
 }
 
 // Weight sums wanted by a call (fa_paged_attn_accum), and where its workspace
-// keeps the decode rows' logits: behind the attention's own, min(16, g *
-// max_q_len) rows of 16 logits for every page that the tables can hold.
+// keeps, behind the attention's own, the first unit of every chunk and the
+// decode rows' logits: min(16, g * max_q_len) rows of 16 for every page that the
+// tables can hold.
 struct AccumArgs {
     const float* in;
     float* out;
@@ -1230,13 +1293,14 @@ struct AccumArgs {
     float decay;
 };
 struct AccumWs {
-    size_t logits, total;
+    size_t k_start, logits, total;
 };
 static AccumWs accum_ws_layout(size_t base, int num_seqs, int mbps, int Hq, int Hkv, int max_q_len) {
     const int g = Hq / Hkv;
     const long rows = g <= kDecodeRows ? std::min<long>(kDecodeRows, (long)g * max_q_len) : 0;
     AccumWs a{};
-    a.logits = align256(base);
+    a.k_start = align256(base);
+    a.logits = align256(a.k_start + sizeof(int32_t) * (2 * (size_t)num_seqs + 1));
     a.total = align256(a.logits + (size_t)num_seqs * mbps * Hkv * rows * kBS * sizeof(float));
     return a;
 }
@@ -1293,7 +1357,9 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         }
         paged_meta_kernel<<<1, 1024, hist_bytes, ms>>>(ctx_lens, q_lens, num_seqs, max_blocks_per_seq, g, causal,
                                                        entry_tokens, q_start, count, list, w.max_entries,
-                                                       mod ? mod->window : 0, mod ? mod->prefix : nullptr, ctx);
+                                                       mod ? mod->window : 0, mod ? mod->prefix : nullptr,
+                                                       acc ? reinterpret_cast<int32_t*>(wsb + aw.k_start) : nullptr,
+                                                       acc ? acc->len : 0, ctx);
         const bool launched = cudaGetLastError() == cudaSuccess;
         if (ss && (cudaEventRecord(ss->join, ss->s) != cudaSuccess || !launched)) {
             (void)cudaStreamWaitEvent(s, ss->join, 0);  // leave the side stream joined
@@ -1341,7 +1407,9 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
     if (acc) {
         // rows whose queries took the decode kernel (and sequences without
         // queries), then the chunks: each sequence is one or the other
-        const dim3 grid(num_seqs, Hkv, (max_blocks_per_seq + kAccumPages - 1) / kAccumPages);
+        // (enough CTAs to fill the GPU about twice: a wide table says little about the contexts)
+        const long want = std::max<long>(1, 16L * sm_count() / ((long)num_seqs * Hkv));
+        const dim3 grid(num_seqs, Hkv, (unsigned)std::min<long>(want, (max_blocks_per_seq + kAccumPages - 1) / kAccumPages));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
         cfg.blockDim = dim3(kAccumPages * kBS);
@@ -1358,7 +1426,10 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         ++launches;
         if (tc_path) {
             st = launch_accum_chunk(q, k_cache, block_table, ctx_lens, q_lens,
-                                    reinterpret_cast<int32_t*>(wsb + w.q_start), mod->lse, acc->in, acc->out, acc->len,
+                                    reinterpret_cast<int32_t*>(wsb + w.q_start),
+                                    reinterpret_cast<int32_t*>(wsb + aw.k_start),
+                                    reinterpret_cast<int32_t*>(wsb + aw.k_start) + num_seqs + 1,
+                                    reinterpret_cast<int32_t*>(wsb + w.work_count) + 2, mod->lse, acc->in, acc->out, acc->len,
                                     acc->decay, num_seqs, max_blocks_per_seq, num_blocks, Hq, Hkv, d, causal, scale,
                                     total_q, *mod, s, ctx);
             if (st != FA_OK) return st;

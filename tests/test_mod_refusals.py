@@ -75,9 +75,11 @@ def test_accum_arguments(fattn, kw):
 def test_accum_workspace_grows_with_the_decode_rows(fattn):
     size = lambda max_q, g=2: fattn.fa_paged_attn_accum_workspace_size(2, 4, 2 * g, 2, 64, 40, max_q)
     base = fattn.fa_paged_attn_mod_workspace_size(2, 4, 4, 2, 64, 40, 1)
-    assert size(1) == base + 2 * 4 * 2 * 2 * 16 * 4
-    assert size(8) == size(30) == base + 2 * 4 * 2 * 16 * 16 * 4  # 16 rows at most
-    assert size(3, g=20) == base  # no decode rows in so wide a group
+    row = 2 * 4 * 2 * 16 * 4  # bytes of a decode row's logits over the pages that the tables hold
+    assert size(1) >= base + 2 * row
+    assert size(2) == size(1) + 2 * row and size(3) == size(1) + 4 * row
+    assert size(8) == size(30) == size(1) + 14 * row  # 16 rows at most
+    assert base < size(3, g=20) < size(1)  # no decode rows in so wide a group
     assert fattn.fa_paged_attn_mod_workspace_size(2, 4, 4, 2, 64, 40, -1) == 0
 
 
