@@ -1414,10 +1414,24 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
     }
     if (threadIdx.x == 0) starts[carry] = n;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int2 r = rows[i];
-        const int s0 = i / T * T, lo = starts[r.x] - s0;
-        rows[i] = make_int2(lo, r.y < 0 ? lo : starts[r.x + 1] - s0);
+    for (int base = threadIdx.x; base < n; base += kDocRows * blockDim.x) {  // each kind of load for all rows at once
+        int2 r[kDocRows];
+        int lo[kDocRows], hi[kDocRows];
+#pragma unroll
+        for (int k = 0; k < kDocRows; ++k) {
+            const int i = base + k * blockDim.x;
+            r[k] = i < n ? rows[i] : make_int2(0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < kDocRows; ++k) {
+            lo[k] = starts[r[k].x];
+            hi[k] = starts[r[k].x + 1];
+        }
+#pragma unroll
+        for (int k = 0; k < kDocRows; ++k) {
+            const int i = base + k * blockDim.x, s0 = i / T * T;
+            if (i < n) rows[i] = make_int2(lo[k] - s0, (r[k].y < 0 ? lo[k] : hi[k]) - s0);
+        }
     }
     __syncthreads();
     const int er = entry_tiles * kTcRows, per = (T + er - 1) / er, entries = B * per;

@@ -161,12 +161,46 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const void* __restrict
 // thread already has its first rows' values on the way; then the rows of all
 // heads of those tokens are turned 16 bytes at a time.
 constexpr int kMaxAxes = 4;
-constexpr int kMropeTokens = 4;  // tokens per CTA, at most
+constexpr int kMropeTokens = 8;  // tokens per CTA, at most
 struct PairAxes {
     uint8_t axis[64];
 };
+// 16 channels of a row as loaded: 8 from each half.
+template <bool kF32>
+struct RawPair {
+    uint4 w[kF32 ? 4 : 2];
+    __device__ __forceinline__ void load(const void* base, long lo, long hi) {
+        constexpr int size = kF32 ? 4 : 2;
+        const uint4* a = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + lo * size);
+        const uint4* b = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + hi * size);
+#pragma unroll
+        for (int i = 0; i < size / 2; ++i) {
+            w[i] = __ldg(a + i);
+            w[size / 2 + i] = __ldg(b + i);
+        }
+    }
+    __device__ __forceinline__ void values(int half, float (&x)[8]) const {
+        if constexpr (kF32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 u = w[2 * half + i];
+                x[4 * i] = __uint_as_float(u.x);
+                x[4 * i + 1] = __uint_as_float(u.y);
+                x[4 * i + 2] = __uint_as_float(u.z);
+                x[4 * i + 3] = __uint_as_float(u.w);
+            }
+        } else {
+            const uint32_t u[4] = {w[half].x, w[half].y, w[half].z, w[half].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(u[i] << 16);
+                x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+            }
+        }
+    }
+};
 template <bool kF32, int D>
-__global__ void __launch_bounds__(256) mrope_append_kernel(const void* __restrict__ q, const void* __restrict__ k,
+__global__ void __launch_bounds__(256, 4) mrope_append_kernel(const void* __restrict__ q, const void* __restrict__ k,
                                                            const void* __restrict__ v,
                                                            const int32_t* __restrict__ positions, int n_axes,
                                                            const __grid_constant__ PairAxes axes,
@@ -197,16 +231,17 @@ __global__ void __launch_bounds__(256) mrope_append_kernel(const void* __restric
     const int c = threadIdx.x % cph;
     constexpr int kStep = 256 / cph;  // rows side by side
     int row = threadIdx.x / cph;
-    float x1[8], x2[8];
-    auto load = [&](int r) {
+    auto load = [&](RawPair<kF32>& x, int r) {
+        if (r >= rows) return;
         const long tok = tok0 + r / rpt;
         const int h = r % rpt;
-        const void* base = h < Hq ? q : k;
         const long src = h < Hq ? (tok * Hq + h) * D : (tok * Hkv + (h - Hq)) * D;
-        load8<kF32>(base, src + c * 8, x1);
-        load8<kF32>(base, src + half + c * 8, x2);
+        x.load(h < Hq ? q : k, src + c * 8, src + half + c * 8);
     };
-    if (row < rows) load(row);
+    // two rows ahead (bf16), one (fp32: twice the registers a row)
+    RawPair<kF32> cur, next;
+    load(cur, row);
+    if constexpr (!kF32) load(next, row + kStep);
     for (int e = threadIdx.x; e < n * half; e += 256) {
         const int t = e / half, j = e % half;
         const int p = __ldg(positions + (long)axes.axis[j] * N + tok0 + t);
@@ -222,7 +257,18 @@ __global__ void __launch_bounds__(256) mrope_append_kernel(const void* __restric
         const bool is_q = r < Hq;
         const int slot = slot_of[t];
         const bool skip = bad[t] || (!is_q && slot < 0);
-        float y1[8], y2[8];
+        RawPair<kF32> val;
+        const long src = (tok * Hkv + (r - Hq)) * D;
+        if (!is_q && !skip) val.load(v, src + c * 8, src + half + c * 8);
+        float x1[8], x2[8], y1[8], y2[8];
+        cur.values(0, x1);
+        cur.values(1, x2);
+        if constexpr (kF32) {
+            load(cur, row + kStep);
+        } else {
+            cur = next;
+            load(next, row + 2 * kStep);
+        }
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
             const float4 co = *reinterpret_cast<const float4*>(&factors[t][c * 8 + i]);
@@ -234,7 +280,6 @@ __global__ void __launch_bounds__(256) mrope_append_kernel(const void* __restric
                 y2[i + e] = fmaf(x2[i + e], cs[e], x1[i + e] * sn[e]);
             }
         }
-        if (row + kStep < rows) load(row + kStep);
         if (skip) continue;
         if (is_q) {
             const long dst = (tok * Hq + r) * D;
@@ -242,11 +287,10 @@ __global__ void __launch_bounds__(256) mrope_append_kernel(const void* __restric
             *reinterpret_cast<uint4*>(q_out + dst + half + c * 8) = pack8(y2);
         } else {
             const int h = r - Hq;
-            const long src = (tok * Hkv + h) * D;
             const long dst = (((long)(slot / kBlock) * Hkv + h) * kBlock + (slot % kBlock)) * D;
             float v1[8], v2[8];
-            load8<kF32>(v, src + c * 8, v1);
-            load8<kF32>(v, src + half + c * 8, v2);
+            val.values(0, v1);
+            val.values(1, v2);
             *reinterpret_cast<uint4*>(kc + dst + c * 8) = pack8(y1);
             *reinterpret_cast<uint4*>(kc + dst + half + c * 8) = pack8(y2);
             *reinterpret_cast<uint4*>(vc + dst + c * 8) = pack8(v1);
@@ -607,8 +651,11 @@ fa_status fa_cache_append_mrope(const void* q, const void* k, const void* v, con
     DevCtx ctx;
     if ((st = make_ctx(&ctx)) != FA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // one token per CTA while that leaves SMs idle, more beyond
-    const int tokens = (int)std::min<long>(kMropeTokens, std::max<long>(1, N / ((long)sm_count() * 4)));
+    // all CTAs at once (four per SM) where eight tokens each allow that: a CTA's
+    // factor lookup is latency, paid once per wave (4096 tokens of 40 heads:
+    // 21 us against 24 with 4 tokens and 29 with 2)
+    const long ctas = (long)sm_count() * 4;
+    const int tokens = (int)std::min<long>(kMropeTokens, (N + ctas - 1) / ctas);
     auto kernel = in_dtype == FA_F32 ? (d == 128 ? mrope_append_kernel<true, 128> : mrope_append_kernel<true, 64>)
                                      : (d == 128 ? mrope_append_kernel<false, 128> : mrope_append_kernel<false, 64>);
     kernel<<<(N + tokens - 1) / tokens, 256, 0, s>>>(q, k, v, positions, n_axes, axes, cos_sin, max_pos,

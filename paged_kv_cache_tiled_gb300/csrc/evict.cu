@@ -352,13 +352,14 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
     DevCtx ctx;
     if ((st = make_ctx(&ctx)) != FA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // CTAs per sequence and head: as many as leave each 2048 tokens, while they
-    // all fit the GPU at once; one when the weights move inside rows too long
-    // for the registers of a cluster (a CTA must not overwrite what another has
-    // yet to read)
+    // CTAs per sequence and head: as few as keep the row in registers (a cluster's
+    // barriers and remote counts cost more than half the tokens save: rows of 4096
+    // tokens took 13 us in pairs of CTAs), while they all fit the GPU at once; one
+    // when the weights move inside rows too long for the registers of a cluster
+    // (a CTA must not overwrite what another has yet to read)
     const long rows = (long)num_seqs * Hkv, longest = std::min<long>((long)max_blocks_per_seq * kEvBlock, acc_len);
     int cluster = 1;
-    while (cluster < 8 && longest > 2048L * cluster && rows * cluster * 2 <= 2L * sm_count()) cluster *= 2;
+    while (cluster < 8 && longest > (long)kEvPass * cluster && rows * cluster * 2 <= 2L * sm_count()) cluster *= 2;
     if (acc_out == acc && longest > (long)cluster * (kEvPass - kEvItems)) cluster = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * cluster));

@@ -1013,19 +1013,22 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
     const int i = threadIdx.x & 15;
     float x[kDecodeRows];  // this token's logits: all loads in flight with the statistics'
     float a = 0.f;
-    auto load = [&]() {
-        const int p = p0 + (threadIdx.x >> 4), t = p * kBS + i;
-        if (t >= cl) return;
-        if (p >= blk0) {
-            const float* src = logits + (seg + p - blk0) * logit_rows * kBS + i;
-#pragma unroll
-            for (int r = 0; r < kDecodeRows; ++r) x[r] = r < nrows ? __ldcg(src + r * kBS) : -INFINITY;
-        }
-        a = acc_in && t < cl - ql ? decay * acc_in[row + t] : 0.f;
+    auto load_sum = [&]() {
+        const int t = (p0 + (threadIdx.x >> 4)) * kBS + i;
+        a = t < cl && acc_in && t < cl - ql ? decay * acc_in[row + t] : 0.f;
     };
-    // inputs only so far; acc_in may be what the call before this one wrote
+    auto load_logits = [&]() {
+        const int p = p0 + (threadIdx.x >> 4), t = p * kBS + i;
+        if (t >= cl || p < blk0) return;
+        const float* src = logits + (seg + p - blk0) * logit_rows * kBS + i;
+#pragma unroll
+        for (int r = 0; r < kDecodeRows; ++r) x[r] = r < nrows ? __ldcg(src + r * kBS) : -INFINITY;
+    };
+    // inputs only so far, the old sums among them: the call's first kernel began
+    // behind everything that could have written them
+    load_sum();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    load();
+    load_logits();
     if (threadIdx.x < nrows) {
         const int r = threadIdx.x;
         const float L = __ldcg(lse + (q0 + r / g) * Hq + hk * g + r % g);
@@ -1045,7 +1048,8 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
         }
         p0 += gridDim.z * kAccumPages;
         if (p0 >= npages) return;
-        load();
+        load_sum();
+        load_logits();
     }
 }
 

@@ -150,7 +150,7 @@ def _device_of(q, name: str) -> int:
     """The current device, on which q must live: a call runs on a stream of the current device."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()
     if q.get_device() != cur:
         raise ValueError(f"{name} is on {q.device}, but the current device is cuda:{cur}")
     return cur
@@ -408,7 +408,7 @@ def fa_cache_append_mrope(q, k, v, positions, pair_axes, cos_sin, k_cache, v_cac
         raise ValueError("q, k, v must all be bf16 or all fp32")
     if not isinstance(pair_axes, bytes):
         pair_axes = bytes(pair_axes)  # ValueError outside 0 .. 255
-    if len(pair_axes) != d // 2 or max(pair_axes) >= n_axes:
+    if len(pair_axes) != d // 2:  # (their range is checked by the C call)
         raise ValueError(f"pair_axes must be {d // 2} integers in [0, {n_axes})")
     if q_out is None:
         q_out = torch.empty(N, Hq, d, dtype=bf16, device=q.device)
