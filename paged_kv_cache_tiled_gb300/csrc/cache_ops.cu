@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(256, 4) mrope_append_kernel(const void* __rest
         const bool skip = bad[t] || (!is_q && slot < 0);
         RawPair<kF32> val;
         const long src = (tok * Hkv + (r - Hq)) * D;
-        if (!is_q && !skip) val.load(v, src + c * 8, src + half + c * 8);
+        if (!kF32 && !is_q && !skip) val.load(v, src + c * 8, src + half + c * 8);
         float x1[8], x2[8], y1[8], y2[8];
         cur.values(0, x1);
         cur.values(1, x2);
@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(256, 4) mrope_append_kernel(const void* __rest
             const int h = r - Hq;
             const long dst = (((long)(slot / kBlock) * Hkv + h) * kBlock + (slot % kBlock)) * D;
             float v1[8], v2[8];
+            if constexpr (kF32) val.load(v, src + c * 8, src + half + c * 8);
             val.values(0, v1);
             val.values(1, v2);
             *reinterpret_cast<uint4*>(kc + dst + c * 8) = pack8(y1);

@@ -43,23 +43,20 @@ __device__ __forceinline__ unsigned cluster_size() {
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The ints at p (an address of this CTA's shared memory) in CTA `rank` of the cluster.
-__device__ __forceinline__ int4 cluster_load4(const int* p, unsigned rank) {
-    uint32_t a;
-    int4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
+// The int at p (an address of this CTA's shared memory) in CTA `rank` of the cluster.
 __device__ __forceinline__ int cluster_load(const int* p, unsigned rank) {
     uint32_t a;
     int v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
+}
+
+// Adds v to the int at p (as above) in CTA `rank` of the cluster.
+__device__ __forceinline__ void cluster_add(int* p, unsigned rank, int v) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
 constexpr int kEvPass = kEvThreads * kEvItems;  // tokens of a scan pass
@@ -70,7 +67,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
                                                                   int dst_mbps, int keep, int recent, int sink,
                                                                   DevCtx ctx) {
     static_assert(kEvBins == 4 * kEvThreads, "a thread owns four bins");
-    __shared__ __align__(16) int hist[2][kEvBins];  // by turns, so that one cluster barrier per pass is enough
+    __shared__ __align__(16) int hist[kEvBins];  // this CTA's counts
+    // the cluster's counts, by turns, so that one cluster barrier per pass is enough (a single CTA uses hist)
+    __shared__ __align__(16) int total[2][kEvBins];
     __shared__ int2 warp_sums[32];
     __shared__ int sel_digit, sel_above, totals[2];
     // the rows' copy may be scheduled; it waits for this grid's end before it reads the list
@@ -130,11 +129,13 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
     uint32_t prefix = 0;  // digits fixed so far
     int need = want;      // tokens still to take among those that match the prefix
     const int top = kEvBins - 4 * (tid + 1);  // this thread's bins [top, top + 4): highest bins first
-    *reinterpret_cast<int4*>(&hist[0][top]) = make_int4(0, 0, 0, 0);
-    __syncthreads();
+    const int4 zero4 = make_int4(0, 0, 0, 0);
+    *reinterpret_cast<int4*>(&hist[top]) = zero4;
+    *reinterpret_cast<int4*>(&total[0][top]) = zero4;
+    if (CL > 1) cluster_sync_all();  // every CTA's counts are clear before another adds to them
+    else __syncthreads();
     for (int pass = 0; pass < 3 && want > 0; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-        int* hs = hist[pass & 1];
         for (int base = p0; base < p1; base += kEvPass) {
             if (!once) load(base + tid * kEvItems);
             if (!__any_sync(0xffffffffu, middle)) continue;
@@ -144,30 +145,26 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
                 const uint32_t digit = in ? (key[k] >> shift) & ((1u << bits) - 1) : 0xffffffffu;
                 // many tokens may hold the same weight (0): one add for the warp then
                 const bool same = __all_sync(0xffffffffu, digit == __shfl_sync(0xffffffffu, digit, 0));
-                if (in && (!same || lane == 0)) atomicAdd(&hs[digit], same ? 32 : 1);
+                if (in && (!same || lane == 0)) atomicAdd(&hist[digit], same ? 32 : 1);
             }
         }
-        if (CL > 1) cluster_sync_all();
-        else __syncthreads();
-        // the digit where the count from the top reaches `need`
-        int4 c = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        int4 c = *reinterpret_cast<const int4*>(&hist[top]);
+        *reinterpret_cast<int4*>(&hist[top]) = zero4;  // (next used behind the barriers below)
         if (CL > 1) {
-            int4 part_c[8];  // all parts' loads in flight together
+            // Few of the bins hold anything, so the counts are added to every CTA's totals
+            // (reading all bins of eight CTAs took 1.6 us a pass).
+            int* sums = total[pass & 1];
+            const int own[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-                part_c[r] = r < CL ? cluster_load4(hs + top, r) : make_int4(0, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                c.x += part_c[r].x;
-                c.y += part_c[r].y;
-                c.z += part_c[r].z;
-                c.w += part_c[r].w;
-            }
-        } else {
-            c = *reinterpret_cast<const int4*>(hs + top);
+            for (int b = 0; b < 4; ++b)
+                if (own[b])
+                    for (int r = 0; r < CL; ++r) cluster_add(&sums[top + b], r, own[b]);
+            *reinterpret_cast<int4*>(&total[(pass + 1) & 1][top]) = zero4;  // read last before the barrier of the pass before
+            cluster_sync_all();
+            c = *reinterpret_cast<const int4*>(&sums[top]);
         }
-        // the other buffer: every CTA read its counts of the pass before ahead of this pass's barrier
-        *reinterpret_cast<int4*>(&hist[(pass + 1) & 1][top]) = make_int4(0, 0, 0, 0);
+        // the digit where the count from the top reaches `need`
         const int own_c = c.x + c.y + c.z + c.w;
         int x = own_c;
 #pragma unroll
