@@ -163,7 +163,8 @@ fa_status fa_prefill_masked(const void* q, const void* k, const void* v, const f
  *     causal != 0:  j <= i, or j < prefix_lens[b]
  *     window > 0:   j > i - window, and, without causal, j < i + window
  *     doc_ids:      every position from i to j holds the same id >= 0
- *   softcap       >= 0, finite; 0: no cap
+ *   softcap       >= 0, finite; 0: no cap.  softcap * log2(e) and scale / softcap
+ *                 must be normal fp32 numbers
  *   alibi_slopes  fp32 [Hq] or NULL (no bias); any finite values
  *   window        >= 0; 0: none
  *   prefix_lens   int32 [B] or NULL; ignored without causal (everything is
@@ -175,7 +176,8 @@ fa_status fa_prefill_masked(const void* q, const void* k, const void* v, const f
  *   lse           fp32 [B, Hq, T] log-sum-exp of the visible logits, or NULL
  *   ws            needed with doc_ids only: at least
  *                 fa_prefill_mod_workspace_size(B, T) bytes, 256-byte aligned
- *                 (row ranges and tile order); contents need not be initialised
+ *                 (row ranges and tile order); contents need not be initialised.
+ *                 Calls that may overlap on the GPU need workspaces of their own
  * A query that sees no key gets output 0 and LSE -inf.  Tiles of 128 keys that
  * none of a tile's queries see are skipped; keys and values in the tiles that
  * are visited must be finite (a weight of 0 times infinity is not a number).
@@ -400,7 +402,8 @@ fa_status fa_paged_attn_mod(const void* q, const void* k_cache, const void* v_ca
  *   ws    at least fa_paged_attn_accum_workspace_size(...) bytes, with the
  *         same max_q_len: beside fa_paged_attn's, the logits of the decode rows
  *         (64 bytes per row, page and kv head that the tables can hold)
- * The sums run in a fixed order: equal inputs give equal bits.  A call without
+ * The sums run in a fixed order: equal inputs give equal bits.  Calls that may
+ * overlap on the GPU need workspaces of their own.  A call without
  * queries (total_q = 0) does nothing.  Everything else as for
  * fa_paged_attn_mod.
  */

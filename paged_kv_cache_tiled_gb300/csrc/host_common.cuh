@@ -57,6 +57,9 @@ inline fa_status make_score_mod(ScoreMod* m, float scale, float softcap, const f
     if (softcap > 0.f) {
         m->cap_in = scale / softcap;
         m->cap_out = softcap * 1.4426950408889634f;
+        // both have to be normal numbers (a bad scale is refused with the other arguments)
+        if (scale > 0.f && !(m->cap_in >= 1.17549435e-38f && m->cap_in < INFINITY && m->cap_out < INFINITY))
+            return FA_ERR_INVALID_ARG;
     }
     m->slopes = slopes;
     m->prefix = prefix;

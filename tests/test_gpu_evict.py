@@ -103,6 +103,33 @@ def test_accum_reports_short_rows(F):
     assert F.fa_get_error() == F.FA_ERR_BOUNDS
     assert (acc[0] == 5.0).all()          # too short for sequence 0: not written
     assert (acc[1, :, 50:] == 5.0).all()  # sequence 1 fits
+    p = R.Paged(21, [50, 100], [1, 40], 4, 2, 64)  # the other way round: the chunk's row is too short
+    q, kc, vc, table, ctx, ql = p.cuda()
+    acc = torch.full((2, 2, 60), 5.0, device="cuda")
+    F.fa_paged_attn_accum(q, kc, vc, table, ctx, ql, acc, acc, max_q_len=40)
+    assert F.fa_get_error() == F.FA_ERR_BOUNDS
+    assert (acc[1] == 5.0).all() and not (acc[0, :, :50] == 5.0).any()
+
+
+def test_accum_wide_tables(F):
+    """Tables and rows far wider than the contexts; one sequence ends where a unit of 256 keys does."""
+    p = R.Paged(22, [256, 40, 513, 100], [20, 1, 300, 2], 8, 2, 64)
+    p.table = torch.cat([p.table, torch.full((4, 3000), -1, dtype=torch.int32)], 1)
+    run_accum(F, p, bias=True)
+
+
+def test_accum_many_sequences(F):
+    """More sequences than a warp, of all kinds, so that places and units run over many of them."""
+    n = 70
+    ctx = [(37 * i) % 300 + 1 for i in range(n)]
+    ql = [min(c, [0, 1, 2, 9, 33][i % 5]) for i, c in enumerate(ctx)]
+    run_accum(F, R.Paged(23, ctx, ql, 4, 2, 64), window=50)
+
+
+def test_accum_long_chunk(F):
+    """One long chunk: several units per CTA, query tiles past a full ring, both row layouts."""
+    run_accum(F, R.Paged(24, [1500], [1400], 4, 2, 64), give=False)
+    run_accum(F, R.Paged(24, [900], [700], 3, 1, 128), give=False, cap=15.0)
 
 
 # ---------------------------------------------------------------------- evict

@@ -286,3 +286,89 @@ def test_paged_mod_graph_replay(F):
         torch.cuda.synchronize()
         assert torch.equal(out, w)
     assert F.fa_get_error() == F.FA_OK
+
+
+def test_prefill_mod_caps_of_all_sizes(F):
+    """The forms of the cap: scores far below it, around it, far above it, and rows whose every score is very low."""
+    for cap, std in ((1e4, 3.0), (300.0, 40.0), (60.0, 8.0), (40.0, 12.0), (30.0, 30.0), (2.0, 20.0), (0.01, 1.0)):
+        run_prefill(F, 1, 200, 2, 1, 64, cap=cap, std=std, causal=False, seed=int(cap))
+    g = torch.Generator().manual_seed(9)
+    T, d = 200, 64
+    k = torch.randn(1, T, 1, d, generator=g).abs().bfloat16()
+    q = -(torch.randn(1, T, 2, d, generator=g).abs() * 4).bfloat16()  # every score is negative
+    v = torch.randn(1, T, 1, d, generator=g).bfloat16()
+    for cap in (50.0, 30.0, 8.0):
+        lse = torch.empty(1, 2, T, device="cuda")
+        out = F.fa_prefill_mod(q.cuda(), k.cuda(), v.cuda(), softcap=cap, lse=lse)
+        pos = torch.arange(T)
+        for h in range(2):
+            ref = R.Rows(q[0, :, h], k[0, :, 0], v[0, :, 0], pos, R.visible(pos, T, True), d ** -0.5, cap)
+            R.check(lse[0, h], ref.lse, ref.lse_tol, f"lse cap {cap}")
+            R.check(out[0, :, h], ref.out, ref.out_tol, f"out cap {cap}")
+
+
+def test_prefill_mod_slopes_of_all_sizes(F):
+    """Steep slopes, none, and slopes that favour distant keys."""
+    g = torch.Generator().manual_seed(10)
+    B, T, Hq, d = 1, 300, 6, 64
+    q = torch.randn(B, T, Hq, d, generator=g).bfloat16()
+    k, v = (torch.randn(B, T, 1, d, generator=g).bfloat16() for _ in range(2))
+    sl = torch.tensor([8.0, 1.5, 0.0, 1e-4, -0.02, -0.5])
+    for kw in (dict(), dict(causal=False), dict(prefix_lens=torch.tensor([150], dtype=torch.int32).cuda())):
+        lse = torch.empty(B, Hq, T, device="cuda")
+        out = F.fa_prefill_mod(q.cuda(), k.cuda(), v.cuda(), alibi_slopes=sl.cuda(), lse=lse, **kw)
+        pos = torch.arange(T)
+        see = R.visible(pos, T, kw.get("causal", True), 0, 150 if "prefix_lens" in kw else 0)
+        for h in range(Hq):
+            ref = R.Rows(q[0, :, h], k[0, :, 0], v[0, :, 0], pos, see, d ** -0.5, 0.0, sl[h])
+            R.check(lse[0, h], ref.lse, ref.lse_tol, f"lse slope {float(sl[h])}")
+            R.check(out[0, :, h], ref.out, ref.out_tol, f"out slope {float(sl[h])}")
+
+
+def test_waits_run_out(F):
+    """Every kernel behind these calls reports a wait that runs out, and works again afterwards."""
+    p = R.Paged(14, [100, 300], [1, 60], 8, 2, 64)
+    q, kc, vc, table, ctx, ql = p.cuda()
+    acc = torch.zeros(2, 2, 300, device="cuda")
+    x = torch.randn(1, 200, 4, 64, device="cuda").bfloat16()
+    calls = [lambda: F.fa_prefill_mod(x, x, x, softcap=5.0),
+             lambda: F.fa_paged_attn_mod(q, kc, vc, table, ctx, ql, window=50, max_q_len=60),
+             lambda: F.fa_paged_attn_accum(q, kc, vc, table, ctx, ql, None, acc, max_q_len=60)]
+    want = [c() for c in calls]
+    assert F.fa_get_error() == F.FA_OK
+    F.fa_debug_set_wait_limit(2_000_000)
+    try:
+        for c in calls:
+            F.fa_debug_force_timeout(True)
+            c()
+            assert F.fa_get_error() == F.FA_ERR_TIMEOUT
+            F.fa_debug_force_timeout(False)
+            assert F.fa_get_error() == F.FA_OK
+    finally:
+        F.fa_debug_force_timeout(False)
+        F.fa_debug_set_wait_limit(4_000_000_000)
+    for c, w in zip(calls, want):
+        assert torch.equal(c(), w)
+    assert F.fa_get_error() == F.FA_OK
+
+
+def test_two_streams_at_once(F):
+    """Calls on two streams at the same time, each with buffers of its own."""
+    ps = [R.Paged(15, [300, 900], [1, 70], 8, 2, 64), R.Paged(16, [700, 50], [90, 1], 8, 2, 64)]
+    args = [p.cuda() for p in ps]
+    want = [F.fa_paged_attn_mod(*a, softcap=20.0, max_q_len=90) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(F.fa_paged_attn_mod(*args[i], softcap=20.0, max_q_len=90))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(x, w) for x in g)
+    # a stream given as an argument: the call's own workspace must outlive it there
+    out = [F.fa_paged_attn_mod(*args[0], softcap=20.0, max_q_len=90, stream=streams[0]) for _ in range(5)]
+    streams[0].synchronize()
+    assert all(torch.equal(x, want[0]) for x in out)
+    assert F.fa_get_error() == F.FA_OK

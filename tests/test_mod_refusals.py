@@ -30,6 +30,7 @@ PREFILL_OK = dict(q=D, k=D, v=D, out=D, lse=None, B=1, T=16, Hq=4, Hkv=2, d=64, 
     (dict(B=-1), "INVALID_ARG"), (dict(T=-1), "INVALID_ARG"), (dict(d=96), "UNSUPPORTED"), (dict(Hq=5), "UNSUPPORTED"),
     (dict(scale=0.0), "INVALID_ARG"), (dict(scale=float("nan")), "INVALID_ARG"), (dict(cap=-1.0), "INVALID_ARG"),
     (dict(cap=float("inf")), "INVALID_ARG"), (dict(cap=float("nan")), "INVALID_ARG"), (dict(window=-1), "INVALID_ARG"),
+    (dict(cap=3e38), "INVALID_ARG"), (dict(cap=1e-40), "INVALID_ARG"), (dict(cap=1e37, scale=1e-3), "INVALID_ARG"),
     (dict(q=None), "INVALID_ARG"), (dict(out=D + 16), "INVALID_ARG"), (dict(k=D + 2), "INVALID_ARG"),
     (dict(docs=D), "WORKSPACE"), (dict(docs=D, ws=D + 8, ws_bytes=1 << 30), "WORKSPACE"),
     (dict(docs=D, ws=D, ws_bytes=10), "WORKSPACE"), (dict(B=70000, T=70000), "UNSUPPORTED"),
