@@ -16,7 +16,9 @@
 //         [128 w, 128 w + 128) and sums the products of K tile kt with query
 //         tile `side` of every pair, while the tensor core works for the other K
 //         tile; side 1 hands its sums to side 0 at the end of a unit;
-//   16    TMA producer and ticket taker;  17  MMA issuer and TMEM owner.
+//   16    TMA producer and ticket taker;  17  MMA issuer and TMEM owner;
+//   18    looks up what the sums need of the query rows (-lse, slope, run of keys)
+//         a pair or two ahead.
 // Per logit the sum costs half a packed multiply-add, an exponential and half a
 // packed add, against two passes over the scores in the attention itself.  The
 // pace is the MMA warp's: 256 query rows per product, because eight MMAs of 128
@@ -28,9 +30,9 @@
 
 namespace fa {
 
-constexpr int kCsThreads = 576;
-constexpr int kCsProducer = 16, kCsMma = 17;
-constexpr int kCsReaders = 17;  // of a unit's mailbox: the summing warps and the MMA warp
+constexpr int kCsThreads = 608;
+constexpr int kCsProducer = 16, kCsMma = 17, kCsStats = 18;
+constexpr int kCsReaders = 18;  // of a unit's mailbox: every warp but the producer
 constexpr int kCsRows = 128;    // keys of a K tile, and query rows of a tile
 constexpr int kCsPairs = 2, kCsUnitSlots = 4;  // query pairs in flight, unit mailboxes
 constexpr float kCsLog2e = 1.4426950408889634f;
@@ -61,10 +63,9 @@ struct CsCfg {
     static constexpr int kAtomBytes = kCsRows * 128;
     static constexpr int kTileBytes = kAtoms * kAtomBytes;
     static constexpr uint32_t kGroup = kAtoms * 1024;  // 8-row groups of the K tile (halves side by side)
-    static constexpr int kBars = 3 + 2 * kCsPairs + 4 + 4 + 2 * kCsUnitSlots + 2;
-    // per summing warp and column: -lse, distance slope, run of keys seen (each
-    // warp keeps its own, so no barrier across warps is needed in the loop)
-    static constexpr int kColBytes = 16 * 3 * kCsRows * 4;
+    static constexpr int kBars = 3 + 2 * kCsPairs + 4 + 4 + 2 * kCsUnitSlots + 2 + 2 * kCsPairs;
+    // per query row of a pair: -lse, distance slope, end and first of the unit's keys seen
+    static constexpr int kColBytes = kCsPairs * 4 * 2 * kCsRows * 4;
     static constexpr int kPartBytes = 2 * kCsRows * 4;
     static constexpr int kSmem = 1024 + (2 + 2 * kCsPairs) * kTileBytes + kColBytes + kPartBytes + kBars * 8 +
                                  kCsUnitSlots * 16 + 16;
@@ -134,7 +135,9 @@ __global__ void __launch_bounds__(kCsThreads, 1)
     uint64_t* pempty = pfull + 2;         // [2] and read
     uint64_t* ufull = pempty + 2;
     uint64_t* uempty = ufull + kCsUnitSlots;
-    uint64_t* drain = uempty + kCsUnitSlots;
+    uint64_t* cfull = uempty + kCsUnitSlots;  // [kCsPairs] a pair's row statistics are in
+    uint64_t* cempty = cfull + kCsPairs;      // and read by every summing warp
+    uint64_t* drain = cempty + kCsPairs;
     uint64_t* never = drain + 1;
     volatile int4* umbox = reinterpret_cast<volatile int4*>((reinterpret_cast<uintptr_t>(never + 1) + 15) & ~uintptr_t(15));
     uint32_t* tmem_slot = const_cast<uint32_t*>(reinterpret_cast<volatile uint32_t*>(umbox + kCsUnitSlots));
@@ -146,6 +149,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
         for (int i = 0; i < kCsPairs; ++i) {
             mbar_init(&qfull[i], 1);
             mbar_init(&qempty[i], 1);
+            mbar_init(&cfull[i], 1);
+            mbar_init(&cempty[i], 16);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&kfull[k], 1);
@@ -359,13 +364,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
         if (lane == 0) umma_commit(drain);
         __syncwarp();
         (void)mbar_wait_bounded(drain, 0, 1000000000ull, nullptr);
-    } else {
-        const int w = warp >> 2, kt = w >> 1, side = w & 1, quarter = warp & 3;
-        const uint32_t trow = tbase + ((uint32_t)(quarter * 32) << 16) + w * 128;
-        float* nlse = cols + warp * 3 * kCsRows;
-        float* slope = nlse + kCsRows;
-        short2* run = reinterpret_cast<short2*>(slope + kCsRows);  // from this warp's first key
-        int sc = 0, handed = 0;  // pairs seen, sums handed over
+    } else if (warp == kCsStats) {
+        int cc = 0;  // pairs described
         for (int i = 0; ok; ++i) {
             int4 u;
             if (!next_unit(i, u)) {
@@ -374,39 +374,78 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             }
             if (u.x < 0) break;
             const CsUnit U = cs_unit(p, u.x, u.y, u.z, tt, heads);
-            if (kt >= U.nk) continue;
-            const int k_lo = U.kv0 + kt * kCsRows + quarter * 32, k_hi = min(U.cl, k_lo + 32);  // this warp's keys
-            float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            // query tile j of the unit: tile `tile` of head `head` of the group, and of the
-            // next one of this side (no divisions in the loop)
-            int tile = U.t_lo + side / heads, head = side % heads, ntile = tile, nhead = head;
-            auto advance = [&](int& t, int& h) {
-                h += 2;
-                while (h >= heads) {
-                    h -= heads;
-                    ++t;
-                }
-            };
-            // -lse (log2 units) of columns lane, lane + 32, ... of the next tile
-            const int ctok = p.pack ? lane >> p.pack_shift : lane, chead = p.pack ? lane & (p.g - 1) : 0;
-            const int cstep = p.pack ? 32 >> p.pack_shift : 32;  // tokens from column c to c + 32
-            const float* lse0 = p.lse + (long)(U.qs + ctok) * p.Hq + U.hk * p.g + chead;
-            float stat[4];
-            auto load_stats = [&](int t, int h) {
-                const int tok0 = t * tt;
-                const float* src = lse0 + (long)tok0 * p.Hq + h;
+            int tile = U.t_lo, head = 0;  // of the pair's first tile
+            for (int j = 0; j < U.n; j += 2, ++cc) {
+                const int slot = cc % kCsPairs;
+                float lse[8], sl[8];
+                int2 seen[8];
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    stat[b] = tok0 + ctok + b * cstep < U.ql ? __ldg(src + (long)b * cstep * p.Hq) : 0.f;
-            };
-            if (side < U.n) load_stats(tile, head);
-            for (int j = side; j - side < U.n; j += 2) {
-                if (j >= U.n) {  // the last pair has one tile only: side 1 lets its turn pass
-                    if (!mbar_wait_warp(&sfull[kt], sc & 1, lim_ns, abort_flag)) ok = false;
-                    if (!ok) break;
-                    ++sc;
-                    mbar_arrive(&sempty[kt]);
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int c = b * 32 + lane;
+                        const int tok = tile * tt + (p.pack ? c >> p.pack_shift : c);
+                        const int hd = U.hk * p.g + head + (p.pack ? c & (p.g - 1) : 0);
+                        const bool real = j + e < U.n && tok < U.ql;
+                        lse[4 * e + b] = real ? __ldg(p.lse + (long)(U.qs + tok) * p.Hq + hd) : 0.f;
+                        if constexpr (MOD == CS_BIAS) sl[4 * e + b] = -__ldg(p.mod.slopes + hd) * kCsLog2e;
+                        seen[4 * e + b] = real ? cs_range(p, U.pos0 + tok, U.prefix, U.cl) : make_int2(0, 0);
+                    }
+                    if (++head == heads) {
+                        head = 0;
+                        ++tile;
+                    }
+                }
+                if (!mbar_wait_warp(&cempty[slot], ((cc / kCsPairs) & 1) ^ 1, lim_ns, abort_flag)) {
+                    ok = false;
                     break;
+                }
+                float* nlse = cols + slot * 4 * 2 * kCsRows;
+                float* slope = nlse + 2 * kCsRows;
+                int* end = reinterpret_cast<int*>(slope + 2 * kCsRows);
+                int* first = end + 2 * kCsRows;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int c = k * 32 + lane;
+                    nlse[c] = lse[k] == -INFINITY ? 0.f : -lse[k] * kCsLog2e;
+                    if constexpr (MOD == CS_BIAS) slope[c] = sl[k];
+                    end[c] = seen[k].y;
+                    first[c] = seen[k].x;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cfull[slot]);
+            }
+        }
+        if (!ok && lane == 0) fail();
+    } else {
+        const int w = warp >> 2, kt = w >> 1, side = w & 1, quarter = warp & 3;
+        const uint32_t trow = tbase + ((uint32_t)(quarter * 32) << 16) + w * 128;
+        int sc = 0, cc = 0, handed = 0;  // products seen, pairs seen, sums handed over
+        for (int i = 0; ok; ++i) {
+            int4 u;
+            if (!next_unit(i, u)) {
+                ok = false;
+                break;
+            }
+            if (u.x < 0) break;
+            const CsUnit U = cs_unit(p, u.x, u.y, u.z, tt, heads);
+            const int k_rel = kt * kCsRows + quarter * 32;  // this warp's keys within the unit
+            const int k_lo = U.kv0 + k_rel, k_hi = min(U.cl, k_lo + 32), key = k_lo + lane;
+            float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            int tile = U.t_lo + side / heads, head = side % heads;
+            for (int j = side; j - side < U.n; j += 2, ++cc) {
+                const int slot = cc % kCsPairs;
+                if (!mbar_wait_warp(&cfull[slot], (cc / kCsPairs) & 1, lim_ns, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                auto done = [&]() {  // the pair's statistics are read
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&cempty[slot]);
+                };
+                if (kt >= U.nk) {  // no such K tile
+                    done();
+                    continue;
                 }
                 const int tok0 = tile * tt;
                 // Warp-uniform: does every row of the tile exist and see every key of this warp
@@ -414,23 +453,11 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 const int2 rf = cs_range(p, U.pos0 + tok0, U.prefix, U.cl);
                 const int2 rl = cs_range(p, U.pos0 + min(U.ql, tok0 + tt) - 1, U.prefix, U.cl);
                 const bool plain = tok0 + tt <= U.ql && k_lo >= rl.x && k_hi <= rf.y;
-                const bool none = k_lo >= rl.y || k_hi <= rf.x;
-                __syncwarp();
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int c = b * 32 + lane;
-                    nlse[c] = stat[b] == -INFINITY ? 0.f : -stat[b] * kCsLog2e;
-                    if constexpr (MOD == CS_BIAS)
-                        slope[c] = -__ldg(p.mod.slopes + U.hk * p.g + head + chead) * kCsLog2e;
-                    if (!plain) {
-                        const int tok = tok0 + ctok + b * cstep;
-                        const int2 seen = tok < U.ql ? cs_range(p, U.pos0 + tok, U.prefix, U.cl) : make_int2(0, 0);
-                        run[c] = make_short2((short)min(32, max(0, seen.x - k_lo)), (short)min(32, max(0, seen.y - k_lo)));
-                    }
-                }
-                __syncwarp();
-                advance(ntile, nhead);
-                if (j + 2 < U.n) load_stats(ntile, nhead);
+                const bool none = j >= U.n || k_lo >= rl.y || k_hi <= rf.x;  // (a last pair may have one tile)
+                const float* nlse = cols + slot * 4 * 2 * kCsRows + side * kCsRows;
+                const float* slope = nlse + 2 * kCsRows;
+                const int* end = reinterpret_cast<const int*>(slope + 2 * kCsRows);
+                const int* first = end + 2 * kCsRows;
                 if (!mbar_wait_warp(&sfull[kt], sc & 1, lim_ns, abort_flag)) {
                     ok = false;
                     break;
@@ -438,7 +465,9 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 ++sc;
                 tc_fence_after();
                 // 32 columns at a time, the next ones on their way while these are summed;
-                // `masked`: some row of the tile is not real or does not see some key
+                // `masked`: 1 some row of the tile is not real or does not see some key, 2 and runs may begin
+                // behind the first key.  Row ends come four at a time: packed into one word per row
+                // their unpacking took a masked tile from 1800 cycles to 8000.
                 auto columns = [&](auto masked) {
                     constexpr int kAhead = MOD == CS_PLAIN ? 1 : 0;  // (registers: 96 a thread)
                     uint32_t raw[1 + kAhead][32];
@@ -457,6 +486,10 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                         for (int jj = 0; jj < 32; jj += 4) {
                             const float4 nl = *reinterpret_cast<const float4*>(nlse + b * 32 + jj);
                             const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
+                            int4 he = make_int4(0, 0, 0, 0), fe = he;
+                            if constexpr (decltype(masked)::value >= 1) he = *reinterpret_cast<const int4*>(end + b * 32 + jj);
+                            if constexpr (decltype(masked)::value == 2)
+                                fe = *reinterpret_cast<const int4*>(first + b * 32 + jj);
 #pragma unroll
                             for (int e = 0; e < 4; e += 2) {
                                 const int c = b * 32 + jj + e;
@@ -476,10 +509,13 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                                     x.y = fmaf(sl.y, fabsf((float)(d0 - (p.pack ? (c + 1) >> p.pack_shift : c + 1))), x.y);
                                 }
                                 float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                                if constexpr (decltype(masked)::value) {
-                                    const short2 ra = run[c], rb = run[c + 1];
-                                    pr.x = lane >= ra.x && lane < ra.y ? pr.x : 0.f;
-                                    pr.y = lane >= rb.x && lane < rb.y ? pr.y : 0.f;
+                                if constexpr (decltype(masked)::value >= 1) {
+                                    pr.x = key < (e ? he.z : he.x) ? pr.x : 0.f;
+                                    pr.y = key < (e ? he.w : he.y) ? pr.y : 0.f;
+                                }
+                                if constexpr (decltype(masked)::value == 2) {
+                                    pr.x = key >= (e ? fe.z : fe.x) ? pr.x : 0.f;
+                                    pr.y = key >= (e ? fe.w : fe.y) ? pr.y : 0.f;
                                 }
                                 sum[(c >> 1) & 3] = __fadd2_rn(sum[(c >> 1) & 3], pr);
                             }
@@ -489,14 +525,17 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 if (none) {
                     mbar_arrive(&sempty[kt]);
                 } else if (plain) {
-                    columns(std::false_type{});
+                    columns(std::integral_constant<int, 0>{});
+                } else if (p.mod.window == 0) {
+                    columns(std::integral_constant<int, 1>{});
                 } else {
-                    columns(std::true_type{});
+                    columns(std::integral_constant<int, 2>{});
                 }
-                tile = ntile;
-                head = nhead;
+                done();
+                for (head += 2; head >= heads; head -= heads) ++tile;
             }
             if (!ok) break;
+            if (kt >= U.nk) continue;
             const float mine =
                 ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
             float* at = part + kt * kCsRows + quarter * 32 + lane;
@@ -514,7 +553,6 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 }
                 const float odd = *at;
                 mbar_arrive(&pempty[kt]);
-                const int key = k_lo + lane;
                 if (key < U.cl) {
                     const long o = ((long)U.seq * p.Hkv + U.hk) * p.acc_len + key;
                     const float old = p.acc_in && key < U.pos0 ? p.decay * p.acc_in[o] : 0.f;

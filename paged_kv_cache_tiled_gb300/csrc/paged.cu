@@ -1411,8 +1411,8 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
     if (acc) {
         // rows whose queries took the decode kernel (and sequences without
         // queries), then the chunks: each sequence is one or the other
-        // (enough CTAs to fill the GPU about twice: a wide table says little about the contexts)
-        const long want = std::max<long>(1, 16L * sm_count() / ((long)num_seqs * Hkv));
+        // (about one wave of CTAs: a wide table says little about the contexts)
+        const long want = std::max<long>(1, 8L * sm_count() / ((long)num_seqs * Hkv));
         const dim3 grid(num_seqs, Hkv, (unsigned)std::min<long>(want, (max_blocks_per_seq + kAccumPages - 1) / kAccumPages));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
