@@ -54,6 +54,7 @@ struct ColsumParams {
     int num_seqs, Hq, Hkv, g, pack, pack_shift, mbps, num_blocks, causal;
     float scale_log2;
     ScoreMod mod;
+    CapPoly cap;
     DevCtx ctx;
 };
 
@@ -64,8 +65,10 @@ struct CsCfg {
     static constexpr int kTileBytes = kAtoms * kAtomBytes;
     static constexpr uint32_t kGroup = kAtoms * 1024;  // 8-row groups of the K tile (halves side by side)
     static constexpr int kBars = 3 + 2 * kCsPairs + 4 + 4 + 2 * kCsUnitSlots + 2 + 2 * kCsPairs;
-    // per query row of a pair: -lse, distance slope, end and first of the unit's keys seen
-    static constexpr int kColBytes = kCsPairs * 4 * 2 * kCsRows * 4;
+    // per query row of a pair: -lse, distance slope, end and first of the keys
+    // seen, position from the unit's first key; then the largest -lse of each tile
+    static constexpr int kColArrays = 5;
+    static constexpr int kColBytes = kCsPairs * (kColArrays * 2 * kCsRows + 4) * 4;
     static constexpr int kPartBytes = 2 * kCsRows * 4;
     static constexpr int kSmem = 1024 + (2 + 2 * kCsPairs) * kTileBytes + kColBytes + kPartBytes + kBars * 8 +
                                  kCsUnitSlots * 16 + 16;
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             int tile = U.t_lo, head = 0;  // of the pair's first tile
             for (int j = 0; j < U.n; j += 2, ++cc) {
                 const int slot = cc % kCsPairs;
-                float lse[8], sl[8];
+                float lse[8], sl[8], at[8];
                 int2 seen[8];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -388,7 +391,10 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                         const int hd = U.hk * p.g + head + (p.pack ? c & (p.g - 1) : 0);
                         const bool real = j + e < U.n && tok < U.ql;
                         lse[4 * e + b] = real ? __ldg(p.lse + (long)(U.qs + tok) * p.Hq + hd) : 0.f;
-                        if constexpr (MOD == CS_BIAS) sl[4 * e + b] = -__ldg(p.mod.slopes + hd) * kCsLog2e;
+                        if constexpr (MOD == CS_BIAS) {
+                            sl[4 * e + b] = -__ldg(p.mod.slopes + hd) * kCsLog2e;
+                            at[4 * e + b] = (float)(U.pos0 + tok - U.kv0);
+                        }
                         seen[4 * e + b] = real ? cs_range(p, U.pos0 + tok, U.prefix, U.cl) : make_int2(0, 0);
                     }
                     if (++head == heads) {
@@ -400,17 +406,32 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                     ok = false;
                     break;
                 }
-                float* nlse = cols + slot * 4 * 2 * kCsRows;
+                float* nlse = cols + slot * (C::kColArrays * 2 * kCsRows + 4);
                 float* slope = nlse + 2 * kCsRows;
                 int* end = reinterpret_cast<int*>(slope + 2 * kCsRows);
                 int* first = end + 2 * kCsRows;
+                float* rel = reinterpret_cast<float*>(first + 2 * kCsRows);
+                float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int c = k * 32 + lane;
-                    nlse[c] = lse[k] == -INFINITY ? 0.f : -lse[k] * kCsLog2e;
-                    if constexpr (MOD == CS_BIAS) slope[c] = sl[k];
+                    const float nl = lse[k] == -INFINITY ? 0.f : -lse[k] * kCsLog2e;
+                    nlse[c] = nl;
+                    if (seen[k].y > 0) most[k >> 2] = fmaxf(most[k >> 2], nl);  // (rows that exist)
+                    if constexpr (MOD == CS_BIAS) {
+                        slope[c] = sl[k];
+                        rel[c] = at[k];
+                    }
                     end[c] = seen[k].y;
                     first[c] = seen[k].x;
+                }
+                if constexpr (MOD == CS_CAP) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) most[e] = fmaxf(most[e], __shfl_xor_sync(0xffffffffu, most[e], o));
+                        if (lane == 0) rel[2 * kCsRows + e] = most[e];
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&cfull[slot]);
@@ -431,6 +452,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             const CsUnit U = cs_unit(p, u.x, u.y, u.z, tt, heads);
             const int k_rel = kt * kCsRows + quarter * 32;  // this warp's keys within the unit
             const int k_lo = U.kv0 + k_rel, k_hi = min(U.cl, k_lo + 32), key = k_lo + lane;
+            [[maybe_unused]] const float key_rel = (float)(k_rel + lane);  // from the unit's first key
             float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             int tile = U.t_lo + side / heads, head = side % heads;
             for (int j = side; j - side < U.n; j += 2, ++cc) {
@@ -454,10 +476,14 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 const int2 rl = cs_range(p, U.pos0 + min(U.ql, tok0 + tt) - 1, U.prefix, U.cl);
                 const bool plain = tok0 + tt <= U.ql && k_lo >= rl.x && k_hi <= rf.y;
                 const bool none = j >= U.n || k_lo >= rl.y || k_hi <= rf.x;  // (a last pair may have one tile)
-                const float* nlse = cols + slot * 4 * 2 * kCsRows + side * kCsRows;
+                const float* nlse = cols + slot * (C::kColArrays * 2 * kCsRows + 4) + side * kCsRows;
                 const float* slope = nlse + 2 * kCsRows;
                 const int* end = reinterpret_cast<const int*>(slope + 2 * kCsRows);
                 const int* first = end + 2 * kCsRows;
+                const float* rel = reinterpret_cast<const float*>(first + 2 * kCsRows);
+                // CapPoly's slack: the smallest lse of the tile stands for the running max
+                [[maybe_unused]] float low = 0.f;
+                if constexpr (MOD == CS_CAP) low = -rel[2 * kCsRows - side * (kCsRows - 1)];
                 if (!mbar_wait_warp(&sfull[kt], sc & 1, lim_ns, abort_flag)) {
                     ok = false;
                     break;
@@ -482,43 +508,71 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                             tc_fence_before();
                             mbar_arrive(&sempty[kt]);
                         }
+                        [[maybe_unused]] int tier = 2;
+                        if constexpr (MOD == CS_CAP) {
+                            float mz[2] = {0.f, 0.f};
 #pragma unroll
-                        for (int jj = 0; jj < 32; jj += 4) {
-                            const float4 nl = *reinterpret_cast<const float4*>(nlse + b * 32 + jj);
-                            const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
-                            int4 he = make_int4(0, 0, 0, 0), fe = he;
-                            if constexpr (decltype(masked)::value >= 1) he = *reinterpret_cast<const int4*>(end + b * 32 + jj);
-                            if constexpr (decltype(masked)::value == 2)
-                                fe = *reinterpret_cast<const int4*>(first + b * 32 + jj);
+                            for (int jj = 0; jj < 32; jj += 2)
+                                mz[(jj >> 1) & 1] = fmax3f(mz[(jj >> 1) & 1], __uint_as_float(raw[0][jj]),
+                                                           __uint_as_float(raw[0][jj + 1]));
+                            const float z = fmaxf(mz[0], mz[1]);
+                            if (__all_sync(0xffffffffu, z <= p.cap.near_max && low + p.cap.near_slack >= 30.f)) tier = 0;
+                            else if (__all_sync(0xffffffffu, z <= p.cap.unit_max && low + p.cap.unit_slack >= 30.f)) tier = 1;
+                        }
+                        auto sum_block = [&](auto form) {
 #pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                const int c = b * 32 + jj + e;
-                                float2 x = make_float2(__uint_as_float(raw[b & kAhead][jj + e]),
-                                                       __uint_as_float(raw[b & kAhead][jj + e + 1]));
-                                const float2 l2 = make_float2(nls[e], nls[e + 1]);
-                                if (MOD == CS_CAP || (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
-                                    x.x = fmaf(p.mod.cap_out, tanh_f32(x.x * p.mod.cap_in), l2.x);
-                                    x.y = fmaf(p.mod.cap_out, tanh_f32(x.y * p.mod.cap_in), l2.y);
-                                } else {
-                                    x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), l2);
+                            for (int jj = 0; jj < 32; jj += 4) {
+                                const float4 nl = *reinterpret_cast<const float4*>(nlse + b * 32 + jj);
+                                const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
+                                [[maybe_unused]] int4 he = make_int4(0, 0, 0, 0), fe = he;
+                                if constexpr (decltype(masked)::value >= 1) he = *reinterpret_cast<const int4*>(end + b * 32 + jj);
+                                if constexpr (decltype(masked)::value == 2)
+                                    fe = *reinterpret_cast<const int4*>(first + b * 32 + jj);
+#pragma unroll
+                                for (int e = 0; e < 4; e += 2) {
+                                    const int c = b * 32 + jj + e;
+                                    float2 x = make_float2(__uint_as_float(raw[b & kAhead][jj + e]),
+                                                           __uint_as_float(raw[b & kAhead][jj + e + 1]));
+                                    const float2 l2 = make_float2(nls[e], nls[e + 1]);
+                                    if constexpr (MOD == CS_CAP && decltype(form)::value < 2) {
+                                        constexpr int top = decltype(form)::value == 0 ? 4 : 6;
+                                        const float2* co = decltype(form)::value == 0 ? p.cap.near : p.cap.unit;
+                                        const float2 q2 = __fmul2_rn(x, x);
+                                        float2 t = __ffma2_rn(co[top], q2, co[top - 1]);
+#pragma unroll
+                                        for (int k = top - 2; k >= 0; --k) t = __ffma2_rn(t, q2, co[k]);
+                                        x = __ffma2_rn(x, t, l2);
+                                    } else if (MOD == CS_CAP || (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
+                                        x.x = fmaf(p.mod.cap_out, tanh_f32(x.x * p.mod.cap_in), l2.x);
+                                        x.y = fmaf(p.mod.cap_out, tanh_f32(x.y * p.mod.cap_in), l2.y);
+                                    } else {
+                                        x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), l2);
+                                    }
+                                    if constexpr (MOD == CS_BIAS) {
+                                        const float2 sl = *reinterpret_cast<const float2*>(slope + c);
+                                        const float2 at = *reinterpret_cast<const float2*>(rel + c);
+                                        x.x = fmaf(sl.x, fabsf(key_rel - at.x), x.x);
+                                        x.y = fmaf(sl.y, fabsf(key_rel - at.y), x.y);
+                                    }
+                                    float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                                    if constexpr (decltype(masked)::value >= 1) {
+                                        pr.x = key < (e ? he.z : he.x) ? pr.x : 0.f;
+                                        pr.y = key < (e ? he.w : he.y) ? pr.y : 0.f;
+                                    }
+                                    if constexpr (decltype(masked)::value == 2) {
+                                        pr.x = key >= (e ? fe.z : fe.x) ? pr.x : 0.f;
+                                        pr.y = key >= (e ? fe.w : fe.y) ? pr.y : 0.f;
+                                    }
+                                    sum[(c >> 1) & 3] = __fadd2_rn(sum[(c >> 1) & 3], pr);
                                 }
-                                if constexpr (MOD == CS_BIAS) {
-                                    const float2 sl = *reinterpret_cast<const float2*>(slope + c);
-                                    const int d0 = k_lo + lane - U.pos0 - tok0;
-                                    x.x = fmaf(sl.x, fabsf((float)(d0 - (p.pack ? c >> p.pack_shift : c))), x.x);
-                                    x.y = fmaf(sl.y, fabsf((float)(d0 - (p.pack ? (c + 1) >> p.pack_shift : c + 1))), x.y);
-                                }
-                                float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                                if constexpr (decltype(masked)::value >= 1) {
-                                    pr.x = key < (e ? he.z : he.x) ? pr.x : 0.f;
-                                    pr.y = key < (e ? he.w : he.y) ? pr.y : 0.f;
-                                }
-                                if constexpr (decltype(masked)::value == 2) {
-                                    pr.x = key >= (e ? fe.z : fe.x) ? pr.x : 0.f;
-                                    pr.y = key >= (e ? fe.w : fe.y) ? pr.y : 0.f;
-                                }
-                                sum[(c >> 1) & 3] = __fadd2_rn(sum[(c >> 1) & 3], pr);
                             }
+                        };
+                        if constexpr (MOD == CS_CAP) {
+                            if (tier == 0) sum_block(std::integral_constant<int, 0>{});
+                            else if (tier == 1) sum_block(std::integral_constant<int, 1>{});
+                            else sum_block(std::integral_constant<int, 2>{});
+                        } else {
+                            sum_block(std::integral_constant<int, 2>{});
                         }
                     }
                 };
@@ -615,6 +669,7 @@ fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* 
     p.causal = causal;
     p.scale_log2 = scale * kCsLog2e;
     p.mod = mod;
+    if (mod.cap_out > 0.f) p.cap = cap_poly(mod);
     p.ctx = ctx;
     const int grid = sm_count();
     auto go = [&](auto dim) {

@@ -588,6 +588,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         *abort_flag = 0;
         mbar_fence_init();
     }
+    // documents: launched while their ranges are still being found (griddepcontrol.wait
+    // returns at once for any other launch)
+    if constexpr (MOD != 0 && MODE == MODE_DENSE)
+        if (warp == kProducerWarp) asm volatile("griddepcontrol.wait;" ::: "memory");
     // The producer's first lane owns the Q barriers' set-up and requests the
     // first unit's Q tiles before the set-up barrier, so that their copies
     // overlap the TMEM allocation and the barrier itself.
@@ -636,6 +640,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if constexpr (MOD != 0 && MODE == MODE_DENSE) asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tbase = *tmem_slot;
 
     int num_units;
@@ -1370,6 +1375,7 @@ constexpr int kDocRows = 8;  // consecutive ids per thread and pass
 __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restrict__ ids, int B, int T, int entry_tiles,
                                                          int2* rows, int* starts, int32_t* __restrict__ order,
                                                          TcParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the attention waits for this grid's end
     extern __shared__ int hist[];  // [nbins + 1]
     __shared__ int warp_sums[32];
     const int n = B * T, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -1473,6 +1479,19 @@ static fa_status launch_tc(const CUtensorMap& tq, const CUtensorMap& tk, const C
                            int grid, cudaStream_t s, const TcSched& sched) {
     const fa_status st = raise_dynamic_smem(reinterpret_cast<const void*>(attn_tc_kernel<D, MODE, MOD>), TcCfg<D>::kSmem);
     if (st != FA_OK) return st;
+    if (MODE == MODE_DENSE && p.doc_rows) {  // its set-up overlaps the kernel that finds the ranges
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(kTcThreads);
+        cfg.dynamicSmemBytes = TcCfg<D>::kSmem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cuda_status(cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, MODE, MOD>, tq, tk, tv, p, sched));
+    }
     attn_tc_kernel<D, MODE, MOD><<<grid, kTcThreads, TcCfg<D>::kSmem, s>>>(tq, tk, tv, p, sched);
     return cuda_status(cudaGetLastError());
 }
@@ -1484,33 +1503,6 @@ static fa_status launch_tc_d(int d, const CUtensorMap& tq, const CUtensorMap& tk
     const TcSched& sc = sched ? *sched : kNone;
     return d == 128 ? launch_tc<128, MODE, MOD>(tq, tk, tv, p, grid, s, sc)
                     : launch_tc<64, MODE, MOD>(tq, tk, tv, p, grid, s, sc);
-}
-
-static CapPoly cap_poly(const ScoreMod& m) {
-    CapPoly c{};
-    const double in = m.cap_in, out = m.cap_out;
-    const double near[5] = {kTanhD0, kTanhD1, kTanhD2, kTanhD3, kTanhD4};
-    const double unit[7] = {kTanhC0, kTanhC1, kTanhC2, kTanhC3, kTanhC4, kTanhC5, kTanhC6};
-    // the last coefficients may be subnormal: 1e-41 still carries 13 bits, more
-    // than the 1e-3 that they add to the result needs
-    auto fits = [](float x) { return std::fabs(x) > 1e-41f && std::fabs(x) < 1e30f; };
-    bool near_fits = true, unit_fits = true;
-    double f = out * in;
-    for (int k = 0; k < 7; ++k, f *= in * in) {
-        const float u = (float)(unit[k] * f);
-        c.unit[k] = make_float2(u, u);
-        unit_fits &= fits(u);
-        if (k < 5) {
-            const float n = (float)(near[k] * f);
-            c.near[k] = make_float2(n, n);
-            near_fits &= fits(n);
-        }
-    }
-    c.near_max = (float)(kTanhNear / in);
-    c.unit_max = (float)(1.0 / in);
-    c.near_slack = near_fits ? (float)(out * std::tanh(0.6)) : -INFINITY;
-    c.unit_slack = unit_fits ? (float)(out * std::tanh(1.0)) : -INFINITY;
-    return c;
 }
 
 // The variant that a call's score modifiers ask for (p.mod is set).

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "common.cuh"
 
 namespace fa {
@@ -66,6 +68,34 @@ inline fa_status make_score_mod(ScoreMod* m, float scale, float softcap, const f
     m->window = window < (1 << 29) ? window : (1 << 29);
     m->lse = lse;
     return FA_OK;
+}
+
+// The polynomial forms of a call's cap (m.cap_out > 0).
+inline CapPoly cap_poly(const ScoreMod& m) {
+    CapPoly c{};
+    const double in = m.cap_in, out = m.cap_out;
+    const double near[5] = {kTanhD0, kTanhD1, kTanhD2, kTanhD3, kTanhD4};
+    const double unit[7] = {kTanhC0, kTanhC1, kTanhC2, kTanhC3, kTanhC4, kTanhC5, kTanhC6};
+    // the last coefficients may be subnormal: 1e-41 still carries 13 bits, more
+    // than the 1e-3 that they add to the result needs
+    auto fits = [](float x) { return std::fabs(x) > 1e-41f && std::fabs(x) < 1e30f; };
+    bool near_fits = true, unit_fits = true;
+    double f = out * in;
+    for (int k = 0; k < 7; ++k, f *= in * in) {
+        const float u = (float)(unit[k] * f);
+        c.unit[k] = make_float2(u, u);
+        unit_fits &= fits(u);
+        if (k < 5) {
+            const float n = (float)(near[k] * f);
+            c.near[k] = make_float2(n, n);
+            near_fits &= fits(n);
+        }
+    }
+    c.near_max = (float)(kTanhNear / in);
+    c.unit_max = (float)(1.0 / in);
+    c.near_slack = near_fits ? (float)(out * std::tanh(0.6)) : -INFINITY;
+    c.unit_slack = unit_fits ? (float)(out * std::tanh(1.0)) : -INFINITY;
+    return c;
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -126,6 +126,11 @@ def test_accum_many_sequences(F):
     run_accum(F, R.Paged(23, ctx, ql, 4, 2, 64), window=50)
 
 
+@pytest.mark.parametrize("cap, std", [(1e4, 3.0), (300.0, 40.0), (60.0, 8.0), (40.0, 12.0), (30.0, 30.0), (2.0, 20.0)])
+def test_accum_caps_of_all_sizes(F, cap, std):
+    run_accum(F, R.Paged(25, [300, 200, 77], [200, 9, 1], 4, 2, 64, std=std), cap=cap)
+
+
 def test_accum_long_chunk(F):
     """One long chunk: several units per CTA, query tiles past a full ring, both row layouts."""
     run_accum(F, R.Paged(24, [1500], [1400], 4, 2, 64), give=False)
