@@ -63,7 +63,7 @@ constexpr int kTcRows = 128;  // rows of a Q tile and of a KV tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;
-// Paged mode hands out work units at run time: the producer takes a ticket
+// Paged mode, and dense mode with documents, hand out work units at run time: the producer takes a ticket
 // from a counter in the workspace (zeroed by the metadata kernel before every
 // launch) when it starts a unit, and passes the unit to the MMA and softmax
 // warps through a ring of kUnitSlots mailboxes.
@@ -504,14 +504,13 @@ __device__ __noinline__ float modified_logits_row(uint32_t taddr, int vlo, int v
     return fmaxf(mx0, mx1);
 }
 
-// The i-th unit of this CTA as the MMA and softmax warps see it: in paged mode
+// The i-th unit of this CTA as the MMA and softmax warps see it: with tickets
 // the one the producer published in mailbox i % kUnitSlots (false if the wait
 // gave up), otherwise the static order.
-template <int MODE>
-__device__ __forceinline__ bool reader_unit(int i, int& u, const TcSched& sched, int G, int num_units,
+__device__ __forceinline__ bool reader_unit(bool tickets, int i, int& u, const TcSched& sched, int G, int num_units,
                                             uint64_t* ufull, uint64_t* uempty, volatile int* umbox,
                                             unsigned long long lim_ns, volatile int* abort_flag) {
-    if constexpr (MODE == MODE_PAGED) {
+    if (tickets) {
         const int k = i % kUnitSlots;
         if (!mbar_wait_warp(&ufull[k], (i / kUnitSlots) & 1, lim_ns, abort_flag)) return false;
         int v = 0;
@@ -571,6 +570,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int* umbox = abort_flag + 1;  // [kUnitSlots]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // units handed out at run time (known at compile time but for modified dense variants)
+    const bool tickets = MODE == MODE_PAGED || (MOD != 0 && MODE == MODE_DENSE && p.doc_order);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         else
             n0 = p.num_units;
         const int u0 = cta_unit(sched, 0, gridDim.x, n0);
-        if constexpr (MODE == MODE_PAGED) {  // the first unit is this CTA's own: published at once
+        if (tickets) {  // the first unit is this CTA's own: published at once
             umbox[0] = u0;
             mbar_arrive(&ufull[0]);
         }
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool held = true;
         for (int i = 0; ok; ++i) {
             int u;
-            if constexpr (MODE == MODE_PAGED) {
+            if (tickets) {
                 // after its first unit a CTA takes the next unit in the longest-first
                 // order that no CTA has taken yet, and hands it to the other warps
                 u = cta_unit(sched, 0, G, num_units);
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
         for (int i = 0; ok; ++i) {
             int u;
-            if (!reader_unit<MODE>(i, u, sched, G, num_units, ufull, uempty, umbox, lim_ns, abort_flag)) {
+            if (!reader_unit(tickets, i, u, sched, G, num_units, ufull, uempty, umbox, lim_ns, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -967,7 +968,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = !p.ctx.force_timeout || mbar_wait_warp(never, 0, lim_ns, abort_flag);
         for (int i = 0; ok; ++i) {
             int u;
-            if (!reader_unit<MODE>(i, u, sched, G, num_units, ufull, uempty, umbox, lim_ns, abort_flag)) {
+            if (!reader_unit(tickets, i, u, sched, G, num_units, ufull, uempty, umbox, lim_ns, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -1374,7 +1375,8 @@ fa_status launch_mask_classify(const float* M, int Tq, int Tk, uint8_t* cls, uin
 constexpr int kDocRows = 8;  // consecutive ids per thread and pass
 __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restrict__ ids, int B, int T, int entry_tiles,
                                                          int2* rows, int* starts, int32_t* __restrict__ order,
-                                                         TcParams p) {
+                                                         int32_t* __restrict__ count, TcParams p) {
+    if (threadIdx.x == 0) count[1] = 0;  // the attention's unit tickets
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the attention waits for this grid's end
     extern __shared__ int hist[];  // [nbins + 1]
     __shared__ int warp_sums[32];
@@ -1823,7 +1825,7 @@ fa_status fa_prefill_masked(const void* q, const void* k, const void* v, const f
 size_t fa_prefill_mod_workspace_size(int B, int T) {
     if (B <= 0 || T <= 0) return 0;
     const size_t n = (size_t)B * T, nt = (size_t)(T + kTcRows - 1) / kTcRows;
-    return align256(n * sizeof(int2)) + align256((n + 1) * sizeof(int32_t)) + align256(B * nt * sizeof(int32_t));
+    return align256(n * sizeof(int2)) + align256((n + 1) * sizeof(int32_t)) + align256(B * nt * sizeof(int32_t)) + 256;
 }
 
 fa_status fa_prefill_mod(const void* q, const void* k, const void* v, void* out, float* lse, int B, int T, int Hq,
@@ -1860,14 +1862,16 @@ fa_status fa_prefill_mod(const void* q, const void* k, const void* v, void* out,
         int2* rows = reinterpret_cast<int2*>(wsb);
         int* starts = reinterpret_cast<int*>(wsb + align256((size_t)B * T * sizeof(int2)));
         int32_t* order = starts + align256(((size_t)B * T + 1) * sizeof(int32_t)) / sizeof(int32_t);
+        int32_t* count = order + align256((size_t)B * nt * sizeof(int32_t)) / sizeof(int32_t);
         if (hist_bytes > 48 * 1024 &&
             (st = raise_dynamic_smem(reinterpret_cast<const void*>(doc_order_kernel), (int)hist_bytes)) != FA_OK)
             return st;
-        doc_order_kernel<<<1, 1024, hist_bytes, s>>>(doc_ids, B, T, p.pair_heads ? 1 : 2, rows, starts, order, p);
+        doc_order_kernel<<<1, 1024, hist_bytes, s>>>(doc_ids, B, T, p.pair_heads ? 1 : 2, rows, starts, order, count, p);
         if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
         ++launches;
         p.doc_rows = rows;
         p.doc_order = order;
+        p.work_count = count;
     }
     const int grid = std::min(p.num_units, sm_count());
     // unit costs are those of the plain causal problem when only the scores are modified
