@@ -445,7 +445,7 @@ fa_status fa_paged_attn_accum(const void* q, const void* k_cache, const void* v_
  *   new_lens     int32 [num_seqs] (written): min(ctx_lens[s], keep)
  *   kept         int32 [num_seqs, Hkv, keep] (written) or NULL: the kept tokens'
  *                old positions, ascending, -1 behind the last
- *   keep > 0, recent >= 0, sink >= 0, sink + recent <= keep
+ *   keep > 0, recent >= 0, sink >= 0, sink + recent <= keep; keep up to 2^20 - 16
  *   ws           needed when kept is NULL: at least
  *                fa_cache_evict_workspace_size(...) bytes, 256-byte aligned
  * A sequence whose lengths do not fit its tables or acc_len records

@@ -1396,9 +1396,12 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
             for (int k = 0; k < kDocRows; ++k) id[k + 1] = i0 + k < n ? __ldg(ids + i0 + k) : 0;
         }
         unsigned first = 0;
+        int pos = i0 % T;
 #pragma unroll
-        for (int k = 0; k < kDocRows; ++k)
-            if (i0 + k < n && ((i0 + k) % T == 0 || id[k + 1] != id[k])) first |= 1u << k;
+        for (int k = 0; k < kDocRows; ++k) {
+            if (i0 + k < n && (pos == 0 || id[k + 1] != id[k])) first |= 1u << k;
+            if (++pos == T) pos = 0;
+        }
         const int c = __popc(first);
         int x = c;
 #pragma unroll
@@ -1422,23 +1425,21 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
     }
     if (threadIdx.x == 0) starts[carry] = n;
     __syncthreads();
-    for (int base = threadIdx.x; base < n; base += kDocRows * blockDim.x) {  // each kind of load for all rows at once
+    for (int i0 = threadIdx.x * kDocRows; i0 < n; i0 += blockDim.x * kDocRows) {  // each kind of load for all rows at once
         int2 r[kDocRows];
         int lo[kDocRows], hi[kDocRows];
 #pragma unroll
-        for (int k = 0; k < kDocRows; ++k) {
-            const int i = base + k * blockDim.x;
-            r[k] = i < n ? rows[i] : make_int2(0, 0);
-        }
+        for (int k = 0; k < kDocRows; ++k) r[k] = i0 + k < n ? rows[i0 + k] : make_int2(0, 0);
 #pragma unroll
         for (int k = 0; k < kDocRows; ++k) {
             lo[k] = starts[r[k].x];
             hi[k] = starts[r[k].x + 1];
         }
+        int s0 = i0 / T * T;  // the sequence's first row
 #pragma unroll
         for (int k = 0; k < kDocRows; ++k) {
-            const int i = base + k * blockDim.x, s0 = i / T * T;
-            if (i < n) rows[i] = make_int2(lo[k] - s0, (r[k].y < 0 ? lo[k] : hi[k]) - s0);
+            if (i0 + k == s0 + T) s0 += T;
+            if (i0 + k < n) rows[i0 + k] = make_int2(lo[k] - s0, (r[k].y < 0 ? lo[k] : hi[k]) - s0);
         }
     }
     __syncthreads();

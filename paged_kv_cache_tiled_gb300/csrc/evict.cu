@@ -268,20 +268,22 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
 // token i of `dst`, K and V, 16 bytes per thread; kEvRows rows per thread whose
 // loads are in flight together, and full occupancy behind the three dependent
 // loads (token, blocks, values) of a row.
+// CTA (sequence and head, group of rows).
 constexpr int kEvRows = 2;
+template <int D>
 __global__ void __launch_bounds__(256, 8) evict_move_kernel(uint16_t* kc, uint16_t* vc, const int32_t* __restrict__ src,
                                                             const int32_t* __restrict__ dst, const int32_t* list,
-                                                            int Hkv, int d, int mbps, int dst_mbps, int keep,
-                                                            int num_blocks, int per, DevCtx ctx) {
+                                                            int Hkv, int mbps, int dst_mbps, int keep, int num_blocks,
+                                                            DevCtx ctx) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is complete
-    const int cpr = d >> 3;            // chunks per row
-    const int lanes = 2 * cpr;         // threads per row pair (K and V)
-    const int rows_cta = 256 / lanes;  // rows side by side
+    constexpr int d = D, cpr = D / 8;      // chunks per row
+    constexpr int lanes = 2 * cpr;         // threads per row pair (K and V)
+    constexpr int rows_cta = 256 / lanes;  // rows side by side
     const int c = threadIdx.x % lanes, rr = threadIdx.x / lanes;
     uint16_t* cache = c < cpr ? kc : vc;
     const int off = (c < cpr ? c : c - cpr) * 8;
-    const int sh = blockIdx.x / per, s = sh / Hkv, h = sh % Hkv;
-    const int i0 = blockIdx.x % per * rows_cta * kEvRows + rr;
+    const int sh = blockIdx.x, s = sh / Hkv, h = sh % Hkv;
+    const int i0 = blockIdx.y * rows_cta * kEvRows + rr;
     const int32_t* tokens = list + (long)sh * keep;
     int t[kEvRows];
 #pragma unroll
@@ -328,8 +330,7 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
         recent < 0 || sink < 0 || recent > keep || sink > keep - recent || acc_len < 0 || acc_out_len < 0)
         return FA_ERR_INVALID_ARG;
     if (block_size != kEvBlock || (d != 64 && d != 128)) return FA_ERR_UNSUPPORTED;
-    if ((long)num_seqs * Hkv >= 1L << 27 || (long)num_seqs * Hkv * ((keep + 15) / 16) >= 1L << 31)
-        return FA_ERR_UNSUPPORTED;  // grid limits
+    if ((long)num_seqs * Hkv >= 1L << 27 || keep > 16 * 65535) return FA_ERR_UNSUPPORTED;  // grid limits
     if (num_seqs == 0) return FA_OK;
     if (!k_cache || !v_cache || !acc || !block_table || !ctx_lens || !dst_table || !new_lens)
         return FA_ERR_INVALID_ARG;
@@ -373,13 +374,14 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
         return FA_ERR_CUDA;
     const int rows_item = 256 / (2 * (d / 8)) * kEvRows;
     const int per = (keep + rows_item - 1) / rows_item;  // CTAs per sequence and head
-    cfg.gridDim = dim3((unsigned)(rows * per));
+    cfg.gridDim = dim3((unsigned)rows, (unsigned)per);
     cfg.blockDim = dim3(256);
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    if (cudaLaunchKernelEx(&cfg, evict_move_kernel, static_cast<uint16_t*>(k_cache), static_cast<uint16_t*>(v_cache),
-                           block_table, dst_table, static_cast<const int32_t*>(list), Hkv, d, max_blocks_per_seq,
-                           dst_blocks_per_seq, keep, num_blocks, per, ctx) != cudaSuccess)
+    auto move = d == 128 ? evict_move_kernel<128> : evict_move_kernel<64>;
+    if (cudaLaunchKernelEx(&cfg, move, static_cast<uint16_t*>(k_cache), static_cast<uint16_t*>(v_cache), block_table,
+                           dst_table, static_cast<const int32_t*>(list), Hkv, max_blocks_per_seq, dst_blocks_per_seq,
+                           keep, num_blocks, ctx) != cudaSuccess)
         return FA_ERR_CUDA;
     set_launch_count(2);
     return FA_OK;

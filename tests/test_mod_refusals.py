@@ -109,7 +109,7 @@ EVICT_OK = dict(kc=D, vc=D, acc=D, acc_len=64, bt=D, ctx=D, dst=2 * D, acc_out=2
     (dict(sink=2 ** 31 - 1, recent=32), 1), (dict(d=96), 2), (dict(bs=8), 2), (dict(kc=None), 1), (dict(acc=None), 1),
     (dict(dst=None), 1), (dict(dst=D), 1), (dict(kc=D + 2), 1), (dict(out_len=31), 1), (dict(acc_out=D, out_len=63), 1),
     (dict(kept=None), 6), (dict(kept=None, ws=D, ws_bytes=16), 6), (dict(new_lens=None), 1), (dict(dmbps=0), 1),
-    (dict(S=0), 0), (dict(acc_len=-1), 1),
+    (dict(S=0), 0), (dict(acc_len=-1), 1), (dict(keep=1 << 20, out_len=1 << 20), 2),
 ], ids=str)
 def test_evict(fattn, kw, want):
     assert call(fattn.library(), "fa_cache_evict", EVICT, EVICT_OK, **kw) == want
