@@ -126,7 +126,7 @@ struct TcParams {
     ScoreMod mod;
     CapPoly cap;
     const int2* doc_rows;      // dense: per row of [B, T] its document's [first, end), empty for padding; or null
-    const int32_t* doc_order;  // dense with documents: (sequence, query tile) entries, longest first
+    const int4* doc_order;     // dense with documents: entries (sequence, query entry, first and end KV tile), longest first
     DevCtx ctx;
 };
 
@@ -274,9 +274,11 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
                 qt = p.causal ? nqt - 1 - rank : rank;
             if constexpr (MOD != 0)
                 if (listed) {
-                    const int e = __ldg(p.doc_order + rank);
-                    U.b = e / nqt;
-                    qt = e % nqt;
+                    const int4 e = __ldg(p.doc_order + rank);
+                    U.b = e.x;
+                    qt = e.y;
+                    U.kt0 = e.z;
+                    U.n_kt = e.w;
                 }
             U.hk = (rest / half) % p.Hkv;
             const int pp = rest % half;
@@ -293,9 +295,11 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
             U.b = rest / p.Hq;
             if constexpr (MOD != 0)
                 if (listed) {
-                    const int e = __ldg(p.doc_order + rank);
-                    U.b = e / ntp;
-                    pt = e % ntp;
+                    const int4 e = __ldg(p.doc_order + rank);
+                    U.b = e.x;
+                    pt = e.y;
+                    U.kt0 = e.z;
+                    U.n_kt = e.w;
                 }
             U.head[0] = U.head[1] = rest % p.Hq;
             U.hk = U.head[0] / p.g;
@@ -312,9 +316,10 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
         U.kv_len = p.Tk;
         U.pos_off = 0;  // rows and keys are both absolute positions in the sequence
         if constexpr (MOD != 0) {
-            U.kv_lo = row_range<MODE>(p, U.b, U.row0[0], U.row0[0], p.Tk).x;
-            U.kt0 = U.kv_lo / kTcRows;
-            U.n_kt = (row_range<MODE>(p, U.b, last - 1, last - 1, p.Tk).y + kTcRows - 1) / kTcRows;
+            if (!p.doc_order) {  // (with documents the entry says)
+                U.kt0 = row_range<MODE>(p, U.b, U.row0[0], U.row0[0], p.Tk).x / kTcRows;
+                U.n_kt = (row_range<MODE>(p, U.b, last - 1, last - 1, p.Tk).y + kTcRows - 1) / kTcRows;
+            }
         } else {
             const int kv_end = p.causal ? min(p.Tk, last) : p.Tk;
             U.kt0 = 0;
@@ -1374,7 +1379,7 @@ fa_status launch_mask_classify(const float* M, int Tq, int Tk, uint8_t* cls, uin
 // counting sort.  `starts` is scratch for the runs' first rows.
 constexpr int kDocRows = 8;  // consecutive ids per thread and pass
 __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restrict__ ids, int B, int T, int entry_tiles,
-                                                         int2* rows, int* starts, int32_t* __restrict__ order,
+                                                         int2* rows, int* starts, int4* __restrict__ order,
                                                          int32_t* __restrict__ count, TcParams p) {
     if (threadIdx.x == 0) count[1] = 0;  // the attention's unit tickets
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the attention waits for this grid's end
@@ -1444,8 +1449,8 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
     }
     __syncthreads();
     const int er = entry_tiles * kTcRows, per = (T + er - 1) / er, entries = B * per;
-    auto cost = [&](int e) {
-        const int b = e / per, r0 = e % per * er, r1 = min(T, r0 + er) - 1;
+    auto entry = [&](int e) {  // (sequence, query entry, first KV tile, their end)
+        const int b = e / per, t = e % per, r0 = t * er, r1 = min(T, r0 + er) - 1;
         auto range = [&](int row) {
             int lo = 0, hi = T;
             if (p.causal) hi = p.mod.prefix ? max(row + 1, p.mod.prefix[b]) : row + 1;
@@ -1454,9 +1459,10 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
             const int2 doc = rows[(long)b * T + row];
             return make_int2(max(lo, doc.x), min(min(hi, doc.y), T));
         };
-        return max(0, (range(r1).y + kTcRows - 1) / kTcRows - range(r0).x / kTcRows);
+        return make_int4(b, t, range(r0).x / kTcRows, (range(r1).y + kTcRows - 1) / kTcRows);
     };
-    for (int e = threadIdx.x; e < entries; e += blockDim.x) atomicAdd(&hist[cost(e)], 1);
+    auto cost = [](const int4& e) { return max(0, e.w - e.z); };
+    for (int e = threadIdx.x; e < entries; e += blockDim.x) atomicAdd(&hist[cost(entry(e))], 1);
     __syncthreads();
     if (w == 0) {  // bucket starts, highest cost first
         int run = 0;
@@ -1473,7 +1479,10 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < entries; e += blockDim.x) order[atomicAdd(&hist[cost(e)], 1)] = e;
+    for (int e = threadIdx.x; e < entries; e += blockDim.x) {
+        const int4 x = entry(e);
+        order[atomicAdd(&hist[cost(x)], 1)] = x;
+    }
 }
 
 // ------------------------------------------------------------ launchers ---
@@ -1826,7 +1835,7 @@ fa_status fa_prefill_masked(const void* q, const void* k, const void* v, const f
 size_t fa_prefill_mod_workspace_size(int B, int T) {
     if (B <= 0 || T <= 0) return 0;
     const size_t n = (size_t)B * T, nt = (size_t)(T + kTcRows - 1) / kTcRows;
-    return align256(n * sizeof(int2)) + align256((n + 1) * sizeof(int32_t)) + align256(B * nt * sizeof(int32_t)) + 256;
+    return align256(n * sizeof(int2)) + align256((n + 1) * sizeof(int32_t)) + align256(B * nt * sizeof(int4)) + 256;
 }
 
 fa_status fa_prefill_mod(const void* q, const void* k, const void* v, void* out, float* lse, int B, int T, int Hq,
@@ -1862,8 +1871,8 @@ fa_status fa_prefill_mod(const void* q, const void* k, const void* v, void* out,
         uint8_t* wsb = static_cast<uint8_t*>(ws);
         int2* rows = reinterpret_cast<int2*>(wsb);
         int* starts = reinterpret_cast<int*>(wsb + align256((size_t)B * T * sizeof(int2)));
-        int32_t* order = starts + align256(((size_t)B * T + 1) * sizeof(int32_t)) / sizeof(int32_t);
-        int32_t* count = order + align256((size_t)B * nt * sizeof(int32_t)) / sizeof(int32_t);
+        int4* order = reinterpret_cast<int4*>(starts + align256(((size_t)B * T + 1) * sizeof(int32_t)) / sizeof(int32_t));
+        int32_t* count = reinterpret_cast<int32_t*>(order + align256((size_t)B * nt * sizeof(int4)) / sizeof(int4));
         if (hist_bytes > 48 * 1024 &&
             (st = raise_dynamic_smem(reinterpret_cast<const void*>(doc_order_kernel), (int)hist_bytes)) != FA_OK)
             return st;
