@@ -543,8 +543,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                                         for (int k = top - 2; k >= 0; --k) t = __ffma2_rn(t, q2, co[k]);
                                         x = __ffma2_rn(x, t, l2);
                                     } else if (MOD == CS_CAP || (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
-                                        x.x = fmaf(p.mod.cap_out, tanh_f32(x.x * p.mod.cap_in), l2.x);
-                                        x.y = fmaf(p.mod.cap_out, tanh_f32(x.y * p.mod.cap_in), l2.y);
+                                        x.x = fmaf(p.mod.cap_out, tanh_abs(x.x * p.mod.cap_in), l2.x);
+                                        x.y = fmaf(p.mod.cap_out, tanh_abs(x.y * p.mod.cap_in), l2.y);
                                     } else {
                                         x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), l2);
                                     }

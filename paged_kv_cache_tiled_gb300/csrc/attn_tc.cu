@@ -1231,9 +1231,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 return __ffma2_rn(z, t, neg_m);
                             });
                         } else {
+                            const float2 cp2 = both(p.mod.cap_out);
                             exp_pairs([&](float2 z, int) {
-                                return __ffma2_rn(make_float2(tanh_f32(z.x * p.mod.cap_in), tanh_f32(z.y * p.mod.cap_in)),
-                                                  both(p.mod.cap_out), neg_m);
+                                return __ffma2_rn(make_float2(tanh_abs(z.x * p.mod.cap_in), tanh_abs(z.y * p.mod.cap_in)),
+                                                  cp2, neg_m);
                             }, std::true_type{});
                         }
                     } else if ((MOD & MOD_BIAS) != 0 && !general) {

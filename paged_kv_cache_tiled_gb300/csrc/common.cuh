@@ -314,11 +314,19 @@ __device__ __forceinline__ float tanh_f32(float u) {
 }
 
 // tanh on |u| <= kTanhNear: u times a degree-4 polynomial in u^2 of the same kind
-// (relative error 1.8e-7 as evaluated).  Both polynomials go on rising past
+// (relative error 2.8e-07 as evaluated).  Both polynomials go on rising past
 // the end of their range, so a score below it only gets a still lower logit.
-constexpr float kTanhNear = 0.6f;
-constexpr float kTanhD0 = 0.99999994f, kTanhD1 = -0.3333231f, kTanhD2 = 0.13310173f, kTanhD3 = -0.05210147f,
-                kTanhD4 = 0.015475417f;
+constexpr float kTanhNear = 0.65f;
+constexpr float kTanhD0 = 0.9999998f, kTanhD1 = -0.333315f, kTanhD2 = 0.13297874f, kTanhD3 = -0.051517908f,
+                kTanhD4 = 0.014625075f;
+// tanh with an absolute (not relative) error below 4e-7 anywhere, all that a
+// capped logit needs: 1 - 2 / (1 + e^(2|u|)) with the hardware's exponential
+// and reciprocal, about half of tanh_f32's instructions.
+__device__ __forceinline__ float tanh_abs(float u) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(fabsf(u) * 2.885390081777927f)));
+    return copysignf(fmaf(-2.f, r, 1.f), u);
+}
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // ------------------------------------------------------- score modifiers ---
@@ -347,7 +355,7 @@ struct ScoreMod {
 struct CapPoly {
     float2 near[5], unit[7];
     float near_max, unit_max;      // largest s
-    float near_slack, unit_slack;  // c log2(e) tanh(0.6), c log2(e) tanh(1)
+    float near_slack, unit_slack;  // c log2(e) tanh(kTanhNear), c log2(e) tanh(1)
 };
 
 // Four E4M3 bytes (byte i = element i) to two f16x2 words: lo = elements

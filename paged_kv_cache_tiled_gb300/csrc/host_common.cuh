@@ -93,7 +93,7 @@ inline CapPoly cap_poly(const ScoreMod& m) {
     }
     c.near_max = (float)(kTanhNear / in);
     c.unit_max = (float)(1.0 / in);
-    c.near_slack = near_fits ? (float)(out * std::tanh(0.6)) : -INFINITY;
+    c.near_slack = near_fits ? (float)(out * std::tanh(kTanhNear)) : -INFINITY;
     c.unit_slack = unit_fits ? (float)(out * std::tanh(1.0)) : -INFINITY;
     return c;
 }
