@@ -495,7 +495,7 @@ __device__ __noinline__ float modified_logits_row(uint32_t taddr, int vlo, int v
         for (int j = 0; j < 32; ++j) {
             const int c = h * 32 + j;
             const float z = __uint_as_float(raw[j]);
-            float x = cap_out > 0.f ? cap_out * tanh_f32(z * cap_in) : z * scale_log2;
+            float x = cap_out > 0.f ? cap_out * tanh_abs(z * cap_in) : z * scale_log2;
             x = fmaf(-slope, fabsf((float)(d0 + c)), x);
             if (c < vlo || c >= vlim) x = -INFINITY;
             raw[j] = __float_as_uint(x);

@@ -124,13 +124,9 @@ struct StreamSplit {
     __device__ __forceinline__ long long begin(int w) const {
         return (long long)w * qt + (int)((unsigned)w * (unsigned)rm / (unsigned)W);
     }
-    // warp whose range holds page x (0 <= x < P)
-    __device__ __forceinline__ int owner(long long x) const {
-        int w = (int)min((long long)W - 1, x * W / P);  // within one of the owner
-        while (w + 1 < W && begin(w + 1) <= x) ++w;
-        while (w > 0 && begin(w) > x) --w;
-        return w;
-    }
+    // warp whose range holds page x (0 <= x < P): the last w with floor(w P / W) <= x,
+    // that is w P < (x + 1) W
+    __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * W - 1) / P); }
 };
 
 // Shared memory of a decode CTA: each warp's TMA ring, then each warp's slot
