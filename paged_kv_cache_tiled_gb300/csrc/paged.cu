@@ -129,6 +129,13 @@ struct StreamSplit {
     __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * W - 1) / P); }
 };
 
+// Warps that share a modified call's stream: at most one per page, in whole CTAs.
+// (Spread over every CTA of the grid, a short context leaves one piece per page
+// to the merge kernel: 90 pages took 22 us, in twelve CTAs they take half.)
+__device__ __forceinline__ int stream_warps(int W, long long P) {
+    return (int)min((long long)W, (P + kStreamWarps - 1) / kStreamWarps * kStreamWarps);
+}
+
 // Shared memory of a decode CTA: each warp's TMA ring, then each warp's slot
 // for the partial of its first segment (ROWS query rows).  The ring has three
 // stages (8 KB each at d = 128, 4 KB at d = 64) except at d = 128 with slots of
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = Hq / Hkv;
-    const int W = gridDim.x * kStreamWarps;
+    int W = gridDim.x * kStreamWarps;
     const int gw = blockIdx.x * kStreamWarps + warp;
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tm_k);
@@ -274,6 +281,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     }
     const long long P = __shfl_sync(0xffffffffu, inc_p, 31);
     if (P == 0) return;
+    if constexpr (MOD != 0) {
+        W = stream_warps(W, P);
+        if (gw >= W) return;  // a whole CTA
+    }
     const StreamSplit split(P, W);
     const long long b0 = split.begin(gw), b1 = split.begin(gw + 1);
     const int n_pages = (int)(b1 - b0);
@@ -826,6 +837,7 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
     }
     const long long P = (long long)Hkv * tot;
     const long long seg_first = (long long)Hkv * pre + (long long)hk * nblk;
+    if constexpr (MOD) W = stream_warps(W, P);
     const StreamSplit split(P, W);  // W: the decode grid's warps
     const int c_lo = split.owner(seg_first) / kStreamWarps, c_hi = split.owner(seg_first + nblk - 1) / kStreamWarps;
     const int npieces = c_hi - c_lo + 1;
