@@ -434,7 +434,7 @@ fa_status fa_paged_attn_accum(const void* q, const void* k_cache, const void* v_
  *   block_table  int32 [num_seqs, max_blocks_per_seq], ctx_lens as for
  *                fa_paged_attn
  *   dst_table    int32 [num_seqs, dst_blocks_per_seq]: blocks for
- *                min(ctx_lens[s], keep) tokens, none of them a block that
+ *                min(ctx_lens[s], keep) tokens, no block twice and none that
  *                block_table lists for any sequence of the call (new blocks of
  *                the pool: the old ones may be shared with other sequences and
  *                are released afterwards); FA_ERR_INVALID_ARG when it is

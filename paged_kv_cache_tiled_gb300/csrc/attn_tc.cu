@@ -201,7 +201,7 @@ __device__ __forceinline__ int2 row_range(const TcParams& p, int b, int row, int
     if (p.mod.window > 0) lo = max(0, pos - p.mod.window + 1);
     if constexpr (MODE == MODE_DENSE) {
         if (p.doc_rows) {
-            const int2 doc = __ldg(p.doc_rows + (long)b * p.T + row);
+            const int2 doc = p.doc_rows[(long)b * p.T + row];  // (a plain load: written while this kernel may already run)
             lo = max(lo, doc.x);
             hi = min(hi, doc.y);
         }
@@ -274,7 +274,7 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
                 qt = p.causal ? nqt - 1 - rank : rank;
             if constexpr (MOD != 0)
                 if (listed) {
-                    const int4 e = __ldg(p.doc_order + rank);
+                    const int4 e = p.doc_order[rank];
                     U.b = e.x;
                     qt = e.y;
                     U.kt0 = e.z;
@@ -295,7 +295,7 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
             U.b = rest / p.Hq;
             if constexpr (MOD != 0)
                 if (listed) {
-                    const int4 e = __ldg(p.doc_order + rank);
+                    const int4 e = p.doc_order[rank];
                     U.b = e.x;
                     pt = e.y;
                     U.kt0 = e.z;

@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         pos_r0 = causal ? ctx_len - q_len + gid / g : ctx_len - 1;
         pos_r1 = causal ? ctx_len - q_len + (gid + 8) / g : ctx_len - 1;
         if constexpr (MOD != 0) {
-            const int prefix = causal && mod.prefix ? __ldg(mod.prefix + cc.s) : 0;
+            const int prefix = causal && mod.prefix ? max(0, __ldg(mod.prefix + cc.s)) : 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 qpos[i] = ctx_len - q_len + rr[i] / g;

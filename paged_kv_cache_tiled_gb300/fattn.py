@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 
 import numpy as np
@@ -186,13 +187,26 @@ def _dims(t, name: str, n: int):
     return t.shape
 
 
-def _kept_for(stream, *tensors):
-    """Tensors that a call made itself come from the current stream's memory: when the call runs on another stream,
-    that memory must not be handed out again before it is done there."""
-    if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        for t in tensors:
-            t.record_stream(s)
+def _empty(shape, dtype, dev: int, stream):
+    """A tensor that a call makes itself.  For a call on a stream other than the current one it is memory of that
+    stream (the current stream's may still be in use by work queued there), kept until the current stream, on which
+    the caller may go on to use it, is done with it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _int(x, name: str) -> int:
+    """x, which a C int has to hold (ctypes would cut it off)."""
+    x = operator.index(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits")
+    return x
 
 
 def _workspace(ws, nbytes: int, dev: int, stream):
@@ -200,8 +214,7 @@ def _workspace(ws, nbytes: int, dev: int, stream):
     if nbytes == 0 and ws is None:
         return None, 0, None
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-        _kept_for(stream, ws)
+        ws = _empty(nbytes, torch.uint8, dev, stream)
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on cuda:{dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
@@ -310,7 +323,8 @@ def fa_prefill_mod(q, k, v, causal: bool = True, scale: float | None = None, sof
     Hkv = _dims(k, "k", 4)[2]
     dev, bf16, f32, i32 = _device_of(q, "q"), torch.bfloat16, torch.float32, torch.int32
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, bf16, dev, stream)
+    window = _int(window, "window")
     wp, wn, ws = _workspace(ws, fa_prefill_mod_workspace_size(B, T), dev, stream) if doc_ids is not None else (None, 0, None)
     _check(_lib.fa_prefill_mod(
         _arg(q, "q", bf16, (B, T, Hq, d), dev), _arg(k, "k", bf16, (B, T, Hkv, d), dev),
@@ -411,7 +425,7 @@ def fa_cache_append_mrope(q, k, v, positions, pair_axes, cos_sin, k_cache, v_cac
     if len(pair_axes) != d // 2:  # (their range is checked by the C call)
         raise ValueError(f"pair_axes must be {d // 2} integers in [0, {n_axes})")
     if q_out is None:
-        q_out = torch.empty(N, Hq, d, dtype=bf16, device=q.device)
+        q_out = _empty((N, Hq, d), bf16, dev, stream)
     _check(_lib.fa_cache_append_mrope(
         _arg(q, "q", dt, (N, Hq, d), dev), _arg(k, "k", dt, (N, Hkv, d), dev), _arg(v, "v", dt, (N, Hkv, d), dev),
         _arg(positions, "positions", torch.int32, (n_axes, N), dev), n_axes, pair_axes,
@@ -627,7 +641,8 @@ def _paged_mod_args(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal, 
     nb, Hkv, bs, _ = _dims(k_cache, "k_cache", 4)
     S, mbps = _dims(block_table, "block_table", 2)
     dev, bf16, i32 = _device_of(q, "q"), torch.bfloat16, torch.int32
-    max_q_len = total_q if max_q_len is None else max_q_len
+    max_q_len = total_q if max_q_len is None else _int(max_q_len, "max_q_len")
+    window = _int(window, "window")
     head = (_arg(q, "q", bf16, (total_q, Hq, d), dev), _arg(k_cache, "k_cache", bf16, (nb, Hkv, bs, d), dev),
             _arg(v_cache, "v_cache", bf16, (nb, Hkv, bs, d), dev), _arg(block_table, "block_table", i32, (S, mbps), dev),
             _arg(ctx_lens, "ctx_lens", i32, (S,), dev), _arg(q_lens, "q_lens", i32, (S,), dev),
@@ -644,7 +659,7 @@ def fa_paged_attn_mod(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal
     """fa_paged_attn with modified scores (as fa_prefill_mod, in cache positions); lse (optional, fp32
     [total_q, Hq]) receives the log-sum-exp of every row."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, _device_of(q, "q"), stream)
     dev, head, tail, sizes = _paged_mod_args(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal, scale, softcap,
                                              alibi_slopes, window, prefix_lens, out, lse, max_q_len)
     wp, wn, ws = _workspace(ws, 0 if ws is not None else fa_paged_attn_mod_workspace_size(*sizes), dev, stream)
@@ -660,10 +675,9 @@ def fa_paged_attn_accum(q, k_cache, v_cache, block_table, ctx_lens, q_lens, acc_
     tokens, and where acc_in is None) + the softmax weights every cached token received from the chunk's queries and
     the group's heads.  acc_in and acc_out may be the same tensor."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, _device_of(q, "q"), stream)
     if lse is None:
-        lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
-        _kept_for(stream, lse)
+        lse = _empty(q.shape[:2], torch.float32, _device_of(q, "q"), stream)
     dev, head, tail, sizes = _paged_mod_args(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal, scale, softcap,
                                              alibi_slopes, window, prefix_lens, out, lse, max_q_len)
     rows = (sizes[0], sizes[3], _dims(acc_out, "acc_out", 3)[2])
@@ -689,7 +703,8 @@ def fa_cache_evict(k_cache, v_cache, acc, block_table, ctx_lens, dst_table, keep
     acc_len, dmbps = _dims(acc, "acc", 3)[2], _dims(dst_table, "dst_table", 2)[1]
     dev, bf16, f32, i32 = _device_of(k_cache, "k_cache"), torch.bfloat16, torch.float32, torch.int32
     if new_lens is None:
-        new_lens = torch.empty(S, dtype=i32, device=k_cache.device)
+        new_lens = _empty(S, i32, dev, stream)
+    keep, recent, sink = _int(keep, "keep"), _int(recent, "recent"), _int(sink, "sink")
     out_len = 0 if acc_out is None else _dims(acc_out, "acc_out", 3)[2]
     need = fa_cache_evict_workspace_size(S, mbps, Hkv, keep) if kept is None and ws is None else 0
     wp, wn, ws = _workspace(ws, need, dev, stream)

@@ -373,3 +373,36 @@ def test_two_streams_at_once(F):
     streams[0].synchronize()
     assert all(torch.equal(x, want[0]) for x in out)
     assert F.fa_get_error() == F.FA_OK
+
+
+def test_own_tensors_come_from_the_calls_stream(F):
+    """A call on a stream given as an argument must not write into memory that the current stream's queued work may
+    still use: what it allocates is that stream's."""
+    q, k, v = (torch.randn(1, 300, h, 64, device="cuda").bfloat16() for h in (4, 2, 2))
+    want = F.fa_prefill_mod(q, k, v, window=50)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        x = torch.empty_like(q)
+        freed = x.data_ptr()
+        del x  # (work queued on the current stream may still be reading it)
+        out = F.fa_prefill_mod(q, k, v, window=50, stream=stream)
+        assert out.data_ptr() != freed
+        side.synchronize()
+        assert torch.equal(out, want)
+    assert torch.equal(F.fa_prefill_mod(q, k, v, window=50, stream=0), want)
+
+
+def test_prefix_of_the_lowest_value(F):
+    """prefix_lens below 1 change nothing, down to the type's lowest value: decode rows and chunks."""
+    lowest = -(1 << 31)
+    p = R.Paged(31, [100, 40, 300], [1, 3, 200], 4, 2, 64)
+    q, kc, vc, table, ctx, ql = p.cuda()
+    want = F.fa_paged_attn_mod(q, kc, vc, table, ctx, ql)
+    got = F.fa_paged_attn_mod(q, kc, vc, table, ctx, ql, prefix_lens=torch.full((3,), lowest, dtype=torch.int32, device="cuda"))
+    assert torch.equal(got, want)
+    x = [torch.randn(1, 200, h, 64, device="cuda").bfloat16() for h in (4, 2, 2)]
+    pre = torch.full((1,), lowest, dtype=torch.int32, device="cuda")
+    assert torch.equal(F.fa_prefill_mod(*x, prefix_lens=pre), F.fa_prefill_mod(*x, window=1 << 30))
+    with pytest.raises(ValueError):
+        F.fa_prefill_mod(*x, window=1 << 32)
