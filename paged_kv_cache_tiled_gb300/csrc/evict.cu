@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
     // the cluster's counts, by turns, so that one cluster barrier per pass is enough (a single CTA uses hist)
     __shared__ __align__(16) int total[2][kEvBins];
     __shared__ int2 warp_sums[32];
-    __shared__ int sel_digit, sel_above, totals[2];
+    __shared__ int sel_digit, sel_above, sel_count, totals[2];
     // the rows' copy may be scheduled; it waits for this grid's end before it reads the list
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int CL = (int)cluster_size(), rank = (int)cluster_rank();
@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
                 if (above < need && above + cs[b] >= need) {
                     sel_digit = top + b;
                     sel_above = above;
+                    sel_count = cs[b];
                 }
                 above += cs[b];
             }
@@ -189,6 +190,13 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
         __syncthreads();
         prefix |= (uint32_t)sel_digit << shift;
         need -= sel_above;
+        // Every token that matches the digits so far is kept: no need to tell them apart (22 bits
+        // mostly single one token out).  Keys above prefix - 1 are kept then.
+        if (sel_count == need && prefix > 0) {
+            --prefix;
+            need = 0;
+            break;
+        }
         // (sel_* is written again only behind the next pass's barriers)
     }
     // tokens above the threshold key, the forced ones, and the first `need` equal to it
