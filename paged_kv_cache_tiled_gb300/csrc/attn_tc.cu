@@ -94,6 +94,25 @@ __constant__ float2 kColumns[32] = {FA_COL8(0.f),  FA_COL8(8.f),  FA_COL8(16.f),
                                     FA_COL8(32.f), FA_COL8(40.f), FA_COL8(48.f), FA_COL8(56.f)};
 #undef FA_COL8
 
+// n / d for 0 <= n < 2^31 by a multiplication: with s = 31 + ceil(log2 d) and
+// m = floor(2^s / d) + 1 the error n (m d - 2^s) / (d 2^s) stays below 1 / d.
+// Every role works its units out behind three such divisions; with the
+// compiler's integer division they took 1000 cycles of each unit's boundary.
+struct FastDiv {
+    uint32_t m = 0;
+    int s = 0;
+    FastDiv() = default;
+    explicit FastDiv(int d) {
+        int c = 0;
+        while ((1ll << c) < d) ++c;
+        s = 31 + c;
+        m = (uint32_t)((1ull << s) / (uint64_t)d + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const {
+        return (int)(((uint64_t)(uint32_t)n * m) >> s);
+    }
+};
+
 struct TcParams {
     int B, T;        // dense / masked: sequence length (row stride of q/k/v/out)
     int q0, Tq, Tk;  // dense: query rows [q0, q0 + Tq) of each sequence against keys [0, Tk)
@@ -105,6 +124,10 @@ struct TcParams {
     int pack;        // paged: a slot is 128/g tokens x the g heads of a group (row = token * g + head)
     int pack_shift;  // log2(g) when packed
     int num_units;   // dense / masked
+    // units of one rank (dense: of one query entry, all sequences; paged: of one work entry), their split
+    // by kv heads and by the heads (head pairs) of a group
+    int per_rank, per_head;
+    FastDiv div_rank, div_hkv, div_head;
     uint16_t* out;
     float* lse;
     // masked
@@ -181,11 +204,6 @@ __device__ __forceinline__ int cta_unit(const TcSched& sc, int i, int G, int num
     return u < num_units ? u : -1;
 }
 
-// Units of one paged work entry: one per kv head (packed), per head pair, or per head.
-__device__ __forceinline__ int paged_units_per_entry(const TcParams& p) {
-    return p.pack ? p.Hkv : (p.pair_heads ? p.Hkv * (p.g / 2) : p.Hq);
-}
-
 // Run [lo, hi) of keys that query row `row` of a unit sees in a modified
 // variant; `pos` is the row's position, kv_len the sequence's keys.  Both ends
 // never decrease along the rows, so a unit's first and last row bound its range.
@@ -215,8 +233,7 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
     U.holes = 0;
     U.kv_lo = 0;
     if constexpr (MODE == MODE_PAGED) {
-        const int per_entry = paged_units_per_entry(p);
-        const int e = u / per_entry, rest = u % per_entry;
+        const int e = p.div_rank(u), rest = u - e * p.per_rank;
         const int seq = __ldg(p.work_list + 2 * e), t0 = __ldg(p.work_list + 2 * e + 1);
         const int ql = __ldg(p.q_lens + seq), cl = __ldg(p.ctx_lens + seq), qs = __ldg(p.q_start + seq);
         U.b = seq;
@@ -228,14 +245,13 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
             U.row0[0] = t0;
             U.row0[1] = t0 + slot_tokens;
         } else if (p.pair_heads) {
-            const int pp = rest % (p.g / 2);
-            U.hk = rest / (p.g / 2);
-            U.head[0] = U.hk * p.g + 2 * pp;
+            U.hk = p.div_head(rest);
+            U.head[0] = U.hk * p.g + 2 * (rest - U.hk * p.per_head);
             U.head[1] = U.head[0] + 1;
             U.row0[0] = U.row0[1] = t0;
         } else {
             U.head[0] = U.head[1] = rest;
-            U.hk = rest / p.g;
+            U.hk = p.div_head(rest);
             U.row0[0] = t0;
             U.row0[1] = t0 + kTcRows;
         }
@@ -260,51 +276,34 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
     } else {
         const int nqt = (p.Tq + kTcRows - 1) / kTcRows;  // query tiles of this launch
         const int qt0 = p.q0 / kTcRows;                  // its first tile within the sequence
+        const int rank = p.div_rank(u), rest = u - rank * p.per_rank;
+        const int bh = p.div_head(rest);  // sequence and kv head
+        const int within = rest - bh * p.per_head;
+        U.b = p.div_hkv(bh);
+        U.hk = bh - U.b * p.Hkv;
+        // query entry: a tile (pair_heads) or two tiles of one head
+        const int entries = p.pair_heads ? nqt : (nqt + 1) / 2;
+        int qe;
+        if constexpr (MODE == MODE_MASKED)
+            qe = p.pair_heads ? __ldg(p.qt_order + rank) : rank;
+        else
+            qe = p.causal ? entries - 1 - rank : rank;
+        if constexpr (MOD != 0)
+            if (p.doc_order) {  // documents: entries (sequence, query entry, KV tiles), longest first
+                const int4 e = p.doc_order[rank];
+                U.b = e.x;
+                qe = e.y;
+                U.kt0 = e.z;
+                U.n_kt = e.w;
+            }
         if (p.pair_heads) {
-            const int half = p.g / 2;
-            bool listed = false;  // documents: entries (sequence, query tile), longest first
-            if constexpr (MOD != 0) listed = p.doc_order != nullptr;
-            const int upt = (listed ? 1 : p.B) * p.Hkv * half;
-            const int rank = u / upt, rest = u % upt;
-            int qt;
-            U.b = rest / (p.Hkv * half);
-            if constexpr (MODE == MODE_MASKED)
-                qt = __ldg(p.qt_order + rank);
-            else
-                qt = p.causal ? nqt - 1 - rank : rank;
-            if constexpr (MOD != 0)
-                if (listed) {
-                    const int4 e = p.doc_order[rank];
-                    U.b = e.x;
-                    qt = e.y;
-                    U.kt0 = e.z;
-                    U.n_kt = e.w;
-                }
-            U.hk = (rest / half) % p.Hkv;
-            const int pp = rest % half;
-            U.head[0] = U.hk * p.g + 2 * pp;
+            U.head[0] = U.hk * p.g + 2 * within;
             U.head[1] = U.head[0] + 1;
-            U.row0[0] = U.row0[1] = (qt0 + qt) * kTcRows;
+            U.row0[0] = U.row0[1] = (qt0 + qe) * kTcRows;
         } else {
-            const int ntp = (nqt + 1) / 2;
-            bool listed = false;
-            if constexpr (MOD != 0) listed = p.doc_order != nullptr;
-            const int upt = (listed ? 1 : p.B) * p.Hq;
-            const int rank = u / upt, rest = u % upt;
-            int pt = (p.causal && MODE == MODE_DENSE) ? ntp - 1 - rank : rank;
-            U.b = rest / p.Hq;
-            if constexpr (MOD != 0)
-                if (listed) {
-                    const int4 e = p.doc_order[rank];
-                    U.b = e.x;
-                    pt = e.y;
-                    U.kt0 = e.z;
-                    U.n_kt = e.w;
-                }
-            U.head[0] = U.head[1] = rest % p.Hq;
-            U.hk = U.head[0] / p.g;
-            U.row0[0] = (qt0 + 2 * pt) * kTcRows;
-            U.row0[1] = (qt0 + 2 * pt + 1) * kTcRows;
+            U.head[0] = U.head[1] = U.hk * p.g + within;
+            U.row0[0] = (qt0 + 2 * qe) * kTcRows;
+            U.row0[1] = (qt0 + 2 * qe + 1) * kTcRows;
         }
         int last = 0;
 #pragma unroll
@@ -614,7 +613,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tma_prefetch_desc(&tm_v);
         int n0;
         if constexpr (MODE == MODE_PAGED)
-            n0 = __ldg(p.work_count) * paged_units_per_entry(p);
+            n0 = __ldg(p.work_count) * p.per_rank;
         else
             n0 = p.num_units;
         const int u0 = cta_unit(sched, 0, gridDim.x, n0);
@@ -651,7 +650,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     int num_units;
     if constexpr (MODE == MODE_PAGED)
-        num_units = __ldg(p.work_count) * paged_units_per_entry(p);
+        num_units = __ldg(p.work_count) * p.per_rank;
     else
         num_units = p.num_units;
     const int G = gridDim.x;
@@ -971,14 +970,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t o_col = s ? C::kO1 : C::kO0;
         int sc = 0, oc = 0;
         bool ok = !p.ctx.force_timeout || mbar_wait_warp(never, 0, lim_ns, abort_flag);
+        // Plain dense variants work the next unit out while the last P*V of this one runs (the
+        // producer hands units out ahead, so that waits for nothing this warp has yet to do);
+        // in the others its registers cost more than the wait they save.
+        constexpr bool kAhead = MODE == MODE_DENSE && (MOD & (MOD_CAP | MOD_BIAS)) == 0;
+        int u = -1;
+        Unit next{};
+        auto fetch = [&](int i) -> bool {
+            if (!reader_unit(tickets, i, u, sched, G, num_units, ufull, uempty, umbox, lim_ns, abort_flag)) return false;
+            if (u >= 0) next = decode_unit<MODE, MOD>(p, u);
+            return true;
+        };
         for (int i = 0; ok; ++i) {
-            int u;
-            if (!reader_unit(tickets, i, u, sched, G, num_units, ufull, uempty, umbox, lim_ns, abort_flag)) {
+            if ((!kAhead || i == 0) && !fetch(i)) {
                 ok = false;
                 break;
             }
             if (u < 0) break;
-            const Unit U = decode_unit<MODE, MOD>(p, u);
+            const Unit U = next;
+            const int u_now = u;
             // query token of this thread's row, and its head within a packed slot
             const int tok = (MODE == MODE_PAGED && p.pack) ? r >> p.pack_shift : r;
             const int hl = (MODE == MODE_PAGED && p.pack) ? r & (p.g - 1) : 0;
@@ -993,6 +1003,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         lse = p.lse + ((long)U.b * p.Hq + sel(U.head, s)) * p.T + row;
                     store_zero_row<D>(out_row<D, MODE>(p, U, s, tok, hl), lse);
                 }
+                __syncwarp();
+                if (kAhead) ok = fetch(i + 1);
                 continue;
             }
             // key j is visible when j <= row + pos_off (causal) and j < kv_len
@@ -1285,13 +1297,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ++it;
             }
             if (!ok) break;
-            if (!mbar_wait_warp(&ofull[s], oc & 1, lim_ns, abort_flag)) {
+            const Unit E = decode_unit<MODE, MOD>(p, u_now);  // re-derived here so its fields are not live across the tile loop
+            if ((kAhead && !fetch(i + 1)) || !mbar_wait_warp(&ofull[s], oc & 1, lim_ns, abort_flag)) {
                 ok = false;
                 break;
             }
             ++oc;
             tc_fence_after();
-            const Unit E = decode_unit<MODE, MOD>(p, u);  // re-derived here so its fields are not live across the tile loop
             uint16_t* orow = out_row<D, MODE>(p, E, s, tok, hl);
             const float inv_l = l > 0.f ? 1.f / l : 0.f;
             // 64 columns per TMEM wait; 32-byte stores of the bf16 row
@@ -1511,9 +1523,14 @@ static fa_status launch_tc(const CUtensorMap& tq, const CUtensorMap& tk, const C
 
 template <int MODE, int MOD = 0>
 static fa_status launch_tc_d(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const TcParams& p, int grid, cudaStream_t s, const TcSched* sched = nullptr) {
+                             TcParams p, int grid, cudaStream_t s, const TcSched* sched = nullptr) {
     static const TcSched kNone = {};  // n == 0: the unit_of order
     const TcSched& sc = sched ? *sched : kNone;
+    p.per_head = p.pair_heads ? p.g / 2 : p.g;
+    p.per_rank = p.Hkv * (MODE == MODE_PAGED ? (p.pack ? 1 : p.per_head) : (p.doc_order ? 1 : p.B) * p.per_head);
+    p.div_rank = FastDiv(p.per_rank);
+    p.div_hkv = FastDiv(p.Hkv);
+    p.div_head = FastDiv(p.per_head);
     return d == 128 ? launch_tc<128, MODE, MOD>(tq, tk, tv, p, grid, s, sc)
                     : launch_tc<64, MODE, MOD>(tq, tk, tv, p, grid, s, sc);
 }
