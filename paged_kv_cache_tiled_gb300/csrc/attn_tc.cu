@@ -94,25 +94,6 @@ __constant__ float2 kColumns[32] = {FA_COL8(0.f),  FA_COL8(8.f),  FA_COL8(16.f),
                                     FA_COL8(32.f), FA_COL8(40.f), FA_COL8(48.f), FA_COL8(56.f)};
 #undef FA_COL8
 
-// n / d for 0 <= n < 2^31 by a multiplication: with s = 31 + ceil(log2 d) and
-// m = floor(2^s / d) + 1 the error n (m d - 2^s) / (d 2^s) stays below 1 / d.
-// Every role works its units out behind three such divisions; with the
-// compiler's integer division they took 1000 cycles of each unit's boundary.
-struct FastDiv {
-    uint32_t m = 0;
-    int s = 0;
-    FastDiv() = default;
-    explicit FastDiv(int d) {
-        int c = 0;
-        while ((1ll << c) < d) ++c;
-        s = 31 + c;
-        m = (uint32_t)((1ull << s) / (uint64_t)d + 1);
-    }
-    __device__ __forceinline__ int operator()(int n) const {
-        return (int)(((uint64_t)(uint32_t)n * m) >> s);
-    }
-};
-
 struct TcParams {
     int B, T;        // dense / masked: sequence length (row stride of q/k/v/out)
     int q0, Tq, Tk;  // dense: query rows [q0, q0 + Tq) of each sequence against keys [0, Tk)
@@ -127,7 +108,7 @@ struct TcParams {
     // units of one rank (dense: of one query entry, all sequences; paged: of one work entry), their split
     // by kv heads and by the heads (head pairs) of a group
     int per_rank, per_head;
-    FastDiv div_rank, div_hkv, div_head;
+    FastDiv div_rank, div_hkv, div_head;  // (with the compiler's division every role lost 1000 cycles at a unit's boundary)
     uint16_t* out;
     float* lse;
     // masked

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(256, 4) mrope_append_kernel(const void* __rest
                                                            const float* __restrict__ cos_sin, int max_pos, uint16_t* __restrict__ q_out,
                                                            uint16_t* __restrict__ kc, uint16_t* __restrict__ vc,
                                                            const int32_t* __restrict__ slots, int N, int Hq, int Hkv,
-                                                           int tokens, int num_blocks, DevCtx ctx) {
+                                                           int tokens, int num_blocks, FastDiv div_rpt, DevCtx ctx) {
     constexpr int half = D / 2, cph = half / 8;  // 8-pair chunks per row
     __shared__ __align__(16) float factors[kMropeTokens][D];
     __shared__ int slot_of[kMropeTokens];  // cache slot, -1: not cached
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(256, 4) mrope_append_kernel(const void* __rest
     int row = threadIdx.x / cph;
     auto load = [&](RawPair<kF32>& x, int r) {
         if (r >= rows) return;
-        const long tok = tok0 + r / rpt;
-        const int h = r % rpt;
+        const int t = div_rpt(r), h = r - t * rpt;
+        const long tok = tok0 + t;
         const long src = h < Hq ? (tok * Hq + h) * D : (tok * Hkv + (h - Hq)) * D;
         x.load(h < Hq ? q : k, src + c * 8, src + half + c * 8);
     };
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(256, 4) mrope_append_kernel(const void* __rest
     }
     __syncthreads();
     for (; row < rows; row += kStep) {
-        const int t = row / rpt, r = row % rpt;
+        const int t = div_rpt(row), r = row - t * rpt;
         const long tok = tok0 + t;
         const bool is_q = r < Hq;
         const int slot = slot_of[t];
@@ -662,7 +662,7 @@ fa_status fa_cache_append_mrope(const void* q, const void* k, const void* v, con
     kernel<<<(N + tokens - 1) / tokens, 256, 0, s>>>(q, k, v, positions, n_axes, axes, cos_sin, max_pos,
                                                      static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_cache),
                                                      static_cast<uint16_t*>(v_cache), slot_mapping, N, Hq, Hkv, tokens,
-                                                     num_blocks, ctx);
+                                                     num_blocks, FastDiv(Hq + Hkv), ctx);
     st = cuda_status(cudaGetLastError());
     if (st == FA_OK) set_launch_count(1);
     return st;

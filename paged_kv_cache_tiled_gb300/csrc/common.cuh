@@ -329,6 +329,21 @@ __device__ __forceinline__ float tanh_abs(float u) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+// n / d for 0 <= n < 2^31 by a multiplication: with s = 31 + ceil(log2 d) and
+// m = floor(2^s / d) + 1 the error n (m d - 2^s) / (d 2^s) stays below 1 / d.
+struct FastDiv {
+    uint32_t m = 0;
+    int s = 0;
+    FastDiv() = default;
+    explicit FastDiv(int d) {
+        int c = 0;
+        while ((1ll << c) < d) ++c;
+        s = 31 + c;
+        m = (uint32_t)((1ull << s) / (uint64_t)d + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> s); }
+};
+
 // ------------------------------------------------------- score modifiers ---
 // Logit of query position i and key position j for dot product s, in log2
 // units:  f(s) - slope_h log2(e) |i - j|,  f(s) = s scale log2(e), or with a cap
