@@ -368,6 +368,10 @@ fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache,
  * prefix_lens int32 [num_seqs] (in cache positions) and no documents.
  *   lse   fp32 [total_q, Hq] natural-log log-sum-exp of the visible logits, or
  *         NULL
+ * Chunks of few queries over long contexts are shared by several SMs along their
+ * keys and joined by log-sum-exp: the workspace then holds the shares' partial
+ * results (up to 42 MB at d = 128).  The shares depend on the lengths alone, so
+ * equal inputs give equal bits.
  * With a window, blocks that no query of a chunk sees are not read, nor are
  * their block-table entries (they may have been freed); a block that is partly
  * visible must hold finite values.  Everything else as for fa_paged_attn.

@@ -127,6 +127,9 @@ struct TcParams {
     const int32_t* work_count;
     int mbps, num_blocks;
     // modified variants
+    const int4* pieces;  // paged: (sequence, first query token, first | end << 16 of its KV tiles, place of its partial results or -1)
+    float4* part_o;      // partial results: [d / 4][256 rows] each
+    float2* part_ml;     // and the rows' running max (log2 units) and sum
     ScoreMod mod;
     CapPoly cap;
     const int2* doc_rows;      // dense: per row of [B, T] its document's [first, end), empty for padding; or null
@@ -146,6 +149,7 @@ struct Unit {
     int kt0;        // first KV tile to scan
     int n_kt;       // KV tiles to scan: [kt0, n_kt)
     int kv_lo;      // modified variants: first key any row of the unit sees
+    int slot;       // modified paged variants: place of the unit's partial results, -1: it has all of its keys
     int holes;      // masked: some tile in [kt0, n_kt) is all -inf for both slots (must be skipped)
 };
 
@@ -213,9 +217,17 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
     Unit U;
     U.holes = 0;
     U.kv_lo = 0;
+    U.slot = -1;
     if constexpr (MODE == MODE_PAGED) {
         const int e = p.div_rank(u), rest = u - e * p.per_rank;
-        const int seq = __ldg(p.work_list + 2 * e), t0 = __ldg(p.work_list + 2 * e + 1);
+        int4 piece = make_int4(0, 0, 0, -1);
+        if constexpr (MOD != 0)
+            piece = __ldg(p.pieces + e);
+        else {
+            piece.x = __ldg(p.work_list + 2 * e);
+            piece.y = __ldg(p.work_list + 2 * e + 1);
+        }
+        const int seq = piece.x, t0 = piece.y;
         const int ql = __ldg(p.q_lens + seq), cl = __ldg(p.ctx_lens + seq), qs = __ldg(p.q_start + seq);
         U.b = seq;
         int slot_tokens = kTcRows;
@@ -247,8 +259,9 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
         U.pos_off = cl - ql;
         if constexpr (MOD != 0) {
             U.kv_lo = row_range<MODE>(p, seq, U.row0[0], U.pos_off + U.row0[0], cl).x;
-            U.kt0 = U.kv_lo / kTcRows;
-            U.n_kt = (row_range<MODE>(p, seq, last - 1, U.pos_off + last - 1, cl).y + kTcRows - 1) / kTcRows;
+            U.kt0 = piece.z & 0xffff;
+            U.n_kt = (int)((unsigned)piece.z >> 16);
+            U.slot = piece.w < 0 ? -1 : piece.w + rest;
         } else {
             const int kv_end = p.causal ? min(cl, cl - ql + last) : cl;
             U.kt0 = 0;
@@ -372,6 +385,28 @@ template <int D>
 __device__ __noinline__ void store_zero_row(uint16_t* orow, float* lse) {
     for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(orow + c) = make_uint4(0, 0, 0, 0);
     if (lse) *lse = -INFINITY;
+}
+
+// A row's partial result: its D channels of O from TMEM at taddr, divided by the
+// sum l, the running max m and l.  Four channels of a unit's 256 rows lie side by
+// side (o: this row's first four), so a warp's stores are whole lines: row by
+// row, 32 rows' lines to a store, they took 4 us a unit.
+template <int D>
+__device__ __noinline__ void store_partial_row(uint32_t taddr, float4* o, float2* ml, float m, float l) {
+    const float inv_l = l > 0.f ? 1.f / l : 0.f;
+    __syncwarp();  // warp-collective TMEM accesses follow
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t raw[32];
+        tmem_ld32(taddr + c * 32, raw);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            o[(c * 8 + j) * 2 * kTcRows] =
+                make_float4(__uint_as_float(raw[4 * j]) * inv_l, __uint_as_float(raw[4 * j + 1]) * inv_l,
+                            __uint_as_float(raw[4 * j + 2]) * inv_l, __uint_as_float(raw[4 * j + 3]) * inv_l);
+    }
+    *ml = make_float2(m, l);
 }
 
 // Zeroes rows [z0, z1) of a staged K/V tile (both 64-channel atoms; every
@@ -574,6 +609,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         *abort_flag = 0;
         mbar_fence_init();
     }
+    // (the kernels that may follow a paged call wait for this grid's end before they read its results)
+    if constexpr (MOD != 0 && MODE == MODE_PAGED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // documents: launched while their ranges are still being found (griddepcontrol.wait
     // returns at once for any other launch)
     if constexpr (MOD != 0 && MODE == MODE_DENSE)
@@ -1285,6 +1322,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             ++oc;
             tc_fence_after();
+            if constexpr (MODE == MODE_PAGED && MOD != 0)
+                if (E.slot >= 0) {  // a piece of the keys: the join kernel puts the pieces together
+                    const int at = s * kTcRows + r;
+                    store_partial_row<D>(trow + o_col, p.part_o + (long)E.slot * (D / 4) * 2 * kTcRows + at,
+                                         p.part_ml + (long)E.slot * 2 * kTcRows + at, m, l);
+                    continue;
+                }
             uint16_t* orow = out_row<D, MODE>(p, E, s, tok, hl);
             const float inv_l = l > 0.f ? 1.f / l : 0.f;
             // 64 columns per TMEM wait; 32-byte stores of the bf16 row
@@ -1695,7 +1739,8 @@ fa_status launch_paged_prefill(const void* q, const void* k_cache, const void* v
                                const int32_t* ctx_lens, const int32_t* q_lens, const int32_t* q_start,
                                const int32_t* work_list, const int32_t* work_count, void* out, int num_seqs,
                                int mbps, int num_blocks, int Hq, int Hkv, int d, int causal, float scale,
-                               int total_q, cudaStream_t s, const DevCtx& ctx, const ScoreMod* mod) {
+                               int total_q, cudaStream_t s, const DevCtx& ctx, const ScoreMod* mod,
+                               const int4* pieces, float4* part_o, float2* part_ml) {
     (void)num_seqs;
     CUtensorMap tq, tk, tv;
     const bool pack = paged_tc_pack(Hq / Hkv);
@@ -1717,6 +1762,9 @@ fa_status launch_paged_prefill(const void* q, const void* k_cache, const void* v
     if (mod) {
         p.mod = *mod;
         p.lse = mod->lse;
+        p.pieces = pieces;
+        p.part_o = part_o;
+        p.part_ml = part_ml;
         return launch_tc_mod<MODE_PAGED>(d, tq, tk, tv, p, sm_count(), s);
     }
     return launch_tc_d<MODE_PAGED>(d, tq, tk, tv, p, sm_count(), s);

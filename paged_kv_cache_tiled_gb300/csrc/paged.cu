@@ -44,7 +44,8 @@ fa_status launch_paged_prefill(const void* q, const void* k_cache, const void* v
                                const int32_t* ctx_lens, const int32_t* q_lens, const int32_t* q_start,
                                const int32_t* work_list, const int32_t* work_count, void* out, int num_seqs,
                                int mbps, int num_blocks, int Hq, int Hkv, int d, int causal, float scale,
-                               int total_q, cudaStream_t s, const DevCtx& ctx, const ScoreMod* mod);
+                               int total_q, cudaStream_t s, const DevCtx& ctx, const ScoreMod* mod,
+                               const int4* pieces, float4* part_o, float2* part_ml);
 // Weight sums of the sequences that take the tensor-core path (attn_colsum.cu).
 fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* block_table, const int32_t* ctx_lens,
                              const int32_t* q_lens, const int32_t* q_start, const int32_t* k_start,
@@ -1067,19 +1068,39 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
 // the sequences that take the tensor-core kernel, ordered by decreasing number
 // of KV tiles (longest first) with a counting sort.  Entry = (sequence, first
 // query token of the entry within the chunk).
+//
+// Calls with modified scores get `pieces` instead: an entry whose KV tiles are
+// many for the work there is (few chunks over long contexts) is cut along its
+// keys, so that the call still fills the GPU; its pieces leave partial results
+// that paged_join_kernel puts together.  With `share` the tiles of all units for
+// each SM, a piece has at least four tiles (a unit's fixed cost is that of
+// three), the share up to six of them (a GPU that is nearly full gains nothing
+// from pieces of four: 4 chunks of 300 over 1000 keys 44 us, whole 33), and half
+// the share beyond.  Measured, 32 heads in 8 groups, d = 128: a chunk of 128
+// over 4000 keys 90 us whole, 35 in pieces; one of 512 over 30000 376 and 146;
+// 16 chunks of 64 over up to 8000 (12 heads in 2 groups) 107 and 73.
+constexpr int kSplitTiles = 4, kSplitShare = 6;
+constexpr int kSplitMost = 32;  // pieces of an entry: the join takes 0.3 us for each
+constexpr int kSplitSlots = 2 * kMaxStreamCtas;  // total / least, at most
 __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restrict__ ctx_lens,
                                                           const int32_t* __restrict__ q_lens, int num_seqs, int mbps,
                                                           int g, int causal, int entry_tokens,
                                                           int32_t* __restrict__ q_start, int32_t* __restrict__ count,
                                                           int32_t* __restrict__ list, int max_entries,
                                                           int window, const int32_t* __restrict__ prefix,
-                                                          int32_t* __restrict__ k_start, int acc_len, DevCtx ctx) {
+                                                          int32_t* __restrict__ k_start, int acc_len,
+                                                          int4* __restrict__ pieces, int4* __restrict__ split,
+                                                          int max_slots, int per_rank, DevCtx ctx) {
     extern __shared__ int hist[];  // [nbins + 1]
     __shared__ int warp_sums[32];
-    __shared__ int carry;
+    __shared__ int carry, n_slots, n_split;
+    __shared__ unsigned long long all_tiles;
     const int nbins = (mbps * kBS + 127) / 128 + 1;
     for (int i = threadIdx.x; i <= nbins; i += blockDim.x) hist[i] = 0;
-    if (threadIdx.x == 0) carry = 0;
+    if (threadIdx.x == 0) {
+        carry = n_slots = n_split = 0;
+        all_tiles = 0;
+    }
     __syncthreads();
     // prefix sum of q_lens, 1024 sequences per pass
     for (int base = 0; base < num_seqs; base += blockDim.x) {
@@ -1160,14 +1181,35 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         }
         if (threadIdx.x == 0) k_start[num_seqs] = carry;
     }
-    // histogram of entry costs
-    auto entry_cost = [&](int s, int ql, int cl, int t0) {
-        const int last_row = min(ql, t0 + entry_tokens) - 1;  // last query row of the entry
-        int kv_end = causal ? cl - ql + last_row + 1 : cl;
-        if (causal && prefix) kv_end = max(kv_end, min(cl, prefix[s]));
-        const int kt0 = window > 0 ? max(0, cl - ql + t0 - window + 1) / 128 : 0;
-        return (kv_end + 127) / 128 - kt0;
+    // an entry's KV tiles [x, y): from the first key its first row sees to the last its last row sees
+    auto entry_tiles = [&](int s, int ql, int cl, int t0) {
+        const int first = cl - ql + t0, last = cl - ql + min(ql, t0 + entry_tokens) - 1;  // positions
+        int hi = causal ? last + 1 : (window > 0 ? last + window : cl);
+        if (causal && prefix) hi = max(hi, prefix[s]);
+        const int lo = window > 0 ? max(0, first - window + 1) : 0;
+        return make_int2(lo / 128, (min(hi, cl) + 127) / 128);
     };
+    auto is_chunk = [&](int ql, int cl) { return ql > 0 && !is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS; };
+    int least = 0;  // tiles of a piece, at least; 0: no entry is cut
+    if (max_slots > 0) {
+        unsigned long long tiles = 0;
+        for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
+            const int ql = q_lens[s], cl = ctx_lens[s];
+            if (!is_chunk(ql, cl)) continue;
+            for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
+                const int2 t = entry_tiles(s, ql, cl, t0);
+                tiles += t.y - t.x;
+            }
+        }
+        if (tiles) atomicAdd(&all_tiles, tiles);
+        __syncthreads();
+        const unsigned long long total = all_tiles * per_rank, share = (total + kMaxStreamCtas - 1) / kMaxStreamCtas;
+        unsigned long long t = max((unsigned long long)kSplitTiles, max(min(share, (unsigned long long)kSplitShare), (share + 1) / 2));
+        t = max(t, (total + max_slots - 1) / max_slots);  // their partial results fit
+        least = (int)min(t, 1ull << 30);
+    }
+    auto cuts = [&](int tiles) { return least > 0 && tiles >= 2 * least ? min(kSplitMost, tiles / least) : 1; };
+    // histogram of the costs
     for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
         const int ql = q_lens[s], cl = ctx_lens[s];
         if (ql <= 0 || is_decode_row(ql, g)) continue;
@@ -1175,7 +1217,11 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
             raise_error(ctx, ERR_BOUNDS_BIT);
             continue;
         }
-        for (int t0 = 0; t0 < ql; t0 += entry_tokens) atomicAdd(&hist[entry_cost(s, ql, cl, t0)], 1);
+        for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
+            const int2 t = entry_tiles(s, ql, cl, t0);
+            const int tiles = t.y - t.x, n = cuts(tiles);
+            for (int i = 0; i < n; ++i) atomicAdd(&hist[(i + 1) * tiles / n - i * tiles / n], 1);
+        }
     }
     __syncthreads();
     if (threadIdx.x == 0) {  // bucket starts, highest cost first
@@ -1193,14 +1239,101 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     __syncthreads();
     for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
         const int ql = q_lens[s], cl = ctx_lens[s];
-        if (ql <= 0 || is_decode_row(ql, g) || ql > cl || cl > mbps * kBS) continue;
+        if (!is_chunk(ql, cl)) continue;
         for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
-            const int pos = atomicAdd(&hist[entry_cost(s, ql, cl, t0)], 1);
-            if (pos < max_entries) {
-                list[2 * pos] = s;
-                list[2 * pos + 1] = t0;
+            const int2 t = entry_tiles(s, ql, cl, t0);
+            const int tiles = t.y - t.x, n = cuts(tiles);
+            int slot = -1;
+            if (n > 1) {
+                slot = atomicAdd(&n_slots, n * per_rank);
+                split[atomicAdd(&n_split, 1)] = make_int4(s, t0, slot, n);
+            }
+            for (int i = 0; i < n; ++i) {
+                const int a = i * tiles / n, b = (i + 1) * tiles / n;
+                const int pos = atomicAdd(&hist[b - a], 1);
+                if (pos >= max_entries) continue;
+                if (pieces) {
+                    pieces[pos] = make_int4(s, t0, (t.x + a) | (t.x + b) << 16, n > 1 ? slot + i * per_rank : -1);
+                } else {
+                    list[2 * pos] = s;
+                    list[2 * pos + 1] = t0;
+                }
             }
         }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) count[3] = n_split;
+}
+
+// Rows of the entries that were cut along their keys: the pieces' partial
+// results weighed by their sums 2^(m_i - M) l_i and added in order, and the
+// log-sum-exp.  A warp takes 16 channels of 32 rows, a row a lane; what it reads
+// is mostly in the L2 that it was just written to.
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_kernel(const int4* split, const int32_t* count, const float4* part_o,
+                                                         const float2* part_ml, const int32_t* __restrict__ q_lens,
+                                                         const int32_t* __restrict__ q_start, uint16_t* __restrict__ out,
+                                                         float* __restrict__ lse, int per_rank, int Hq, int g) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kSlices = D / 16;
+    const int lane = threadIdx.x & 31;
+    const long items = (long)__ldcg(count + 3) * per_rank * 8 * kSlices;
+    const bool pack = paged_tc_pack(g);
+    for (long idx = (long)blockIdx.x * 8 + (threadIdx.x >> 5); idx < items; idx += (long)gridDim.x * 8) {
+        const int slice = (int)(idx % kSlices), row = (int)(idx / kSlices % 8) * 32 + lane;
+        const int unit = (int)(idx / (8 * kSlices)), rest = unit % per_rank;
+        const int4 e = __ldcg(split + unit / per_rank);
+        const int ql = __ldg(q_lens + e.x), qs = __ldg(q_start + e.x);
+        const float2* ml = part_ml + (long)(e.z + rest) * 256 + row;
+        const float4* src = part_o + ((long)(e.z + rest) * (D / 4) + slice * 4) * 256 + row;
+        float M = -INFINITY, sum = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < e.w; ++i) {
+            const float2 x = __ldcg(ml + (long)i * per_rank * 256);
+            if (x.y > 0.f) M = fmaxf(M, x.x);
+        }
+        float acc[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) acc[c] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < e.w; ++i) {
+            const float2 x = __ldcg(ml + (long)i * per_rank * 256);
+            float4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = __ldcg(src + ((long)i * per_rank * (D / 4) + j) * 256);
+            const float f = x.y > 0.f ? x.y * fast_exp2(x.x - M) : 0.f;  // (a piece without a visible key has no share)
+            sum += f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[4 * j] = f > 0.f ? fmaf(f, v[j].x, acc[4 * j]) : acc[4 * j];
+                acc[4 * j + 1] = f > 0.f ? fmaf(f, v[j].y, acc[4 * j + 1]) : acc[4 * j + 1];
+                acc[4 * j + 2] = f > 0.f ? fmaf(f, v[j].z, acc[4 * j + 2]) : acc[4 * j + 2];
+                acc[4 * j + 3] = f > 0.f ? fmaf(f, v[j].w, acc[4 * j + 3]) : acc[4 * j + 3];
+            }
+        }
+        // as the attention lays a unit's two slots out
+        int tok, head;
+        if (pack) {
+            tok = e.y + row / g;
+            head = rest * g + row % g;
+        } else if (g % 2 == 0) {
+            tok = e.y + (row & 127);
+            head = rest / (g / 2) * g + 2 * (rest % (g / 2)) + (row >> 7);
+        } else {
+            tok = e.y + row;
+            head = rest;
+        }
+        if (tok >= ql) continue;
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const long at = ((long)qs + tok) * Hq + head;
+        if (lse && slice == 0) lse[at] = sum > 0.f ? (M + __log2f(sum)) * kLn2f : -INFINITY;
+        uint4* dst = reinterpret_cast<uint4*>(out + at * D + slice * 16);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            dst[j] = make_uint4(pack_bf16x2(acc[8 * j] * inv, acc[8 * j + 1] * inv),
+                                pack_bf16x2(acc[8 * j + 2] * inv, acc[8 * j + 3] * inv),
+                                pack_bf16x2(acc[8 * j + 4] * inv, acc[8 * j + 5] * inv),
+                                pack_bf16x2(acc[8 * j + 6] * inv, acc[8 * j + 7] * inv));
     }
 }
 
@@ -1294,6 +1427,34 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
     return FA_OK;
 }
 
+// Behind the attention's own workspace, calls with modified scores keep their
+// pieces and the partial results of those that do not have all of their keys:
+// as many as the tables' tiles and the queries could ask for, at most kSplitSlots.
+struct PiecesWs {
+    int slots, per_rank, max_pieces;
+    size_t list, split, ml, o, total;
+};
+static PiecesWs pieces_ws_layout(const PagedWs& w, int num_seqs, int mbps, int Hq, int Hkv, int d, int total_q,
+                                 int max_q_len) {
+    PiecesWs x{};
+    const int g = Hq / Hkv;
+    x.per_rank = paged_tc_pack(g) ? Hkv : (g % 2 == 0 ? Hkv * (g / 2) : Hq);
+    const long tiles = ((long)mbps * kBS + 127) / 128, entries = total_q / paged_tc_entry_tokens(g) + (long)num_seqs;
+    // (an entry is cut into tiles / kSplitTiles pieces at most, and only when that is two or more)
+    // (none for queries that make a unit for every SM anyway: the join's launch would cost 3 us)
+    const bool few = max_q_len > 0 && !is_decode_row(max_q_len, g) &&
+                     total_q / paged_tc_entry_tokens(g) * (long)x.per_rank < kMaxStreamCtas;
+    const long cuts = !few || tiles / kSplitTiles < 2 ? 0 : std::min<long>(tiles / kSplitTiles, kSplitSlots);
+    x.slots = (int)std::min<long>(kSplitSlots, std::min<long>(entries, kSplitSlots) * x.per_rank * cuts);
+    x.max_pieces = w.max_entries + x.slots;
+    x.list = align256(w.total);
+    x.split = align256(x.list + sizeof(int4) * (size_t)x.max_pieces);
+    x.ml = align256(x.split + sizeof(int4) * (size_t)(x.slots / 2 + 1));
+    x.o = align256(x.ml + sizeof(float2) * 256 * (size_t)x.slots);
+    x.total = align256(x.o + sizeof(float) * 256 * (size_t)x.slots * d);
+    return x;
+}
+
 // Weight sums wanted by a call (fa_paged_attn_accum), and where its workspace
 // keeps, behind the attention's own, the first unit of every chunk and the
 // decode rows' logits: min(16, g * max_q_len) rows of 16 for every page that the
@@ -1332,8 +1493,9 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned32(out)) return FA_ERR_INVALID_ARG;
     if (num_blocks == 0 || max_blocks_per_seq == 0) return FA_ERR_INVALID_ARG;
     const PagedWs w = paged_ws_layout(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q);
-    const AccumWs aw = acc ? accum_ws_layout(w.total, num_seqs, max_blocks_per_seq, Hq, Hkv, max_q_len) : AccumWs{};
-    if (!ws || ws_bytes < (acc ? aw.total : w.total) || (reinterpret_cast<uintptr_t>(ws) & 255)) return FA_ERR_WORKSPACE;
+    const PiecesWs pw = mod ? pieces_ws_layout(w, num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len) : PiecesWs{};
+    const AccumWs aw = acc ? accum_ws_layout(pw.total, num_seqs, max_blocks_per_seq, Hq, Hkv, max_q_len) : AccumWs{};
+    if (!ws || ws_bytes < (acc ? aw.total : mod ? pw.total : w.total) || (reinterpret_cast<uintptr_t>(ws) & 255)) return FA_ERR_WORKSPACE;
     fa_status st = check_device();
     if (st != FA_OK) return st;
     DevCtx ctx;
@@ -1368,10 +1530,14 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
             ms = ss->s;
         }
         paged_meta_kernel<<<1, 1024, hist_bytes, ms>>>(ctx_lens, q_lens, num_seqs, max_blocks_per_seq, g, causal,
-                                                       entry_tokens, q_start, count, list, w.max_entries,
+                                                       entry_tokens, q_start, count, list,
+                                                       mod ? pw.max_pieces : w.max_entries,
                                                        mod ? mod->window : 0, mod ? mod->prefix : nullptr,
                                                        acc ? reinterpret_cast<int32_t*>(wsb + aw.k_start) : nullptr,
-                                                       acc ? acc->len : 0, ctx);
+                                                       acc ? acc->len : 0,
+                                                       mod ? reinterpret_cast<int4*>(wsb + pw.list) : nullptr,
+                                                       mod ? reinterpret_cast<int4*>(wsb + pw.split) : nullptr,
+                                                       pw.slots, pw.per_rank, ctx);
         const bool launched = cudaGetLastError() == cudaSuccess;
         if (ss && (cudaEventRecord(ss->join, ss->s) != cudaSuccess || !launched)) {
             (void)cudaStreamWaitEvent(s, ss->join, 0);  // leave the side stream joined
@@ -1412,9 +1578,29 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         int32_t* list = reinterpret_cast<int32_t*>(wsb + w.work_list);
         st = launch_paged_prefill(q, k_cache, v_cache, block_table, ctx_lens, q_lens, q_start, list, count, out,
                                   num_seqs, max_blocks_per_seq, num_blocks, Hq, Hkv, d, causal, scale, total_q, s,
-                                  ctx, mod);
+                                  ctx, mod, mod ? reinterpret_cast<const int4*>(wsb + pw.list) : nullptr,
+                                  reinterpret_cast<float4*>(wsb + pw.o), reinterpret_cast<float2*>(wsb + pw.ml));
         if (st != FA_OK) return st;
         ++launches;
+        if (pw.slots > 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(4 * sm_count());
+            cfg.blockDim = dim3(256);
+            cfg.stream = s;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            auto join = d == 128 ? paged_join_kernel<128> : paged_join_kernel<64>;
+            if (cudaLaunchKernelEx(&cfg, join, reinterpret_cast<const int4*>(wsb + pw.split),
+                                   static_cast<const int32_t*>(count), reinterpret_cast<const float4*>(wsb + pw.o),
+                                   reinterpret_cast<const float2*>(wsb + pw.ml), q_lens,
+                                   static_cast<const int32_t*>(q_start), static_cast<uint16_t*>(out), mod->lse, pw.per_rank, Hq,
+                                   g) != cudaSuccess)
+                return FA_ERR_CUDA;
+            ++launches;
+        }
     }
     if (acc) {
         // rows whose queries took the decode kernel (and sequences without
@@ -1475,7 +1661,9 @@ fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache,
 size_t fa_paged_attn_mod_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv, int d, int total_q,
                                         int max_q_len) {
     if (max_q_len < 0) return 0;
-    return fa_paged_attn_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q);
+    if (fa_paged_attn_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q) == 0 || Hq % Hkv != 0) return 0;
+    const PagedWs w = paged_ws_layout(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q);
+    return pieces_ws_layout(w, num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len).total;
 }
 
 fa_status fa_paged_attn_mod(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,

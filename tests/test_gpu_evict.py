@@ -118,6 +118,13 @@ def test_accum_wide_tables(F):
     run_accum(F, p, bias=True)
 
 
+def test_accum_chunks_over_long_contexts(F):
+    """The sums go by the log-sum-exp that the pieces' join writes."""
+    p = R.Paged(44, [3500, 60, 1800], [50, 1, 100], 8, 2, 128)
+    run_accum(F, p, decay=0.5)
+    run_accum(F, p, bias=True, prefix=[3480, 60, 500])
+
+
 def test_accum_many_sequences(F):
     """More sequences than a warp, of all kinds, so that places and units run over many of them."""
     n = 70

@@ -406,3 +406,44 @@ def test_prefix_of_the_lowest_value(F):
     assert torch.equal(F.fa_prefill_mod(*x, prefix_lens=pre), F.fa_prefill_mod(*x, window=1 << 30))
     with pytest.raises(ValueError):
         F.fa_prefill_mod(*x, window=1 << 32)
+
+
+# chunks over contexts long enough that their keys are shared by several work units
+LONG_MODS = [dict(), dict(cap=30.0), dict(bias=True), dict(window=1500), dict(window=900, bias=True, cap=25.0),
+             dict(prefix=[3900, 0, 90, 700]), dict(causal=False, window=1100), dict(causal=False, cap=12.0)]
+
+
+@pytest.mark.parametrize("mod", LONG_MODS, ids=str)
+@pytest.mark.parametrize("heads", [(4, 1, 128), (6, 1, 64), (3, 1, 128), (1, 1, 64), (16, 2, 64)], ids=str)
+def test_paged_mod_chunks_over_long_contexts(F, heads, mod):
+    """Cut along their keys, beside a short chunk and a single token; with a window some rows see nothing in a piece."""
+    p = R.Paged(41, [4000, 1700, 90, 2500], [70, 33, 40, 1], *heads, std=4.0 if mod.get("cap") else 1.0,
+                window=mod.get("window", 0))
+    run_paged(F, p, max_q_len=70, **mod)
+
+
+def test_paged_mod_more_pieces_than_lanes(F):
+    p = R.Paged(42, [27000], [24], 2, 1, 64)
+    run_paged(F, p)
+    run_paged(F, p, bias=True, cap=20.0)
+
+
+def test_paged_mod_long_chunks_replayed(F):
+    """One captured call, replayed on contexts that are cut and on some that are not; twice the same call, the same bits."""
+    p = R.Paged(43, [3000, 2000], [40, 90], 8, 2, 128)
+    q, kc, vc, table, ctx, ql = p.cuda()
+    ctxs = [ctx.clone(), torch.tensor([300, 100], dtype=torch.int32, device="cuda"),
+            torch.tensor([1999, 1111], dtype=torch.int32, device="cuda")]
+    want = [F.fa_paged_attn_mod(q, kc, vc, table, c, ql, window=2500, max_q_len=90) for c in ctxs]
+    out = torch.empty_like(q)
+    ws = torch.full((F.fa_paged_attn_mod_workspace_size(2, table.shape[1], 8, 2, 128, q.shape[0], 90),), 255,
+                    dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        F.fa_paged_attn_mod(q, kc, vc, table, ctx, ql, window=2500, max_q_len=90, out=out, ws=ws)
+    for c, w in zip(ctxs + ctxs[::-1], want + want[::-1]):
+        ctx.copy_(c)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, w)
+    assert F.fa_get_error() == F.FA_OK
