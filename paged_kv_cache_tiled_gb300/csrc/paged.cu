@@ -1080,8 +1080,12 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
 // over 4000 keys 90 us whole, 35 in pieces; one of 512 over 30000 376 and 146;
 // 16 chunks of 64 over up to 8000 (12 heads in 2 groups) 107 and 73.
 constexpr int kSplitTiles = 4, kSplitShare = 6;
-constexpr int kSplitMost = 32;  // pieces of an entry: the join takes 0.3 us for each
+constexpr int kSplitMost = 32;  // pieces of an entry (a warp lists them, the join takes 0.3 us for each)
 constexpr int kSplitSlots = 2 * kMaxStreamCtas;  // total / least, at most
+// (Cutting is a variant of its own: its divisions and counters in the kernel that
+// every chunked call waits for cost 5 us of 225.)
+enum { META_LIST = 0, META_PIECES = 1, META_CUT = 2 };
+template <int KIND>
 __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restrict__ ctx_lens,
                                                           const int32_t* __restrict__ q_lens, int num_seqs, int mbps,
                                                           int g, int causal, int entry_tokens,
@@ -1096,6 +1100,11 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     __shared__ int carry, n_slots, n_split;
     __shared__ unsigned long long all_tiles;
     const int nbins = (mbps * kBS + 127) / 128 + 1;
+    // the lengths of this thread's first sequence stay in registers: every step below asks for them
+    const int ql0 = threadIdx.x < num_seqs ? __ldg(q_lens + threadIdx.x) : 0;
+    const int cl0 = threadIdx.x < num_seqs ? __ldg(ctx_lens + threadIdx.x) : 0;
+    auto q_len = [&](int s) { return s == threadIdx.x ? ql0 : __ldg(q_lens + s); };
+    auto ctx_len = [&](int s) { return s == threadIdx.x ? cl0 : __ldg(ctx_lens + s); };
     for (int i = threadIdx.x; i <= nbins; i += blockDim.x) hist[i] = 0;
     if (threadIdx.x == 0) {
         carry = n_slots = n_split = 0;
@@ -1105,7 +1114,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     // prefix sum of q_lens, 1024 sequences per pass
     for (int base = 0; base < num_seqs; base += blockDim.x) {
         const int s = base + threadIdx.x;
-        int v = s < num_seqs ? q_lens[s] : 0;
+        int v = s < num_seqs ? q_len(s) : 0;
         int x = v;
         const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
@@ -1136,10 +1145,10 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     // lengths; the order only decides who goes first), then their units of 256
     // keys in that order (none for a sequence whose sums do not fit, which is
     // reported, and for those without a chunk)
-    if (k_start) {
+    if (KIND != META_LIST && k_start) {
         __shared__ int order[64];
         int32_t* k_seq = k_start + num_seqs + 1;
-        auto rank_bin = [&](int s) { return 63 - min(63, max(0, q_lens[s]) / 32); };
+        auto rank_bin = [&](int s) { return 63 - min(63, max(0, q_len(s)) / 32); };
         __syncthreads();
         if (threadIdx.x < 64) order[threadIdx.x] = 0;
         if (threadIdx.x == 0) carry = 0;
@@ -1190,11 +1199,11 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         return make_int2(lo / 128, (min(hi, cl) + 127) / 128);
     };
     auto is_chunk = [&](int ql, int cl) { return ql > 0 && !is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS; };
-    int least = 0;  // tiles of a piece, at least; 0: no entry is cut
-    if (max_slots > 0) {
+    [[maybe_unused]] int least = 1;  // tiles of a piece, at least
+    if constexpr (KIND == META_CUT) {
         unsigned long long tiles = 0;
         for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
-            const int ql = q_lens[s], cl = ctx_lens[s];
+            const int ql = q_len(s), cl = ctx_len(s);
             if (!is_chunk(ql, cl)) continue;
             for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
                 const int2 t = entry_tiles(s, ql, cl, t0);
@@ -1208,10 +1217,17 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         t = max(t, (total + max_slots - 1) / max_slots);  // their partial results fit
         least = (int)min(t, 1ull << 30);
     }
-    auto cuts = [&](int tiles) { return least > 0 && tiles >= 2 * least ? min(kSplitMost, tiles / least) : 1; };
+    auto cuts = [&](int tiles) { return KIND == META_CUT && tiles >= 2 * least ? min(kSplitMost, tiles / least) : 1; };
+    auto cut = [](int i, int n, int tiles) {  // end of piece i
+        return i + 1 == n ? tiles : (KIND == META_CUT ? (i + 1) * tiles / n : 0);
+    };
+    // a thread per sequence, or a warp whose lanes are an entry's pieces
+    constexpr bool cutting = KIND == META_CUT;
+    const int seq0 = cutting ? threadIdx.x >> 5 : threadIdx.x, seq_step = cutting ? blockDim.x >> 5 : blockDim.x;
+    const int lane_piece = cutting ? threadIdx.x & 31 : 0;
     // histogram of the costs
-    for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
-        const int ql = q_lens[s], cl = ctx_lens[s];
+    for (int s = seq0; s < num_seqs; s += seq_step) {
+        const int ql = q_len(s), cl = ctx_len(s);
         if (ql <= 0 || is_decode_row(ql, g)) continue;
         if (ql > cl || cl > mbps * kBS) {
             raise_error(ctx, ERR_BOUNDS_BIT);
@@ -1219,50 +1235,61 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         }
         for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
             const int2 t = entry_tiles(s, ql, cl, t0);
-            const int tiles = t.y - t.x, n = cuts(tiles);
-            for (int i = 0; i < n; ++i) atomicAdd(&hist[(i + 1) * tiles / n - i * tiles / n], 1);
+            const int tiles = t.y - t.x, n = cuts(tiles), i = lane_piece;
+            if (i < n) atomicAdd(&hist[cut(i, n, tiles) - cut(i - 1, n, tiles)], 1);
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) {  // bucket starts, highest cost first
+    if (threadIdx.x < 32) {  // bucket starts, highest cost first (a warp: a wide table has thousands of buckets)
+        const int lane = threadIdx.x;
         int run = 0;
-        for (int b = nbins - 1; b >= 0; --b) {
-            const int c = hist[b];
-            hist[b] = run;
-            run += c;
+        for (int b0 = nbins - 1; b0 >= 0; b0 -= 32) {
+            const int b = b0 - lane, c = b >= 0 ? hist[b] : 0;
+            int x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b >= 0) hist[b] = run + x - c;
+            run += __shfl_sync(0xffffffffu, x, 31);
         }
-        hist[nbins] = run;
-        *count = run < max_entries ? run : max_entries;
-        count[1] = 0;  // the tensor-core kernel's unit tickets
-        count[2] = 0;  // and the weight sums'
+        if (lane == 0) {
+            *count = run < max_entries ? run : max_entries;
+            count[1] = 0;  // the tensor-core kernel's unit tickets
+            count[2] = 0;  // and the weight sums'
+        }
     }
     __syncthreads();
-    for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
-        const int ql = q_lens[s], cl = ctx_lens[s];
+    for (int s = seq0; s < num_seqs; s += seq_step) {
+        const int ql = q_len(s), cl = ctx_len(s);
         if (!is_chunk(ql, cl)) continue;
         for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
             const int2 t = entry_tiles(s, ql, cl, t0);
-            const int tiles = t.y - t.x, n = cuts(tiles);
-            int slot = -1;
-            if (n > 1) {
-                slot = atomicAdd(&n_slots, n * per_rank);
-                split[atomicAdd(&n_split, 1)] = make_int4(s, t0, slot, n);
-            }
-            for (int i = 0; i < n; ++i) {
-                const int a = i * tiles / n, b = (i + 1) * tiles / n;
-                const int pos = atomicAdd(&hist[b - a], 1);
-                if (pos >= max_entries) continue;
-                if (pieces) {
-                    pieces[pos] = make_int4(s, t0, (t.x + a) | (t.x + b) << 16, n > 1 ? slot + i * per_rank : -1);
-                } else {
-                    list[2 * pos] = s;
-                    list[2 * pos + 1] = t0;
+            const int tiles = t.y - t.x, n = cuts(tiles), i = lane_piece;
+            [[maybe_unused]] int slot = -1;
+            if (cutting && n > 1) {
+                if (i == 0) {
+                    slot = atomicAdd(&n_slots, n * per_rank);
+                    split[atomicAdd(&n_split, 1)] = make_int4(s, t0, slot, n);
                 }
+                slot = __shfl_sync(0xffffffffu, slot, 0) + i * per_rank;
+            }
+            if (i >= n) continue;
+            const int a = cut(i - 1, n, tiles), b = cut(i, n, tiles), pos = atomicAdd(&hist[b - a], 1);
+            if (pos >= max_entries) continue;
+            if constexpr (KIND != META_LIST) {
+                pieces[pos] = make_int4(s, t0, (t.x + a) | (t.x + b) << 16, slot);
+            } else {
+                list[2 * pos] = s;
+                list[2 * pos + 1] = t0;
             }
         }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) count[3] = n_split;
+    if constexpr (KIND == META_CUT) {
+        __syncthreads();
+        if (threadIdx.x == 0) count[3] = n_split;
+    }
 }
 
 // Rows of the entries that were cut along their keys: the pieces' partial
@@ -1518,8 +1545,10 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         const int nbins = (max_blocks_per_seq * kBS + 127) / 128 + 1;
         const size_t hist_bytes = sizeof(int) * (size_t)(nbins + 1);
         if (hist_bytes > 200 * 1024) return FA_ERR_UNSUPPORTED;
+        auto meta = pw.slots > 0 ? paged_meta_kernel<META_CUT>
+                                 : (mod ? paged_meta_kernel<META_PIECES> : paged_meta_kernel<META_LIST>);
         if (hist_bytes > 48 * 1024 &&
-            (st = raise_dynamic_smem(reinterpret_cast<const void*>(paged_meta_kernel), (int)hist_bytes)) != FA_OK)
+            (st = raise_dynamic_smem(reinterpret_cast<const void*>(meta), (int)hist_bytes)) != FA_OK)
             return st;
         cudaStream_t ms = s;
         if (decode_path) {
@@ -1529,7 +1558,7 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
                 return FA_ERR_CUDA;
             ms = ss->s;
         }
-        paged_meta_kernel<<<1, 1024, hist_bytes, ms>>>(ctx_lens, q_lens, num_seqs, max_blocks_per_seq, g, causal,
+        meta<<<1, 1024, hist_bytes, ms>>>(ctx_lens, q_lens, num_seqs, max_blocks_per_seq, g, causal,
                                                        entry_tokens, q_start, count, list,
                                                        mod ? pw.max_pieces : w.max_entries,
                                                        mod ? mod->window : 0, mod ? mod->prefix : nullptr,
