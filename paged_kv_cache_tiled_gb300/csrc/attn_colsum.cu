@@ -23,6 +23,9 @@
 // packed add, against two passes over the scores in the attention itself.  The
 // pace is the MMA warp's: 256 query rows per product, because eight MMAs of 128
 // columns took 950 cycles to issue and each commit and barrier check 100 to 200.
+// Eight chunks of up to 512 queries over up to 4600 keys (32 heads in 8 groups,
+// d = 128): 59 us, the tensor pipe 42 % busy, the exponential unit 41 % (one CTA
+// per 128 keys took 82 us, 128-row products in a persistent kernel 77).
 #include <cmath>
 #include <type_traits>
 

@@ -11,6 +11,13 @@
 //   * chunked prefill over the paged cache, every K/V tile gathered block by
 //     block through the block table, one copy per 16-token block (MODE_PAGED;
 //     section "Paged Attention Kernels").
+// Dense and paged mode have variants with modified scores (MOD_*): a cap, a bias
+// by distance, and a run of visible keys per row (window, prefix, documents).
+// Tiles outside a unit's runs are skipped, the others cost what a causal limit
+// does.  In paged mode a unit may then be a piece of its rows' keys (few queries
+// over a long context); its partial rows go to the workspace.  Measured at
+// d = 128: 12 heads in 2 groups, 4 prompts of 2041 tokens with a bias 60 us (44
+// without); 32 heads in 8 groups, 8192 tokens in 6 documents 151 us, capped 231.
 //
 // CTA layout (320 threads, one CTA per SM, persistent over work units):
 //   warps 0-3   softmax warpgroup of Q slot 0, warps 4-7 of Q slot 1: thread

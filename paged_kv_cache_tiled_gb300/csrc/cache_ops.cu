@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const void* __restrict
 // few tokens: their d factors are looked up once, element by element since
 // neighbouring pairs may use different rows, into shared memory, while every
 // thread already has its first rows' values on the way; then the rows of all
-// heads of those tokens are turned 16 bytes at a time.
+// heads of those tokens are turned 16 bytes at a time.  Memory bound: 4096 tokens
+// of 32 + 8 heads, d = 128, 19.3 us, 5.3 TB/s of 6.8.
 constexpr int kMaxAxes = 4;
 constexpr int kMropeTokens = 8;  // tokens per CTA, at most
 struct PairAxes {
@@ -654,7 +655,7 @@ fa_status fa_cache_append_mrope(const void* q, const void* k, const void* v, con
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // all CTAs at once (four per SM) where eight tokens each allow that: a CTA's
     // factor lookup is latency, paid once per wave (4096 tokens of 40 heads:
-    // 21 us against 24 with 4 tokens and 29 with 2)
+    // with 4 tokens 3 us more, with 2 8 more)
     const long ctas = (long)sm_count() * 4;
     const int tokens = (int)std::min<long>(kMropeTokens, (N + ctas - 1) / ctas);
     auto kernel = in_dtype == FA_F32 ? (d == 128 ? mrope_append_kernel<true, 128> : mrope_append_kernel<true, 64>)

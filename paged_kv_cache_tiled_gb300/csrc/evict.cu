@@ -11,7 +11,9 @@
 // its part (kept in registers when it has at most 4096 tokens), the parts are
 // added through distributed shared memory, and every CTA takes the same
 // decision.  evict_move_kernel gathers the kept rows.  Memory bound: the weights
-// are read once, each kept row once.
+// are read once, each kept row once.  Two sequences of 32768 tokens to 8192 (8
+// heads, d = 128): 39 us, 25 of them the copy (5.4 TB/s); 64 sequences of up to
+// 4096 to 512 (2 heads): 20.5.
 #include <algorithm>
 
 #include "host_common.cuh"

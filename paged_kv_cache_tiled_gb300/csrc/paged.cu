@@ -28,6 +28,11 @@
 //     CTA that a second kernel merges the same way.
 // Longer chunks take the tensor-core kernel (attn_tc.cu) through a work list
 // built on the device by `paged_meta_kernel`.
+// With modified scores (MOD variants) the stream holds only the blocks that a
+// window leaves, and the weight sums' variant keeps its logits for
+// `accum_decode_kernel`: 64 sequences of up to 8192 tokens with a window of 4096
+// and a cap 41 us (the stream alone 4.8 TB/s), up to 4096 tokens with the sums 39
+// us (33 without).
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
