@@ -1105,11 +1105,12 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     __shared__ int carry, n_slots, n_split;
     __shared__ unsigned long long all_tiles;
     const int nbins = (mbps * kBS + 127) / 128 + 1;
-    // the lengths of this thread's first sequence stay in registers: every step below asks for them
-    const int ql0 = threadIdx.x < num_seqs ? __ldg(q_lens + threadIdx.x) : 0;
-    const int cl0 = threadIdx.x < num_seqs ? __ldg(ctx_lens + threadIdx.x) : 0;
-    auto q_len = [&](int s) { return s == threadIdx.x ? ql0 : __ldg(q_lens + s); };
-    auto ctx_len = [&](int s) { return s == threadIdx.x ? cl0 : __ldg(ctx_lens + s); };
+    // This thread's sequences are mine, mine + 1024, ...; the lengths of the first stay in registers, every
+    // step below asks for them.  (Neighbours go to different warps when a warp works on one entry at a time.)
+    const int mine = KIND == META_CUT ? (threadIdx.x & 31) * 32 + (threadIdx.x >> 5) : threadIdx.x;
+    const int ql0 = mine < num_seqs ? __ldg(q_lens + mine) : 0, cl0 = mine < num_seqs ? __ldg(ctx_lens + mine) : 0;
+    auto q_len = [&](int s) { return s == mine ? ql0 : __ldg(q_lens + s); };
+    auto ctx_len = [&](int s) { return s == mine ? cl0 : __ldg(ctx_lens + s); };
     for (int i = threadIdx.x; i <= nbins; i += blockDim.x) hist[i] = 0;
     if (threadIdx.x == 0) {
         carry = n_slots = n_split = 0;
@@ -1207,7 +1208,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     [[maybe_unused]] int least = 1;  // tiles of a piece, at least
     if constexpr (KIND == META_CUT) {
         unsigned long long tiles = 0;
-        for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
+        for (int s = mine; s < num_seqs; s += blockDim.x) {
             const int ql = q_len(s), cl = ctx_len(s);
             if (!is_chunk(ql, cl)) continue;
             for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
@@ -1226,24 +1227,32 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     auto cut = [](int i, int n, int tiles) {  // end of piece i
         return i + 1 == n ? tiles : (KIND == META_CUT ? (i + 1) * tiles / n : 0);
     };
-    // a thread per sequence, or a warp whose lanes are an entry's pieces
-    constexpr bool cutting = KIND == META_CUT;
-    const int seq0 = cutting ? threadIdx.x >> 5 : threadIdx.x, seq_step = cutting ? blockDim.x >> 5 : blockDim.x;
-    const int lane_piece = cutting ? threadIdx.x & 31 : 0;
-    // histogram of the costs
-    for (int s = seq0; s < num_seqs; s += seq_step) {
+    // f(sequence, its lengths, first token, piece) for every entry: a thread per sequence, or, when entries
+    // are cut, a warp for 32 sequences whose lanes are the pieces of one entry after another
+    auto for_entries = [&](auto f) {
+        const int lane = threadIdx.x & 31;
+        for (int s = mine; s < num_seqs + (KIND == META_CUT ? lane * 32 : 0); s += blockDim.x) {
+            const int ql = s < num_seqs ? q_len(s) : 0, cl = s < num_seqs ? ctx_len(s) : 0;
+            if constexpr (KIND == META_CUT) {
+                for (unsigned m = __ballot_sync(0xffffffffu, is_chunk(ql, cl)); m; m &= m - 1) {
+                    const int b = __ffs(m) - 1, ql_b = __shfl_sync(0xffffffffu, ql, b), cl_b = __shfl_sync(0xffffffffu, cl, b);
+                    for (int t0 = 0; t0 < ql_b; t0 += entry_tokens) f(s + (b - lane) * 32, ql_b, cl_b, t0, lane);
+                }
+            } else if (is_chunk(ql, cl)) {
+                for (int t0 = 0; t0 < ql; t0 += entry_tokens) f(s, ql, cl, t0, 0);
+            }
+        }
+    };
+    for (int s = mine; s < num_seqs; s += blockDim.x) {
         const int ql = q_len(s), cl = ctx_len(s);
-        if (ql <= 0 || is_decode_row(ql, g)) continue;
-        if (ql > cl || cl > mbps * kBS) {
-            raise_error(ctx, ERR_BOUNDS_BIT);
-            continue;
-        }
-        for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
-            const int2 t = entry_tiles(s, ql, cl, t0);
-            const int tiles = t.y - t.x, n = cuts(tiles), i = lane_piece;
-            if (i < n) atomicAdd(&hist[cut(i, n, tiles) - cut(i - 1, n, tiles)], 1);
-        }
+        if (ql > 0 && !is_decode_row(ql, g) && !is_chunk(ql, cl)) raise_error(ctx, ERR_BOUNDS_BIT);
     }
+    // histogram of the costs
+    for_entries([&](int s, int ql, int cl, int t0, int i) {
+        const int2 t = entry_tiles(s, ql, cl, t0);
+        const int tiles = t.y - t.x, n = cuts(tiles);
+        if (i < n) atomicAdd(&hist[cut(i, n, tiles) - cut(i - 1, n, tiles)], 1);
+    });
     __syncthreads();
     if (threadIdx.x < 32) {  // bucket starts, highest cost first (a warp: a wide table has thousands of buckets)
         const int lane = threadIdx.x;
@@ -1266,31 +1275,27 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         }
     }
     __syncthreads();
-    for (int s = seq0; s < num_seqs; s += seq_step) {
-        const int ql = q_len(s), cl = ctx_len(s);
-        if (!is_chunk(ql, cl)) continue;
-        for (int t0 = 0; t0 < ql; t0 += entry_tokens) {
-            const int2 t = entry_tiles(s, ql, cl, t0);
-            const int tiles = t.y - t.x, n = cuts(tiles), i = lane_piece;
-            [[maybe_unused]] int slot = -1;
-            if (cutting && n > 1) {
-                if (i == 0) {
-                    slot = atomicAdd(&n_slots, n * per_rank);
-                    split[atomicAdd(&n_split, 1)] = make_int4(s, t0, slot, n);
-                }
-                slot = __shfl_sync(0xffffffffu, slot, 0) + i * per_rank;
+    for_entries([&](int s, int ql, int cl, int t0, int i) {
+        const int2 t = entry_tiles(s, ql, cl, t0);
+        const int tiles = t.y - t.x, n = cuts(tiles);
+        [[maybe_unused]] int slot = -1;
+        if (KIND == META_CUT && n > 1) {
+            if (i == 0) {
+                slot = atomicAdd(&n_slots, n * per_rank);
+                split[atomicAdd(&n_split, 1)] = make_int4(s, t0, slot, n);
             }
-            if (i >= n) continue;
-            const int a = cut(i - 1, n, tiles), b = cut(i, n, tiles), pos = atomicAdd(&hist[b - a], 1);
-            if (pos >= max_entries) continue;
-            if constexpr (KIND != META_LIST) {
-                pieces[pos] = make_int4(s, t0, (t.x + a) | (t.x + b) << 16, slot);
-            } else {
-                list[2 * pos] = s;
-                list[2 * pos + 1] = t0;
-            }
+            slot = __shfl_sync(0xffffffffu, slot, 0) + i * per_rank;
         }
-    }
+        if (i >= n) return;
+        const int a = cut(i - 1, n, tiles), b = cut(i, n, tiles), pos = atomicAdd(&hist[b - a], 1);
+        if (pos >= max_entries) return;
+        if constexpr (KIND != META_LIST) {
+            pieces[pos] = make_int4(s, t0, (t.x + a) | (t.x + b) << 16, slot);
+        } else {
+            list[2 * pos] = s;
+            list[2 * pos + 1] = t0;
+        }
+    });
     if constexpr (KIND == META_CUT) {
         __syncthreads();
         if (threadIdx.x == 0) count[3] = n_split;

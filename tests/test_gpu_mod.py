@@ -447,3 +447,12 @@ def test_paged_mod_long_chunks_replayed(F):
         torch.cuda.synchronize()
         assert torch.equal(out, w)
     assert F.fa_get_error() == F.FA_OK
+
+
+def test_paged_mod_long_chunks_among_many_tokens(F):
+    """Cut chunks among more sequences than a block has threads: places and lists run over all of them."""
+    n = 1100
+    ctx, ql = [3 + i % 20 for i in range(n)], [1] * n
+    for at, c, q in ((5, 2600, 30), (700, 1500, 25), (1099, 1800, 40)):
+        ctx[at], ql[at] = c, q
+    run_paged(F, R.Paged(45, ctx, ql, 2, 1, 64), max_q_len=40)
