@@ -404,7 +404,7 @@ fa_status fa_paged_attn_mod(const void* q, const void* k_cache, const void* v_ca
  *   decay finite, >= 0
  *   lse   fp32 [total_q, Hq], required (written)
  *   ws    at least fa_paged_attn_accum_workspace_size(...) bytes, with the
- *         same max_q_len: beside fa_paged_attn's, the logits of the decode rows
+ *         same max_q_len: beside fa_paged_attn_mod's, the logits of the decode rows
  *         (64 bytes per row, page and kv head that the tables can hold)
  * The sums run in a fixed order: equal inputs give equal bits.  Calls that may
  * overlap on the GPU need workspaces of their own.  A call without

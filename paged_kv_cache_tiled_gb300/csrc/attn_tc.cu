@@ -17,7 +17,7 @@
 // does.  In paged mode a unit may then be a piece of its rows' keys (few queries
 // over a long context); its partial rows go to the workspace.  Measured at
 // d = 128: 12 heads in 2 groups, 4 prompts of 2041 tokens with a bias 60 us (44
-// without); 32 heads in 8 groups, 8192 tokens in 6 documents 151 us, capped 231.
+// without); 32 heads in 8 groups, 8192 tokens in 6 documents 145 us, capped 225.
 //
 // CTA layout (320 threads, one CTA per SM, persistent over work units):
 //   warps 0-3   softmax warpgroup of Q slot 0, warps 4-7 of Q slot 1: thread
@@ -1421,10 +1421,14 @@ fa_status launch_mask_classify(const float* M, int Tq, int Tk, uint8_t* cls, uin
 // sequence.  Writes every row's run [first, end) of positions (empty, at the
 // run's first position, for ids < 0), then orders the query entries
 // (entry_tiles tiles of 128 rows) by decreasing number of KV tiles with a
-// counting sort.  `starts` is scratch for the runs' first rows.
+// counting sort.  `starts` is scratch for the runs' first rows.  The attention
+// waits for all of it, so what fits one pass never leaves the SM: up to kDocSmall
+// rows keep their run in registers and the runs' first rows in shared memory
+// (8192 rows in 6 documents: 6 us less of 232).
 constexpr int kDocRows = 8;  // consecutive ids per thread and pass
+constexpr int kDocSmall = 1024 * kDocRows;
 __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restrict__ ids, int B, int T, int entry_tiles,
-                                                         int2* rows, int* starts, int4* __restrict__ order,
+                                                         int2* rows, int* starts_far, int4* __restrict__ order,
                                                          int32_t* __restrict__ count, TcParams p) {
     if (threadIdx.x == 0) count[1] = 0;  // the attention's unit tickets
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the attention waits for this grid's end
@@ -1432,6 +1436,9 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
     __shared__ int warp_sums[32];
     const int n = B * T, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int nbins = (T + kTcRows - 1) / kTcRows + 1;
+    const bool small = n <= kDocSmall;
+    int* starts = small ? hist + nbins + 1 : starts_far;
+    int2 r[kDocRows];  // (run, id) of this thread's rows
     for (int i = threadIdx.x; i <= nbins; i += blockDim.x) hist[i] = 0;
     int carry = 0;
     for (int base = 0; base < n; base += blockDim.x * kDocRows) {
@@ -1468,7 +1475,8 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
         for (int k = 0; k < kDocRows; ++k)
             if (i0 + k < n) {
                 if (first & (1u << k)) starts[++run] = i0 + k;
-                rows[i0 + k] = make_int2(run, id[k + 1]);
+                r[k] = make_int2(run, id[k + 1]);
+                if (!small) rows[i0 + k] = r[k];
             }
         carry += total;
         __syncthreads();
@@ -1476,10 +1484,10 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
     if (threadIdx.x == 0) starts[carry] = n;
     __syncthreads();
     for (int i0 = threadIdx.x * kDocRows; i0 < n; i0 += blockDim.x * kDocRows) {  // each kind of load for all rows at once
-        int2 r[kDocRows];
         int lo[kDocRows], hi[kDocRows];
 #pragma unroll
-        for (int k = 0; k < kDocRows; ++k) r[k] = i0 + k < n ? rows[i0 + k] : make_int2(0, 0);
+        for (int k = 0; k < kDocRows; ++k)
+            if (!small || i0 + k >= n) r[k] = i0 + k < n ? rows[i0 + k] : make_int2(0, 0);
 #pragma unroll
         for (int k = 0; k < kDocRows; ++k) {
             lo[k] = starts[r[k].x];
@@ -1507,7 +1515,9 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
         return make_int4(b, t, range(r0).x / kTcRows, (range(r1).y + kTcRows - 1) / kTcRows);
     };
     auto cost = [](const int4& e) { return max(0, e.w - e.z); };
-    for (int e = threadIdx.x; e < entries; e += blockDim.x) atomicAdd(&hist[cost(entry(e))], 1);
+    const int4 first = threadIdx.x < entries ? entry(threadIdx.x) : make_int4(0, 0, 0, 0);
+    for (int e = threadIdx.x; e < entries; e += blockDim.x)
+        atomicAdd(&hist[cost(e == threadIdx.x ? first : entry(e))], 1);
     __syncthreads();
     if (w == 0) {  // bucket starts, highest cost first
         int run = 0;
@@ -1525,7 +1535,7 @@ __global__ void __launch_bounds__(1024) doc_order_kernel(const int32_t* __restri
     }
     __syncthreads();
     for (int e = threadIdx.x; e < entries; e += blockDim.x) {
-        const int4 x = entry(e);
+        const int4 x = e == threadIdx.x ? first : entry(e);
         order[atomicAdd(&hist[cost(x)], 1)] = x;
     }
 }
@@ -1905,7 +1915,8 @@ fa_status fa_prefill_mod(const void* q, const void* k, const void* v, void* out,
     if (B == 0 || T == 0) return FA_OK;
     if ((long)B * T >= (1L << 31) - 8192) return FA_ERR_UNSUPPORTED;
     const int nt = (T + kTcRows - 1) / kTcRows;
-    const size_t hist_bytes = (size_t)(nt + 2) * sizeof(int);
+    const size_t hist_bytes =
+        (size_t)(nt + 2) * sizeof(int) + ((long)B * T <= kDocSmall ? ((size_t)B * T + 1) * sizeof(int) : 0);
     if (doc_ids) {
         if (!ws || ws_bytes < fa_prefill_mod_workspace_size(B, T) || (reinterpret_cast<uintptr_t>(ws) & 255))
             return FA_ERR_WORKSPACE;

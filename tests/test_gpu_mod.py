@@ -456,3 +456,15 @@ def test_paged_mod_long_chunks_among_many_tokens(F):
     for at, c, q in ((5, 2600, 30), (700, 1500, 25), (1099, 1800, 40)):
         ctx[at], ql[at] = c, q
     run_paged(F, R.Paged(45, ctx, ql, 2, 1, 64), max_q_len=40)
+
+
+def test_prefill_mod_documents_of_large_batches(F):
+    """More rows than one pass over the ids takes: the same bits as one sequence at a time."""
+    B, T = 3, 4001
+    g = torch.Generator().manual_seed(46)
+    q, k, v = (torch.randn(B, T, h, 64, generator=g).bfloat16().cuda() for h in (2, 1, 1))
+    ids = doc_ids(B, T, 47).cuda()
+    out = F.fa_prefill_mod(q, k, v, doc_ids=ids, window=700)
+    for b in range(B):
+        x = slice(b, b + 1)
+        assert torch.equal(out[x], F.fa_prefill_mod(q[x], k[x], v[x], doc_ids=ids[x].contiguous(), window=700))
