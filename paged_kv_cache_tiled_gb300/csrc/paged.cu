@@ -1068,11 +1068,12 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
 }
 
 // ------------------------------------------------------------ metadata -----
-// One CTA: q_start (exclusive prefix sum of q_lens) and the list of work
-// entries (entry_tokens consecutive query tokens, paged_tc_entry_tokens) of
-// the sequences that take the tensor-core kernel, ordered by decreasing number
-// of KV tiles (longest first) with a counting sort.  Entry = (sequence, first
-// query token of the entry within the chunk).
+// Two CTAs side by side, since every chunked call waits for them.  The second:
+// q_start (exclusive prefix sum of q_lens), and the weight sums' units.  The
+// first: the list of work entries (entry_tokens consecutive query tokens,
+// paged_tc_entry_tokens) of the sequences that take the tensor-core kernel,
+// ordered by decreasing number of KV tiles (longest first) with a counting sort.
+// Entry = (sequence, first query token of the entry within the chunk).
 //
 // Calls with modified scores get `pieces` instead: an entry whose KV tiles are
 // many for the work there is (few chunks over long contexts) is cut along its
@@ -1117,84 +1118,87 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         all_tiles = 0;
     }
     __syncthreads();
-    // prefix sum of q_lens, 1024 sequences per pass
-    for (int base = 0; base < num_seqs; base += blockDim.x) {
-        const int s = base + threadIdx.x;
-        int v = s < num_seqs ? q_len(s) : 0;
-        int x = v;
-        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) warp_sums[w] = x;
-        __syncthreads();
-        if (w == 0) {
-            int t = warp_sums[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                int y = __shfl_up_sync(0xffffffffu, t, o);
-                if (lane >= o) t += y;
-            }
-            warp_sums[lane] = t;
-        }
-        __syncthreads();
-        const int excl = carry + (w ? warp_sums[w - 1] : 0) + x - v;
-        if (s < num_seqs) q_start[s] = excl;
-        __syncthreads();
-        if (threadIdx.x == blockDim.x - 1) carry = excl + v;
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) q_start[num_seqs] = carry;
-    // weight sums: sequences by decreasing chunk length (a counting sort over 64
-    // lengths; the order only decides who goes first), then their units of 256
-    // keys in that order (none for a sequence whose sums do not fit, which is
-    // reported, and for those without a chunk)
-    if (KIND != META_LIST && k_start) {
-        __shared__ int order[64];
-        int32_t* k_seq = k_start + num_seqs + 1;
-        auto rank_bin = [&](int s) { return 63 - min(63, max(0, q_len(s)) / 32); };
-        __syncthreads();
-        if (threadIdx.x < 64) order[threadIdx.x] = 0;
-        if (threadIdx.x == 0) carry = 0;
-        __syncthreads();
-        for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) atomicAdd(&order[rank_bin(s)], 1);
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            int run = 0;
-            for (int b = 0; b < 64; ++b) {
-                const int c = order[b];
-                order[b] = run;
-                run += c;
-            }
-        }
-        __syncthreads();
-        for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) k_seq[atomicAdd(&order[rank_bin(s)], 1)] = s;
-        __syncthreads();
+    if (blockIdx.x == 1) {
+        // prefix sum of q_lens, 1024 sequences per pass
         for (int base = 0; base < num_seqs; base += blockDim.x) {
-            const int r = base + threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-            const int s = r < num_seqs ? k_seq[r] : 0;
-            const int ql = r < num_seqs ? q_lens[s] : 0, cl = r < num_seqs ? ctx_lens[s] : 0;
-            const bool chunk = ql > 0 && !is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS;
-            if (chunk && cl > acc_len) raise_error(ctx, ERR_BOUNDS_BIT);
-            const int v = chunk && cl <= acc_len ? (cl + 255) / 256 : 0;
+            const int s = base + threadIdx.x;
+            int v = s < num_seqs ? q_len(s) : 0;
             int x = v;
+            const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                int y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
             if (lane == 31) warp_sums[w] = x;
             __syncthreads();
-            const int t = warp_sums[lane];
-            const int before = carry + __reduce_add_sync(0xffffffffu, lane < w ? t : 0) + x - v;
-            if (r < num_seqs) k_start[r] = before;
+            if (w == 0) {
+                int t = warp_sums[lane];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    int y = __shfl_up_sync(0xffffffffu, t, o);
+                    if (lane >= o) t += y;
+                }
+                warp_sums[lane] = t;
+            }
             __syncthreads();
-            if (threadIdx.x == blockDim.x - 1) carry = before + v;
+            const int excl = carry + (w ? warp_sums[w - 1] : 0) + x - v;
+            if (s < num_seqs) q_start[s] = excl;
+            __syncthreads();
+            if (threadIdx.x == blockDim.x - 1) carry = excl + v;
             __syncthreads();
         }
-        if (threadIdx.x == 0) k_start[num_seqs] = carry;
+        if (threadIdx.x == 0) q_start[num_seqs] = carry;
+        // weight sums: sequences by decreasing chunk length (a counting sort over 64
+        // lengths; the order only decides who goes first), then their units of 256
+        // keys in that order (none for a sequence whose sums do not fit, which is
+        // reported, and for those without a chunk)
+        if (KIND != META_LIST && k_start) {
+            __shared__ int order[64];
+            int32_t* k_seq = k_start + num_seqs + 1;
+            auto rank_bin = [&](int s) { return 63 - min(63, max(0, q_len(s)) / 32); };
+            __syncthreads();
+            if (threadIdx.x < 64) order[threadIdx.x] = 0;
+            if (threadIdx.x == 0) carry = 0;
+            __syncthreads();
+            for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) atomicAdd(&order[rank_bin(s)], 1);
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                int run = 0;
+                for (int b = 0; b < 64; ++b) {
+                    const int c = order[b];
+                    order[b] = run;
+                    run += c;
+                }
+            }
+            __syncthreads();
+            for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) k_seq[atomicAdd(&order[rank_bin(s)], 1)] = s;
+            __syncthreads();
+            for (int base = 0; base < num_seqs; base += blockDim.x) {
+                const int r = base + threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+                const int s = r < num_seqs ? k_seq[r] : 0;
+                const int ql = r < num_seqs ? q_lens[s] : 0, cl = r < num_seqs ? ctx_lens[s] : 0;
+                const bool chunk = ql > 0 && !is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS;
+                if (chunk && cl > acc_len) raise_error(ctx, ERR_BOUNDS_BIT);
+                const int v = chunk && cl <= acc_len ? (cl + 255) / 256 : 0;
+                int x = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (lane == 31) warp_sums[w] = x;
+                __syncthreads();
+                const int t = warp_sums[lane];
+                const int before = carry + __reduce_add_sync(0xffffffffu, lane < w ? t : 0) + x - v;
+                if (r < num_seqs) k_start[r] = before;
+                __syncthreads();
+                if (threadIdx.x == blockDim.x - 1) carry = before + v;
+                __syncthreads();
+            }
+            if (threadIdx.x == 0) k_start[num_seqs] = carry;
+        }
+        return;
     }
     // an entry's KV tiles [x, y): from the first key its first row sees to the last its last row sees
     auto entry_tiles = [&](int s, int ql, int cl, int t0) {
@@ -1374,8 +1378,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const int4* split, cons
     }
 }
 
-// A library-owned side stream per device: the chunked-prefill metadata pass (one
-// CTA) runs there beside the split-KV decode kernel and its merge, which do
+// A library-owned side stream per device: the chunked-prefill metadata pass (two
+// CTAs) runs there beside the split-KV decode kernel and its merge, which do
 // not depend on it; two events fork it from and join it back to the caller's
 // stream (both capturable, so the call may be recorded into a CUDA graph).
 constexpr int kMaxSideDevices = 64;
@@ -1568,7 +1572,7 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
                 return FA_ERR_CUDA;
             ms = ss->s;
         }
-        meta<<<1, 1024, hist_bytes, ms>>>(ctx_lens, q_lens, num_seqs, max_blocks_per_seq, g, causal,
+        meta<<<2, 1024, hist_bytes, ms>>>(ctx_lens, q_lens, num_seqs, max_blocks_per_seq, g, causal,
                                                        entry_tokens, q_start, count, list,
                                                        mod ? pw.max_pieces : w.max_entries,
                                                        mod ? mod->window : 0, mod ? mod->prefix : nullptr,
