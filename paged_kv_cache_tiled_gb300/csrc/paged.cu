@@ -1083,8 +1083,8 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
 // three), the share up to six of them (a GPU that is nearly full gains nothing
 // from pieces of four: 4 chunks of 300 over 1000 keys 44 us, whole 33), and half
 // the share beyond.  Measured, 32 heads in 8 groups, d = 128: a chunk of 128
-// over 4000 keys 90 us whole, 35 in pieces; one of 512 over 30000 376 and 146;
-// 16 chunks of 64 over up to 8000 (12 heads in 2 groups) 107 and 73.
+// over 4000 keys 88 us whole, 32 in pieces; one of 512 over 30000 376 and 140;
+// 16 chunks of 64 over up to 8000 (12 heads in 2 groups) 107 and 74.
 constexpr int kSplitTiles = 4, kSplitShare = 6;
 constexpr int kSplitMost = 32;  // pieces of an entry (a warp lists them, the join takes 0.3 us for each)
 constexpr int kSplitSlots = 2 * kMaxStreamCtas;  // total / least, at most
