@@ -513,6 +513,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                         }
                         [[maybe_unused]] int tier = 2;
                         if constexpr (MOD == CS_CAP) {
+                            if (p.cap.wide) tier = 3;
                             float mz[2] = {0.f, 0.f};
 #pragma unroll
                             for (int jj = 0; jj < 32; jj += 2)
@@ -545,7 +546,11 @@ __global__ void __launch_bounds__(kCsThreads, 1)
 #pragma unroll
                                         for (int k = top - 2; k >= 0; --k) t = __ffma2_rn(t, q2, co[k]);
                                         x = __ffma2_rn(x, t, l2);
-                                    } else if (MOD == CS_CAP || (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
+                                    } else if ((MOD == CS_CAP && decltype(form)::value == 3) ||
+                                               (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
+                                        x.x = fmaf(p.mod.cap_out, tanh_f32(x.x * p.mod.cap_in), l2.x);
+                                        x.y = fmaf(p.mod.cap_out, tanh_f32(x.y * p.mod.cap_in), l2.y);
+                                    } else if (MOD == CS_CAP) {
                                         x.x = fmaf(p.mod.cap_out, tanh_abs(x.x * p.mod.cap_in), l2.x);
                                         x.y = fmaf(p.mod.cap_out, tanh_abs(x.y * p.mod.cap_in), l2.y);
                                     } else {
@@ -573,7 +578,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                         if constexpr (MOD == CS_CAP) {
                             if (tier == 0) sum_block(std::integral_constant<int, 0>{});
                             else if (tier == 1) sum_block(std::integral_constant<int, 1>{});
-                            else sum_block(std::integral_constant<int, 2>{});
+                            else if (tier == 2) sum_block(std::integral_constant<int, 2>{});
+                            else sum_block(std::integral_constant<int, 3>{});
                         } else {
                             sum_block(std::integral_constant<int, 2>{});
                         }

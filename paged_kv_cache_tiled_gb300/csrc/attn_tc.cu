@@ -517,7 +517,7 @@ __device__ __noinline__ float modified_logits_row(uint32_t taddr, int vlo, int v
         for (int j = 0; j < 32; ++j) {
             const int c = h * 32 + j;
             const float z = __uint_as_float(raw[j]);
-            float x = cap_out > 0.f ? cap_out * tanh_abs(z * cap_in) : z * scale_log2;
+            float x = cap_out > 0.f ? cap_out * tanh_f32(z * cap_in) : z * scale_log2;
             x = fmaf(-slope, fabsf((float)(d0 + c)), x);
             if (c < vlo || c >= vlim) x = -INFINITY;
             raw[j] = __float_as_uint(x);
@@ -1198,6 +1198,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // which form of the cap serves every row of the warp (CapPoly; a row that sees nothing takes any)
                 [[maybe_unused]] int cap_tier = 2;
                 if constexpr ((MOD & MOD_CAP) != 0) {
+                    if (p.cap.wide) cap_tier = 3;
                     const bool none = m == -INFINITY;
                     if (__all_sync(0xffffffffu, none || (raw_max <= p.cap.near_max && m + p.cap.near_slack >= 30.f)))
                         cap_tier = 0;
@@ -1267,10 +1268,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 t = __ffma2_rn(t, w, p.cap.unit[0]);
                                 return __ffma2_rn(z, t, neg_m);
                             });
-                        } else {
+                        } else if (cap_tier == 2) {
                             const float2 cp2 = both(p.mod.cap_out);
                             exp_pairs([&](float2 z, int) {
                                 return __ffma2_rn(make_float2(tanh_abs(z.x * p.mod.cap_in), tanh_abs(z.y * p.mod.cap_in)),
+                                                  cp2, neg_m);
+                            }, std::true_type{});
+                        } else {
+                            const float2 cp2 = both(p.mod.cap_out);
+                            exp_pairs([&](float2 z, int) {
+                                return __ffma2_rn(make_float2(tanh_f32(z.x * p.mod.cap_in), tanh_f32(z.y * p.mod.cap_in)),
                                                   cp2, neg_m);
                             }, std::true_type{});
                         }

@@ -319,9 +319,11 @@ __device__ __forceinline__ float tanh_f32(float u) {
 constexpr float kTanhNear = 0.65f;
 constexpr float kTanhD0 = 0.9999998f, kTanhD1 = -0.333315f, kTanhD2 = 0.13297874f, kTanhD3 = -0.051517908f,
                 kTanhD4 = 0.014625075f;
-// tanh with an absolute (not relative) error below 4e-7 anywhere, all that a
-// capped logit needs: 1 - 2 / (1 + e^(2|u|)) with the hardware's exponential
-// and reciprocal, about half of tanh_f32's instructions.
+// tanh with an absolute (not relative) error below 4e-7 anywhere:
+// 1 - 2 / (1 + e^(2|u|)) with the hardware's exponential and reciprocal, about
+// half of tanh_f32's instructions.  A logit is then off by 4e-7 of the cap, which
+// is as much as its own rounding for the caps in use and more than all of its
+// digits for very large ones: caps above kWideCap take tanh_f32.
 __device__ __forceinline__ float tanh_abs(float u) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(fabsf(u) * 2.885390081777927f)));
@@ -367,10 +369,14 @@ struct ScoreMod {
 // below minus that bound gets a wrong logit, which is harmless when its weight
 // is below 2^-30 of the row's: `slack` plus the row's running max (log2 units)
 // has to reach 30.  slack is -inf when a coefficient leaves fp32's range.
+// Other rows take the exact tanh_abs, or tanh_f32 when the cap is `wide`: rows
+// share a form with their warp, so that a row of ordinary logits meets it too.
+constexpr float kWideCap = 256.f;  // c log2(e) up to which tanh_abs is exact enough: 1e-4 of a logit
 struct CapPoly {
     float2 near[5], unit[7];
     float near_max, unit_max;      // largest s
     float near_slack, unit_slack;  // c log2(e) tanh(kTanhNear), c log2(e) tanh(1)
+    int wide;
 };
 
 // Four E4M3 bytes (byte i = element i) to two f16x2 words: lo = elements

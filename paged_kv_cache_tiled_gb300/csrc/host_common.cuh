@@ -91,6 +91,7 @@ inline CapPoly cap_poly(const ScoreMod& m) {
             near_fits &= fits(n);
         }
     }
+    c.wide = m.cap_out > kWideCap;
     c.near_max = (float)(kTanhNear / in);
     c.unit_max = (float)(1.0 / in);
     c.near_slack = near_fits ? (float)(out * std::tanh(kTanhNear)) : -INFINITY;
