@@ -165,7 +165,8 @@ fa_status fa_prefill_masked(const void* q, const void* k, const void* v, const f
  *     doc_ids:      every position from i to j holds the same id >= 0
  *   softcap       >= 0, finite; 0: no cap.  softcap * log2(e) and scale / softcap
  *                 must be normal fp32 numbers
- *   alibi_slopes  fp32 [Hq] or NULL (no bias); any finite values
+ *   alibi_slopes  fp32 [Hq] or NULL (no bias); finite.  Logits are fp32 numbers in log2 units,
+ *                 so a negative slope times the farthest distance seen has to stay above -2.3e38
  *   window        >= 0; 0: none
  *   prefix_lens   int32 [B] or NULL; ignored without causal (everything is
  *                 visible then); values below 1 change nothing, values past T

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                         const bool real = j + e < U.n && tok < U.ql;
                         lse[4 * e + b] = real ? __ldg(p.lse + (long)(U.qs + tok) * p.Hq + hd) : 0.f;
                         if constexpr (MOD == CS_BIAS) {
-                            sl[4 * e + b] = -__ldg(p.mod.slopes + hd) * kCsLog2e;
+                            sl[4 * e + b] = -slope_log2(__ldg(p.mod.slopes + hd));
                             at[4 * e + b] = (float)(U.pos0 + tok - U.kv0);
                         }
                         seen[4 * e + b] = real ? cs_range(p, U.pos0 + tok, U.prefix, U.cl) : make_int2(0, 0);

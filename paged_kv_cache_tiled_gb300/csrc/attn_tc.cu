@@ -1044,7 +1044,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int2 run = row_range<MODE>(p, U.b, rowc, rowc + U.pos_off, U.kv_len);
                 vis_lo = run.x;
                 vis_end = run.y;
-                if constexpr ((MOD & MOD_BIAS) != 0) slope = __ldg(p.mod.slopes + sel(U.head, s) + hl) * kLog2e;
+                if constexpr ((MOD & MOD_BIAS) != 0) slope = slope_log2(__ldg(p.mod.slopes + sel(U.head, s) + hl));
             }
             float m = -INFINITY, l = 0.f;
             int it = 0;

@@ -363,6 +363,13 @@ struct ScoreMod {
     int logit_rows;         // rows a page's logits take in that buffer
 };
 
+// A distance slope in log2 units.  Bounded, so that a slope near fp32's largest
+// still times distance 0 is 0 (an infinite one gave NaN for the query's own key).
+__device__ __forceinline__ float slope_log2(float slope) {
+    constexpr float most = 3.4028235e38f;
+    return fminf(fmaxf(slope * 1.4426950408889634f, -most), most);
+}
+
 // The capped logit as a polynomial of the raw dot product s, in pairs of equal
 // coefficients: c log2(e) tanh(s scale / c) = s (a_0 + a_1 s^2 + ...) while the
 // row's largest s scale / c is at most kTanhNear (near) or 1 (unit).  A score

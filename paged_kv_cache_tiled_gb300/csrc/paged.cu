@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
             for (int i = 0; i < 2; ++i) {
                 qpos[i] = ctx_len - q_len + rr[i] / g;
                 lo_r[i] = window > 0 ? qpos[i] - window + 1 : 0;
-                slope[i] = mod.slopes && rr[i] < nrows ? __ldg(mod.slopes + cc.hk * g + rr[i] % g) * kLog2ef : 0.f;
+                slope[i] = mod.slopes && rr[i] < nrows ? slope_log2(__ldg(mod.slopes + cc.hk * g + rr[i] % g)) : 0.f;
             }
             pos_r0 = max(pos_r0, prefix - 1);
             pos_r1 = max(pos_r1, prefix - 1);
