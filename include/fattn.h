@@ -447,7 +447,8 @@ fa_status fa_paged_attn_accum(const void* q, const void* k_cache, const void* v_
  *   acc_out      fp32 [num_seqs, Hkv, acc_out_len] or NULL; acc_out_len >=
  *                keep; may be acc itself (with the same row length); elements
  *                past the kept tokens are left as they were
- *   new_lens     int32 [num_seqs] (written): min(ctx_lens[s], keep)
+ *   new_lens     int32 [num_seqs] (written): min(ctx_lens[s], keep); may be ctx_lens
+ *                itself
  *   kept         int32 [num_seqs, Hkv, keep] (written) or NULL: the kept tokens'
  *                old positions, ascending, -1 behind the last
  *   keep > 0, recent >= 0, sink >= 0, sink + recent <= keep; keep up to 2^20 - 16

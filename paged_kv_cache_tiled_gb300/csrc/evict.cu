@@ -61,13 +61,17 @@ __device__ __forceinline__ void cluster_add(int* p, unsigned rank, int v) {
     asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
+// Do a context of cl tokens and the n kept ones fit the tables and the row of weights?
+__device__ __forceinline__ bool lens_fit(int cl, int n, int mbps, int dst_mbps, int acc_len) {
+    return cl >= 0 && cl <= mbps * kEvBlock && cl <= acc_len && n <= dst_mbps * kEvBlock;
+}
+
 constexpr int kEvPass = kEvThreads * kEvItems;  // tokens of a scan pass
 __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* acc, int acc_len,
                                                                   const int32_t* __restrict__ ctx_lens, float* acc_out,
-                                                                  int out_len, int32_t* __restrict__ list,
-                                                                  int32_t* __restrict__ new_lens, int Hkv, int mbps,
-                                                                  int dst_mbps, int keep, int recent, int sink,
-                                                                  DevCtx ctx) {
+                                                                  int out_len, int32_t* __restrict__ list, int Hkv,
+                                                                  int mbps, int dst_mbps, int keep, int recent,
+                                                                  int sink, DevCtx ctx) {
     static_assert(kEvBins == 4 * kEvThreads, "a thread owns four bins");
     __shared__ __align__(16) int hist[kEvBins];  // this CTA's counts
     // the cluster's counts, by turns, so that one cluster barrier per pass is enough (a single CTA uses hist)
@@ -77,20 +81,17 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
     // the rows' copy may be scheduled; it waits for this grid's end before it reads the list
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int CL = (int)cluster_size(), rank = (int)cluster_rank();
-    const int sh = blockIdx.x / CL, s = sh / Hkv, h = sh % Hkv;
+    const int sh = blockIdx.x / CL, s = sh / Hkv;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int cl = __ldg(ctx_lens + s);
     int32_t* out = list + (long)sh * keep;
     const int n = min(cl, keep);
-    const bool first = h == 0 && rank == 0 && tid == 0;
     const int gtid = rank * kEvThreads + tid, gthreads = CL * kEvThreads;
-    if (cl < 0 || cl > mbps * kEvBlock || cl > acc_len || n > dst_mbps * kEvBlock) {  // the same for the whole cluster
+    if (!lens_fit(cl, n, mbps, dst_mbps, acc_len)) {  // the same for the whole cluster
         if (rank == 0 && tid == 0) raise_error(ctx, ERR_BOUNDS_BIT);
         for (int i = gtid; i < keep; i += gthreads) out[i] = -1;
-        if (first) new_lens[s] = 0;
         return;
     }
-    if (first) new_lens[s] = n;
     for (int i = n + gtid; i < keep; i += gthreads) out[i] = -1;
     const float* a = acc + (long)sh * acc_len;
     float* ao = acc_out ? acc_out + (long)sh * out_len : nullptr;
@@ -278,11 +279,14 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* a
 // token i of `dst`, K and V, 16 bytes per thread; kEvRows rows per thread whose
 // loads are in flight together, and full occupancy behind the three dependent
 // loads (token, blocks, values) of a row.
-// CTA (sequence and head, group of rows).
+// CTA (sequence and head, group of rows).  The first of a sequence writes its new
+// length, here and not in the select: new_lens may be ctx_lens itself, which every
+// CTA of the select reads.
 constexpr int kEvRows = 2;
 template <int D>
 __global__ void __launch_bounds__(256, 8) evict_move_kernel(uint16_t* kc, uint16_t* vc, const int32_t* __restrict__ src,
                                                             const int32_t* __restrict__ dst, const int32_t* list,
+                                                            const int32_t* ctx_lens, int32_t* new_lens, int acc_len,
                                                             int Hkv, int mbps, int dst_mbps, int keep, int num_blocks,
                                                             DevCtx ctx) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is complete
@@ -293,6 +297,10 @@ __global__ void __launch_bounds__(256, 8) evict_move_kernel(uint16_t* kc, uint16
     uint16_t* cache = c < cpr ? kc : vc;
     const int off = (c < cpr ? c : c - cpr) * 8;
     const int sh = blockIdx.x, s = sh / Hkv, h = sh % Hkv;
+    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) {
+        const int cl = ctx_lens[s], n = min(cl, keep);
+        new_lens[s] = lens_fit(cl, n, mbps, dst_mbps, acc_len) ? n : 0;
+    }
     const int i0 = blockIdx.y * rows_cta * kEvRows + rr;
     const int32_t* tokens = list + (long)sh * keep;
     int t[kEvRows];
@@ -379,7 +387,7 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, acc, acc_len, ctx_lens, acc_out, acc_out_len, list, new_lens, Hkv,
+    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, acc, acc_len, ctx_lens, acc_out, acc_out_len, list, Hkv,
                            max_blocks_per_seq, dst_blocks_per_seq, keep, recent, sink, ctx) != cudaSuccess)
         return FA_ERR_CUDA;
     const int rows_item = 256 / (2 * (d / 8)) * kEvRows;
@@ -390,8 +398,8 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     auto move = d == 128 ? evict_move_kernel<128> : evict_move_kernel<64>;
     if (cudaLaunchKernelEx(&cfg, move, static_cast<uint16_t*>(k_cache), static_cast<uint16_t*>(v_cache), block_table,
-                           dst_table, static_cast<const int32_t*>(list), Hkv, max_blocks_per_seq, dst_blocks_per_seq,
-                           keep, num_blocks, ctx) != cudaSuccess)
+                           dst_table, static_cast<const int32_t*>(list), ctx_lens, new_lens, acc_len, Hkv, max_blocks_per_seq,
+                           dst_blocks_per_seq, keep, num_blocks, ctx) != cudaSuccess)
         return FA_ERR_CUDA;
     set_launch_count(2);
     return FA_OK;
