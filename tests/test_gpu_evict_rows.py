@@ -1,4 +1,5 @@
-"""Eviction with the new lengths written over the old ones."""
+"""Eviction with rows of every alignment shared by several CTAs and read in several passes, and with the new lengths
+written over the old ones."""
 import numpy as np
 import pytest
 import torch
@@ -61,6 +62,23 @@ def run(F, ctx, Hkv, keep, recent, sink, row, shift=0, inplace_acc=False, inplac
             ek[db, h, i % 16], ev[db, h, i % 16] = kc[sb, h, t % 16], vc[sb, h, t % 16]
             ea[s, h, :n] = acc[s, h, t]
     assert torch.equal(k2.cpu(), ek) and torch.equal(v2.cpu(), ev) and torch.equal(ao.cpu(), ea)
+
+
+LONG = [([20000], 9000), ([5000, 9000, 2100], 600), ([70000], 3000), ([8191, 8185, 4099], 4096)]
+
+
+@pytest.mark.parametrize("ctx, keep", LONG, ids=str)
+@pytest.mark.parametrize("pad", [0, 4, 16, 1, 2])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_rows_of_every_alignment(F, ctx, keep, pad, inplace):
+    """Rows of a multiple of four elements are read four at a time, by clusters and in several passes too; the last
+    tokens of a context that ends anywhere one at a time."""
+    run(F, ctx, 1, keep, 40, 3, -(-max(ctx) // 4) * 4 + pad, inplace_acc=inplace)
+
+
+@pytest.mark.parametrize("shift", [1, 4])
+def test_rows_that_start_anywhere(F, shift):
+    run(F, [9000, 7000], 2, 1000, 5, 0, 9004, shift=shift)
 
 
 @pytest.mark.parametrize("many", [False, True], ids=["one CTA a row", "CTAs that share a row"])
