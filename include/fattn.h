@@ -333,8 +333,9 @@ fa_status fa_paged_attn_fp8(const void* q, const void* k_cache, const void* v_ca
  *   max_q_len    host-side upper bound on every q_lens[s] (total_q is always
  *                a valid bound); used to skip launching a kernel that would
  *                find no work and to size the decode kernel's partial slots
- *                ((Hq/Hkv) * max_q_len <= 6 rows keeps its deeper ring); a
- *                decode chunk above the bound is reported as FA_ERR_BOUNDS
+ *                ((Hq/Hkv) * max_q_len <= 6 rows keeps its deeper ring).  With
+ *                (Hq/Hkv) * max_q_len <= 16, which launches the decode kernel
+ *                alone, any chunk above the bound is reported as FA_ERR_BOUNDS
  *                (fa_get_error) and its rows are not valid
  *   block_size   must be 16
  *   scale        finite and > 0, multiplies Q K^T

@@ -34,6 +34,7 @@
 // and a cap 41 us (the stream alone 4.8 TB/s), up to 4096 tokens with the sums 39
 // us (33 without).
 #include <algorithm>
+#include <climits>
 #include <mutex>
 #include <type_traits>
 
@@ -188,6 +189,9 @@ struct Cursor {
 // stream.  MOD 2 also keeps every logit (log2 units, -inf where masked) at
 // [page of the stream][row][token] for the weight sums that need the final
 // log-sum-exp: logit_rows * 64 bytes beside the page's 64 d.
+// max_q_len: the call's bound on the chunks' lengths when it has no other kernel for
+// longer ones; it sizes the slots, the merge's CTAs and the logits, so a chunk
+// above it is an error (and its rows are not valid).
 constexpr int kLensPerLane = 8;  // sequences per lane whose lengths are loaded in one batch
 constexpr float kLn2f = 0.6931471805599453f, kLog2ef = 1.4426950408889634f;
 template <int D, bool KV8, int ROWS, int MOD>
@@ -196,8 +200,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
                         const uint16_t* __restrict__ q, const int32_t* __restrict__ bt,
                         const int32_t* __restrict__ ctx_lens, const int32_t* __restrict__ q_lens,
                         uint16_t* __restrict__ out, float* __restrict__ part_o, float2* __restrict__ part_ml,
-                        int num_seqs, int mbps, int num_blocks, int Hq, int Hkv, int q_prefetch_rows, int causal,
-                        float scale_log2, float v_scale, DevCtx ctx, ScoreMod mod) {
+                        int num_seqs, int mbps, int num_blocks, int Hq, int Hkv, int max_q_len, int q_prefetch_rows,
+                        int causal, float scale_log2, float v_scale, DevCtx ctx, ScoreMod mod) {
     static_assert(MOD == 0 || !KV8, "score modifiers are built for the bf16 cache");
     const int window = MOD ? mod.window : 0;
     // the merge kernel that follows may be scheduled now; it waits for this
@@ -251,6 +255,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     bool bad = false;
     auto count = [&](int ql, int cl) {
         my_q += ql;
+        bad |= ql > max_q_len;
         if (!is_decode_row(ql, g)) return;
         if (ql > cl || cl > mbps * kBS) {
             bad = true;
@@ -1405,8 +1410,8 @@ template <int D, bool KV8 = false, int MOD = 0>
 static fa_status launch_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* bt,
                                const int32_t* ctx_lens, const int32_t* q_lens, void* out, const PagedWs& w,
                                uint8_t* ws, int num_seqs, int mbps, int num_blocks, int Hq, int Hkv,
-                               int q_prefetch_rows, int causal, float scale, int merge_rows, cudaStream_t s,
-                               const DevCtx& ctx, int* launches,
+                               int max_q_len, int q_prefetch_rows, int causal, float scale, int merge_rows,
+                               cudaStream_t s, const DevCtx& ctx, int* launches,
                                float k_scale = 1.f, float v_scale = 1.f, const ScoreMod& mod = ScoreMod{}) {
     CUtensorMap tk, tv;
     fa_status st;
@@ -1444,8 +1449,7 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
         if (st2 != FA_OK) return st2;
         paged_decode_kernel<D, KV8, R, MOD><<<grid, kStreamWarps * 32, L::kBytes, s>>>(
             tk, tv, static_cast<const uint16_t*>(q), bt, ctx_lens, q_lens, static_cast<uint16_t*>(out), part_o, part_ml,
-            num_seqs, mbps, num_blocks, Hq, Hkv, q_prefetch_rows, causal, scale_log2, v_scale, ctx,
-            mod);
+            num_seqs, mbps, num_blocks, Hq, Hkv, max_q_len, q_prefetch_rows, causal, scale_log2, v_scale, ctx, mod);
         return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     };
     st = merge_rows <= 6 ? launch(std::integral_constant<int, 6>{}) : launch(std::integral_constant<int, kDecodeRows>{});
@@ -1599,7 +1603,7 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         auto go = [&](auto dim, auto variant) {
             return launch_decode<decltype(dim)::value, false, decltype(variant)::value>(
                 q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w, wsb, num_seqs, max_blocks_per_seq,
-                num_blocks, Hq, Hkv, qpf, causal, scale, merge_rows, s, ctx, &launches, 1.f, 1.f,
+                num_blocks, Hq, Hkv, tc_path ? INT_MAX : max_q_len, qpf, causal, scale, merge_rows, s, ctx, &launches, 1.f, 1.f,
                 mod ? *mod : ScoreMod{});
         };
         auto go_d = [&](auto variant) {
@@ -1774,7 +1778,7 @@ fa_status fa_paged_attn_fp8(const void* q, const void* k_cache, const void* v_ca
     int launches = 0;
     st = launch_decode<128, true>(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w,
                                   static_cast<uint8_t*>(ws), num_seqs, max_blocks_per_seq, num_blocks, Hq, Hkv,
-                                  total_q, causal, scale, (Hq / Hkv) * max_q_len,
+                                  max_q_len, total_q, causal, scale, (Hq / Hkv) * max_q_len,
                                   reinterpret_cast<cudaStream_t>(stream), ctx, &launches, k_scale, v_scale);
     if (st != FA_OK) return st;
     set_launch_count(launches);
