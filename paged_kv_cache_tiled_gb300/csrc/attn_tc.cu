@@ -1945,7 +1945,7 @@ fa_status fa_prefill_mod(const void* q, const void* k, const void* v, void* out,
         int* starts = reinterpret_cast<int*>(wsb + align256((size_t)B * T * sizeof(int2)));
         int4* order = reinterpret_cast<int4*>(starts + align256(((size_t)B * T + 1) * sizeof(int32_t)) / sizeof(int32_t));
         int32_t* count = reinterpret_cast<int32_t*>(order + align256((size_t)B * nt * sizeof(int4)) / sizeof(int4));
-        if (hist_bytes > 48 * 1024 &&
+        if (hist_bytes > kUnraisedSmem &&
             (st = raise_dynamic_smem(reinterpret_cast<const void*>(doc_order_kernel), (int)hist_bytes)) != FA_OK)
             return st;
         doc_order_kernel<<<1, 1024, hist_bytes, s>>>(doc_ids, B, T, p.pair_heads ? 1 : 2, rows, starts, order, count, p);

@@ -28,6 +28,11 @@ fa_status check_device();
 // current device, once per (device, kernel); thread-safe.
 fa_status raise_dynamic_smem(const void* kernel, int bytes);
 
+// Dynamic shared memory that a kernel may be launched with without that: 48 KB less
+// its static shared memory (the kernels whose lists grow with a call's sizes have
+// at most 416 bytes of it).
+constexpr size_t kUnraisedSmem = 48 * 1024 - 1024;
+
 // Records how many kernels the current API call launched (per host thread).
 void set_launch_count(int n);
 

@@ -1565,7 +1565,7 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         if (hist_bytes > 200 * 1024) return FA_ERR_UNSUPPORTED;
         auto meta = pw.slots > 0 ? paged_meta_kernel<META_CUT>
                                  : (mod ? paged_meta_kernel<META_PIECES> : paged_meta_kernel<META_LIST>);
-        if (hist_bytes > 48 * 1024 &&
+        if (hist_bytes > kUnraisedSmem &&
             (st = raise_dynamic_smem(reinterpret_cast<const void*>(meta), (int)hist_bytes)) != FA_OK)
             return st;
         cudaStream_t ms = s;
