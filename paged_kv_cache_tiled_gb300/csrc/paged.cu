@@ -1489,7 +1489,8 @@ static PiecesWs pieces_ws_layout(const PagedWs& w, int num_seqs, int mbps, int H
     // (none for queries that make a unit for every SM anyway: the join's launch would cost 3 us)
     const bool few = max_q_len > 0 && !is_decode_row(max_q_len, g) &&
                      total_q / paged_tc_entry_tokens(g) * (long)x.per_rank < kMaxStreamCtas;
-    const long cuts = !few || tiles / kSplitTiles < 2 ? 0 : std::min<long>(tiles / kSplitTiles, kSplitSlots);
+    // (rounded up, so that the places never limit the cuts below kSplitSlots: the shares go by the lengths alone)
+    const long cuts = !few || tiles / kSplitTiles < 2 ? 0 : std::min<long>((tiles + kSplitTiles - 1) / kSplitTiles, kSplitSlots);
     x.slots = (int)std::min<long>(kSplitSlots, std::min<long>(entries, kSplitSlots) * x.per_rank * cuts);
     x.max_pieces = w.max_entries + x.slots;
     x.list = align256(w.total);
