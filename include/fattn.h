@@ -372,8 +372,10 @@ fa_status fa_paged_attn(const void* q, const void* k_cache, const void* v_cache,
  *         NULL
  * Chunks of few queries over long contexts are shared by several SMs along their
  * keys and joined by log-sum-exp: the workspace then holds the shares' partial
- * results (up to 42 MB at d = 128).  The shares depend on the lengths alone, so
- * equal inputs give equal bits.
+ * results (up to 42 MB at d = 128).  A workspace of the size for some num_seqs,
+ * max_blocks_per_seq, total_q and max_q_len serves every call of no larger ones
+ * with the same heads.  The shares depend on the lengths alone, so equal inputs
+ * give equal bits.
  * With a window, blocks that no query of a chunk sees are not read, nor are
  * their block-table entries (they may have been freed); a block that is partly
  * visible must hold finite values.  Everything else as for fa_paged_attn.
@@ -405,8 +407,8 @@ fa_status fa_paged_attn_mod(const void* q, const void* k_cache, const void* v_ca
  *         than acc_len records FA_ERR_BOUNDS and its sums are not written
  *   decay finite, >= 0
  *   lse   fp32 [total_q, Hq], required (written)
- *   ws    at least fa_paged_attn_accum_workspace_size(...) bytes, with the
- *         same max_q_len: beside fa_paged_attn_mod's, the logits of the decode rows
+ *   ws    at least fa_paged_attn_accum_workspace_size(...) bytes (for these or
+ *         larger sizes): beside fa_paged_attn_mod's, the logits of the decode rows
  *         (64 bytes per row, page and kv head that the tables can hold)
  * The sums run in a fixed order: equal inputs give equal bits.  Calls that may
  * overlap on the GPU need workspaces of their own.  A call without

@@ -1479,8 +1479,10 @@ struct PiecesWs {
     int slots, per_rank, max_pieces;
     size_t list, split, ml, o, total;
 };
+// `smaller`: room for every problem of no larger sizes too (those of few queries
+// need more than this one may), which is what the size queries give.
 static PiecesWs pieces_ws_layout(const PagedWs& w, int num_seqs, int mbps, int Hq, int Hkv, int d, int total_q,
-                                 int max_q_len) {
+                                 int max_q_len, bool smaller) {
     PiecesWs x{};
     const int g = Hq / Hkv;
     x.per_rank = paged_tc_pack(g) ? Hkv : (g % 2 == 0 ? Hkv * (g / 2) : Hq);
@@ -1488,7 +1490,7 @@ static PiecesWs pieces_ws_layout(const PagedWs& w, int num_seqs, int mbps, int H
     // (an entry is cut into tiles / kSplitTiles pieces at most, and only when that is two or more)
     // (none for queries that make a unit for every SM anyway: the join's launch would cost 3 us)
     const bool few = max_q_len > 0 && !is_decode_row(max_q_len, g) &&
-                     total_q / paged_tc_entry_tokens(g) * (long)x.per_rank < kMaxStreamCtas;
+                     (smaller || total_q / paged_tc_entry_tokens(g) * (long)x.per_rank < kMaxStreamCtas);
     // (rounded up, so that the places never limit the cuts below kSplitSlots: the shares go by the lengths alone)
     const long cuts = !few || tiles / kSplitTiles < 2 ? 0 : std::min<long>((tiles + kSplitTiles - 1) / kSplitTiles, kSplitSlots);
     x.slots = (int)std::min<long>(kSplitSlots, std::min<long>(entries, kSplitSlots) * x.per_rank * cuts);
@@ -1539,7 +1541,8 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned32(out)) return FA_ERR_INVALID_ARG;
     if (num_blocks == 0 || max_blocks_per_seq == 0) return FA_ERR_INVALID_ARG;
     const PagedWs w = paged_ws_layout(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q);
-    const PiecesWs pw = mod ? pieces_ws_layout(w, num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len) : PiecesWs{};
+    const PiecesWs pw =
+        mod ? pieces_ws_layout(w, num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len, false) : PiecesWs{};
     const AccumWs aw = acc ? accum_ws_layout(pw.total, num_seqs, max_blocks_per_seq, Hq, Hkv, max_q_len) : AccumWs{};
     if (!ws || ws_bytes < (acc ? aw.total : mod ? pw.total : w.total) || (reinterpret_cast<uintptr_t>(ws) & 255)) return FA_ERR_WORKSPACE;
     fa_status st = check_device();
@@ -1711,7 +1714,7 @@ size_t fa_paged_attn_mod_workspace_size(int num_seqs, int max_blocks_per_seq, in
     if (max_q_len < 0) return 0;
     if (fa_paged_attn_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q) == 0 || Hq % Hkv != 0) return 0;
     const PagedWs w = paged_ws_layout(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q);
-    return pieces_ws_layout(w, num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len).total;
+    return pieces_ws_layout(w, num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len, true).total;
 }
 
 fa_status fa_paged_attn_mod(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
