@@ -330,7 +330,7 @@ def fa_prefill_mod(q, k, v, causal: bool = True, scale: float | None = None, sof
         _arg(q, "q", bf16, (B, T, Hq, d), dev), _arg(k, "k", bf16, (B, T, Hkv, d), dev),
         _arg(v, "v", bf16, (B, T, Hkv, d), dev), _arg(out, "out", bf16, (B, T, Hq, d), dev),
         _opt(lse, "lse", f32, (B, Hq, T), dev), B, T, Hq, Hkv, d, 1 if causal else 0,
-        d ** -0.5 if scale is None else scale, softcap, _opt(alibi_slopes, "alibi_slopes", f32, (Hq,), dev), window,
+        d ** -0.5 if scale is None else float(scale), float(softcap), _opt(alibi_slopes, "alibi_slopes", f32, (Hq,), dev), window,
         _opt(prefix_lens, "prefix_lens", i32, (B,), dev), _opt(doc_ids, "doc_ids", i32, (B, T), dev), wp, wn,
         _current_stream(stream, dev)), "fa_prefill_mod")
     return out
@@ -409,6 +409,18 @@ def fa_cache_append_rope(q, k, v, positions, cos_sin, k_cache, v_cache, slot_map
     return q_out
 
 
+def _pair_axes(x, n: int) -> bytes:
+    """n axis numbers as the C call reads them; it checks that there are so many axes.  (bytes() of a number would be that
+    many zeros, and of an array its memory.)"""
+    try:
+        b = x if isinstance(x, bytes) else bytes(x if isinstance(x, (list, tuple)) else [operator.index(a) for a in x])
+    except (TypeError, ValueError):  # not a sequence, not whole numbers, outside 0 .. 255
+        b = b""
+    if len(b) != n:
+        raise ValueError(f"pair_axes must be {n} axis numbers")
+    return b
+
+
 def fa_cache_append_mrope(q, k, v, positions, pair_axes, cos_sin, k_cache, v_cache, slot_mapping, q_out=None,
                           stream=None):
     """fa_cache_append_rope with positions [n_axes, N]: channel pair j turns by the table row of
@@ -420,10 +432,7 @@ def fa_cache_append_mrope(q, k, v, positions, pair_axes, cos_sin, k_cache, v_cac
     dev, dt, bf16 = _device_of(q, "q"), q.dtype, torch.bfloat16
     if dt is not torch.bfloat16 and dt is not torch.float32:
         raise ValueError("q, k, v must all be bf16 or all fp32")
-    if not isinstance(pair_axes, bytes):
-        pair_axes = bytes(pair_axes)  # ValueError outside 0 .. 255
-    if len(pair_axes) != d // 2:  # (their range is checked by the C call)
-        raise ValueError(f"pair_axes must be {d // 2} integers in [0, {n_axes})")
+    pair_axes = _pair_axes(pair_axes, d // 2)
     if q_out is None:
         q_out = _empty((N, Hq, d), bf16, dev, stream)
     _check(_lib.fa_cache_append_mrope(
@@ -647,7 +656,7 @@ def _paged_mod_args(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal, 
             _arg(v_cache, "v_cache", bf16, (nb, Hkv, bs, d), dev), _arg(block_table, "block_table", i32, (S, mbps), dev),
             _arg(ctx_lens, "ctx_lens", i32, (S,), dev), _arg(q_lens, "q_lens", i32, (S,), dev),
             _arg(out, "out", bf16, (total_q, Hq, d), dev), _opt(lse, "lse", torch.float32, (total_q, Hq), dev))
-    tail = (S, mbps, nb, Hq, Hkv, d, bs, 1 if causal else 0, d ** -0.5 if scale is None else scale, softcap,
+    tail = (S, mbps, nb, Hq, Hkv, d, bs, 1 if causal else 0, d ** -0.5 if scale is None else float(scale), float(softcap),
             _opt(alibi_slopes, "alibi_slopes", torch.float32, (Hq,), dev), window,
             _opt(prefix_lens, "prefix_lens", i32, (S,), dev), total_q, max_q_len)
     return dev, head, tail, (S, mbps, Hq, Hkv, d, total_q, max_q_len)
@@ -683,7 +692,7 @@ def fa_paged_attn_accum(q, k_cache, v_cache, block_table, ctx_lens, q_lens, acc_
     rows = (sizes[0], sizes[3], _dims(acc_out, "acc_out", 3)[2])
     wp, wn, ws = _workspace(ws, 0 if ws is not None else fa_paged_attn_accum_workspace_size(*sizes), dev, stream)
     _check(_lib.fa_paged_attn_accum(*head, _opt(acc_in, "acc_in", torch.float32, rows, dev),
-                                    _arg(acc_out, "acc_out", torch.float32, rows, dev), rows[2], decay, *tail, wp, wn,
+                                    _arg(acc_out, "acc_out", torch.float32, rows, dev), rows[2], float(decay), *tail, wp, wn,
                                     _current_stream(stream, dev)), "fa_paged_attn_accum")
     return out
 

@@ -1,6 +1,7 @@
-"""Workspace sizes of the paged calls with modified scores, on the host."""
+"""Sizes and arguments of the calls with modified scores and of the several-axes append, on the host."""
 import itertools
 
+import numpy as np
 import pytest
 import torch
 
@@ -37,3 +38,17 @@ def test_a_call_takes_the_workspace_of_a_larger_one(F):
     assert call(1000) == F.FA_ERR_WORKSPACE
     if not torch.cuda.is_available():  # (with a device it would go on to read its inputs)
         assert call(size) != F.FA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("axes", [[0, 1, 2, 1] * 8, (0, 1, 2, 1) * 8, bytes([0, 1, 2, 1] * 8), np.array([0, 1, 2, 1] * 8),
+                                  np.array([0, 1, 2, 1] * 8, np.uint8), torch.tensor([0, 1, 2, 1] * 8),
+                                  (a for a in [0, 1, 2, 1] * 8), bytearray([0, 1, 2, 1] * 8)], ids=lambda a: type(a).__name__)
+def test_pair_axes(F, axes):
+    assert F._pair_axes(axes, 32) == bytes([0, 1, 2, 1] * 8)
+
+
+@pytest.mark.parametrize("axes", [32, [0] * 31, [0] * 33, [-1] * 32, [256] * 32, [0.0] * 32, np.zeros(4, np.int64), None, "0" * 32,
+                                  np.zeros(32, np.float32), np.zeros((4, 8), np.int64)], ids=str)
+def test_pair_axes_refused(F, axes):
+    with pytest.raises(ValueError):
+        F._pair_axes(axes, 32)
