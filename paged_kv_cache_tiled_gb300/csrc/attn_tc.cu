@@ -501,9 +501,9 @@ __device__ __noinline__ float masked_logits_row(uint32_t taddr, const float* mro
 }
 
 // The same for a modified tile that one multiply-add per score cannot do: a
-// distance bias on a tile with keys on both sides of the row's position, or a
-// cap together with a bias.  Columns outside [vlo, vlim) get -inf; d0 is the
-// first column's key minus the row's position.
+// distance bias on a tile with keys on both sides of the row's position, a cap
+// together with a bias, or a wide cap that no polynomial serves.  Columns outside
+// [vlo, vlim) get -inf; d0 is the first column's key minus the row's position.
 __device__ __noinline__ float modified_logits_row(uint32_t taddr, int vlo, int vlim, float scale_log2, float cap_in,
                                                   float cap_out, float slope, int d0) {
     float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -1198,12 +1198,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // which form of the cap serves every row of the warp (CapPoly; a row that sees nothing takes any)
                 [[maybe_unused]] int cap_tier = 2;
                 if constexpr ((MOD & MOD_CAP) != 0) {
-                    if (p.cap.wide) cap_tier = 3;
                     const bool none = m == -INFINITY;
                     if (__all_sync(0xffffffffu, none || (raw_max <= p.cap.near_max && m + p.cap.near_slack >= 30.f)))
                         cap_tier = 0;
                     else if (__all_sync(0xffffffffu, none || (raw_max <= p.cap.unit_max && m + p.cap.unit_slack >= 30.f)))
                         cap_tier = 1;
+                    else if (p.cap.wide) {  // (out of line: one more form in the loop below cost ordinary caps 4 %)
+                        cap_tier = 3;
+                        (void)modified_logits_row(trow + s_col, vlo, vlim, p.scale_log2, p.mod.cap_in, p.mod.cap_out, 0.f, 0);
+                    }
                 }
                 // O must be rescaled before the first P*V of this tile: in that
                 // (rare) case both halves are signalled after the rescale
@@ -1274,12 +1277,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 return __ffma2_rn(make_float2(tanh_abs(z.x * p.mod.cap_in), tanh_abs(z.y * p.mod.cap_in)),
                                                   cp2, neg_m);
                             }, std::true_type{});
-                        } else {
-                            const float2 cp2 = both(p.mod.cap_out);
-                            exp_pairs([&](float2 z, int) {
-                                return __ffma2_rn(make_float2(tanh_f32(z.x * p.mod.cap_in), tanh_f32(z.y * p.mod.cap_in)),
-                                                  cp2, neg_m);
-                            }, std::true_type{});
+                        } else {  // logits, -inf where masked
+                            exp_pairs([&](float2 z, int) { return __fadd2_rn(z, neg_m); }, std::false_type{});
                         }
                     } else if ((MOD & MOD_BIAS) != 0 && !general) {
                         const float2 k2 = both(bias_k), b2 = both(fmaf(bias_k, (float)(h * 64), bias0) - m_use);
