@@ -39,7 +39,9 @@ constexpr int kCsReaders = 18;  // of a unit's mailbox: every warp but the produ
 constexpr int kCsRows = 128;    // keys of a K tile, and query rows of a tile
 constexpr int kCsPairs = 2, kCsUnitSlots = 4;  // query pairs in flight, unit mailboxes
 constexpr float kCsLog2e = 1.4426950408889634f;
-enum { CS_PLAIN = 0, CS_CAP = 1, CS_BIAS = 2 };  // CS_BIAS also caps when asked
+// CS_BIAS also caps when asked.  kWide variants: the cap is wider than kWideCap (the
+// other form of tanh beside the first cost ordinary caps 3 % and caps with a bias 22 %).
+enum { CS_PLAIN = 0, CS_CAP = 1, CS_BIAS = 2 };
 
 struct ColsumParams {
     const int32_t* bt;
@@ -120,7 +122,7 @@ __device__ __forceinline__ CsUnit cs_unit(const ColsumParams& p, int seq, int hk
     return U;
 }
 
-template <int D, int MOD>
+template <int D, int MOD, bool kWide>
 __global__ void __launch_bounds__(kCsThreads, 1)
     attn_colsum_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const ColsumParams p) {
@@ -513,7 +515,6 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                         }
                         [[maybe_unused]] int tier = 2;
                         if constexpr (MOD == CS_CAP) {
-                            if (p.cap.wide) tier = 3;
                             float mz[2] = {0.f, 0.f};
 #pragma unroll
                             for (int jj = 0; jj < 32; jj += 2)
@@ -546,13 +547,10 @@ __global__ void __launch_bounds__(kCsThreads, 1)
 #pragma unroll
                                         for (int k = top - 2; k >= 0; --k) t = __ffma2_rn(t, q2, co[k]);
                                         x = __ffma2_rn(x, t, l2);
-                                    } else if ((MOD == CS_CAP && decltype(form)::value == 3) ||
-                                               (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
-                                        x.x = fmaf(p.mod.cap_out, tanh_f32(x.x * p.mod.cap_in), l2.x);
-                                        x.y = fmaf(p.mod.cap_out, tanh_f32(x.y * p.mod.cap_in), l2.y);
-                                    } else if (MOD == CS_CAP) {
-                                        x.x = fmaf(p.mod.cap_out, tanh_abs(x.x * p.mod.cap_in), l2.x);
-                                        x.y = fmaf(p.mod.cap_out, tanh_abs(x.y * p.mod.cap_in), l2.y);
+                                    } else if (MOD == CS_CAP || (MOD == CS_BIAS && p.mod.cap_out > 0.f)) {
+                                        auto tanh_of = [](float u) { return kWide ? tanh_f32(u) : tanh_abs(u); };
+                                        x.x = fmaf(p.mod.cap_out, tanh_of(x.x * p.mod.cap_in), l2.x);
+                                        x.y = fmaf(p.mod.cap_out, tanh_of(x.y * p.mod.cap_in), l2.y);
                                     } else {
                                         x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), l2);
                                     }
@@ -578,8 +576,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                         if constexpr (MOD == CS_CAP) {
                             if (tier == 0) sum_block(std::integral_constant<int, 0>{});
                             else if (tier == 1) sum_block(std::integral_constant<int, 1>{});
-                            else if (tier == 2) sum_block(std::integral_constant<int, 2>{});
-                            else sum_block(std::integral_constant<int, 3>{});
+                            else sum_block(std::integral_constant<int, 2>{});
                         } else {
                             sum_block(std::integral_constant<int, 2>{});
                         }
@@ -633,13 +630,13 @@ __global__ void __launch_bounds__(kCsThreads, 1)
     if (warp == kCsMma) tmem_dealloc(tbase, 512);
 }
 
-template <int D, int MOD>
+template <int D, int MOD, bool kWide = false>
 static fa_status launch_colsum(const CUtensorMap& tq, const CUtensorMap& tk, const ColsumParams& p, int grid,
                                cudaStream_t s) {
     const fa_status st =
-        raise_dynamic_smem(reinterpret_cast<const void*>(attn_colsum_kernel<D, MOD>), CsCfg<D>::kSmem);
+        raise_dynamic_smem(reinterpret_cast<const void*>(attn_colsum_kernel<D, MOD, kWide>), CsCfg<D>::kSmem);
     if (st != FA_OK) return st;
-    attn_colsum_kernel<D, MOD><<<grid, kCsThreads, CsCfg<D>::kSmem, s>>>(tq, tk, p);
+    attn_colsum_kernel<D, MOD, kWide><<<grid, kCsThreads, CsCfg<D>::kSmem, s>>>(tq, tk, p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -683,8 +680,10 @@ fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* 
     const int grid = sm_count();
     auto go = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
-        if (mod.slopes) return launch_colsum<D, CS_BIAS>(tq, tk, p, grid, s);
-        if (mod.cap_out > 0.f) return launch_colsum<D, CS_CAP>(tq, tk, p, grid, s);
+        if (mod.slopes)
+            return p.cap.wide ? launch_colsum<D, CS_BIAS, true>(tq, tk, p, grid, s) : launch_colsum<D, CS_BIAS>(tq, tk, p, grid, s);
+        if (mod.cap_out > 0.f)
+            return p.cap.wide ? launch_colsum<D, CS_CAP, true>(tq, tk, p, grid, s) : launch_colsum<D, CS_CAP>(tq, tk, p, grid, s);
         return launch_colsum<D, CS_PLAIN>(tq, tk, p, grid, s);
     };
     return d == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 64>{});

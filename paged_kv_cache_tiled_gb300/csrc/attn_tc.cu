@@ -60,8 +60,11 @@ enum { MODE_DENSE = 0, MODE_MASKED = 1, MODE_PAGED = 2 };
 // Score modifiers of a kernel variant (DENSE and PAGED modes): MOD_RANGE gives
 // every row a run [lo, hi) of visible keys (window, prefix, documents) and is
 // set in every modified variant; MOD_CAP caps the scores; MOD_BIAS subtracts
-// slope |i - j| (and caps them when asked: a rare pair that needs no variant).
-enum { MOD_RANGE = 1, MOD_CAP = 2, MOD_BIAS = 4 };
+// slope |i - j| (and caps them when asked: a rare pair that needs no variant);
+// MOD_WIDE says that the cap is wider than kWideCap (both forms of tanh in one
+// variant, in line or out of it, cost ordinary caps up to 4 % of a prompt's time
+// and 8 % of a chunk's).
+enum { MOD_RANGE = 1, MOD_CAP = 2, MOD_BIAS = 4, MOD_WIDE = 8 };
 constexpr float kBiasSlack = 32.f;  // log2 units that the running max of a biased row may lie above its largest logit
 constexpr int kRangeHoles = 1 << 30;  // flag bit of a query tile's visible KV range
 constexpr int kTcThreads = 320;
@@ -501,9 +504,10 @@ __device__ __noinline__ float masked_logits_row(uint32_t taddr, const float* mro
 }
 
 // The same for a modified tile that one multiply-add per score cannot do: a
-// distance bias on a tile with keys on both sides of the row's position, a cap
-// together with a bias, or a wide cap that no polynomial serves.  Columns outside
-// [vlo, vlim) get -inf; d0 is the first column's key minus the row's position.
+// distance bias on a tile with keys on both sides of the row's position, or a cap
+// together with a bias (kWide: one wider than kWideCap).  Columns outside [vlo, vlim)
+// get -inf; d0 is the first column's key minus the row's position.
+template <bool kWide>
 __device__ __noinline__ float modified_logits_row(uint32_t taddr, int vlo, int vlim, float scale_log2, float cap_in,
                                                   float cap_out, float slope, int d0) {
     float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -517,7 +521,7 @@ __device__ __noinline__ float modified_logits_row(uint32_t taddr, int vlo, int v
         for (int j = 0; j < 32; ++j) {
             const int c = h * 32 + j;
             const float z = __uint_as_float(raw[j]);
-            float x = cap_out > 0.f ? cap_out * tanh_f32(z * cap_in) : z * scale_log2;
+            float x = cap_out > 0.f ? cap_out * (kWide ? tanh_f32(z * cap_in) : tanh_abs(z * cap_in)) : z * scale_log2;
             x = fmaf(-slope, fabsf((float)(d0 + c)), x);
             if (c < vlo || c >= vlim) x = -INFINITY;
             raw[j] = __float_as_uint(x);
@@ -1172,8 +1176,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                        j + 1 >= vlo && j + 1 < vlim ? __uint_as_float(raw[j + 1]) : -INFINITY);
                     }
                 } else if constexpr ((MOD & MOD_BIAS) != 0) {
-                    mxp[0] = modified_logits_row(trow + s_col, vlo, vlim, p.scale_log2, p.mod.cap_in, p.mod.cap_out,
-                                                 slope, kv0 - qpos);
+                    mxp[0] = p.cap.wide ? modified_logits_row<true>(trow + s_col, vlo, vlim, p.scale_log2, p.mod.cap_in,
+                                                                    p.mod.cap_out, slope, kv0 - qpos)
+                                        : modified_logits_row<false>(trow + s_col, vlo, vlim, p.scale_log2, p.mod.cap_in,
+                                                                     p.mod.cap_out, slope, kv0 - qpos);
                 } else {
                     mxp[0] = masked_logits_row(trow + s_col, mrow, lim, p.scale_log2, mrow && ((p.T & 3) == 0));
                 }
@@ -1203,10 +1209,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         cap_tier = 0;
                     else if (__all_sync(0xffffffffu, none || (raw_max <= p.cap.unit_max && m + p.cap.unit_slack >= 30.f)))
                         cap_tier = 1;
-                    else if (p.cap.wide) {  // (out of line: one more form in the loop below cost ordinary caps 4 %)
-                        cap_tier = 3;
-                        (void)modified_logits_row(trow + s_col, vlo, vlim, p.scale_log2, p.mod.cap_in, p.mod.cap_out, 0.f, 0);
-                    }
                 }
                 // O must be rescaled before the first P*V of this tile: in that
                 // (rare) case both halves are signalled after the rescale
@@ -1271,14 +1273,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 t = __ffma2_rn(t, w, p.cap.unit[0]);
                                 return __ffma2_rn(z, t, neg_m);
                             });
-                        } else if (cap_tier == 2) {
+                        } else {
                             const float2 cp2 = both(p.mod.cap_out);
+                            auto tanh_of = [](float u) { return (MOD & MOD_WIDE) != 0 ? tanh_f32(u) : tanh_abs(u); };
                             exp_pairs([&](float2 z, int) {
-                                return __ffma2_rn(make_float2(tanh_abs(z.x * p.mod.cap_in), tanh_abs(z.y * p.mod.cap_in)),
+                                return __ffma2_rn(make_float2(tanh_of(z.x * p.mod.cap_in), tanh_of(z.y * p.mod.cap_in)),
                                                   cp2, neg_m);
                             }, std::true_type{});
-                        } else {  // logits, -inf where masked
-                            exp_pairs([&](float2 z, int) { return __fadd2_rn(z, neg_m); }, std::false_type{});
                         }
                     } else if ((MOD & MOD_BIAS) != 0 && !general) {
                         const float2 k2 = both(bias_k), b2 = both(fmaf(bias_k, (float)(h * 64), bias0) - m_use);
@@ -1589,6 +1590,7 @@ static fa_status launch_tc_mod(int d, const CUtensorMap& tq, const CUtensorMap& 
                                int grid, cudaStream_t s, const TcSched* sched = nullptr) {
     if (p.mod.cap_out > 0.f) p.cap = cap_poly(p.mod);
     if (p.mod.slopes) return launch_tc_d<MODE, MOD_RANGE | MOD_BIAS>(d, tq, tk, tv, p, grid, s, sched);
+    if (p.cap.wide) return launch_tc_d<MODE, MOD_RANGE | MOD_CAP | MOD_WIDE>(d, tq, tk, tv, p, grid, s, sched);
     if (p.mod.cap_out > 0.f) return launch_tc_d<MODE, MOD_RANGE | MOD_CAP>(d, tq, tk, tv, p, grid, s, sched);
     return launch_tc_d<MODE, MOD_RANGE>(d, tq, tk, tv, p, grid, s, sched);
 }

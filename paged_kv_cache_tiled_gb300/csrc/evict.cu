@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(256, 8) evict_move_kernel(uint16_t* kc, uint16
                                                             const int32_t* ctx_lens, int32_t* new_lens, int acc_len,
                                                             int Hkv, int mbps, int dst_mbps, int keep, int num_blocks,
                                                             DevCtx ctx) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is complete
     constexpr int d = D, cpr = D / 8;      // chunks per row
     constexpr int lanes = 2 * cpr;         // threads per row pair (K and V)
     constexpr int rows_cta = 256 / lanes;  // rows side by side
@@ -297,8 +296,11 @@ __global__ void __launch_bounds__(256, 8) evict_move_kernel(uint16_t* kc, uint16
     uint16_t* cache = c < cpr ? kc : vc;
     const int off = (c < cpr ? c : c - cpr) * 8;
     const int sh = blockIdx.x, s = sh / Hkv, h = sh % Hkv;
-    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) {
-        const int cl = ctx_lens[s], n = min(cl, keep);
+    const bool first = blockIdx.y == 0 && h == 0 && threadIdx.x == 0;
+    const int cl = first ? ctx_lens[s] : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is complete
+    if (first) {
+        const int n = min(cl, keep);
         new_lens[s] = lens_fit(cl, n, mbps, dst_mbps, acc_len) ? n : 0;
     }
     const int i0 = blockIdx.y * rows_cta * kEvRows + rr;
