@@ -189,9 +189,6 @@ struct Cursor {
 // stream.  MOD 2 also keeps every logit (log2 units, -inf where masked) at
 // [page of the stream][row][token] for the weight sums that need the final
 // log-sum-exp: logit_rows * 64 bytes beside the page's 64 d.
-// max_q_len: the call's bound on the chunks' lengths when it has no other kernel for
-// longer ones; it sizes the slots, the merge's CTAs and the logits, so a chunk
-// above it is an error (and its rows are not valid).
 constexpr int kLensPerLane = 8;  // sequences per lane whose lengths are loaded in one batch
 constexpr float kLn2f = 0.6931471805599453f, kLog2ef = 1.4426950408889634f;
 template <int D, bool KV8, int ROWS, int MOD>
@@ -200,8 +197,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
                         const uint16_t* __restrict__ q, const int32_t* __restrict__ bt,
                         const int32_t* __restrict__ ctx_lens, const int32_t* __restrict__ q_lens,
                         uint16_t* __restrict__ out, float* __restrict__ part_o, float2* __restrict__ part_ml,
-                        int num_seqs, int mbps, int num_blocks, int Hq, int Hkv, int max_q_len, int q_prefetch_rows,
-                        int causal, float scale_log2, float v_scale, DevCtx ctx, ScoreMod mod) {
+                        int num_seqs, int mbps, int num_blocks, int Hq, int Hkv, int q_prefetch_rows, int causal,
+                        float scale_log2, float v_scale, DevCtx ctx, ScoreMod mod) {
     static_assert(MOD == 0 || !KV8, "score modifiers are built for the bf16 cache");
     const int window = MOD ? mod.window : 0;
     // the merge kernel that follows may be scheduled now; it waits for this
@@ -255,7 +252,6 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     bool bad = false;
     auto count = [&](int ql, int cl) {
         my_q += ql;
-        bad |= ql > max_q_len;
         if (!is_decode_row(ql, g)) return;
         if (ql > cl || cl > mbps * kBS) {
             bad = true;
@@ -806,13 +802,18 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
 // (then four) at a time, so a segment cut into few pieces costs one round
 // trip.  The programmatic launch lets the CTAs compute their offsets as decode
 // CTAs exit; they read partials only after griddepcontrol.wait.
+// max_q_len: the call's bound on the chunks' lengths when it has no other kernel for
+// longer ones.  It sizes the slots, these CTAs and the logits, so a chunk above
+// it is an error, reported here (in the decode kernel the comparison cost 0.1 to
+// 0.4 us).
 constexpr int kMergeMaxThreads = 32 * kDecodeRows;
 template <int D, bool MOD>
 __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const int32_t* __restrict__ ctx_lens,
                                                                     const int32_t* __restrict__ q_lens,
                                                                     const float* part_o, const float2* part_ml,
                                                                     uint16_t* __restrict__ out, int num_seqs,
-                                                                    int Hq, int Hkv, int mbps, int W, ScoreMod mod) {
+                                                                    int Hq, int Hkv, int mbps, int W, int max_q_len,
+                                                                    DevCtx ctx, ScoreMod mod) {
     // (the weight sums that may follow wait for this grid's end before they read)
     if constexpr (MOD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int window = MOD ? mod.window : 0;
@@ -820,6 +821,7 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
     const int s = blockIdx.x, hk = blockIdx.y, r = threadIdx.x >> 5, g = Hq / Hkv;
     const int lane = threadIdx.x & 31;
     const int ql_s = __ldg(q_lens + s), cl_s = __ldg(ctx_lens + s);
+    if (ql_s > max_q_len && hk == 0 && threadIdx.x == 0) raise_error(ctx, ERR_BOUNDS_BIT);
     const bool mine = is_decode_row(ql_s, g) && ql_s <= cl_s && cl_s <= mbps * kBS && r < g * ql_s;
     if (!mine) {
         // every CTA waits for the decode grid, so this grid never completes ahead of it
@@ -1449,7 +1451,8 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
         if (st2 != FA_OK) return st2;
         paged_decode_kernel<D, KV8, R, MOD><<<grid, kStreamWarps * 32, L::kBytes, s>>>(
             tk, tv, static_cast<const uint16_t*>(q), bt, ctx_lens, q_lens, static_cast<uint16_t*>(out), part_o, part_ml,
-            num_seqs, mbps, num_blocks, Hq, Hkv, max_q_len, q_prefetch_rows, causal, scale_log2, v_scale, ctx, mod);
+            num_seqs, mbps, num_blocks, Hq, Hkv, q_prefetch_rows, causal, scale_log2, v_scale, ctx,
+            mod);
         return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     };
     st = merge_rows <= 6 ? launch(std::integral_constant<int, 6>{}) : launch(std::integral_constant<int, kDecodeRows>{});
@@ -1466,7 +1469,7 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, MOD != 0>, ctx_lens, q_lens, static_cast<const float*>(part_o),
                            static_cast<const float2*>(part_ml), static_cast<uint16_t*>(out), num_seqs, Hq, Hkv,
-                           mbps, grid * kStreamWarps, mod) != cudaSuccess)
+                           mbps, grid * kStreamWarps, max_q_len, ctx, mod) != cudaSuccess)
         return FA_ERR_CUDA;
     ++*launches;
     return FA_OK;
