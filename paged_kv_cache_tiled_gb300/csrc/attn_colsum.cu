@@ -6,7 +6,7 @@
 //
 // The transposed product S^T = K Q^T puts a key in each TMEM lane and the query
 // rows in the columns, so the sum over queries is a sum along a thread's own
-// columns: no shuffles, no atomics, a fixed order.  Persistent CTAs (576 threads,
+// columns: no shuffles, no atomics, a fixed order.  Persistent CTAs (608 threads,
 // one per SM) take units of 256 keys of one (sequence, kv head) from a ticket
 // counter, chunks with many query tiles first.  A unit's two K tiles stay in
 // shared memory while the query tiles that see it pass through a ring of two

@@ -19,7 +19,8 @@
 //     at most 16 rows) share each K/V load: they form the M dimension of
 //     m16n8k16 warp MMAs, so K and V are read from HBM exactly once;
 //   * the running row max / row sum are kept in fp32 (online softmax with
-//     base-2 exponentials, scale * log2(e) folded into the scores);
+//     base-2 exponentials, scale * log2(e) folded into the scores); P is rounded
+//     to V's type for the P V product (an MMA's operands have one type);
 //   * a segment inside one warp's range is written as final bf16 output; a
 //     segment cut by a range boundary leaves fp32 partials (unnormalised O,
 //     running max, running sum) in shared memory, which the CTA combines with
