@@ -22,7 +22,7 @@ own = False
 
 BLOCK = 16
 BIAS = 127  # scale code e stands for 2^(e - BIAS)
-LEAST = 8  # the smallest scale code
+LEAST = 87  # the smallest scale code
 LOG_BASE = math.log(1.0e6)  # rotary base of the shapes below
 FP8 = torch.float8_e4m3fn
 
