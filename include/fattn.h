@@ -473,6 +473,146 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
                          fa_stream_t stream);
 
 /*
+ * The 8-bit cache with a scale per block.  Passage: as for fa_cache_append_fp8 and
+ * fa_paged_attn; the pages fix no format.  Reading: E4M3 codes as there, and for
+ * every (block, kv head) one power of two for its keys and one for its values:
+ *   k_cache uint8 [num_blocks, Hkv, 16, d]   (a token's d codes contiguous)
+ *   v_cache uint8 [num_blocks, Hkv, d, 16]   (a channel's 16 tokens contiguous)
+ *   k_exp, v_exp uint8 [num_blocks, Hkv]     code e: the block's values are
+ *                                            E4M3 * 2^(e - 127)
+ *
+ * fa_cache_append_fp8_scaled -- writes the new tokens of every sequence, keys and
+ * queries rotated on the way if asked.
+ *   k, v    [total_q, Hkv, d] in `in_dtype`, sequences packed in order: the last
+ *           q_lens[s] tokens of sequence s, which sit at cache positions
+ *           ctx_lens[s] - q_lens[s] .. ctx_lens[s] - 1 of its blocks
+ *   block_table, ctx_lens, q_lens  as for fa_paged_attn; sum(q_lens) = total_q.
+ *           A block that new tokens go to must not be listed by another sequence
+ *           (fa_pool_* keeps to that: shared blocks are full)
+ *   cos_sin fp32 [max_pos, d] or NULL (no rotation), as for fa_cache_append_rope:
+ *           keys are turned in fp32 by the row of the token's position
+ *   positions int32 [total_q], or NULL: the cache positions.  A position outside
+ *           [0, max_pos) records FA_ERR_BOUNDS; that token and its query are left out
+ *   q       [total_q, Hq, d] in `in_dtype` or NULL; needs cos_sin.  Turned rows go to
+ *           q_out bf16 [total_q, Hq, d]
+ * For each block and head the scale code becomes the smallest e >= 87 whose 448 *
+ * 2^(e - 127) reaches the largest magnitude of the block's new values, or the
+ * block's old code if that is larger and the block holds older tokens of the
+ * sequence; those keep their values, rounded again only where a larger scale leaves
+ * E4M3 no digits for them (below 2^-6 of it).  New codes: E4M3(x * 2^(127 - e)),
+ * round to nearest even.  Infinities become +-448, NaN stays NaN; neither moves the
+ * scale.  Slots behind the last token are left as they were.  Without a rotation the
+ * codes are exact; with one, values within fp32's rounding of a border between two
+ * codes may get either.  Sequences with inconsistent lengths record FA_ERR_BOUNDS
+ * and are skipped, as are blocks outside the pool.  d = 64 or 128; pointers
+ * 16-byte aligned.  One launch.
+ */
+fa_status fa_cache_append_fp8_scaled(const void* q, const void* k, const void* v, const int32_t* positions,
+                                     const float* cos_sin, int max_pos, void* q_out, void* k_cache, void* v_cache,
+                                     uint8_t* k_exp, uint8_t* v_exp, const int32_t* block_table,
+                                     const int32_t* ctx_lens, const int32_t* q_lens, int num_seqs,
+                                     int max_blocks_per_seq, int num_blocks, int total_q, int Hq, int Hkv, int d,
+                                     int block_size, fa_dtype in_dtype, fa_stream_t stream);
+
+/*
+ * fa_paged_attn_fp8_scaled -- fa_paged_attn over that cache, single tokens and
+ * chunks, d = 64 or 128.
+ *   lse   fp32 [total_q, Hq] natural-log log-sum-exp of each row's scores, or NULL
+ *   ws    at least fa_paged_attn_fp8_scaled_workspace_size(...) bytes, 256-byte
+ *         aligned; the size for some num_seqs, max_blocks_per_seq, total_q and
+ *         max_q_len serves every call of no larger ones with the same heads
+ * Queries may have any bf16 magnitude.  The codes are widened to f16 (exactly) and
+ * the softmax weights are f16 relative to the largest weight * value scale of the
+ * row, sums fp32; a context's v_exp codes must lie within 100 of each other for
+ * the row sums to keep all their digits (the append's codes do below values of 2^68).
+ * Codes of tokens below ctx_lens[s] must not be NaN; what is stored behind them does
+ * not matter.  Equal inputs give equal bits.  Everything else as for fa_paged_attn.
+ */
+size_t fa_paged_attn_fp8_scaled_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv,
+                                               int d, int total_q, int max_q_len);
+fa_status fa_paged_attn_fp8_scaled(const void* q, const void* k_cache, const void* v_cache,
+                                   const uint8_t* k_exp, const uint8_t* v_exp, const int32_t* block_table,
+                                   const int32_t* ctx_lens, const int32_t* q_lens, void* out, float* lse,
+                                   int num_seqs, int max_blocks_per_seq, int num_blocks, int Hq, int Hkv,
+                                   int d, int block_size, int causal, float scale, int total_q, int max_q_len,
+                                   void* ws, size_t ws_bytes, fa_stream_t stream);
+
+/*
+ * Attention over the blocks that matter to a query: a summary of every block
+ * (fa_block_bounds), a choice of blocks for each query by those summaries
+ * (fa_block_select), and attention over the chosen blocks (fa_paged_attn_blocks).
+ * Passage: "Paged Attention Kernels" (fixed blocks behind a block table; the list
+ * of blocks a query reads is another level of it).
+ *
+ * fa_block_bounds -- smallest and largest value of every channel over a block's keys.
+ *   k_cache  bf16 [num_blocks, Hkv, 16, d], or the 8-bit cache with its k_exp
+ *            (k_exp NULL: bf16)
+ *   bounds   bf16 [num_blocks, Hkv, 2, d]: [.., 0, :] the minima, [.., 1, :] the maxima
+ * Written for the blocks that the last q_lens[s] tokens of each sequence lie in (to
+ * be called after they were appended; q_lens = ctx_lens: all blocks), over the tokens
+ * below ctx_lens[s]; other blocks' bounds are left as they were.  Exact.  NaN keys
+ * are passed over.  block_table, ctx_lens, q_lens, total_q as for fa_paged_attn.
+ */
+fa_status fa_block_bounds(const void* k_cache, const uint8_t* k_exp, const int32_t* block_table,
+                          const int32_t* ctx_lens, const int32_t* q_lens, void* bounds, int num_seqs,
+                          int max_blocks_per_seq, int num_blocks, int total_q, int Hkv, int d,
+                          int block_size, fa_stream_t stream);
+
+/*
+ * fa_block_select -- for each query and kv head the blocks whose keys may get the
+ * largest scores.  The query at position p = ctx_lens[s] - q_lens[s] + r sees
+ * the blocks 0 .. p / 16 of its sequence.  Score of a block: the most that q . k can be
+ * for a key within its bounds, for the query head of the group that gives the most,
+ *     u = max over the group's heads of sum over c of max(q_c lo_c, q_c hi_c).
+ * If the query sees more than `keep` blocks: the first `sink`, the last `recent` and,
+ * of the others, those with the largest u (equal: the earlier block), `keep` in all;
+ * else all of them.
+ *   q        bf16 [total_q, Hq, d], finite; bounds as above, finite
+ *   sel      int32 [total_q, Hkv, keep] (written): block numbers within the
+ *            sequence, ascending, -1 behind the last
+ *   keep > 0, recent >= 0, sink >= 0, sink + recent <= keep
+ *   max_q_len  host-side upper bound on q_lens (total_q is always valid): only
+ *            the work's division goes by it
+ *   ws       at least fa_block_select_workspace_size(...) bytes, 256-byte aligned
+ *            (the scores, 4 bytes for each query, kv head and table entry, and 12
+ *            bytes a table entry for each of 640 CTAs)
+ * The choice is that of exact arithmetic: blocks whose scores are too close to tell
+ * apart in fp32 are summed again in 64 bits.  Calls that may overlap on the GPU need
+ * workspaces of their own.  Sequences with inconsistent lengths record
+ * FA_ERR_BOUNDS and their rows are left as they were; a block outside the pool
+ * records it and counts as one of bounds 0.
+ */
+size_t fa_block_select_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv, int d,
+                                      int total_q);
+fa_status fa_block_select(const void* q, const void* bounds, const int32_t* block_table,
+                          const int32_t* ctx_lens, const int32_t* q_lens, int32_t* sel, int num_seqs,
+                          int max_blocks_per_seq, int num_blocks, int Hq, int Hkv, int d, int block_size,
+                          int keep, int recent, int sink, int total_q, int max_q_len, void* ws,
+                          size_t ws_bytes, fa_stream_t stream);
+
+/*
+ * fa_paged_attn_blocks -- attention of each query over the listed blocks of its
+ * sequence (causal: the keys at its own position and before).
+ *   k_cache, v_cache  bf16 as for fa_paged_attn (k_exp, v_exp NULL), or the 8-bit
+ *            cache with block scales
+ *   sel      int32 [total_q, Hkv, keep]: block numbers within the sequence, in any
+ *            order, none twice; negative entries are passed over; a block behind
+ *            the query's position has no visible key; one behind the context's
+ *            last block records FA_ERR_BOUNDS and is passed over
+ *   lse      fp32 [total_q, Hq] log-sum-exp of the visible scores, or NULL
+ * A query without a visible key gets output 0 and LSE -inf.  The values of visible
+ * keys must be finite; nothing else of a block reaches the result.  No workspace, one
+ * launch; equal inputs give equal bits.  out 16-byte aligned.  Everything else as for
+ * fa_paged_attn and fa_paged_attn_fp8_scaled.
+ */
+fa_status fa_paged_attn_blocks(const void* q, const void* k_cache, const void* v_cache,
+                               const uint8_t* k_exp, const uint8_t* v_exp, const int32_t* block_table,
+                               const int32_t* ctx_lens, const int32_t* q_lens, const int32_t* sel, int keep,
+                               void* out, float* lse, int num_seqs, int max_blocks_per_seq, int num_blocks,
+                               int Hq, int Hkv, int d, int block_size, float scale, int total_q,
+                               fa_stream_t stream);
+
+/*
  * fa_paged_attn_noalloc -- fa_paged_attn for callers that cannot allocate
  * device memory.  The pages have no counterpart: this is a convenience of the
  * library, not part of the method.

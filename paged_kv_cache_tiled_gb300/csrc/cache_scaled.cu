@@ -1,0 +1,374 @@
+// The paged cache in 8 bits with a scale per block and kv head, and the blocks'
+// channel bounds.
+//
+// fa_cache_append_fp8_scaled: a (block, kv head) holds E4M3 codes and one scale
+// 2^(e - 127) for its keys, one for its values.  The scale is a power of two: E4M3
+// is a floating format, so a finer scale would not make its values any finer, and
+// with powers of two a block whose scale grows keeps its codes' values exactly (only
+// what falls below 2^-6 of the new scale is rounded again).  The call knows its
+// tokens by sequence (block table and lengths), so one warp owns a (block, head) of
+// K or of V: it loads the block's new tokens (at most 16, a lane D / 32 channels of
+// each, all loads in flight), turns the keys, finds the largest magnitude, and
+// writes codes; no atomics, nothing that depends on an order.  V is channel-major:
+// a lane's codes are whole 16-byte rows.  Queries are turned by further warps of the
+// same launch, one a token.  Memory bound on prompts, latency bound on single tokens.
+//
+// fa_block_bounds: smallest and largest value of every channel over a block's tokens,
+// recomputed for the blocks that a chunk's tokens lie in; a warp a (block, head).
+#include <algorithm>
+
+#include "cache_scaled.cuh"
+
+namespace fa {
+
+struct AppendArgs {
+    const void *q, *k, *v;
+    const int32_t* positions;  // null: the cache positions
+    const float* cos_sin;      // null: no rotation
+    uint16_t* q_out;
+    uint8_t *kc, *vc, *ke, *ve;
+    const int32_t *bt, *ctx_lens, *q_lens;
+    int max_pos, num_seqs, mbps, num_blocks, total_q, Hq, Hkv;
+    long block_warps;  // warps of the blocks, those of the queries follow
+    DevCtx ctx;
+};
+
+// N consecutive values (N = 2 or 4) as fp32.
+template <bool kF32, int N>
+struct Raw {
+    uint32_t w[kF32 ? N : N / 2];
+    __device__ __forceinline__ void load(const void* base, long at) {
+        if constexpr (kF32) {
+            const float* p = static_cast<const float*>(base) + at;
+            if constexpr (N == 4) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+                w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+            } else {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+                w[0] = u.x; w[1] = u.y;
+            }
+        } else {
+            const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+            if constexpr (N == 4) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+                w[0] = u.x; w[1] = u.y;
+            } else {
+                w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (kF32) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+};
+
+// E4M3 codes times `ratio` (a power of two), rounded again.
+__device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float ratio) {
+    float x[4];
+    e4m3x4_to_f32x4(w, ratio, x);
+    return f32x4_to_e4m3x4(x[0], x[1], x[2], x[3]);
+}
+
+// The new tokens of one (block, head), K or V.
+template <int D, bool kF32>
+__device__ __forceinline__ void append_block(const AppendArgs& a, const SeqItem& it, int hk, bool is_v) {
+    constexpr int N = D / 32, B = kScaledBlock;
+    const int lane = threadIdx.x & 31;
+    const int first = it.cl - it.ql, blk = first / B + it.off;
+    const int lo = max(0, first - blk * B), hi = min(B, it.cl - blk * B);  // the block's new tokens
+    const int phys = __ldg(a.bt + (long)it.s * a.mbps + blk);
+    if (phys < 0 || phys >= a.num_blocks) {
+        if (lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        return;
+    }
+    const long row0 = (long)it.q0 + blk * B - first;  // packed row of the block's token 0
+    const long head = (long)phys * a.Hkv + hk;
+    uint8_t* page = (is_v ? a.vc : a.kc) + head * B * D;
+    uint8_t* exps = is_v ? a.ve : a.ke;
+    const int e_old = lo > 0 ? (int)exps[head] : 0;
+    Raw<kF32, N> raw[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+        if (i >= lo && i < hi) raw[i].load(is_v ? a.v : a.k, ((row0 + i) * a.Hkv + hk) * D + lane * N);
+    float x[B][N];
+    unsigned live = ((1u << hi) - 1) & ~((1u << lo) - 1);
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int c = 0; c < N; ++c) x[i][c] = i >= lo && i < hi ? raw[i].get(c) : 0.f;
+    if (!is_v && a.cos_sin) {
+        // channel j < D/2 (lanes 0 .. 15) pairs with j + D/2 (lanes 16 .. 31)
+        const int at = (lane & 15) * N;
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (i < lo || i >= hi) continue;  // (the same for the whole warp)
+            const int pos = a.positions ? __ldg(a.positions + row0 + i) : blk * B + i;
+            if (pos < 0 || pos >= a.max_pos) {
+                if (lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
+                live &= ~(1u << i);
+                continue;
+            }
+            Raw<true, N> co, si;
+            co.load(a.cos_sin, (long)pos * D + at);
+            si.load(a.cos_sin, (long)pos * D + D / 2 + at);
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                const float y = __shfl_xor_sync(0xffffffffu, x[i][c], 16);
+                x[i][c] = lane < 16 ? fmaf(x[i][c], co.get(c), -(y * si.get(c))) : fmaf(x[i][c], co.get(c), y * si.get(c));
+            }
+        }
+    }
+    // the largest finite magnitude
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const float v = fabsf(x[i][c]);
+            if (((live >> i) & 1u) && v < INFINITY) m = fmaxf(m, v);
+        }
+    // the smallest code whose 448 (1.75 * 2^8) times the scale reaches it
+    const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    const int e = max(max(e_old, kExpLeast), (int)(mb >> 23) - 8 + ((mb & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+    const float inv = __uint_as_float((uint32_t)max(0, 254 - e) << 23);                  // 2^(127 - e)
+    const float ratio = __uint_as_float((uint32_t)max(0, kExpBias + e_old - e) << 23);  // of the older tokens' codes
+    const bool moved = lo > 0 && e != e_old;
+    if (!is_v) {
+        uint8_t* at = page + lane * N;
+        if (moved) {
+            for (int i = 0; i < lo; ++i) {
+                if constexpr (N == 4)
+                    *reinterpret_cast<uint32_t*>(at + i * D) = rescale_codes(*reinterpret_cast<uint32_t*>(at + i * D), ratio);
+                else
+                    *reinterpret_cast<uint16_t*>(at + i * D) =
+                        (uint16_t)rescale_codes(*reinterpret_cast<uint16_t*>(at + i * D), ratio);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (!((live >> i) & 1u)) continue;
+            const uint32_t lo2 = f32x2_to_e4m3x2(x[i][0] * inv, x[i][1] * inv);
+            if constexpr (N == 4)
+                *reinterpret_cast<uint32_t*>(at + i * D) = lo2 | f32x2_to_e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16;
+            else
+                *reinterpret_cast<uint16_t*>(at + i * D) = (uint16_t)lo2;
+        }
+    } else {
+        uint4* at = reinterpret_cast<uint4*>(page) + lane * N;  // a channel's 16 tokens
+        uint4 old[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) old[c] = live == 0xffffu ? make_uint4(0, 0, 0, 0) : at[c];
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            uint32_t o[4] = {old[c].x, old[c].y, old[c].z, old[c].w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const unsigned l4 = (live >> (4 * w)) & 15u;
+                auto bytes = [](unsigned b) {
+                    return ((b & 1u) | (b & 2u) << 7 | (b & 4u) << 14 | (b & 8u) << 21) * 255u;
+                };
+                if (moved) {
+                    const uint32_t mask = bytes((((1u << lo) - 1) >> (4 * w)) & 15u);
+                    o[w] = (o[w] & ~mask) | (rescale_codes(o[w], ratio) & mask);
+                }
+                const uint32_t mask = bytes(l4);
+                o[w] = (o[w] & ~mask) | (f32x4_to_e4m3x4(x[4 * w][c] * inv, x[4 * w + 1][c] * inv, x[4 * w + 2][c] * inv,
+                                                         x[4 * w + 3][c] * inv) & mask);
+            }
+            at[c] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+    if (lane == 0) exps[head] = (uint8_t)e;
+}
+
+template <int D, bool kF32>
+__global__ void __launch_bounds__(128) append_scaled_kernel(const __grid_constant__ AppendArgs a) {
+    const long w = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    SeqItem it;
+    if (w < a.block_warps) {
+        const int per = 2 * a.Hkv;
+        const bool some = find_item(a.q_lens, a.ctx_lens, a.num_seqs, w / per,
+                                    [&](int ql, int cl) { return chunk_blocks(ql, cl, a.mbps); }, it);
+        if (w == 0 && lane == 0 && (it.bad || it.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        if (!some || (long long)it.q0 + it.ql > a.total_q) return;
+        const int r = (int)(w % per);
+        append_block<D, kF32>(a, it, r >> 1, r & 1);
+        return;
+    }
+    // a query row's heads
+    const long row = w - a.block_warps;
+    if (row >= a.total_q || !a.q) return;
+    if (!find_item(a.q_lens, a.ctx_lens, a.num_seqs, row,
+                   [&](int ql, int cl) { return lens_ok(ql, cl, a.mbps) ? ql : -1; }, it))
+        return;
+    const long at_row = (long)it.q0 + it.off;  // (rows of sequences with inconsistent lengths have no place in the count)
+    if (at_row >= a.total_q) return;
+    const int pos = a.positions ? __ldg(a.positions + at_row) : it.cl - it.ql + it.off;
+    if (pos < 0 || pos >= a.max_pos) {
+        if (lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        return;
+    }
+    constexpr int kLanes = D / 8;  // lanes a row: 4 channel pairs each
+    const int c = (lane % kLanes) * 4;
+    Raw<true, 4> co, si;
+    co.load(a.cos_sin, (long)pos * D + c);
+    si.load(a.cos_sin, (long)pos * D + D / 2 + c);
+#pragma unroll 4
+    for (int h = lane / kLanes; h < a.Hq; h += 32 / kLanes) {
+        const long at = (at_row * a.Hq + h) * D + c;
+        Raw<kF32, 4> x, y;
+        x.load(a.q, at);
+        y.load(a.q, at + D / 2);
+        float u[4], v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u[i] = fmaf(x.get(i), co.get(i), -(y.get(i) * si.get(i)));
+            v[i] = fmaf(y.get(i), co.get(i), x.get(i) * si.get(i));
+        }
+        *reinterpret_cast<uint2*>(a.q_out + at) = make_uint2(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]));
+        *reinterpret_cast<uint2*>(a.q_out + at + D / 2) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
+}
+
+// ------------------------------------------------------------------ bounds --
+template <int D, bool KV8>
+__global__ void __launch_bounds__(128) block_bounds_kernel(const void* __restrict__ kc, const uint8_t* __restrict__ ke,
+                                                           const int32_t* __restrict__ bt,
+                                                           const int32_t* __restrict__ ctx_lens,
+                                                           const int32_t* __restrict__ q_lens, uint16_t* __restrict__ bounds,
+                                                           int num_seqs, int mbps, int num_blocks, int total_q, int Hkv,
+                                                           DevCtx ctx) {
+    constexpr int N = D / 32, B = kScaledBlock;
+    const long w = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, hk = (int)(w % Hkv);
+    SeqItem it;
+    const bool some = find_item(q_lens, ctx_lens, num_seqs, w / Hkv,
+                                [&](int ql, int cl) { return chunk_blocks(ql, cl, mbps); }, it);
+    if (w == 0 && lane == 0 && (it.bad || it.rows != total_q)) raise_error(ctx, ERR_BOUNDS_BIT);
+    if (!some) return;
+    const int blk = (it.cl - it.ql) / B + it.off, n = min(B, it.cl - blk * B);
+    const int phys = __ldg(bt + (long)it.s * mbps + blk);
+    if (phys < 0 || phys >= num_blocks) {
+        if (lane == 0) raise_error(ctx, ERR_BOUNDS_BIT);
+        return;
+    }
+    const long head = (long)phys * Hkv + hk;
+    float lo[N], hi[N];
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        lo[c] = INFINITY;
+        hi[c] = -INFINITY;
+    }
+    uint32_t raw[B][KV8 ? 1 : N / 2];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+        const long at = head * B * D + i * D + lane * N;
+        if (i >= n) continue;
+        if constexpr (KV8) {
+            if constexpr (N == 4) raw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(kc) + at));
+            else raw[i][0] = __ldg(reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(kc) + at));
+        } else {
+            Raw<false, N> r;
+            r.load(kc, at);
+#pragma unroll
+            for (int c = 0; c < N / 2; ++c) raw[i][c] = r.w[c];
+        }
+    }
+    const float f = KV8 ? scale_of(ke[head]) : 1.f;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+        if (i >= n) continue;
+        float x[4];
+        if constexpr (KV8) {
+            e4m3x4_to_f32x4(raw[i][0], f, x);
+        } else {
+#pragma unroll
+            for (int c = 0; c < N; ++c) x[c] = __uint_as_float(c & 1 ? raw[i][c / 2] & 0xFFFF0000u : raw[i][c / 2] << 16);
+        }
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            lo[c] = fminf(lo[c], x[c]);
+            hi[c] = fmaxf(hi[c], x[c]);
+        }
+    }
+    uint16_t* dst = bounds + head * 2 * D + lane * N;  // (bf16 values, or E4M3 ones times a power of two: exact)
+    if constexpr (N == 4) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
+        *reinterpret_cast<uint2*>(dst + D) = make_uint2(pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]));
+    } else {
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(lo[0], lo[1]);
+        *reinterpret_cast<uint32_t*>(dst + D) = pack_bf16x2(hi[0], hi[1]);
+    }
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_cache_append_fp8_scaled(const void* q, const void* k, const void* v, const int32_t* positions,
+                                     const float* cos_sin, int max_pos, void* q_out, void* k_cache, void* v_cache,
+                                     uint8_t* k_exp, uint8_t* v_exp, const int32_t* block_table, const int32_t* ctx_lens,
+                                     const int32_t* q_lens, int num_seqs, int max_blocks_per_seq, int num_blocks,
+                                     int total_q, int Hq, int Hkv, int d, int block_size, fa_dtype in_dtype,
+                                     fa_stream_t stream) {
+    set_launch_count(0);
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || num_blocks < 0 || total_q < 0 || Hkv <= 0 || max_pos < 0 ||
+        (q && Hq <= 0) || (in_dtype != FA_BF16 && in_dtype != FA_F32))
+        return FA_ERR_INVALID_ARG;
+    if (block_size != kScaledBlock || (d != 64 && d != 128)) return FA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || total_q == 0) return FA_OK;
+    if (!k || !v || !k_cache || !v_cache || !k_exp || !v_exp || !block_table || !ctx_lens || !q_lens) return FA_ERR_INVALID_ARG;
+    if ((q && (!q_out || !cos_sin)) || (positions && !cos_sin)) return FA_ERR_INVALID_ARG;  // queries are only turned
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q) || !aligned16(q_out) ||
+        !aligned16(cos_sin))
+        return FA_ERR_INVALID_ARG;
+    if (num_blocks == 0 || max_blocks_per_seq == 0) return FA_ERR_INVALID_ARG;
+    fa_status st = check_device();
+    if (st != FA_OK) return st;
+    AppendArgs a{q, k, v, positions, cos_sin, static_cast<uint16_t*>(q_out), static_cast<uint8_t*>(k_cache),
+                 static_cast<uint8_t*>(v_cache), k_exp, v_exp, block_table, ctx_lens, q_lens, max_pos, num_seqs,
+                 max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, 0, {}};
+    if ((st = make_ctx(&a.ctx)) != FA_OK) return st;
+    a.block_warps = chunk_blocks_bound(num_seqs, total_q) * 2 * Hkv;
+    const long ctas = (a.block_warps + (q ? total_q : 0) + 3) / 4;
+    if (ctas > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto kernel = d == 128 ? (in_dtype == FA_F32 ? append_scaled_kernel<128, true> : append_scaled_kernel<128, false>)
+                           : (in_dtype == FA_F32 ? append_scaled_kernel<64, true> : append_scaled_kernel<64, false>);
+    kernel<<<(unsigned)ctas, 128, 0, s>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    set_launch_count(1);
+    return FA_OK;
+}
+
+fa_status fa_block_bounds(const void* k_cache, const uint8_t* k_exp, const int32_t* block_table, const int32_t* ctx_lens,
+                          const int32_t* q_lens, void* bounds, int num_seqs, int max_blocks_per_seq, int num_blocks,
+                          int total_q, int Hkv, int d, int block_size, fa_stream_t stream) {
+    set_launch_count(0);
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || num_blocks < 0 || total_q < 0 || Hkv <= 0) return FA_ERR_INVALID_ARG;
+    if (block_size != kScaledBlock || (d != 64 && d != 128)) return FA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || total_q == 0) return FA_OK;
+    if (!k_cache || !block_table || !ctx_lens || !q_lens || !bounds) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(bounds)) return FA_ERR_INVALID_ARG;
+    if (num_blocks == 0 || max_blocks_per_seq == 0) return FA_ERR_INVALID_ARG;
+    fa_status st = check_device();
+    if (st != FA_OK) return st;
+    DevCtx ctx;
+    if ((st = make_ctx(&ctx)) != FA_OK) return st;
+    const long ctas = (chunk_blocks_bound(num_seqs, total_q) * Hkv + 3) / 4;
+    if (ctas > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
+    auto kernel = d == 128 ? (k_exp ? block_bounds_kernel<128, true> : block_bounds_kernel<128, false>)
+                           : (k_exp ? block_bounds_kernel<64, true> : block_bounds_kernel<64, false>);
+    kernel<<<(unsigned)ctas, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        k_cache, k_exp, block_table, ctx_lens, q_lens, static_cast<uint16_t*>(bounds), num_seqs, max_blocks_per_seq,
+        num_blocks, total_q, Hkv, ctx);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    set_launch_count(1);
+    return FA_OK;
+}
+
+}  // extern "C"

@@ -39,7 +39,7 @@
 #include <mutex>
 #include <type_traits>
 
-#include "host_common.cuh"
+#include "page_mma.cuh"
 
 namespace fa {
 
@@ -53,6 +53,13 @@ fa_status launch_paged_prefill(const void* q, const void* k_cache, const void* v
                                int mbps, int num_blocks, int Hq, int Hkv, int d, int causal, float scale,
                                int total_q, cudaStream_t s, const DevCtx& ctx, const ScoreMod* mod,
                                const int4* pieces, float4* part_o, float2* part_ml);
+// The same over the 8-bit cache with block scales, launched from attn_tc8.cu.
+fa_status launch_paged_prefill_fp8(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_exp,
+                                   const uint8_t* v_exp, const int32_t* block_table, const int32_t* ctx_lens,
+                                   const int32_t* q_lens, const int32_t* q_start, const int32_t* work_count, void* out,
+                                   float* lse, int mbps, int num_blocks, int Hq, int Hkv, int d, int causal, float scale,
+                                   int total_q, const int4* pieces, float4* part_o, float2* part_ml, cudaStream_t s,
+                                   const DevCtx& ctx);
 // Weight sums of the sequences that take the tensor-core path (attn_colsum.cu).
 fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* block_table, const int32_t* ctx_lens,
                              const int32_t* q_lens, const int32_t* q_start, const int32_t* k_start,
@@ -144,13 +151,19 @@ __device__ __forceinline__ int stream_warps(int W, long long P) {
     return (int)min((long long)W, (P + kStreamWarps - 1) / kStreamWarps * kStreamWarps);
 }
 
+// The cache that a decode kernel reads: bf16, E4M3 with a scale for the whole cache, or
+// E4M3 with a power of two for every block and kv head (PageMma's form).
+enum { KV_BF16 = 0, KV_FP8 = 1, KV_FP8_SCALED = 2 };
+constexpr int kPageBatch = 32;  // KV_FP8_SCALED: pages that a warp looks up at a time, a lane each
+
 // Shared memory of a decode CTA: each warp's TMA ring, then each warp's slot
 // for the partial of its first segment (ROWS query rows).  The ring has three
 // stages (8 KB each at d = 128, 4 KB at d = 64) except at d = 128 with slots of
 // 16 rows, which leave room for two; the 8-bit (E4M3) cache's pages are half
 // the bytes, so its ring is twice as deep to keep the same bytes in flight.
-template <int D, bool KV8, int ROWS>
+template <int D, int KV, int ROWS>
 struct StreamSmem {
+    static constexpr bool KV8 = KV != KV_BF16;
     static constexpr int kPage = kBS * D * (KV8 ? 1 : 2);  // bytes of one K (or V) page
     static constexpr int kStage = 2 * kPage;              // K page + V page
     static constexpr int kStages = (KV8 ? 2 : 1) * (D == 128 && ROWS > 6 ? 2 : 3);
@@ -162,7 +175,8 @@ struct StreamSmem {
     static constexpr int kSlots = kStreamWarps * kSlotBytes;
     static constexpr int kBars = kStreamWarps * kStages + 1;
     static constexpr int kCutEntries = 2 * kStreamWarps;  // segments cut between the CTA's warps, at most
-    static constexpr int kBytes = 1024 /*align slack*/ + kRing + kSlots + kBars * 8 + 64 + kCutEntries * 32;
+    static constexpr int kLists = KV == KV_FP8_SCALED ? kStreamWarps * 2 * kPageBatch * 8 : 0;  // pages looked up
+    static constexpr int kBytes = 1024 /*align slack*/ + kRing + kSlots + kBars * 8 + 64 + kCutEntries * 32 + kLists;
     static_assert(kSlotBytes <= kStages * kStage, "a warp's ring holds the partial of its last segment");
     static_assert(kSlots % 64 == 0 && kSlotBytes % 16 == 0, "slots keep 16-byte alignment");
     static_assert((kStreamWarps * kStages * 8) % 64 == 0, "the barrier after the ring barriers is 64-byte aligned");
@@ -192,20 +206,24 @@ struct Cursor {
 // log-sum-exp: logit_rows * 64 bytes beside the page's 64 d.
 constexpr int kLensPerLane = 8;  // sequences per lane whose lengths are loaded in one batch
 constexpr float kLn2f = 0.6931471805599453f, kLog2ef = 1.4426950408889634f;
-template <int D, bool KV8, int ROWS, int MOD>
+// KV_FP8_SCALED takes the warps' pages two (d = 64: four) at a time, and block numbers
+// and scales ahead in batches of 32.
+template <int D, int KV, int ROWS, int MOD>
 __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const uint16_t* __restrict__ q, const int32_t* __restrict__ bt,
                         const int32_t* __restrict__ ctx_lens, const int32_t* __restrict__ q_lens,
                         uint16_t* __restrict__ out, float* __restrict__ part_o, float2* __restrict__ part_ml,
                         int num_seqs, int mbps, int num_blocks, int Hq, int Hkv, int q_prefetch_rows, int causal,
-                        float scale_log2, float v_scale, DevCtx ctx, ScoreMod mod) {
+                        float scale_log2, float v_scale, DevCtx ctx, ScoreMod mod, const uint8_t* __restrict__ k_exp,
+                        const uint8_t* __restrict__ v_exp) {
+    constexpr bool KV8 = KV != KV_BF16, SCALED = KV == KV_FP8_SCALED;
     static_assert(MOD == 0 || !KV8, "score modifiers are built for the bf16 cache");
     const int window = MOD ? mod.window : 0;
     // the merge kernel that follows may be scheduled now; it waits for this
     // grid's completion before reading anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    using L = StreamSmem<D, KV8, ROWS>;
+    using L = StreamSmem<D, KV, ROWS>;
     constexpr int kStreamStages = L::kStages;  // ring depth of this variant
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -289,7 +307,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     }
     const long long P = __shfl_sync(0xffffffffu, inc_p, 31);
     if (P == 0) return;
-    if constexpr (MOD != 0) {
+    if constexpr (MOD != 0 || SCALED) {
         W = stream_warps(W, P);
         if (gw >= W) return;  // a whole CTA
     }
@@ -353,12 +371,62 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
             if (c.s < num_seqs) c.blk0 = first_block(__ldg(ctx_lens + c.s), __ldg(q_lens + c.s), window);
     };
 
-    Cursor ci = start;  // issue cursor (lane 0 only)
+    Cursor ci = start;  // issue cursor (lane 0 only; SCALED: of the next batch's first page)
+    // SCALED: (block, kv head << 16 | v scale << 8 | k scale) of the warp's pages, two batches by turns.  Lane j
+    // looks up page j of the batch at `ci`: its place, its block (into `found`), and later its scales.
+    [[maybe_unused]] int2* list = reinterpret_cast<int2*>(cut_table + 2 * L::kCutEntries) + warp * 2 * kPageBatch;
+    [[maybe_unused]] int found = -1, found_hk = 0, found_scales = 0;
+    [[maybe_unused]] auto look_up_blocks = [&](int first) {  // pages first .. first + 31 of the warp
+        found = -1;
+        const bool in = first + lane < n_pages;
+        Cursor c = ci;
+        int off = lane;  // pages from `ci` on
+        while (in) {
+            const int left = c.nblk - c.blk;
+            if (off < left) break;
+            off -= left;
+            c.blk = c.nblk - 1;
+            advance(c);
+        }
+        if (in) {
+            c.blk += off;
+            found = __ldg(bt + (long)c.s * mbps + c.blk);
+            found_hk = c.hk;
+            if (lane == kPageBatch - 1) advance(c);
+        }
+        // the next batch begins behind the last lane's page (if there is one)
+        ci.s = __shfl_sync(0xffffffffu, c.s, kPageBatch - 1);
+        ci.hk = __shfl_sync(0xffffffffu, c.hk, kPageBatch - 1);
+        ci.blk = __shfl_sync(0xffffffffu, c.blk, kPageBatch - 1);
+        ci.nblk = __shfl_sync(0xffffffffu, c.nblk, kPageBatch - 1);
+    };
+    [[maybe_unused]] auto look_up_scales = [&]() {
+        found_scales = 0;
+        if (found >= 0 && found < num_blocks) {
+            const long at = (long)found * Hkv + found_hk;
+            found_scales = __ldg(k_exp + at) | __ldg(v_exp + at) << 8;
+        }
+    };
+    [[maybe_unused]] auto keep_batch = [&](int first) {
+        int phys = found;
+        if (first + lane < n_pages && (phys < 0 || phys >= num_blocks)) {
+            raise_error(ctx, ERR_BOUNDS_BIT);
+            phys = num_blocks;  // outside the tensor map: the copy fills zeros
+        }
+        list[(first / kPageBatch & 1) * kPageBatch + lane] =
+            make_int2(phys, (int)((unsigned)found_hk << 16 | (unsigned)found_scales));
+        __syncwarp();
+    };
     // lane 0 reads the block-table entry of the next page one issue ahead, so
     // that load's latency is not on the copy's path
-    int next_phys = lane == 0 ? __ldg(bt + (long)ci.s * mbps + ci.blk0 + ci.blk) : 0;
+    int next_phys = !SCALED && lane == 0 ? __ldg(bt + (long)ci.s * mbps + ci.blk0 + ci.blk) : 0;
     auto issue = [&](int i) {
         const int stage = i % kStreamStages;
+        if constexpr (SCALED) {
+            const int2 e = list[i % (2 * kPageBatch)];
+            load_page<D, true>(ring + stage * L::kStage, &tm_k, &tm_v, &wbar[stage], (int)((unsigned)e.y >> 16), e.x);
+            return;
+        }
         int phys = next_phys;
         if (phys < 0 || phys >= num_blocks) {
             raise_error(ctx, ERR_BOUNDS_BIT);
@@ -386,6 +454,11 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         *abort_flag = 1;
     }
     int issued = 0;  // lane 0's count of copies issued
+    if constexpr (SCALED) {
+        look_up_blocks(0);
+        look_up_scales();
+        keep_batch(0);
+    }
     if (lane == 0 && ok)
         for (; issued < n_pages && issued < kStreamStages; ++issued) issue(issued);
 
@@ -398,9 +471,12 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     int ctx_len = 0, q_len = 0, nrows = 0, pos_r0 = 0, pos_r1 = 0;
     int qpos[2] = {0, 0}, lo_r[2] = {0, 0};  // MOD: position and first visible key of rows gid, gid + 8
     float slope[2] = {0.f, 0.f};             // MOD: their distance slopes (log2 units)
-    uint32_t qa[D / 16][4];
-    float o[D / 8][4];
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    PageMma<D, KV8> acc;  // the segment's queries, running max and sum, and O
+    auto& qa = acc.qa;
+    auto& o = acc.o;
+    float &m0 = acc.m[0], &m1 = acc.m[1], &l0 = acc.l[0], &l1 = acc.l[1];
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
 
     // starts segment (cc.s, cc.hk): loads its query rows as MMA A fragments
     // (rows r = token * g + head-in-group) and resets the softmax state
@@ -417,7 +493,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             qrow[i] = rr[i] < nrows ? q + ((long)(cc.q0 + rr[i] / g) * Hq + cc.hk * g + rr[i] % g) * D : nullptr;
-        if constexpr (KV8) {
+        if constexpr (SCALED) {
+            acc.load_q(qrow[0], qrow[1], scale_log2);
+        } else if constexpr (KV8) {
             // f16, channels 4t .. 4t+3 of each 16-channel step (the permuted K order)
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
@@ -479,7 +557,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
                 if (r >= nrows) continue;
                 const float inv = ls[i] > 0.f ? v_scale / ls[i] : 0.f;
                 uint16_t* dst = out + ((long)(cc.q0 + r / g) * Hq + cc.hk * g + r % g) * D;
-                if constexpr (MOD != 0)
+                if constexpr (MOD != 0 || SCALED)
                     if (mod.lse && tig == 0)
                         mod.lse[(long)(cc.q0 + r / g) * Hq + cc.hk * g + r % g] =
                             ls[i] > 0.f ? (ml[i] + __log2f(ls[i])) * kLn2f : -INFINITY;
@@ -507,6 +585,65 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
 
     int consumed = 0;
     if (ok) begin_segment();
+    if constexpr (SCALED) {
+        constexpr int NP = D == 64 ? 4 : 2;  // pages at a time
+        static_assert(NP < kStreamStages && kStreamStages + NP <= kPageBatch, "copies in flight during a pass");
+        int ready = kPageBatch;  // pages whose list entries are kept
+        int step = 0;            // of the next batch: 0 nothing, 1 blocks asked for, 2 scales asked for
+        for (int i = 0; ok && i < n_pages;) {
+            if (i > 0 && cc.blk == 0) {  // the cursor entered a new segment
+                seg_first = b0 + i;
+                begin_segment();
+            }
+            const int np = min(NP, min(n_pages - i, cc.nblk - cc.blk));
+            uint32_t kv[NP];
+            int tok[NP], ks[NP], ev[NP];
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                const int stage = (i + j) % kStreamStages;
+                kv[j] = smem_u32(ring + stage * L::kStage);
+                const unsigned e = (unsigned)list[(i + j) % (2 * kPageBatch)].y;
+                ks[j] = (int)(e & 255u);
+                ev[j] = (int)(e >> 8 & 255u);
+                tok[j] = (cc.blk + j) * kBS;
+                if (j < np && ok && !mbar_wait_warp(&wbar[stage], ((i + j) / kStreamStages) & 1, ctx.wait_ns, abort_flag)) {
+                    if (lane == 0) {
+                        raise_error(ctx, ERR_TIMEOUT_BIT);
+                        *abort_flag = 1;
+                    }
+                    ok = false;
+                }
+            }
+            if (!ok) break;
+            acc.template step<NP>(np, kv, tok, ks, ev, pos_r0, pos_r1, ctx_len);
+            __syncwarp();
+            if (i + np == n_pages || cc.blk + np == cc.nblk) end_segment();
+            cc.blk += np - 1;
+            advance(cc);
+            i += np;
+            consumed = i;
+            // The next batch: its blocks as early as can be, its scales 16 pages ahead, its list when the next
+            // copy needs it.  (The half that it takes held pages below i by then: the ring is shorter than a batch.)
+            if (ready < n_pages) {
+                const bool now = i + kStreamStages > ready;
+                if (step == 0) {
+                    look_up_blocks(ready);
+                    step = 1;
+                } else if (step == 1 && i + kStreamStages + kPageBatch / 2 > ready) {
+                    look_up_scales();
+                    step = 2;
+                }
+                if (now) {
+                    if (step == 1) look_up_scales();
+                    keep_batch(ready);
+                    ready += kPageBatch;
+                    step = 0;
+                }
+            }
+            if (lane == 0)
+                while (issued < n_pages && issued < i + kStreamStages) issue(issued++);
+        }
+    } else
     for (int i = 0; ok && i < n_pages; ++i, consumed = i) {
         if (i > 0 && cc.blk == 0) {  // the cursor entered a new segment
             seg_first = b0 + i;
@@ -773,7 +910,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         if (t.x < 0) {
             const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
             uint16_t* dst = out + ((long)(h.x + r / g) * Hq + h.y * g + r % g) * D + lane * kPer;
-            if constexpr (MOD != 0)
+            if constexpr (MOD != 0 || SCALED)
                 if (mod.lse && lane == 0)
                     mod.lse[(long)(h.x + r / g) * Hq + h.y * g + r % g] =
                         lsum > 0.f ? (M + __log2f(lsum)) * kLn2f : -INFINITY;
@@ -1409,16 +1546,20 @@ static fa_status side_stream(SideStream** out) {
     return FA_OK;
 }
 
-template <int D, bool KV8 = false, int MOD = 0>
+template <int D, int KV = KV_BF16, int MOD = 0>
 static fa_status launch_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* bt,
                                const int32_t* ctx_lens, const int32_t* q_lens, void* out, const PagedWs& w,
                                uint8_t* ws, int num_seqs, int mbps, int num_blocks, int Hq, int Hkv,
                                int max_q_len, int q_prefetch_rows, int causal, float scale, int merge_rows,
                                cudaStream_t s, const DevCtx& ctx, int* launches,
-                               float k_scale = 1.f, float v_scale = 1.f, const ScoreMod& mod = ScoreMod{}) {
+                               float k_scale = 1.f, float v_scale = 1.f, const ScoreMod& mod = ScoreMod{},
+                               const uint8_t* k_exp = nullptr, const uint8_t* v_exp = nullptr) {
     CUtensorMap tk, tv;
     fa_status st;
-    if constexpr (KV8) {
+    if constexpr (KV == KV_FP8_SCALED) {
+        st = page_maps<D, true>(k_cache, v_cache, num_blocks, Hkv, &tk, &tv);
+        if (st != FA_OK) return st;
+    } else if constexpr (KV == KV_FP8) {
         // K [blocks][Hkv][16][D] bytes, rows of D bytes, 128-byte swizzle;
         // V [blocks][Hkv][D][16] bytes, one 16-byte row per channel
         const uint64_t kd[4] = {(uint64_t)D, (uint64_t)kBS, (uint64_t)Hkv, (uint64_t)num_blocks};
@@ -1447,13 +1588,13 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
     // three stages at d = 128), else of 16
     auto launch = [&](auto rows) -> fa_status {
         constexpr int R = decltype(rows)::value;
-        using L = StreamSmem<D, KV8, R>;
-        const fa_status st2 = raise_dynamic_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, KV8, R, MOD>), L::kBytes);
+        using L = StreamSmem<D, KV, R>;
+        const fa_status st2 = raise_dynamic_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, KV, R, MOD>), L::kBytes);
         if (st2 != FA_OK) return st2;
-        paged_decode_kernel<D, KV8, R, MOD><<<grid, kStreamWarps * 32, L::kBytes, s>>>(
+        paged_decode_kernel<D, KV, R, MOD><<<grid, kStreamWarps * 32, L::kBytes, s>>>(
             tk, tv, static_cast<const uint16_t*>(q), bt, ctx_lens, q_lens, static_cast<uint16_t*>(out), part_o, part_ml,
             num_seqs, mbps, num_blocks, Hq, Hkv, q_prefetch_rows, causal, scale_log2, v_scale, ctx,
-            mod);
+            mod, k_exp, v_exp);
         return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     };
     st = merge_rows <= 6 ? launch(std::integral_constant<int, 6>{}) : launch(std::integral_constant<int, kDecodeRows>{});
@@ -1468,7 +1609,7 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, MOD != 0>, ctx_lens, q_lens, static_cast<const float*>(part_o),
+    if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, (MOD != 0 || KV == KV_FP8_SCALED)>, ctx_lens, q_lens, static_cast<const float*>(part_o),
                            static_cast<const float2*>(part_ml), static_cast<uint16_t*>(out), num_seqs, Hq, Hkv,
                            mbps, grid * kStreamWarps, max_q_len, ctx, mod) != cudaSuccess)
         return FA_ERR_CUDA;
@@ -1530,11 +1671,16 @@ static AccumWs accum_ws_layout(size_t base, int num_seqs, int mbps, int Hq, int 
     return a;
 }
 
+// The scale codes of a cache in 8 bits (such a call comes with a `mod` that modifies nothing).
+struct ScaledKv {
+    const uint8_t *k_exp, *v_exp;
+};
+
 static fa_status paged_attn_run(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                         const int32_t* ctx_lens, const int32_t* q_lens, void* out, int num_seqs,
                         int max_blocks_per_seq, int num_blocks, int Hq, int Hkv, int d, int block_size, int causal,
                         float scale, int total_q, int max_q_len, void* ws, size_t ws_bytes, fa_stream_t stream,
-                                ScoreMod* mod, const AccumArgs* acc) {
+                                ScoreMod* mod, const AccumArgs* acc, const ScaledKv* kv8 = nullptr) {
     set_launch_count(0);
     if (num_seqs < 0 || max_blocks_per_seq < 0 || num_blocks < 0 || Hq <= 0 || Hkv <= 0 || total_q < 0 ||
         max_q_len < 0 || !(scale > 0.f) || !(scale < INFINITY))
@@ -1608,19 +1754,21 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
             mod->logits = reinterpret_cast<float*>(wsb + aw.logits);
             mod->logit_rows = merge_rows;
         }
-        auto go = [&](auto dim, auto variant) {
-            return launch_decode<decltype(dim)::value, false, decltype(variant)::value>(
+        auto go = [&](auto dim, auto variant, auto cache) {
+            return launch_decode<decltype(dim)::value, decltype(cache)::value, decltype(variant)::value>(
                 q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w, wsb, num_seqs, max_blocks_per_seq,
                 num_blocks, Hq, Hkv, tc_path ? INT_MAX : max_q_len, qpf, causal, scale, merge_rows, s, ctx, &launches, 1.f, 1.f,
-                mod ? *mod : ScoreMod{});
+                mod ? *mod : ScoreMod{}, kv8 ? kv8->k_exp : nullptr, kv8 ? kv8->v_exp : nullptr);
         };
-        auto go_d = [&](auto variant) {
-            return d == 128 ? go(std::integral_constant<int, 128>{}, variant)
-                            : go(std::integral_constant<int, 64>{}, variant);
+        auto go_d = [&](auto variant, auto cache) {
+            return d == 128 ? go(std::integral_constant<int, 128>{}, variant, cache)
+                            : go(std::integral_constant<int, 64>{}, variant, cache);
         };
-        st = acc   ? go_d(std::integral_constant<int, 2>{})
-             : mod ? go_d(std::integral_constant<int, 1>{})
-                   : go_d(std::integral_constant<int, 0>{});
+        const std::integral_constant<int, KV_BF16> bf16{};
+        st = kv8   ? go_d(std::integral_constant<int, 0>{}, std::integral_constant<int, KV_FP8_SCALED>{})
+             : acc ? go_d(std::integral_constant<int, 2>{}, bf16)
+             : mod ? go_d(std::integral_constant<int, 1>{}, bf16)
+                   : go_d(std::integral_constant<int, 0>{}, bf16);
         if (st != FA_OK) {
             if (ss) (void)cudaStreamWaitEvent(s, ss->join, 0);  // keep the side stream joined
             return st;
@@ -1631,10 +1779,16 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         int32_t* q_start = reinterpret_cast<int32_t*>(wsb + w.q_start);
         int32_t* count = reinterpret_cast<int32_t*>(wsb + w.work_count);
         int32_t* list = reinterpret_cast<int32_t*>(wsb + w.work_list);
-        st = launch_paged_prefill(q, k_cache, v_cache, block_table, ctx_lens, q_lens, q_start, list, count, out,
-                                  num_seqs, max_blocks_per_seq, num_blocks, Hq, Hkv, d, causal, scale, total_q, s,
-                                  ctx, mod, mod ? reinterpret_cast<const int4*>(wsb + pw.list) : nullptr,
-                                  reinterpret_cast<float4*>(wsb + pw.o), reinterpret_cast<float2*>(wsb + pw.ml));
+        if (kv8)
+            st = launch_paged_prefill_fp8(q, k_cache, v_cache, kv8->k_exp, kv8->v_exp, block_table, ctx_lens, q_lens, q_start,
+                                          count, out, mod->lse, max_blocks_per_seq, num_blocks, Hq, Hkv, d, causal, scale,
+                                          total_q, reinterpret_cast<const int4*>(wsb + pw.list),
+                                          reinterpret_cast<float4*>(wsb + pw.o), reinterpret_cast<float2*>(wsb + pw.ml), s, ctx);
+        else
+            st = launch_paged_prefill(q, k_cache, v_cache, block_table, ctx_lens, q_lens, q_start, list, count, out,
+                                      num_seqs, max_blocks_per_seq, num_blocks, Hq, Hkv, d, causal, scale, total_q, s,
+                                      ctx, mod, mod ? reinterpret_cast<const int4*>(wsb + pw.list) : nullptr,
+                                      reinterpret_cast<float4*>(wsb + pw.o), reinterpret_cast<float2*>(wsb + pw.ml));
         if (st != FA_OK) return st;
         ++launches;
         if (pw.slots > 0) {
@@ -1784,13 +1938,37 @@ fa_status fa_paged_attn_fp8(const void* q, const void* k_cache, const void* v_ca
     DevCtx ctx;
     if ((st = make_ctx(&ctx)) != FA_OK) return st;
     int launches = 0;
-    st = launch_decode<128, true>(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w,
+    st = launch_decode<128, KV_FP8>(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w,
                                   static_cast<uint8_t*>(ws), num_seqs, max_blocks_per_seq, num_blocks, Hq, Hkv,
                                   max_q_len, total_q, causal, scale, (Hq / Hkv) * max_q_len,
                                   reinterpret_cast<cudaStream_t>(stream), ctx, &launches, k_scale, v_scale);
     if (st != FA_OK) return st;
     set_launch_count(launches);
     return FA_OK;
+}
+
+}  // extern "C"
+
+extern "C" {
+
+size_t fa_paged_attn_fp8_scaled_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv, int d, int total_q,
+                                               int max_q_len) {
+    return fa_paged_attn_mod_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len);
+}
+
+fa_status fa_paged_attn_fp8_scaled(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_exp,
+                                   const uint8_t* v_exp, const int32_t* block_table, const int32_t* ctx_lens,
+                                   const int32_t* q_lens, void* out, float* lse, int num_seqs, int max_blocks_per_seq,
+                                   int num_blocks, int Hq, int Hkv, int d, int block_size, int causal, float scale, int total_q,
+                                   int max_q_len, void* ws, size_t ws_bytes, fa_stream_t stream) {
+    set_launch_count(0);
+    if (num_seqs > 0 && total_q > 0 && max_q_len > 0 && (!k_exp || !v_exp)) return FA_ERR_INVALID_ARG;
+    if (Hkv > 0xffff) return FA_ERR_UNSUPPORTED;  // (a page's list entry has 16 bits for its head)
+    ScoreMod mod{};  // nothing modified: its path keeps the log-sum-exp and shares chunks along their keys
+    mod.lse = lse;
+    const ScaledKv kv{k_exp, v_exp};
+    return paged_attn_run(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, num_seqs, max_blocks_per_seq, num_blocks,
+                          Hq, Hkv, d, block_size, causal, scale, total_q, max_q_len, ws, ws_bytes, stream, &mod, nullptr, &kv);
 }
 
 }  // extern "C"

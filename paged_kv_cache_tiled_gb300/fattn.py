@@ -34,7 +34,9 @@ EXPORTS = [
     "fa_copy_blocks", "fa_cache_append_fp8", "fa_paged_attn_fp8", "fa_prefill_host", "fa_mask_tile_classes",
     "fa_prefill_rows", "fa_prefill_mod_workspace_size", "fa_prefill_mod", "fa_cache_append_mrope",
     "fa_paged_attn_mod_workspace_size", "fa_paged_attn_mod", "fa_paged_attn_accum_workspace_size",
-    "fa_paged_attn_accum", "fa_cache_evict_workspace_size", "fa_cache_evict",
+    "fa_paged_attn_accum", "fa_cache_evict_workspace_size", "fa_cache_evict", "fa_cache_append_fp8_scaled",
+    "fa_paged_attn_fp8_scaled_workspace_size", "fa_paged_attn_fp8_scaled", "fa_block_bounds",
+    "fa_block_select_workspace_size", "fa_block_select", "fa_paged_attn_blocks",
 ]
 NOALLOC_SCRATCH_BYTES = 32 << 20  # FA_NOALLOC_SCRATCH_BYTES
 
@@ -99,6 +101,13 @@ def _load() -> ctypes.CDLL:
                                     Z, P]),
         "fa_cache_evict_workspace_size": (Z, [I, I, I, I]),
         "fa_cache_evict": (I, [P, P, P, I, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, I, P, Z, P]),
+        "fa_cache_append_fp8_scaled": (I, [P, P, P, P, P, I, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P]),
+        "fa_paged_attn_fp8_scaled_workspace_size": (Z, [I, I, I, I, I, I, I]),
+        "fa_paged_attn_fp8_scaled": (I, [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, I, P, Z, P]),
+        "fa_block_bounds": (I, [P, P, P, P, P, P, I, I, I, I, I, I, I, P]),
+        "fa_block_select_workspace_size": (Z, [I, I, I, I, I, I]),
+        "fa_block_select": (I, [P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, I, P, Z, P]),
+        "fa_paged_attn_blocks": (I, [P, P, P, P, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, F, I, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -725,6 +734,158 @@ def fa_cache_evict(k_cache, v_cache, acc, block_table, ctx_lens, dst_table, keep
         _opt(kept, "kept", i32, (S, Hkv, keep), dev), S, mbps, dmbps, nb, Hkv, d, bs, keep, recent, sink, wp, wn,
         _current_stream(stream, dev)), "fa_cache_evict")
     return new_lens
+
+
+def _cache_shapes(k_cache, v_cache, k_exp, v_exp, dev: int):
+    """Checks a cache, bf16 or (k_exp, v_exp given) in 8 bits with block scales: (num_blocks, Hkv, block_size, d, the four
+    addresses)."""
+    nb, Hkv, bs, d = _dims(k_cache, "k_cache", 4)
+    if (k_exp is None) != (v_exp is None):
+        raise ValueError("k_exp and v_exp go together")
+    if k_exp is None:
+        ptrs = (_arg(k_cache, "k_cache", torch.bfloat16, (nb, Hkv, bs, d), dev),
+                _arg(v_cache, "v_cache", torch.bfloat16, (nb, Hkv, bs, d), dev), None, None)
+    else:
+        u8 = torch.uint8
+        ptrs = (_arg(k_cache, "k_cache", u8, (nb, Hkv, bs, d), dev), _arg(v_cache, "v_cache", u8, (nb, Hkv, d, bs), dev),
+                _arg(k_exp, "k_exp", u8, (nb, Hkv), dev), _arg(v_exp, "v_exp", u8, (nb, Hkv), dev))
+    return nb, Hkv, bs, d, ptrs
+
+
+def _batch(block_table, ctx_lens, q_lens, dev: int):
+    """Checks a batch's tables: (num_seqs, max_blocks_per_seq, the three addresses)."""
+    S, mbps = _dims(block_table, "block_table", 2)
+    i32 = torch.int32
+    return S, mbps, (_arg(block_table, "block_table", i32, (S, mbps), dev), _arg(ctx_lens, "ctx_lens", i32, (S,), dev),
+                     _arg(q_lens, "q_lens", i32, (S,), dev))
+
+
+def fa_cache_append_fp8_scaled(k, v, k_cache, v_cache, k_exp, v_exp, block_table, ctx_lens, q_lens, q=None, positions=None,
+                               cos_sin=None, q_out=None, stream=None):
+    """Writes the last q_lens[s] tokens of every sequence (k, v packed [total_q, Hkv, d], bf16 or fp32; ctx_lens count
+    them) to the 8-bit cache, k_cache uint8 [nb, Hkv, 16, d] and v_cache uint8 [nb, Hkv, d, 16], with a power-of-two scale
+    for each block and head, k_exp and v_exp uint8 [nb, Hkv].  With cos_sin (fp32 [max_pos, d]) the keys are turned by the
+    rows of `positions` (int32 [total_q]; None: the cache positions), and so are the queries q [total_q, Hq, d], which
+    are returned (bf16)."""
+    N, Hkv, d = _dims(k, "k", 3)
+    dev, dt, bf16 = _device_of(k, "k"), k.dtype, torch.bfloat16
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError("q, k, v must all be bf16 or all fp32")
+    if k_exp is None or v_exp is None:
+        raise ValueError("k_exp and v_exp are needed")
+    nb, Hkv_c, bs, d_c, cache = _cache_shapes(k_cache, v_cache, k_exp, v_exp, dev)
+    if (Hkv_c, d_c) != (Hkv, d):
+        raise ValueError(f"k_cache must have {Hkv} heads of {d} channels")
+    S, mbps, tables = _batch(block_table, ctx_lens, q_lens, dev)
+    Hq, max_pos = 0, 0
+    if cos_sin is not None:
+        max_pos = _dims(cos_sin, "cos_sin", 2)[0]
+    elif q is not None or positions is not None:
+        raise ValueError("q and positions need cos_sin")
+    if q is not None:
+        Hq = _dims(q, "q", 3)[1]
+        if q_out is None:
+            q_out = _empty((N, Hq, d), bf16, dev, stream)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _check(_lib.fa_cache_append_fp8_scaled(
+        _opt(q, "q", dt, (N, Hq, d), dev), _arg(k, "k", dt, (N, Hkv, d), dev), _arg(v, "v", dt, (N, Hkv, d), dev),
+        _opt(positions, "positions", torch.int32, (N,), dev), _opt(cos_sin, "cos_sin", torch.float32, (max_pos, d), dev),
+        max_pos, _opt(q_out, "q_out", bf16, (N, Hq, d), dev), *cache, *tables, S, mbps, nb, N, Hq, Hkv, d, bs,
+        FA_F32 if dt is torch.float32 else FA_BF16, _current_stream(stream, dev)), "fa_cache_append_fp8_scaled")
+    return q_out
+
+
+def fa_paged_attn_fp8_scaled_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len) -> int:
+    return int(_lib.fa_paged_attn_fp8_scaled_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q, max_q_len))
+
+
+def fa_paged_attn_fp8_scaled(q, k_cache, v_cache, k_exp, v_exp, block_table, ctx_lens, q_lens, causal: bool = True,
+                             scale: float | None = None, out=None, lse=None, max_q_len: int | None = None, ws=None,
+                             stream=None):
+    """fa_paged_attn over the 8-bit cache with block scales, single tokens and chunks; lse (optional, fp32 [total_q, Hq])
+    receives the log-sum-exp of every row."""
+    total_q, Hq, d = _dims(q, "q", 3)
+    dev, bf16 = _device_of(q, "q"), torch.bfloat16
+    if k_exp is None or v_exp is None:
+        raise ValueError("k_exp and v_exp are needed")
+    nb, Hkv, bs, d_c, cache = _cache_shapes(k_cache, v_cache, k_exp, v_exp, dev)
+    if d_c != d:
+        raise ValueError(f"k_cache must have heads of {d} channels")
+    S, mbps, tables = _batch(block_table, ctx_lens, q_lens, dev)
+    if out is None:
+        out = _empty(q.shape, bf16, dev, stream)
+    max_q_len = total_q if max_q_len is None else _int(max_q_len, "max_q_len")
+    need = 0 if ws is not None else fa_paged_attn_fp8_scaled_workspace_size(S, mbps, Hq, Hkv, d, total_q, max_q_len)
+    wp, wn, ws = _workspace(ws, need, dev, stream)
+    _check(_lib.fa_paged_attn_fp8_scaled(
+        _arg(q, "q", bf16, (total_q, Hq, d), dev), *cache, *tables, _arg(out, "out", bf16, (total_q, Hq, d), dev),
+        _opt(lse, "lse", torch.float32, (total_q, Hq), dev), S, mbps, nb, Hq, Hkv, d, bs, 1 if causal else 0,
+        d ** -0.5 if scale is None else float(scale), total_q, max_q_len, wp, wn, _current_stream(stream, dev)),
+        "fa_paged_attn_fp8_scaled")
+    return out
+
+
+def fa_block_bounds(k_cache, block_table, ctx_lens, q_lens, bounds, *, total_q: int, k_exp=None, stream=None):
+    """Writes the smallest and the largest value of every channel over a block's keys to bounds (bf16 [nb, Hkv, 2, d]),
+    for the blocks that the last q_lens[s] tokens of each sequence lie in; total_q is the sum of q_lens.  k_cache is bf16
+    [nb, Hkv, 16, d], or with k_exp the 8-bit cache."""
+    nb, Hkv, bs, d = _dims(k_cache, "k_cache", 4)
+    dev, bf16 = _device_of(k_cache, "k_cache"), torch.bfloat16
+    S, mbps, tables = _batch(block_table, ctx_lens, q_lens, dev)
+    _check(_lib.fa_block_bounds(
+        _arg(k_cache, "k_cache", bf16 if k_exp is None else torch.uint8, (nb, Hkv, bs, d), dev),
+        _opt(k_exp, "k_exp", torch.uint8, (nb, Hkv), dev), *tables, _arg(bounds, "bounds", bf16, (nb, Hkv, 2, d), dev), S,
+        mbps, nb, _int(total_q, "total_q"), Hkv, d, bs, _current_stream(stream, dev)), "fa_block_bounds")
+    return bounds
+
+
+def fa_block_select_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q) -> int:
+    return int(_lib.fa_block_select_workspace_size(num_seqs, max_blocks_per_seq, Hq, Hkv, d, total_q))
+
+
+def fa_block_select(q, bounds, block_table, ctx_lens, q_lens, keep: int, recent: int = 1, sink: int = 0, sel=None,
+                    max_q_len: int | None = None, ws=None, stream=None):
+    """For each query of q [total_q, Hq, d] and kv head the numbers of `keep` blocks of its sequence, ascending (-1 behind
+    the last): the first `sink`, the last `recent`, and those whose bounds (bf16 [nb, Hkv, 2, d]) allow the largest
+    scores.  Returns sel int32 [total_q, Hkv, keep]."""
+    total_q, Hq, d = _dims(q, "q", 3)
+    nb, Hkv = _dims(bounds, "bounds", 4)[:2]
+    dev, bf16 = _device_of(q, "q"), torch.bfloat16
+    S, mbps, tables = _batch(block_table, ctx_lens, q_lens, dev)
+    keep, recent, sink = _int(keep, "keep"), _int(recent, "recent"), _int(sink, "sink")
+    max_q_len = total_q if max_q_len is None else _int(max_q_len, "max_q_len")
+    if sel is None:
+        sel = _empty((total_q, Hkv, max(keep, 0)), torch.int32, dev, stream)
+    need = 0 if ws is not None else fa_block_select_workspace_size(S, mbps, Hq, Hkv, d, total_q)
+    wp, wn, ws = _workspace(ws, need, dev, stream)
+    _check(_lib.fa_block_select(
+        _arg(q, "q", bf16, (total_q, Hq, d), dev), _arg(bounds, "bounds", bf16, (nb, Hkv, 2, d), dev), *tables,
+        _arg(sel, "sel", torch.int32, (total_q, Hkv, max(keep, 0)), dev), S, mbps, nb, Hq, Hkv, d, 16, keep, recent, sink,
+        total_q, max_q_len, wp, wn, _current_stream(stream, dev)), "fa_block_select")
+    return sel
+
+
+def fa_paged_attn_blocks(q, k_cache, v_cache, block_table, ctx_lens, q_lens, sel, k_exp=None, v_exp=None,
+                         scale: float | None = None, out=None, lse=None, stream=None):
+    """Attention of each query of q [total_q, Hq, d] over the blocks of its sequence listed in sel (int32 [total_q, Hkv,
+    keep], negative entries passed over), up to its own position.  The cache is bf16, or with k_exp and v_exp the 8-bit
+    cache with block scales; lse (optional, fp32 [total_q, Hq]) receives the log-sum-exp of every row."""
+    total_q, Hq, d = _dims(q, "q", 3)
+    dev, bf16 = _device_of(q, "q"), torch.bfloat16
+    nb, Hkv, bs, d_c, cache = _cache_shapes(k_cache, v_cache, k_exp, v_exp, dev)
+    if d_c != d:
+        raise ValueError(f"k_cache must have heads of {d} channels")
+    S, mbps, tables = _batch(block_table, ctx_lens, q_lens, dev)
+    keep = _dims(sel, "sel", 3)[2]
+    if out is None:
+        out = _empty(q.shape, bf16, dev, stream)
+    _check(_lib.fa_paged_attn_blocks(
+        _arg(q, "q", bf16, (total_q, Hq, d), dev), *cache, *tables, _arg(sel, "sel", torch.int32, (total_q, Hkv, keep), dev),
+        keep, _arg(out, "out", bf16, (total_q, Hq, d), dev), _opt(lse, "lse", torch.float32, (total_q, Hq), dev), S, mbps, nb,
+        Hq, Hkv, d, bs, d ** -0.5 if scale is None else float(scale), total_q, _current_stream(stream, dev)),
+        "fa_paged_attn_blocks")
+    return out
 
 
 def fa_paged_attn_noalloc(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal: bool = True,
