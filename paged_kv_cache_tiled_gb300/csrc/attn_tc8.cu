@@ -761,14 +761,13 @@ fa_status launch_paged_prefill_fp8(const void* q, const void* k_cache, const voi
     CUtensorMap tq, tk, tv;
     fa_status st = paged_query_map(&tq, q, Hq, Hkv, d, total_q);
     if (st != FA_OK) return st;
-    // K [blocks][Hkv][16][d] and V [blocks][Hkv][d][16] bytes, a box a page, landing as they are
-    const uint64_t B = kScaledBlock, D = d, H = Hkv;
-    const uint64_t kd[4] = {D, B, H, (uint64_t)num_blocks}, ks[3] = {D, B * D, H * B * D};
-    const uint64_t vd[4] = {B, D, H, (uint64_t)num_blocks}, vs[3] = {B, B * D, H * B * D};
-    const uint32_t kb[4] = {(uint32_t)d, (uint32_t)B, 1, 1}, vb[4] = {(uint32_t)B, (uint32_t)d, 1, 1};
-    st = encode_tmap_4d(&tk, k_cache, kd, ks, kb, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE);
+    // a box a page of 16 d bytes, landing as it is, in rows of 128 bytes
+    const uint64_t page = (uint64_t)kScaledBlock * d;
+    const uint64_t dims[4] = {128, page / 128, (uint64_t)Hkv, (uint64_t)num_blocks}, strides[3] = {128, page, Hkv * page};
+    const uint32_t box[4] = {128, (uint32_t)(page / 128), 1, 1};
+    st = encode_tmap_4d(&tk, k_cache, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st == FA_OK)
-        st = encode_tmap_4d(&tv, v_cache, vd, vs, vb, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE);
+        st = encode_tmap_4d(&tv, v_cache, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != FA_OK) return st;
     T8Params p{};
     p.Hq = Hq;

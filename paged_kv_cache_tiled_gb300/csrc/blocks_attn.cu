@@ -33,12 +33,14 @@ template <int D, bool KV8>
 struct BlocksSmem {
     using M = PageMma<D, KV8>;
     static constexpr int kStage = 2 * M::kPage;
-    static constexpr int kStages = KV8 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
-    static constexpr int kPages = KV8 || D == 64 ? 4 : 2;  // pages of one pass
+    static constexpr int kStages = KV8 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 4);
+    static constexpr int kPages = KV8 ? (D == 128 ? 2 : 4) : (D == 128 ? 1 : 2);  // pages of one pass
     static constexpr int kRing = kBlWarps * kStages * kStage;
-    static constexpr int kSlots = kBlWarps * M::kSlotFloats * 4;
-    static constexpr int kBytes = 1024 + kRing + kSlots + kBlWarps * kBlBatch * 16 + (kBlWarps * kStages + 1) * 8 + 16;
+    // a warp's partial result takes its ring's place when its pages are read, four of the CTA's joined rows lie behind each
+    static constexpr int kJoined = (M::kSlotFloats * 4 + 127) / 128 * 128;
+    static constexpr int kBytes = 1024 + kRing + kBlWarps * kBlBatch * 16 + (kBlWarps * kStages + 1) * 8 + 16;
     static_assert(kStages > kPages, "copies in flight while a pass runs");
+    static_assert(kJoined + 16 / kBlWarps * D * 4 <= kStages * kStage, "a ring holds a partial result and the joined rows");
 };
 
 __device__ __forceinline__ void blocks_cluster_sync() {
@@ -64,7 +66,7 @@ __device__ __forceinline__ float2 remote_f2(const float2* p, unsigned rank) {
 }
 
 template <int D, bool KV8>
-__global__ void __launch_bounds__(kBlWarps * 32)
+__global__ void __launch_bounds__(kBlWarps * 32, 3)
     blocks_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ BlocksArgs a) {
     using L = BlocksSmem<D, KV8>;
@@ -72,8 +74,7 @@ __global__ void __launch_bounds__(kBlWarps * 32)
     constexpr int NP = L::kPages, ST = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    float* slots = reinterpret_cast<float*>(smem + L::kRing);
-    int4* lists = reinterpret_cast<int4*>(smem + L::kRing + L::kSlots);
+    int4* lists = reinterpret_cast<int4*>(smem + L::kRing);
     uint64_t* bars = reinterpret_cast<uint64_t*>(lists + kBlWarps * kBlBatch);
     uint64_t* never = bars + kBlWarps * ST;  // nothing arrives on it (time-out test hook)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
@@ -92,37 +93,39 @@ __global__ void __launch_bounds__(kBlWarps * 32)
     const int unit = blockIdx.x / C, ht = unit % a.head_tiles, list = unit / a.head_tiles;
     const int hk = list % a.Hkv, row = list / a.Hkv, g = a.Hq / a.Hkv;
     const int nrows = min(16, g - ht * 16);
-    SeqItem it;
-    const bool some = find_item(a.q_lens, a.ctx_lens, a.num_seqs, row,
-                                [&](int ql, int cl) { return lens_ok(ql, cl, a.mbps) ? ql : -1; }, it);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && (it.bad || it.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
-    __syncthreads();
-    // (the whole cluster takes the same way)
-    if (!some || it.q0 + it.off >= a.total_q) return;
-    const int at_row = it.q0 + it.off, pos = it.cl - it.ql + it.off;
+    // the first entries and the queries are on their way while the row's sequence is found
     const int gid = lane >> 2;
-    const long out_row = (long)at_row * a.Hq + hk * g + ht * 16;  // of the tile's first head
+    const long out_row = (long)row * a.Hq + hk * g + ht * 16;  // of the tile's first head
+    const int32_t* sel = a.sel + ((long)row * a.Hkv + hk) * a.keep;
+    const int W = kBlWarps * (int)C, w0 = (int)rank * kBlWarps + warp;
+    int b_next = w0 + lane * W < a.keep ? __ldg(sel + w0 + lane * W) : -1;
     M t;
     {
         const uint16_t* q = a.q + out_row * D;
         t.load_q(gid < nrows ? q + gid * D : nullptr, gid + 8 < nrows ? q + (gid + 8) * D : nullptr, a.scale_log2);
     }
     t.reset();
+    SeqItem it;
+    const bool some = find_item(a.q_lens, a.ctx_lens, a.num_seqs, row, [](int ql, int) { return max(0, ql); }, it);
+    // (the whole cluster takes the same way)
+    const bool fits = some && lens_ok(it.ql, it.cl, a.mbps);
+    if (blockIdx.x % C == 0 && threadIdx.x == 0 && (!fits || it.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+    __syncthreads();
+    if (!fits) return;
+    const int pos = it.cl - it.ql + it.off;
     uint8_t* ring = smem + warp * ST * L::kStage;
     uint64_t* wbar = bars + warp * ST;
     int4* entries = lists + warp * kBlBatch;
-    const int32_t* sel = a.sel + ((long)at_row * a.Hkv + hk) * a.keep;
-    const int W = kBlWarps * (int)C, w0 = (int)rank * kBlWarps + warp;
     bool ok = !a.ctx.force_timeout || mbar_wait_warp(never, 0, a.ctx.wait_ns, abort_flag);
     int done = 0;  // pages taken from the ring so far
     for (int base = w0; base < a.keep && ok; base += W * kBlBatch) {
         // the next 32 entries of this warp: table and scales looked up by a lane each
-        int n;
+        int n, place, ks_new = 0, ev_new = 0;
         {
-            const int i = base + lane * W;
-            const int b = i < a.keep ? __ldg(sel + i) : -1;
+            const int b = b_next, after = base + (lane + kBlBatch) * W;
+            b_next = after < a.keep ? __ldg(sel + after) : -1;
             bool use = b >= 0;
-            int phys = -1, ks = 0, ev = 0;
+            int phys = -1;
             if (use) {
                 if (b > (it.cl - 1) / kScaledBlock) {
                     raise_error(a.ctx, ERR_BOUNDS_BIT);
@@ -136,14 +139,21 @@ __global__ void __launch_bounds__(kBlWarps * 32)
                 if (phys < 0 || phys >= a.num_blocks) {
                     raise_error(a.ctx, ERR_BOUNDS_BIT);
                     use = false;
-                } else if (KV8) {
-                    ks = __ldg(a.ke + (long)phys * a.Hkv + hk);
-                    ev = __ldg(a.ve + (long)phys * a.Hkv + hk);
                 }
             }
             const unsigned live = __ballot_sync(0xffffffffu, use);
             n = __popc(live);
-            if (use) entries[__popc(live & ((1u << lane) - 1))] = make_int4(phys, b * kScaledBlock, ks, ev);
+            place = __popc(live & ((1u << lane) - 1));
+            if (use) {
+                entries[place].x = phys;
+                entries[place].y = b * kScaledBlock;
+            } else {
+                place = -1;
+            }
+            if (KV8 && use) {  // (on their way while the first pages are asked for)
+                ks_new = __ldg(a.ke + (long)phys * a.Hkv + hk);
+                ev_new = __ldg(a.ve + (long)phys * a.Hkv + hk);
+            }
             __syncwarp();
         }
         int issued = 0;
@@ -154,6 +164,11 @@ __global__ void __launch_bounds__(kBlWarps * 32)
         };
         if (lane == 0)
             while (issued < n && issued < ST) issue();
+        if (KV8 && place >= 0) {
+            entries[place].z = ks_new;
+            entries[place].w = ev_new;
+        }
+        __syncwarp();
         for (int i = 0; i < n && ok;) {
             const int np = min(NP, n - i);
             uint32_t kv[NP];
@@ -188,7 +203,7 @@ __global__ void __launch_bounds__(kBlWarps * 32)
     }
     // join the warps, then the cluster's CTAs: row by row M = max m, weights 2^(m - M)
     t.finish();
-    t.store_partial(slots + warp * M::kSlotFloats, nrows);
+    t.store_partial(reinterpret_cast<float*>(ring), nrows);
     __syncthreads();
     constexpr int kCols = D / 4;
     auto write = [&](int r, int c, float4 v, float mx, float sum) {
@@ -214,13 +229,14 @@ __global__ void __launch_bounds__(kBlWarps * 32)
             v.w = fmaf(f, x.w, v.w);
         }
     };
-    auto warp_ml = [&](int i, int r) { return reinterpret_cast<const float2*>(slots + i * M::kSlotFloats + 16 * M::kSlotRow)[r]; };
-    auto warp_o = [&](int i, int r, int c) {
-        return *reinterpret_cast<const float4*>(slots + i * M::kSlotFloats + r * M::kSlotRow + c * 4);
+    auto slot = [&](int i) { return reinterpret_cast<const float*>(smem + i * ST * L::kStage); };
+    auto warp_ml = [&](int i, int r) { return reinterpret_cast<const float2*>(slot(i) + 16 * M::kSlotRow)[r]; };
+    auto warp_o = [&](int i, int r, int c) { return *reinterpret_cast<const float4*>(slot(i) + r * M::kSlotRow + c * 4); };
+    constexpr int kRowsEach = 16 / kBlWarps;
+    auto mine = [&](int r) {
+        return reinterpret_cast<float*>(smem + r / kRowsEach * ST * L::kStage + L::kJoined) + r % kRowsEach * D;
     };
-    // (the rings are read: they take the CTA's joined rows)
-    float* mine = reinterpret_cast<float*>(smem);
-    float2* mine_ml = reinterpret_cast<float2*>(mine + 16 * D);
+    float2* mine_ml = reinterpret_cast<float2*>(lists);  // (the lists are read)
     for (int i = threadIdx.x; i < nrows * kCols; i += blockDim.x) {
         const int r = i / kCols, c = i % kCols;
         float4 v;
@@ -229,7 +245,7 @@ __global__ void __launch_bounds__(kBlWarps * 32)
         if (C == 1) {
             if (!*abort_flag) write(r, c, v, mx, sum);
         } else {
-            *reinterpret_cast<float4*>(mine + r * D + c * 4) = v;
+            *reinterpret_cast<float4*>(mine(r) + c * 4) = v;
             if (c == 0) mine_ml[r] = make_float2(mx, sum);
         }
     }
@@ -240,7 +256,7 @@ __global__ void __launch_bounds__(kBlWarps * 32)
         float4 v;
         float mx, sum;
         join(r, c, (int)C, [&](int k, int rr) { return remote_f2(mine_ml + rr, k); },
-             [&](int k, int rr, int cc) { return remote_f4(mine + rr * D + cc * 4, k); }, v, mx, sum);
+             [&](int k, int rr, int cc) { return remote_f4(mine(rr) + cc * 4, k); }, v, mx, sum);
         if (!*abort_flag) write(r, c, v, mx, sum);
     }
     blocks_cluster_sync();  // no CTA leaves while another reads its rows
@@ -255,9 +271,9 @@ static fa_status launch_blocks(const void* k_cache, const void* v_cache, const B
     auto kernel = blocks_attn_kernel<D, KV8>;
     if ((st = raise_dynamic_smem(reinterpret_cast<const void*>(kernel), L::kBytes)) != FA_OK) return st;
     const long units = (long)a.total_q * a.Hkv * a.head_tiles;
-    // CTAs per list: while they all fit the GPU at once (two a SM) and each warp still gets pages for a pass
+    // CTAs per list: while they all fit the GPU at once (three a SM) and each warp still gets pages for a pass
     int cluster = 1;
-    while (cluster < 8 && units * cluster * 2 <= 2L * sm_count() && a.keep >= kBlWarps * cluster * 2 * L::kPages) cluster *= 2;
+    while (cluster < 8 && units * cluster * 2 <= 3L * sm_count() && a.keep >= kBlWarps * cluster * 2 * L::kPages) cluster *= 2;
     if (units * cluster > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * cluster));

@@ -63,6 +63,24 @@ struct Raw {
     }
 };
 
+// Eight of them.
+template <bool kF32>
+struct Raw8 {
+    uint4 w[kF32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* base, long at) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * (kF32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < (kF32 ? 2 : 1); ++i) w[i] = __ldg(p + i);
+    }
+    __device__ __forceinline__ float get(int i) const {
+        const uint4& u = w[kF32 ? i / 4 : 0];
+        const int k = kF32 ? i % 4 : i / 2;
+        const uint32_t v = k == 0 ? u.x : (k == 1 ? u.y : (k == 2 ? u.z : u.w));
+        if constexpr (kF32) return __uint_as_float(v);
+        else return __uint_as_float(i & 1 ? v & 0xFFFF0000u : v << 16);
+    }
+};
+
 // E4M3 codes times `ratio` (a power of two), rounded again.
 __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float ratio) {
     float x[4];
@@ -197,38 +215,50 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const __grid_constan
         append_block<D, kF32>(a, it, r >> 1, r & 1);
         return;
     }
-    // a query row's heads
+    // a query token's heads: D / 16 lanes a head, 8 channel pairs each
     const long row = w - a.block_warps;
     if (row >= a.total_q || !a.q) return;
-    if (!find_item(a.q_lens, a.ctx_lens, a.num_seqs, row,
-                   [&](int ql, int cl) { return lens_ok(ql, cl, a.mbps) ? ql : -1; }, it))
-        return;
-    const long at_row = (long)it.q0 + it.off;  // (rows of sequences with inconsistent lengths have no place in the count)
-    if (at_row >= a.total_q) return;
-    const int pos = a.positions ? __ldg(a.positions + at_row) : it.cl - it.ql + it.off;
+    constexpr int kLanes = D / 16, kHeads = 32 / kLanes, kAhead = 4;
+    const int c = (lane % kLanes) * 8, h0 = lane / kLanes;
+    Raw8<kF32> x[kAhead], y[kAhead];  // the first heads' values are on their way while the token's sequence is found
+    const long base = row * a.Hq * D + c;
+    auto load = [&](int h) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (h + k * kHeads < a.Hq) {
+                x[k].load(a.q, base + (long)(h + k * kHeads) * D);
+                y[k].load(a.q, base + (long)(h + k * kHeads) * D + D / 2);
+            }
+    };
+    load(h0);
+    int pos;
+    if (!find_item(a.q_lens, a.ctx_lens, a.num_seqs, row, [](int ql, int) { return max(0, ql); }, it)) return;
+    if (!lens_ok(it.ql, it.cl, a.mbps)) return;  // (reported above)
+    pos = a.positions ? __ldg(a.positions + row) : it.cl - it.ql + it.off;
     if (pos < 0 || pos >= a.max_pos) {
         if (lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
         return;
     }
-    constexpr int kLanes = D / 8;  // lanes a row: 4 channel pairs each
-    const int c = (lane % kLanes) * 4;
-    Raw<true, 4> co, si;
+    Raw8<true> co, si;
     co.load(a.cos_sin, (long)pos * D + c);
     si.load(a.cos_sin, (long)pos * D + D / 2 + c);
-#pragma unroll 4
-    for (int h = lane / kLanes; h < a.Hq; h += 32 / kLanes) {
-        const long at = (at_row * a.Hq + h) * D + c;
-        Raw<kF32, 4> x, y;
-        x.load(a.q, at);
-        y.load(a.q, at + D / 2);
-        float u[4], v[4];
+    for (int h = h0; h < a.Hq; h += kAhead * kHeads) {
+        if (h != h0) load(h);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            u[i] = fmaf(x.get(i), co.get(i), -(y.get(i) * si.get(i)));
-            v[i] = fmaf(y.get(i), co.get(i), x.get(i) * si.get(i));
+        for (int k = 0; k < kAhead; ++k) {
+            if (h + k * kHeads >= a.Hq) break;
+            const long at = base + (long)(h + k * kHeads) * D;
+            float u[8], v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                u[i] = fmaf(x[k].get(i), co.get(i), -(y[k].get(i) * si.get(i)));
+                v[i] = fmaf(y[k].get(i), co.get(i), x[k].get(i) * si.get(i));
+            }
+            *reinterpret_cast<uint4*>(a.q_out + at) =
+                make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+            *reinterpret_cast<uint4*>(a.q_out + at + D / 2) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
         }
-        *reinterpret_cast<uint2*>(a.q_out + at) = make_uint2(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]));
-        *reinterpret_cast<uint2*>(a.q_out + at + D / 2) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
 }
 

@@ -109,14 +109,35 @@ struct PageMma {
             }
         }
     }
-    // O += P V; tokens from nvalid on count as zeros, whatever is stored there
-    __device__ __forceinline__ void add_pv(uint32_t vbase, const float (&p)[2][4], int nvalid) {
-        const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7, tig = lane & 3;
+    // Zeroes the values of tokens from nvalid on in a V page (whatever is stored there must not meet a weight of 0).
+    static __device__ __forceinline__ void clear_tail(uint32_t vbase, int nvalid) {
+        const int lane = threadIdx.x & 31;
+        if constexpr (KV8) {
+            for (int c = lane; c < D; c += 32)
+                for (int w = 0; w < 4; ++w) {
+                    const int left = nvalid - 4 * w;
+                    if (left >= 4) continue;
+                    uint32_t v;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(vbase + c * 16 + w * 4));
+                    v &= left <= 0 ? 0u : (1u << (8 * left)) - 1;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(vbase + c * 16 + w * 4), "r"(v) : "memory");
+                }
+        } else {
+            for (int i = lane; i < (kScaledBlock - nvalid) * (D / 8); i += 32) {
+                const int row = nvalid + i / (D / 8), c = i % (D / 8);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vbase + (c >> 3) * 2048 + row * 128 + (c & 7) * 16), "r"(0)
+                             : "memory");
+            }
+        }
+        fence_proxy_async_smem();  // (the next copy to this place comes through the async proxy)
+        __syncwarp();
+    }
+    // O += P V
+    __device__ __forceinline__ void add_pv(uint32_t vbase, const float (&p)[2][4]) {
+        const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7;
         if constexpr (KV8) {
             const uint32_t pa[4] = {pack_f16x2(p[0][0], p[0][1]), pack_f16x2(p[0][2], p[0][3]), pack_f16x2(p[1][0], p[1][1]),
                                     pack_f16x2(p[1][2], p[1][3])};
-            const int left = nvalid - tig * 4;
-            const uint32_t keep = left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1);
 #pragma unroll
             for (int q4 = 0; q4 < D / 32; ++q4) {
                 uint32_t w[4];
@@ -124,22 +145,20 @@ struct PageMma {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t b0, b1;
-                    e4m3x4_to_f16x4(w[i] & keep, b0, b1);
+                    e4m3x4_to_f16x4(w[i], b0, b1);
                     mma_f16_16816(o[4 * q4 + i], pa, b0, b1);
                 }
             }
         } else {
             const uint32_t pa[4] = {pack_bf16x2(p[0][0], p[0][1]), pack_bf16x2(p[0][2], p[0][3]),
                                     pack_bf16x2(p[1][0], p[1][1]), pack_bf16x2(p[1][2], p[1][3])};
-            const uint32_t zlo = (tig * 2 < nvalid ? 0x0000ffffu : 0u) | (tig * 2 + 1 < nvalid ? 0xffff0000u : 0u);
-            const uint32_t zhi = (tig * 2 + 8 < nvalid ? 0x0000ffffu : 0u) | (tig * 2 + 9 < nvalid ? 0xffff0000u : 0u);
 #pragma unroll
             for (int dn = 0; dn < D / 16; ++dn) {
                 const int tok = (mi & 1) * 8 + r8, chunk = dn * 2 + (mi >> 1);
                 uint32_t b0, b1, b2, b3;
                 ldsm_x4_t(vbase + (chunk >> 3) * 2048 + sw128_offset(tok, chunk & 7), b0, b1, b2, b3);
-                mma_bf16_16816(o[2 * dn], pa, b0 & zlo, b1 & zhi);
-                mma_bf16_16816(o[2 * dn + 1], pa, b2 & zlo, b3 & zhi);
+                mma_bf16_16816(o[2 * dn], pa, b0, b1);
+                mma_bf16_16816(o[2 * dn + 1], pa, b2, b3);
             }
         }
     }
@@ -157,21 +176,34 @@ struct PageMma {
             for (int e = 0; e < 4; ++e) x[i][0][e] = x[i][1][e] = 0.f;
             if (i < n) scores(kv[i], x[i]);
         }
+        bool all = n == NP;  // every key of every page visible to every row
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const float f0 = KV8 ? mul[0] * scale_of(ks[i]) : mul[0], f1 = KV8 ? mul[1] * scale_of(ks[i]) : mul[1];
             const float add = KV8 ? (float)(ev[i] - kExpBias) : 0.f;
-            const int a0 = i < n ? lim0 - tok[i] : -1, a1 = i < n ? lim1 - tok[i] : -1;
+            all = all && min(lim0, lim1) - tok[i] >= kScaledBlock - 1;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = token(nt, e & 1);
-                    const float w = KV8 ? fmaf(x[i][nt][e], e < 2 ? f0 : f1, add) : x[i][nt][e] * (e < 2 ? f0 : f1);
-                    x[i][nt][e] = t <= (e < 2 ? a0 : a1) ? w : -INFINITY;
-                    mx[e >> 1] = fmaxf(mx[e >> 1], x[i][nt][e]);
-                }
+                for (int e = 0; e < 4; ++e)
+                    x[i][nt][e] = KV8 ? fmaf(x[i][nt][e], e < 2 ? f0 : f1, add) : x[i][nt][e] * (e < 2 ? f0 : f1);
         }
+        if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int a0 = i < n ? lim0 - tok[i] : -1, a1 = i < n ? lim1 - tok[i] : -1;
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (token(nt, e & 1) > (e < 2 ? a0 : a1)) x[i][nt][e] = -INFINITY;
+                if (i < n && len - tok[i] < kScaledBlock) clear_tail(kv[i] + kPage, max(0, len - tok[i]));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], fmaxf(x[i][0][e], x[i][1][e]));
         float a[2], use[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -202,7 +234,7 @@ struct PageMma {
             const float back = KV8 ? scale_of(2 * kExpBias - ev[i]) : 1.f;  // 2^-ev
             l[0] = fmaf(back, (x[i][0][0] + x[i][0][1]) + (x[i][1][0] + x[i][1][1]), l[0]);
             l[1] = fmaf(back, (x[i][0][2] + x[i][0][3]) + (x[i][1][2] + x[i][1][3]), l[1]);
-            add_pv(kv[i] + kPage, x[i], len - tok[i]);
+            add_pv(kv[i] + kPage, x[i]);
         }
     }
     // The rows' sums over the four lanes that share them.
@@ -237,9 +269,10 @@ inline fa_status page_maps(const void* k_cache, const void* v_cache, int num_blo
     const uint64_t ks[3] = {D * size, B * D * size, Hkv * B * D * size};
     fa_status st;
     if constexpr (KV8) {
-        const uint32_t kb[4] = {D, (uint32_t)B, 1, 1}, vb[4] = {(uint32_t)B, D, 1, 1};
-        const uint64_t vd[4] = {B, (uint64_t)D, (uint64_t)Hkv, (uint64_t)num_blocks};
-        const uint64_t vs[3] = {B, B * D, Hkv * B * D};
+        // (a V page lands as it is: in rows of 128 bytes, since TMA takes rows of 16 bytes at a fraction of the rate)
+        const uint32_t kb[4] = {D, (uint32_t)B, 1, 1}, vb[4] = {128, D / 8, 1, 1};
+        const uint64_t vd[4] = {128, (uint64_t)D / 8, (uint64_t)Hkv, (uint64_t)num_blocks};
+        const uint64_t vs[3] = {128, B * D, Hkv * B * D};
         st = encode_tmap_4d(tk, k_cache, kd, ks, kb, CU_TENSOR_MAP_DATA_TYPE_UINT8,
                             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
         if (st == FA_OK) st = encode_tmap_4d(tv, v_cache, vd, vs, vb, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE);

@@ -144,11 +144,12 @@ struct StreamSplit {
     __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * W - 1) / P); }
 };
 
-// Warps that share a modified call's stream: at most one per page, in whole CTAs.
+// Warps that share a modified call's stream: at most one per `pages` pages, in whole CTAs.
 // (Spread over every CTA of the grid, a short context leaves one piece per page
 // to the merge kernel: 90 pages took 22 us, in twelve CTAs they take half.)
-__device__ __forceinline__ int stream_warps(int W, long long P) {
-    return (int)min((long long)W, (P + kStreamWarps - 1) / kStreamWarps * kStreamWarps);
+__device__ __forceinline__ int stream_warps(int W, long long P, int pages) {
+    const int cta = pages * kStreamWarps;
+    return (int)min((long long)W, (P + cta - 1) / cta * kStreamWarps);
 }
 
 // The cache that a decode kernel reads: bf16, E4M3 with a scale for the whole cache, or
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     const long long P = __shfl_sync(0xffffffffu, inc_p, 31);
     if (P == 0) return;
     if constexpr (MOD != 0 || SCALED) {
-        W = stream_warps(W, P);
+        W = stream_warps(W, P, SCALED ? 2 : 1);
         if (gw >= W) return;  // a whole CTA
     }
     const StreamSplit split(P, W);
@@ -407,14 +408,17 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
             found_scales = __ldg(k_exp + at) | __ldg(v_exp + at) << 8;
         }
     };
-    [[maybe_unused]] auto keep_batch = [&](int first) {
+    [[maybe_unused]] auto keep_blocks = [&](int first) {
         int phys = found;
         if (first + lane < n_pages && (phys < 0 || phys >= num_blocks)) {
             raise_error(ctx, ERR_BOUNDS_BIT);
             phys = num_blocks;  // outside the tensor map: the copy fills zeros
         }
-        list[(first / kPageBatch & 1) * kPageBatch + lane] =
-            make_int2(phys, (int)((unsigned)found_hk << 16 | (unsigned)found_scales));
+        list[(first / kPageBatch & 1) * kPageBatch + lane] = make_int2(phys, (int)((unsigned)found_hk << 16));
+        __syncwarp();
+    };
+    [[maybe_unused]] auto keep_scales = [&](int first) {
+        list[(first / kPageBatch & 1) * kPageBatch + lane].y = (int)((unsigned)found_hk << 16 | (unsigned)found_scales);
         __syncwarp();
     };
     // lane 0 reads the block-table entry of the next page one issue ahead, so
@@ -456,11 +460,15 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     int issued = 0;  // lane 0's count of copies issued
     if constexpr (SCALED) {
         look_up_blocks(0);
-        look_up_scales();
-        keep_batch(0);
+        keep_blocks(0);
+        look_up_scales();  // (on their way while the first pages are asked for)
     }
     if (lane == 0 && ok)
         for (; issued < n_pages && issued < kStreamStages; ++issued) issue(issued);
+    if constexpr (SCALED) {
+        __syncwarp();
+        keep_scales(0);
+    }
 
     const int gid = lane >> 2, tig = lane & 3, mi = lane >> 3, r8 = lane & 7;
     Cursor cc = start;            // compute cursor (all lanes)
@@ -635,7 +643,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
                 }
                 if (now) {
                     if (step == 1) look_up_scales();
-                    keep_batch(ready);
+                    keep_blocks(ready);
+                    keep_scales(ready);
                     ready += kPageBatch;
                     step = 0;
                 }
@@ -945,7 +954,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
 // it is an error, reported here (in the decode kernel the comparison cost 0.1 to
 // 0.4 us).
 constexpr int kMergeMaxThreads = 32 * kDecodeRows;
-template <int D, bool MOD>
+// PAGES: as in the decode kernel's stream_warps (0: every warp of the grid).
+template <int D, bool MOD, int PAGES = MOD ? 1 : 0>
 __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const int32_t* __restrict__ ctx_lens,
                                                                     const int32_t* __restrict__ q_lens,
                                                                     const float* part_o, const float2* part_ml,
@@ -988,7 +998,7 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
     }
     const long long P = (long long)Hkv * tot;
     const long long seg_first = (long long)Hkv * pre + (long long)hk * nblk;
-    if constexpr (MOD) W = stream_warps(W, P);
+    if constexpr (PAGES > 0) W = stream_warps(W, P, PAGES);
     const StreamSplit split(P, W);  // W: the decode grid's warps
     const int c_lo = split.owner(seg_first) / kStreamWarps, c_hi = split.owner(seg_first + nblk - 1) / kStreamWarps;
     const int npieces = c_hi - c_lo + 1;
@@ -1609,9 +1619,11 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, (MOD != 0 || KV == KV_FP8_SCALED)>, ctx_lens, q_lens, static_cast<const float*>(part_o),
-                           static_cast<const float2*>(part_ml), static_cast<uint16_t*>(out), num_seqs, Hq, Hkv,
-                           mbps, grid * kStreamWarps, max_q_len, ctx, mod) != cudaSuccess)
+    constexpr bool kScaled = KV == KV_FP8_SCALED;
+    if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, (MOD != 0 || kScaled), kScaled ? 2 : (MOD != 0 ? 1 : 0)>, ctx_lens, q_lens,
+                           static_cast<const float*>(part_o), static_cast<const float2*>(part_ml),
+                           static_cast<uint16_t*>(out), num_seqs, Hq, Hkv, mbps, grid * kStreamWarps, max_q_len, ctx, mod) !=
+        cudaSuccess)
         return FA_ERR_CUDA;
     ++*launches;
     return FA_OK;
