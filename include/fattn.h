@@ -575,7 +575,7 @@ fa_status fa_block_bounds(const void* k_cache, const uint8_t* k_exp, const int32
  *            the work's division goes by it
  *   ws       at least fa_block_select_workspace_size(...) bytes, 256-byte aligned
  *            (the scores, 4 bytes for each query, kv head and table entry, and 12
- *            bytes a table entry for each of 640 CTAs)
+ *            bytes a table entry for each of 1280 CTAs)
  * The choice is that of exact arithmetic: blocks whose scores are too close to tell
  * apart in fp32 are summed again in 64 bits.  Calls that may overlap on the GPU need
  * workspaces of their own.  Sequences with inconsistent lengths record

@@ -8,27 +8,36 @@
 // m16n8k16 warp MMAs (rows: the queries' heads, columns: 8 blocks).  A block counts as
 // much as it does for the head of the group that wants it most.
 //
-// block_score_kernel reads each block's bounds once for all rows of a tile (4 d bytes,
-// straight to registers: the MMA's K dimension is taken in an order in which a lane's B
-// operands are 16 consecutive bytes).  Memory bound for single tokens.
-// block_top_kernel finds the score of the last block taken with a radix select over
-// order-preserving integer keys.  An MMA's sum is off by its roundings, which must not
-// decide: blocks whose score lies within the rounding bound of that border are summed
-// again in 64 bits and ordered by that, equal ones by their number, so that the
-// choice is that of exact arithmetic.  Few blocks are that close (a handful of
-// thousands), unless many are equal.
+// block_score_kernel lays the steps of 32 blocks of all (sequence, kv head, set of query
+// tiles) end to end and gives each CTA of one wave an equal run of them, so that contexts
+// of any mix of lengths fill the GPU.  A producer warp looks a step's blocks up, a lane
+// each, and copies their bounds (4 d bytes a block) into a ring in shared memory; four
+// warps take eight of its blocks each for one tile, or, when a sequence has four tiles or
+// more, all of them for a tile each, so that they are read once for four tiles.  The MMA's
+// K dimension is taken in an order in which a lane's B operands are 16 consecutive
+// bytes of a block's row.  Memory bound for single tokens.
+//
+// block_top_kernel, a CTA a row, finds the border with a histogram over the scores' own
+// range (again within the bin that holds the border, if that is full).  An MMA's sum is off
+// by its roundings, which must not decide: blocks whose score lies within the
+// rounding bound of the border are summed again in twice fp32's digits and ordered by
+// that, equal ones by their number, so that the choice is that of exact
+// arithmetic.  Few blocks are that close (a handful of thousands), unless many are equal.
 #include <algorithm>
+#include <type_traits>
 
 #include "cache_scaled.cuh"
 
 namespace fa {
 
-constexpr int kScWarps = 8;
-constexpr int kTopThreads = 256;
-constexpr int kTopItems = 16;    // scores per thread that stay in registers
-constexpr int kTopBins = 2048;
-constexpr int kTopCount = 256;   // blocks near the border that are ranked by counting
-constexpr int kTopCtasPerSm = 4;  // grid of the top kernel, and its scratch
+constexpr int kScWarps = 4, kScCtasPerSm = 3;  // warps beside the producer
+constexpr int kScBlocks = 32, kScStages = 4;   // blocks of a step, steps of the ring
+
+constexpr int kTopItems = 16;     // scores per thread that stay in registers
+constexpr int kTopBins = 1024;
+constexpr int kTopNear = 256;     // blocks near the border that are ranked in shared memory, by counting
+constexpr int kTopCtas = 8 * 160;   // grid of the top kernel at most, and its scratch
+constexpr int kTopFew = 512, kTopMany = 128;  // threads of a row's CTA when there are few rows (latency), and many
 
 struct SelectArgs {
     const uint16_t *q, *bounds;
@@ -39,6 +48,7 @@ struct SelectArgs {
     unsigned long long* near_key;  // and their keys
     int32_t* sel;
     int num_seqs, mbps, num_blocks, total_q, Hq, Hkv, keep, recent, sink;
+    int g2_log, per;  // rows that a token's heads take in a tile (log2), tokens a tile
     DevCtx ctx;
 };
 
@@ -53,138 +63,287 @@ __device__ __forceinline__ uint32_t max0_bf16x2(uint32_t x) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// CTA (sequence and kv head; share of its blocks; share of its tokens).  A warp takes
-// groups of 8 blocks and tiles of 16 / g tokens (one token and its heads in turns of 16
-// when g > 16); with many tokens the warps of a CTA take different tokens of the
-// same blocks, whose bounds they then find in L1.
 template <int D>
-__global__ void __launch_bounds__(kScWarps * 32, 2) block_score_kernel(const __grid_constant__ SelectArgs a) {
+struct ScoreSmem {
+    static constexpr int kRow = 4 * D + 64;  // bytes between blocks: two neighbours' 64 bytes lie in different banks
+    static constexpr int kStage = kScBlocks * kRow;
+    static constexpr int kBytes = kScStages * kStage + (2 * kScStages + 1) * 8 + 16;
+};
+
+// A tile's rows: `per` tokens, each with its g heads in 2^g2_log rows (the least such number, at
+// most 16; the rows behind the g-th repeat the first head, which changes no maximum); with
+// g > 16 one token, whose heads come 16 at a time.
+//
+// A place in the run: sequence, kv head, set of tiles, step.  A sequence of four tiles or
+// more has sets of four, each warp a tile; otherwise a set is a tile.
+struct ScorePlace {
+    SeqItem it;
+    int tiles, sets, steps;
+    int hk, set, step;
+};
+__device__ __forceinline__ int score_tiles(const SelectArgs& a, int ql) { return (ql + a.per - 1) >> (4 - a.g2_log); }
+__device__ __forceinline__ int score_sets(int tiles) { return tiles >= kScWarps ? (tiles + kScWarps - 1) / kScWarps : tiles; }
+__device__ __forceinline__ int score_steps(int cl) { return ((cl - 1) / kScaledBlock + kScBlocks) / kScBlocks; }
+__device__ __forceinline__ long long score_items(const SelectArgs& a, int ql, int cl) {
+    if (!lens_ok(ql, cl, a.mbps) || ql == 0 || (cl - 1) / kScaledBlock + 1 <= a.keep) return 0;
+    return (long long)a.Hkv * score_sets(score_tiles(a, ql)) * score_steps(cl);
+}
+__device__ __forceinline__ void score_enter(const SelectArgs& a, ScorePlace& p) {
+    p.tiles = score_tiles(a, p.it.ql);
+    p.sets = score_sets(p.tiles);
+    p.steps = score_steps(p.it.cl);
+}
+// (only called while there are items left)
+__device__ __forceinline__ void score_advance(const SelectArgs& a, ScorePlace& p) {
+    if (++p.step < p.steps) return;
+    p.step = 0;
+    if (++p.set < p.sets) return;
+    p.set = 0;
+    if (++p.hk < a.Hkv) return;
+    p.hk = 0;
+    long long q0 = p.it.q0;
+    do {
+        q0 += max(0, p.it.ql);
+        ++p.it.s;
+        p.it.ql = __ldg(a.q_lens + p.it.s);
+        p.it.cl = __ldg(a.ctx_lens + p.it.s);
+    } while (score_items(a, p.it.ql, p.it.cl) == 0);
+    p.it.q0 = (int)min(q0, 0x7fffffffll);
+    score_enter(a, p);
+}
+
+// BIG: groups of more than 16 heads.
+template <int D, bool BIG>
+__global__ void __launch_bounds__((kScWarps + 1) * 32, kScCtasPerSm) block_score_kernel(const __grid_constant__ SelectArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    using L = ScoreSmem<D>;
     constexpr int CH = D / 32;  // 16-byte chunks of a bound row per lane
-    __shared__ float tile[kScWarps][16][8 + 1];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    const int s = blockIdx.x / a.Hkv, hk = blockIdx.x % a.Hkv, g = a.Hq / a.Hkv;
-    const int ql = __ldg(a.q_lens + s), cl = __ldg(a.ctx_lens + s);
-    if (!lens_ok(ql, cl, a.mbps) || ql == 0 || (cl - 1) / kScaledBlock + 1 <= a.keep) return;
-    long long q0 = 0;
-    for (int i = lane; i < s; i += 32) q0 += max(0, __ldg(a.q_lens + i));
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kScStages * L::kStage);
+    uint64_t* empty = full + kScStages;
+    uint64_t* never = empty + kScStages;  // nothing arrives on it (time-out test hook)
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = a.Hq / a.Hkv;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kScStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kScWarps);
+        }
+        mbar_init(never, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    // this CTA's run of items, and where its first one is
+    ScorePlace p;
+    long long n_items;
+    {
+        auto count = [&](int ql, int cl) { return score_items(a, ql, cl); };
+        const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+        const long long W = gridDim.x, w = blockIdx.x;
+        const long long each = scan.items < 1ll << 31 ? (int)scan.items / (int)gridDim.x : scan.items / W, more = scan.items - each * W;
+        n_items = each + (w < more ? 1 : 0);
+        if (n_items > 0) {  // (else there is no such item)
+            scan.find(a.q_lens, a.ctx_lens, w * each + min(w, more), count, p.it);
+            score_enter(a, p);
+            const long long of_set = p.it.off < 1ll << 31 ? (int)p.it.off / p.steps : p.it.off / p.steps;
+            p.step = (int)(p.it.off - of_set * p.steps);
+            p.hk = (int)(of_set < 1ll << 31 ? (int)of_set / p.sets : of_set / p.sets);
+            p.set = (int)(of_set - (long long)p.hk * p.sets);
+        }
+    }
+    __syncthreads();
+    if (n_items <= 0) return;
+    bool ok = !a.ctx.force_timeout || mbar_wait_warp(never, 0, a.ctx.wait_ns, abort_flag);
+    if (warp == kScWarps) {
+        // producer: lane j copies the bounds of the step's j-th block
+        auto block_of = [&](const ScorePlace& x) {
+            const int b = x.step * kScBlocks + lane;
+            return b <= (x.it.cl - 1) / kScaledBlock ? __ldg(a.bt + (long)x.it.s * a.mbps + b) : -2;  // (-2: behind the last)
+        };
+        long long i = 0;
+        int phys = block_of(p), hk = p.hk;
+        for (; i < n_items && ok; ++i) {
+            const int cur = phys, cur_hk = hk;
+            if (i + 1 < n_items) {
+                score_advance(a, p);
+                phys = block_of(p);
+                hk = p.hk;
+            }
+            const int st = (int)(i % kScStages);
+            if (!mbar_wait_warp(&empty[st], (((int)(i / kScStages)) & 1) ^ 1, a.ctx.wait_ns, abort_flag)) {
+                ok = false;
+                break;
+            }
+            uint8_t* row = smem + st * L::kStage + lane * L::kRow;
+            const bool in = cur >= 0 && cur < a.num_blocks;
+            const int rows = __popc(__ballot_sync(0xffffffffu, in));
+            if (!in && cur != -2) {  // counts as a block of bounds 0
+                raise_error(a.ctx, ERR_BOUNDS_BIT);
+                for (int c = 0; c < 4 * D; c += 16) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], rows * 4 * D);
+            __syncwarp();
+            if (in)
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                 smem_u32(row)),
+                             "l"(a.bounds + ((long)cur * a.Hkv + cur_hk) * 2 * D), "r"(4 * D), "r"(smem_u32(&full[st]))
+                             : "memory");
+        }
+        if (!ok) {
+            if (lane == 0) {
+                raise_error(a.ctx, ERR_TIMEOUT_BIT);
+                *abort_flag = 1;
+            }
+            // let every copy already issued land before the CTA can exit
+            for (long long f = max(0ll, i - kScStages); f < i; ++f)
+                (void)mbar_wait_warp(&full[f % kScStages], (int)(f / kScStages) & 1, 1000000000ull, nullptr);
+        }
+        return;
+    }
+    const int gid = lane >> 2, tig = lane & 3;
+    const int rows_log = a.g2_log, row_mask = (1 << rows_log) - 1;
+    uint32_t lo[2 * CH][4], hi[2 * CH][4];  // q- and q+: [chunk][half of it] channels 32 i + 8 tig + 4 j + {0, 1}, {2, 3}
+    int ti = 0, t0 = 0, nt = 0, blocks = 0;  // the warp's tile, its first token, its tokens, the blocks that its last token sees
+    float *dst[2] = {nullptr, nullptr}, *most = nullptr;
+    auto load_q = [&](int h0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) q0 += __shfl_xor_sync(0xffffffffu, q0, o);
-    if (q0 + ql > a.total_q) return;
-    const int per = g <= 16 ? 16 / g : 1, tiles = (ql + per - 1) / per;  // tokens a tile, tiles
-    int side = 1;  // warps side by side along the tokens
-    while (side < kScWarps && side < tiles) side *= 2;
-    const int my_tile = blockIdx.z * side + warp % side, my_group = blockIdx.y * (kScWarps / side) + warp / side;
-    const int tile_step = gridDim.z * side, group_step = gridDim.y * (kScWarps / side);
-    for (int ti = my_tile; ti < tiles; ti += tile_step) {
-        const int t0 = ti * per, nt = min(per, ql - t0);
-        const int blocks = (cl - ql + t0 + nt - 1) / kScaledBlock + 1;  // that the tile's last token sees
-        if (blocks <= a.keep) continue;
-        const int groups = (blocks + 7) / 8;
-        for (int h0 = 0; h0 < g; h0 += 16) {
-            // A rows: token t0 + r / g, head r % g of the group (g > 16: head h0 + r of one token)
-            const int nr = g <= 16 ? nt * g : min(16, g - h0);
-            uint32_t qa[2 * CH][4];  // [chunk][half of it]: channels 32 i + 8 tig + 4 j + {0, 1}, {2, 3} of rows gid, gid + 8
+        for (int r = 0; r < 2; ++r) {
+            const int rr = gid + 8 * r, h = h0 + (rr & row_mask), tok = rr >> rows_log;
+            const uint16_t* src = a.q + (((long)p.it.q0 + t0 + tok) * a.Hq + p.hk * g + (h < g ? h : 0)) * D + 8 * tig;
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
+            for (int i = 0; i < CH; ++i) {
+                const uint4 w = tok < nt ? __ldg(reinterpret_cast<const uint4*>(src + 32 * i)) : make_uint4(0, 0, 0, 0);
+                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int rr = gid + 8 * r;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (rr < nr) {
-                        const int tok = g <= 16 ? t0 + rr / g : t0, head = g <= 16 ? rr % g : h0 + rr;
-                        w = __ldg(reinterpret_cast<const uint4*>(a.q + ((q0 + tok) * a.Hq + hk * g + head) * D + 32 * i + 8 * tig));
-                    }
-                    qa[2 * i][r] = w.x;
-                    qa[2 * i][r + 2] = w.y;
-                    qa[2 * i + 1][r] = w.z;
-                    qa[2 * i + 1][r + 2] = w.w;
+                for (int k = 0; k < 4; ++k) {
+                    lo[2 * i + k / 2][r + 2 * (k & 1)] = min0_bf16x2(v[k]);
+                    hi[2 * i + k / 2][r + 2 * (k & 1)] = max0_bf16x2(v[k]);
                 }
-            auto block_of = [&](int grp) {
-                const int b = grp * 8 + gid;
-                int phys = grp < groups && b < blocks ? __ldg(a.bt + (long)s * a.mbps + b) : -1;
-                if (phys >= a.num_blocks) phys = -1;
-                return phys;
-            };
-            uint4 w[2 * CH], next[2 * CH];  // lo's chunks, then hi's
-            auto load = [&](int phys, uint4 (&x)[2 * CH]) {
-                const uint4* src = reinterpret_cast<const uint4*>(a.bounds + ((long)phys * a.Hkv + hk) * 2 * D) + tig;
+            }
+        }
+    };
+    for (long long i = 0; i < n_items && ok; ++i) {
+        const bool many = p.tiles >= kScWarps;
+        if (i == 0 || p.step == 0) {  // another set
+            ti = many ? p.set * kScWarps + warp : p.set;
+            t0 = ti * a.per;
+            nt = min(a.per, p.it.ql - t0);
+            blocks = (p.it.cl - p.it.ql + t0 + nt - 1) / kScaledBlock + 1;
+            if (ti >= p.tiles || blocks <= a.keep || (long long)p.it.q0 + p.it.ql > a.total_q) blocks = 0;  // nothing to do
+            if (blocks > 0) {
 #pragma unroll
-                for (int i = 0; i < 2 * CH; ++i) x[i] = phys >= 0 ? __ldg(src + 4 * i) : make_uint4(0, 0, 0, 0);
-            };
-            int phys = block_of(my_group), phys_next = block_of(my_group + group_step);
-            load(phys, w);
-            for (int grp = my_group; grp < groups; grp += group_step) {
-                load(phys_next, next);
-                const int phys_after = block_of(grp + 2 * group_step);
-                if (phys < 0 && grp * 8 + gid < blocks) raise_error(a.ctx, ERR_BOUNDS_BIT);
-                float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t top = 0;
+                for (int r = 0; r < 2; ++r) {  // scores of rows gid, gid + 8 (null: not a token's first row)
+                    const int rr = gid + 8 * r, tok = rr >> rows_log;
+                    dst[r] = (rr & row_mask) == 0 && tok < nt
+                                 ? a.scores + (((long)p.it.q0 + t0 + tok) * a.Hkv + p.hk) * a.mbps + 2 * tig : nullptr;
+                }
+                // the tile that sees every block writes their largest |bound|
+                most = ti == p.tiles - 1 ? a.largest + ((long)p.it.s * a.Hkv + p.hk) * a.mbps + gid : nullptr;
+                load_q(0);
+            }
+        }
+        const int st = (int)(i % kScStages);
+        if (!mbar_wait_warp(&full[st], ((int)(i / kScStages)) & 1, a.ctx.wait_ns, abort_flag)) {
+            ok = false;
+            break;
+        }
+        const int b0 = p.step * kScBlocks;
+        // NG groups of 8 blocks from bg on at once, so that their chains of MMAs overlap
+        auto groups = [&](auto ng, int bg) {
+            constexpr int NG = decltype(ng)::value;
+            const uint8_t* row = smem + st * L::kStage + (bg - b0 + gid) * L::kRow + tig * 16;
+            float m[NG][4];  // rows gid, gid + 8; blocks 2 tig, 2 tig + 1
 #pragma unroll
-                for (int i = 0; i < CH; ++i)
+            for (int u = 0; u < NG; ++u) m[u][0] = m[u][1] = m[u][2] = m[u][3] = -INFINITY;
+            for (int h0 = 0; h0 < (BIG ? g : 1); h0 += 16) {
+                if (BIG) load_q(h0);
+                float c[NG][2][4];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t lo[4], hi[4];
+                for (int u = 0; u < NG; ++u)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            lo[r] = min0_bf16x2(qa[2 * i + j][r]);
-                            hi[r] = max0_bf16x2(qa[2 * i + j][r]);
-                        }
-                        const uint4 &bl = w[i], &bh = w[CH + i];
-                        mma_bf16_16816(c, lo, j ? bl.z : bl.x, j ? bl.w : bl.y);
-                        mma_bf16_16816(c2, hi, j ? bh.z : bh.x, j ? bh.w : bh.y);
+                    for (int k = 0; k < 2; ++k) c[u][k][0] = c[u][k][1] = c[u][k][2] = c[u][k][3] = 0.f;
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+                    for (int u = 0; u < NG; ++u) {
+                        const uint4 bl = *reinterpret_cast<const uint4*>(row + u * 8 * L::kRow + ch * 64);
+                        const uint4 bh = *reinterpret_cast<const uint4*>(row + u * 8 * L::kRow + 2 * D + ch * 64);
+                        mma_bf16_16816(c[u][0], lo[2 * ch], bl.x, bl.y);
+                        mma_bf16_16816(c[u][1], hi[2 * ch], bh.x, bh.y);
+                        mma_bf16_16816(c[u][0], lo[2 * ch + 1], bl.z, bl.w);
+                        mma_bf16_16816(c[u][1], hi[2 * ch + 1], bh.z, bh.w);
                     }
-                const bool last = ti == tiles - 1 && h0 == 0;  // the tile that sees every block
-                if (last) {  // the block's largest |bound|
 #pragma unroll
-                    for (int i = 0; i < 2 * CH; ++i) {
-                        const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                for (int u = 0; u < NG; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[u][e] = fmaxf(m[u][e], c[u][0][e] + c[u][1][e]);
+            }
+            // the maximum over a token's rows
+            if (rows_log == 4) {
+#pragma unroll
+                for (int u = 0; u < NG; ++u) {
+                    m[u][0] = fmaxf(m[u][0], m[u][2]);
+                    m[u][1] = fmaxf(m[u][1], m[u][3]);
+                }
+            }
+#pragma unroll
+            for (int o = 0; o < 3; ++o)
+                if (o < rows_log) {
+#pragma unroll
+                    for (int u = 0; u < NG; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m[u][e] = fmaxf(m[u][e], __shfl_xor_sync(0xffffffffu, m[u][e], 4 << o));
+                }
+            const int last = blocks - 2 * tig;  // this lane's columns from `last` on do not exist
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (dst[r]) {
+#pragma unroll
+                    for (int u = 0; u < NG; ++u) {
+                        if (bg + 8 * u < last) dst[r][bg + 8 * u] = m[u][2 * r];
+                        if (bg + 8 * u + 1 < last) dst[r][bg + 8 * u + 1] = m[u][2 * r + 1];
+                    }
+                }
+            if (most) {
+#pragma unroll 1
+                for (int u = 0; u < NG; ++u) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i2 = 0; i2 < 2 * CH; ++i2) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(row + u * 8 * L::kRow + i2 * 64);
+                        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
                     }
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    if (tig == 0 && bg + 8 * u + gid < blocks) most[bg + 8 * u] = __uint_as_float(top << 16);
                 }
-                __syncwarp();  // the tile's values of the group before are read
-                tile[warp][gid][2 * tig] = c[0] + c2[0];
-                tile[warp][gid][2 * tig + 1] = c[1] + c2[1];
-                tile[warp][gid + 8][2 * tig] = c[2] + c2[2];
-                tile[warp][gid + 8][2 * tig + 1] = c[3] + c2[3];
-                __syncwarp();
-                for (int x = lane; x < nt * 8; x += 32) {
-                    const int tok = x >> 3, b = grp * 8 + (x & 7);
-                    const int r0 = g <= 16 ? tok * g : 0, r1 = g <= 16 ? r0 + g : nr;
-                    float m = -INFINITY;
-                    for (int r = r0; r < r1; ++r) m = fmaxf(m, tile[warp][r][x & 7]);
-                    if (b >= blocks) continue;
-                    float* dst = a.scores + ((q0 + t0 + tok) * a.Hkv + hk) * a.mbps + b;
-                    *dst = h0 > 0 ? fmaxf(m, *dst) : m;
-                }
-                if (last && tig == 0 && grp * 8 + gid < blocks)
-                    a.largest[((long)s * a.Hkv + hk) * a.mbps + grp * 8 + gid] = __uint_as_float(top << 16);
-#pragma unroll
-                for (int i = 0; i < 2 * CH; ++i) w[i] = next[i];
-                phys = phys_next;
-                phys_next = phys_after;
             }
+        };
+        if (many) {
+#pragma unroll 1
+            for (int bg = b0; bg < min(blocks, b0 + kScBlocks); bg += 16) groups(std::integral_constant<int, 2>{}, bg);
+        } else if (b0 + 8 * warp < blocks) {
+            groups(std::integral_constant<int, 1>{}, b0 + 8 * warp);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+        if (i + 1 < n_items) score_advance(a, p);
+    }
+    if (!ok && lane == 0) {
+        raise_error(a.ctx, ERR_TIMEOUT_BIT);
+        *abort_flag = 1;
     }
 }
 
-// Larger score, larger key; NaN below everything, -0 as 0.
-__device__ __forceinline__ uint32_t score_key(float x) {
-    if (!(x == x)) return 0u;
-    const uint32_t b = __float_as_uint(x + 0.f);
+__device__ __forceinline__ uint32_t float_key(float x) {  // order-preserving, of a number
+    const uint32_t b = __float_as_uint(x);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-__device__ __forceinline__ float key_score(uint32_t k) {
-    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
-}
-__device__ __forceinline__ unsigned long long score_key64(double x) {
-    if (!(x == x)) return 0ull;
-    const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);
-    return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
-}
+__device__ __forceinline__ float key_float(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k); }
 
 // An MMA sum differs from the exact one by at most this times sum |products|: 2 (d / 16)
 // steps and the final addition; in a step 16 exact products and the accumulator are
@@ -192,72 +351,84 @@ __device__ __forceinline__ unsigned long long score_key64(double x) {
 // of the magnitudes that meet in it.
 __device__ __forceinline__ float sum_slack(int d) { return (float)(d / 8 + 1) * 3.814697265625e-6f; }
 
+// A number in two fp32 parts, sums of such (Knuth's error-free addition of the first parts), and their order as
+// integers: larger number, larger key; NaN below everything.
+struct TwoFloat {
+    float hi, lo;
+    __device__ __forceinline__ void add(float bh, float bl) {
+        const float s = __fadd_rn(hi, bh), t = __fsub_rn(s, hi);
+        const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(bh, t));
+        hi = s;
+        lo = __fadd_rn(lo, __fadd_rn(bl, e));
+    }
+    __device__ __forceinline__ unsigned long long key() const {
+        const float h = __fadd_rn(hi, lo), l = __fsub_rn(lo, __fsub_rn(h, hi));  // (h is the nearest to the number)
+        if (!(h == h)) return 0ull;
+        return (unsigned long long)float_key(h + 0.f) << 32 | float_key(l == l ? l + 0.f : 0.f);
+    }
+};
+
+// The exact score of block `phys` for a token's heads (q: the first head's channels): a warp.
 template <int D>
-__global__ void __launch_bounds__(kTopThreads, kTopCtasPerSm) block_top_kernel(const __grid_constant__ SelectArgs a) {
+__device__ __forceinline__ unsigned long long exact_key(const uint16_t* __restrict__ q, int g, const uint16_t* __restrict__ box) {
+    constexpr int N = D / 32;  // channels per lane
+    const int lane = threadIdx.x & 31;
+    uint32_t l[N / 2], h[N / 2];
+    auto load = [&](const uint16_t* p, uint32_t (&x)[N / 2]) {
+        if constexpr (N == 4) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + lane * 4));
+            x[0] = u.x;
+            x[1] = u.y;
+        } else {
+            x[0] = __ldg(reinterpret_cast<const uint32_t*>(p + lane * 2));
+        }
+    };
+    auto get = [](const uint32_t (&x)[N / 2], int c) { return __uint_as_float(c & 1 ? x[c / 2] & 0xFFFF0000u : x[c / 2] << 16); };
+    load(box, l);
+    load(box + D, h);
+    unsigned long long best = 0;
+    for (int h0 = 0; h0 < g; h0 += 4) {  // four heads' sums side by side
+        TwoFloat s[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t x[N / 2];
+            load(q + (long)min(h0 + k, g - 1) * D, x);
+            s[k] = TwoFloat{0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < N; ++c) {  // (a product of two bf16 numbers is exact in fp32)
+                const float v = get(x, c);
+                s[k].add(__fmul_rn(v, v < 0.f ? get(l, c) : get(h, c)), 0.f);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float bh = __shfl_xor_sync(0xffffffffu, s[k].hi, o), bl = __shfl_xor_sync(0xffffffffu, s[k].lo, o);
+                s[k].add(bh, bl);
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) best = max(best, s[k].key());
+    }
+    return best;
+}
+
+template <int D, int kTopThreads>
+__global__ void __launch_bounds__(kTopThreads, 1024 / kTopThreads) block_top_kernel(const __grid_constant__ SelectArgs a) {
     extern __shared__ uint32_t taken[];  // a bit for each block
     __shared__ __align__(16) int hist[kTopBins];
-    __shared__ int warp_sums[kTopThreads / 32], digit_sel, above_sel, near_n, sure_n;
-    __shared__ float slack_sh[2];
+    __shared__ unsigned long long near_key_sh[kTopNear];
+    __shared__ int near_b_sh[kTopNear];
+    __shared__ int warp_sums[kTopThreads / 32], bin_sel, above_sel, count_sel, near_n, sure_n;
+    __shared__ uint32_t lo_sh, hi_sh, big_sh, sum_sh;  // keys of the range's ends; bits of the largest |bound| and sum of |q|
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = a.Hq / a.Hkv;
     constexpr int kBinsPer = kTopBins / kTopThreads;
-    int32_t* near_b = a.near_b + (long)blockIdx.x * a.mbps;
-    unsigned long long* near_key = a.near_key + (long)blockIdx.x * a.mbps;
     bool waited = false;
     const long rows = (long)a.total_q * a.Hkv;
     for (long row = blockIdx.x; row < rows; row += gridDim.x) {
         const int hk = (int)(row % a.Hkv);
-        SeqItem it;
-        const bool some = find_item(a.q_lens, a.ctx_lens, a.num_seqs, row / a.Hkv,
-                                    [&](int ql, int cl) { return lens_ok(ql, cl, a.mbps) ? ql : -1; }, it);
-        if (row == 0 && tid == 0 && (it.bad || it.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
-        if (!some || (long long)it.q0 + it.ql > a.total_q) continue;
-        const long at_row = (long)it.q0 + it.off;
-        int32_t* out = a.sel + (at_row * a.Hkv + hk) * a.keep;
-        const int n = (it.cl - it.ql + it.off) / kScaledBlock + 1;  // blocks that the query sees
-        if (n <= a.keep) {
-            for (int i = tid; i < a.keep; i += kTopThreads) out[i] = i < n ? i : -1;
-            continue;
-        }
-        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are complete
-        waited = true;
-        const float* sc = a.scores + (at_row * a.Hkv + hk) * a.mbps;
-        const int mid0 = a.sink, mid1 = n - a.recent;  // the scores decide about blocks [mid0, mid1)
-        const int want = a.keep - a.sink - a.recent;
-        const bool once = n <= kTopThreads * kTopItems;
-        uint32_t key[kTopItems];
-        unsigned middle;
-        auto load = [&](int base) {
-            middle = 0;
-#pragma unroll
-            for (int k = 0; k < kTopItems; ++k) {
-                const int b = base + k * kTopThreads + tid;
-                key[k] = 0;
-                if (b >= mid0 && b < mid1) {
-                    key[k] = score_key(__ldcg(sc + b));
-                    middle |= 1u << k;
-                }
-            }
-        };
-        load(0);
-        const int words = (n + 31) / 32;
-        __syncthreads();  // `taken` of the row before is read
-        for (int w = tid; w < words; w += kTopThreads) {
-            uint32_t bits = 0;  // the first and the last blocks
-            const int b0 = w * 32;
-            if (mid0 > b0) bits |= mid0 - b0 >= 32 ? 0xffffffffu : (1u << (mid0 - b0)) - 1;
-            if (mid1 < b0 + 32) bits |= mid1 <= b0 ? 0xffffffffu : ~((1u << (mid1 - b0)) - 1);
-            if (n < b0 + 32) bits &= (1u << (n - b0)) - 1;
-            taken[w] = bits;
-        }
-        for (int i = tid; i < kTopBins; i += kTopThreads) hist[i] = 0;
-        if (tid == 0) near_n = sure_n = 0;
-        // the rounding bound: the largest bound of the blocks, times the largest sum of |q| of a head
-        float big = 0.f;
-        for (int b = mid0 + tid; b < mid1; b += kTopThreads)
-            big = fmaxf(big, __ldcg(a.largest + ((long)it.s * a.Hkv + hk) * a.mbps + b));
-        if (tid < 2) slack_sh[tid] = 0.f;
-        __syncthreads();
-        big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+        const long at_row = row / a.Hkv;
+        // the largest sum of |q| of a head
         float sum_q = 0.f;
         for (int h = warp; h < g; h += kTopThreads / 32) {
             const uint16_t* q = a.q + (at_row * a.Hq + hk * g + h) * D;
@@ -268,121 +439,225 @@ __global__ void __launch_bounds__(kTopThreads, kTopCtasPerSm) block_top_kernel(c
             for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             sum_q = fmaxf(sum_q, x);
         }
-        if (lane == 0) {  // (not negative: as integers in order)
-            atomicMax(reinterpret_cast<int*>(&slack_sh[0]), __float_as_int(big));
-            atomicMax(reinterpret_cast<int*>(&slack_sh[1]), __float_as_int(sum_q));
+        SeqItem it;
+        auto count = [](int ql, int) { return max(0, ql); };
+        const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+        const bool some = scan.find(a.q_lens, a.ctx_lens, at_row, count, it);
+        const bool fits = some && lens_ok(it.ql, it.cl, a.mbps) && (long long)it.q0 + it.ql <= a.total_q;
+        if (hk == 0 && tid == 0 && (!fits || scan.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        if (!fits) continue;
+        int32_t* out = a.sel + row * a.keep;
+        const int n = (it.cl - it.ql + (int)it.off) / kScaledBlock + 1;  // blocks that the query sees
+        if (n <= a.keep) {
+            for (int i = tid; i < a.keep; i += kTopThreads) out[i] = i < n ? i : -1;
+            continue;
         }
-        uint32_t prefix = 0;
-        int need = want;
-        for (int pass = 0; pass < 3 && want > 0; ++pass) {
-            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-            for (int base = 0; base < n; base += kTopThreads * kTopItems) {
+        const int mid0 = a.sink, mid1 = n - a.recent;  // the scores decide about blocks [mid0, mid1)
+        const int want = a.keep - a.sink - a.recent;
+        const int words = (n + 31) / 32;
+        __syncthreads();  // what the row before left in shared memory is read
+        for (int w = tid; w < words; w += kTopThreads) {
+            uint32_t bits = 0;  // the first and the last blocks
+            const int b0 = w * 32;
+            if (mid0 > b0) bits |= mid0 - b0 >= 32 ? 0xffffffffu : (1u << (mid0 - b0)) - 1;
+            if (mid1 < b0 + 32) bits |= mid1 <= b0 ? 0xffffffffu : ~((1u << (mid1 - b0)) - 1);
+            if (n < b0 + 32) bits &= (1u << (n - b0)) - 1;
+            taken[w] = bits;
+        }
+        auto clear_bins = [&]() {
+#pragma unroll
+            for (int k = 0; k < kTopBins / 2 / kTopThreads; ++k)
+                reinterpret_cast<int2*>(hist)[k * kTopThreads + tid] = make_int2(0, 0);
+        };
+        clear_bins();
+        if (tid == 0) {
+            near_n = sure_n = 0;
+            lo_sh = 0xffffffffu;
+            hi_sh = big_sh = sum_sh = 0u;
+        }
+        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are complete
+        waited = true;
+        const float* sc = a.scores + row * a.mbps;
+        const float* largest = a.largest + ((long)it.s * a.Hkv + hk) * a.mbps;
+        constexpr int kPass = kTopThreads * kTopItems;
+        const bool once = n <= kPass;
+        float v[kTopItems];
+        auto load = [&](int base) {  // scores of blocks base + 256 k + tid (finite: the largest numbers stand for infinities, NaN last)
+#pragma unroll
+            for (int k = 0; k < kTopItems; ++k) {
+                if (base + k * kTopThreads >= mid1) break;  // (the same for the whole CTA)
+                const int b = base + k * kTopThreads + tid;
+                const float x = b >= mid0 && b < mid1 ? __ldcg(sc + b) : 0.f;
+                v[k] = x == x ? fminf(fmaxf(x, -1e38f), 1e38f) : -1e38f;
+            }
+        };
+        // f(block, its score, whether the scores decide about it) for all of them, whole warps
+        auto for_scores = [&](auto f) {
+            for (int base = 0; base < mid1; base += kPass) {
                 if (!once) load(base);
 #pragma unroll
                 for (int k = 0; k < kTopItems; ++k) {
-                    const bool in = ((middle >> k) & 1u) && (pass == 0 || ((key[k] ^ prefix) >> (shift + bits)) == 0);
-                    if (in) atomicAdd(&hist[(key[k] >> shift) & ((1u << bits) - 1)], 1);
-                }
-            }
-            __syncthreads();
-            const int top = kTopBins - kBinsPer * (tid + 1);  // this thread's bins, highest first
-            int cnt[kBinsPer], own = 0;
-#pragma unroll
-            for (int b = 0; b < kBinsPer; ++b) {
-                cnt[b] = hist[top + b];
-                hist[top + b] = 0;
-                own += cnt[b];
-            }
-            int x = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            if (lane == 31) warp_sums[warp] = x;
-            __syncthreads();
-            int above = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane & 7] : 0) + x - own;
-            if (above < need && above + own >= need) {
-#pragma unroll
-                for (int b = kBinsPer - 1; b >= 0; --b) {
-                    if (above < need && above + cnt[b] >= need) {
-                        digit_sel = top + b;
-                        above_sel = above;
-                    }
-                    above += cnt[b];
-                }
-            }
-            __syncthreads();
-            prefix |= (uint32_t)digit_sel << shift;
-            need -= above_sel;
-        }
-        if (want > 0) {
-            // sure: above the border by more than both sums' errors; near: within them
-            const float t = key_score(prefix);
-            float slack = 2.f * slack_sh[0] * slack_sh[1] * sum_slack(D);
-            if (!(slack < INFINITY)) slack = 0.f;  // bounds or queries that are not finite: as they come
-            const uint32_t hi = prefix == 0u ? 0u : score_key(t + slack), lo = prefix == 0u ? 0u : score_key(t - slack);
-            for (int base = 0; base < n; base += kTopThreads * kTopItems) {
-                if (!once) load(base);
-                int sure = 0;
-#pragma unroll
-                for (int k = 0; k < kTopItems; ++k) {
+                    if (base + k * kTopThreads >= mid1) break;
                     const int b = base + k * kTopThreads + tid;
-                    const bool in = (middle >> k) & 1u, is_sure = in && key[k] > hi, is_near = in && key[k] >= lo && key[k] <= hi;
-                    const unsigned ms = __ballot_sync(0xffffffffu, is_sure), mn = __ballot_sync(0xffffffffu, is_near);
-                    sure += __popc(ms);
-                    if (lane == 0 && ms) atomicOr(&taken[b >> 5], ms);  // (a warp's 32 blocks are one word)
-                    if (mn) {
-                        int at = 0;
-                        if (lane == 0) at = atomicAdd(&near_n, __popc(mn));
-                        at = __shfl_sync(0xffffffffu, at, 0);
-                        if (is_near) near_b[at + __popc(mn & ((1u << lane) - 1))] = b;
-                    }
+                    f(b, v[k], b >= mid0 && b < mid1);
                 }
-                if (lane == 0 && sure) atomicAdd(&sure_n, sure);
+            }
+        };
+        float big = 0.f;
+        for (int b = mid0 + tid; b < mid1; b += kTopThreads) big = fmaxf(big, __ldcg(largest + b));
+        load(0);
+        __syncthreads();
+        if (want > 0) {
+            uint32_t klo = 0xffffffffu, khi = 0u;
+            for_scores([&](int, float x, bool in) {
+                if (in) {
+                    klo = min(klo, float_key(x));
+                    khi = max(khi, float_key(x));
+                }
+            });
+            klo = __reduce_min_sync(0xffffffffu, klo);
+            khi = __reduce_max_sync(0xffffffffu, khi);
+            const uint32_t kbig = __reduce_max_sync(0xffffffffu, __float_as_uint(big));  // (not negative: in order as integers)
+            if (lane == 0) {
+                atomicMin(&lo_sh, klo);
+                atomicMax(&hi_sh, khi);
+                atomicMax(&big_sh, kbig);
+                atomicMax(&sum_sh, __float_as_uint(sum_q));
             }
             __syncthreads();
-            const int cand = near_n, left = want - sure_n;
-            if (cand <= left) {
-                for (int i = tid; i < cand; i += kTopThreads) atomicOr(&taken[near_b[i] >> 5], 1u << (near_b[i] & 31));
-            } else {
-                // exact keys of the blocks near the border (equal scores for sure: all alike)
-                for (int i = warp; i < cand; i += kTopThreads / 32) {
-                    const int phys = __ldg(a.bt + (long)it.s * a.mbps + near_b[i]);
-                    double best = 0.0;
-                    if (slack > 0.f && phys >= 0 && phys < a.num_blocks) {
-                        const uint16_t* box = a.bounds + ((long)phys * a.Hkv + hk) * 2 * D;
-                        for (int h = 0; h < g; ++h) {
-                            const uint16_t* q = a.q + (at_row * a.Hq + hk * g + h) * D;
-                            double sum = 0.0;
+            float lo = key_float(lo_sh), hi = key_float(hi_sh);
+            float slack = 2.f * __uint_as_float(big_sh) * __uint_as_float(sum_sh) * sum_slack(D);
+            if (!(slack < 1e37f)) slack = 0.f;  // bounds or queries that are not finite: as they come
+            // Bins of the range [lo, hi]; the range becomes that of the bin with the last block taken while it holds
+            // many blocks and is wider than what the roundings blur anyway.
+            int need = want, sel = 0;  // blocks to take of the range
+            float inv;
+            auto bin = [&](float x) { return min(kTopBins - 1, max(0, (int)((x - lo) * inv))); };
+            for (int pass = 0;; ++pass) {
+                inv = fminf((kTopBins - 1) / fmaxf(hi - lo, 1e-37f), 1e37f);
+                for_scores([&](int, float x, bool in) {
+                    if (in && x >= lo && x <= hi) atomicAdd(&hist[bin(x)], 1);
+                });
+                __syncthreads();
+                const int top = kTopBins - kBinsPer * (tid + 1);  // this thread's bins, highest first
+                int cnt[kBinsPer], own = 0;
 #pragma unroll
-                            for (int c = lane; c < D; c += 32) {
-                                const float x = __uint_as_float((uint32_t)__ldg(q + c) << 16);
-                                // (a product of two bf16 numbers is exact in fp32, unless it leaves its range)
-                                sum += (double)x * (double)__uint_as_float((uint32_t)__ldg(box + (x < 0.f ? c : D + c)) << 16);
-                            }
+                for (int b = 0; b < kBinsPer; b += 2) {
+                    const int2 c = *reinterpret_cast<const int2*>(&hist[top + b]);
+                    cnt[b] = c.x;
+                    cnt[b + 1] = c.y;
+                    own += c.x + c.y;
+                }
+                int x = own;
 #pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                            best = h == 0 || sum > best ? sum : best;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (lane == 31) warp_sums[warp] = x;
+                __syncthreads();
+                int above = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane & (kTopThreads / 32 - 1)] : 0) + x - own;
+                if (above < need && above + own >= need) {
+#pragma unroll
+                    for (int b = kBinsPer - 1; b >= 0; --b) {
+                        if (above < need && above + cnt[b] >= need) {
+                            bin_sel = top + b;
+                            above_sel = above;
+                            count_sel = cnt[b];
                         }
+                        above += cnt[b];
                     }
-                    if (lane == 0) near_key[i] = score_key64(best);
+                }
+                if (tid == 0) {
+                    lo_sh = 0xffffffffu;
+                    hi_sh = 0u;
+                }
+                clear_bins();
+                __syncthreads();
+                sel = bin_sel;
+                if (count_sel <= 32 || pass == 5 || !(1.f > slack * inv)) break;
+                need -= above_sel;
+                klo = 0xffffffffu;
+                khi = 0u;
+                for_scores([&](int, float y, bool in) {
+                    if (in && y >= lo && y <= hi && bin(y) == sel) {
+                        klo = min(klo, float_key(y));
+                        khi = max(khi, float_key(y));
+                    }
+                });
+                klo = __reduce_min_sync(0xffffffffu, klo);
+                khi = __reduce_max_sync(0xffffffffu, khi);
+                if (lane == 0) {
+                    atomicMin(&lo_sh, klo);
+                    atomicMax(&hi_sh, khi);
                 }
                 __syncthreads();
-                // the `left` largest, equal ones by block number
-                if (cand <= kTopCount) {
+                lo = key_float(lo_sh);
+                hi = key_float(hi_sh);
+                if (lo == hi) break;  // (all alike)
+            }
+            // The border lies in bin `sel` of [lo, hi], or at lo = hi.  Sure: above it by more than both sums' errors;
+            // near: within them (a bin more, for the rounding of the bins themselves).
+            const int blur = lo == hi ? 0 : (int)fminf(slack * inv, (float)kTopBins) + 2;
+            int32_t* near_far = a.near_b + (long)blockIdx.x * a.mbps;
+            int sure = 0;
+            for_scores([&](int b, float x, bool in) {
+                bool is_sure = x > hi + slack, is_near = x >= lo - slack && !is_sure;
+                if (lo != hi && x >= lo && x <= hi) {
+                    is_sure = bin(x) > sel + blur;
+                    is_near = !is_sure && bin(x) >= sel - blur;
+                } else if (lo != hi) {  // outside the last range: near if within the slack of the border's bin
+                    is_near = is_near && (x > hi ? kTopBins - 1 - sel <= blur : sel <= blur);
+                    is_sure = x > hi && !is_near;
+                }
+                is_sure = is_sure && in;
+                is_near = is_near && in;
+                const unsigned ms = __ballot_sync(0xffffffffu, is_sure), mn = __ballot_sync(0xffffffffu, is_near);
+                sure += __popc(ms);
+                if (lane == 0 && ms) atomicOr(&taken[b >> 5], ms);  // (a warp's 32 blocks are one word)
+                if (mn) {
+                    int at = 0;
+                    if (lane == 0) at = atomicAdd(&near_n, __popc(mn));
+                    at = __shfl_sync(0xffffffffu, at, 0) + __popc(mn & ((1u << lane) - 1));
+                    if (is_near) {
+                        if (at < kTopNear) near_b_sh[at] = b;
+                        near_far[at] = b;
+                    }
+                }
+            });
+            if (lane == 0 && sure) atomicAdd(&sure_n, sure);
+            __syncthreads();
+            const int cand = near_n, rest0 = want - sure_n;
+            const bool far = cand > kTopNear;
+            const int32_t* near_b = far ? near_far : near_b_sh;
+            unsigned long long* near_key = far ? a.near_key + (long)blockIdx.x * a.mbps : near_key_sh;
+            if (cand <= rest0) {
+                for (int i = tid; i < cand; i += kTopThreads) atomicOr(&taken[near_b[i] >> 5], 1u << (near_b[i] & 31));
+            } else {
+                // exact keys of the blocks near the border (without a bound on the roundings, all alike)
+                const uint16_t* q = a.q + (at_row * a.Hq + hk * g) * D;
+                for (int i = warp; i < cand; i += kTopThreads / 32) {
+                    const int phys = __ldg(a.bt + (long)it.s * a.mbps + near_b[i]);
+                    unsigned long long key = 1ull << 63 | 1ull << 31;  // a score of 0
+                    if (slack > 0.f && phys >= 0 && phys < a.num_blocks)
+                        key = exact_key<D>(q, g, a.bounds + ((long)phys * a.Hkv + hk) * 2 * D);
+                    if (lane == 0) near_key[i] = key;
+                }
+                __syncthreads();
+                // the `rest0` largest, equal ones by block number
+                if (!far) {
                     for (int i = tid; i < cand; i += kTopThreads) {
-                        const unsigned long long k = near_key[i];
-                        const int b = near_b[i];
+                        const unsigned long long k = near_key_sh[i];
+                        const int b = near_b_sh[i];
                         int before = 0;
-                        for (int j = 0; j < cand; ++j) before += near_key[j] > k || (near_key[j] == k && near_b[j] < b);
-                        if (before < left) atomicOr(&taken[b >> 5], 1u << (b & 31));
+                        for (int j = 0; j < cand; ++j) before += near_key_sh[j] > k || (near_key_sh[j] == k && near_b_sh[j] < b);
+                        if (before < rest0) atomicOr(&taken[b >> 5], 1u << (b & 31));
                     }
                 } else {
                     // radix select over (key, ~block number), 8 bits at a time: distinct, so it ends with one
                     unsigned long long p0 = 0;
                     uint32_t p1 = 0;
-                    int rest = left;
+                    int rest = rest0;
                     for (int pass = 0; pass < 12; ++pass) {
                         const int sh = 56 - 8 * pass, sh1 = 24 - 8 * (pass - 8);
                         for (int i = tid; i < cand; i += kTopThreads) {
@@ -414,7 +689,7 @@ __global__ void __launch_bounds__(kTopThreads, kTopCtasPerSm) block_top_kernel(c
                                 for (int b = 0; b < 8; ++b) {
                                     const int c = hist[255 - 8 * lane - b];
                                     if (above < rest && above + c >= rest) {
-                                        digit_sel = 255 - 8 * lane - b;
+                                        bin_sel = 255 - 8 * lane - b;
                                         above_sel = above;
                                     }
                                     above += c;
@@ -422,8 +697,8 @@ __global__ void __launch_bounds__(kTopThreads, kTopCtasPerSm) block_top_kernel(c
                         }
                         __syncthreads();
                         for (int i = tid; i < 256; i += kTopThreads) hist[i] = 0;
-                        if (pass < 8) p0 |= (unsigned long long)digit_sel << sh;
-                        else p1 |= (uint32_t)digit_sel << sh1;
+                        if (pass < 8) p0 |= (unsigned long long)bin_sel << sh;
+                        else p1 |= (uint32_t)bin_sel << sh1;
                         rest -= above_sel;
                         __syncthreads();
                     }
@@ -448,7 +723,7 @@ __global__ void __launch_bounds__(kTopThreads, kTopCtasPerSm) block_top_kernel(c
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            __syncthreads();  // warp_sums is read
+            if (base > 0) __syncthreads();  // warp_sums is read
             if (lane == 31) warp_sums[warp] = x;
             __syncthreads();
             const int ws = lane < kTopThreads / 32 ? warp_sums[lane] : 0;
@@ -469,7 +744,7 @@ static SelectWs select_ws_layout(int num_seqs, int mbps, int Hkv, int total_q) {
     w.scores = 0;
     w.largest = align256(sizeof(float) * (size_t)total_q * Hkv * mbps);
     w.near_key = align256(w.largest + sizeof(float) * (size_t)num_seqs * Hkv * mbps);
-    const size_t ctas = (size_t)kTopCtasPerSm * 160;
+    const size_t ctas = kTopCtas;
     w.near_b = align256(w.near_key + sizeof(unsigned long long) * ctas * mbps);
     w.total = align256(w.near_b + sizeof(int32_t) * ctas * mbps);
     return w;
@@ -509,30 +784,35 @@ fa_status fa_block_select(const void* q, const void* bounds, const int32_t* bloc
     SelectArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(bounds), block_table, ctx_lens, q_lens,
                  reinterpret_cast<float*>(wsb + w.scores), reinterpret_cast<float*>(wsb + w.largest),
                  reinterpret_cast<int32_t*>(wsb + w.near_b), reinterpret_cast<unsigned long long*>(wsb + w.near_key), sel,
-                 num_seqs, max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, keep, recent, sink, {}};
+                 num_seqs, max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, keep, recent, sink, 0, 1, {}};
+    while (1 << a.g2_log < Hq / Hkv && a.g2_log < 4) ++a.g2_log;
+    a.per = 16 >> a.g2_log;
     if ((st = make_ctx(&a.ctx)) != FA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int launches = 0;
     if (max_blocks_per_seq > keep) {  // else every block is taken
-        const int g = Hq / Hkv, per = g <= 16 ? 16 / g : 1;
-        const long tiles = (std::min(max_q_len, total_q) + per - 1) / per;
-        const long seg = (long)num_seqs * Hkv, groups = (max_blocks_per_seq + 7) / 8;
-        const long z = std::min<long>((tiles + kScWarps - 1) / kScWarps, 64);
-        const long side = tiles >= kScWarps ? 1 : kScWarps;  // about how many of a CTA's warps take groups of their own
-        const long y = std::max<long>(1, std::min((groups + side - 1) / side, 8L * sm_count() / std::max<long>(1, seg * z)));
-        const dim3 grid((unsigned)seg, (unsigned)std::min<long>(y, 65535), (unsigned)z);
-        if (d == 128) block_score_kernel<128><<<grid, kScWarps * 32, 0, s>>>(a);
-        else block_score_kernel<64><<<grid, kScWarps * 32, 0, s>>>(a);
+        const unsigned grid = (unsigned)(kScCtasPerSm * sm_count());
+        const bool big = Hq / Hkv > 16;
+        auto score = d == 128 ? (big ? block_score_kernel<128, true> : block_score_kernel<128, false>)
+                              : (big ? block_score_kernel<64, true> : block_score_kernel<64, false>);
+        const int smem = d == 128 ? ScoreSmem<128>::kBytes : ScoreSmem<64>::kBytes;
+        if ((st = raise_dynamic_smem(reinterpret_cast<const void*>(score), smem)) != FA_OK) return st;
+        score<<<grid, (kScWarps + 1) * 32, smem, s>>>(a);
         if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
         ++launches;
     }
-    auto top = d == 128 ? block_top_kernel<128> : block_top_kernel<64>;
-    if (bitmap + sizeof(int) * kTopBins > kUnraisedSmem &&
+    // few rows: more threads each (128 rows of 1270 scores 17 us with 256 threads, 24 with 128; 1140 rows of 350
+    // 28 us with 256, 24 with 128)
+    const long rows = (long)total_q * Hkv;
+    const int threads = rows <= 2L * sm_count() ? kTopFew : kTopMany;
+    auto top = threads == kTopFew ? (d == 128 ? block_top_kernel<128, kTopFew> : block_top_kernel<64, kTopFew>)
+                                  : (d == 128 ? block_top_kernel<128, kTopMany> : block_top_kernel<64, kTopMany>);
+    if (bitmap + 16 * 1024 > kUnraisedSmem &&
         (st = raise_dynamic_smem(reinterpret_cast<const void*>(top), (int)bitmap)) != FA_OK)
         return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long>((long)total_q * Hkv, (long)kTopCtasPerSm * std::min(sm_count(), 160)));
-    cfg.blockDim = dim3(kTopThreads);
+    cfg.gridDim = dim3((unsigned)std::min<long>(rows, std::min<long>(kTopCtas, 1024L / threads * sm_count())));
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = bitmap;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -106,13 +106,15 @@ __global__ void __launch_bounds__(kBlWarps * 32, 3)
     }
     t.reset();
     SeqItem it;
-    const bool some = find_item(a.q_lens, a.ctx_lens, a.num_seqs, row, [](int ql, int) { return max(0, ql); }, it);
+    auto count = [](int ql, int) { return max(0, ql); };
+    const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+    const bool some = scan.find(a.q_lens, a.ctx_lens, row, count, it);
     // (the whole cluster takes the same way)
     const bool fits = some && lens_ok(it.ql, it.cl, a.mbps);
-    if (blockIdx.x % C == 0 && threadIdx.x == 0 && (!fits || it.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+    if (blockIdx.x % C == 0 && threadIdx.x == 0 && (!fits || scan.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
     __syncthreads();
     if (!fits) return;
-    const int pos = it.cl - it.ql + it.off;
+    const int pos = it.cl - it.ql + (int)it.off;
     uint8_t* ring = smem + warp * ST * L::kStage;
     uint64_t* wbar = bars + warp * ST;
     int4* entries = lists + warp * kBlBatch;

@@ -93,7 +93,7 @@ template <int D, bool kF32>
 __device__ __forceinline__ void append_block(const AppendArgs& a, const SeqItem& it, int hk, bool is_v) {
     constexpr int N = D / 32, B = kScaledBlock;
     const int lane = threadIdx.x & 31;
-    const int first = it.cl - it.ql, blk = first / B + it.off;
+    const int first = it.cl - it.ql, blk = first / B + (int)it.off;
     const int lo = max(0, first - blk * B), hi = min(B, it.cl - blk * B);  // the block's new tokens
     const int phys = __ldg(a.bt + (long)it.s * a.mbps + blk);
     if (phys < 0 || phys >= a.num_blocks) {
@@ -207,9 +207,10 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const __grid_constan
     SeqItem it;
     if (w < a.block_warps) {
         const int per = 2 * a.Hkv;
-        const bool some = find_item(a.q_lens, a.ctx_lens, a.num_seqs, w / per,
-                                    [&](int ql, int cl) { return chunk_blocks(ql, cl, a.mbps); }, it);
-        if (w == 0 && lane == 0 && (it.bad || it.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        auto count = [&](int ql, int cl) { return chunk_blocks(ql, cl, a.mbps); };
+        const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+        if (w == 0 && lane == 0 && (scan.bad || scan.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        const bool some = scan.find(a.q_lens, a.ctx_lens, w / per, count, it);
         if (!some || (long long)it.q0 + it.ql > a.total_q) return;
         const int r = (int)(w % per);
         append_block<D, kF32>(a, it, r >> 1, r & 1);
@@ -232,9 +233,10 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const __grid_constan
     };
     load(h0);
     int pos;
-    if (!find_item(a.q_lens, a.ctx_lens, a.num_seqs, row, [](int ql, int) { return max(0, ql); }, it)) return;
+    auto count = [](int ql, int) { return max(0, ql); };
+    if (!SeqScan(a.q_lens, a.ctx_lens, a.num_seqs, count).find(a.q_lens, a.ctx_lens, row, count, it)) return;
     if (!lens_ok(it.ql, it.cl, a.mbps)) return;  // (reported above)
-    pos = a.positions ? __ldg(a.positions + row) : it.cl - it.ql + it.off;
+    pos = a.positions ? __ldg(a.positions + row) : it.cl - it.ql + (int)it.off;
     if (pos < 0 || pos >= a.max_pos) {
         if (lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
         return;
@@ -274,11 +276,11 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const void* __restric
     const long w = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, hk = (int)(w % Hkv);
     SeqItem it;
-    const bool some = find_item(q_lens, ctx_lens, num_seqs, w / Hkv,
-                                [&](int ql, int cl) { return chunk_blocks(ql, cl, mbps); }, it);
-    if (w == 0 && lane == 0 && (it.bad || it.rows != total_q)) raise_error(ctx, ERR_BOUNDS_BIT);
-    if (!some) return;
-    const int blk = (it.cl - it.ql) / B + it.off, n = min(B, it.cl - blk * B);
+    auto count = [&](int ql, int cl) { return chunk_blocks(ql, cl, mbps); };
+    const SeqScan scan(q_lens, ctx_lens, num_seqs, count);
+    if (w == 0 && lane == 0 && (scan.bad || scan.rows != total_q)) raise_error(ctx, ERR_BOUNDS_BIT);
+    if (!scan.find(q_lens, ctx_lens, w / Hkv, count, it)) return;
+    const int blk = (it.cl - it.ql) / B + (int)it.off, n = min(B, it.cl - blk * B);
     const int phys = __ldg(bt + (long)it.s * mbps + blk);
     if (phys < 0 || phys >= num_blocks) {
         if (lane == 0) raise_error(ctx, ERR_BOUNDS_BIT);

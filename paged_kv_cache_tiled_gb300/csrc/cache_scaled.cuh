@@ -17,67 +17,83 @@ constexpr int kExpLeast = 87;
 // 2^(code - 127) for a scale code (0: 2^-127; 255: +inf, as the power of two it is not).
 __device__ __forceinline__ float scale_of(int code) { return __uint_as_float(code > 0 ? (uint32_t)code << 23 : 0x00400000u); }
 
-// Where item `idx` of a batch lies when sequence s has count(q_len, ctx_len) items
-// (negative: its lengths are inconsistent, it has none).  Called by a whole warp.
+// Where items of a batch lie when sequence s has count(q_len, ctx_len) of them (negative:
+// its lengths are inconsistent, it has none).  Made and asked by whole warps.
 struct SeqItem {
     int s, ql, cl;   // sequence and its lengths
-    int off;         // item within the sequence
+    long long off;   // item within the sequence
     int q0;          // first packed query row of the sequence
-    long long rows;  // query rows of the batch
-    bool bad;        // some sequence's lengths are inconsistent
 };
-template <class Count>
-__device__ __forceinline__ bool find_item(const int32_t* __restrict__ q_lens, const int32_t* __restrict__ ctx_lens,
-                                          int num_seqs, long long idx, Count count, SeqItem& it) {
-    const int lane = threadIdx.x & 31, per = (num_seqs + 31) >> 5;
-    const int lo = min(num_seqs, lane * per), hi = min(num_seqs, lo + per);
-    long long n = 0, q = 0;
-    bool bad = false;
+struct SeqScan {
+    long long items, rows;  // of the batch
+    bool bad;               // some sequence's lengths are inconsistent
+    long long n, in, iq, q; // this lane's items and rows, and those up to its end
+    int lo, hi;             // its sequences
+
+    template <class Count>
+    __device__ __forceinline__ SeqScan(const int32_t* __restrict__ q_lens, const int32_t* __restrict__ ctx_lens, int num_seqs,
+                                       Count count) {
+        const int lane = threadIdx.x & 31, per = (num_seqs + 31) >> 5;
+        lo = min(num_seqs, lane * per);
+        hi = min(num_seqs, lo + per);
+        n = q = 0;
+        bool b = false;
 #pragma unroll 4
-    for (int s = lo; s < hi; ++s) {
-        const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s), c = count(ql, cl);
-        n += max(0, c);
-        q += max(0, ql);
-        bad |= c < 0;
-    }
-    long long in = n, iq = q;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long a = __shfl_up_sync(0xffffffffu, in, o), b = __shfl_up_sync(0xffffffffu, iq, o);
-        if (lane >= o) {
-            in += a;
-            iq += b;
-        }
-    }
-    it.rows = __shfl_sync(0xffffffffu, iq, 31);
-    it.bad = __any_sync(0xffffffffu, bad);
-    const unsigned hit = __ballot_sync(0xffffffffu, n > 0 && idx >= in - n && idx < in);
-    if (!hit) return false;
-    const int src = __ffs(hit) - 1;
-    int s_ = 0, ql_ = 0, cl_ = 0, off_ = 0, q0_ = 0;
-    if (lane == src) {
-        long long off = idx - (in - n), q0 = iq - q;
         for (int s = lo; s < hi; ++s) {
-            const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s), c = max(0, count(ql, cl));
-            if (off < c) {
-                s_ = s;
-                ql_ = ql;
-                cl_ = cl;
-                off_ = (int)off;
-                q0_ = (int)min(q0, 0x7fffffffLL);  // (past any row when the lengths are nonsense)
-                break;
-            }
-            off -= c;
-            q0 += max(0, ql);
+            const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s);
+            const long long c = count(ql, cl);
+            n += max(0ll, c);
+            q += max(0, ql);
+            b |= c < 0;
         }
+        in = n;
+        iq = q;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, in, o), y = __shfl_up_sync(0xffffffffu, iq, o);
+            if (lane >= o) {
+                in += x;
+                iq += y;
+            }
+        }
+        items = __shfl_sync(0xffffffffu, in, 31);
+        rows = __shfl_sync(0xffffffffu, iq, 31);
+        bad = __any_sync(0xffffffffu, b);
     }
-    it.s = __shfl_sync(0xffffffffu, s_, src);
-    it.ql = __shfl_sync(0xffffffffu, ql_, src);
-    it.cl = __shfl_sync(0xffffffffu, cl_, src);
-    it.off = __shfl_sync(0xffffffffu, off_, src);
-    it.q0 = __shfl_sync(0xffffffffu, q0_, src);
-    return true;
-}
+    template <class Count>
+    __device__ __forceinline__ bool find(const int32_t* __restrict__ q_lens, const int32_t* __restrict__ ctx_lens, long long idx,
+                                         Count count, SeqItem& it) const {
+        const int lane = threadIdx.x & 31;
+        const unsigned hit = __ballot_sync(0xffffffffu, n > 0 && idx >= in - n && idx < in);
+        if (!hit) return false;
+        const int src = __ffs(hit) - 1;
+        int s_ = 0, ql_ = 0, cl_ = 0, q0_ = 0;
+        long long off_ = 0;
+        if (lane == src) {
+            long long off = idx - (in - n), q0 = iq - q;
+            for (int s = lo; s < hi; ++s) {
+                const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s);
+                const long long c = max(0ll, (long long)count(ql, cl));
+                if (off < c) {
+                    s_ = s;
+                    ql_ = ql;
+                    cl_ = cl;
+                    off_ = off;
+                    q0_ = (int)min(q0, 0x7fffffffLL);  // (past any row when the lengths are nonsense)
+                    break;
+                }
+                off -= c;
+                q0 += max(0, ql);
+            }
+        }
+        it.s = __shfl_sync(0xffffffffu, s_, src);
+        it.ql = __shfl_sync(0xffffffffu, ql_, src);
+        it.cl = __shfl_sync(0xffffffffu, cl_, src);
+        it.off = __shfl_sync(0xffffffffu, off_, src);
+        it.q0 = __shfl_sync(0xffffffffu, q0_, src);
+        return true;
+    }
+};
 
 // Do a chunk of ql tokens and a context of cl of them (the chunk included) fit the table?
 __device__ __forceinline__ bool lens_ok(int ql, int cl, int mbps) {
