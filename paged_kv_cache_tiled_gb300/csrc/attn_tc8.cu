@@ -40,7 +40,7 @@ struct T8Cfg {
     static constexpr int kStages = 4, kStaging = 2;
     static constexpr int kBars = 2 * kStages + 2 * kStaging + 2 * 7 + 2 + 2 * kT8Units;
     static constexpr int kSmem = 1024 + 2 * kTileBytes + kStages * kTileBytes + kStaging * kStageBytes +
-                                 kT8Scales * 16 * 4 + kBars * 8 + 16 + 4 * kT8Units;
+                                 kT8Scales * 24 * 4 + kBars * 8 + 16 + 4 * kT8Units;
     static constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 256 + D;
 };
 static_assert(T8Cfg<128>::kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -143,6 +143,10 @@ __device__ __noinline__ void t8_partial_row(uint32_t taddr, float4* o, float2* m
     *ml = make_float2(m, l);
 }
 
+__device__ __forceinline__ void st_shared(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // Turns row r of a query tile (128-byte swizzled atoms of 64 channels) from bf16 to f16 in
 // place, divided by a power of two that brings its largest magnitude below 2; returns
 // that power.
@@ -197,8 +201,8 @@ __global__ void __launch_bounds__(kT8Threads, 1)
     uint8_t* qbuf = smem;
     uint8_t* ring = qbuf + 2 * C::kTileBytes;
     uint8_t* staging = ring + S * C::kTileBytes;
-    float* scales = reinterpret_cast<float*>(staging + G8 * C::kStageBytes);  // [kT8Scales][8 key factors, 8 value exponents]
-    uint64_t* full = reinterpret_cast<uint64_t*>(scales + kT8Scales * 16);
+    float* scales = reinterpret_cast<float*>(staging + G8 * C::kStageBytes);  // [kT8Scales][8 key factors, 8 value exponents, 8 times 2^-exponent]
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + kT8Scales * 24);
     uint64_t* empty = full + S;
     uint64_t* sfill = empty + S;      // [2] staging: codes have landed
     uint64_t* sfree = sfill + G8;     // [2] and are converted
@@ -347,9 +351,10 @@ __global__ void __launch_bounds__(kT8Threads, 1)
                     if (which == 0 && lane < 8) {
                         // (this tile's place held scales of four tiles ago, whose softmax is done: its K tile's
                         // place in the ring was taken again since)
-                        float* sc = scales + (tiles % kT8Scales) * 16;
+                        float* sc = scales + (tiles % kT8Scales) * 24;
                         sc[lane] = scale_of(exps & 255);
                         sc[8 + lane] = (float)((exps >> 8) - kExpBias);
+                        sc[16 + lane] = scale_of(2 * kExpBias - (exps >> 8));
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&sfill[st], C::kStageBytes);
@@ -382,7 +387,12 @@ __global__ void __launch_bounds__(kT8Threads, 1)
         const int t = threadIdx.x - kT8Convert * 32;
         constexpr int kThreads = kT8Converters * 32;
         int n = 0;  // tiles (K and V) converted
-        auto widen = [](uint32_t w, uint32_t& lo, uint32_t& hi) { e4m3x4_to_f16x4(w, lo, hi); };
+        auto widen = [](const uint4& w, uint4& a, uint4& b) {
+            e4m3x4_to_f16x4(w.x, a.x, a.y);
+            e4m3x4_to_f16x4(w.y, a.z, a.w);
+            e4m3x4_to_f16x4(w.z, b.x, b.y);
+            e4m3x4_to_f16x4(w.w, b.z, b.w);
+        };
         for (int i = 0; ok; ++i) {
             int u;
             if (!read_unit(i, u)) {
@@ -401,46 +411,54 @@ __global__ void __launch_bounds__(kT8Threads, 1)
                     }
                     const uint8_t* src = staging + st * C::kStageBytes;
                     uint8_t* dst = ring + stage * C::kTileBytes;
-                    if (which == 0) {
-                        constexpr int kPer = D / 16;  // 16-code pieces of a token's row
-#pragma unroll 4
-                        for (int x = t; x < kT8Rows * kPer; x += kThreads) {
-                            const int tok = x / kPer, c = x % kPer;
-                            const uint4 w = *reinterpret_cast<const uint4*>(src + x * 16);
-                            uint4 a, b;
-                            widen(w.x, a.x, a.y);
-                            widen(w.y, a.z, a.w);
-                            widen(w.z, b.x, b.y);
-                            widen(w.w, b.z, b.w);
-                            uint8_t* atom = dst + (c >> 2) * C::kAtomBytes;
-                            // the second atom's pieces store their halves in the other order: eight lanes, eight bank groups
-                            const int c0 = 2 * (c & 3), swap = c >> 2;
-                            *reinterpret_cast<uint4*>(atom + sw128_offset(tok, c0 + swap)) = swap ? b : a;
-                            *reinterpret_cast<uint4*>(atom + sw128_offset(tok, c0 + 1 - swap)) = swap ? a : b;
-                        }
-                    } else {
-                        const int left = U.kv_len - kt * kT8Rows;  // tokens of the tile that exist
-#pragma unroll 4
-                        for (int x = t; x < 8 * D; x += kThreads) {
-                            const int page = x / D, c = x % D;
-                            uint4 w = *reinterpret_cast<const uint4*>(src + x * 16);
-                            const int have = left - page * kScaledBlock;
-                            if (have < kScaledBlock) {  // whatever is stored behind the last token counts as zeros
-                                auto cut = [&](uint32_t v, int k) {
-                                    const int h = have - 4 * k;
-                                    return h >= 4 ? v : (h <= 0 ? 0u : v & ((1u << (8 * h)) - 1));
-                                };
-                                w = make_uint4(cut(w.x, 0), cut(w.y, 1), cut(w.z, 2), cut(w.w, 3));
+                    // Piece k of 16 codes is this thread's x = t + 64 k.  Eight are loaded before the first is stored (the
+                    // compiler cannot tell the two buffers apart); every address is a base plus a constant.
+                    constexpr int kPieces = kT8Rows * D / 16 / kThreads, kAhead = 8;
+                    const int left = U.kv_len - kt * kT8Rows;  // tokens of the tile that exist
+                    const uint8_t* from = src + t * 16;
+#pragma unroll
+                    for (int k0 = 0; k0 < kPieces; k0 += kAhead) {
+                        uint4 w[kAhead];
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k) w[k] = *reinterpret_cast<const uint4*>(from + (k0 + k) * kThreads * 16);
+                        if (which == 0) {
+                            // token t / kPer + k * kStep, piece t % kPer of its row (k moves whole groups of eight rows).  The
+                            // second atom's pieces store their halves in the other order: eight lanes, eight bank groups.
+                            constexpr uint32_t kPer = D / 16, kStep = kThreads / kPer;
+                            static_assert(kStep % 8 == 0, "the swizzle is the same for every k");
+                            const uint32_t tok = (uint32_t)t / kPer, c = (uint32_t)t % kPer, c0 = 2 * (c & 3), swap = c >> 2;
+                            uint8_t* atom = dst + swap * C::kAtomBytes;
+                            uint8_t *to0 = atom + sw128_offset(tok, c0 + swap), *to1 = atom + sw128_offset(tok, c0 + 1 - swap);
+#pragma unroll
+                            for (int k = 0; k < kAhead; ++k) {
+                                uint4 a, b;
+                                widen(w[k], a, b);
+                                *reinterpret_cast<uint4*>(to0 + (k0 + k) * kStep * 128) = swap ? b : a;
+                                *reinterpret_cast<uint4*>(to1 + (k0 + k) * kStep * 128) = swap ? a : b;
                             }
-                            uint4 a, b;
-                            widen(w.x, a.x, a.y);
-                            widen(w.y, a.z, a.w);
-                            widen(w.z, b.x, b.y);
-                            widen(w.w, b.z, b.w);
-                            uint8_t* half = dst + (page >> 2) * (D * 128);
-                            const int c0 = 2 * (page & 3);
-                            *reinterpret_cast<uint4*>(half + sw128_offset(c, c0)) = a;
-                            *reinterpret_cast<uint4*>(half + sw128_offset(c, c0 + 1)) = b;
+                        } else {
+                            constexpr int kPerPage = D / kThreads;  // a thread's pieces of a page: channels t, t + 64
+                            if (left < kT8Rows) {                   // whatever is stored behind the last token counts as zeros
+#pragma unroll
+                                for (int k = 0; k < kAhead; ++k) {
+                                    const int have = left - (k0 + k) / kPerPage * kScaledBlock;
+                                    auto cut = [&](uint32_t v, int q) {
+                                        const int h = have - 4 * q;
+                                        return h >= 4 ? v : (h <= 0 ? 0u : v & ((1u << (8 * h)) - 1));
+                                    };
+                                    w[k] = make_uint4(cut(w[k].x, 0), cut(w[k].y, 1), cut(w[k].z, 2), cut(w[k].w, 3));
+                                }
+                            }
+                            const uint32_t row = smem_u32(dst) + t * 128 + ((t & 7) << 4);  // chunk 0 of channel t, swizzled
+#pragma unroll
+                            for (int k = 0; k < kAhead; ++k) {
+                                const int page = (k0 + k) / kPerPage, far = (k0 + k) % kPerPage;
+                                uint4 a, b;
+                                widen(w[k], a, b);
+                                const uint32_t at = row + (page >> 2) * (D * 128) + far * kThreads * 128;
+                                st_shared(at ^ (2 * (page & 3)) << 4, a);
+                                st_shared(at ^ (2 * (page & 3) + 1) << 4, b);
+                            }
                         }
                     }
                     fence_proxy_async_smem();
@@ -600,7 +618,7 @@ __global__ void __launch_bounds__(kT8Threads, 1)
                 tc_fence_after();
                 const int vlim = vis_end - kt * kT8Rows;  // visible columns: [0, vlim)
                 const bool plain = __all_sync(0xffffffffu, vlim >= kT8Rows);
-                const float4* sv = reinterpret_cast<const float4*>(scales + (tiles % kT8Scales) * 16);
+                const float4* sv = reinterpret_cast<const float4*>(scales + (tiles % kT8Scales) * 24);
                 // pass 1: the largest w = s mul 2^ks + ev, a block's 16 columns at a time
                 float mx = -INFINITY;
                 {
@@ -611,15 +629,20 @@ __global__ void __launch_bounds__(kT8Threads, 1)
                     float gm[8];
 #pragma unroll
                     for (int b = 0; b < 8; ++b) gm[b] = -INFINITY;
+                    // (group after group in turn: eight independent chains)
                     if (plain) {
 #pragma unroll
-                        for (int j = 0; j < kT8Rows; j += 2)
-                            gm[j >> 4] = fmax3f(gm[j >> 4], __uint_as_float(raw[j]), __uint_as_float(raw[j + 1]));
+                        for (int j = 0; j < kT8Rows / 2; ++j) {
+                            const int b = j & 7, c = 16 * b + 2 * (j >> 3);
+                            gm[b] = fmax3f(gm[b], __uint_as_float(raw[c]), __uint_as_float(raw[c + 1]));
+                        }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < kT8Rows; j += 2)
-                            gm[j >> 4] = fmax3f(gm[j >> 4], j < vlim ? __uint_as_float(raw[j]) : -INFINITY,
-                                                j + 1 < vlim ? __uint_as_float(raw[j + 1]) : -INFINITY);
+                        for (int j = 0; j < kT8Rows / 2; ++j) {
+                            const int b = j & 7, c = 16 * b + 2 * (j >> 3);
+                            gm[b] = fmax3f(gm[b], c < vlim ? __uint_as_float(raw[c]) : -INFINITY,
+                                           c + 1 < vlim ? __uint_as_float(raw[c + 1]) : -INFINITY);
+                        }
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -649,37 +672,40 @@ __global__ void __launch_bounds__(kT8Threads, 1)
                     uint32_t raw[64];
                     tmem_ld32(trow + s_col + h * 64, *reinterpret_cast<uint32_t(*)[32]>(raw));
                     tmem_ld32(trow + s_col + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(raw + 32));
-                    const float4 kf = sv[h], va = sv[2 + h];
-                    const float k4[4] = {kf.x, kf.y, kf.z, kf.w}, v4[4] = {va.x, va.y, va.z, va.w};
-                    tmem_wait_ld();
-                    uint32_t pk[32];
+                    const float4 kf = sv[h], va = sv[2 + h], vb = sv[4 + h];
+                    const float k4[4] = {kf.x, kf.y, kf.z, kf.w}, v4[4] = {va.x, va.y, va.z, va.w}, b4[4] = {vb.x, vb.y, vb.z, vb.w};
+                    float2 f2[4], add2[4], sum[4];
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        const float2 f2 = both(mul * k4[b]), add2 = both(v4[b] - m_use);
-                        float2 sum = make_float2(0.f, 0.f);
-                        if (plain) {
-#pragma unroll
-                            for (int j = 8 * b; j < 8 * b + 8; ++j) {
-                                const float2 x = __ffma2_rn(
-                                    make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), f2, add2);
-                                const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                                sum = __fadd2_rn(sum, pp);
-                                pk[j] = pack_f16x2(pp.x, pp.y);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 8 * b; j < 8 * b + 8; ++j) {
-                                const float2 x = __ffma2_rn(
-                                    make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), f2, add2);
-                                const int c = h * 64 + 2 * j;
-                                const float2 pp = make_float2(c < vlim ? fast_exp2(x.x) : 0.f, c + 1 < vlim ? fast_exp2(x.y) : 0.f);
-                                sum = __fadd2_rn(sum, pp);
-                                pk[j] = pack_f16x2(pp.x, pp.y);
-                            }
-                        }
-                        // 2^-ev, ev a whole number
-                        l = fmaf(sum.x + sum.y, __uint_as_float((uint32_t)max(1, 127 - (int)v4[b]) << 23), l);
+                        f2[b] = both(mul * k4[b]);
+                        add2[b] = both(v4[b] - m_use);
+                        sum[b] = make_float2(0.f, 0.f);
                     }
+                    tmem_wait_ld();
+                    uint32_t pk[32];
+                    if (plain) {
+#pragma unroll
+                        for (int j0 = 0; j0 < 32; ++j0) {
+                            const int b = j0 & 3, j = 8 * b + (j0 >> 2);
+                            const float2 x =
+                                __ffma2_rn(make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), f2[b], add2[b]);
+                            const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            sum[b] = __fadd2_rn(sum[b], pp);
+                            pk[j] = pack_f16x2(pp.x, pp.y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j0 = 0; j0 < 32; ++j0) {
+                            const int b = j0 & 3, j = 8 * b + (j0 >> 2), c = h * 64 + 2 * j;
+                            const float2 x =
+                                __ffma2_rn(make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), f2[b], add2[b]);
+                            const float2 pp = make_float2(c < vlim ? fast_exp2(x.x) : 0.f, c + 1 < vlim ? fast_exp2(x.y) : 0.f);
+                            sum[b] = __fadd2_rn(sum[b], pp);
+                            pk[j] = pack_f16x2(pp.x, pp.y);
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) l = fmaf(sum[b].x + sum[b].y, b4[b], l);  // 2^-ev
                     tmem_st32(trow + s_col + h * 32, pk);
                     if (!rescale_o) {
                         tmem_wait_st();

@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(kTopThreads, 1024 / kTopThreads) block_top_ker
     bool waited = false;
     const long rows = (long)a.total_q * a.Hkv;
     for (long row = blockIdx.x; row < rows; row += gridDim.x) {
-        const int hk = (int)(row % a.Hkv);
-        const long at_row = row / a.Hkv;
+        const long at_row = row < 1l << 31 ? (int)row / a.Hkv : row / a.Hkv;
+        const int hk = (int)(row - at_row * a.Hkv);
         // the largest sum of |q| of a head
         float sum_q = 0.f;
         for (int h = warp; h < g; h += kTopThreads / 32) {

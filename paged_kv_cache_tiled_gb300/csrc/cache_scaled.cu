@@ -6,12 +6,13 @@
 // is a floating format, so a finer scale would not make its values any finer, and
 // with powers of two a block whose scale grows keeps its codes' values exactly (only
 // what falls below 2^-6 of the new scale is rounded again).  The call knows its
-// tokens by sequence (block table and lengths), so one warp owns a (block, head) of
-// K or of V: it loads the block's new tokens (at most 16, a lane D / 32 channels of
-// each, all loads in flight), turns the keys, finds the largest magnitude, and
-// writes codes; no atomics, nothing that depends on an order.  V is channel-major:
-// a lane's codes are whole 16-byte rows.  Queries are turned by further warps of the
-// same launch, one a token.  Memory bound on prompts, latency bound on single tokens.
+// tokens by sequence (block table and lengths), so a warp owns the codes of a (block,
+// head) of K or of V: it loads the block's new tokens (at most 16, a lane D / 32
+// channels of each, all loads in flight), turns the keys by rows of cos_sin that its CTA
+// has in shared memory for all heads, finds the largest magnitude, and writes codes; no
+// atomics, nothing that depends on an order.  V is channel-major: a lane's codes are whole
+// 16-byte rows.  Queries are turned by further CTAs of the same launch.  Memory bound on
+// prompts, latency bound on single tokens.
 //
 // fa_block_bounds: smallest and largest value of every channel over a block's tokens,
 // recomputed for the blocks that a chunk's tokens lie in; a warp a (block, head).
@@ -29,7 +30,8 @@ struct AppendArgs {
     uint8_t *kc, *vc, *ke, *ve;
     const int32_t *bt, *ctx_lens, *q_lens;
     int max_pos, num_seqs, mbps, num_blocks, total_q, Hq, Hkv;
-    long block_warps;  // warps of the blocks, those of the queries follow
+    int parts, block_ctas;  // CTAs a block, and of all blocks; those of the queries follow
+    int tokens;       // query tokens a warp
     DevCtx ctx;
 };
 
@@ -88,142 +90,147 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float ratio) {
     return f32x4_to_e4m3x4(x[0], x[1], x[2], x[3]);
 }
 
-// The new tokens of one (block, head), K or V.
-template <int D, bool kF32>
-__device__ __forceinline__ void append_block(const AppendArgs& a, const SeqItem& it, int hk, bool is_v) {
-    constexpr int N = D / 32, B = kScaledBlock;
-    const int lane = threadIdx.x & 31;
-    const int first = it.cl - it.ql, blk = first / B + (int)it.off;
-    const int lo = max(0, first - blk * B), hi = min(B, it.cl - blk * B);  // the block's new tokens
-    const int phys = __ldg(a.bt + (long)it.s * a.mbps + blk);
-    if (phys < 0 || phys >= a.num_blocks) {
-        if (lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
-        return;
-    }
-    const long row0 = (long)it.q0 + blk * B - first;  // packed row of the block's token 0
-    const long head = (long)phys * a.Hkv + hk;
-    uint8_t* page = (is_v ? a.vc : a.kc) + head * B * D;
-    uint8_t* exps = is_v ? a.ve : a.ke;
-    const int e_old = lo > 0 ? (int)exps[head] : 0;
-    Raw<kF32, N> raw[B];
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-        if (i >= lo && i < hi) raw[i].load(is_v ? a.v : a.k, ((row0 + i) * a.Hkv + hk) * D + lane * N);
-    float x[B][N];
-    unsigned live = ((1u << hi) - 1) & ~((1u << lo) - 1);
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-#pragma unroll
-        for (int c = 0; c < N; ++c) x[i][c] = i >= lo && i < hi ? raw[i].get(c) : 0.f;
-    if (!is_v && a.cos_sin) {
-        // channel j < D/2 (lanes 0 .. 15) pairs with j + D/2 (lanes 16 .. 31)
-        const int at = (lane & 15) * N;
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            if (i < lo || i >= hi) continue;  // (the same for the whole warp)
-            const int pos = a.positions ? __ldg(a.positions + row0 + i) : blk * B + i;
-            if (pos < 0 || pos >= a.max_pos) {
-                if (lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
-                live &= ~(1u << i);
-                continue;
-            }
-            Raw<true, N> co, si;
-            co.load(a.cos_sin, (long)pos * D + at);
-            si.load(a.cos_sin, (long)pos * D + D / 2 + at);
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-                const float y = __shfl_xor_sync(0xffffffffu, x[i][c], 16);
-                x[i][c] = lane < 16 ? fmaf(x[i][c], co.get(c), -(y * si.get(c))) : fmaf(x[i][c], co.get(c), y * si.get(c));
-            }
-        }
-    }
-    // the largest finite magnitude
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-            const float v = fabsf(x[i][c]);
-            if (((live >> i) & 1u) && v < INFINITY) m = fmaxf(m, v);
-        }
-    // the smallest code whose 448 (1.75 * 2^8) times the scale reaches it
-    const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    const int e = max(max(e_old, kExpLeast), (int)(mb >> 23) - 8 + ((mb & 0x7FFFFFu) > 0x600000u ? 1 : 0));
-    const float inv = __uint_as_float((uint32_t)max(0, 254 - e) << 23);                  // 2^(127 - e)
-    const float ratio = __uint_as_float((uint32_t)max(0, kExpBias + e_old - e) << 23);  // of the older tokens' codes
-    const bool moved = lo > 0 && e != e_old;
-    if (!is_v) {
-        uint8_t* at = page + lane * N;
-        if (moved) {
-            for (int i = 0; i < lo; ++i) {
-                if constexpr (N == 4)
-                    *reinterpret_cast<uint32_t*>(at + i * D) = rescale_codes(*reinterpret_cast<uint32_t*>(at + i * D), ratio);
-                else
-                    *reinterpret_cast<uint16_t*>(at + i * D) =
-                        (uint16_t)rescale_codes(*reinterpret_cast<uint16_t*>(at + i * D), ratio);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            if (!((live >> i) & 1u)) continue;
-            const uint32_t lo2 = f32x2_to_e4m3x2(x[i][0] * inv, x[i][1] * inv);
-            if constexpr (N == 4)
-                *reinterpret_cast<uint32_t*>(at + i * D) = lo2 | f32x2_to_e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16;
-            else
-                *reinterpret_cast<uint16_t*>(at + i * D) = (uint16_t)lo2;
-        }
-    } else {
-        uint4* at = reinterpret_cast<uint4*>(page) + lane * N;  // a channel's 16 tokens
-        uint4 old[N];
-#pragma unroll
-        for (int c = 0; c < N; ++c) old[c] = live == 0xffffu ? make_uint4(0, 0, 0, 0) : at[c];
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-            uint32_t o[4] = {old[c].x, old[c].y, old[c].z, old[c].w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const unsigned l4 = (live >> (4 * w)) & 15u;
-                auto bytes = [](unsigned b) {
-                    return ((b & 1u) | (b & 2u) << 7 | (b & 4u) << 14 | (b & 8u) << 21) * 255u;
-                };
-                if (moved) {
-                    const uint32_t mask = bytes((((1u << lo) - 1) >> (4 * w)) & 15u);
-                    o[w] = (o[w] & ~mask) | (rescale_codes(o[w], ratio) & mask);
-                }
-                const uint32_t mask = bytes(l4);
-                o[w] = (o[w] & ~mask) | (f32x4_to_e4m3x4(x[4 * w][c] * inv, x[4 * w + 1][c] * inv, x[4 * w + 2][c] * inv,
-                                                         x[4 * w + 3][c] * inv) & mask);
-            }
-            at[c] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-    }
-    if (lane == 0) exps[head] = (uint8_t)e;
-}
+// A CTA takes a block that new tokens go to, or half of its heads when there are many: kPart
+// (head, K or V) pairs, even warps keys, odd warps values.
+constexpr int kAppendWarps = 4, kPart = 2 * kAppendWarps;
 
 template <int D, bool kF32>
-__global__ void __launch_bounds__(128) append_scaled_kernel(const __grid_constant__ AppendArgs a) {
-    const long w = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kAppendWarps * 32, 4) append_scaled_kernel(const __grid_constant__ AppendArgs a) {
+    constexpr int N = D / 32, B = kScaledBlock;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     SeqItem it;
-    if (w < a.block_warps) {
-        const int per = 2 * a.Hkv;
+    if ((int)blockIdx.x < a.block_ctas) {
+        __shared__ __align__(16) float turns[B][D];  // the tokens' rows of cos_sin
+        const int part = blockIdx.x % a.parts, place = blockIdx.x / a.parts;
         auto count = [&](int ql, int cl) { return chunk_blocks(ql, cl, a.mbps); };
         const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
-        if (w == 0 && lane == 0 && (scan.bad || scan.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
-        const bool some = scan.find(a.q_lens, a.ctx_lens, w / per, count, it);
-        if (!some || (long long)it.q0 + it.ql > a.total_q) return;
-        const int r = (int)(w % per);
-        append_block<D, kF32>(a, it, r >> 1, r & 1);
+        if (blockIdx.x == 0 && threadIdx.x == 0 && (scan.bad || scan.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        // (the same for the whole CTA from here on, but for the pairs)
+        if (!scan.find(a.q_lens, a.ctx_lens, place, count, it) || (long long)it.q0 + it.ql > a.total_q) return;
+        const int first = it.cl - it.ql, blk = first / B + (int)it.off;
+        const int lo = max(0, first - blk * B), hi = min(B, it.cl - blk * B);  // the block's new tokens
+        const int phys = __ldg(a.bt + (long)it.s * a.mbps + blk);
+        const long row0 = (long)it.q0 + blk * B - first;  // packed row of the block's token 0
+        Raw<kF32, N> raw[B];
+        const bool is_v = warp & 1;
+        auto load = [&](int pair) {
+            const long at = (row0 * a.Hkv + pair / 2) * D + lane * N;
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+                if (i >= lo && i < hi) raw[i].load(is_v ? a.v : a.k, at + (long)i * a.Hkv * D);
+        };
+        const int end = min(2 * a.Hkv, (part + 1) * kPart);
+        int pair = part * kPart + warp;
+        if (pair < end) load(pair);
+        unsigned live = ((1u << hi) - 1) & ~((1u << lo) - 1);
+        if (a.cos_sin) {
+            // lane i: token i's position
+            const int i = lane & 15;
+            const bool in = lane < B && i >= lo && i < hi;
+            const int pos = !in ? 0 : (a.positions ? __ldg(a.positions + row0 + i) : blk * B + i);
+            const unsigned out = __ballot_sync(0xffffffffu, in && (pos < 0 || pos >= a.max_pos));
+            if (out && threadIdx.x == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
+            live &= ~out;
+            constexpr int kQuads = D / 4;
+            for (int x = threadIdx.x; x < B * kQuads; x += kAppendWarps * 32) {  // (whole warps)
+                const int tok = x / kQuads, p = __shfl_sync(0xffffffffu, pos, tok);
+                if ((live >> tok) & 1u)
+                    *reinterpret_cast<float4*>(&turns[tok][x % kQuads * 4]) =
+                        __ldg(reinterpret_cast<const float4*>(a.cos_sin + (long)p * D) + x % kQuads);
+            }
+            __syncthreads();
+        }
+        if (phys < 0 || phys >= a.num_blocks) {
+            if (threadIdx.x == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
+            return;
+        }
+        const bool turned = !is_v && a.cos_sin;
+        const int at_pair = (lane & 15) * N;  // channel j < D/2 (lanes 0 .. 15) pairs with j + D/2 (lanes 16 .. 31)
+        for (; pair < end; pair += kAppendWarps) {
+            const long head = (long)phys * a.Hkv + pair / 2;
+            uint8_t* page = (is_v ? a.vc : a.kc) + head * B * D;
+            uint8_t* exps = is_v ? a.ve : a.ke;
+            const int e_old = lo > 0 ? (int)exps[head] : 0;
+            // token by token: values turned, and the largest finite magnitude
+            float x[B][N], m = 0.f;
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if (!((live >> i) & 1u)) continue;  // (the same for the whole warp)
+#pragma unroll
+                for (int c = 0; c < N; ++c) x[i][c] = raw[i].get(c);
+                if (turned) {
+#pragma unroll
+                    for (int c = 0; c < N; ++c) {
+                        const float y = __shfl_xor_sync(0xffffffffu, x[i][c], 16);
+                        const float co = turns[i][at_pair + c], ys = y * turns[i][D / 2 + at_pair + c];
+                        x[i][c] = fmaf(x[i][c], co, lane < 16 ? -ys : ys);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < N; ++c) m = fabsf(x[i][c]) < INFINITY ? fmaxf(m, fabsf(x[i][c])) : m;
+            }
+            if (pair + kAppendWarps < end) load(pair + kAppendWarps);
+            // the smallest code whose 448 (1.75 * 2^8) times the scale reaches it
+            const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+            const int e = max(max(e_old, kExpLeast), (int)(mb >> 23) - 8 + ((mb & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+            const float inv = __uint_as_float((uint32_t)max(0, 254 - e) << 23);                 // 2^(127 - e)
+            const float ratio = __uint_as_float((uint32_t)max(0, kExpBias + e_old - e) << 23);  // of the older tokens' codes
+            const bool moved = lo > 0 && e != e_old;
+            if (!is_v) {
+                uint8_t* at = page + lane * N;
+                if (moved) {
+                    for (int i = 0; i < lo; ++i) {
+                        if constexpr (N == 4)
+                            *reinterpret_cast<uint32_t*>(at + i * D) = rescale_codes(*reinterpret_cast<uint32_t*>(at + i * D), ratio);
+                        else
+                            *reinterpret_cast<uint16_t*>(at + i * D) =
+                                (uint16_t)rescale_codes(*reinterpret_cast<uint16_t*>(at + i * D), ratio);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    if (!((live >> i) & 1u)) continue;
+                    const uint32_t lo2 = f32x2_to_e4m3x2(x[i][0] * inv, x[i][1] * inv);
+                    if constexpr (N == 4)
+                        *reinterpret_cast<uint32_t*>(at + i * D) = lo2 | f32x2_to_e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16;
+                    else
+                        *reinterpret_cast<uint16_t*>(at + i * D) = (uint16_t)lo2;
+                }
+            } else {
+                uint4* at = reinterpret_cast<uint4*>(page) + lane * N;  // a channel's 16 tokens
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    const uint4 old = live == 0xffffu ? make_uint4(0, 0, 0, 0) : at[c];
+                    uint32_t o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        auto bytes = [](unsigned b) {
+                            return ((b & 1u) | (b & 2u) << 7 | (b & 4u) << 14 | (b & 8u) << 21) * 255u;
+                        };
+                        if (moved) {
+                            const uint32_t mask = bytes((((1u << lo) - 1) >> (4 * w)) & 15u);
+                            o[w] = (o[w] & ~mask) | (rescale_codes(o[w], ratio) & mask);
+                        }
+                        const uint32_t mask = bytes((live >> (4 * w)) & 15u);
+                        o[w] = (o[w] & ~mask) | (f32x4_to_e4m3x4(x[4 * w][c] * inv, x[4 * w + 1][c] * inv, x[4 * w + 2][c] * inv,
+                                                                 x[4 * w + 3][c] * inv) & mask);
+                    }
+                    at[c] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            if (lane == 0) exps[head] = (uint8_t)e;
+        }
         return;
     }
-    // a query token's heads: D / 16 lanes a head, 8 channel pairs each
-    const long row = w - a.block_warps;
-    if (row >= a.total_q || !a.q) return;
+    const int w = ((int)blockIdx.x - a.block_ctas) * kAppendWarps + warp;
+    // query tokens, `tokens` a warp: D / 16 lanes a head, 8 channel pairs each
+    const int row0 = w * a.tokens, row1 = min(a.total_q, row0 + a.tokens);
+    if (row0 >= row1 || !a.q) return;
     constexpr int kLanes = D / 16, kHeads = 32 / kLanes, kAhead = 4;
     const int c = (lane % kLanes) * 8, h0 = lane / kLanes;
-    Raw8<kF32> x[kAhead], y[kAhead];  // the first heads' values are on their way while the token's sequence is found
-    const long base = row * a.Hq * D + c;
-    auto load = [&](int h) {
+    Raw8<kF32> x[kAhead], y[kAhead];
+    auto load = [&](int row, int h) {
+        const long base = (long)row * a.Hq * D + c;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (h + k * kHeads < a.Hq) {
@@ -231,35 +238,40 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const __grid_constan
                 y[k].load(a.q, base + (long)(h + k * kHeads) * D + D / 2);
             }
     };
-    load(h0);
-    int pos;
+    load(row0, h0);  // on their way while the token's sequence is found
     auto count = [](int ql, int) { return max(0, ql); };
-    if (!SeqScan(a.q_lens, a.ctx_lens, a.num_seqs, count).find(a.q_lens, a.ctx_lens, row, count, it)) return;
-    if (!lens_ok(it.ql, it.cl, a.mbps)) return;  // (reported above)
-    pos = a.positions ? __ldg(a.positions + row) : it.cl - it.ql + (int)it.off;
-    if (pos < 0 || pos >= a.max_pos) {
-        if (lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
-        return;
-    }
-    Raw8<true> co, si;
-    co.load(a.cos_sin, (long)pos * D + c);
-    si.load(a.cos_sin, (long)pos * D + D / 2 + c);
-    for (int h = h0; h < a.Hq; h += kAhead * kHeads) {
-        if (h != h0) load(h);
+    const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+    long long end = 0;  // first row behind the sequence found
+    for (int row = row0; row < row1; ++row) {
+        if (row >= end) {
+            if (!scan.find(a.q_lens, a.ctx_lens, row, count, it)) return;
+            end = (long long)it.q0 + it.ql;
+        }
+        const int pos = a.positions ? __ldg(a.positions + row) : it.cl - it.ql + (row - it.q0);
+        const bool fits = lens_ok(it.ql, it.cl, a.mbps), in = pos >= 0 && pos < a.max_pos;  // (lengths are reported above)
+        if (fits && !in && lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        if (fits && in) {
+            Raw8<true> co, si;
+            co.load(a.cos_sin, (long)pos * D + c);
+            si.load(a.cos_sin, (long)pos * D + D / 2 + c);
+            for (int h = h0; h < a.Hq; h += kAhead * kHeads) {
+                if (h != h0 || row != row0) load(row, h);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (h + k * kHeads >= a.Hq) break;
-            const long at = base + (long)(h + k * kHeads) * D;
-            float u[8], v[8];
+                for (int k = 0; k < kAhead; ++k) {
+                    if (h + k * kHeads >= a.Hq) break;
+                    const long at = ((long)row * a.Hq + h + k * kHeads) * D + c;
+                    float u[8], v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                u[i] = fmaf(x[k].get(i), co.get(i), -(y[k].get(i) * si.get(i)));
-                v[i] = fmaf(y[k].get(i), co.get(i), x[k].get(i) * si.get(i));
+                    for (int i = 0; i < 8; ++i) {
+                        u[i] = fmaf(x[k].get(i), co.get(i), -(y[k].get(i) * si.get(i)));
+                        v[i] = fmaf(y[k].get(i), co.get(i), x[k].get(i) * si.get(i));
+                    }
+                    *reinterpret_cast<uint4*>(a.q_out + at) =
+                        make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+                    *reinterpret_cast<uint4*>(a.q_out + at + D / 2) =
+                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                }
             }
-            *reinterpret_cast<uint4*>(a.q_out + at) =
-                make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
-            *reinterpret_cast<uint4*>(a.q_out + at + D / 2) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
         }
     }
 }
@@ -273,8 +285,7 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const void* __restric
                                                            int num_seqs, int mbps, int num_blocks, int total_q, int Hkv,
                                                            DevCtx ctx) {
     constexpr int N = D / 32, B = kScaledBlock;
-    const long w = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, hk = (int)(w % Hkv);
+    const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, hk = w % Hkv;
     SeqItem it;
     auto count = [&](int ql, int cl) { return chunk_blocks(ql, cl, mbps); };
     const SeqScan scan(q_lens, ctx_lens, num_seqs, count);
@@ -363,15 +374,19 @@ fa_status fa_cache_append_fp8_scaled(const void* q, const void* k, const void* v
     if (st != FA_OK) return st;
     AppendArgs a{q, k, v, positions, cos_sin, static_cast<uint16_t*>(q_out), static_cast<uint8_t*>(k_cache),
                  static_cast<uint8_t*>(v_cache), k_exp, v_exp, block_table, ctx_lens, q_lens, max_pos, num_seqs,
-                 max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, 0, {}};
+                 max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, 1, 0, 1, {}};
     if ((st = make_ctx(&a.ctx)) != FA_OK) return st;
-    a.block_warps = chunk_blocks_bound(num_seqs, total_q) * 2 * Hkv;
-    const long ctas = (a.block_warps + (q ? total_q : 0) + 3) / 4;
+    a.parts = (2 * Hkv + kPart - 1) / kPart;
+    const long block_ctas = chunk_blocks_bound(num_seqs, total_q) * a.parts;
+    // (with more tokens than the GPU holds warps, two share a warp's search for their sequence)
+    a.tokens = total_q > 20 * sm_count() ? 2 : 1;
+    const long q_warps = q ? (total_q + a.tokens - 1) / a.tokens : 0, ctas = block_ctas + (q_warps + kAppendWarps - 1) / kAppendWarps;
     if (ctas > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
+    a.block_ctas = (int)block_ctas;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto kernel = d == 128 ? (in_dtype == FA_F32 ? append_scaled_kernel<128, true> : append_scaled_kernel<128, false>)
                            : (in_dtype == FA_F32 ? append_scaled_kernel<64, true> : append_scaled_kernel<64, false>);
-    kernel<<<(unsigned)ctas, 128, 0, s>>>(a);
+    kernel<<<(unsigned)ctas, kAppendWarps * 32, 0, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     set_launch_count(1);
     return FA_OK;
@@ -392,7 +407,7 @@ fa_status fa_block_bounds(const void* k_cache, const uint8_t* k_exp, const int32
     DevCtx ctx;
     if ((st = make_ctx(&ctx)) != FA_OK) return st;
     const long ctas = (chunk_blocks_bound(num_seqs, total_q) * Hkv + 3) / 4;
-    if (ctas > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
+    if (ctas > 0x1fffffffL) return FA_ERR_UNSUPPORTED;
     auto kernel = d == 128 ? (k_exp ? block_bounds_kernel<128, true> : block_bounds_kernel<128, false>)
                            : (k_exp ? block_bounds_kernel<64, true> : block_bounds_kernel<64, false>);
     kernel<<<(unsigned)ctas, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(

@@ -46,14 +46,28 @@ struct SeqScan {
             q += max(0, ql);
             b |= c < 0;
         }
-        in = n;
-        iq = q;
+        if (!__any_sync(0xffffffffu, n > 1 << 26 || q > 1 << 26)) {  // 32 bits hold every sum
+            int x = (int)n, y = (int)q;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, in, o), y = __shfl_up_sync(0xffffffffu, iq, o);
-            if (lane >= o) {
-                in += x;
-                iq += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+                if (lane >= o) {
+                    x += u;
+                    y += v;
+                }
+            }
+            in = x;
+            iq = y;
+        } else {
+            in = n;
+            iq = q;
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, in, o), v = __shfl_up_sync(0xffffffffu, iq, o);
+                if (lane >= o) {
+                    in += u;
+                    iq += v;
+                }
             }
         }
         items = __shfl_sync(0xffffffffu, in, 31);
