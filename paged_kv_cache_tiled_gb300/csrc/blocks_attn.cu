@@ -2,8 +2,8 @@
 //
 // One list per (query token, kv head): the Hq / Hkv heads of the group are the rows
 // of m16n8k16 warp MMAs, so that a listed block is read once for all of them.  A CTA
-// of four warps, or a cluster of up to eight of them when there are few lists, takes
-// one list: warp w of W takes entries w, w + W, ..., streams their pages through a
+// of two or four warps, or a cluster of up to eight of them when there are few lists,
+// takes one list: warp w of W takes entries w, w + W, ..., streams their pages through a
 // ring of its own in shared memory (TMA, the block looked up in the sequence's table)
 // and keeps a softmax of its own; at the end the warps' results are joined with
 // log-sum-exp weights in shared memory, across a cluster through distributed shared
@@ -15,7 +15,7 @@
 
 namespace fa {
 
-constexpr int kBlWarps = 4;
+constexpr int kBlSmWarps = 12;  // warps that an SM holds, by their registers and rings
 constexpr int kBlBatch = 32;  // list entries that a warp looks up at a time
 
 struct BlocksArgs {
@@ -29,18 +29,18 @@ struct BlocksArgs {
     DevCtx ctx;
 };
 
-template <int D, bool KV8>
+template <int D, bool KV8, int NW>
 struct BlocksSmem {
     using M = PageMma<D, KV8>;
     static constexpr int kStage = 2 * M::kPage;
     static constexpr int kStages = KV8 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 4);
     static constexpr int kPages = KV8 ? (D == 128 ? 2 : 4) : (D == 128 ? 1 : 2);  // pages of one pass
-    static constexpr int kRing = kBlWarps * kStages * kStage;
+    static constexpr int kRing = NW * kStages * kStage;
     // a warp's partial result takes its ring's place when its pages are read, four of the CTA's joined rows lie behind each
     static constexpr int kJoined = (M::kSlotFloats * 4 + 127) / 128 * 128;
-    static constexpr int kBytes = 1024 + kRing + kBlWarps * kBlBatch * 16 + (kBlWarps * kStages + 1) * 8 + 16;
+    static constexpr int kBytes = 1024 + kRing + NW * kBlBatch * 16 + (NW * kStages + 1) * 8 + 16;
     static_assert(kStages > kPages, "copies in flight while a pass runs");
-    static_assert(kJoined + 16 / kBlWarps * D * 4 <= kStages * kStage, "a ring holds a partial result and the joined rows");
+    static_assert(NW < 4 || kJoined + 16 / NW * D * 4 <= kStages * kStage, "a ring holds a partial result and the joined rows");
 };
 
 __device__ __forceinline__ void blocks_cluster_sync() {
@@ -65,18 +65,18 @@ __device__ __forceinline__ float2 remote_f2(const float2* p, unsigned rank) {
     return v;
 }
 
-template <int D, bool KV8>
-__global__ void __launch_bounds__(kBlWarps * 32, 3)
+template <int D, bool KV8, int NW>
+__global__ void __launch_bounds__(NW * 32, kBlSmWarps / NW)
     blocks_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ BlocksArgs a) {
-    using L = BlocksSmem<D, KV8>;
+    using L = BlocksSmem<D, KV8, NW>;
     using M = PageMma<D, KV8>;
     constexpr int NP = L::kPages, ST = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     int4* lists = reinterpret_cast<int4*>(smem + L::kRing);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(lists + kBlWarps * kBlBatch);
-    uint64_t* never = bars + kBlWarps * ST;  // nothing arrives on it (time-out test hook)
+    uint64_t* bars = reinterpret_cast<uint64_t*>(lists + NW * kBlBatch);
+    uint64_t* never = bars + NW * ST;  // nothing arrives on it (time-out test hook)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned rank, C;
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kBlWarps * 32, 3)
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
-        for (int i = 0; i < kBlWarps * ST + 1; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < NW * ST + 1; ++i) mbar_init(&bars[i], 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kBlWarps * 32, 3)
     const int gid = lane >> 2;
     const long out_row = (long)row * a.Hq + hk * g + ht * 16;  // of the tile's first head
     const int32_t* sel = a.sel + ((long)row * a.Hkv + hk) * a.keep;
-    const int W = kBlWarps * (int)C, w0 = (int)rank * kBlWarps + warp;
+    const int W = NW * (int)C, w0 = (int)rank * NW + warp;
     int b_next = w0 + lane * W < a.keep ? __ldg(sel + w0 + lane * W) : -1;
     M t;
     {
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kBlWarps * 32, 3)
     auto slot = [&](int i) { return reinterpret_cast<const float*>(smem + i * ST * L::kStage); };
     auto warp_ml = [&](int i, int r) { return reinterpret_cast<const float2*>(slot(i) + 16 * M::kSlotRow)[r]; };
     auto warp_o = [&](int i, int r, int c) { return *reinterpret_cast<const float4*>(slot(i) + r * M::kSlotRow + c * 4); };
-    constexpr int kRowsEach = 16 / kBlWarps;
+    constexpr int kRowsEach = 16 / NW;  // of the CTA's joined rows behind each warp's partial result
     auto mine = [&](int r) {
         return reinterpret_cast<float*>(smem + r / kRowsEach * ST * L::kStage + L::kJoined) + r % kRowsEach * D;
     };
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kBlWarps * 32, 3)
         const int r = i / kCols, c = i % kCols;
         float4 v;
         float mx, sum;
-        join(r, c, kBlWarps, warp_ml, warp_o, v, mx, sum);
+        join(r, c, NW, warp_ml, warp_o, v, mx, sum);
         if (C == 1) {
             if (!*abort_flag) write(r, c, v, mx, sum);
         } else {
@@ -264,22 +264,16 @@ __global__ void __launch_bounds__(kBlWarps * 32, 3)
     blocks_cluster_sync();  // no CTA leaves while another reads its rows
 }
 
-template <int D, bool KV8>
-static fa_status launch_blocks(const void* k_cache, const void* v_cache, const BlocksArgs& a, cudaStream_t s) {
-    using L = BlocksSmem<D, KV8>;
-    CUtensorMap tk, tv;
-    fa_status st = page_maps<D, KV8>(k_cache, v_cache, a.num_blocks, a.Hkv, &tk, &tv);
+template <int D, bool KV8, int NW>
+static fa_status launch_blocks_warps(const CUtensorMap& tk, const CUtensorMap& tv, const BlocksArgs& a, long units, int cluster,
+                                     cudaStream_t s) {
+    using L = BlocksSmem<D, KV8, NW>;
+    auto kernel = blocks_attn_kernel<D, KV8, NW>;
+    const fa_status st = raise_dynamic_smem(reinterpret_cast<const void*>(kernel), L::kBytes);
     if (st != FA_OK) return st;
-    auto kernel = blocks_attn_kernel<D, KV8>;
-    if ((st = raise_dynamic_smem(reinterpret_cast<const void*>(kernel), L::kBytes)) != FA_OK) return st;
-    const long units = (long)a.total_q * a.Hkv * a.head_tiles;
-    // CTAs per list: while they all fit the GPU at once (three a SM) and each warp still gets pages for a pass
-    int cluster = 1;
-    while (cluster < 8 && units * cluster * 2 <= 3L * sm_count() && a.keep >= kBlWarps * cluster * 2 * L::kPages) cluster *= 2;
-    if (units * cluster > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * cluster));
-    cfg.blockDim = dim3(kBlWarps * 32);
+    cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = L::kBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -289,6 +283,24 @@ static fa_status launch_blocks(const void* k_cache, const void* v_cache, const B
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, tk, tv, a));
+}
+
+template <int D, bool KV8>
+static fa_status launch_blocks(const void* k_cache, const void* v_cache, const BlocksArgs& a, cudaStream_t s) {
+    CUtensorMap tk, tv;
+    const fa_status st = page_maps<D, KV8>(k_cache, v_cache, a.num_blocks, a.Hkv, &tk, &tv);
+    if (st != FA_OK) return st;
+    const long units = (long)a.total_q * a.Hkv * a.head_tiles;
+    const long slots = (long)kBlSmWarps * sm_count();
+    // Few lists: four warps and clusters of such CTAs, while they all fit the GPU at once and each warp still gets
+    // pages for a pass.  Many: two warps a list, so that fewer wait for their list's others (512 lists of 64 8-bit
+    // blocks 34.5 us, with four warps 41, with one 49; 8352 of 48 230, 250 and 266; but 160 lists of 256 56, with four
+    // 41).
+    int cluster = 1;
+    while (cluster < 8 && units * cluster * 8 <= slots && a.keep >= 8 * cluster * BlocksSmem<D, KV8, 4>::kPages) cluster *= 2;
+    if (units * cluster > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
+    if (units * 4 > slots) return launch_blocks_warps<D, KV8, 2>(tk, tv, a, units, 1, s);
+    return launch_blocks_warps<D, KV8, 4>(tk, tv, a, units, cluster, s);
 }
 
 }  // namespace fa

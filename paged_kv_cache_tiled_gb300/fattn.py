@@ -191,9 +191,10 @@ def _opt(t, name: str, dtype, shape, dev: int):
 
 def _dims(t, name: str, n: int):
     """The shape of a tensor of n dims."""
-    if not isinstance(t, torch.Tensor) or t.dim() != n:
+    shape = getattr(t, "shape", ())
+    if len(shape) != n or not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor of {n} dims")
-    return t.shape
+    return shape
 
 
 def _empty(shape, dtype, dev: int, stream):
