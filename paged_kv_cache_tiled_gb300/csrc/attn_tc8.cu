@@ -29,7 +29,7 @@ constexpr int kT8Rows = 128;
 constexpr int kT8Units = 4;                     // mailboxes
 constexpr int kT8Readers = 9 + kT8Converters;   // their readers
 constexpr int kT8Scales = 4;                    // tiles whose block scales are kept
-constexpr float kT8Rescale = 8.f;
+constexpr float kT8Rescale = 14.f;  // growth of a maximum that moves it: weights up to 2^14 still fit f16
 
 template <int D>
 struct T8Cfg {
