@@ -49,6 +49,7 @@ struct SelectArgs {
     int32_t* sel;
     int num_seqs, mbps, num_blocks, total_q, Hq, Hkv, keep, recent, sink;
     int g2_log, per;  // rows that a token's heads take in a tile (log2), tokens a tile
+    int many;         // some sequence may have kScWarps tiles or more
     DevCtx ctx;
 };
 
@@ -75,22 +76,25 @@ struct ScoreSmem {
 // g > 16 one token, whose heads come 16 at a time.
 //
 // A place in the run: sequence, kv head, set of tiles, step.  A sequence of four tiles or
-// more has sets of four, each warp a tile; otherwise a set is a tile.
+// more has sets of four, each warp a tile; otherwise (and in a call whose bound on the
+// chunks' lengths leaves room for none) a set is a tile.
 struct ScorePlace {
     SeqItem it;
     int tiles, sets, steps;
     int hk, set, step;
 };
 __device__ __forceinline__ int score_tiles(const SelectArgs& a, int ql) { return (ql + a.per - 1) >> (4 - a.g2_log); }
-__device__ __forceinline__ int score_sets(int tiles) { return tiles >= kScWarps ? (tiles + kScWarps - 1) / kScWarps : tiles; }
+__device__ __forceinline__ int score_sets(const SelectArgs& a, int tiles) {
+    return a.many && tiles >= kScWarps ? (tiles + kScWarps - 1) / kScWarps : tiles;
+}
 __device__ __forceinline__ int score_steps(int cl) { return ((cl - 1) / kScaledBlock + kScBlocks) / kScBlocks; }
 __device__ __forceinline__ long long score_items(const SelectArgs& a, int ql, int cl) {
     if (!lens_ok(ql, cl, a.mbps) || ql == 0 || (cl - 1) / kScaledBlock + 1 <= a.keep) return 0;
-    return (long long)a.Hkv * score_sets(score_tiles(a, ql)) * score_steps(cl);
+    return (long long)a.Hkv * score_sets(a, score_tiles(a, ql)) * score_steps(cl);
 }
 __device__ __forceinline__ void score_enter(const SelectArgs& a, ScorePlace& p) {
     p.tiles = score_tiles(a, p.it.ql);
-    p.sets = score_sets(p.tiles);
+    p.sets = score_sets(a, p.tiles);
     p.steps = score_steps(p.it.cl);
 }
 // (only called while there are items left)
@@ -112,8 +116,8 @@ __device__ __forceinline__ void score_advance(const SelectArgs& a, ScorePlace& p
     score_enter(a, p);
 }
 
-// BIG: groups of more than 16 heads.
-template <int D, bool BIG>
+// BIG: groups of more than 16 heads.  MANY: some sequence may have four tiles.
+template <int D, bool BIG, bool MANY>
 __global__ void __launch_bounds__((kScWarps + 1) * 32, kScCtasPerSm) block_score_kernel(const __grid_constant__ SelectArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     using L = ScoreSmem<D>;
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__((kScWarps + 1) * 32, kScCtasPerSm) block_score
         }
     };
     for (long long i = 0; i < n_items && ok; ++i) {
-        const bool many = p.tiles >= kScWarps;
+        const bool many = MANY && p.tiles >= kScWarps;
         if (i == 0 || p.step == 0) {  // another set
             ti = many ? p.set * kScWarps + warp : p.set;
             t0 = ti * a.per;
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__((kScWarps + 1) * 32, kScCtasPerSm) block_score
                 }
             }
         };
-        if (many) {
+        if (MANY && many) {
 #pragma unroll 1
             for (int bg = b0; bg < min(blocks, b0 + kScBlocks); bg += 16) groups(std::integral_constant<int, 2>{}, bg);
         } else if (b0 + 8 * warp < blocks) {
@@ -784,17 +788,22 @@ fa_status fa_block_select(const void* q, const void* bounds, const int32_t* bloc
     SelectArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(bounds), block_table, ctx_lens, q_lens,
                  reinterpret_cast<float*>(wsb + w.scores), reinterpret_cast<float*>(wsb + w.largest),
                  reinterpret_cast<int32_t*>(wsb + w.near_b), reinterpret_cast<unsigned long long*>(wsb + w.near_key), sel,
-                 num_seqs, max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, keep, recent, sink, 0, 1, {}};
+                 num_seqs, max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, keep, recent, sink, 0, 1, 0, {}};
     while (1 << a.g2_log < Hq / Hkv && a.g2_log < 4) ++a.g2_log;
     a.per = 16 >> a.g2_log;
+    a.many = max_q_len > (kScWarps - 1) * a.per;
     if ((st = make_ctx(&a.ctx)) != FA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int launches = 0;
     if (max_blocks_per_seq > keep) {  // else every block is taken
         const unsigned grid = (unsigned)(kScCtasPerSm * sm_count());
-        const bool big = Hq / Hkv > 16;
-        auto score = d == 128 ? (big ? block_score_kernel<128, true> : block_score_kernel<128, false>)
-                              : (big ? block_score_kernel<64, true> : block_score_kernel<64, false>);
+        auto variant = [&](auto big, auto many) {
+            constexpr bool BIG = decltype(big)::value, MANY = decltype(many)::value;
+            return d == 128 ? block_score_kernel<128, BIG, MANY> : block_score_kernel<64, BIG, MANY>;
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        auto score = Hq / Hkv > 16 ? (a.many ? variant(yes, yes) : variant(yes, no)) : (a.many ? variant(no, yes) : variant(no, no));
         const int smem = d == 128 ? ScoreSmem<128>::kBytes : ScoreSmem<64>::kBytes;
         if ((st = raise_dynamic_smem(reinterpret_cast<const void*>(score), smem)) != FA_OK) return st;
         score<<<grid, (kScWarps + 1) * 32, smem, s>>>(a);

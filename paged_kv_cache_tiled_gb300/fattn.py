@@ -189,6 +189,16 @@ def _opt(t, name: str, dtype, shape, dev: int):
     return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
+def _tensor(t, name: str, dtype, dev: int):
+    """_arg for a tensor that the call takes its sizes from."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _arg(t, name, dtype, getattr(t, "shape", ()), dev)
+
+
 def _dims(t, name: str, n: int):
     """The shape of a tensor of n dims."""
     shape = getattr(t, "shape", ())
@@ -744,11 +754,11 @@ def _cache_shapes(k_cache, v_cache, k_exp, v_exp, dev: int):
     if (k_exp is None) != (v_exp is None):
         raise ValueError("k_exp and v_exp go together")
     if k_exp is None:
-        ptrs = (_arg(k_cache, "k_cache", torch.bfloat16, (nb, Hkv, bs, d), dev),
+        ptrs = (_tensor(k_cache, "k_cache", torch.bfloat16, dev),
                 _arg(v_cache, "v_cache", torch.bfloat16, (nb, Hkv, bs, d), dev), None, None)
     else:
         u8 = torch.uint8
-        ptrs = (_arg(k_cache, "k_cache", u8, (nb, Hkv, bs, d), dev), _arg(v_cache, "v_cache", u8, (nb, Hkv, d, bs), dev),
+        ptrs = (_tensor(k_cache, "k_cache", u8, dev), _arg(v_cache, "v_cache", u8, (nb, Hkv, d, bs), dev),
                 _arg(k_exp, "k_exp", u8, (nb, Hkv), dev), _arg(v_exp, "v_exp", u8, (nb, Hkv), dev))
     return nb, Hkv, bs, d, ptrs
 
@@ -757,7 +767,7 @@ def _batch(block_table, ctx_lens, q_lens, dev: int):
     """Checks a batch's tables: (num_seqs, max_blocks_per_seq, the three addresses)."""
     S, mbps = _dims(block_table, "block_table", 2)
     i32 = torch.int32
-    return S, mbps, (_arg(block_table, "block_table", i32, (S, mbps), dev), _arg(ctx_lens, "ctx_lens", i32, (S,), dev),
+    return S, mbps, (_tensor(block_table, "block_table", i32, dev), _arg(ctx_lens, "ctx_lens", i32, (S,), dev),
                      _arg(q_lens, "q_lens", i32, (S,), dev))
 
 
@@ -790,7 +800,7 @@ def fa_cache_append_fp8_scaled(k, v, k_cache, v_cache, k_exp, v_exp, block_table
     elif q_out is not None:
         raise ValueError("q_out needs q")
     _check(_lib.fa_cache_append_fp8_scaled(
-        _opt(q, "q", dt, (N, Hq, d), dev), _arg(k, "k", dt, (N, Hkv, d), dev), _arg(v, "v", dt, (N, Hkv, d), dev),
+        _opt(q, "q", dt, (N, Hq, d), dev), _tensor(k, "k", dt, dev), _arg(v, "v", dt, (N, Hkv, d), dev),
         _opt(positions, "positions", torch.int32, (N,), dev), _opt(cos_sin, "cos_sin", torch.float32, (max_pos, d), dev),
         max_pos, _opt(q_out, "q_out", bf16, (N, Hq, d), dev), *cache, *tables, S, mbps, nb, N, Hq, Hkv, d, bs,
         FA_F32 if dt is torch.float32 else FA_BF16, _current_stream(stream, dev)), "fa_cache_append_fp8_scaled")
@@ -820,7 +830,7 @@ def fa_paged_attn_fp8_scaled(q, k_cache, v_cache, k_exp, v_exp, block_table, ctx
     need = 0 if ws is not None else fa_paged_attn_fp8_scaled_workspace_size(S, mbps, Hq, Hkv, d, total_q, max_q_len)
     wp, wn, ws = _workspace(ws, need, dev, stream)
     _check(_lib.fa_paged_attn_fp8_scaled(
-        _arg(q, "q", bf16, (total_q, Hq, d), dev), *cache, *tables, _arg(out, "out", bf16, (total_q, Hq, d), dev),
+        _tensor(q, "q", bf16, dev), *cache, *tables, _arg(out, "out", bf16, (total_q, Hq, d), dev),
         _opt(lse, "lse", torch.float32, (total_q, Hq), dev), S, mbps, nb, Hq, Hkv, d, bs, 1 if causal else 0,
         d ** -0.5 if scale is None else float(scale), total_q, max_q_len, wp, wn, _current_stream(stream, dev)),
         "fa_paged_attn_fp8_scaled")
@@ -835,7 +845,7 @@ def fa_block_bounds(k_cache, block_table, ctx_lens, q_lens, bounds, *, total_q: 
     dev, bf16 = _device_of(k_cache, "k_cache"), torch.bfloat16
     S, mbps, tables = _batch(block_table, ctx_lens, q_lens, dev)
     _check(_lib.fa_block_bounds(
-        _arg(k_cache, "k_cache", bf16 if k_exp is None else torch.uint8, (nb, Hkv, bs, d), dev),
+        _tensor(k_cache, "k_cache", bf16 if k_exp is None else torch.uint8, dev),
         _opt(k_exp, "k_exp", torch.uint8, (nb, Hkv), dev), *tables, _arg(bounds, "bounds", bf16, (nb, Hkv, 2, d), dev), S,
         mbps, nb, _int(total_q, "total_q"), Hkv, d, bs, _current_stream(stream, dev)), "fa_block_bounds")
     return bounds
@@ -861,7 +871,7 @@ def fa_block_select(q, bounds, block_table, ctx_lens, q_lens, keep: int, recent:
     need = 0 if ws is not None else fa_block_select_workspace_size(S, mbps, Hq, Hkv, d, total_q)
     wp, wn, ws = _workspace(ws, need, dev, stream)
     _check(_lib.fa_block_select(
-        _arg(q, "q", bf16, (total_q, Hq, d), dev), _arg(bounds, "bounds", bf16, (nb, Hkv, 2, d), dev), *tables,
+        _tensor(q, "q", bf16, dev), _arg(bounds, "bounds", bf16, (nb, Hkv, 2, d), dev), *tables,
         _arg(sel, "sel", torch.int32, (total_q, Hkv, max(keep, 0)), dev), S, mbps, nb, Hq, Hkv, d, 16, keep, recent, sink,
         total_q, max_q_len, wp, wn, _current_stream(stream, dev)), "fa_block_select")
     return sel
@@ -882,7 +892,7 @@ def fa_paged_attn_blocks(q, k_cache, v_cache, block_table, ctx_lens, q_lens, sel
     if out is None:
         out = _empty(q.shape, bf16, dev, stream)
     _check(_lib.fa_paged_attn_blocks(
-        _arg(q, "q", bf16, (total_q, Hq, d), dev), *cache, *tables, _arg(sel, "sel", torch.int32, (total_q, Hkv, keep), dev),
+        _tensor(q, "q", bf16, dev), *cache, *tables, _arg(sel, "sel", torch.int32, (total_q, Hkv, keep), dev),
         keep, _arg(out, "out", bf16, (total_q, Hq, d), dev), _opt(lse, "lse", torch.float32, (total_q, Hq), dev), S, mbps, nb,
         Hq, Hkv, d, bs, d ** -0.5 if scale is None else float(scale), total_q, _current_stream(stream, dev)),
         "fa_paged_attn_blocks")

@@ -125,6 +125,23 @@ def test_select_reports_what_is_inconsistent(F):
     assert bool(((sel >= 0) & (sel < 63)).all())
 
 
+def test_select_time_out_is_reported_and_recoverable(F):
+    for ql in ([1, 1], [60, 9]):
+        table, nb = R.tables([3000, 1000], 94)
+        args = cuda(R.normal(sum(ql), 4, 64, seed=95), boxes(nb, 2, 64, 96), table, R.i32([3000, 1000]), R.i32(ql))
+        want = F.fa_block_select(*args, 12, max_q_len=max(ql))
+        assert F.fa_get_error() == F.FA_OK
+        try:
+            F.fa_debug_set_wait_limit(1_000_000)
+            F.fa_debug_force_timeout(True)
+            F.fa_block_select(*args, 12, max_q_len=max(ql))
+            assert F.fa_get_error() == F.FA_ERR_TIMEOUT
+        finally:
+            F.fa_debug_force_timeout(False)
+            F.fa_debug_set_wait_limit(4_000_000_000)
+        assert torch.equal(F.fa_block_select(*args, 12, max_q_len=max(ql)), want) and F.fa_get_error() == F.FA_OK
+
+
 def test_select_infinite_and_nan_inputs_end(F):
     ctx = [3000]
     table, nb = R.tables(ctx, 91)
@@ -156,11 +173,14 @@ def check_blocks(F, ctx, ql, Hq, H, d, keep, fp8, seed, shuffle=True, sel=None, 
                 b = b if shuffle else b.sort().values
                 at = torch.randperm(keep, generator=g)[:len(b)].sort().values if shuffle else torch.arange(len(b))
                 sel[i, h, at] = b
-    if fp8:  # keys and values behind the last token must not matter
-        for s, c in enumerate(ctx):
-            if c % 16:
-                k[int(table[s, c // 16]), :, c % 16:] = 0x7F
-                v[int(table[s, c // 16]), :, :, c % 16:] = 0x7F
+    for s, c in enumerate(ctx):  # keys and values behind the last token must not matter
+        if c % 16:
+            b = int(table[s, c // 16])
+            k[b, :, c % 16:] = 0x7F if fp8 else float("nan")
+            if fp8:
+                v[b, :, :, c % 16:] = 0x7F
+            else:
+                v[b, :, c % 16:] = float("inf")
     lse = torch.full((N, Hq), 7.0).cuda()
     out = F.fa_paged_attn_blocks(*cuda(q, k, v, table, R.i32(ctx), R.i32(ql), sel), *cuda(ke, ve), lse=lse)
     assert F.fa_get_error() == F.FA_OK
@@ -248,6 +268,58 @@ def test_blocks_time_out_is_reported_and_recoverable(F):
             F.fa_debug_force_timeout(False)
             F.fa_debug_set_wait_limit(4_000_000_000)
         assert torch.equal(F.fa_paged_attn_blocks(*args), want) and F.fa_get_error() == F.FA_OK
+
+
+def test_offsets_past_32_bits(F):
+    """Caches, bounds and scores whose elements need more than 32 bits to number; the sequence's blocks at both ends."""
+    d, H, nb = 128, 8, 270_000  # 2^32 bf16 elements in 262144 blocks
+    kc = torch.empty(nb, H, 16, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    bounds = torch.empty(nb, H, 2, d, dtype=torch.bfloat16, device="cuda")
+    ids = torch.cat([torch.arange(30), torch.arange(nb - 30, nb)])[torch.randperm(60, generator=torch.Generator().manual_seed(1))]
+    k, v = R.normal(60, H, 16, d, seed=2), R.normal(60, H, 16, d, seed=3)
+    kc[ids.cuda()], vc[ids.cuda()] = k.cuda(), v.cuda()
+    table, c = ids.int()[None], 16 * 60 - 5
+    q = R.normal(1, 16, d, seed=4, std=2.0)
+    at = cuda(table, R.i32([c]), R.i32([c]))
+    F.fa_block_bounds(kc, *at, bounds, total_q=c)
+    one = cuda(table, R.i32([c]), R.i32([1]))
+    sel = F.fa_block_select(q.cuda(), bounds, *one, 20, recent=2, sink=1)
+    out = F.fa_paged_attn_blocks(q.cuda(), kc, vc, *one, sel)
+    assert F.fa_get_error() == F.FA_OK
+    want = torch.stack([k[:, :, :, :].amin(2), k.amax(2)], 2)
+    want[59] = torch.stack([k[59, :, :11].amin(1), k[59, :, :11].amax(1)], 1)
+    assert torch.equal(bounds[ids.cuda()].cpu(), want)
+    full = torch.arange(60).int()[None]
+    pick = R.select(q, want, full, [c], [1], 20, 1 + 1, 1)
+    assert torch.equal(sel.cpu(), pick)
+    for h in range(H):
+        b = pick[0, h].long()
+        see = ((b[:, None] * 16 + torch.arange(16)).reshape(1, -1) < c).expand(2, -1)
+        R.Rows(q[0, 2 * h:2 * h + 2], k[b, h].double().reshape(-1, d), v[b, h].double().reshape(-1, d), see, d ** -0.5,
+               R.HALF_BF16).check(out.cpu()[0, 2 * h:2 * h + 2], what=f"head {h}")
+
+
+def test_two_streams_and_equal_bits(F):
+    """Calls side by side on two streams, each with memory of its own, give what they give alone."""
+    d, H, Hq, S = 128, 2, 8, 40
+    lens = [500 + 37 * i for i in range(S)]
+    table, nb = R.tables(lens, 108)
+    k, v, ke, ve = R.random_cache8(nb, H, d, 108, 2)
+    bounds, q = boxes(nb, H, d, 109), R.normal(S, Hq, d, seed=110)
+    args = cuda(q, k, v, ke, ve, bounds, table, R.i32(lens), R.i32([1] * S))
+
+    def step(stream=None):
+        q, k, v, ke, ve, bounds, *at = args
+        sel = F.fa_block_select(q, bounds, *at, 16, recent=2, max_q_len=1, stream=stream)
+        return sel, F.fa_paged_attn_blocks(q, k, v, *at, sel, k_exp=ke, v_exp=ve, stream=stream), \
+            F.fa_paged_attn_fp8_scaled(q, k, v, ke, ve, *at, max_q_len=1, stream=stream)
+    want = step()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [step(s) for _ in range(10) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want)) and F.fa_get_error() == F.FA_OK
 
 
 # ------------------------------------------------------------ as a user would --

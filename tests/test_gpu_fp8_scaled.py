@@ -267,3 +267,62 @@ def test_time_outs_are_reported_and_recoverable(F):
             F.fa_debug_set_wait_limit(4_000_000_000)
         assert torch.equal(F.fa_paged_attn_fp8_scaled(*args, max_q_len=max(ql)), want)
         assert F.fa_get_error() == F.FA_OK
+
+
+def test_a_workspace_for_larger_sizes_serves_smaller_ones(F):
+    """One workspace, several shapes after one another, and two graphs that share it when replayed in turn."""
+    d, H, Hq = 64, 2, 8
+    ws = torch.empty(F.fa_paged_attn_fp8_scaled_workspace_size(6, 200, Hq, H, d, 700, 300), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    runs = []
+    for i, (ctx, ql) in enumerate([([3000], [40]), ([100, 900, 33], [1, 300, 2]), ([50] * 6, [1] * 6)]):
+        table, nb = R.tables(ctx, 120 + i)
+        args = cuda(R.normal(sum(ql), Hq, d, seed=i), *R.random_cache8(nb, H, d, i), table, R.i32(ctx), R.i32(ql))
+        want = F.fa_paged_attn_fp8_scaled(*args, max_q_len=max(ql))
+        assert torch.equal(F.fa_paged_attn_fp8_scaled(*args, max_q_len=max(ql), ws=ws), want)
+        runs.append((args, max(ql), want))
+    graphs = []
+    for args, m, want in runs:
+        out, graph = torch.empty_like(want), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            F.fa_paged_attn_fp8_scaled(*args, max_q_len=m, ws=ws, out=out)
+        graphs.append((graph, out, want))
+    for _ in range(3):
+        for graph, out, want in graphs:
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+    assert F.fa_get_error() == F.FA_OK
+
+
+def test_large_pool_offsets(F):
+    """A pool whose bytes need more than 32 bits to number, the sequence's blocks at both ends of it."""
+    d, H, nb = 128, 8, 270_000  # 2^32 bytes in 262144 blocks
+    kc = torch.empty(nb, H, 16, d, dtype=torch.uint8, device="cuda")
+    vc = torch.empty(nb, H, d, 16, dtype=torch.uint8, device="cuda")
+    ke, ve = (torch.zeros(nb, H, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ids = torch.cat([torch.arange(10), torch.arange(nb - 10, nb)])[torch.randperm(20, generator=torch.Generator().manual_seed(1))]
+    c = 20 * 16 - 3
+    k, v = R.normal(c, H, d, seed=2), R.normal(c, H, d, seed=3)
+    at = cuda(ids.int()[None], R.i32([c]), R.i32([c]))
+    F.fa_cache_append_fp8_scaled(*cuda(k, v), kc, vc, ke, ve, *at)
+    small = [torch.zeros(20, H, 16, d, dtype=torch.uint8), torch.zeros(20, H, d, 16, dtype=torch.uint8),
+             torch.zeros(20, H, dtype=torch.uint8), torch.zeros(20, H, dtype=torch.uint8)]
+    R.append(*small, k.double(), v.double(), torch.arange(20)[None], [c], [c])
+    for got, want in zip((kc, vc, ke, ve), small):
+        got = got[ids.cuda()].cpu()
+        if want.dim() == 4:  # the last block's slots behind the last token are not written
+            part = (slice(None), slice(None), slice(0, 13)) if want.shape[2] == 16 else (slice(None), slice(None), slice(None), slice(0, 13))
+            assert torch.equal(got[:19], want[:19]) and torch.equal(got[19:][part], want[19:][part])
+        else:
+            assert torch.equal(got, want)
+    for n in (1, 100):
+        q = R.normal(n, 16, d, seed=4, std=2.0)
+        out = F.fa_paged_attn_fp8_scaled(q.cuda(), kc, vc, ke, ve, *cuda(ids.int()[None], R.i32([c]), R.i32([n])), max_q_len=n)
+        assert F.fa_get_error() == F.FA_OK
+        see = torch.arange(c)[None] <= torch.arange(c - n, c)[:, None]
+        for h in range(16):
+            kk = R.values(small[0][:, h // 2], small[2][:, h // 2]).reshape(-1, d)[:c]
+            vv = R.values(small[1][:, h // 2], small[3][:, h // 2], True).reshape(-1, d)[:c]
+            R.Rows(q[:, h], kk, vv, see, d ** -0.5, R.HALF_F16).check(out.cpu()[:, h], what=f"head {h}")
