@@ -1,4 +1,5 @@
-// Attention of each query over the cache blocks listed for it (fa_paged_attn_blocks).
+// Attention of each query over the cache blocks listed for it (fa_paged_attn_blocks), and
+// of single tokens over every block of short contexts in the 8-bit cache.
 //
 // One list per (query token, kv head): the Hq / Hkv heads of the group are the rows
 // of m16n8k16 warp MMAs, so that a listed block is read once for all of them.  A CTA
@@ -10,12 +11,12 @@
 // memory.  Nothing passes through device memory and one launch does it all.  Memory
 // bound: 2 * 16 d values a block.
 #include <algorithm>
+#include <climits>
 
 #include "page_mma.cuh"
 
 namespace fa {
 
-constexpr int kBlSmWarps = 12;  // warps that an SM holds, by their registers and rings
 constexpr int kBlBatch = 32;  // list entries that a warp looks up at a time
 
 struct BlocksArgs {
@@ -25,6 +26,7 @@ struct BlocksArgs {
     uint16_t* out;
     float* lse;
     int num_seqs, mbps, num_blocks, total_q, Hq, Hkv, keep, head_tiles;
+    int max_q_len;  // longer chunks are reported
     float scale_log2;
     DevCtx ctx;
 };
@@ -66,7 +68,7 @@ __device__ __forceinline__ float2 remote_f2(const float2* p, unsigned rank) {
 }
 
 template <int D, bool KV8, int NW>
-__global__ void __launch_bounds__(NW * 32, kBlSmWarps / NW)
+__global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     blocks_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ BlocksArgs a) {
     using L = BlocksSmem<D, KV8, NW>;
@@ -96,9 +98,10 @@ __global__ void __launch_bounds__(NW * 32, kBlSmWarps / NW)
     // the first entries and the queries are on their way while the row's sequence is found
     const int gid = lane >> 2;
     const long out_row = (long)row * a.Hq + hk * g + ht * 16;  // of the tile's first head
-    const int32_t* sel = a.sel + ((long)row * a.Hkv + hk) * a.keep;
+    const int32_t* sel = a.sel ? a.sel + ((long)row * a.Hkv + hk) * a.keep : nullptr;  // null: every block of the table
     const int W = NW * (int)C, w0 = (int)rank * NW + warp;
-    int b_next = w0 + lane * W < a.keep ? __ldg(sel + w0 + lane * W) : -1;
+    auto entry = [&](int i) { return i >= a.keep ? -1 : (sel ? __ldg(sel + i) : i); };
+    int b_next = entry(w0 + lane * W);
     M t;
     {
         const uint16_t* q = a.q + out_row * D;
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(NW * 32, kBlSmWarps / NW)
     const bool some = scan.find(a.q_lens, a.ctx_lens, row, count, it);
     // (the whole cluster takes the same way)
     const bool fits = some && lens_ok(it.ql, it.cl, a.mbps);
-    if (blockIdx.x % C == 0 && threadIdx.x == 0 && (!fits || scan.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+    if (blockIdx.x % C == 0 && threadIdx.x == 0 && (!fits || scan.rows != a.total_q || it.ql > a.max_q_len)) raise_error(a.ctx, ERR_BOUNDS_BIT);
     __syncthreads();
     if (!fits) return;
     const int pos = it.cl - it.ql + (int)it.off;
@@ -124,13 +127,13 @@ __global__ void __launch_bounds__(NW * 32, kBlSmWarps / NW)
         // the next 32 entries of this warp: table and scales looked up by a lane each
         int n, place, ks_new = 0, ev_new = 0;
         {
-            const int b = b_next, after = base + (lane + kBlBatch) * W;
-            b_next = after < a.keep ? __ldg(sel + after) : -1;
+            const int b = b_next;
+            b_next = entry(base + (lane + kBlBatch) * W);
             bool use = b >= 0;
             int phys = -1;
             if (use) {
                 if (b > (it.cl - 1) / kScaledBlock) {
-                    raise_error(a.ctx, ERR_BOUNDS_BIT);
+                    if (sel) raise_error(a.ctx, ERR_BOUNDS_BIT);
                     use = false;
                 } else if (b * kScaledBlock > pos) {
                     use = false;  // nothing of it is visible
@@ -291,7 +294,7 @@ static fa_status launch_blocks(const void* k_cache, const void* v_cache, const B
     const fa_status st = page_maps<D, KV8>(k_cache, v_cache, a.num_blocks, a.Hkv, &tk, &tv);
     if (st != FA_OK) return st;
     const long units = (long)a.total_q * a.Hkv * a.head_tiles;
-    const long slots = (long)kBlSmWarps * sm_count();
+    const long slots = (long)kListSmWarps * sm_count();
     // Few lists: four warps and clusters of such CTAs, while they all fit the GPU at once and each warp still gets
     // pages for a pass.  Many: two warps a list, so that fewer wait for their list's others (512 lists of 64 8-bit
     // blocks 34.5 us, with four warps 41, with one 49; 8352 of 48 230, 250 and 266; but 160 lists of 256 56, with four
@@ -301,6 +304,17 @@ static fa_status launch_blocks(const void* k_cache, const void* v_cache, const B
     if (units * cluster > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
     if (units * 4 > slots) return launch_blocks_warps<D, KV8, 2>(tk, tv, a, units, 1, s);
     return launch_blocks_warps<D, KV8, 4>(tk, tv, a, units, cluster, s);
+}
+
+// Single tokens over every block of short tables (fa_paged_attn_fp8_scaled).
+fa_status launch_whole_lists(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_exp, const uint8_t* v_exp,
+                             const int32_t* block_table, const int32_t* ctx_lens, const int32_t* q_lens, void* out, float* lse,
+                             int num_seqs, int mbps, int num_blocks, int Hq, int Hkv, int d, float scale, int total_q,
+                             int max_q_len, cudaStream_t s, const DevCtx& ctx) {
+    const BlocksArgs a{static_cast<const uint16_t*>(q), block_table, ctx_lens, q_lens, nullptr, k_exp, v_exp,
+                       static_cast<uint16_t*>(out), lse, num_seqs, mbps, num_blocks, total_q, Hq, Hkv, mbps,
+                       (Hq / Hkv + 15) / 16, max_q_len, scale * 1.4426950408889634f, ctx};
+    return d == 128 ? launch_blocks<128, true>(k_cache, v_cache, a, s) : launch_blocks<64, true>(k_cache, v_cache, a, s);
 }
 
 }  // namespace fa
@@ -326,7 +340,7 @@ extern "C" fa_status fa_paged_attn_blocks(const void* q, const void* k_cache, co
     if (st != FA_OK) return st;
     BlocksArgs a{static_cast<const uint16_t*>(q), block_table, ctx_lens, q_lens, sel, k_exp, v_exp, static_cast<uint16_t*>(out),
                  lse, num_seqs, max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, keep, (Hq / Hkv + 15) / 16,
-                 scale * 1.4426950408889634f, {}};
+                 INT_MAX, scale * 1.4426950408889634f, {}};
     if ((st = make_ctx(&a.ctx)) != FA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (d == 128) st = k_exp ? launch_blocks<128, true>(k_cache, v_cache, a, s) : launch_blocks<128, false>(k_cache, v_cache, a, s);

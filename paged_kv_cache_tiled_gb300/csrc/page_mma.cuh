@@ -261,6 +261,9 @@ struct PageMma {
     static constexpr int kSlotFloats = 16 * kSlotRow + 32;
 };
 
+// Warps of the kernel for listed blocks that an SM holds, by their registers and rings.
+constexpr int kListSmWarps = 12;
+
 // Tensor maps of the caches as these kernels take them (one box a page; bf16: a half of one).
 template <int D, bool KV8>
 inline fa_status page_maps(const void* k_cache, const void* v_cache, int num_blocks, int Hkv, CUtensorMap* tk, CUtensorMap* tv) {

@@ -60,6 +60,11 @@ fa_status launch_paged_prefill_fp8(const void* q, const void* k_cache, const voi
                                    float* lse, int mbps, int num_blocks, int Hq, int Hkv, int d, int causal, float scale,
                                    int total_q, const int4* pieces, float4* part_o, float2* part_ml, cudaStream_t s,
                                    const DevCtx& ctx);
+// Single tokens over every block of short tables in one launch (blocks_attn.cu).
+fa_status launch_whole_lists(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_exp, const uint8_t* v_exp,
+                             const int32_t* block_table, const int32_t* ctx_lens, const int32_t* q_lens, void* out, float* lse,
+                             int num_seqs, int mbps, int num_blocks, int Hq, int Hkv, int d, float scale, int total_q,
+                             int max_q_len, cudaStream_t s, const DevCtx& ctx);
 // Weight sums of the sequences that take the tensor-core path (attn_colsum.cu).
 fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* block_table, const int32_t* ctx_lens,
                              const int32_t* q_lens, const int32_t* q_start, const int32_t* k_start,
@@ -1688,6 +1693,19 @@ struct ScaledKv {
     const uint8_t *k_exp, *v_exp;
 };
 
+// Does a call over the 8-bit cache take a CTA or a cluster for each (sequence, kv head), in one launch
+// (blocks_attn.cu), instead of the stream and its merge?  Only single tokens, by the longest context that the tables
+// can hold.  Measured at d = 128 (lists and stream, us): 8 pairs, 1000 tokens 8.3 and 12.3, 4000 12.3 and 14.4, 8000
+// both 16.4; 128 pairs, 2000 18.5 and 20.5, 4000 30.7 and 28.7; 512 pairs, 1000 28.8 and 30.6, 2000 53.3 and 49.6;
+// 2400 pairs, 2000 149 and 167.
+static bool whole_lists(int num_seqs, int mbps, int Hkv, int g, int max_q_len) {
+    if (max_q_len != 1) return false;
+    const long lists = (long)num_seqs * Hkv * ((g + 15) / 16), warps = (long)kListSmWarps * sm_count();
+    if (mbps <= 64) return true;
+    if (mbps <= 128) return lists * 8 <= warps || lists >= warps;
+    return mbps <= 256 && (lists * 32 <= warps || lists >= warps);
+}
+
 static fa_status paged_attn_run(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                         const int32_t* ctx_lens, const int32_t* q_lens, void* out, int num_seqs,
                         int max_blocks_per_seq, int num_blocks, int Hq, int Hkv, int d, int block_size, int causal,
@@ -1714,6 +1732,12 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     const int g = Hq / Hkv;
+    if (kv8 && whole_lists(num_seqs, max_blocks_per_seq, Hkv, g, max_q_len)) {
+        st = launch_whole_lists(q, k_cache, v_cache, kv8->k_exp, kv8->v_exp, block_table, ctx_lens, q_lens, out, mod->lse, num_seqs,
+                                max_blocks_per_seq, num_blocks, Hq, Hkv, d, scale, total_q, max_q_len, s, ctx);
+        if (st == FA_OK) set_launch_count(1);
+        return st;
+    }
     int launches = 0;
     const bool decode_path = g <= kDecodeRows;  // some sequences may be decode rows
     const bool tc_path = !is_decode_row(max_q_len, g);

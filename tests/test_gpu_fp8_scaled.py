@@ -224,17 +224,32 @@ def test_many_sequences_short_and_wide_table(F):
     check_attention(F, [30, 2, 500], [1, 2, 1], 4, 2, 128, 51, mbps=3001)
 
 
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("S, Hq, H, longest", [(1, 8, 8, 900), (1, 4, 1, 4000), (3, 40, 2, 2000), (12, 8, 4, 2000), (40, 16, 8, 1000),
+                                               (60, 8, 8, 700), (40, 4, 2, 4090)])
+def test_single_tokens_of_all_batch_sizes(F, d, S, Hq, H, longest):
+    """Batches that take clusters, single CTAs of four and of two warps, and the stream."""
+    g = torch.Generator().manual_seed(S)
+    ctx = [longest] + torch.randint(1, longest + 1, (S - 1,), generator=g).tolist()
+    check_attention(F, ctx, [1] * S, Hq, H, d, 53)
+
+
+def test_single_tokens_and_sequences_without_queries(F):
+    check_attention(F, [100, 0, 64, 900], [1, 0, 0, 1], 4, 2, 128, 54, max_q=1)
+
+
 def test_long_streams_per_warp(F):
     """More pages to a warp than it looks up at a time."""
     check_attention(F, [20000, 15001, 30000], [1, 1, 1], 4, 4, 64, 52, stale_nan=True)
 
 
 def test_a_bound_below_a_chunk_is_reported(F):
-    table, nb = R.tables([50, 60], 3)
-    k, v, ke, ve = R.random_cache8(nb, 2, 64, 3)
-    q = R.normal(6, 4, 64, seed=1)
-    F.fa_paged_attn_fp8_scaled(*cuda(q, k, v, ke, ve, table, R.i32([50, 60]), R.i32([1, 5])), max_q_len=2)
-    assert F.fa_get_error() == F.FA_ERR_BOUNDS
+    for bound, wide in ((2, None), (1, None), (1, 3000)):
+        table, nb = R.tables([50, 60], 3, mbps=wide)
+        k, v, ke, ve = R.random_cache8(nb, 2, 64, 3)
+        q = R.normal(6, 4, 64, seed=1)
+        F.fa_paged_attn_fp8_scaled(*cuda(q, k, v, ke, ve, table, R.i32([50, 60]), R.i32([1, 5])), max_q_len=bound)
+        assert F.fa_get_error() == F.FA_ERR_BOUNDS
 
 
 def test_bad_blocks_are_reported(F):
