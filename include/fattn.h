@@ -577,10 +577,11 @@ fa_status fa_block_bounds(const void* k_cache, const uint8_t* k_exp, const int32
  *            (the scores, 4 bytes for each query, kv head and table entry, and 12
  *            bytes a table entry for each of 1280 CTAs)
  * The choice is that of exact arithmetic: blocks whose scores are too close to tell
- * apart in fp32 are summed again in 64 bits.  Calls that may overlap on the GPU need
- * workspaces of their own.  Sequences with inconsistent lengths record
- * FA_ERR_BOUNDS and their rows are left as they were; a block outside the pool
- * records it and counts as one of bounds 0.
+ * apart in fp32 are summed again in twice its digits (scores within 2^-40 of the sum of
+ * their products' magnitudes, and not equal, may count in either order).  Calls that
+ * may overlap on the GPU need workspaces of their own.  Sequences with inconsistent
+ * lengths record FA_ERR_BOUNDS and their rows are left as they were; a block outside
+ * the pool records it and counts as one of bounds 0.
  */
 size_t fa_block_select_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv, int d,
                                       int total_q);

@@ -349,11 +349,11 @@ __device__ __forceinline__ uint32_t float_key(float x) {  // order-preserving, o
 }
 __device__ __forceinline__ float key_float(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k); }
 
-// An MMA sum differs from the exact one by at most this times sum |products|: 2 (d / 16)
-// steps and the final addition; in a step 16 exact products and the accumulator are
-// aligned to the largest and may each lose what lies below its 24 bits, 17 * 2^-23 < 2^-18
-// of the magnitudes that meet in it.
-__device__ __forceinline__ float sum_slack(int d) { return (float)(d / 8 + 1) * 3.814697265625e-6f; }
+// An MMA sum differs from the exact one by at most this times sum |products|.  q-'s and q+'s
+// products are summed apart, in d / 16 steps each and one addition.  In a step 16 exact products
+// and the sum so far (or 8 and the sum, twice: 18 terms) are aligned to the largest and may each
+// lose what lies below its 24 bits, 2^-23 of the magnitudes that meet in it; the addition rounds once.
+__device__ __forceinline__ float sum_slack(int d) { return (float)(d / 16 * 18 + 1) * 1.1920929e-7f; }
 
 // A number in two fp32 parts, sums of such (Knuth's error-free addition of the first parts), and their order as
 // integers: larger number, larger key; NaN below everything.
@@ -810,8 +810,8 @@ fa_status fa_block_select(const void* q, const void* bounds, const int32_t* bloc
         if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
         ++launches;
     }
-    // few rows: more threads each (128 rows of 1270 scores 17 us with 256 threads, 24 with 128; 1140 rows of 350
-    // 28 us with 256, 24 with 128)
+    // few rows: more threads each (the call with 128 rows of up to 2048 scores 35.0 us, with 256 threads 37.1; with 1140
+    // rows of up to 500 36.7, with 256 threads 41.2)
     const long rows = (long)total_q * Hkv;
     const int threads = rows <= 2L * sm_count() ? kTopFew : kTopMany;
     auto top = threads == kTopFew ? (d == 128 ? block_top_kernel<128, kTopFew> : block_top_kernel<64, kTopFew>)
