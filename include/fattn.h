@@ -486,7 +486,9 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
  *   k, v    [total_q, Hkv, d] in `in_dtype`, sequences packed in order: the last
  *           q_lens[s] tokens of sequence s, which sit at cache positions
  *           ctx_lens[s] - q_lens[s] .. ctx_lens[s] - 1 of its blocks
- *   block_table, ctx_lens, q_lens  as for fa_paged_attn; sum(q_lens) = total_q.
+ *   block_table, ctx_lens, q_lens  as for fa_paged_attn; here and in the calls below
+ *           sum(q_lens) may be less than total_q: rows behind the last sequence's
+ *           are neither read for a result nor written.
  *           A block that new tokens go to must not be listed by another sequence
  *           (fa_pool_* keeps to that: shared blocks are full)
  *   cos_sin fp32 [max_pos, d] or NULL (no rotation), as for fa_cache_append_rope:

@@ -444,12 +444,12 @@ __global__ void __launch_bounds__(kTopThreads, 1024 / kTopThreads) block_top_ker
             sum_q = fmaxf(sum_q, x);
         }
         SeqItem it;
-        auto count = [](int ql, int) { return max(0, ql); };
+        auto count = [](int ql, int) { return ql; };
         const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
         const bool some = scan.find(a.q_lens, a.ctx_lens, at_row, count, it);
         const bool fits = some && lens_ok(it.ql, it.cl, a.mbps) && (long long)it.q0 + it.ql <= a.total_q;
-        if (hk == 0 && tid == 0 && (!fits || scan.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
-        if (!fits) continue;
+        if (hk == 0 && tid == 0 && (some != fits || scan.bad || scan.rows > a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        if (!fits) continue;  // (or a row behind the last sequence)
         int32_t* out = a.sel + row * a.keep;
         const int n = (it.cl - it.ql + (int)it.off) / kScaledBlock + 1;  // blocks that the query sees
         if (n <= a.keep) {

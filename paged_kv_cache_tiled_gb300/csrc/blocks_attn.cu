@@ -109,12 +109,13 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     }
     t.reset();
     SeqItem it;
-    auto count = [](int ql, int) { return max(0, ql); };
+    auto count = [](int ql, int) { return ql; };
     const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
     const bool some = scan.find(a.q_lens, a.ctx_lens, row, count, it);
     // (the whole cluster takes the same way)
     const bool fits = some && lens_ok(it.ql, it.cl, a.mbps);
-    if (blockIdx.x % C == 0 && threadIdx.x == 0 && (!fits || scan.rows != a.total_q || it.ql > a.max_q_len)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+    if (blockIdx.x % C == 0 && threadIdx.x == 0 && (some != fits || scan.bad || scan.rows > a.total_q || (some && it.ql > a.max_q_len)))
+        raise_error(a.ctx, ERR_BOUNDS_BIT);
     __syncthreads();
     if (!fits) return;
     const int pos = it.cl - it.ql + (int)it.off;

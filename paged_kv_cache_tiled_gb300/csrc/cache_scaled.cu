@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append_scaled_kernel(con
         const int part = blockIdx.x % a.parts, place = blockIdx.x / a.parts;
         auto count = [&](int ql, int cl) { return chunk_blocks(ql, cl, a.mbps); };
         const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
-        if (blockIdx.x == 0 && threadIdx.x == 0 && (scan.bad || scan.rows != a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
+        if (blockIdx.x == 0 && threadIdx.x == 0 && (scan.bad || scan.rows > a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
         // (the same for the whole CTA from here on, but for the pairs)
         if (!scan.find(a.q_lens, a.ctx_lens, place, count, it) || (long long)it.q0 + it.ql > a.total_q) return;
         const int first = it.cl - it.ql, blk = first / B + (int)it.off;
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const void* __restric
     SeqItem it;
     auto count = [&](int ql, int cl) { return chunk_blocks(ql, cl, mbps); };
     const SeqScan scan(q_lens, ctx_lens, num_seqs, count);
-    if (w == 0 && lane == 0 && (scan.bad || scan.rows != total_q)) raise_error(ctx, ERR_BOUNDS_BIT);
+    if (w == 0 && lane == 0 && (scan.bad || scan.rows > total_q)) raise_error(ctx, ERR_BOUNDS_BIT);
     if (!scan.find(q_lens, ctx_lens, w / Hkv, count, it)) return;
     const int blk = (it.cl - it.ql) / B + (int)it.off, n = min(B, it.cl - blk * B);
     const int phys = __ldg(bt + (long)it.s * mbps + blk);
