@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kT8Threads, 1)
 
     if (warp == kT8Producer) {
         // ================================================== TMA producer ====
-        int fill = 0, qcnt = 0, tiles = 0;
+        int fill = 0, q_loads = 0, tiles = 0;  // (query loads: slots by turns)
         for (int i = 0; ok; ++i) {
             // the first unit is this CTA's own, then the next in the longest-first order that no CTA has taken
             int v = -1;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kT8Threads, 1)
             const T8Unit U = t8_unit(p, u);
             if (U.kt0 >= U.n_kt) continue;
             for (int s = 0; s < 2 && ok; ++s) {
-                if (!t8_wait_sleepy(&qempty[s], (qcnt & 1) ^ 1, lim_ns, abort_flag)) {
+                if (!t8_wait_sleepy(&qempty[s], ((q_loads >> 1) & 1) ^ 1, lim_ns, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -318,9 +318,9 @@ __global__ void __launch_bounds__(kT8Threads, 1)
                                     pick(U.qtok, s), 0);
                 }
                 __syncwarp();
+                ++q_loads;
             }
             if (!ok) break;
-            ++qcnt;
             // lane j < 8: the tile's j-th block.  Blocks are looked up two tiles ahead, scales one.
             auto load_blk = [&](int kt) -> int {
                 const int lb = kt * 8 + lane;
@@ -379,8 +379,8 @@ __global__ void __launch_bounds__(kT8Threads, 1)
             // let every copy already issued land before the CTA can exit
             for (int f = max(0, fill - G8); f < fill; ++f)
                 (void)mbar_wait_warp(&sfill[f % G8], (f / G8) & 1, 1000000000ull, nullptr);
-            if (qcnt > 0)
-                for (int s = 0; s < 2; ++s) (void)mbar_wait_warp(&qfull[s], (qcnt - 1) & 1, 1000000000ull, nullptr);
+            for (int f = max(0, q_loads - 2); f < q_loads; ++f)
+                (void)mbar_wait_warp(&qfull[f & 1], (f >> 1) & 1, 1000000000ull, nullptr);
         }
     } else if (warp >= kT8Convert) {
         // ===================================================== converters ===
