@@ -3,7 +3,7 @@
 //
 // One list per (query token, kv head): the Hq / Hkv heads of the group are the rows
 // of m16n8k16 warp MMAs, so that a listed block is read once for all of them.  A CTA
-// of two or four warps, or a cluster of up to eight of them when there are few lists,
+// of two to four warps, or a cluster of up to eight of them when there are few lists,
 // takes one list: warp w of W takes entries w, w + W, ..., streams their pages through a
 // ring of its own in shared memory (TMA, the block looked up in the sequence's table)
 // and keeps a softmax of its own; at the end the warps' results are joined with
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     auto slot = [&](int i) { return reinterpret_cast<const float*>(smem + i * ST * L::kStage); };
     auto warp_ml = [&](int i, int r) { return reinterpret_cast<const float2*>(slot(i) + 16 * M::kSlotRow)[r]; };
     auto warp_o = [&](int i, int r, int c) { return *reinterpret_cast<const float4*>(slot(i) + r * M::kSlotRow + c * 4); };
-    constexpr int kRowsEach = 16 / NW;  // of the CTA's joined rows behind each warp's partial result
+    constexpr int kRowsEach = (16 + NW - 1) / NW;  // of the CTA's joined rows behind each warp's partial result
     auto mine = [&](int r) {
         return reinterpret_cast<float*>(smem + r / kRowsEach * ST * L::kStage + L::kJoined) + r % kRowsEach * D;
     };
@@ -297,13 +297,14 @@ static fa_status launch_blocks(const void* k_cache, const void* v_cache, const B
     const long units = (long)a.total_q * a.Hkv * a.head_tiles;
     const long slots = (long)kListSmWarps * sm_count();
     // Few lists: four warps and clusters of such CTAs, while they all fit the GPU at once and each warp still gets
-    // pages for a pass.  Many: two warps a list, so that fewer wait for their list's others (512 lists of 64 8-bit
-    // blocks 34.5 us, with four warps 41, with one 49; 8352 of 48 230, 250 and 266; but 160 lists of 256 56, with four
-    // 41).
+    // pages for a pass (160 lists of 256: 41 us, with two warps 56).  More: three warps while all lists fit at once
+    // (518 bf16 lists of 48 22.7 us, with two 26.7; 512 8-bit ones of 64 32.8, with two 34.3, with four 41, with one 49).
+    // Many: two warps, so that fewer wait for their list's others (8352 lists of 48 230 us, with one 250, with four 266).
     int cluster = 1;
     while (cluster < 8 && units * cluster * 8 <= slots && a.keep >= 8 * cluster * BlocksSmem<D, KV8, 4>::kPages) cluster *= 2;
     if (units * cluster > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
-    if (units * 4 > slots) return launch_blocks_warps<D, KV8, 2>(tk, tv, a, units, 1, s);
+    if (units * 3 > slots) return launch_blocks_warps<D, KV8, 2>(tk, tv, a, units, 1, s);
+    if (units * 4 > slots) return launch_blocks_warps<D, KV8, 3>(tk, tv, a, units, 1, s);
     return launch_blocks_warps<D, KV8, 4>(tk, tv, a, units, cluster, s);
 }
 

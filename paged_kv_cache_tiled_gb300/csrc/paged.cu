@@ -1695,9 +1695,13 @@ struct ScaledKv {
 
 // Does a call over the 8-bit cache take a CTA or a cluster for each (sequence, kv head), in one launch
 // (blocks_attn.cu), instead of the stream and its merge?  Only single tokens, by the longest context that the tables
-// can hold.  Measured at d = 128 (lists and stream, us): 8 pairs, 1000 tokens 8.3 and 12.3, 4000 12.3 and 14.4, 8000
-// both 16.4; 128 pairs, 2000 18.5 and 20.5, 4000 30.7 and 28.7; 512 pairs, 1000 28.8 and 30.6, 2000 53.3 and 49.6;
-// 2400 pairs, 2000 149 and 167.
+// can hold.  Measured at d = 128 (lists and stream, us; tables as long as the longest context; all sequences that long,
+// a quarter of it and more, one that long and the others an eighth of it at most):
+//   8 pairs, 4000 tokens     12.3 14.9   12.3 15.3   12.3 14.5
+//   128 pairs, 2000          20.5 23.0   20.5 22.5   16.4 16.4;  4000  34.6 38.9   30.7 30.7   26.6 18.4
+//   512 pairs, 1000          31.1 41.0   24.6 28.8   20.5 16.4;  2000  50.0 62.8   46.5 47.2   32.8 20.5
+//   2400 pairs, 2000          201 239     151 168    61.7 51.2;  4000   380 445     290 300     108 72
+// The lists win by a fifth at most, and lose more the longer a single context can be: they are taken while that is short.
 static bool whole_lists(int num_seqs, int mbps, int Hkv, int g, int max_q_len) {
     if (max_q_len != 1) return false;
     const long lists = (long)num_seqs * Hkv * ((g + 15) / 16), warps = (long)kListSmWarps * sm_count();

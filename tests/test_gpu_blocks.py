@@ -211,6 +211,14 @@ def test_blocks_chunks(F, fp8, d, Hq, H):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("n, Hq, H", [(550, 3, 1), (275, 20, 1), (325, 4, 2)])
+def test_blocks_of_several_hundred_lists(F, fp8, d, n, Hq, H):
+    """About as many lists as the GPU takes at once, with three warps each and with two."""
+    check_blocks(F, [n + 150], [n], Hq, H, d, 10, fp8, 108)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_blocks_rows_without_keys(F, fp8):
     """Lists of nothing, and of blocks behind the position only."""
     sel = torch.full((3, 2, 6), -1, dtype=torch.int32)
