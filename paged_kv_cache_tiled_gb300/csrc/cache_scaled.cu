@@ -31,8 +31,7 @@ struct AppendArgs {
     uint8_t *kc, *vc, *ke, *ve;
     const int32_t *bt, *ctx_lens, *q_lens;
     int max_pos, num_seqs, mbps, num_blocks, total_q, Hq, Hkv;
-    int parts, block_ctas;  // CTAs a block, and of all blocks; those of the queries follow
-    int tokens;       // query tokens a warp
+    int pairs, parts, block_ctas;  // (head, K or V) pairs a CTA, CTAs a block, and of all blocks; those of the queries follow
     DevCtx ctx;
 };
 
@@ -91,12 +90,14 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float ratio) {
     return f32x4_to_e4m3x4(x[0], x[1], x[2], x[3]);
 }
 
-// A CTA takes a block that new tokens go to, or half of its heads when there are many: kPart
-// (head, K or V) pairs, even warps keys, odd warps values.
-constexpr int kAppendWarps = 4, kPart = 2 * kAppendWarps;
+// A CTA takes a block that new tokens go to, or a part of its heads: one (head, K or V) pair a warp, two when there
+// are many blocks; even warps keys, odd warps values.  Prompts need bytes in flight, so no register holds a value that
+// can be worked out again and an SM has seven CTAs (with four and all values kept 5123 tokens of 8 heads took 32.9 us, now
+// 26.6; 1117 tokens with two pairs a warp 14.4, with one 10.3).
+constexpr int kAppendWarps = 4;
 
 template <int D, bool kF32>
-__global__ void __launch_bounds__(kAppendWarps * 32, 4) append_scaled_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendWarps * 32, kF32 ? 4 : 7) append_scaled_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int N = D / 32, B = kScaledBlock;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     SeqItem it;
@@ -120,8 +121,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append_scaled_kernel(con
             for (int i = 0; i < B; ++i)
                 if (i >= lo && i < hi) raw[i].load(is_v ? a.v : a.k, at + (long)i * a.Hkv * D);
         };
-        const int end = min(2 * a.Hkv, (part + 1) * kPart);
-        int pair = part * kPart + warp;
+        const int end = min(2 * a.Hkv, (part + 1) * a.pairs);
+        int pair = part * a.pairs + warp;
         if (pair < end) load(pair);
         unsigned live = ((1u << hi) - 1) & ~((1u << lo) - 1);
         if (a.cos_sin) {
@@ -152,25 +153,28 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append_scaled_kernel(con
             uint8_t* page = (is_v ? a.vc : a.kc) + head * B * D;
             uint8_t* exps = is_v ? a.ve : a.ke;
             const int e_old = lo > 0 ? (int)exps[head] : 0;
-            // token by token: values turned, and the largest finite magnitude
-            float x[B][N], m = 0.f;
+            // token i's values, turned (worked out twice: registers for all of them would halve the loads in flight)
+            auto values = [&](int i, float (&x)[N]) {
 #pragma unroll
-            for (int i = 0; i < B; ++i) {
-                if (!((live >> i) & 1u)) continue;  // (the same for the whole warp)
-#pragma unroll
-                for (int c = 0; c < N; ++c) x[i][c] = raw[i].get(c);
+                for (int c = 0; c < N; ++c) x[c] = raw[i].get(c);
                 if (turned) {
 #pragma unroll
                     for (int c = 0; c < N; ++c) {
-                        const float y = __shfl_xor_sync(0xffffffffu, x[i][c], 16);
+                        const float y = __shfl_xor_sync(0xffffffffu, x[c], 16);
                         const float co = turns[i][at_pair + c], ys = y * turns[i][D / 2 + at_pair + c];
-                        x[i][c] = fmaf(x[i][c], co, lane < 16 ? -ys : ys);
+                        x[c] = fmaf(x[c], co, lane < 16 ? -ys : ys);
                     }
                 }
+            };
+            float m = 0.f;  // the largest finite magnitude
 #pragma unroll
-                for (int c = 0; c < N; ++c) m = fabsf(x[i][c]) < INFINITY ? fmaxf(m, fabsf(x[i][c])) : m;
+            for (int i = 0; i < B; ++i) {
+                if (!((live >> i) & 1u)) continue;  // (the same for the whole warp)
+                float x[N];
+                values(i, x);
+#pragma unroll
+                for (int c = 0; c < N; ++c) m = fabsf(x[c]) < INFINITY ? fmaxf(m, fabsf(x[c])) : m;
             }
-            if (pair + kAppendWarps < end) load(pair + kAppendWarps);
             // the smallest code whose 448 (1.75 * 2^8) times the scale reaches it
             const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
             const int e = max(max(e_old, kExpLeast), (int)(mb >> 23) - 8 + ((mb & 0x7FFFFFu) > 0x600000u ? 1 : 0));
@@ -191,9 +195,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append_scaled_kernel(con
 #pragma unroll
                 for (int i = 0; i < B; ++i) {
                     if (!((live >> i) & 1u)) continue;
-                    const uint32_t lo2 = f32x2_to_e4m3x2(x[i][0] * inv, x[i][1] * inv);
+                    float x[N];
+                    values(i, x);
+                    const uint32_t lo2 = f32x2_to_e4m3x2(x[0] * inv, x[1] * inv);
                     if constexpr (N == 4)
-                        *reinterpret_cast<uint32_t*>(at + i * D) = lo2 | f32x2_to_e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16;
+                        *reinterpret_cast<uint32_t*>(at + i * D) = lo2 | f32x2_to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
                     else
                         *reinterpret_cast<uint16_t*>(at + i * D) = (uint16_t)lo2;
                 }
@@ -213,24 +219,24 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append_scaled_kernel(con
                             o[w] = (o[w] & ~mask) | (rescale_codes(o[w], ratio) & mask);
                         }
                         const uint32_t mask = bytes((live >> (4 * w)) & 15u);
-                        o[w] = (o[w] & ~mask) | (f32x4_to_e4m3x4(x[4 * w][c] * inv, x[4 * w + 1][c] * inv, x[4 * w + 2][c] * inv,
-                                                                 x[4 * w + 3][c] * inv) & mask);
+                        o[w] = (o[w] & ~mask) | (f32x4_to_e4m3x4(raw[4 * w].get(c) * inv, raw[4 * w + 1].get(c) * inv,
+                                                                 raw[4 * w + 2].get(c) * inv, raw[4 * w + 3].get(c) * inv) & mask);
                     }
                     at[c] = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             if (lane == 0) exps[head] = (uint8_t)e;
+            if (pair + kAppendWarps < end) load(pair + kAppendWarps);
         }
         return;
     }
-    const int w = ((int)blockIdx.x - a.block_ctas) * kAppendWarps + warp;
-    // query tokens, `tokens` a warp: D / 16 lanes a head, 8 channel pairs each
-    const int row0 = w * a.tokens, row1 = min(a.total_q, row0 + a.tokens);
-    if (row0 >= row1 || !a.q) return;
+    // a query token a warp: D / 16 lanes a head, 8 channel pairs each
+    const int row = ((int)blockIdx.x - a.block_ctas) * kAppendWarps + warp;
+    if (row >= a.total_q || !a.q) return;
     constexpr int kLanes = D / 16, kHeads = 32 / kLanes, kAhead = 4;
     const int c = (lane % kLanes) * 8, h0 = lane / kLanes;
     Raw8<kF32> x[kAhead], y[kAhead];
-    auto load = [&](int row, int h) {
+    auto load = [&](int h) {
         const long base = (long)row * a.Hq * D + c;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
@@ -239,39 +245,33 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append_scaled_kernel(con
                 y[k].load(a.q, base + (long)(h + k * kHeads) * D + D / 2);
             }
     };
-    load(row0, h0);  // on their way while the token's sequence is found
+    load(h0);  // on their way while the token's sequence is found
     auto count = [](int ql, int) { return max(0, ql); };
     const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
-    long long end = 0;  // first row behind the sequence found
-    for (int row = row0; row < row1; ++row) {
-        if (row >= end) {
-            if (!scan.find(a.q_lens, a.ctx_lens, row, count, it)) return;
-            end = (long long)it.q0 + it.ql;
-        }
-        const int pos = a.positions ? __ldg(a.positions + row) : it.cl - it.ql + (row - it.q0);
-        const bool fits = lens_ok(it.ql, it.cl, a.mbps), in = pos >= 0 && pos < a.max_pos;  // (lengths are reported above)
-        if (fits && !in && lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
-        if (fits && in) {
-            Raw8<true> co, si;
-            co.load(a.cos_sin, (long)pos * D + c);
-            si.load(a.cos_sin, (long)pos * D + D / 2 + c);
-            for (int h = h0; h < a.Hq; h += kAhead * kHeads) {
-                if (h != h0 || row != row0) load(row, h);
+    if (!scan.find(a.q_lens, a.ctx_lens, row, count, it)) return;
+    const int pos = a.positions ? __ldg(a.positions + row) : it.cl - it.ql + (row - it.q0);
+    const bool fits = lens_ok(it.ql, it.cl, a.mbps), in = pos >= 0 && pos < a.max_pos;  // (lengths are reported above)
+    if (fits && !in && lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
+    if (fits && in) {
+        Raw8<true> co, si;
+        co.load(a.cos_sin, (long)pos * D + c);
+        si.load(a.cos_sin, (long)pos * D + D / 2 + c);
+        for (int h = h0; h < a.Hq; h += kAhead * kHeads) {
+            if (h != h0) load(h);
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    if (h + k * kHeads >= a.Hq) break;
-                    const long at = ((long)row * a.Hq + h + k * kHeads) * D + c;
-                    float u[8], v[8];
+            for (int k = 0; k < kAhead; ++k) {
+                if (h + k * kHeads >= a.Hq) break;
+                const long at = ((long)row * a.Hq + h + k * kHeads) * D + c;
+                float u[8], v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        u[i] = fmaf(x[k].get(i), co.get(i), -(y[k].get(i) * si.get(i)));
-                        v[i] = fmaf(y[k].get(i), co.get(i), x[k].get(i) * si.get(i));
-                    }
-                    *reinterpret_cast<uint4*>(a.q_out + at) =
-                        make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
-                    *reinterpret_cast<uint4*>(a.q_out + at + D / 2) =
-                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                for (int i = 0; i < 8; ++i) {
+                    u[i] = fmaf(x[k].get(i), co.get(i), -(y[k].get(i) * si.get(i)));
+                    v[i] = fmaf(y[k].get(i), co.get(i), x[k].get(i) * si.get(i));
                 }
+                *reinterpret_cast<uint4*>(a.q_out + at) =
+                    make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+                *reinterpret_cast<uint4*>(a.q_out + at + D / 2) =
+                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
             }
         }
     }
@@ -388,13 +388,13 @@ fa_status fa_cache_append_fp8_scaled(const void* q, const void* k, const void* v
     if (st != FA_OK) return st;
     AppendArgs a{q, k, v, positions, cos_sin, static_cast<uint16_t*>(q_out), static_cast<uint8_t*>(k_cache),
                  static_cast<uint8_t*>(v_cache), k_exp, v_exp, block_table, ctx_lens, q_lens, max_pos, num_seqs,
-                 max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, 1, 0, 1, {}};
+                 max_blocks_per_seq, num_blocks, total_q, Hq, Hkv, kAppendWarps, 1, 0, {}};
     if ((st = make_ctx(&a.ctx)) != FA_OK) return st;
-    a.parts = (2 * Hkv + kPart - 1) / kPart;
-    const long block_ctas = chunk_blocks_bound(num_seqs, total_q) * a.parts;
-    // (with more tokens than the GPU holds warps, two share a warp's search for their sequence)
-    a.tokens = total_q > 20 * sm_count() ? 2 : 1;
-    const long q_warps = q ? (total_q + a.tokens - 1) / a.tokens : 0, ctas = block_ctas + (q_warps + kAppendWarps - 1) / kAppendWarps;
+    const long blocks = chunk_blocks_bound(num_seqs, total_q);
+    // (more CTAs than the GPU holds at once: two pairs a warp, which share a CTA's search and its rows of cos_sin)
+    if (blocks * ((2 * Hkv + kAppendWarps - 1) / kAppendWarps) > 7L * sm_count()) a.pairs = 2 * kAppendWarps;
+    a.parts = (2 * Hkv + a.pairs - 1) / a.pairs;
+    const long block_ctas = blocks * a.parts, ctas = block_ctas + (q ? (total_q + kAppendWarps - 1) / kAppendWarps : 0);
     if (ctas > 0x7fffffffL) return FA_ERR_UNSUPPORTED;
     a.block_ctas = (int)block_ctas;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
