@@ -45,6 +45,27 @@ def test_bounds(F, fp8, d, H, ctx, ql):
     assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [128, 64])
+def test_bounds_pass_over_nan(F, fp8, d):
+    table, nb = R.tables([40], 63)
+    k, _, e, _ = R.random_cache8(nb, 1, d, 63, 20) if fp8 else (R.normal(nb, 1, 16, d, seed=63), None, None, None)
+    vals = R.values(k, e) if fp8 else k.double()
+    lost = torch.rand(k.shape, generator=torch.Generator().manual_seed(64)) < 0.3
+    lost[:, :, 0] = False  # (a channel keeps a number)
+    k[lost] = 0xFF if fp8 else float("nan")
+    bounds = torch.zeros(nb, 1, 2, d, dtype=torch.bfloat16)
+    want = bounds.clone()
+    for b in range(3):
+        p, n = int(table[0, b]), min(16, 40 - 16 * b)
+        page, no = vals[p, :, :n], lost[p, :, :n]
+        want[p] = torch.stack([page.masked_fill(no, 1e300).amin(1), page.masked_fill(no, -1e300).amax(1)], 1).bfloat16()
+    got = bounds.cuda()
+    F.fa_block_bounds(k.cuda(), *cuda(table, R.i32([40]), R.i32([40])), got, k_exp=None if e is None else e.cuda(), total_q=40)
+    assert F.fa_get_error() == F.FA_OK
+    assert torch.equal(got.cpu(), want)
+
+
 # ------------------------------------------------------------------ select --
 def boxes(nb, H, d, seed):
     mid, wide = R.normal(nb, H, d, seed=seed).float(), R.normal(nb, H, d, seed=seed + 1).float().abs() + 0.5
