@@ -328,7 +328,10 @@ fa_status fa_paged_attn_fp8(const void* q, const void* k_cache, const void* v_ca
  *   ctx_lens     int32 [num_seqs]: tokens of sequence s in the cache, the new
  *                chunk included (its queries sit at ctx - q_len .. ctx - 1)
  *   q_lens       int32 [num_seqs], 0 <= q_lens[s] <= ctx_lens[s];
- *                sum(q_lens) must equal total_q
+ *                sum(q_lens) must equal total_q.  A sequence whose lengths do not
+ *                fit, or whose rows do not all lie in total_q, records
+ *                FA_ERR_BOUNDS and its rows are left as they were (a negative
+ *                length counts as no rows)
  *   out          bf16 [total_q, Hq, d], 32-byte aligned
  *   max_q_len    host-side upper bound on every q_lens[s] (total_q is always
  *                a valid bound); used to skip launching a kernel that would

@@ -137,7 +137,7 @@ struct TcParams {
     const int32_t* q_start;
     const int32_t* work_list;
     const int32_t* work_count;
-    int mbps, num_blocks;
+    int mbps, num_blocks, total_q;
     // modified variants
     const int4* pieces;  // paged: (sequence, first query token, first | end << 16 of its KV tiles, place of its partial results or -1)
     float4* part_o;      // partial results: [d / 4][256 rows] each
@@ -240,7 +240,9 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
             piece.y = __ldg(p.work_list + 2 * e + 1);
         }
         const int seq = piece.x, t0 = piece.y;
-        const int ql = __ldg(p.q_lens + seq), cl = __ldg(p.ctx_lens + seq), qs = __ldg(p.q_start + seq);
+        const int ql = __ldg(p.q_lens + seq), cl = __ldg(p.ctx_lens + seq);
+        int qs = __ldg(p.q_start + seq), rows = ql;
+        if (!rows_fit(qs, ql, p.total_q)) qs = rows = 0;  // (reported by the metadata kernel; nothing is written)
         U.b = seq;
         int slot_tokens = kTcRows;
         if (p.pack) {  // all heads of kv head `rest`'s group, two blocks of 128/g tokens
@@ -263,7 +265,7 @@ __device__ __forceinline__ Unit decode_unit(const TcParams& p, int u) {
         int last = 0;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            U.nrows[s] = max(0, min(slot_tokens, ql - U.row0[s]));  // query tokens of the slot
+            U.nrows[s] = max(0, min(slot_tokens, rows - U.row0[s]));  // query tokens of the slot
             U.qtok[s] = qs + U.row0[s];
             if (U.nrows[s] > 0) last = max(last, U.row0[s] + U.nrows[s]);
         }
@@ -1786,6 +1788,7 @@ fa_status launch_paged_prefill(const void* q, const void* k_cache, const void* v
     p.work_count = work_count;
     p.mbps = mbps;
     p.num_blocks = num_blocks;
+    p.total_q = total_q;
     if (mod) {
         p.mod = *mod;
         p.lse = mod->lse;

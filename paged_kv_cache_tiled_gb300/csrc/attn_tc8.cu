@@ -46,7 +46,7 @@ struct T8Cfg {
 static_assert(T8Cfg<128>::kSmem <= 227 * 1024, "shared memory of a CTA");
 
 struct T8Params {
-    int Hq, Hkv, g, causal, pair_heads, pack, pack_shift, per_rank, per_head, mbps, num_blocks;
+    int Hq, Hkv, g, causal, pair_heads, pack, pack_shift, per_rank, per_head, mbps, num_blocks, total_q;
     FastDiv div_rank, div_head;
     float scale_log2;
     uint16_t* out;
@@ -70,7 +70,9 @@ __device__ __forceinline__ T8Unit t8_unit(const T8Params& p, int u) {
     T8Unit U;
     const int e = p.div_rank(u), rest = u - e * p.per_rank;
     const int4 piece = __ldg(p.pieces + e);
-    const int ql = __ldg(p.q_lens + piece.x), cl = __ldg(p.ctx_lens + piece.x), qs = __ldg(p.q_start + piece.x);
+    const int ql = __ldg(p.q_lens + piece.x), cl = __ldg(p.ctx_lens + piece.x);
+    int qs = __ldg(p.q_start + piece.x), rows = ql;
+    if (!rows_fit(qs, ql, p.total_q)) qs = rows = 0;  // (reported by the metadata kernel; nothing is written)
     U.seq = piece.x;
     int tokens = kT8Rows;
     if (p.pack) {  // 128 / g tokens x the heads of kv head `rest`'s group
@@ -92,7 +94,7 @@ __device__ __forceinline__ T8Unit t8_unit(const T8Params& p, int u) {
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        U.nrows[s] = max(0, min(tokens, ql - U.row0[s]));
+        U.nrows[s] = max(0, min(tokens, rows - U.row0[s]));
         U.qtok[s] = qs + U.row0[s];
     }
     U.kv_len = cl;
@@ -809,6 +811,7 @@ fa_status launch_paged_prefill_fp8(const void* q, const void* k_cache, const voi
     p.div_head = FastDiv(p.per_head);
     p.mbps = mbps;
     p.num_blocks = num_blocks;
+    p.total_q = total_q;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
     const bool some = scan.find(a.q_lens, a.ctx_lens, row, count, it);
     // (the whole cluster takes the same way)
-    const bool fits = some && lens_ok(it.ql, it.cl, a.mbps);
+    const bool fits = some && lens_ok(it.ql, it.cl, a.mbps) && (long long)it.q0 + it.ql <= a.total_q;
     if (blockIdx.x % C == 0 && threadIdx.x == 0 && (some != fits || scan.bad || scan.rows > a.total_q || (some && it.ql > a.max_q_len)))
         raise_error(a.ctx, ERR_BOUNDS_BIT);
     __syncthreads();

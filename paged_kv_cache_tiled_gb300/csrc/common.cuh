@@ -31,6 +31,9 @@ __host__ __device__ inline int paged_tc_entry_tokens(int g) {
     return paged_tc_pack(g) ? 2 * (128 / g) : (g % 2 == 0 ? 128 : 256);
 }
 
+// Do the rows [q0, q0 + q_len) of a sequence lie in a call's total_q?  (Neither q0 nor q_len negative.)
+__host__ __device__ inline bool rows_fit(int q0, int q_len, int total_q) { return q_len <= total_q - q0; }
+
 // ---------------------------------------------------------------- errors ---
 // Bits of the per-device error word.
 enum : unsigned { ERR_BOUNDS_BIT = 1u, ERR_TIMEOUT_BIT = 2u };

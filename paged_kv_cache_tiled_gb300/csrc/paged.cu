@@ -75,6 +75,11 @@ fa_status launch_accum_chunk(const void* q, const void* k_cache, const int32_t* 
 
 __host__ __device__ inline bool is_decode_row(int q_len, int g) { return q_len >= 1 && g * q_len <= kDecodeRows; }
 
+// Rows of a batch: sequence s has max(0, q_lens[s]) of them behind those of the sequences
+// before it (q0, at most INT_MAX).  A sequence whose rows do not all lie in the call's
+// total_q, as after lengths that are wrong, is reported (with the negative lengths) by the
+// merge or the metadata kernel, and nothing of it is read from q or written.
+
 // ------------------------------------------------------------------ layout --
 constexpr int kStreamWarps = 8;      // page streams per decode CTA
 constexpr int kMaxStreamCtas = 160;  // decode grid cap (one CTA per SM); sizes the partial slots
@@ -221,8 +226,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
                         const int32_t* __restrict__ ctx_lens, const int32_t* __restrict__ q_lens,
                         uint16_t* __restrict__ out, float* __restrict__ part_o, float2* __restrict__ part_ml,
                         int num_seqs, int mbps, int num_blocks, int Hq, int Hkv, int q_prefetch_rows, int causal,
-                        float scale_log2, float v_scale, DevCtx ctx, ScoreMod mod, const uint8_t* __restrict__ k_exp,
-                        const uint8_t* __restrict__ v_exp) {
+                        float scale_log2, float v_scale, int total_q, DevCtx ctx, ScoreMod mod,
+                        const uint8_t* __restrict__ k_exp, const uint8_t* __restrict__ v_exp) {
     constexpr bool KV8 = KV != KV_BF16, SCALED = KV == KV_FP8_SCALED;
     static_assert(MOD == 0 || !KV8, "score modifiers are built for the bf16 cache");
     const int window = MOD ? mod.window : 0;
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     long long my_p = 0, my_q = 0;
     bool bad = false;
     auto count = [&](int ql, int cl) {
-        my_q += ql;
+        my_q += max(0, ql);
         if (!is_decode_row(ql, g)) return;
         if (ql > cl || cl > mbps * kBS) {
             bad = true;
@@ -338,11 +343,11 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
                 if (off < n) {
                     a_s = s;
                     a_off = (int)off;
-                    a_q0 = (int)q0;
+                    a_q0 = (int)min(q0, 0x7fffffffll);
                     break;
                 }
                 off -= n;
-                q0 += ql;
+                q0 += max(0, ql);
             }
         }
         start.s = __shfl_sync(0xffffffffu, a_s, src);
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         if (++c.hk < Hkv) return;
         c.hk = 0;
         do {
-            c.q0 += __ldg(q_lens + c.s);
+            c.q0 = (int)min((unsigned)c.q0 + (unsigned)max(0, __ldg(q_lens + c.s)), 0x7fffffffu);
             ++c.s;
             c.nblk = c.s < num_seqs ? decode_blocks(q_lens, ctx_lens, c.s, g, mbps, window) : 0;
         } while (c.s < num_seqs && c.nblk == 0);
@@ -498,7 +503,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         seg_last_first = seg_first;
         ctx_len = __ldg(ctx_lens + cc.s);
         q_len = __ldg(q_lens + cc.s);
-        nrows = g * q_len;
+        nrows = rows_fit(cc.q0, q_len, total_q) ? g * q_len : 0;  // (else none is read or written)
         seg_last_rows = nrows;
         if (first_rows < 0) first_rows = nrows;
         const int rr[2] = {gid, gid + 8};
@@ -966,7 +971,7 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
                                                                     const float* part_o, const float2* part_ml,
                                                                     uint16_t* __restrict__ out, int num_seqs,
                                                                     int Hq, int Hkv, int mbps, int W, int max_q_len,
-                                                                    DevCtx ctx, ScoreMod mod) {
+                                                                    int total_q, DevCtx ctx, ScoreMod mod) {
     // (the weight sums that may follow wait for this grid's end before they read)
     if constexpr (MOD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int window = MOD ? mod.window : 0;
@@ -974,7 +979,7 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
     const int s = blockIdx.x, hk = blockIdx.y, r = threadIdx.x >> 5, g = Hq / Hkv;
     const int lane = threadIdx.x & 31;
     const int ql_s = __ldg(q_lens + s), cl_s = __ldg(ctx_lens + s);
-    if (ql_s > max_q_len && hk == 0 && threadIdx.x == 0) raise_error(ctx, ERR_BOUNDS_BIT);
+    if ((ql_s > max_q_len || ql_s < 0) && hk == 0 && threadIdx.x == 0) raise_error(ctx, ERR_BOUNDS_BIT);
     const bool mine = is_decode_row(ql_s, g) && ql_s <= cl_s && cl_s <= mbps * kBS && r < g * ql_s;
     if (!mine) {
         // every CTA waits for the decode grid, so this grid never completes ahead of it
@@ -992,7 +997,7 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
         tot += n;
         if (i < s) {
             pre += n;
-            q0 += ql;
+            q0 += max(0, ql);
         }
     }
 #pragma unroll
@@ -1001,6 +1006,8 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
         pre += __shfl_xor_sync(0xffffffffu, pre, o);
         q0 += __shfl_xor_sync(0xffffffffu, q0, o);
     }
+    const bool fits = q0 + ql_s <= total_q;
+    if (!fits && hk == 0 && threadIdx.x == 0) raise_error(ctx, ERR_BOUNDS_BIT);
     const long long P = (long long)Hkv * tot;
     const long long seg_first = (long long)Hkv * pre + (long long)hk * nblk;
     if constexpr (PAGES > 0) W = stream_warps(W, P, PAGES);
@@ -1017,7 +1024,7 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
     };
     const long lane_slot = lane < npieces ? slot_of(lane) : -1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (c_lo == c_hi) return;  // the whole segment was finished inside one decode CTA
+    if (c_lo == c_hi || !fits) return;  // the whole segment was finished inside one decode CTA
 
     constexpr int kPer = D / 32;  // channels per lane
     float acc[kPer];
@@ -1153,7 +1160,7 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
                                                            const float* lse, const float* logits, int logit_rows,
                                                            const float* acc_in, float* acc_out, int acc_len,
                                                            float decay, int num_seqs, int mbps, int Hq, int Hkv,
-                                                           int window, DevCtx ctx) {
+                                                           int window, int total_q, DevCtx ctx) {
     const int s = blockIdx.x, hk = blockIdx.y, g = Hq / Hkv, lane = threadIdx.x & 31;
     const int ql = __ldg(q_lens + s), cl = __ldg(ctx_lens + s);
     int p0 = blockIdx.z * kAccumPages;
@@ -1172,13 +1179,17 @@ __global__ void __launch_bounds__(256) accum_decode_kernel(const int32_t* __rest
             const int qi = __ldg(q_lens + i), ci = __ldg(ctx_lens + i);
             if (is_decode_row(qi, g) && qi <= ci && ci <= mbps * kBS)
                 pre += (ci + kBS - 1) / kBS - first_block(ci, qi, window);
-            q0 += qi;
+            q0 += max(0, qi);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             pre += __shfl_xor_sync(0xffffffffu, pre, o);
             q0 += __shfl_xor_sync(0xffffffffu, q0, o);
         }
+    }
+    if (q0 + ql > total_q) {  // (the same for the whole CTA; reported by the merge kernel)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
     }
     const int nrows = ql > 0 ? min(g * ql, logit_rows) : 0;
     const int blk0 = ql > 0 ? first_block(cl, ql, window) : 0;
@@ -1260,9 +1271,10 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
                                                           int window, const int32_t* __restrict__ prefix,
                                                           int32_t* __restrict__ k_start, int acc_len,
                                                           int4* __restrict__ pieces, int4* __restrict__ split,
-                                                          int max_slots, int per_rank, DevCtx ctx) {
+                                                          int max_slots, int per_rank, int total_q, DevCtx ctx) {
     extern __shared__ int hist[];  // [nbins + 1]
     __shared__ int warp_sums[32];
+    __shared__ long long row_sums[32], rows_before;
     __shared__ int carry, n_slots, n_split;
     __shared__ unsigned long long all_tiles;
     const int nbins = (mbps * kBS + 127) / 128 + 1;
@@ -1275,6 +1287,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     for (int i = threadIdx.x; i <= nbins; i += blockDim.x) hist[i] = 0;
     if (threadIdx.x == 0) {
         carry = n_slots = n_split = 0;
+        rows_before = 0;
         all_tiles = 0;
     }
     __syncthreads();
@@ -1282,33 +1295,33 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
         // prefix sum of q_lens, 1024 sequences per pass
         for (int base = 0; base < num_seqs; base += blockDim.x) {
             const int s = base + threadIdx.x;
-            int v = s < num_seqs ? q_len(s) : 0;
-            int x = v;
+            const int v = s < num_seqs ? max(0, q_len(s)) : 0;
+            long long x = v;
             const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                int y = __shfl_up_sync(0xffffffffu, x, o);
+                const long long y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            if (lane == 31) warp_sums[w] = x;
+            if (lane == 31) row_sums[w] = x;
             __syncthreads();
             if (w == 0) {
-                int t = warp_sums[lane];
+                long long t = row_sums[lane];
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    int y = __shfl_up_sync(0xffffffffu, t, o);
+                    const long long y = __shfl_up_sync(0xffffffffu, t, o);
                     if (lane >= o) t += y;
                 }
-                warp_sums[lane] = t;
+                row_sums[lane] = t;
             }
             __syncthreads();
-            const int excl = carry + (w ? warp_sums[w - 1] : 0) + x - v;
-            if (s < num_seqs) q_start[s] = excl;
+            const long long excl = rows_before + (w ? row_sums[w - 1] : 0) + x - v;
+            if (s < num_seqs) q_start[s] = (int)min(excl, 0x7fffffffll);
+            if (v > 0 && excl + v > total_q) raise_error(ctx, ERR_BOUNDS_BIT);
             __syncthreads();
-            if (threadIdx.x == blockDim.x - 1) carry = excl + v;
+            if (threadIdx.x == blockDim.x - 1) rows_before = excl + v;
             __syncthreads();
         }
-        if (threadIdx.x == 0) q_start[num_seqs] = carry;
         // weight sums: sequences by decreasing chunk length (a counting sort over 64
         // lengths; the order only decides who goes first), then their units of 256
         // keys in that order (none for a sequence whose sums do not fit, which is
@@ -1338,7 +1351,8 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
                 const int r = base + threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
                 const int s = r < num_seqs ? k_seq[r] : 0;
                 const int ql = r < num_seqs ? q_lens[s] : 0, cl = r < num_seqs ? ctx_lens[s] : 0;
-                const bool chunk = ql > 0 && !is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS;
+                const bool chunk = ql > 0 && !is_decode_row(ql, g) && ql <= cl && cl <= mbps * kBS &&
+                                   rows_fit(q_start[s], ql, total_q);
                 if (chunk && cl > acc_len) raise_error(ctx, ERR_BOUNDS_BIT);
                 const int v = chunk && cl <= acc_len ? (cl + 255) / 256 : 0;
                 int x = v;
@@ -1409,7 +1423,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     };
     for (int s = mine; s < num_seqs; s += blockDim.x) {
         const int ql = q_len(s), cl = ctx_len(s);
-        if (ql > 0 && !is_decode_row(ql, g) && !is_chunk(ql, cl)) raise_error(ctx, ERR_BOUNDS_BIT);
+        if (ql < 0 || (ql > 0 && !is_decode_row(ql, g) && !is_chunk(ql, cl))) raise_error(ctx, ERR_BOUNDS_BIT);
     }
     // histogram of the costs
     for_entries([&](int s, int ql, int cl, int t0, int i) {
@@ -1474,7 +1488,7 @@ template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(const int4* split, const int32_t* count, const float4* part_o,
                                                          const float2* part_ml, const int32_t* __restrict__ q_lens,
                                                          const int32_t* __restrict__ q_start, uint16_t* __restrict__ out,
-                                                         float* __restrict__ lse, int per_rank, int Hq, int g) {
+                                                         float* __restrict__ lse, int per_rank, int Hq, int g, int total_q) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kSlices = D / 16;
     const int lane = threadIdx.x & 31;
@@ -1524,7 +1538,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const int4* split, cons
             tok = e.y + row;
             head = rest;
         }
-        if (tok >= ql) continue;
+        if (tok >= ql || !rows_fit(qs, ql, total_q)) continue;
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const long at = ((long)qs + tok) * Hq + head;
         if (lse && slice == 0) lse[at] = sum > 0.f ? (M + __log2f(sum)) * kLn2f : -INFINITY;
@@ -1565,7 +1579,7 @@ template <int D, int KV = KV_BF16, int MOD = 0>
 static fa_status launch_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* bt,
                                const int32_t* ctx_lens, const int32_t* q_lens, void* out, const PagedWs& w,
                                uint8_t* ws, int num_seqs, int mbps, int num_blocks, int Hq, int Hkv,
-                               int max_q_len, int q_prefetch_rows, int causal, float scale, int merge_rows,
+                               int max_q_len, int total_q, int q_prefetch_rows, int causal, float scale, int merge_rows,
                                cudaStream_t s, const DevCtx& ctx, int* launches,
                                float k_scale = 1.f, float v_scale = 1.f, const ScoreMod& mod = ScoreMod{},
                                const uint8_t* k_exp = nullptr, const uint8_t* v_exp = nullptr) {
@@ -1608,7 +1622,7 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
         if (st2 != FA_OK) return st2;
         paged_decode_kernel<D, KV, R, MOD><<<grid, kStreamWarps * 32, L::kBytes, s>>>(
             tk, tv, static_cast<const uint16_t*>(q), bt, ctx_lens, q_lens, static_cast<uint16_t*>(out), part_o, part_ml,
-            num_seqs, mbps, num_blocks, Hq, Hkv, q_prefetch_rows, causal, scale_log2, v_scale, ctx,
+            num_seqs, mbps, num_blocks, Hq, Hkv, q_prefetch_rows, causal, scale_log2, v_scale, total_q, ctx,
             mod, k_exp, v_exp);
         return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     };
@@ -1627,7 +1641,7 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
     constexpr bool kScaled = KV == KV_FP8_SCALED;
     if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, (MOD != 0 || kScaled), kScaled ? 2 : (MOD != 0 ? 1 : 0)>, ctx_lens, q_lens,
                            static_cast<const float*>(part_o), static_cast<const float2*>(part_ml),
-                           static_cast<uint16_t*>(out), num_seqs, Hq, Hkv, mbps, grid * kStreamWarps, max_q_len, ctx, mod) !=
+                           static_cast<uint16_t*>(out), num_seqs, Hq, Hkv, mbps, grid * kStreamWarps, max_q_len, total_q, ctx, mod) !=
         cudaSuccess)
         return FA_ERR_CUDA;
     ++*launches;
@@ -1778,7 +1792,7 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
                                                        acc ? acc->len : 0,
                                                        mod ? reinterpret_cast<int4*>(wsb + pw.list) : nullptr,
                                                        mod ? reinterpret_cast<int4*>(wsb + pw.split) : nullptr,
-                                                       pw.slots, pw.per_rank, ctx);
+                                                       pw.slots, pw.per_rank, total_q, ctx);
         const bool launched = cudaGetLastError() == cudaSuccess;
         if (ss && (cudaEventRecord(ss->join, ss->s) != cudaSuccess || !launched)) {
             (void)cudaStreamWaitEvent(s, ss->join, 0);  // leave the side stream joined
@@ -1797,7 +1811,7 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         auto go = [&](auto dim, auto variant, auto cache) {
             return launch_decode<decltype(dim)::value, decltype(cache)::value, decltype(variant)::value>(
                 q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w, wsb, num_seqs, max_blocks_per_seq,
-                num_blocks, Hq, Hkv, tc_path ? INT_MAX : max_q_len, qpf, causal, scale, merge_rows, s, ctx, &launches, 1.f, 1.f,
+                num_blocks, Hq, Hkv, tc_path ? INT_MAX : max_q_len, total_q, qpf, causal, scale, merge_rows, s, ctx, &launches, 1.f, 1.f,
                 mod ? *mod : ScoreMod{}, kv8 ? kv8->k_exp : nullptr, kv8 ? kv8->v_exp : nullptr);
         };
         auto go_d = [&](auto variant, auto cache) {
@@ -1846,7 +1860,7 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
                                    static_cast<const int32_t*>(count), reinterpret_cast<const float4*>(wsb + pw.o),
                                    reinterpret_cast<const float2*>(wsb + pw.ml), q_lens,
                                    static_cast<const int32_t*>(q_start), static_cast<uint16_t*>(out), mod->lse, pw.per_rank, Hq,
-                                   g) != cudaSuccess)
+                                   g, total_q) != cudaSuccess)
                 return FA_ERR_CUDA;
             ++launches;
         }
@@ -1868,7 +1882,8 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, accum_decode_kernel, ctx_lens, q_lens, static_cast<const float*>(mod->lse),
                                static_cast<const float*>(mod->logits), mod->logit_rows, acc->in, acc->out, acc->len,
-                               acc->decay, num_seqs, max_blocks_per_seq, Hq, Hkv, mod->window, ctx) != cudaSuccess)
+                               acc->decay, num_seqs, max_blocks_per_seq, Hq, Hkv, mod->window, total_q, ctx) !=
+            cudaSuccess)
             return FA_ERR_CUDA;
         ++launches;
         if (tc_path) {
@@ -1980,7 +1995,7 @@ fa_status fa_paged_attn_fp8(const void* q, const void* k_cache, const void* v_ca
     int launches = 0;
     st = launch_decode<128, KV_FP8>(q, k_cache, v_cache, block_table, ctx_lens, q_lens, out, w,
                                   static_cast<uint8_t*>(ws), num_seqs, max_blocks_per_seq, num_blocks, Hq, Hkv,
-                                  max_q_len, total_q, causal, scale, (Hq / Hkv) * max_q_len,
+                                  max_q_len, total_q, total_q, causal, scale, (Hq / Hkv) * max_q_len,
                                   reinterpret_cast<cudaStream_t>(stream), ctx, &launches, k_scale, v_scale);
     if (st != FA_OK) return st;
     set_launch_count(launches);
