@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kF32 ? 4 : 7) append_scaled
     const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
     if (!scan.find(a.q_lens, a.ctx_lens, row, count, it)) return;
     const int pos = a.positions ? __ldg(a.positions + row) : it.cl - it.ql + (row - it.q0);
-    const bool fits = lens_ok(it.ql, it.cl, a.mbps), in = pos >= 0 && pos < a.max_pos;  // (lengths are reported above)
+    const bool fits = lens_ok(it.ql, it.cl, a.mbps) && rows_fit(it.q0, it.ql, a.total_q);  // (reported above)
+    const bool in = pos >= 0 && pos < a.max_pos;
     if (fits && !in && lane == 0) raise_error(a.ctx, ERR_BOUNDS_BIT);
     if (fits && in) {
         Raw8<true> co, si;
