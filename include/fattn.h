@@ -531,7 +531,8 @@ fa_status fa_cache_append_fp8_scaled(const void* q, const void* k, const void* v
  * row, sums fp32; a context's v_exp codes must lie within 100 of each other for
  * the row sums to keep all their digits (the append's codes do below values of 2^68).
  * Codes of tokens below ctx_lens[s] must not be NaN; what is stored behind them does
- * not matter.  Equal inputs give equal bits.  Everything else as for fa_paged_attn.
+ * not matter.  The lengths of sequences without queries are checked as well, as in the
+ * append and the calls below.  Equal inputs give equal bits.  Everything else as for fa_paged_attn.
  */
 size_t fa_paged_attn_fp8_scaled_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv,
                                                int d, int total_q, int max_q_len);

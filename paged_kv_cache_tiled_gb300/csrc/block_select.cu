@@ -142,7 +142,7 @@ __global__ void __launch_bounds__((kScWarps + 1) * 32, kScCtasPerSm) block_score
     long long n_items;
     {
         auto count = [&](int ql, int cl) { return score_items(a, ql, cl); };
-        const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+        const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, a.mbps, count);
         const long long W = gridDim.x, w = blockIdx.x;
         const long long each = scan.items < 1ll << 31 ? (int)scan.items / (int)gridDim.x : scan.items / W, more = scan.items - each * W;
         n_items = each + (w < more ? 1 : 0);
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kTopThreads, 1024 / kTopThreads) block_top_ker
         }
         SeqItem it;
         auto count = [](int ql, int) { return ql; };
-        const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+        const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, a.mbps, count);
         const bool some = scan.find(a.q_lens, a.ctx_lens, at_row, count, it);
         const bool fits = some && lens_ok(it.ql, it.cl, a.mbps) && (long long)it.q0 + it.ql <= a.total_q;
         if (hk == 0 && tid == 0 && (some != fits || scan.bad || scan.rows > a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     t.reset();
     SeqItem it;
     auto count = [](int ql, int) { return ql; };
-    const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+    const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, a.mbps, count);
     const bool some = scan.find(a.q_lens, a.ctx_lens, row, count, it);
     // (the whole cluster takes the same way)
     const bool fits = some && lens_ok(it.ql, it.cl, a.mbps) && (long long)it.q0 + it.ql <= a.total_q;

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kF32 ? 4 : 7) append_scaled
         __shared__ __align__(16) float turns[B][D];  // the tokens' rows of cos_sin
         const int part = blockIdx.x % a.parts, place = blockIdx.x / a.parts;
         auto count = [&](int ql, int cl) { return chunk_blocks(ql, cl, a.mbps); };
-        const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+        const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, a.mbps, count);
         if (blockIdx.x == 0 && threadIdx.x == 0 && (scan.bad || scan.rows > a.total_q)) raise_error(a.ctx, ERR_BOUNDS_BIT);
         // (the same for the whole CTA from here on, but for the pairs)
         if (!scan.find(a.q_lens, a.ctx_lens, place, count, it) || (long long)it.q0 + it.ql > a.total_q) return;
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kF32 ? 4 : 7) append_scaled
     };
     load(h0);  // on their way while the token's sequence is found
     auto count = [](int ql, int) { return max(0, ql); };
-    const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, count);
+    const SeqScan scan(a.q_lens, a.ctx_lens, a.num_seqs, a.mbps, count);
     if (!scan.find(a.q_lens, a.ctx_lens, row, count, it)) return;
     const int pos = a.positions ? __ldg(a.positions + row) : it.cl - it.ql + (row - it.q0);
     const bool fits = lens_ok(it.ql, it.cl, a.mbps) && rows_fit(it.q0, it.ql, a.total_q);  // (reported above)
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(128, 12) block_bounds_kernel(const void* __res
     const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, hk = w % Hkv;
     SeqItem it;
     auto count = [&](int ql, int cl) { return chunk_blocks(ql, cl, mbps); };
-    const SeqScan scan(q_lens, ctx_lens, num_seqs, count);
+    const SeqScan scan(q_lens, ctx_lens, num_seqs, mbps, count);
     if (w == 0 && lane == 0 && (scan.bad || scan.rows > total_q)) raise_error(ctx, ERR_BOUNDS_BIT);
     if (!scan.find(q_lens, ctx_lens, w / Hkv, count, it)) return;
     const int blk = (it.cl - it.ql) / B + (int)it.off, n = min(B, it.cl - blk * B);

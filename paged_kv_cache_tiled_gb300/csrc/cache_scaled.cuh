@@ -17,8 +17,13 @@ constexpr int kExpLeast = 87;
 // 2^(code - 127) for a scale code (0: 2^-127; 255: +inf, as the power of two it is not).
 __device__ __forceinline__ float scale_of(int code) { return __uint_as_float(code > 0 ? (uint32_t)code << 23 : 0x00400000u); }
 
+// Do a chunk of ql tokens and a context of cl of them (the chunk included) fit the table?
+__device__ __forceinline__ bool lens_ok(int ql, int cl, int mbps) {
+    return ql >= 0 && ql <= cl && cl <= (long long)mbps * kScaledBlock;
+}
+
 // Where items of a batch lie when sequence s has count(q_len, ctx_len) of them (negative:
-// its lengths are inconsistent, it has none).  Made and asked by whole warps.
+// none).  Made and asked by whole warps.
 struct SeqItem {
     int s, ql, cl;   // sequence and its lengths
     long long off;   // item within the sequence
@@ -26,13 +31,13 @@ struct SeqItem {
 };
 struct SeqScan {
     long long items, rows;  // of the batch
-    bool bad;               // some sequence's lengths are inconsistent
+    bool bad;               // some sequence's lengths are inconsistent, with queries or without
     long long n, in, iq, q; // this lane's items and rows, and those up to its end
     int lo, hi;             // its sequences
 
     template <class Count>
     __device__ __forceinline__ SeqScan(const int32_t* __restrict__ q_lens, const int32_t* __restrict__ ctx_lens, int num_seqs,
-                                       Count count) {
+                                       int mbps, Count count) {
         const int lane = threadIdx.x & 31, per = (num_seqs + 31) >> 5;
         lo = min(num_seqs, lane * per);
         hi = min(num_seqs, lo + per);
@@ -44,7 +49,7 @@ struct SeqScan {
             const long long c = count(ql, cl);
             n += max(0ll, c);
             q += max(0, ql);
-            b |= c < 0;
+            b |= !lens_ok(ql, cl, mbps);
         }
         if (!__any_sync(0xffffffffu, n > 1 << 26 || q > 1 << 26)) {  // 32 bits hold every sum
             int x = (int)n, y = (int)q;
@@ -109,10 +114,6 @@ struct SeqScan {
     }
 };
 
-// Do a chunk of ql tokens and a context of cl of them (the chunk included) fit the table?
-__device__ __forceinline__ bool lens_ok(int ql, int cl, int mbps) {
-    return ql >= 0 && ql <= cl && cl <= (long long)mbps * kScaledBlock;
-}
 // Blocks that a chunk's tokens lie in (-1: inconsistent lengths).
 __device__ __forceinline__ int chunk_blocks(int ql, int cl, int mbps) {
     if (!lens_ok(ql, cl, mbps)) return -1;

@@ -979,7 +979,9 @@ __global__ void __launch_bounds__(kMergeMaxThreads, 1) paged_merge_kernel(const 
     const int s = blockIdx.x, hk = blockIdx.y, r = threadIdx.x >> 5, g = Hq / Hkv;
     const int lane = threadIdx.x & 31;
     const int ql_s = __ldg(q_lens + s), cl_s = __ldg(ctx_lens + s);
-    if ((ql_s > max_q_len || ql_s < 0) && hk == 0 && threadIdx.x == 0) raise_error(ctx, ERR_BOUNDS_BIT);
+    // (PAGES 2, the 8-bit cache with block scales: also the lengths of sequences without queries, as its other forms)
+    if ((ql_s > max_q_len || ql_s < 0 || (PAGES == 2 && !lens_ok(ql_s, cl_s, mbps))) && hk == 0 && threadIdx.x == 0)
+        raise_error(ctx, ERR_BOUNDS_BIT);
     const bool mine = is_decode_row(ql_s, g) && ql_s <= cl_s && cl_s <= mbps * kBS && r < g * ql_s;
     if (!mine) {
         // every CTA waits for the decode grid, so this grid never completes ahead of it
@@ -1271,7 +1273,7 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
                                                           int window, const int32_t* __restrict__ prefix,
                                                           int32_t* __restrict__ k_start, int acc_len,
                                                           int4* __restrict__ pieces, int4* __restrict__ split,
-                                                          int max_slots, int per_rank, int total_q, DevCtx ctx) {
+                                                          int max_slots, int per_rank, int total_q, int all_lens, DevCtx ctx) {
     extern __shared__ int hist[];  // [nbins + 1]
     __shared__ int warp_sums[32];
     __shared__ long long row_sums[32], rows_before;
@@ -1423,7 +1425,8 @@ __global__ void __launch_bounds__(1024) paged_meta_kernel(const int32_t* __restr
     };
     for (int s = mine; s < num_seqs; s += blockDim.x) {
         const int ql = q_len(s), cl = ctx_len(s);
-        if (ql < 0 || (ql > 0 && !is_decode_row(ql, g) && !is_chunk(ql, cl))) raise_error(ctx, ERR_BOUNDS_BIT);
+        if (ql < 0 || (ql > 0 && !is_decode_row(ql, g) && !is_chunk(ql, cl)) || (all_lens && !lens_ok(ql, cl, mbps)))
+            raise_error(ctx, ERR_BOUNDS_BIT);
     }
     // histogram of the costs
     for_entries([&](int s, int ql, int cl, int t0, int i) {
@@ -1792,7 +1795,7 @@ static fa_status paged_attn_run(const void* q, const void* k_cache, const void* 
                                                        acc ? acc->len : 0,
                                                        mod ? reinterpret_cast<int4*>(wsb + pw.list) : nullptr,
                                                        mod ? reinterpret_cast<int4*>(wsb + pw.split) : nullptr,
-                                                       pw.slots, pw.per_rank, total_q, ctx);
+                                                       pw.slots, pw.per_rank, total_q, kv8 != nullptr, ctx);
         const bool launched = cudaGetLastError() == cudaSuccess;
         if (ss && (cudaEventRecord(ss->join, ss->s) != cudaSuccess || !launched)) {
             (void)cudaStreamWaitEvent(s, ss->join, 0);  // leave the side stream joined

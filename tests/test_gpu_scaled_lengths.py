@@ -38,3 +38,36 @@ def test_append_leaves_queries_out_with_their_keys(F, ctx, ql, n, k):
     assert F.fa_get_error() == F.FA_OK
     assert torch.equal(out, want) and bool((out[k:] == 7.0).all())
     assert all(torch.equal(a, b) for a, b in zip(cache, before))
+
+
+@pytest.mark.parametrize("ctx, ql, Hq, wide", [([40, 300], [1, 0], 4, False), ([40, 300], [1, 0], 4, True), ([40, 300], [30, 0], 4, False),
+                                               ([40, 300], [30, 0], 40, False), ([300, 40], [2, 0], 40, True)])
+@pytest.mark.parametrize("bad", [-3, 1 << 20, -(1 << 31)])
+def test_lengths_of_sequences_without_queries_are_checked(F, ctx, ql, Hq, wide, bad):
+    """A context that is negative or longer than its table is reported by every call, whatever form the sizes choose;
+    the other sequence gets what it gets without."""
+    d, H, n = 128, 2, sum(ql)
+    table, nb = R.tables(ctx, 11, mbps=600 if wide else None)
+    cache = cuda(*R.random_cache8(nb, H, d, 12))
+    q, kv = R.normal(n, Hq, d, seed=13).cuda(), R.normal(n, H, d, seed=14).cuda()
+    bounds = torch.zeros(nb, H, 2, d, dtype=torch.bfloat16).cuda()
+    sel = torch.tensor([0, 1, -1]).int().expand(n, H, 3).contiguous().cuda()
+
+    def run(ctx):
+        got, errors = [], []
+
+        def call(f, *a, **k):
+            got.append(f(*a, **k))
+            errors.append(F.fa_get_error())
+        at = cuda(table, R.i32(ctx), R.i32(ql))
+        mine = [t.clone() for t in cache]
+        call(F.fa_cache_append_fp8_scaled, kv, kv, *mine, *at)
+        call(F.fa_block_bounds, mine[0], *at, bounds.clone(), total_q=n, k_exp=mine[2])
+        call(F.fa_block_select, q, got[-1], *at, 2)
+        call(F.fa_paged_attn_blocks, q, mine[0], mine[1], *at, sel, k_exp=mine[2], v_exp=mine[3])
+        call(F.fa_paged_attn_fp8_scaled, q, *mine, *at, max_q_len=max(ql))
+        return got[1:] + mine, errors
+    want, fine = run(ctx)
+    got, errors = run([ctx[0], bad])
+    assert fine == [F.FA_OK] * 5 and errors == [F.FA_ERR_BOUNDS] * 5
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
