@@ -51,7 +51,7 @@ struct SeqScan {
             q += max(0, ql);
             b |= !lens_ok(ql, cl, mbps);
         }
-        if (!__any_sync(0xffffffffu, n > 1 << 26 || q > 1 << 26)) {  // 32 bits hold every sum
+        if (!__any_sync(0xffffffffu, n >= 1 << 26 || q >= 1 << 26)) {  // 32 bits hold every sum
             int x = (int)n, y = (int)q;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

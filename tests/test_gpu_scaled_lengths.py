@@ -71,3 +71,15 @@ def test_lengths_of_sequences_without_queries_are_checked(F, ctx, ql, Hq, wide, 
     got, errors = run([ctx[0], bad])
     assert fine == [F.FA_OK] * 5 and errors == [F.FA_ERR_BOUNDS] * 5
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_rows_that_add_up_to_two_to_the_31_are_reported(F):
+    """32 sequences of 2^26 rows each, every one of them consistent, in a call of ten rows."""
+    n, many = 32, 1 << 26
+    table = torch.zeros(n, many // 16, dtype=torch.int32, device="cuda")  # (512 MB; the first blocks of the first are done)
+    lens = torch.full((n,), many, dtype=torch.int32, device="cuda")
+    k = R.normal(1, 1, 16, 64, seed=1).cuda()
+    bounds = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    F.fa_block_bounds(k, table, lens, lens, bounds, total_q=10)
+    assert F.fa_get_error() == F.FA_ERR_BOUNDS
+    assert torch.equal(bounds, torch.stack([k.amin(2), k.amax(2)], 2))
