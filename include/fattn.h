@@ -777,7 +777,9 @@ void fa_debug_set_wait_limit(unsigned long long nanoseconds);
  * wait on a barrier that nothing ever arrives on; the wait runs out after the
  * current wait limit, the kernel records FA_ERR_TIMEOUT, drains the copies it
  * issued, releases its tensor memory and exits.  No fault, trap or hang is
- * involved.  Host-side setting.
+ * involved.  With enable = n > 1 the kernel behind fa_paged_attn_blocks (and behind
+ * fa_paged_attn_fp8_scaled over short tables) waits so later, with copies in flight:
+ * each of its warps before the n-th page that it would read.  Host-side setting.
  */
 void fa_debug_force_timeout(int enable);
 

@@ -190,7 +190,7 @@ void fa_debug_set_wait_limit(unsigned long long ns) {
 
 void fa_debug_force_timeout(int enable) {
     std::lock_guard<std::mutex> lk(fa::g_mu);
-    fa::g_force_timeout = enable ? 1 : 0;
+    fa::g_force_timeout = enable < 0 ? 1 : enable;
 }
 
 int fa_last_launch_count(void) { return fa::t_launches; }

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     uint8_t* ring = smem + warp * ST * L::kStage;
     uint64_t* wbar = bars + warp * ST;
     int4* entries = lists + warp * kBlBatch;
-    bool ok = !a.ctx.force_timeout || mbar_wait_warp(never, 0, a.ctx.wait_ns, abort_flag);
+    bool ok = a.ctx.force_timeout != 1 || mbar_wait_warp(never, 0, a.ctx.wait_ns, abort_flag);
     int done = 0;  // pages taken from the ring so far
     for (int base = w0; base < a.keep && ok; base += W * kBlBatch) {
         // the next 32 entries of this warp: table and scales looked up by a lane each
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             }
             __syncwarp();
         }
-        int issued = 0;
+        int issued = 0, i = 0;  // pages of these entries asked for, and taken from the ring
         auto issue = [&]() {
             const int stage = (done + issued) % ST;
             load_page<D, KV8>(ring + stage * L::kStage, &tm_k, &tm_v, &wbar[stage], hk, entries[issued].x);
@@ -175,8 +175,10 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             entries[place].w = ev_new;
         }
         __syncwarp();
-        for (int i = 0; i < n && ok;) {
+        while (i < n && ok) {
             const int np = min(NP, n - i);
+            if (a.ctx.force_timeout > 1 && done + i + np >= a.ctx.force_timeout)  // (test hook, with copies in flight)
+                ok = mbar_wait_warp(never, 0, a.ctx.wait_ns, abort_flag);
             uint32_t kv[NP];
             int tok[NP], ks[NP], ev[NP];
 #pragma unroll
@@ -196,8 +198,8 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             if (lane == 0)
                 while (issued < n && issued < i + ST) issue();
         }
-        if (!ok && lane == 0) {  // let the copies in flight land before the CTA may end
-            for (int i = 0; i < issued; ++i)
+        if (!ok && lane == 0) {  // let the copies in flight land before the CTA may end (earlier phases are over)
+            for (; i < issued; ++i)
                 (void)mbar_wait_bounded(&wbar[(done + i) % ST], ((done + i) / ST) & 1, 1000000000ull, nullptr);
         }
         done += n;

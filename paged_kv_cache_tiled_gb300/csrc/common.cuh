@@ -41,7 +41,8 @@ enum : unsigned { ERR_BOUNDS_BIT = 1u, ERR_TIMEOUT_BIT = 2u };
 struct DevCtx {
     unsigned* err;              // device error word
     unsigned long long wait_ns; // bound on each pipeline wait
-    int force_timeout;          // test hook: start every role with a wait that cannot complete
+    int force_timeout;          // test hook: start every role with a wait that cannot complete (n > 1: the listed
+                                // blocks' warps wait so before the n-th page instead)
 };
 
 __device__ __forceinline__ void raise_error(const DevCtx& c, unsigned bit) { atomicOr(c.err, bit); }

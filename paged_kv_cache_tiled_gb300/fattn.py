@@ -949,8 +949,8 @@ def fa_debug_set_wait_limit(nanoseconds: int):
     _lib.fa_debug_set_wait_limit(int(nanoseconds))
 
 
-def fa_debug_force_timeout(enable: bool):
-    _lib.fa_debug_force_timeout(int(bool(enable)))
+def fa_debug_force_timeout(enable):
+    _lib.fa_debug_force_timeout(int(enable))
 
 
 def fa_last_launch_count() -> int:
