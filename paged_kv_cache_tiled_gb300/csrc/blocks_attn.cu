@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     __syncthreads();
     constexpr int kCols = D / 4;
     auto write = [&](int r, int c, float4 v, float mx, float sum) {
+        if (sum < 0.f) return;  // (a part of the row's keys is missing)
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         *reinterpret_cast<uint2*>(a.out + (out_row + r) * D + c * 4) =
             make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
@@ -225,17 +226,20 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
         mx = -INFINITY;
         sum = 0.f;
         v = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool whole = true;
         for (int i = 0; i < parts; ++i) mx = fmaxf(mx, ml_of(i, r).x);
         for (int i = 0; i < parts; ++i) {
             const float2 ml = ml_of(i, r);
             const float4 x = o_of(i, r, c);
             const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mx);
+            whole = whole && !(ml.y < 0.f);
             sum = fmaf(f, ml.y, sum);
             v.x = fmaf(f, x.x, v.x);
             v.y = fmaf(f, x.y, v.y);
             v.z = fmaf(f, x.z, v.z);
             v.w = fmaf(f, x.w, v.w);
         }
+        if (!whole) sum = -1.f;
     };
     auto slot = [&](int i) { return reinterpret_cast<const float*>(smem + i * ST * L::kStage); };
     auto warp_ml = [&](int i, int r) { return reinterpret_cast<const float2*>(slot(i) + 16 * M::kSlotRow)[r]; };
@@ -254,7 +258,8 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             if (!*abort_flag) write(r, c, v, mx, sum);
         } else {
             *reinterpret_cast<float4*>(mine(r) + c * 4) = v;
-            if (c == 0) mine_ml[r] = make_float2(mx, sum);
+            // (a CTA whose waits gave up says so with a negative sum: no CTA of the cluster writes its share of the rows)
+            if (c == 0) mine_ml[r] = *abort_flag ? make_float2(-INFINITY, -1.f) : make_float2(mx, sum);
         }
     }
     if (C == 1) return;
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
         float mx, sum;
         join(r, c, (int)C, [&](int k, int rr) { return remote_f2(mine_ml + rr, k); },
              [&](int k, int rr, int cc) { return remote_f4(mine(rr) + cc * 4, k); }, v, mx, sum);
-        if (!*abort_flag) write(r, c, v, mx, sum);
+        write(r, c, v, mx, sum);
     }
     blocks_cluster_sync();  // no CTA leaves while another reads its rows
 }

@@ -68,3 +68,25 @@ def test_only_copies_in_flight_are_waited_for(F, fp8, d, page):
         assert time.perf_counter() - began < 0.5
     assert bool((out == 7.0).all())
     assert torch.equal(F.fa_paged_attn_blocks(*args, sel, **exps), want) and F.fa_get_error() == F.FA_OK
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("slow", [0, 5, 31])
+def test_a_cluster_writes_whole_rows_or_none(F, fp8, d, slow):
+    """One warp of a cluster gives up, the others have read their pages: nothing of that list's rows is written, and all of
+    the other list's."""
+    args, exps = case(1, 8, 2, d, fp8, 4)
+    sel = torch.full((1, 2, 256), -1, dtype=torch.int32)
+    sel[0, 0, slow::32] = torch.arange(8).int() + 20  # eight pages for one of 32 warps
+    sel[0, :, 1::37] = torch.arange(60, 67).int()     # one here and there
+    sel = sel.cuda()
+    lse = torch.zeros(1, 8).cuda()
+    want = F.fa_paged_attn_blocks(*args, sel, lse=lse, **exps)
+    assert F.fa_get_error() == F.FA_OK
+    out, got = torch.full_like(want, 7.0), torch.full_like(lse, 7.0)
+    with gives_up_at(F, 6):
+        F.fa_paged_attn_blocks(*args, sel, out=out, lse=got, **exps)
+        assert F.fa_get_error() == F.FA_ERR_TIMEOUT
+    assert bool((out[:, :4] == 7.0).all()) and bool((got[:, :4] == 7.0).all())
+    assert torch.equal(out[:, 4:], want[:, 4:]) and torch.equal(got[:, 4:], lse[:, 4:])
