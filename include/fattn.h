@@ -579,9 +579,10 @@ fa_status fa_block_bounds(const void* k_cache, const uint8_t* k_exp, const int32
  *   keep > 0, recent >= 0, sink >= 0, sink + recent <= keep
  *   max_q_len  host-side upper bound on q_lens (total_q is always valid): only
  *            the work's division goes by it
- *   ws       at least fa_block_select_workspace_size(...) bytes, 256-byte aligned
- *            (the scores, 4 bytes for each query, kv head and table entry, and 12
- *            bytes a table entry for each of 1280 CTAs)
+ *   ws       at least fa_block_select_workspace_size(...) bytes, 256-byte aligned:
+ *            for each table entry 4 bytes for each query and kv head (scores), 4 for
+ *            each sequence and kv head (largest bounds), and 12 for each query and kv
+ *            head up to 1280 of them (blocks near the border)
  * The choice is that of exact arithmetic: blocks whose scores are too close to tell
  * apart in fp32 are summed again in twice its digits (scores within 2^-40 of the sum of
  * their products' magnitudes, and not equal, may count in either order).  Calls that

@@ -748,7 +748,7 @@ static SelectWs select_ws_layout(int num_seqs, int mbps, int Hkv, int total_q) {
     w.scores = 0;
     w.largest = align256(sizeof(float) * (size_t)total_q * Hkv * mbps);
     w.near_key = align256(w.largest + sizeof(float) * (size_t)num_seqs * Hkv * mbps);
-    const size_t ctas = kTopCtas;
+    const size_t ctas = std::min<size_t>((size_t)total_q * Hkv, kTopCtas);  // (a CTA a row while they last)
     w.near_b = align256(w.near_key + sizeof(unsigned long long) * ctas * mbps);
     w.total = align256(w.near_b + sizeof(int32_t) * ctas * mbps);
     return w;
