@@ -556,8 +556,9 @@ fa_status fa_paged_attn_fp8_scaled(const void* q, const void* k_cache, const voi
  *   bounds   bf16 [num_blocks, Hkv, 2, d]: [.., 0, :] the minima, [.., 1, :] the maxima
  * Written for the blocks that the last q_lens[s] tokens of each sequence lie in (to
  * be called after they were appended; q_lens = ctx_lens: all blocks), over the tokens
- * below ctx_lens[s]; other blocks' bounds are left as they were.  Exact.  NaN keys
- * are passed over.  block_table, ctx_lens, q_lens, total_q as for fa_paged_attn.
+ * below ctx_lens[s]; other blocks' bounds are left as they were.  Exact (8 bits: for
+ * scale codes 3 to 246).  NaN keys are passed over; a channel without any other gets
+ * 0 and 0.  block_table, ctx_lens, q_lens, total_q as for fa_paged_attn.
  */
 fa_status fa_block_bounds(const void* k_cache, const uint8_t* k_exp, const int32_t* block_table,
                           const int32_t* ctx_lens, const int32_t* q_lens, void* bounds, int num_seqs,
@@ -583,9 +584,12 @@ fa_status fa_block_bounds(const void* k_cache, const uint8_t* k_exp, const int32
  *            for each table entry 4 bytes for each query and kv head (scores), 4 for
  *            each sequence and kv head (largest bounds), and 12 for each query and kv
  *            head up to 1280 of them (blocks near the border)
- * The choice is that of exact arithmetic: blocks whose scores are too close to tell
- * apart in fp32 are summed again in twice its digits (scores within 2^-40 of the sum of
- * their products' magnitudes, and not equal, may count in either order).  Calls that
+ * The choice is that of exact arithmetic while no head's sum of |q_c| times the largest
+ * |bound| reaches 2^126: blocks whose scores are too close to tell apart in fp32 are
+ * summed again in twice its digits.  (Scores within 2^-40 of the sum of their products'
+ * magnitudes may count in either order unless their products are the same; products
+ * below 2^-126 may count as 0.)  A block whose bounds are not finite is taken before or
+ * after all others and leaves their order as it is.  Calls that
  * may overlap on the GPU need workspaces of their own.  Sequences with inconsistent
  * lengths record FA_ERR_BOUNDS and their rows are left as they were; a block outside
  * the pool records it and counts as one of bounds 0.

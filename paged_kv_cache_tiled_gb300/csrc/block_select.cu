@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kTopThreads, 1024 / kTopThreads) block_top_ker
         constexpr int kPass = kTopThreads * kTopItems;
         const bool once = n <= kPass;
         float v[kTopItems];
-        auto load = [&](int base) {  // scores of blocks base + 256 k + tid (finite: the largest numbers stand for infinities, NaN last)
+        auto load = [&](int base) {  // scores of blocks base + kTopThreads k + tid (finite: the largest numbers stand for infinities, NaN last)
 #pragma unroll
             for (int k = 0; k < kTopItems; ++k) {
                 if (base + k * kTopThreads >= mid1) break;  // (the same for the whole CTA)
@@ -508,7 +508,10 @@ __global__ void __launch_bounds__(kTopThreads, 1024 / kTopThreads) block_top_ker
             }
         };
         float big = 0.f;
-        for (int b = mid0 + tid; b < mid1; b += kTopThreads) big = fmaxf(big, __ldcg(largest + b));
+        for (int b = mid0 + tid; b < mid1; b += kTopThreads) {
+            const float x = __ldcg(largest + b);
+            if (x < INFINITY) big = fmaxf(big, x);  // (an infinite bound says nothing about the others' roundings)
+        }
         load(0);
         __syncthreads();
         if (want > 0) {
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kTopThreads, 1024 / kTopThreads) block_top_ker
             __syncthreads();
             float lo = key_float(lo_sh), hi = key_float(hi_sh);
             float slack = 2.f * __uint_as_float(big_sh) * __uint_as_float(sum_sh) * sum_slack(D);
-            if (!(slack < 1e37f)) slack = 0.f;  // bounds or queries that are not finite: as they come
+            if (!(slack < 1e37f)) slack = 0.f;  // queries that are not finite, or products that fp32 cannot hold: as they come
             // Bins of the range [lo, hi]; the range becomes that of the bin with the last block taken while it holds
             // many blocks and is wider than what the roundings blur anyway.
             int need = want, sel = 0;  // blocks to take of the range

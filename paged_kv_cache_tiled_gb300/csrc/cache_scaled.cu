@@ -343,6 +343,14 @@ __global__ void __launch_bounds__(128, 12) block_bounds_kernel(const void* __res
             hi[c] = __hmax2(hi[c], two(x[c]));
         }
     }
+    // a channel without a number (its keys are NaN) is 0 to 0, so that bounds are finite
+#pragma unroll
+    for (int c = 0; c < N / 2; ++c) {
+        const uint32_t some = ~__hgt2_mask(lo[c], hi[c]);
+        const uint32_t l = *reinterpret_cast<const uint32_t*>(&lo[c]) & some, h = *reinterpret_cast<const uint32_t*>(&hi[c]) & some;
+        lo[c] = two(l);
+        hi[c] = two(h);
+    }
     auto word = [&](const Two& v) -> uint32_t {
         if constexpr (KV8) {
             const float2 x = __half22float2(v);
