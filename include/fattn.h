@@ -531,7 +531,8 @@ fa_status fa_cache_append_fp8_scaled(const void* q, const void* k, const void* v
  * row, sums fp32; a context's v_exp codes must lie within 100 of each other for
  * the row sums to keep all their digits (the append's codes do below values of 2^68).
  * Codes of tokens below ctx_lens[s] must not be NaN; what is stored behind them does
- * not matter.  The lengths of sequences without queries are checked as well, as in the
+ * not matter.  A block outside the pool records FA_ERR_BOUNDS and counts as zeros at
+ * scale 1.  The lengths of sequences without queries are checked as well, as in the
  * append and the calls below.  Equal inputs give equal bits.  Everything else as for fa_paged_attn.
  */
 size_t fa_paged_attn_fp8_scaled_workspace_size(int num_seqs, int max_blocks_per_seq, int Hq, int Hkv,
@@ -610,7 +611,8 @@ fa_status fa_block_select(const void* q, const void* bounds, const int32_t* bloc
  *   sel      int32 [total_q, Hkv, keep]: block numbers within the sequence, in any
  *            order, none twice; negative entries are passed over; a block behind
  *            the query's position has no visible key; one behind the context's
- *            last block records FA_ERR_BOUNDS and is passed over
+ *            last block records FA_ERR_BOUNDS and is passed over; one outside the pool
+ *            records it and counts as zeros
  *   lse      fp32 [total_q, Hq] log-sum-exp of the visible scores, or NULL
  * A query without a visible key gets output 0 and LSE -inf.  The values of visible
  * keys must be finite; nothing else of a block reaches the result.  No workspace, one

@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             b_next = entry(base + (lane + kBlBatch) * W);
             bool use = b >= 0;
             int phys = -1;
+            bool found = false;  // in the pool (else a block of zeros at scale 1)
             if (use) {
                 if (b > (it.cl - 1) / kScaledBlock) {
                     if (sel) raise_error(a.ctx, ERR_BOUNDS_BIT);
@@ -142,9 +143,10 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             }
             if (use) {
                 phys = __ldg(a.bt + (long)it.s * a.mbps + b);
-                if (phys < 0 || phys >= a.num_blocks) {
+                found = phys >= 0 && phys < a.num_blocks;
+                if (!found) {
                     raise_error(a.ctx, ERR_BOUNDS_BIT);
-                    use = false;
+                    phys = a.num_blocks;  // outside the tensor map: the copy fills zeros
                 }
             }
             const unsigned live = __ballot_sync(0xffffffffu, use);
@@ -157,8 +159,8 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
                 place = -1;
             }
             if (KV8 && use) {  // (on their way while the first pages are asked for)
-                ks_new = __ldg(a.ke + (long)phys * a.Hkv + hk);
-                ev_new = __ldg(a.ve + (long)phys * a.Hkv + hk);
+                ks_new = found ? __ldg(a.ke + (long)phys * a.Hkv + hk) : kExpBias;
+                ev_new = found ? __ldg(a.ve + (long)phys * a.Hkv + hk) : kExpBias;
             }
             __syncwarp();
         }

@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
         ci.nblk = __shfl_sync(0xffffffffu, c.nblk, kPageBatch - 1);
     };
     [[maybe_unused]] auto look_up_scales = [&]() {
-        found_scales = 0;
+        found_scales = kExpBias | kExpBias << 8;  // (outside the pool: zeros at scale 1, as the chunks' kernel)
         if (found >= 0 && found < num_blocks) {
             const long at = (long)found * Hkv + found_hk;
             found_scales = __ldg(k_exp + at) | __ldg(v_exp + at) << 8;
