@@ -528,7 +528,8 @@ fa_status fa_cache_append_fp8_scaled(const void* q, const void* k, const void* v
  *         max_q_len serves every call of no larger ones with the same heads
  * Queries may have any bf16 magnitude.  The codes are widened to f16 (exactly) and
  * the softmax weights are f16 relative to the largest weight * value scale of the
- * row, sums fp32; a context's v_exp codes must lie within 100 of each other for
+ * row: all its digits down to 2^-14 of that, nothing below 2^-25 (sequences with
+ * (Hq/Hkv) * q_len <= 16 and single tokens: 2^-29 and 2^-40); sums fp32; a context's v_exp codes must lie within 100 of each other for
  * the row sums to keep all their digits (the append's codes do below values of 2^68).
  * Codes of tokens below ctx_lens[s] must not be NaN; what is stored behind them does
  * not matter.  A block outside the pool records FA_ERR_BOUNDS and counts as zeros at

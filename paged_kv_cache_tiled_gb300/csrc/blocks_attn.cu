@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     constexpr int kCols = D / 4;
     auto write = [&](int r, int c, float4 v, float mx, float sum) {
         if (sum < 0.f) return;  // (a part of the row's keys is missing)
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum > 0.f ? M::kDown / sum : 0.f;
         *reinterpret_cast<uint2*>(a.out + (out_row + r) * D + c * 4) =
             make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
         if (a.lse && c == 0)

@@ -19,11 +19,15 @@ namespace fa {
 // A block's scales 2^ks (keys) and 2^ev (values) are powers of two.  2^ks multiplies the
 // scores; 2^ev goes into the exponent: with w = x + ev the weights are
 // p = 2^(w - m), m the running maximum of w, so that f16 holds them whatever the
-// scales; O = sum p code, l = sum 2^-ev p, and the result is O / l.
+// scales; O = sum p code, l = sum 2^-ev p, and the result is O / l.  No weight passes 1,
+// so they go to f16 times 2^15 (32768 of 65504): it keeps all its digits down to 2^-29 of
+// the largest and something down to 2^-40, which without it would be 2^-14 and 2^-25.
+// O is that much larger until the end (kDown); l and m are not.
 template <int D, bool KV8>
 struct PageMma {
     static constexpr int kPage = kScaledBlock * D * (KV8 ? 1 : 2);  // bytes of a K (or V) page
     static constexpr int kSlotRow = D + 8;                          // floats between rows of a partial result
+    static constexpr float kUp = KV8 ? 15.f : 0.f, kDown = KV8 ? 0x1p-15f : 1.f;  // O is 2^kUp times the sum of p and values
     uint32_t qa[D / 16][4];
     float o[D / 8][4];
     float m[2], l[2];
@@ -204,14 +208,15 @@ struct PageMma {
         for (int i = 0; i < NP; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], fmaxf(x[i][0][e], x[i][1][e]));
-        float a[2], use[2];
+        float a[2], use[2];  // (use: what a weight's exponent is less than its w by)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
             const float mn = fmaxf(m[r], mx[r]);
-            use[r] = mn == -INFINITY ? 0.f : mn;
-            a[r] = fast_exp2(m[r] - use[r]);
+            const float top = mn == -INFINITY ? 0.f : mn;
+            a[r] = fast_exp2(m[r] - top);
+            use[r] = top - kUp;
             m[r] = mn;
             l[r] *= a[r];
         }
@@ -232,8 +237,8 @@ struct PageMma {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i][nt][e] = fast_exp2(x[i][nt][e] - use[e >> 1]);
             const float back = KV8 ? scale_of(2 * kExpBias - ev[i]) : 1.f;  // 2^-ev
-            l[0] = fmaf(back, (x[i][0][0] + x[i][0][1]) + (x[i][1][0] + x[i][1][1]), l[0]);
-            l[1] = fmaf(back, (x[i][0][2] + x[i][0][3]) + (x[i][1][2] + x[i][1][3]), l[1]);
+            l[0] = fmaf(back, ((x[i][0][0] + x[i][0][1]) + (x[i][1][0] + x[i][1][1])) * kDown, l[0]);
+            l[1] = fmaf(back, ((x[i][0][2] + x[i][0][3]) + (x[i][1][2] + x[i][1][3])) * kDown, l[1]);
             add_pv(kv[i] + kPage, x[i]);
         }
     }

@@ -1589,6 +1589,7 @@ static fa_status launch_decode(const void* q, const void* k_cache, const void* v
     CUtensorMap tk, tv;
     fa_status st;
     if constexpr (KV == KV_FP8_SCALED) {
+        v_scale = PageMma<D, true>::kDown;
         st = page_maps<D, true>(k_cache, v_cache, num_blocks, Hkv, &tk, &tv);
         if (st != FA_OK) return st;
     } else if constexpr (KV == KV_FP8) {
