@@ -126,13 +126,12 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     int done = 0;  // pages taken from the ring so far
     for (int base = w0; base < a.keep && ok; base += W * kBlBatch) {
         // the next 32 entries of this warp: table and scales looked up by a lane each
-        int n, place, ks_new = 0, ev_new = 0;
+        int n, place, ks_new = kExpBias, ev_new = kExpBias;
         {
             const int b = b_next;
             b_next = entry(base + (lane + kBlBatch) * W);
             bool use = b >= 0;
             int phys = -1;
-            bool found = false;  // in the pool (else a block of zeros at scale 1)
             if (use) {
                 if (b > (it.cl - 1) / kScaledBlock) {
                     if (sel) raise_error(a.ctx, ERR_BOUNDS_BIT);
@@ -143,10 +142,9 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             }
             if (use) {
                 phys = __ldg(a.bt + (long)it.s * a.mbps + b);
-                found = phys >= 0 && phys < a.num_blocks;
-                if (!found) {
+                if (phys < 0 || phys >= a.num_blocks) {
                     raise_error(a.ctx, ERR_BOUNDS_BIT);
-                    phys = a.num_blocks;  // outside the tensor map: the copy fills zeros
+                    phys = a.num_blocks;  // outside the tensor map: the copy fills zeros, at scale 1
                 }
             }
             const unsigned live = __ballot_sync(0xffffffffu, use);
@@ -158,9 +156,9 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             } else {
                 place = -1;
             }
-            if (KV8 && use) {  // (on their way while the first pages are asked for)
-                ks_new = found ? __ldg(a.ke + (long)phys * a.Hkv + hk) : kExpBias;
-                ev_new = found ? __ldg(a.ve + (long)phys * a.Hkv + hk) : kExpBias;
+            if (KV8 && use && phys < a.num_blocks) {  // (on their way while the first pages are asked for)
+                ks_new = __ldg(a.ke + (long)phys * a.Hkv + hk);
+                ev_new = __ldg(a.ve + (long)phys * a.Hkv + hk);
             }
             __syncwarp();
         }
@@ -177,10 +175,10 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             entries[place].w = ev_new;
         }
         __syncwarp();
-        while (i < n && ok) {
-            const int np = min(NP, n - i);
-            if (a.ctx.force_timeout > 1 && done + i + np >= a.ctx.force_timeout)  // (test hook, with copies in flight)
-                ok = mbar_wait_warp(never, 0, a.ctx.wait_ns, abort_flag);
+        // (the test hook that gives up later, with copies in flight, ends the loop before: a test in it cost 2 %)
+        const int stop = a.ctx.force_timeout > 1 ? min(n, max(0, a.ctx.force_timeout - 1 - done)) : n;
+        while (i < stop && ok) {
+            const int np = min(NP, stop - i);
             uint32_t kv[NP];
             int tok[NP], ks[NP], ev[NP];
 #pragma unroll
@@ -200,6 +198,7 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
             if (lane == 0)
                 while (issued < n && issued < i + ST) issue();
         }
+        if (stop < n && ok) ok = mbar_wait_warp(never, 0, a.ctx.wait_ns, abort_flag);
         if (!ok && lane == 0) {  // let the copies in flight land before the CTA may end (earlier phases are over)
             for (; i < issued; ++i)
                 (void)mbar_wait_bounded(&wbar[(done + i) % ST], ((done + i) / ST) & 1, 1000000000ull, nullptr);
@@ -217,7 +216,6 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
     __syncthreads();
     constexpr int kCols = D / 4;
     auto write = [&](int r, int c, float4 v, float mx, float sum) {
-        if (sum < 0.f) return;  // (a part of the row's keys is missing)
         const float inv = sum > 0.f ? M::kDown / sum : 0.f;
         *reinterpret_cast<uint2*>(a.out + (out_row + r) * D + c * 4) =
             make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
@@ -228,20 +226,17 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
         mx = -INFINITY;
         sum = 0.f;
         v = make_float4(0.f, 0.f, 0.f, 0.f);
-        bool whole = true;
         for (int i = 0; i < parts; ++i) mx = fmaxf(mx, ml_of(i, r).x);
         for (int i = 0; i < parts; ++i) {
             const float2 ml = ml_of(i, r);
             const float4 x = o_of(i, r, c);
             const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mx);
-            whole = whole && !(ml.y < 0.f);
             sum = fmaf(f, ml.y, sum);
             v.x = fmaf(f, x.x, v.x);
             v.y = fmaf(f, x.y, v.y);
             v.z = fmaf(f, x.z, v.z);
             v.w = fmaf(f, x.w, v.w);
         }
-        if (!whole) sum = -1.f;
     };
     auto slot = [&](int i) { return reinterpret_cast<const float*>(smem + i * ST * L::kStage); };
     auto warp_ml = [&](int i, int r) { return reinterpret_cast<const float2*>(slot(i) + 16 * M::kSlotRow)[r]; };
@@ -270,9 +265,15 @@ __global__ void __launch_bounds__(NW * 32, kListSmWarps / NW)
         const int r = i / kCols, c = i % kCols;
         float4 v;
         float mx, sum;
-        join(r, c, (int)C, [&](int k, int rr) { return remote_f2(mine_ml + rr, k); },
+        bool whole = true;  // (else a part of the row's keys is missing)
+        auto cta_ml = [&](int k, int rr) {
+            const float2 ml = remote_f2(mine_ml + rr, k);
+            whole = whole && !(ml.y < 0.f);
+            return ml;
+        };
+        join(r, c, (int)C, cta_ml,
              [&](int k, int rr, int cc) { return remote_f4(mine(rr) + cc * 4, k); }, v, mx, sum);
-        write(r, c, v, mx, sum);
+        if (whole) write(r, c, v, mx, sum);
     }
     blocks_cluster_sync();  // no CTA leaves while another reads its rows
 }

@@ -236,9 +236,9 @@ struct PageMma {
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i][nt][e] = fast_exp2(x[i][nt][e] - use[e >> 1]);
-            const float back = KV8 ? scale_of(2 * kExpBias - ev[i]) : 1.f;  // 2^-ev
-            l[0] = fmaf(back, ((x[i][0][0] + x[i][0][1]) + (x[i][1][0] + x[i][1][1])) * kDown, l[0]);
-            l[1] = fmaf(back, ((x[i][0][2] + x[i][0][3]) + (x[i][1][2] + x[i][1][3])) * kDown, l[1]);
+            const float back = KV8 ? scale_of(2 * kExpBias - ev[i]) * kDown : 1.f;  // 2^-ev, of sums 2^kUp times too large
+            l[0] = fmaf(back, (x[i][0][0] + x[i][0][1]) + (x[i][1][0] + x[i][1][1]), l[0]);
+            l[1] = fmaf(back, (x[i][0][2] + x[i][0][3]) + (x[i][1][2] + x[i][1][3]), l[1]);
             add_pv(kv[i] + kPage, x[i]);
         }
     }
