@@ -493,7 +493,9 @@ fa_status fa_cache_evict(void* k_cache, void* v_cache, const float* acc, int acc
  *           sum(q_lens) may be less than total_q: rows behind the last sequence's
  *           are neither read for a result nor written.
  *           A block that new tokens go to must not be listed by another sequence
- *           (fa_pool_* keeps to that: shared blocks are full)
+ *           (fa_pool_* keeps to that: shared blocks are full.  After a fork inside a
+ *           block the caller copies the codes, scale codes and bounds of that block:
+ *           fa_copy_blocks copies bf16 caches)
  *   cos_sin fp32 [max_pos, d] or NULL (no rotation), as for fa_cache_append_rope:
  *           keys are turned in fp32 by the row of the token's position
  *   positions int32 [total_q], or NULL: the cache positions.  A position outside

@@ -1719,7 +1719,9 @@ struct ScaledKv {
 //   128 pairs, 2000          20.5 23.0   20.5 22.5   16.4 16.4;  4000  34.6 38.9   30.7 30.7   26.6 18.4
 //   512 pairs, 1000          31.1 41.0   24.6 28.8   20.5 16.4;  2000  50.0 62.8   46.5 47.2   32.8 20.5
 //   2400 pairs, 2000          201 239     151 168    61.7 51.2;  4000   380 445     290 300     108 72
-// The lists win by a fifth at most, and lose more the longer a single context can be: they are taken while that is short.
+// The lists win by a fifth at most while contexts are about as long, and lose when one long context lies among short
+// ones: by a fifth over 1000 and 2000 tokens (20.5 16.4, 61.7 51.2), by half over 4000 (108 72).  The lengths are on the
+// device, so the rule goes by the longest context there can be, and takes the lists while that is short.
 static bool whole_lists(int num_seqs, int mbps, int Hkv, int g, int max_q_len) {
     if (max_q_len != 1) return false;
     const long lists = (long)num_seqs * Hkv * ((g + 15) / 16), warps = (long)kListSmWarps * sm_count();
