@@ -950,7 +950,7 @@ def fa_debug_set_wait_limit(nanoseconds: int):
 
 
 def fa_debug_force_timeout(enable):
-    _lib.fa_debug_force_timeout(int(enable))
+    _lib.fa_debug_force_timeout(enable if isinstance(enable, int) else int(bool(enable)))
 
 
 def fa_last_launch_count() -> int:
